@@ -102,13 +102,47 @@ enum {
                                dims = {B, H, D=128, Lcap, Lmax >= every lens[b], Ccap >= B*H};
                                fparam[0] = scale */
     GPUOS_OP_VECMAT = 13,   /* out[n] = sum_k a[k] b[k][n]; b row-major [K][N]; dims = {K, N}; bf16 */
-    GPUOS_OP_BUILTIN_COUNT = 14,
+    /* The 4-bit paged key/value cache. A page holds GPUOS_KV4_PAGE = 32 tokens of every cache
+     * head; the pool is [npages][Hkv][34 D] bytes (gpuos_kv4_pool_bytes), D = 64 or 128, 16-byte
+     * aligned. Each run of 32 channels of a token is 32 codes of 4 bits (sign, and one of
+     * {0, .5, 1, 1.5, 2, 3, 4, 6}) under one scale byte e + 127: value = code * 2^e (255: the run
+     * held a NaN or an infinity, and reads as NaN). Slot s is key s % 32 of page s / 32. Pages
+     * are caller-owned like every tensor; so are the tables that say which are in use. */
+    GPUOS_OP_KV4_WRITE = 14, /* rows a=k[N][Hkv][D], b=v, f32|bf16, quantised into slots aux0 =
+                               i32[N] of pool `out`; dims = {N, Hkv, D, npages}. e is the least
+                               exponent >= -127 (at most 125) with max|x| <= 6 * 2^e, codes are
+                               the nearest, ties to the even code. A negative slot is skipped.
+                               The slots of one descriptor are distinct (of two rows for one slot
+                               either, or parts of both, may stay) */
+    GPUOS_OP_KV4_READ = 15,  /* the inverse: slots aux0 of pool a -> out=k[N][Hkv][D], aux1=v,
+                               f32|bf16 (exact in both); a negative slot gives zeros; dims as above */
+    GPUOS_OP_KV4_SDPA = 16,  /* attention of T query tokens a request over the cache: out[b][t][h] =
+                               softmax(scale q.K^T) V over keys 0 .. lens[b] - T + t of the pages
+                               aux1 = table i32[B][P]; a=q[B][T][H][D], out alike, bf16; b = pool;
+                               aux0 = lens i32[B], 0 <= lens[b] <= 32 P (the T new tokens
+                               included); query head h reads cache head h / (H / Hkv); a query that
+                               sees no key gives zeros; aux2 = workspace of GPUOS_KV4_WORKSPACE
+                               bytes (below); dims = {B, H | Hkv << 16, D | T << 16, P, npages},
+                               T <= 32, H % Hkv == 0; fparam[0] = scale */
+    GPUOS_OP_PAGE_COPY = 17, /* a[l][dst] = a[l][src] for the pairs aux0 = i32[n][2] of {src, dst}
+                               and every layer l of pool a[layers][npages][16 * page16] bytes (any
+                               paged cache, this one or another); dims = {n, page16, npages,
+                               layers}. Pairs with a negative page are skipped; a source may be in
+                               several pairs; a destination is in one, and is no pair's source */
+    GPUOS_OP_BUILTIN_COUNT = 18,
     GPUOS_OP_USER_FIRST = 64, /* ids >= this are free for gpuos_register_op */
     GPUOS_MAX_OPS = 256
 };
 
 #define GPUOS_F32 0
 #define GPUOS_BF16 1
+
+#define GPUOS_KV4_PAGE 32u /* tokens of a page of the 4-bit cache */
+#define GPUOS_KV4_MAX_T 32u /* query tokens of a request in one KV4_SDPA */
+/* Workspace of KV4_SDPA, whatever its sizes: 16-byte aligned, its first 8 KiB
+ * zero before the first use; every descriptor leaves them zero. Descriptors
+ * (launches, replayed graphs) that share a workspace run one after another. */
+#define GPUOS_KV4_WORKSPACE (32u << 20)
 
 /* descriptor flags */
 #define GPUOS_FLAG_FENCE 1u   /* start only after every earlier descriptor completed */
@@ -226,7 +260,7 @@ typedef struct gpuos_stats_t {
 /* Where the executor's worker warps spent their time, per op id (device
  * clock, summed over warps). Bucket b < GPUOS_OP_BUILTIN_COUNT is op id b;
  * bucket GPUOS_OP_BUILTIN_COUNT gathers every user op id. */
-#define GPUOS_PROF_BUCKETS 16
+#define GPUOS_PROF_BUCKETS 32
 #define GPUOS_PROF_FIELDS 4
 typedef struct gpuos_tile_profile {
     uint64_t tiles[GPUOS_PROF_BUCKETS];     /* tiles run */
@@ -446,6 +480,10 @@ GPUOS_API int gpuos_tile_profile_get(gpuos_ctx *ctx, gpuos_tile_profile *out);
  *                      shortens the chunks when the requests' lengths lens[b]
  *                      leave tiles idle: see the sdpa op body)
  *   vecmat             ceil(N / 8) (eight output columns per tile)
+ *   kv4_write, _read   runs of r rows (token, head), r = ceil(N Hkv / 1536) within [4, 64]
+ *   kv4_sdpa           min(1536, B * P * Hkv * row tiles) equal runs of pages
+ *                      (a row tile: 8 of the T * H / Hkv query rows of a cache head)
+ *   page_copy          layers * n * ceil(page bytes / 16384)
  *   nop / empty op     1
  * Returns GPUOS_EINVAL for a descriptor the library would reject. */
 GPUOS_API int gpuos_op_ntiles(const gpuos_desc *d, uint32_t *ntiles);
@@ -456,6 +494,11 @@ GPUOS_API int gpuos_op_ntiles(const gpuos_desc *d, uint32_t *ntiles);
  * (b, h), rounded up to 4, then fp32 partials for the finest split (32-row
  * chunks). */
 GPUOS_API size_t gpuos_sdpa_workspace_bytes(uint32_t B, uint32_t H, uint32_t D, uint32_t Lmax);
+
+/* Bytes of a 4-bit cache pool: npages * Hkv * 34 * D; 0 for sizes that the
+ * KV4 ops reject. Source: the KV-cache update of GPUOS page §3 Q2, operator
+ * library; the page's cache is dense, this one is the library's own. */
+GPUOS_API size_t gpuos_kv4_pool_bytes(uint32_t npages, uint32_t Hkv, uint32_t D);
 
 /* Source: the eager baseline of GPUOS page §3 Q3 (Table 2, latency
  * breakdown: one kernel launch per operation).

@@ -1823,6 +1823,8 @@ DEV int vecmat_tile(const gpuos_devdesc *d, uint32_t tile)
 }
 
 /* ---- table entries ----------------------------------------------------------- */
+#include "gpuos_kv4.cuh"
+
 __device__ __noinline__ int op_nop(const gpuos_devdesc *, uint32_t) { return GPUOS_ST_OK; }
 __device__ __noinline__ int op_add(const gpuos_devdesc *d, uint32_t t) { return ew_dispatch<EW_ADD>(d, t); }
 __device__ __noinline__ int op_mul(const gpuos_devdesc *d, uint32_t t) { return ew_dispatch<EW_MUL>(d, t); }
@@ -1837,10 +1839,15 @@ __device__ __noinline__ int op_rope(const gpuos_devdesc *d, uint32_t t) { return
 __device__ __noinline__ int op_kv_write(const gpuos_devdesc *d, uint32_t t) { return kv_tile(d, t); }
 __device__ __noinline__ int op_sdpa(const gpuos_devdesc *d, uint32_t t) { return sdpa_tile(d, t); }
 __device__ __noinline__ int op_vecmat(const gpuos_devdesc *d, uint32_t t) { return vecmat_tile(d, t); }
+__device__ __noinline__ int op_kv4_write(const gpuos_devdesc *d, uint32_t t) { return kv4_write_op(d, t); }
+__device__ __noinline__ int op_kv4_read(const gpuos_devdesc *d, uint32_t t) { return kv4_read_op(d, t); }
+__device__ __noinline__ int op_kv4_sdpa(const gpuos_devdesc *d, uint32_t t) { return kv4_sdpa_op(d, t); }
+__device__ __noinline__ int op_page_copy(const gpuos_devdesc *d, uint32_t t) { return page_copy_op(d, t); }
 
 __device__ gpuos_op_fn g_builtin_ops[GPUOS_OP_BUILTIN_COUNT] = {
     op_nop, op_add, op_mul, op_relu, op_gelu, op_softmax, op_layernorm,
     op_rowsum, op_rowmax, op_rowmin, op_rope, op_kv_write, op_sdpa, op_vecmat,
+    op_kv4_write, op_kv4_read, op_kv4_sdpa, op_page_copy,
 };
 
 /* The body of built-in op `kind`, inlined (the eager kernel). */
@@ -2597,11 +2604,18 @@ DEV void worker(const gpuos_exec_params &p, gpuos_devdesc *sd, uint32_t gw, uint
             const uint32_t bk = sd->op_id < GPUOS_OP_BUILTIN_COUNT ? sd->op_id : GPUOS_OP_BUILTIN_COUNT;
             const uint64_t t_fin = globaltimer();
             const uint64_t add[GPUOS_PROF_FIELDS] = {count, t_body - t_deps, t_fin - t_body, t_deps - t_found};
+            if (bk < GPUOS_PROF_SMEM_BUCKETS) {
 #pragma unroll
-            for (int f = 0; f < GPUOS_PROF_FIELDS; f++) {
-                const uint64_t v = sprof[f * GPUOS_PROF_BUCKETS + bk] + add[f];
-                sprof[f * GPUOS_PROF_BUCKETS + bk] = v;
-                ws[GPUOS_WS_PROF + f * GPUOS_PROF_BUCKETS + bk] = v;
+                for (int f = 0; f < GPUOS_PROF_FIELDS; f++) {
+                    const uint64_t v = sprof[f * GPUOS_PROF_SMEM_BUCKETS + bk] + add[f];
+                    sprof[f * GPUOS_PROF_SMEM_BUCKETS + bk] = v;
+                    ws[GPUOS_WS_PROF + f * GPUOS_PROF_BUCKETS + bk] = v;
+                }
+            } else {
+#pragma unroll
+                for (int f = 0; f < GPUOS_PROF_FIELDS; f++)
+                    atomicAdd(reinterpret_cast<unsigned long long *>(ws + GPUOS_WS_PROF + f * GPUOS_PROF_BUCKETS + bk),
+                              (unsigned long long)add[f]);
             }
             n_tiles += count;
             ws[GPUOS_WS_TILES] = n_tiles;
@@ -2628,9 +2642,9 @@ extern "C" __global__ void __launch_bounds__(GPUOS_MAX_WPB * 32, 1) gpuos_execut
 {
     __shared__ __align__(16) gpuos_devdesc sdesc[GPUOS_MAX_WPB];
     __shared__ unsigned long long s_table[GPUOS_MAX_OPS]; /* the sequencer's copy of one table slot */
-    __shared__ uint64_t s_prof[GPUOS_MAX_WPB][GPUOS_PROF_FIELDS * GPUOS_PROF_BUCKETS]; /* tile profiles */
+    __shared__ uint64_t s_prof[GPUOS_MAX_WPB][GPUOS_PROF_FIELDS * GPUOS_PROF_SMEM_BUCKETS]; /* tile profiles */
     const uint32_t warp = threadIdx.x >> 5;
-    for (uint32_t i = threadIdx.x & 31u; i < GPUOS_PROF_FIELDS * GPUOS_PROF_BUCKETS; i += 32) s_prof[warp][i] = 0;
+    for (uint32_t i = threadIdx.x & 31u; i < GPUOS_PROF_FIELDS * GPUOS_PROF_SMEM_BUCKETS; i += 32) s_prof[warp][i] = 0;
     stage_init(p.stage_bytes); /* (its block barriers also order the clearing above) */
     const uint32_t gw = blockIdx.x * (blockDim.x >> 5) + warp;
     /* Blocks 0 .. S-1 each hold one sequencer warp and nothing else (unless
@@ -2705,12 +2719,29 @@ extern "C" int gpuos_dev_preload(void)
     return 0;
 }
 
+/* One of the KV4 / page kernels on `stream` (at most 24 KB of staging: no
+ * attribute to raise). */
+template <int OP>
+static int kv4_eager_launch(const gpuos_devdesc &dd, uint32_t stage_bytes, void *stream)
+{
+    const uint32_t dyn = gpuos_dev_dyn_smem(1, stage_bytes);
+    gpuos_kv4_eager_kernel<OP><<<dd.ntiles, 32, dyn, (cudaStream_t)stream>>>(dd, stage_bytes);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
 extern "C" int gpuos_dev_eager_launch(const gpuos_desc *d, uint32_t ntiles, uint32_t stage_bytes, void *stream)
 {
     gpuos_devdesc dd;
     static_assert(sizeof(dd) == sizeof(*d), "layout");
     memcpy(&dd, d, sizeof(dd));
     dd.ntiles = ntiles;
+    switch (d->op_id) {
+    case GPUOS_OP_KV4_SDPA: return kv4_eager_launch<GPUOS_OP_KV4_SDPA>(dd, stage_bytes, stream);
+    case GPUOS_OP_KV4_WRITE: return kv4_eager_launch<GPUOS_OP_KV4_WRITE>(dd, 0, stream);
+    case GPUOS_OP_KV4_READ: return kv4_eager_launch<GPUOS_OP_KV4_READ>(dd, 0, stream);
+    case GPUOS_OP_PAGE_COPY: return kv4_eager_launch<GPUOS_OP_PAGE_COPY>(dd, 0, stream);
+    default: break;
+    }
     const uint32_t grid = (ntiles + EAGER_WPB - 1) / EAGER_WPB;
     const uint32_t dyn = gpuos_dev_dyn_smem(EAGER_WPB, stage_bytes);
     static uint32_t attr_set = 0;

@@ -402,6 +402,12 @@ static uint64_t sdpa_chunks(uint64_t BH, uint64_t Lmax)
     return ceil_div(Lmax, ch);
 }
 
+/* Sizes that the KV4 row ops share: dims = {N, Hkv, D, npages}. */
+static bool kv4_sizes_ok(uint32_t Hkv, uint32_t D, uint32_t npages)
+{
+    return Hkv >= 1 && Hkv <= 0xFFFFu && (D == 64 || D == 128) && npages >= 1 && npages <= GPUOS_KV4_MAX_PAGES;
+}
+
 /* Host-side validation (the page's "bounds checking") and tiling rule. */
 static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool user_op_known)
 {
@@ -470,6 +476,47 @@ static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool use
     case GPUOS_OP_VECMAT:
         if (m[1] && (!d->a || !d->b || !d->out || m[0] == 0)) return GPUOS_EINVAL;
         nt = ceil_div(m[1], GPUOS_VM_COLS);
+        break;
+    case GPUOS_OP_KV4_WRITE:
+    case GPUOS_OP_KV4_READ: {
+        if (d->dtype != GPUOS_F32 && d->dtype != GPUOS_BF16) return GPUOS_EINVAL;
+        const bool rd = d->op_id == GPUOS_OP_KV4_READ;
+        if (m[0]) {
+            const uint64_t second = rd ? d->aux1 : d->b;
+            if (!kv4_sizes_ok(m[1], m[2], m[3])) return GPUOS_EINVAL;
+            if (!d->a || !second || !d->out || !d->aux0 || (d->aux0 & 3u)) return GPUOS_EINVAL;
+            if (!al16(d->a) || !al16(second) || !al16(d->out)) return GPUOS_EINVAL;
+        }
+        const uint64_t rows = (uint64_t)m[0] * m[1];
+        uint64_t per = ceil_div(rows, GPUOS_KV4_TILES);
+        per = per < 4 ? 4 : (per > 64 ? 64 : per);
+        nt = ceil_div(rows, per);
+        break;
+    }
+    case GPUOS_OP_KV4_SDPA: {
+        if (d->dtype != GPUOS_BF16) return GPUOS_EINVAL;
+        if (m[0] == 0) break;
+        const uint32_t H = m[1] & 0xFFFFu, Hkv = m[1] >> 16, D = m[2] & 0xFFFFu, T = m[2] >> 16;
+        if (!kv4_sizes_ok(Hkv, D, m[4]) || H == 0 || H % Hkv || T == 0 || T > GPUOS_KV4_MAX_T) return GPUOS_EINVAL;
+        if (m[3] == 0 || m[3] > GPUOS_KV4_MAX_PAGES) return GPUOS_EINVAL;
+        if (!d->a || !d->b || !d->out || !d->aux0 || !d->aux1 || !d->aux2) return GPUOS_EINVAL;
+        if (!al16(d->a) || !al16(d->b) || !al16(d->out) || !al16(d->aux2) || ((d->aux0 | d->aux1) & 3u)) return GPUOS_EINVAL;
+        /* pages by (head, row tile): kept below 2^50, so that the products
+         * that cut them into runs fit 64 bits */
+        const uint64_t per_page = (uint64_t)Hkv * ceil_div((uint64_t)T * (H / Hkv), GPUOS_KV4_ROWS);
+        if ((uint64_t)m[0] * m[3] > (1ull << 50) / per_page) return GPUOS_EINVAL;
+        const uint64_t units = (uint64_t)m[0] * m[3] * per_page;
+        nt = units < GPUOS_KV4_TILES ? units : GPUOS_KV4_TILES;
+        break;
+    }
+    case GPUOS_OP_PAGE_COPY:
+        if (m[0]) {
+            if (!d->a || !d->aux0 || !al16(d->a) || (d->aux0 & 7u)) return GPUOS_EINVAL;
+            if (m[1] == 0 || m[2] == 0 || m[2] > 0x7FFFFFFFu || m[3] == 0) return GPUOS_EINVAL;
+            const uint64_t chunks = ceil_div(m[1], GPUOS_PAGE_CHUNK / 16);
+            if ((uint64_t)m[0] * m[3] > GPUOS_TILE_MAX / chunks) return GPUOS_EINVAL;
+            nt = (uint64_t)m[0] * m[3] * chunks;
+        }
         break;
     default:
         if (d->op_id < GPUOS_OP_USER_FIRST && d->op_id >= GPUOS_OP_BUILTIN_COUNT) return GPUOS_EINVAL;
@@ -1685,6 +1732,11 @@ int gpuos_shutdown(gpuos_ctx *c, uint32_t timeout_ms)
     }
     free_all(c);
     return rc;
+}
+
+size_t gpuos_kv4_pool_bytes(uint32_t npages, uint32_t Hkv, uint32_t D)
+{
+    return kv4_sizes_ok(Hkv, D, npages) ? (size_t)npages * Hkv * 34u * D : 0;
 }
 
 int gpuos_eager_run(const gpuos_desc *d, uint32_t count, uint32_t stage_bytes, void *stream)

@@ -26,13 +26,22 @@
 #define GPUOS_SDPA_SPLIT 1536             /* decode-attention tiles at most (unless B * H is more) */
 #define GPUOS_HEAD_GROUP 4                /* heads per RoPE / KV-write tile */
 #define GPUOS_VM_COLS 8                   /* output columns per vecmat tile (16 bytes of a row) */
+#define GPUOS_KV4_ROWS 8                  /* query rows of a KV4 attention tile (one n8 block of the matrix instruction) */
+#define GPUOS_KV4_TILES 1536              /* KV4 attention tiles (and KV4 row tiles aimed at) */
+#define GPUOS_KV4_MAX_TILES 2048          /* counters at the start of the KV4 workspace */
+#define GPUOS_KV4_MAX_PAGES (1u << 26)    /* pages of a pool, and of a table row: slots are below 2^31 */
+#define GPUOS_PAGE_CHUNK 16384            /* bytes of a page-copy tile */
 #define GPUOS_ROW_REG_MAX 4096            /* rows up to this width stay in registers */
 #define GPUOS_MAX_WPB 12
 #define GPUOS_MAX_SEQ 4 /* sequencer warps at most */
 #define GPUOS_SHORT_SLEEP_NS 256u /* longest idle sleep on the dispatch path (ring poll, dependency waits) */
 /* static shared memory of the executor kernel: descriptor copies, the
  * sequencer's table copy, per-warp tile profiles */
-#define GPUOS_EXEC_STATIC_SMEM (GPUOS_MAX_WPB * 128 + 256 * 8 + GPUOS_MAX_WPB * GPUOS_PROF_FIELDS * GPUOS_PROF_BUCKETS * 8)
+#define GPUOS_EXEC_STATIC_SMEM \
+    (GPUOS_MAX_WPB * 128 + 256 * 8 + GPUOS_MAX_WPB * GPUOS_PROF_FIELDS * GPUOS_PROF_SMEM_BUCKETS * 8)
+/* buckets kept in shared memory (more would take what the largest staging
+ * buffers need); the others are added to in the warp's row */
+#define GPUOS_PROF_SMEM_BUCKETS 16
 #define GPUOS_MAX_REGS 168 /* registers per thread: 65536 / (12 warps x 32), in steps of 8 */
 #define GPUOS_TILE_MAX (1u << 30)          /* tiles per descriptor */
 #define GPUOS_HELPERS 2048                 /* work-queue entries (helper warps) per descriptor at most */

@@ -1,0 +1,1064 @@
+/*
+ * The 4-bit paged key/value cache: attention, write, read back and page copy
+ * (included by gpuos_device.cu, whose memory, bf16 and staging helpers it
+ * uses).
+ *
+ * Page layout (one page = GPUOS_KV4_PAGE = 32 tokens of every cache head; the
+ * pool is [npages][Hkv][34 D] bytes, G = D / 32 scale groups per token):
+ *
+ *   keys          [key>>4][key>>2 & 3][key & 1][c>>3][key>>1 & 1][g][c>>1 & 3]   16 D bytes
+ *   values        [key>>4][c>>2][key>>2 & 3][key & 3][g][c>>1 & 1]               16 D bytes
+ *   key scales    [key][g]                                                          D bytes
+ *   value scales  [key>>4][key>>2 & 3][g][key & 3]                                  D bytes
+ *
+ * (c = channel within its group g; two neighbouring channels to a byte, the
+ * even one low). A code is e2m1: sign, and {0, .5, 1, 1.5, 2, 3, 4, 6}; a
+ * scale byte is an exponent + 127 (255: the group held a NaN or infinity).
+ * 4.25 bits an element.
+ *
+ * The order is that of the matrix fragments. mma.m16n8k16 is used with the
+ * cache as its A operand (S^T = K q^T and O^T = V^T p^T): 16 keys or 16
+ * channels against 8 query rows, so up to eight query rows that share a cache
+ * head cost one pass over it, and a lane's codes of a 16-key tile are 8 G
+ * contiguous bytes of keys and of values: one or two 16-byte loads, the whole
+ * warp's contiguous. Row m of S^T (and k of O^T's product) stands for key
+ * 4 (m>>1 & 3) + (m & 1) + 2 (m >> 3): then lane (i = lane / 4, j = lane % 4)
+ * needs keys 4 j .. 4 j + 3 of the values.
+ */
+#ifndef GPUOS_KV4_CUH
+#define GPUOS_KV4_CUH
+
+#include <cuda_fp16.h>
+
+DEV constexpr uint32_t kv4_page_bytes(uint32_t D) { return 34u * D; }
+
+/* 2^e for an exponent in [-126, 127] */
+DEV float kv4_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+/* Four bytes of code pairs -> four f16x2 (exact); low nibble in the low half. */
+DEV void kv4_decode4(uint32_t w, uint32_t (&o)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+/* Eight values -> eight codes, value 0 in the lowest nibble; nearest, ties to
+ * the even code (|x| <= 6 but for a clamped scale, where 6 is the answer). */
+DEV uint32_t kv4_encode8(const float (&x)[8])
+{
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return w;
+}
+DEV void kv4_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+DEV uint32_t kv4_trans8x8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+DEV uint32_t kv4_pack_h2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+DEV uint32_t kv4_hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+DEV float kv4_ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+/* ---------------------------------------------------------------------------
+ * Attention: o[r] = sum_n softmax_n(scale q[r].K[n]) V[n] over the keys that
+ * row r sees. The T g query rows of a request that share a cache head
+ * (g = H / Hkv; row r = t g + hh) are cut into row tiles of 8 NT rows.
+ *
+ * Work is counted in units of one page of one (request, head, row tile), a
+ * request of length 0 being one unit; the units are numbered in that order
+ * and cut into equal runs, one per warp, whatever the requests' lengths. A
+ * run that ends inside an item leaves a partial state, merged with its
+ * neighbours' (below).
+ *
+ * Numerics. q is scaled by a power of two for each row to [128, 256) and held
+ * in f16: exact for the bf16 values within 2^-21 of the row's largest, and
+ * off by at most 2^-32 of it below. Codes are exact in f16; the products are
+ * summed in fp32 for each scale group, and the groups' sums are scaled and
+ * added in fp32. p 2^7 is rounded to f16 (11 bits; bf16's 8 would show in a
+ * bf16 output), and multiplied there by 2^(b - E + 8), b the value's scale
+ * exponent and E the largest met so far in its group: exact unless the
+ * product falls below 2^-14, 2^29 below the largest possible. The softmax's
+ * maximum and sum and the output accumulators are fp32.
+ * ------------------------------------------------------------------------- */
+struct Kv4Args {
+    const uint16_t *q;
+    const unsigned char *pool;
+    const int32_t *lens;
+    const int32_t *table;
+    uint16_t *out;
+    uint32_t B, H, Hkv, T, g, RT, P, npages;
+    float scale; /* times log2 e */
+};
+DEV void kv4_args(const gpuos_devdesc *d, uint32_t rows_per_tile, Kv4Args &a)
+{
+    a.q = reinterpret_cast<const uint16_t *>(d->a);
+    a.pool = reinterpret_cast<const unsigned char *>(d->b);
+    a.lens = reinterpret_cast<const int32_t *>(d->aux0);
+    a.table = reinterpret_cast<const int32_t *>(d->aux1);
+    a.out = reinterpret_cast<uint16_t *>(d->out);
+    a.B = d->dims[0];
+    a.H = d->dims[1] & 0xFFFFu;
+    a.Hkv = d->dims[1] >> 16;
+    a.T = d->dims[2] >> 16;
+    a.g = a.H / a.Hkv;
+    a.RT = (a.T * a.g + rows_per_tile - 1) / rows_per_tile;
+    a.P = d->dims[3];
+    a.npages = d->dims[4];
+    a.scale = d->fparam[0] * 1.4426950408889634f;
+}
+/* Pages of a request; a length that its table row cannot hold counts as one
+ * unit that does nothing (bad). */
+DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len, bool &bad)
+{
+    bad = len < 0 || (uint64_t)len > (uint64_t)a.P * GPUOS_KV4_PAGE;
+    return bad || len == 0 ? 1u : ((uint32_t)len + GPUOS_KV4_PAGE - 1u) / GPUOS_KV4_PAGE;
+}
+DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len)
+{
+    bool bad;
+    return kv4_pages(a, len, bad);
+}
+
+/* A warp's place in the work. */
+struct Kv4Pos {
+    uint32_t b, item; /* request; head * RT + row tile */
+    uint32_t page, np; /* next page, the request's pages */
+    int32_t len;
+    uint64_t first; /* first unit of the item */
+};
+/* All units of the call (every lane). */
+DEV uint64_t kv4_units(const Kv4Args &a)
+{
+    unsigned long long n = 0;
+    for (uint32_t i = lane_id(); i < a.B; i += 32) n += kv4_pages(a, __ldcg(a.lens + i));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    return n * a.Hkv * a.RT;
+}
+/* The place of unit u (u < the number of units). */
+DEV void kv4_seek(const Kv4Args &a, uint64_t u, Kv4Pos &p)
+{
+    const uint32_t lane = lane_id(), HR = a.Hkv * a.RT;
+    unsigned long long base = 0;
+    for (uint32_t i0 = 0; i0 < a.B; i0 += 32) {
+        const uint32_t i = i0 + lane;
+        const int32_t len = i < a.B ? __ldcg(a.lens + i) : 0;
+        const unsigned long long cnt = i < a.B ? (unsigned long long)kv4_pages(a, len) * HR : 0ull;
+        unsigned long long incl = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= (uint32_t)o) incl += v;
+        }
+        const unsigned long long lo = base + incl - cnt;
+        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, u >= lo && u < lo + cnt);
+        if (bal) {
+            const int src = __ffs(bal) - 1;
+            p.b = i0 + (uint32_t)src;
+            p.len = __shfl_sync(0xFFFFFFFFu, len, src);
+            p.np = kv4_pages(a, p.len);
+            const uint64_t lo_b = __shfl_sync(0xFFFFFFFFu, lo, src);
+            const uint64_t off = u - lo_b;
+            p.item = (uint32_t)(off / p.np);
+            p.page = (uint32_t)(off - (uint64_t)p.item * p.np);
+            p.first = lo_b + (uint64_t)p.item * p.np;
+            return;
+        }
+        base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    p.b = a.B; /* not reached for u < kv4_units() */
+    p.len = 0;
+    p.np = 1;
+    p.item = p.page = 0;
+    p.first = u;
+}
+/* The next item. */
+DEV void kv4_next(const Kv4Args &a, Kv4Pos &p)
+{
+    p.first += p.np;
+    p.page = 0;
+    if (++p.item < a.Hkv * a.RT) return;
+    p.item = 0;
+    if (++p.b >= a.B) return;
+    p.len = __ldcg(a.lens + p.b);
+    p.np = kv4_pages(a, p.len);
+}
+
+/* One item's running state in a warp: lane (i, j) holds query rows
+ * 8 nt + 2 j + {0, 1} (index r) and channels 32 g + 4 i + {0..3} of O^T. */
+template <int G, int NT>
+struct Kv4State {
+    uint32_t q[NT][G][4]; /* f16x2 of row 8 nt + i: channels 32 g + 8 j + {0..7} */
+    float f[NT][2];       /* score factor of rows 2 j, 2 j + 1: scale log2(e) 2^k */
+    float m[NT][2];       /* running maximum (log2) less 7, equal in the lanes of a row */
+    float l[NT][2];       /* this lane's part of the running sum */
+    float acc[NT][G][2][4];
+    uint32_t E[G]; /* largest value-scale exponent met in each group */
+    uint32_t lim[NT][2]; /* keys that the row sees */
+    uint32_t min_lim;    /* least of them over the tile's rows */
+};
+
+DEV uint32_t kv4_row_limit(const Kv4Args &a, int32_t len, uint32_t r)
+{
+    if (r >= a.T * a.g) return (uint32_t)len;
+    const int64_t n = (int64_t)len - (int64_t)a.T + 1 + (int64_t)(r / a.g);
+    return n > 0 ? (uint32_t)n : 0u;
+}
+
+template <int G, int NT>
+DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, Kv4State<G, NT> &s)
+{
+    constexpr uint32_t D = 32u * G;
+    const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
+    const uint32_t h = p.item / a.RT, r0 = (p.item - h * a.RT) * 8u * NT;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        const uint32_t r = r0 + 8u * nt + i;
+        uint4 raw[G];
+        const bool have = r < a.T * a.g;
+        const uint32_t t = r / a.g, hh = r - t * a.g;
+        const uint16_t *qr = a.q + (((uint64_t)p.b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 8u * j;
+#pragma unroll
+        for (int g = 0; g < G; g++)
+            raw[g] = have ? __ldcg(reinterpret_cast<const uint4 *>(qr + 32 * g)) : make_uint4(0, 0, 0, 0);
+        float top = 0.0f;
+        bool odd = false; /* a NaN or infinity in the row: left as it is */
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            float x[8];
+            unpack8(raw[g], x);
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                top = fmaxf(top, fabsf(x[c]));
+                odd |= !(fabsf(x[c]) < INFINITY);
+            }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const uint32_t oddrow = __ballot_sync(0xFFFFFFFFu, odd) >> (4u * i) & 15u;
+        /* k: top 2^-k in [128, 256); both 2^k and 2^-k stay normal numbers */
+        int k = (int)(__float_as_uint(top) >> 23) - 127 - 7;
+        if (oddrow || top == 0.0f) k = 0;
+        k = max(-126, min(126, k));
+        const float down = kv4_pow2(-k);
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            float x[8];
+            unpack8(raw[g], x);
+#pragma unroll
+            for (int c = 0; c < 4; c++) s.q[nt][g][c] = kv4_pack_h2(x[2 * c] * down, x[2 * c + 1] * down);
+        }
+        const float f = a.scale * kv4_pow2(k);
+        s.f[nt][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * j);
+        s.f[nt][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * j + 4);
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            s.m[nt][c] = -INFINITY;
+            s.l[nt][c] = 0.0f;
+            s.lim[nt][c] = kv4_row_limit(a, p.len, r0 + 8u * nt + 2u * j + c);
+        }
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int c = 0; c < 4; c++) s.acc[nt][g][u][c] = 0.0f;
+    }
+#pragma unroll
+    for (int g = 0; g < G; g++) s.E[g] = 0;
+    s.min_lim = kv4_row_limit(a, p.len, r0); /* rows come in order of t */
+}
+
+template <bool GLOBAL>
+DEV uint4 kv4_ld16(const unsigned char *p)
+{
+    if (GLOBAL) return __ldcg(reinterpret_cast<const uint4 *>(p));
+    return *reinterpret_cast<const uint4 *>(p);
+}
+template <bool GLOBAL>
+DEV uint2 kv4_ld8(const unsigned char *p)
+{
+    if (GLOBAL) return __ldcg(reinterpret_cast<const uint2 *>(p));
+    return *reinterpret_cast<const uint2 *>(p);
+}
+template <bool GLOBAL>
+DEV uint32_t kv4_ld4(const unsigned char *p)
+{
+    if (GLOBAL) return __ldcg(reinterpret_cast<const uint32_t *>(p));
+    return *reinterpret_cast<const uint32_t *>(p);
+}
+/* The bytes of a word of four keys from key0 on that are below n. */
+DEV uint32_t kv4_keep(uint32_t key0, uint32_t n)
+{
+    if (key0 + 4u <= n) return 0xFFFFFFFFu;
+    if (key0 >= n) return 0u;
+    return (1u << (8u * (n - key0))) - 1u;
+}
+
+/* One page: keys [base, base + 32) of the item, of which those below `valid`
+ * exist (the rest of a request's last page holds anything). */
+template <int G, int NT, bool GLOBAL>
+DEV void kv4_page(const unsigned char *pg, uint32_t base, uint32_t valid, Kv4State<G, NT> &s)
+{
+    constexpr uint32_t D = 32u * G;
+    const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
+    const uint32_t nv = valid > base ? min(valid - base, (uint32_t)GPUOS_KV4_PAGE) : 0u; /* existing keys of the page */
+
+    /* ---- scores: S^T tile t = keys 16 t .. 16 t + 15 against the rows ---- */
+    float sc[2][NT][4];
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        const uint32_t k0 = 16u * t + 4u * (i >> 1) + (i & 1u); /* the lane's keys: k0 (c 0, 1) and k0 + 2 (c 2, 3) */
+        uint32_t kw[2][G], ks[2];
+        const unsigned char *kp = pg + (uint32_t)t * 8u * D + lane * 8u * G;
+        if (G == 4) {
+            const uint4 x = kv4_ld16<GLOBAL>(kp), y = kv4_ld16<GLOBAL>(kp + 16);
+            kw[0][0] = x.x; kw[0][1] = x.y; kw[0][G - 2] = x.z; kw[0][G - 1] = x.w;
+            kw[1][0] = y.x; kw[1][1] = y.y; kw[1][G - 2] = y.z; kw[1][G - 1] = y.w;
+            ks[0] = kv4_ld4<GLOBAL>(pg + 32u * D + k0 * 4u);
+            ks[1] = kv4_ld4<GLOBAL>(pg + 32u * D + (k0 + 2u) * 4u);
+        } else {
+            const uint4 x = kv4_ld16<GLOBAL>(kp);
+            kw[0][0] = x.x; kw[0][1] = x.y;
+            kw[1][0] = x.z; kw[1][1] = x.w;
+            /* two bytes a key: the word of keys k0 & ~1, k0 | 1 */
+            const uint32_t odd = 16u * (k0 & 1u);
+            ks[0] = kv4_ld4<GLOBAL>(pg + 32u * D + (k0 & ~1u) * 2u) >> odd;
+            ks[1] = kv4_ld4<GLOBAL>(pg + 32u * D + ((k0 & ~1u) + 2u) * 2u) >> odd;
+        }
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            uint32_t x0[4], x1[4];
+            kv4_decode4(kw[0][g], x0);
+            kv4_decode4(kw[1][g], x1);
+            /* exponent byte -> the float 2^(byte - 127) (byte 0 gives 0: such
+             * a group's values are below 2^-124; 255 gives infinity, and NaN
+             * with the zero codes that the write leaves beside it) */
+            const float s0 = __uint_as_float((ks[0] >> (8 * g) & 255u) << 23);
+            const float s1 = __uint_as_float((ks[1] >> (8 * g) & 255u) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                kv4_mma(c, x0[0], x1[0], x0[1], x1[1], s.q[nt][g][0], s.q[nt][g][1]);
+                kv4_mma(c, x0[2], x1[2], x0[3], x1[3], s.q[nt][g][2], s.q[nt][g][3]);
+                if (g == 0) {
+                    sc[t][nt][0] = c[0] * s0; sc[t][nt][1] = c[1] * s0;
+                    sc[t][nt][2] = c[2] * s1; sc[t][nt][3] = c[3] * s1;
+                } else {
+                    sc[t][nt][0] = fmaf(c[0], s0, sc[t][nt][0]); sc[t][nt][1] = fmaf(c[1], s0, sc[t][nt][1]);
+                    sc[t][nt][2] = fmaf(c[2], s1, sc[t][nt][2]); sc[t][nt][3] = fmaf(c[3], s1, sc[t][nt][3]);
+                }
+            }
+        }
+    }
+    const bool masked = base + GPUOS_KV4_PAGE > s.min_lim || nv < GPUOS_KV4_PAGE; /* warp-uniform */
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) sc[t][nt][c] *= s.f[nt][c & 1];
+    if (masked) {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const uint32_t key = 16u * t + 4u * (i >> 1) + (i & 1u) + (c & 2u);
+                    if (key >= nv || base + key >= s.lim[nt][c & 1]) sc[t][nt][c] = -INFINITY;
+                }
+    }
+
+    /* ---- the largest value scale of each group ---- */
+    const bool tail = nv < GPUOS_KV4_PAGE;
+    uint32_t vw[2][G]; /* scales of keys 16 t + 4 j .. + 3, group g */
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        const unsigned char *vp = pg + 33u * D + ((uint32_t)t * 4u + j) * 4u * G;
+        if (G == 4) {
+            const uint4 x = kv4_ld16<GLOBAL>(vp);
+            vw[t][0] = x.x; vw[t][1] = x.y; vw[t][G - 2] = x.z; vw[t][G - 1] = x.w;
+        } else {
+            const uint2 x = kv4_ld8<GLOBAL>(vp);
+            vw[t][0] = x.x; vw[t][1] = x.y;
+        }
+    }
+    if (tail) { /* what lies behind the last key is anything: no scale */
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            const uint32_t keep = kv4_keep(16u * t + 4u * j, nv);
+#pragma unroll
+            for (int g = 0; g < G; g++) vw[t][g] &= keep;
+        }
+    }
+    float up[G]; /* what the accumulators are multiplied by */
+    uint32_t grow = 0;
+    {
+        uint32_t mx[G];
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            mx[g] = __vmaxu4(vw[0][g], vw[1][g]);
+            grow |= __vcmpgtu4(mx[g], s.E[g] * 0x01010101u);
+        }
+        grow = __any_sync(0xFFFFFFFFu, grow != 0u);
+        if (grow) {
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                uint32_t x = mx[g];
+                x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                x = __vmaxu4(x, x >> 16);
+                x = max(x & 255u, x >> 8 & 255u);
+                if (x == 255u) {
+                    /* a NaN group: NaN for the rows that see such a key; the
+                     * scale itself is dropped */
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        const uint32_t bad = __vcmpeq4(vw[t][g], 0xFFFFFFFFu);
+                        uint32_t lo = 4u * GPUOS_KV4_PAGE; /* the first such key of the page */
+                        if (bad) lo = 16u * t + 4u * j + ((uint32_t)__ffs((int)bad) - 1u) / 8u;
+                        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 1));
+                        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 2));
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int c = 0; c < 4; c++)
+                                if (lo < GPUOS_KV4_PAGE && base + lo < s.lim[nt][c & 1]) {
+                                    s.acc[nt][g][0][c] = NAN;
+                                    s.acc[nt][g][1][c] = NAN;
+                                }
+                        vw[t][g] &= ~bad;
+                    }
+                    x = __vmaxu4(vw[0][g], vw[1][g]);
+                    x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                    x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                    x = __vmaxu4(x, x >> 16);
+                    x = max(x & 255u, x >> 8 & 255u);
+                }
+                const uint32_t e = max(s.E[g], x);
+                /* 2^(E - e); below 2^-126 nothing is left of it */
+                up[g] = (int)(s.E[g] + 127u) > (int)e ? kv4_pow2((int)s.E[g] - (int)e) : 0.0f;
+                s.E[g] = e;
+            }
+        }
+    }
+
+    /* ---- online softmax ---- */
+    uint32_t pb[2][NT][2]; /* p^T: B fragments of the second product */
+    float alpha[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            float mx = fmaxf(fmaxf(sc[0][nt][r], sc[0][nt][r + 2]), fmaxf(sc[1][nt][r], sc[1][nt][r + 2]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            const float mn = fmaxf(s.m[nt][r], mx - 7.0f);
+            const float mu = mn == -INFINITY ? 0.0f : mn;
+            alpha[nt][r] = kv4_ex2(s.m[nt][r] - mu);
+            s.m[nt][r] = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                sc[t][nt][r] = kv4_ex2(sc[t][nt][r] - mu);
+                sc[t][nt][r + 2] = kv4_ex2(sc[t][nt][r + 2] - mu);
+                sum += sc[t][nt][r] + sc[t][nt][r + 2];
+            }
+            s.l[nt][r] = fmaf(s.l[nt][r], alpha[nt][r], sum);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            pb[t][nt][0] = kv4_trans8x8(kv4_pack_h2(sc[t][nt][0], sc[t][nt][1]));
+            pb[t][nt][1] = kv4_trans8x8(kv4_pack_h2(sc[t][nt][2], sc[t][nt][3]));
+        }
+    }
+    /* ---- O^T += V^T p^T ---- */
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+        const float ug = grow ? up[g] : 1.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const float x = alpha[nt][c & 1] * ug;
+                s.acc[nt][g][0][c] *= x;
+                s.acc[nt][g][1][c] *= x;
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        const unsigned char *vp = pg + 16u * D + (uint32_t)t * 8u * D + lane * 8u * G;
+        uint32_t w[4][G / 2]; /* key 4 j + slot: groups 2 w, 2 w + 1 */
+        if (G == 4) {
+            const uint4 x = kv4_ld16<GLOBAL>(vp), y = kv4_ld16<GLOBAL>(vp + 16);
+            w[0][0] = x.x; w[0][G / 2 - 1] = x.y; w[1][0] = x.z; w[1][G / 2 - 1] = x.w;
+            w[2][0] = y.x; w[2][G / 2 - 1] = y.y; w[3][0] = y.z; w[3][G / 2 - 1] = y.w;
+        } else {
+            const uint4 x = kv4_ld16<GLOBAL>(vp);
+            w[0][0] = x.x; w[1][0] = x.y; w[2][0] = x.z; w[3][0] = x.w;
+        }
+#pragma unroll
+        for (int x = 0; x < G / 2; x++) {
+            /* bytes of (key, key + 1) pairs of one channel: even channels, odd channels */
+            uint32_t e01[4], o01[4], e23[4], o23[4];
+            kv4_decode4((w[0][x] & 0x0F0F0F0Fu) | ((w[1][x] << 4) & 0xF0F0F0F0u), e01);
+            kv4_decode4(((w[0][x] >> 4) & 0x0F0F0F0Fu) | (w[1][x] & 0xF0F0F0F0u), o01);
+            kv4_decode4((w[2][x] & 0x0F0F0F0Fu) | ((w[3][x] << 4) & 0xF0F0F0F0u), e23);
+            kv4_decode4(((w[2][x] >> 4) & 0x0F0F0F0Fu) | (w[3][x] & 0xF0F0F0F0u), o23);
+#pragma unroll
+            for (int gg = 0; gg < 2; gg++) {
+                const int g = 2 * x + gg;
+                /* f16x2 of 2^(b - E + 8): exponent field b - E + 23, zero below 1 */
+                const uint32_t bias = (23u - s.E[g]) & 0xFFFFu, bias2 = bias | bias << 16;
+                const uint32_t s01 = __viaddmax_s16x2(__byte_perm(vw[t][g], 0u, 0x4140), bias2, 0u) << 10;
+                const uint32_t s23 = __viaddmax_s16x2(__byte_perm(vw[t][g], 0u, 0x4342), bias2, 0u) << 10;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    const uint32_t b0 = kv4_hmul2(pb[t][nt][0], s01), b1 = kv4_hmul2(pb[t][nt][1], s23);
+                    kv4_mma(s.acc[nt][g][0], e01[2 * gg], o01[2 * gg], e23[2 * gg], o23[2 * gg], b0, b1);
+                    kv4_mma(s.acc[nt][g][1], e01[2 * gg + 1], o01[2 * gg + 1], e23[2 * gg + 1], o23[2 * gg + 1], b0, b1);
+                }
+            }
+        }
+    }
+}
+
+/* End of a run within an item: l summed over the lanes of a row, acc brought
+ * to the mean of the values under this run's weights. */
+template <int G, int NT>
+DEV void kv4_finish(Kv4State<G, NT> &s)
+{
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            float l = s.l[nt][r];
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+            s.l[nt][r] = l;
+        }
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            /* 2^(E - 127 - 8) in two factors (E - 135 may be below -126) */
+            const int e = (int)s.E[g] - 135, e1 = e / 2;
+            const float p1 = kv4_pow2(e1), p2 = kv4_pow2(e - e1);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const float l = s.l[nt][c & 1], inv = l != 0.0f ? 1.0f / l : 0.0f;
+                s.acc[nt][g][0][c] = s.acc[nt][g][0][c] * inv * p1 * p2;
+                s.acc[nt][g][1][c] = s.acc[nt][g][1][c] * inv * p1 * p2;
+            }
+        }
+    }
+}
+/* Rows that see no key are zero; the sum of a row that sees some is zero only
+ * when no score is a number. */
+DEV float kv4_empty(uint32_t lim) { return lim ? NAN : 0.0f; }
+
+template <int G, int NT>
+DEV void kv4_store(const Kv4Args &a, const Kv4Pos &p, const Kv4State<G, NT> &s)
+{
+    constexpr uint32_t D = 32u * G;
+    const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
+    const uint32_t h = p.item / a.RT, r0 = (p.item - h * a.RT) * 8u * NT;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            const uint32_t r = r0 + 8u * nt + 2u * j + c;
+            if (r >= a.T * a.g) continue;
+            const uint32_t t = r / a.g, hh = r - t * a.g;
+            uint16_t *o = a.out + (((uint64_t)p.b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 4u * i;
+            const bool none = s.l[nt][c] == 0.0f;
+            const float z = kv4_empty(s.lim[nt][c]);
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                uint2 w;
+                w.x = pack_bf2(none ? z : s.acc[nt][g][0][c], none ? z : s.acc[nt][g][0][c + 2]);
+                w.y = pack_bf2(none ? z : s.acc[nt][g][1][c], none ? z : s.acc[nt][g][1][c + 2]);
+                *reinterpret_cast<uint2 *>(o + 32 * g) = w;
+            }
+        }
+}
+
+/* A partial state in memory: NT x 4 float4 {m0, l0, m1, l1} (by j), then the
+ * accumulators [nt][g][r][lane] as float4 of the lane's four channels. */
+template <int G, int NT>
+struct Kv4Part {
+    static constexpr uint32_t floats = NT * 16u + NT * G * 256u;
+};
+template <int G, int NT>
+DEV void kv4_part_store(float *part, const Kv4State<G, NT> &s)
+{
+    const uint32_t lane = lane_id(), j = lane & 3u;
+    float4 *p4 = reinterpret_cast<float4 *>(part);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        if (lane < 4) __stcg(p4 + nt * 4 + j, make_float4(s.m[nt][0], s.l[nt][0], s.m[nt][1], s.l[nt][1]));
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int r = 0; r < 2; r++)
+                __stcg(p4 + NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane,
+                       make_float4(s.acc[nt][g][0][r], s.acc[nt][g][0][r + 2], s.acc[nt][g][1][r], s.acc[nt][g][1][r + 2]));
+    }
+}
+/* s := the merge of s and the stored state; `left`: s comes first (the order
+ * of the arithmetic is that of the keys, whoever does it). */
+template <int G, int NT>
+DEV void kv4_part_merge(const float *part, Kv4State<G, NT> &s, bool left)
+{
+    const uint32_t lane = lane_id(), j = lane & 3u;
+    const float4 *p4 = reinterpret_cast<const float4 *>(part);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        const float4 ml = __ldcg(p4 + nt * 4 + j);
+        float4 x[G][2];
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int r = 0; r < 2; r++) x[g][r] = __ldcg(p4 + NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane);
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            const float mo = r ? ml.z : ml.x, lo = r ? ml.w : ml.y;
+            const float mn = fmaxf(s.m[nt][r], mo), mu = mn == -INFINITY ? 0.0f : mn;
+            const float ws = s.l[nt][r] * kv4_ex2(s.m[nt][r] - mu), wo = lo * kv4_ex2(mo - mu);
+            const float l = left ? ws + wo : wo + ws, inv = l != 0.0f ? 1.0f / l : 0.0f;
+            const float a0 = ws * inv, b0 = wo * inv;
+            s.m[nt][r] = mn;
+            s.l[nt][r] = l;
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const float o4[4] = {x[g][r].x, x[g][r].y, x[g][r].z, x[g][r].w};
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    float &v = s.acc[nt][g][c >> 1][r + 2 * (c & 1)];
+                    v = left ? fmaf(o4[c], b0, v * a0) : fmaf(v, a0, o4[c] * b0);
+                }
+            }
+        }
+    }
+}
+
+/* The pages of one run within an item, [p.page, end): into the state. With
+ * staging the pages arrive by bulk copies into the two halves of the warp's
+ * buffer in turn. */
+template <int G, int NT>
+DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT> &s)
+{
+    constexpr uint32_t PB = kv4_page_bytes(32u * G);
+    const uint32_t lane = lane_id(), h = p.item / a.RT;
+    const int32_t *row = a.table + (uint64_t)p.b * a.P;
+    const uint64_t stride = (uint64_t)a.Hkv * PB;
+    const unsigned char *pool = a.pool + (uint64_t)h * PB;
+    const bool staged = stage_hdr()->stage_bytes >= 2u * PB;
+    WarpStage *w = warp_stage();
+    unsigned char *buf = warp_stage_buf();
+    int status = GPUOS_ST_OK;
+    uint32_t phs = staged ? w->phase[0] | w->phase[1] << 1 : 0u;
+    /* page ids, 32 at a time in the warp's lanes; one that is not in the pool
+     * stands for no keys (page 0 is read and masked) */
+    const uint32_t n = end - p.page;
+    int32_t ids = 0, ids_next = 0;
+    auto load_ids = [&](uint32_t k) { return p.page + k + lane < end ? __ldcg(row + p.page + k + lane) : 0; };
+    ids = load_ids(0);
+    auto issue = [&](uint32_t k, int32_t id) {
+        if (lane == 0) {
+            mbar_expect(&w->mbar[k & 1u], PB);
+            bulk_g2s(buf + (k & 1u) * PB, pool + (uint64_t)((uint32_t)id < a.npages ? (uint32_t)id : 0u) * stride, PB,
+                     &w->mbar[k & 1u]);
+        }
+    };
+    if (staged) {
+        asm volatile("fence.proxy.async;" ::: "memory"); /* pages written by other ops, slots read by the last run */
+        issue(0, __shfl_sync(0xFFFFFFFFu, ids, 0));
+        if (n > 1) issue(1, __shfl_sync(0xFFFFFFFFu, ids, 1));
+    }
+    for (uint32_t k = 0; k < n; k++) {
+        if ((k & 31u) == 0) {
+            if (k) ids = ids_next;
+            ids_next = load_ids(k + 32);
+        }
+        const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k & 31u);
+        const bool there = (uint32_t)id < a.npages;
+        if (!there) status = GPUOS_ST_BAD_ARGS;
+        const uint32_t base = (p.page + k) * GPUOS_KV4_PAGE, valid = there ? (uint32_t)p.len : 0u;
+        if (staged) {
+            const uint32_t hb = k & 1u;
+            if (!mbar_wait(&w->mbar[hb], phs >> hb & 1u)) {
+                /* leave no copy in flight: wait once more (bounded) for this
+                 * half and for the other one if it has a copy out */
+                mbar_wait(&w->mbar[hb], phs >> hb & 1u);
+                phs ^= 1u << hb;
+                if (k + 1 < n) {
+                    mbar_wait(&w->mbar[hb ^ 1u], phs >> (hb ^ 1u) & 1u);
+                    phs ^= 1u << (hb ^ 1u);
+                }
+                status = GPUOS_ST_COPY_TIMEOUT;
+                break;
+            }
+            phs ^= 1u << hb;
+            kv4_page<G, NT, false>(buf + hb * PB, base, valid, s);
+            if (k + 2 < n) {
+                const int32_t nx = (k & 31u) < 30u ? __shfl_sync(0xFFFFFFFFu, ids, (k + 2) & 31u)
+                                                   : __shfl_sync(0xFFFFFFFFu, ids_next, (k + 2) & 31u);
+                __syncwarp(); /* every lane is done with this half */
+                if (lane == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                issue(k + 2, nx);
+            }
+        } else {
+            kv4_page<G, NT, true>(pool + (uint64_t)(there ? (uint32_t)id : 0u) * stride, base, valid, s);
+        }
+    }
+    if (staged) {
+        __syncwarp();
+        if (lane == 0) {
+            w->phase[0] = phs & 1u;
+            w->phase[1] = phs >> 1 & 1u;
+        }
+        __syncwarp();
+    }
+    return status;
+}
+
+/* The workspace: GPUOS_KV4_MAX_TILES counters, then two partial states for
+ * each tile (an item that began before the tile, an item that ends after it). */
+DEV uint32_t *kv4_counters(const gpuos_devdesc *d) { return reinterpret_cast<uint32_t *>(d->aux2); }
+template <int G, int NT>
+DEV float *kv4_slot(const gpuos_devdesc *d, uint32_t tile, uint32_t which)
+{
+    return reinterpret_cast<float *>(d->aux2) + GPUOS_KV4_MAX_TILES + ((uint64_t)tile * 2u + which) * Kv4Part<G, NT>::floats;
+}
+
+/* One executor tile: a warp's run of units. Partial states of an item meet in
+ * a binary tree over its tiles, numbered from the item's first: at the node
+ * that splits at s the second to arrive merges the two halves and goes on, so
+ * the merge's depth is the logarithm of the tiles and no tile waits. */
+template <int G, int NT>
+DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
+{
+    Kv4Args a;
+    kv4_args(d, 8u * NT, a);
+    const uint64_t W = kv4_units(a);
+    const uint64_t nt = d->ntiles < W ? d->ntiles : W;
+    if (tile >= nt) return GPUOS_ST_OK;
+    uint64_t u = W * tile / nt;
+    const uint64_t u1 = W * (tile + 1ull) / nt;
+    Kv4Pos p;
+    kv4_seek(a, u, p);
+    int status = GPUOS_ST_OK;
+    while (u < u1) {
+        const uint32_t end = (uint32_t)(u1 - u < p.np - p.page ? p.page + (u1 - u) : p.np);
+        const uint32_t begin = p.page;
+        bool bad;
+        (void)kv4_pages(a, p.len, bad);
+        if (bad) {
+            status = GPUOS_ST_BAD_ARGS; /* the request's rows are left as they were */
+        } else {
+            Kv4State<G, NT> s;
+            kv4_begin(a, p, s);
+            const int st = p.len ? kv4_run(a, p, end, s) : GPUOS_ST_OK;
+            if (st) status = st;
+            kv4_finish(s);
+            if (begin != 0 || end != p.np) {
+                const uint32_t first = (uint32_t)(((p.first + 1) * nt - 1) / W);
+                const uint32_t F = (uint32_t)(((p.first + p.np) * nt - 1) / W) - first + 1;
+                uint32_t c = tile - first;
+                bool done = true;
+                for (uint32_t step = 1; step < F; step <<= 1) {
+                    const uint32_t other = c ^ step;
+                    if (other < F) {
+                        uint32_t *cnt = kv4_counters(d) + first + (c | step);
+                        kv4_part_store<G, NT>(kv4_slot<G, NT>(d, first + c, c == 0), s);
+                        __syncwarp();
+                        uint32_t old = 0;
+                        if (lane_id() == 0) old = atom_add_acq_rel_gpu32(cnt, 1u);
+                        old = __shfl_sync(0xFFFFFFFFu, old, 0);
+                        if (old == 0) {
+                            done = false;
+                            break;
+                        }
+                        __syncwarp();
+                        kv4_part_merge<G, NT>(kv4_slot<G, NT>(d, first + other, other == 0), s, c < other);
+                        if (lane_id() == 0) *cnt = 0; /* left zero for the next call */
+                    }
+                    c &= ~step;
+                }
+                if (done) kv4_store(a, p, s);
+            } else {
+                kv4_store(a, p, s);
+            }
+        }
+        u += end - begin;
+        kv4_next(a, p);
+    }
+    return status;
+}
+
+DEV int kv4_sdpa_op(const gpuos_devdesc *d, uint32_t tile)
+{
+    if (d->dims[0] == 0) return GPUOS_ST_OK;
+    return (d->dims[2] & 0xFFFFu) == 128 ? kv4_sdpa_tile<4, 1>(d, tile) : kv4_sdpa_tile<2, 1>(d, tile);
+}
+
+/* ---------------------------------------------------------------------------
+ * Write and read back. Row (n, h) is token n's head h: keys and values of a
+ * row go to (come from) slot slots[n] = page * 32 + key. A lane takes eight
+ * neighbouring channels: one word of the keys' codes, two half words of the
+ * values'. A negative slot is a hole: not written, read as zeros.
+ *
+ * Scale: the least e >= -127 with max |x| <= 6 2^e (at most 125, so that
+ * 6 2^e is finite: above it the largest code stands for what is larger).
+ * x 2^-e is exact, so a code is the correctly rounded one.
+ * ------------------------------------------------------------------------- */
+struct Kv4Row {
+    unsigned char *k, *v, *ks, *vs; /* the lane's key word, first value half word, scale bytes */
+};
+template <int G>
+DEV Kv4Row kv4_row(unsigned char *pool, uint32_t H, uint32_t slot, uint32_t h, uint32_t c8)
+{
+    constexpr uint32_t D = 32u * G;
+    const uint32_t key = slot % GPUOS_KV4_PAGE, t = key >> 4, quad = key >> 2 & 3u, r = key & 3u;
+    const uint32_t g = c8 >> 2, x = c8 & 3u; /* channels 32 g + 8 x .. + 7 */
+    unsigned char *pg = pool + ((uint64_t)(slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
+    Kv4Row o;
+    o.k = pg + t * 8u * D + (((quad * 2u + (r & 1u)) * 4u + x) * 2u + (r >> 1)) * 4u * G + 4u * g;
+    o.v = pg + 16u * D + t * 8u * D + ((2u * x * 4u + quad) * 4u + r) * 2u * G + 2u * g; /* the next: + 32 G */
+    o.ks = pg + 32u * D + key * G + g;
+    o.vs = pg + 33u * D + ((t * 4u + quad) * G + g) * 4u + r;
+    return o;
+}
+/* Rows of a tile: the host's tiles cut the N H rows into equal runs. */
+DEV void kv4_rows(const gpuos_devdesc *d, uint32_t tile, uint64_t &r0, uint64_t &r1)
+{
+    const uint64_t rows = (uint64_t)d->dims[0] * d->dims[1], per = (rows + d->ntiles - 1) / d->ntiles;
+    r0 = per * tile;
+    r1 = r0 + per < rows ? r0 + per : rows;
+}
+template <bool F32>
+DEV void kv4_load8(const void *base, uint64_t e, float (&x)[8])
+{
+    if (F32) {
+        const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + e);
+        const float4 u = __ldcg(p), v = __ldcg(p + 1);
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    } else {
+        unpack8(__ldcg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + e)), x);
+    }
+}
+/* The scale byte of a group of 32 (four lanes of eight values) and the codes. */
+DEV uint32_t kv4_quantise(float (&x)[8], uint32_t &byte)
+{
+    float top = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+        top = fmaxf(top, fabsf(x[c]));
+        odd |= !(fabsf(x[c]) < INFINITY);
+    }
+    top = odd ? INFINITY : top;
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const uint32_t bits = __float_as_uint(top);
+    int e = (int)(bits >> 23) - 129 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+    e = max(-127, min(125, e));
+    const float down = kv4_pow2(-e);
+#pragma unroll
+    for (int c = 0; c < 8; c++) x[c] *= down;
+    const bool none = top == INFINITY;
+    byte = none ? 255u : (uint32_t)(e + 127);
+    return none ? 0u : kv4_encode8(x);
+}
+template <int G, bool F32>
+DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
+{
+    constexpr uint32_t LPR = 4u * G, RPI = 16u / LPR; /* lanes of a row; rows a step (keys and values each) */
+    const uint32_t H = d->dims[1], lane = lane_id();
+    const uint32_t c8 = lane % LPR, val = lane / LPR & 1u, sub = lane / (2u * LPR);
+    const int32_t *slots = reinterpret_cast<const int32_t *>(d->aux0);
+    const uint32_t nslots = d->dims[3] * GPUOS_KV4_PAGE;
+    uint64_t r0, r1;
+    kv4_rows(d, tile, r0, r1);
+    int status = GPUOS_ST_OK;
+    for (uint64_t r = r0; r < r1; r += RPI) {
+        const uint64_t row = r + sub;
+        const bool have = row < r1;
+        const uint32_t n = have ? (uint32_t)(row / H) : 0u, h = have ? (uint32_t)(row - (uint64_t)n * H) : 0u;
+        const int32_t slot = have ? __ldcg(slots + n) : -1;
+        if (slot >= 0 && (uint32_t)slot >= nslots) status = GPUOS_ST_BAD_ARGS;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (have) kv4_load8<F32>(reinterpret_cast<const void *>(val ? d->b : d->a), row * (32u * G) + 8u * c8, x);
+        uint32_t byte;
+        const uint32_t w = kv4_quantise(x, byte);
+        if (slot >= 0 && (uint32_t)slot < nslots) {
+            const Kv4Row o = kv4_row<G>(reinterpret_cast<unsigned char *>(d->out), H, (uint32_t)slot, h, c8);
+            if (val) {
+                *reinterpret_cast<uint16_t *>(o.v) = (uint16_t)w;
+                *reinterpret_cast<uint16_t *>(o.v + 32u * G) = (uint16_t)(w >> 16);
+                if ((c8 & 3u) == 0) *o.vs = (unsigned char)byte;
+            } else {
+                *reinterpret_cast<uint32_t *>(o.k) = w;
+                if ((c8 & 3u) == 0) *o.ks = (unsigned char)byte;
+            }
+        }
+    }
+    return __any_sync(0xFFFFFFFFu, status != GPUOS_ST_OK) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
+}
+/* Values of eight codes under a scale byte. */
+DEV void kv4_dequantise(uint32_t w, uint32_t byte, float (&x)[8])
+{
+    uint32_t h[4];
+    kv4_decode4(w, h);
+    float s = __uint_as_float(byte ? byte << 23 : 0x00400000u); /* 2^-127 is a subnormal number */
+    if (byte == 255u) s = NAN;
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[c]));
+        x[2 * c] = f.x * s;
+        x[2 * c + 1] = f.y * s;
+    }
+}
+template <int G, bool F32>
+DEV int kv4_read_tile(const gpuos_devdesc *d, uint32_t tile)
+{
+    constexpr uint32_t LPR = 4u * G, RPI = 16u / LPR;
+    const uint32_t H = d->dims[1], lane = lane_id();
+    const uint32_t c8 = lane % LPR, val = lane / LPR & 1u, sub = lane / (2u * LPR);
+    const int32_t *slots = reinterpret_cast<const int32_t *>(d->aux0);
+    const uint32_t nslots = d->dims[3] * GPUOS_KV4_PAGE;
+    uint64_t r0, r1;
+    kv4_rows(d, tile, r0, r1);
+    int status = GPUOS_ST_OK;
+    for (uint64_t r = r0; r < r1; r += RPI) {
+        const uint64_t row = r + sub;
+        if (row >= r1) break;
+        const uint32_t n = (uint32_t)(row / H), h = (uint32_t)(row - (uint64_t)n * H);
+        const int32_t slot = __ldcg(slots + n);
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (slot >= 0 && (uint32_t)slot < nslots) {
+            const Kv4Row o = kv4_row<G>(reinterpret_cast<unsigned char *>(d->a), H, (uint32_t)slot, h, c8);
+            uint32_t w, byte;
+            if (val) {
+                w = (uint32_t)__ldcg(reinterpret_cast<const uint16_t *>(o.v)) |
+                    (uint32_t)__ldcg(reinterpret_cast<const uint16_t *>(o.v + 32u * G)) << 16;
+                byte = __ldcg(o.vs);
+            } else {
+                w = __ldcg(reinterpret_cast<const uint32_t *>(o.k));
+                byte = __ldcg(o.ks);
+            }
+            kv4_dequantise(w, byte, x);
+        } else if (slot >= 0) {
+            status = GPUOS_ST_BAD_ARGS;
+        }
+        const uint64_t e = row * (32u * G) + 8u * c8;
+        if (F32) {
+            float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(val ? d->aux1 : d->out) + e);
+            o[0] = make_float4(x[0], x[1], x[2], x[3]);
+            o[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(val ? d->aux1 : d->out) + e) = pack8(x);
+        }
+    }
+    return __any_sync(0xFFFFFFFFu, status != GPUOS_ST_OK) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
+}
+DEV int kv4_write_op(const gpuos_devdesc *d, uint32_t tile)
+{
+    if (d->dims[0] == 0) return GPUOS_ST_OK;
+    const bool f32 = d->dtype == GPUOS_F32;
+    if (d->dims[2] == 128) return f32 ? kv4_write_tile<4, true>(d, tile) : kv4_write_tile<4, false>(d, tile);
+    return f32 ? kv4_write_tile<2, true>(d, tile) : kv4_write_tile<2, false>(d, tile);
+}
+DEV int kv4_read_op(const gpuos_devdesc *d, uint32_t tile)
+{
+    if (d->dims[0] == 0) return GPUOS_ST_OK;
+    const bool f32 = d->dtype == GPUOS_F32;
+    if (d->dims[2] == 128) return f32 ? kv4_read_tile<4, true>(d, tile) : kv4_read_tile<4, false>(d, tile);
+    return f32 ? kv4_read_tile<2, true>(d, tile) : kv4_read_tile<2, false>(d, tile);
+}
+
+/* ---------------------------------------------------------------------------
+ * Page copy: pool[layer][dst] = pool[layer][src] for every (src, dst) pair and
+ * layer, GPUOS_PAGE_CHUNK bytes a tile, eight 16-byte loads in flight a lane.
+ * ------------------------------------------------------------------------- */
+DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
+{
+    const uint32_t n = d->dims[0], p16 = d->dims[1], npages = d->dims[2], layers = d->dims[3];
+    if (n == 0 || p16 == 0 || layers == 0) return GPUOS_ST_OK;
+    constexpr uint32_t C = GPUOS_PAGE_CHUNK / 16u;
+    const uint32_t nc = (p16 + C - 1) / C;
+    const uint32_t pair = tile / nc, c0 = (tile - pair * nc) * C;
+    const uint32_t layer = pair / n, k = pair - layer * n;
+    if (layer >= layers) return GPUOS_ST_OK;
+    const int2 sd = __ldcg(reinterpret_cast<const int2 *>(d->aux0) + k);
+    if (sd.x < 0 || sd.y < 0 || sd.x == sd.y) return GPUOS_ST_OK;
+    if ((uint32_t)sd.x >= npages || (uint32_t)sd.y >= npages) return GPUOS_ST_BAD_ARGS;
+    uint4 *pool = reinterpret_cast<uint4 *>(d->a) + (uint64_t)layer * npages * p16 + c0;
+    const uint4 *src = pool + (uint64_t)sd.x * p16;
+    uint4 *dst = pool + (uint64_t)sd.y * p16;
+    const uint32_t m = p16 - c0 < C ? p16 - c0 : C;
+    constexpr int U = 8;
+    for (uint32_t i0 = lane_id(); i0 < m; i0 += 32u * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (i0 + 32u * u < m) v[u] = __ldcg(src + i0 + 32u * u);
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (i0 + 32u * u < m) __stcg(dst + i0 + 32u * u, v[u]);
+    }
+    return GPUOS_ST_OK;
+}
+
+/* ---------------------------------------------------------------------------
+ * Eager launches (one kernel for each op, so that the attention's registers
+ * are not those of the small ops).
+ * ------------------------------------------------------------------------- */
+template <int OP>
+__global__ void __launch_bounds__(32) gpuos_kv4_eager_kernel(gpuos_devdesc d, uint32_t stage_bytes)
+{
+    __shared__ __align__(16) gpuos_devdesc sd;
+    stage_init(stage_bytes);
+    reinterpret_cast<uint32_t *>(&sd)[lane_id()] = reinterpret_cast<const uint32_t *>(&d)[lane_id()];
+    __syncwarp();
+    if (OP == GPUOS_OP_KV4_SDPA) (void)kv4_sdpa_op(&sd, blockIdx.x);
+    if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_op(&sd, blockIdx.x);
+    if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_op(&sd, blockIdx.x);
+    if (OP == GPUOS_OP_PAGE_COPY) (void)page_copy_op(&sd, blockIdx.x);
+}
+#endif /* GPUOS_KV4_CUH */

@@ -21,7 +21,7 @@ OK, EINVAL, EAGAIN, ETIMEDOUT, EDEVICE, ECUDA, ESTOPPED, ENOMEM, EBUSY, ETOOBIG,
     0, -1, -2, -3, -4, -5, -6, -7, -8, -9, -10
 ST_OK, ST_BAD_OP, ST_BAD_ARGS, ST_DEP_TIMEOUT, ST_ABORTED, ST_BAD_DESC, ST_COPY_TIMEOUT = 0, 1, 2, 3, 4, 5, 6
 OP = dict(nop=0, add=1, mul=2, relu=3, gelu=4, softmax=5, layernorm=6, rowsum=7, rowmax=8, rowmin=9,
-          rope=10, kv_write=11, sdpa=12, vecmat=13)
+          rope=10, kv_write=11, sdpa=12, vecmat=13, kv4_write=14, kv4_read=15, kv4_sdpa=16, page_copy=17)
 OP_USER_FIRST = 64
 F32, BF16 = 0, 1
 DTYPE = {"f32": F32, "bf16": BF16}
@@ -78,7 +78,7 @@ class Stats(C.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_ if k != "reserved"}
 
 
-PROF_BUCKETS = 16
+PROF_BUCKETS = 32
 
 
 class TileProfile(C.Structure):
@@ -113,6 +113,7 @@ API = {
     "gpuos_executor_stream": (C.c_int, [C.c_void_p, C.POINTER(C.c_void_p)]),
     "gpuos_op_ntiles": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
     "gpuos_sdpa_workspace_bytes": (C.c_size_t, [C.c_uint32, C.c_uint32, C.c_uint32, C.c_uint32]),
+    "gpuos_kv4_pool_bytes": (C.c_size_t, [C.c_uint32, C.c_uint32, C.c_uint32]),
     "gpuos_eager_run": (C.c_int, [C.c_void_p, C.c_uint32, C.c_uint32, C.c_void_p]),
     "gpuos_host_now_ns": (C.c_uint64, []),
     "gpuos_sdpa_noalloc": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint32,
