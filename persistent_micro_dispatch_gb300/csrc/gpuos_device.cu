@@ -2719,29 +2719,13 @@ extern "C" int gpuos_dev_preload(void)
     return 0;
 }
 
-/* One of the KV4 / page kernels on `stream` (at most 24 KB of staging: no
- * attribute to raise). */
-template <int OP>
-static int kv4_eager_launch(const gpuos_devdesc &dd, uint32_t stage_bytes, void *stream)
-{
-    const uint32_t dyn = gpuos_dev_dyn_smem(1, stage_bytes);
-    gpuos_kv4_eager_kernel<OP><<<dd.ntiles, 32, dyn, (cudaStream_t)stream>>>(dd, stage_bytes);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
-}
-
 extern "C" int gpuos_dev_eager_launch(const gpuos_desc *d, uint32_t ntiles, uint32_t stage_bytes, void *stream)
 {
     gpuos_devdesc dd;
     static_assert(sizeof(dd) == sizeof(*d), "layout");
     memcpy(&dd, d, sizeof(dd));
     dd.ntiles = ntiles;
-    switch (d->op_id) {
-    case GPUOS_OP_KV4_SDPA: return kv4_eager_launch<GPUOS_OP_KV4_SDPA>(dd, stage_bytes, stream);
-    case GPUOS_OP_KV4_WRITE: return kv4_eager_launch<GPUOS_OP_KV4_WRITE>(dd, 0, stream);
-    case GPUOS_OP_KV4_READ: return kv4_eager_launch<GPUOS_OP_KV4_READ>(dd, 0, stream);
-    case GPUOS_OP_PAGE_COPY: return kv4_eager_launch<GPUOS_OP_PAGE_COPY>(dd, 0, stream);
-    default: break;
-    }
+    if (d->op_id >= GPUOS_OP_KV4_WRITE && d->op_id <= GPUOS_OP_PAGE_COPY) return kv4_eager_launch(dd, stream);
     const uint32_t grid = (ntiles + EAGER_WPB - 1) / EAGER_WPB;
     const uint32_t dyn = gpuos_dev_dyn_smem(EAGER_WPB, stage_bytes);
     static uint32_t attr_set = 0;

@@ -29,6 +29,11 @@
 #define GPUOS_KV4_CUH
 
 #include <cuda_fp16.h>
+#include <float.h>
+
+#include <atomic>
+
+#define GPUOS_KV4_SCRATCH 768u /* bytes of a warp's converted scales */
 
 DEV constexpr uint32_t kv4_page_bytes(uint32_t D) { return 34u * D; }
 
@@ -106,11 +111,14 @@ DEV float kv4_ex2(float x)
  * in f16: exact for the bf16 values within 2^-21 of the row's largest, and
  * off by at most 2^-32 of it below. Codes are exact in f16; the products are
  * summed in fp32 for each scale group, and the groups' sums are scaled and
- * added in fp32. p 2^7 is rounded to f16 (11 bits; bf16's 8 would show in a
- * bf16 output), and multiplied there by 2^(b - E + 8), b the value's scale
- * exponent and E the largest met so far in its group: exact unless the
- * product falls below 2^-14, 2^29 below the largest possible. The softmax's
- * maximum and sum and the output accumulators are fp32.
+ * added in fp32. Weights p, the largest 2^6 to 2^8, are rounded to f16 (11
+ * bits; bf16's 8 would show in a bf16 output; one 2^-20 of the largest still
+ * has them all, below that the error is at most 2^-31 of the largest), and
+ * multiplied there by 2^(b - E + 7), b the value's scale exponent and E the
+ * largest met so far in its group: exact unless the product falls below
+ * 2^-14, that is 2^-27 of the largest; a scale 2^-22 below E counts as zero.
+ * The softmax's
+ * reference and sum and the output accumulators are fp32.
  * ------------------------------------------------------------------------- */
 struct Kv4Args {
     const uint16_t *q;
@@ -221,8 +229,8 @@ DEV void kv4_next(const Kv4Args &a, Kv4Pos &p)
 template <int G, int NT>
 struct Kv4State {
     uint32_t q[NT][G][4]; /* f16x2 of row 8 nt + i: channels 32 g + 8 j + {0..7} */
-    float f[NT][2];       /* score factor of rows 2 j, 2 j + 1: scale log2(e) 2^k */
-    float m[NT][2];       /* running maximum (log2) less 7, equal in the lanes of a row */
+    float f[NT][2];       /* score factor of rows 2 j, 2 j + 1: |scale| log2(e) 2^k, positive */
+    float m[NT][2];       /* the reference that scores are taken against, equal in the lanes of a row */
     float l[NT][2];       /* this lane's part of the running sum */
     float acc[NT][G][2][4];
     uint32_t E[G]; /* largest value-scale exponent met in each group */
@@ -272,7 +280,14 @@ DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, Kv4State<G, NT> &s)
         int k = (int)(__float_as_uint(top) >> 23) - 127 - 7;
         if (oddrow || top == 0.0f) k = 0;
         k = max(-126, min(126, k));
-        const float down = kv4_pow2(-k);
+        /* the factor stays positive: a negative scale turns q, one of zero
+         * (or a product with 2^k below every number) empties it */
+        float down = kv4_pow2(-k), f = fabsf(a.scale) * kv4_pow2(k);
+        if (a.scale < 0.0f) down = -down;
+        if (f == 0.0f) {
+            down = 0.0f;
+            f = 1.0f;
+        }
 #pragma unroll
         for (int g = 0; g < G; g++) {
             float x[8];
@@ -280,12 +295,11 @@ DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, Kv4State<G, NT> &s)
 #pragma unroll
             for (int c = 0; c < 4; c++) s.q[nt][g][c] = kv4_pack_h2(x[2 * c] * down, x[2 * c + 1] * down);
         }
-        const float f = a.scale * kv4_pow2(k);
         s.f[nt][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * j);
         s.f[nt][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * j + 4);
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-            s.m[nt][c] = -INFINITY;
+            s.m[nt][c] = -FLT_MAX;
             s.l[nt][c] = 0.0f;
             s.lim[nt][c] = kv4_row_limit(a, p.len, r0 + 8u * nt + 2u * j + c);
         }
@@ -327,70 +341,159 @@ DEV uint32_t kv4_keep(uint32_t key0, uint32_t n)
     return (1u << (8u * (n - key0))) - 1u;
 }
 
+/* The page's largest value scale of a group exceeds s.E (rare: at a run's
+ * first page, then with each new largest). E grows, the accumulators follow.
+ * vw: the lane's word of value scales, group lane % G, keys key0 .. key0 + 3
+ * of the page, already without what lies behind the last key. A scale of 255
+ * makes NaN what the rows that see the key hold of the group, and is dropped
+ * from vw. */
+template <int G, int NT>
+DEV void kv4_grow(uint32_t base, uint32_t key0, uint32_t &vw, Kv4State<G, NT> &s)
+{
+    const uint32_t lane = lane_id();
+    const uint32_t nan = __vcmpeq4(vw, 0xFFFFFFFFu);
+    if (__any_sync(0xFFFFFFFFu, nan != 0u)) {
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            /* the page's first such key of the group */
+            uint32_t lo = GPUOS_KV4_PAGE;
+            if (nan && lane % G == (uint32_t)g) lo = key0 + ((uint32_t)__ffs((int)nan) - 1u) / 8u;
+            lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    if (lo < GPUOS_KV4_PAGE && base + lo < s.lim[nt][c & 1]) {
+                        s.acc[nt][g][0][c] = NAN;
+                        s.acc[nt][g][1][c] = NAN;
+                    }
+        }
+        vw &= ~nan;
+    }
+    uint32_t x = max(max(vw & 255u, vw >> 8 & 255u), max(vw >> 16 & 255u, vw >> 24));
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+        const uint32_t e = max(s.E[g], __reduce_max_sync(0xFFFFFFFFu, lane % G == (uint32_t)g ? x : 0u));
+        /* 2^(E - e); below 2^-126 nothing is left of it */
+        const float up = s.E[g] + 127u > e ? kv4_pow2((int)s.E[g] - (int)e) : 0.0f;
+        s.E[g] = e;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int c = 0; c < 4; c++) s.acc[nt][g][u][c] *= up;
+    }
+}
+
 /* One page: keys [base, base + 32) of the item, of which those below `valid`
- * exist (the rest of a request's last page holds anything). */
+ * exist (the rest of a request's last page holds anything). `scratch` (768
+ * bytes of the warp's) passes the scales from the lane that converts a word
+ * of them to the lanes that use them; without it (GLOBAL: the page is in
+ * global memory, there is no staging) they pass by shuffles. */
 template <int G, int NT, bool GLOBAL>
-DEV void kv4_page(const unsigned char *pg, uint32_t base, uint32_t valid, Kv4State<G, NT> &s)
+DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base, uint32_t valid, Kv4State<G, NT> &s)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
     const uint32_t nv = valid > base ? min(valid - base, (uint32_t)GPUOS_KV4_PAGE) : 0u; /* existing keys of the page */
+
+    /* ---- scales. Key scales: lane = key, G bytes -> G floats 2^(byte - 127)
+     * (byte 0 gives 0: such a group's values are below 2^-124; 255 gives
+     * infinity, and NaN with the zero codes that the write leaves beside it).
+     * Value scales: lane = word ((key / 4) G + group) -> four f16, 2^(byte -
+     * E + 7): exponent field byte - E + 22, zero below 1. ---- */
+    float kf[G];
+    {
+        const uint32_t w = G == 4 ? kv4_ld4<GLOBAL>(pg + 32u * D + 4u * lane)
+                                  : kv4_ld4<GLOBAL>(pg + 32u * D + 4u * (lane >> 1)) >> (16u * (lane & 1u));
+#pragma unroll
+        for (int g = 0; g < G; g++) kf[g] = __uint_as_float((g < 3 ? w << (23 - 8 * g) : w >> 1) & 0x7F800000u);
+    }
+    uint2 vs;
+    {
+        const uint32_t word = lane % (8u * G), key0 = word / G * 4u;
+        uint32_t vw = kv4_ld4<GLOBAL>(pg + 33u * D + 4u * word);
+        if (nv < GPUOS_KV4_PAGE) vw &= kv4_keep(key0, nv);
+        /* E of the lane's group */
+        uint32_t E = s.E[0];
+#pragma unroll
+        for (int g = 1; g < G; g++) E = lane % G == (uint32_t)g ? s.E[g] : E;
+        const uint32_t b02 = vw & 0x00FF00FFu, b13 = vw >> 8 & 0x00FF00FFu;
+        const uint32_t top = __vimax_s16x2_relu(b02, b13);
+        if (__any_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16) > E)) {
+            kv4_grow<G, NT>(base, key0, vw, s);
+            E = s.E[0];
+#pragma unroll
+            for (int g = 1; g < G; g++) E = lane % G == (uint32_t)g ? s.E[g] : E;
+        }
+        const uint32_t bias = (22u - E) & 0xFFFFu, bias2 = bias | bias << 16;
+        vs.x = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4140), bias2, 0u) << 10;
+        vs.y = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4342), bias2, 0u) << 10;
+    }
+    if (!GLOBAL) {
+        __syncwarp(); /* the last page's readers are done */
+        if (G == 4) *reinterpret_cast<float4 *>(scratch + 16u * lane) = make_float4(kf[0], kf[1], kf[G - 2], kf[G - 1]);
+        else *reinterpret_cast<float2 *>(scratch + 8u * lane) = make_float2(kf[0], kf[1]);
+        *reinterpret_cast<uint2 *>(scratch + 512u + 8u * (lane % (8u * G))) = vs; /* (G == 2: both halves of the warp alike) */
+        __syncwarp();
+    }
 
     /* ---- scores: S^T tile t = keys 16 t .. 16 t + 15 against the rows ---- */
     float sc[2][NT][4];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
         const uint32_t k0 = 16u * t + 4u * (i >> 1) + (i & 1u); /* the lane's keys: k0 (c 0, 1) and k0 + 2 (c 2, 3) */
-        uint32_t kw[2][G], ks[2];
+        uint32_t kw[2][G];
+        float f0[G], f1[G];
         const unsigned char *kp = pg + (uint32_t)t * 8u * D + lane * 8u * G;
         if (G == 4) {
             const uint4 x = kv4_ld16<GLOBAL>(kp), y = kv4_ld16<GLOBAL>(kp + 16);
             kw[0][0] = x.x; kw[0][1] = x.y; kw[0][G - 2] = x.z; kw[0][G - 1] = x.w;
             kw[1][0] = y.x; kw[1][1] = y.y; kw[1][G - 2] = y.z; kw[1][G - 1] = y.w;
-            ks[0] = kv4_ld4<GLOBAL>(pg + 32u * D + k0 * 4u);
-            ks[1] = kv4_ld4<GLOBAL>(pg + 32u * D + (k0 + 2u) * 4u);
         } else {
             const uint4 x = kv4_ld16<GLOBAL>(kp);
             kw[0][0] = x.x; kw[0][1] = x.y;
             kw[1][0] = x.z; kw[1][1] = x.w;
-            /* two bytes a key: the word of keys k0 & ~1, k0 | 1 */
-            const uint32_t odd = 16u * (k0 & 1u);
-            ks[0] = kv4_ld4<GLOBAL>(pg + 32u * D + (k0 & ~1u) * 2u) >> odd;
-            ks[1] = kv4_ld4<GLOBAL>(pg + 32u * D + ((k0 & ~1u) + 2u) * 2u) >> odd;
+        }
+        if (GLOBAL) {
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                f0[g] = __shfl_sync(0xFFFFFFFFu, kf[g], k0);
+                f1[g] = __shfl_sync(0xFFFFFFFFu, kf[g], k0 + 2u);
+            }
+        } else if (G == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(scratch + 16u * k0);
+            const float4 y = *reinterpret_cast<const float4 *>(scratch + 16u * (k0 + 2u));
+            f0[0] = x.x; f0[1] = x.y; f0[G - 2] = x.z; f0[G - 1] = x.w;
+            f1[0] = y.x; f1[1] = y.y; f1[G - 2] = y.z; f1[G - 1] = y.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(scratch + 8u * k0);
+            const float2 y = *reinterpret_cast<const float2 *>(scratch + 8u * (k0 + 2u));
+            f0[0] = x.x; f0[1] = x.y;
+            f1[0] = y.x; f1[1] = y.y;
         }
 #pragma unroll
         for (int g = 0; g < G; g++) {
             uint32_t x0[4], x1[4];
             kv4_decode4(kw[0][g], x0);
             kv4_decode4(kw[1][g], x1);
-            /* exponent byte -> the float 2^(byte - 127) (byte 0 gives 0: such
-             * a group's values are below 2^-124; 255 gives infinity, and NaN
-             * with the zero codes that the write leaves beside it) */
-            const float s0 = __uint_as_float((ks[0] >> (8 * g) & 255u) << 23);
-            const float s1 = __uint_as_float((ks[1] >> (8 * g) & 255u) << 23);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
                 float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 kv4_mma(c, x0[0], x1[0], x0[1], x1[1], s.q[nt][g][0], s.q[nt][g][1]);
                 kv4_mma(c, x0[2], x1[2], x0[3], x1[3], s.q[nt][g][2], s.q[nt][g][3]);
                 if (g == 0) {
-                    sc[t][nt][0] = c[0] * s0; sc[t][nt][1] = c[1] * s0;
-                    sc[t][nt][2] = c[2] * s1; sc[t][nt][3] = c[3] * s1;
+                    sc[t][nt][0] = c[0] * f0[g]; sc[t][nt][1] = c[1] * f0[g];
+                    sc[t][nt][2] = c[2] * f1[g]; sc[t][nt][3] = c[3] * f1[g];
                 } else {
-                    sc[t][nt][0] = fmaf(c[0], s0, sc[t][nt][0]); sc[t][nt][1] = fmaf(c[1], s0, sc[t][nt][1]);
-                    sc[t][nt][2] = fmaf(c[2], s1, sc[t][nt][2]); sc[t][nt][3] = fmaf(c[3], s1, sc[t][nt][3]);
+                    sc[t][nt][0] = fmaf(c[0], f0[g], sc[t][nt][0]); sc[t][nt][1] = fmaf(c[1], f0[g], sc[t][nt][1]);
+                    sc[t][nt][2] = fmaf(c[2], f1[g], sc[t][nt][2]); sc[t][nt][3] = fmaf(c[3], f1[g], sc[t][nt][3]);
                 }
             }
         }
     }
-    const bool masked = base + GPUOS_KV4_PAGE > s.min_lim || nv < GPUOS_KV4_PAGE; /* warp-uniform */
-#pragma unroll
-    for (int t = 0; t < 2; t++)
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int c = 0; c < 4; c++) sc[t][nt][c] *= s.f[nt][c & 1];
-    if (masked) {
+    if (base + GPUOS_KV4_PAGE > s.min_lim || nv < GPUOS_KV4_PAGE) { /* the same in every lane */
 #pragma unroll
         for (int t = 0; t < 2; t++)
 #pragma unroll
@@ -402,123 +505,54 @@ DEV void kv4_page(const unsigned char *pg, uint32_t base, uint32_t valid, Kv4Sta
                 }
     }
 
-    /* ---- the largest value scale of each group ---- */
-    const bool tail = nv < GPUOS_KV4_PAGE;
-    uint32_t vw[2][G]; /* scales of keys 16 t + 4 j .. + 3, group g */
+    /* ---- online softmax. Weights are 2^(score - m), m a reference 7 below
+     * the largest score when it was last set: it is set anew (and what is
+     * accumulated rescaled) only when a score comes 8 above it. ---- */
+    float high[NT][2];
+    bool over = false;
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
-        const unsigned char *vp = pg + 33u * D + ((uint32_t)t * 4u + j) * 4u * G;
-        if (G == 4) {
-            const uint4 x = kv4_ld16<GLOBAL>(vp);
-            vw[t][0] = x.x; vw[t][1] = x.y; vw[t][G - 2] = x.z; vw[t][G - 1] = x.w;
-        } else {
-            const uint2 x = kv4_ld8<GLOBAL>(vp);
-            vw[t][0] = x.x; vw[t][1] = x.y;
-        }
-    }
-    if (tail) { /* what lies behind the last key is anything: no scale */
-#pragma unroll
-        for (int t = 0; t < 2; t++) {
-            const uint32_t keep = kv4_keep(16u * t + 4u * j, nv);
-#pragma unroll
-            for (int g = 0; g < G; g++) vw[t][g] &= keep;
-        }
-    }
-    float up[G]; /* what the accumulators are multiplied by */
-    uint32_t grow = 0;
-    {
-        uint32_t mx[G];
-#pragma unroll
-        for (int g = 0; g < G; g++) {
-            mx[g] = __vmaxu4(vw[0][g], vw[1][g]);
-            grow |= __vcmpgtu4(mx[g], s.E[g] * 0x01010101u);
-        }
-        grow = __any_sync(0xFFFFFFFFu, grow != 0u);
-        if (grow) {
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-                uint32_t x = mx[g];
-                x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-                x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                x = __vmaxu4(x, x >> 16);
-                x = max(x & 255u, x >> 8 & 255u);
-                if (x == 255u) {
-                    /* a NaN group: NaN for the rows that see such a key; the
-                     * scale itself is dropped */
-#pragma unroll
-                    for (int t = 0; t < 2; t++) {
-                        const uint32_t bad = __vcmpeq4(vw[t][g], 0xFFFFFFFFu);
-                        uint32_t lo = 4u * GPUOS_KV4_PAGE; /* the first such key of the page */
-                        if (bad) lo = 16u * t + 4u * j + ((uint32_t)__ffs((int)bad) - 1u) / 8u;
-                        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 1));
-                        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 2));
-#pragma unroll
-                        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                            for (int c = 0; c < 4; c++)
-                                if (lo < GPUOS_KV4_PAGE && base + lo < s.lim[nt][c & 1]) {
-                                    s.acc[nt][g][0][c] = NAN;
-                                    s.acc[nt][g][1][c] = NAN;
-                                }
-                        vw[t][g] &= ~bad;
-                    }
-                    x = __vmaxu4(vw[0][g], vw[1][g]);
-                    x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-                    x = __vmaxu4(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                    x = __vmaxu4(x, x >> 16);
-                    x = max(x & 255u, x >> 8 & 255u);
-                }
-                const uint32_t e = max(s.E[g], x);
-                /* 2^(E - e); below 2^-126 nothing is left of it */
-                up[g] = (int)(s.E[g] + 127u) > (int)e ? kv4_pow2((int)s.E[g] - (int)e) : 0.0f;
-                s.E[g] = e;
-            }
-        }
-    }
-
-    /* ---- online softmax ---- */
-    uint32_t pb[2][NT][2]; /* p^T: B fragments of the second product */
-    float alpha[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++) {
+    for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int r = 0; r < 2; r++) {
-            float mx = fmaxf(fmaxf(sc[0][nt][r], sc[0][nt][r + 2]), fmaxf(sc[1][nt][r], sc[1][nt][r + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-            const float mn = fmaxf(s.m[nt][r], mx - 7.0f);
-            const float mu = mn == -INFINITY ? 0.0f : mn;
-            alpha[nt][r] = kv4_ex2(s.m[nt][r] - mu);
-            s.m[nt][r] = mn;
-            float sum = 0.0f;
-#pragma unroll
-            for (int t = 0; t < 2; t++) {
-                sc[t][nt][r] = kv4_ex2(sc[t][nt][r] - mu);
-                sc[t][nt][r + 2] = kv4_ex2(sc[t][nt][r + 2] - mu);
-                sum += sc[t][nt][r] + sc[t][nt][r + 2];
-            }
-            s.l[nt][r] = fmaf(s.l[nt][r], alpha[nt][r], sum);
+            high[nt][r] = fmaxf(fmaxf(sc[0][nt][r], sc[0][nt][r + 2]), fmaxf(sc[1][nt][r], sc[1][nt][r + 2]));
+            over |= fmaf(high[nt][r], s.f[nt][r], -8.0f) > s.m[nt][r];
         }
-#pragma unroll
-        for (int t = 0; t < 2; t++) {
-            pb[t][nt][0] = kv4_trans8x8(kv4_pack_h2(sc[t][nt][0], sc[t][nt][1]));
-            pb[t][nt][1] = kv4_trans8x8(kv4_pack_h2(sc[t][nt][2], sc[t][nt][3]));
-        }
-    }
-    /* ---- O^T += V^T p^T ---- */
-#pragma unroll
-    for (int g = 0; g < G; g++) {
-        const float ug = grow ? up[g] : 1.0f;
+    if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                const float x = alpha[nt][c & 1] * ug;
-                s.acc[nt][g][0][c] *= x;
-                s.acc[nt][g][1][c] *= x;
+            for (int r = 0; r < 2; r++) {
+                float mx = high[nt][r] * s.f[nt][r];
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+                const float mn = fmaxf(s.m[nt][r], mx - 7.0f);
+                const float alpha = kv4_ex2(s.m[nt][r] - mn); /* 0 from the first reference, -FLT_MAX */
+                s.m[nt][r] = mn;
+                s.l[nt][r] *= alpha;
+#pragma unroll
+                for (int g = 0; g < G; g++)
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        s.acc[nt][g][u][r] *= alpha;
+                        s.acc[nt][g][u][r + 2] *= alpha;
+                    }
             }
     }
+    uint32_t pb[2][NT][2]; /* p^T: B fragments of the second product */
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                sc[t][nt][c] = kv4_ex2(fmaf(sc[t][nt][c], s.f[nt][c & 1], -s.m[nt][c & 1]));
+            s.l[nt][0] += sc[t][nt][0] + sc[t][nt][2];
+            s.l[nt][1] += sc[t][nt][1] + sc[t][nt][3];
+            pb[t][nt][0] = kv4_trans8x8(kv4_pack_h2(sc[t][nt][0], sc[t][nt][1]));
+            pb[t][nt][1] = kv4_trans8x8(kv4_pack_h2(sc[t][nt][2], sc[t][nt][3]));
+        }
+    /* ---- O^T += V^T p^T ---- */
 #pragma unroll
     for (int t = 0; t < 2; t++) {
         const unsigned char *vp = pg + 16u * D + (uint32_t)t * 8u * D + lane * 8u * G;
@@ -531,6 +565,21 @@ DEV void kv4_page(const unsigned char *pg, uint32_t base, uint32_t valid, Kv4Sta
             const uint4 x = kv4_ld16<GLOBAL>(vp);
             w[0][0] = x.x; w[1][0] = x.y; w[2][0] = x.z; w[3][0] = x.w;
         }
+        uint32_t s01[G], s23[G];
+        if (GLOBAL) {
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                s01[g] = __shfl_sync(0xFFFFFFFFu, vs.x, ((uint32_t)t * 4u + j) * G + g);
+                s23[g] = __shfl_sync(0xFFFFFFFFu, vs.y, ((uint32_t)t * 4u + j) * G + g);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < G / 2; x++) {
+                const uint4 y = *reinterpret_cast<const uint4 *>(scratch + 512u + (((uint32_t)t * 4u + j) * G + 2 * x) * 8u);
+                s01[2 * x] = y.x; s23[2 * x] = y.y;
+                s01[2 * x + 1] = y.z; s23[2 * x + 1] = y.w;
+            }
+        }
 #pragma unroll
         for (int x = 0; x < G / 2; x++) {
             /* bytes of (key, key + 1) pairs of one channel: even channels, odd channels */
@@ -542,13 +591,9 @@ DEV void kv4_page(const unsigned char *pg, uint32_t base, uint32_t valid, Kv4Sta
 #pragma unroll
             for (int gg = 0; gg < 2; gg++) {
                 const int g = 2 * x + gg;
-                /* f16x2 of 2^(b - E + 8): exponent field b - E + 23, zero below 1 */
-                const uint32_t bias = (23u - s.E[g]) & 0xFFFFu, bias2 = bias | bias << 16;
-                const uint32_t s01 = __viaddmax_s16x2(__byte_perm(vw[t][g], 0u, 0x4140), bias2, 0u) << 10;
-                const uint32_t s23 = __viaddmax_s16x2(__byte_perm(vw[t][g], 0u, 0x4342), bias2, 0u) << 10;
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
-                    const uint32_t b0 = kv4_hmul2(pb[t][nt][0], s01), b1 = kv4_hmul2(pb[t][nt][1], s23);
+                    const uint32_t b0 = kv4_hmul2(pb[t][nt][0], s01[g]), b1 = kv4_hmul2(pb[t][nt][1], s23[g]);
                     kv4_mma(s.acc[nt][g][0], e01[2 * gg], o01[2 * gg], e23[2 * gg], o23[2 * gg], b0, b1);
                     kv4_mma(s.acc[nt][g][1], e01[2 * gg + 1], o01[2 * gg + 1], e23[2 * gg + 1], o23[2 * gg + 1], b0, b1);
                 }
@@ -574,8 +619,8 @@ DEV void kv4_finish(Kv4State<G, NT> &s)
         }
 #pragma unroll
         for (int g = 0; g < G; g++) {
-            /* 2^(E - 127 - 8) in two factors (E - 135 may be below -126) */
-            const int e = (int)s.E[g] - 135, e1 = e / 2;
+            /* 2^(E - 127 - 7) in two factors (E - 134 may be below -126) */
+            const int e = (int)s.E[g] - 134, e1 = e / 2;
             const float p1 = kv4_pow2(e1), p2 = kv4_pow2(e - e1);
 #pragma unroll
             for (int c = 0; c < 4; c++) {
@@ -656,8 +701,8 @@ DEV void kv4_part_merge(const float *part, Kv4State<G, NT> &s, bool left)
 #pragma unroll
         for (int r = 0; r < 2; r++) {
             const float mo = r ? ml.z : ml.x, lo = r ? ml.w : ml.y;
-            const float mn = fmaxf(s.m[nt][r], mo), mu = mn == -INFINITY ? 0.0f : mn;
-            const float ws = s.l[nt][r] * kv4_ex2(s.m[nt][r] - mu), wo = lo * kv4_ex2(mo - mu);
+            const float mn = fmaxf(s.m[nt][r], mo);
+            const float ws = s.l[nt][r] * kv4_ex2(s.m[nt][r] - mn), wo = lo * kv4_ex2(mo - mn);
             const float l = left ? ws + wo : wo + ws, inv = l != 0.0f ? 1.0f / l : 0.0f;
             const float a0 = ws * inv, b0 = wo * inv;
             s.m[nt][r] = mn;
@@ -686,7 +731,7 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT>
     const int32_t *row = a.table + (uint64_t)p.b * a.P;
     const uint64_t stride = (uint64_t)a.Hkv * PB;
     const unsigned char *pool = a.pool + (uint64_t)h * PB;
-    const bool staged = stage_hdr()->stage_bytes >= 2u * PB;
+    const bool staged = stage_hdr()->stage_bytes >= 2u * PB + GPUOS_KV4_SCRATCH;
     WarpStage *w = warp_stage();
     unsigned char *buf = warp_stage_buf();
     int status = GPUOS_ST_OK;
@@ -733,7 +778,7 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT>
                 break;
             }
             phs ^= 1u << hb;
-            kv4_page<G, NT, false>(buf + hb * PB, base, valid, s);
+            kv4_page<G, NT, false>(buf + hb * PB, buf + 2u * PB, base, valid, s);
             if (k + 2 < n) {
                 const int32_t nx = (k & 31u) < 30u ? __shfl_sync(0xFFFFFFFFu, ids, (k + 2) & 31u)
                                                    : __shfl_sync(0xFFFFFFFFu, ids_next, (k + 2) & 31u);
@@ -742,7 +787,7 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT>
                 issue(k + 2, nx);
             }
         } else {
-            kv4_page<G, NT, true>(pool + (uint64_t)(there ? (uint32_t)id : 0u) * stride, base, valid, s);
+            kv4_page<G, NT, true>(pool + (uint64_t)(there ? (uint32_t)id : 0u) * stride, nullptr, base, valid, s);
         }
     }
     if (staged) {
@@ -1046,19 +1091,335 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
 }
 
 /* ---------------------------------------------------------------------------
- * Eager launches (one kernel for each op, so that the attention's registers
- * are not those of the small ops).
+ * Attention as a launch of its own (gpuos_eager_run). The runs are those of
+ * the executor's tiles, one for each warp, but a block has every SM to itself:
+ * NS pages in flight a warp, and the partial states of an item that warps of
+ * one block share meet in shared memory. An item that spans blocks leaves one
+ * partial state for each of them in the workspace; the last block to arrive
+ * merges them, all at once and in the order of the keys.
  * ------------------------------------------------------------------------- */
-template <int OP>
-__global__ void __launch_bounds__(32) gpuos_kv4_eager_kernel(gpuos_devdesc d, uint32_t stage_bytes)
+template <int G, int NT>
+struct Kv4Block {
+    static constexpr uint32_t WARPS = NT == 1 ? 12 : 8; /* 168 and 255 registers a thread */
+    static constexpr uint32_t NS = NT == 1 ? 3 : 4;
+    static constexpr uint32_t PB = 34u * 32u * G;
+    static constexpr uint32_t FRAG = Kv4Part<G, NT>::floats * 4u;
+    static constexpr uint32_t WARP_BYTES = NS * PB + GPUOS_KV4_SCRATCH;
+    static constexpr uint32_t SMEM = WARPS * (WARP_BYTES + FRAG);
+    static_assert(FRAG <= NS * PB, "a warp's last partial state takes the place of its pages");
+    static_assert(WARP_BYTES % 16 == 0 && FRAG % 16 == 0, "alignment");
+};
+/* What a warp leaves: the state of the item it began in the middle of, and of
+ * the item that it does not finish (none: first = ~0). */
+struct Kv4Left {
+    unsigned long long head, tail; /* the item's first unit */
+    uint32_t b, item, np, pad;     /* of the tail, or else of the head */
+    uint32_t hb, hitem, hnp, pad2; /* of the head */
+};
+
+template <int G, int NT>
+DEV void kv4_part_put(float4 *p4, const Kv4State<G, NT> &s)
 {
-    __shared__ __align__(16) gpuos_devdesc sd;
-    stage_init(stage_bytes);
-    reinterpret_cast<uint32_t *>(&sd)[lane_id()] = reinterpret_cast<const uint32_t *>(&d)[lane_id()];
+    const uint32_t lane = lane_id();
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        if (lane < 4) p4[nt * 4 + lane] = make_float4(s.m[nt][0], s.l[nt][0], s.m[nt][1], s.l[nt][1]);
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int r = 0; r < 2; r++)
+                p4[NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane] =
+                    make_float4(s.acc[nt][g][0][r], s.acc[nt][g][0][r + 2], s.acc[nt][g][1][r], s.acc[nt][g][1][r + 2]);
+    }
+}
+/* One quarter row of the output: element idx of a state's accumulators. */
+template <int G, int NT>
+DEV void kv4_out4(const Kv4Args &a, uint32_t b, uint32_t item, int32_t len, uint32_t idx, float l, float4 v)
+{
+    constexpr uint32_t D = 32u * G;
+    const uint32_t lane = idx & 31u, r2 = idx >> 5 & 1u, g = idx >> 6 & (G - 1u), nt = idx / (64u * G);
+    const uint32_t h = item / a.RT, r = (item - h * a.RT) * 8u * NT + 8u * nt + 2u * (lane & 3u) + r2;
+    if (r >= a.T * a.g) return;
+    const uint32_t t = r / a.g, hh = r - t * a.g;
+    if (l == 0.0f) {
+        const float z = kv4_empty(kv4_row_limit(a, len, r));
+        v = make_float4(z, z, z, z);
+    }
+    uint2 w;
+    w.x = pack_bf2(v.x, v.y);
+    w.y = pack_bf2(v.z, v.w);
+    *reinterpret_cast<uint2 *>(a.out + (((uint64_t)b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 32u * g + 4u * (lane >> 2)) = w;
+}
+/* m, l of element idx's row in a state. */
+template <int G, int NT>
+DEV float2 kv4_ml(float4 x, uint32_t idx) { return idx >> 5 & 1u ? make_float2(x.z, x.w) : make_float2(x.x, x.y); }
+template <int G, int NT>
+DEV uint32_t kv4_ml_at(uint32_t idx) { return idx / (64u * G) * 4u + (idx & 3u); }
+
+/* Add a state's element to a merge under way: mean v, weight l 2^m. */
+DEV void kv4_fold(float2 ml, float4 x, float &m, float &l, float4 &v)
+{
+    const float mn = fmaxf(m, ml.x);
+    const float ws = l * kv4_ex2(m - mn), wo = ml.y * kv4_ex2(ml.x - mn);
+    const float n = ws + wo, inv = n != 0.0f ? 1.0f / n : 0.0f;
+    const float c0 = ws * inv, c1 = wo * inv;
+    v.x = fmaf(x.x, c1, v.x * c0);
+    v.y = fmaf(x.y, c1, v.y * c0);
+    v.z = fmaf(x.z, c1, v.z * c0);
+    v.w = fmaf(x.w, c1, v.w * c0);
+    m = mn;
+    l = n;
+}
+
+template <int G, int NT>
+__global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_attend_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    using C = Kv4Block<G, NT>;
+    constexpr uint32_t PB = C::PB, NS = C::NS;
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ __align__(8) unsigned long long bars[C::WARPS][C::NS];
+    __shared__ Kv4Left left[C::WARPS];
+    __shared__ uint32_t last[2];
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    unsigned char *mine = sm + warp * C::WARP_BYTES;
+    if (lane == 0) {
+        for (uint32_t k = 0; k < NS; k++)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&bars[warp][k])) : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        left[warp].head = left[warp].tail = ~0ull;
+    }
     __syncwarp();
-    if (OP == GPUOS_OP_KV4_SDPA) (void)kv4_sdpa_op(&sd, blockIdx.x);
-    if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_op(&sd, blockIdx.x);
-    if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_op(&sd, blockIdx.x);
-    if (OP == GPUOS_OP_PAGE_COPY) (void)page_copy_op(&sd, blockIdx.x);
+    Kv4Args a;
+    kv4_args(&d, 8u * NT, a);
+    const uint64_t W = kv4_units(a);
+    /* at least GPUOS_KV4_RUN pages a warp: fewer blocks, and fewer states to merge, when there is little work */
+    uint64_t nblk = (W + C::WARPS * GPUOS_KV4_RUN - 1) / (C::WARPS * GPUOS_KV4_RUN);
+    if (nblk > gridDim.x) nblk = gridDim.x;
+    if (blockIdx.x >= nblk) return;
+    const uint64_t nt = nblk * C::WARPS;
+    const uint64_t tile = (uint64_t)blockIdx.x * C::WARPS + warp;
+    uint64_t u = W * tile / nt;
+    const uint64_t u1 = W * (tile + 1) / nt;
+    Kv4Pos p;
+    uint32_t used = 0; /* pages taken so far: the ring's position */
+    if (u < u1) kv4_seek(a, u, p);
+    while (u < u1) {
+        const uint32_t end = (uint32_t)(u1 - u < p.np - p.page ? p.page + (u1 - u) : p.np);
+        const uint32_t begin = p.page;
+        bool bad;
+        (void)kv4_pages(a, p.len, bad);
+        if (!bad) { /* else the request's rows are left as they were */
+            Kv4State<G, NT> s;
+            const uint32_t h = p.item / a.RT, n = p.len ? end - begin : 0u;
+            const int32_t *row = a.table + (uint64_t)p.b * a.P + begin;
+            const uint64_t stride = (uint64_t)a.Hkv * PB;
+            const unsigned char *pool = a.pool + (uint64_t)h * PB;
+            /* page ids, 32 at a time in the lanes; one that is not in the
+             * pool stands for no keys (page 0 is read and masked) */
+            int32_t ids = lane < n ? __ldcg(row + lane) : 0, ids_next = 0;
+            auto issue = [&](uint32_t k, int32_t id) {
+                if (lane == 0) {
+                    const uint32_t slot = (used + k) % NS;
+                    mbar_expect(&bars[warp][slot], PB);
+                    bulk_g2s(mine + slot * PB, pool + (uint64_t)((uint32_t)id < a.npages ? (uint32_t)id : 0u) * stride, PB,
+                             &bars[warp][slot]);
+                }
+            };
+#pragma unroll
+            for (uint32_t k = 0; k < NS; k++) {
+                const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k);
+                if (k < n) issue(k, id);
+            }
+            kv4_begin(a, p, s);
+            for (uint32_t k = 0; k < n; k++) {
+                if ((k & 31u) == 0) {
+                    if (k) ids = ids_next;
+                    ids_next = k + 32u + lane < n ? __ldcg(row + k + 32u + lane) : 0;
+                }
+                const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k & 31u);
+                const uint32_t slot = (used + k) % NS, base = (begin + k) * GPUOS_KV4_PAGE;
+                const uint32_t valid = (uint32_t)id < a.npages ? (uint32_t)p.len : 0u;
+                (void)mbar_wait(&bars[warp][slot], (used + k) / NS & 1u); /* bounded, like every wait */
+                kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, s);
+                if (k + NS < n) {
+                    const uint32_t kn = k + NS;
+                    const int32_t nx = __shfl_sync(0xFFFFFFFFu, kn >> 5 != k >> 5 ? ids_next : ids, kn & 31u);
+                    __syncwarp(); /* every lane is done with this slot */
+                    if (lane == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    issue(kn, nx);
+                }
+            }
+            used += n;
+            kv4_finish(s);
+            if (begin == 0 && end == p.np) {
+                kv4_store(a, p, s);
+            } else {
+                /* the item goes on in the next warp: its state ends this
+                 * warp's run, and takes the place of the pages */
+                const bool tail = begin == 0;
+                __syncwarp();
+                kv4_part_put<G, NT>(reinterpret_cast<float4 *>(tail ? mine : sm + C::WARPS * C::WARP_BYTES + warp * C::FRAG), s);
+                if (lane == 0) {
+                    if (tail) {
+                        left[warp].tail = p.first;
+                        left[warp].b = p.b;
+                        left[warp].item = p.item;
+                        left[warp].np = p.np;
+                    } else {
+                        left[warp].head = p.first;
+                        left[warp].hb = p.b;
+                        left[warp].hitem = p.item;
+                        left[warp].hnp = p.np;
+                    }
+                }
+            }
+        }
+        u += end - begin;
+        kv4_next(a, p);
+    }
+    __syncthreads();
+    /* the items that warps of this block share, in order: a state that begins
+     * one (or goes on from the last block) and those that follow it */
+    const uint64_t b0 = W * (uint64_t)blockIdx.x / nblk, b1 = W * (blockIdx.x + 1ull) / nblk; /* the block's units */
+    constexpr uint32_t NE = NT * G * 64u; /* float4s of a state's accumulators */
+    float4 *const ws = reinterpret_cast<float4 *>(reinterpret_cast<float *>(d.aux2) + GPUOS_KV4_MAX_TILES);
+    bool out[2] = {false, false}; /* a state for the workspace: of an item that began earlier; of one that goes on */
+    uint32_t ob[2], oitem[2], onp[2];
+    unsigned long long ofirst[2];
+    bool seen = false;
+    for (uint32_t c = 0; c < 2u * C::WARPS; c++) { /* 2 w: warp w's head, 2 w + 1: its tail */
+        const uint32_t w0 = c >> 1;
+        const bool tail = c & 1u;
+        const unsigned long long first = tail ? left[w0].tail : left[w0].head;
+        if (first == ~0ull) continue;
+        /* a head goes with the state that an earlier warp of this block left
+         * of its item; only the block's first state can lack one */
+        if (!tail && (first >= b0 || seen)) continue;
+        seen = true;
+        const uint32_t b = tail ? left[w0].b : left[w0].hb, item = tail ? left[w0].item : left[w0].hitem;
+        const uint32_t np = tail ? left[w0].np : left[w0].hnp;
+        const bool begins = tail, ends = first + np <= b1;
+        for (uint32_t idx = threadIdx.x; idx < NE; idx += C::WARPS * 32u) {
+            float m = -FLT_MAX, l = 0.0f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t w = w0; w < C::WARPS; w++) {
+                const bool t = w == w0 && tail;
+                if (w > w0 && left[w].head != first) continue;
+                const float4 *st = reinterpret_cast<const float4 *>(t ? sm + w * C::WARP_BYTES : sm + C::WARPS * C::WARP_BYTES + w * C::FRAG);
+                kv4_fold(kv4_ml<G, NT>(st[kv4_ml_at<G, NT>(idx)], idx), st[NT * 4 + idx], m, l, v);
+            }
+            if (begins && ends) {
+                kv4_out4<G, NT>(a, b, item, __ldcg(a.lens + b), idx, l, v);
+            } else {
+                float4 *st = ws + ((uint64_t)blockIdx.x * 2u + (begins ? 1u : 0u)) * (Kv4Part<G, NT>::floats / 4u);
+                __stcg(st + NT * 4 + idx, v);
+                if ((idx & 31u) < 4u && (idx >> 6 & (G - 1u)) == 0u) /* the row's (m, l), once */
+                    __stcg(reinterpret_cast<float2 *>(st + kv4_ml_at<G, NT>(idx)) + (idx >> 5 & 1u), make_float2(m, l));
+            }
+        }
+        if (!(begins && ends)) {
+            const int k = begins ? 1 : 0;
+            out[k] = true;
+            ob[k] = b;
+            oitem[k] = item;
+            onp[k] = np;
+            ofirst[k] = first;
+        }
+    }
+    if (!out[0] && !out[1]) return;
+    __syncthreads();
+    if (threadIdx.x < 2u) {
+        last[threadIdx.x] = 0;
+        if (out[threadIdx.x]) {
+            /* the blocks of an item count at the counter of its first block */
+            const uint64_t first = ofirst[threadIdx.x];
+            const uint32_t blk0 = (uint32_t)(((first + 1) * nblk - 1) / W);
+            const uint32_t F = (uint32_t)(((first + onp[threadIdx.x]) * nblk - 1) / W) - blk0 + 1;
+            uint32_t *cnt = kv4_counters(&d) + blk0;
+            if (atom_add_acq_rel_gpu32(cnt, 1u) == F - 1) {
+                *cnt = 0; /* left zero for the next call */
+                last[threadIdx.x] = F;
+            }
+        }
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; k++) {
+        const uint32_t F = last[k];
+        if (F == 0) continue;
+        const uint32_t blk0 = (uint32_t)(((ofirst[k] + 1) * nblk - 1) / W);
+        const int32_t len = __ldcg(a.lens + ob[k]);
+        for (uint32_t idx = threadIdx.x; idx < NE; idx += C::WARPS * 32u) {
+            float m = -FLT_MAX, l = 0.0f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t f0 = 0; f0 < F; f0 += 8) {
+                float4 ml[8], x[8];
+#pragma unroll
+                for (uint32_t f = 0; f < 8; f++) {
+                    const uint32_t ff = min(f0 + f, F - 1);
+                    const float4 *st = ws + ((uint64_t)(blk0 + ff) * 2u + (ff == 0 ? 1u : 0u)) * (Kv4Part<G, NT>::floats / 4u);
+                    ml[f] = __ldcg(st + kv4_ml_at<G, NT>(idx));
+                    x[f] = __ldcg(st + NT * 4 + idx);
+                }
+#pragma unroll
+                for (uint32_t f = 0; f < 8; f++)
+                    if (f0 + f < F) kv4_fold(kv4_ml<G, NT>(ml[f], idx), x[f], m, l, v);
+            }
+            kv4_out4<G, NT>(a, ob[k], oitem[k], len, idx, l, v);
+        }
+    }
+}
+
+template <int G, int NT>
+static int kv4_attend_launch(const gpuos_devdesc &d, void *stream)
+{
+    using C = Kv4Block<G, NT>;
+    /* once per device: its SMs, and the kernel's shared memory there */
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+    int sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+        if (cudaFuncSetAttribute(gpuos_kv4_attend_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)C::SMEM) != cudaSuccess)
+            return -1;
+        known[dev].store(sms, std::memory_order_relaxed);
+    }
+    /* no more blocks than the longest requests can fill */
+    const uint64_t g = (d.dims[1] & 0xFFFFu) / (d.dims[1] >> 16), T = d.dims[2] >> 16;
+    const uint64_t units = (uint64_t)d.dims[0] * d.dims[3] * (d.dims[1] >> 16) * ((T * g + 8 * NT - 1) / (8 * NT));
+    uint64_t grid = (units + C::WARPS * GPUOS_KV4_RUN - 1) / (C::WARPS * GPUOS_KV4_RUN);
+    if (grid > (uint64_t)sms) grid = (uint64_t)sms;
+    if (grid > GPUOS_KV4_MAX_BLOCKS) grid = GPUOS_KV4_MAX_BLOCKS;
+    gpuos_kv4_attend_kernel<G, NT><<<(uint32_t)grid, C::WARPS * 32, C::SMEM, (cudaStream_t)stream>>>(d);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+/* The other ops: one warp a tile, as in the executor. */
+template <int OP>
+__global__ void __launch_bounds__(32) gpuos_kv4_eager_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_op(&d, blockIdx.x);
+    if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_op(&d, blockIdx.x);
+    if (OP == GPUOS_OP_PAGE_COPY) (void)page_copy_op(&d, blockIdx.x);
+}
+template <int OP>
+static int kv4_tiles_launch(const gpuos_devdesc &d, void *stream)
+{
+    gpuos_kv4_eager_kernel<OP><<<d.ntiles, 32, 0, (cudaStream_t)stream>>>(d);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+static int kv4_eager_launch(const gpuos_devdesc &d, void *stream)
+{
+    switch (d.op_id) {
+    case GPUOS_OP_KV4_WRITE: return kv4_tiles_launch<GPUOS_OP_KV4_WRITE>(d, stream);
+    case GPUOS_OP_KV4_READ: return kv4_tiles_launch<GPUOS_OP_KV4_READ>(d, stream);
+    case GPUOS_OP_PAGE_COPY: return kv4_tiles_launch<GPUOS_OP_PAGE_COPY>(d, stream);
+    default: break;
+    }
+    if (d.dims[0] == 0) return 0;
+    const uint32_t rows = (d.dims[2] >> 16) * ((d.dims[1] & 0xFFFFu) / (d.dims[1] >> 16));
+    if ((d.dims[2] & 0xFFFFu) == 128) return rows <= 8 ? kv4_attend_launch<4, 1>(d, stream) : kv4_attend_launch<4, 2>(d, stream);
+    return rows <= 8 ? kv4_attend_launch<2, 1>(d, stream) : kv4_attend_launch<2, 2>(d, stream);
 }
 #endif /* GPUOS_KV4_CUH */

@@ -69,7 +69,7 @@ _maps = {}
 
 
 def unpack(pool):
-    """Keys and values float64 [pages, heads, 32, D] of a pool."""
+    """Keys, values and the values' scales float64 [pages, heads, 32, D] of a pool."""
     D = pool.shape[2] // 34
     if D not in _maps:
         key, c = np.meshgrid(np.arange(PAGE), np.arange(D), indexing="ij")
@@ -79,6 +79,7 @@ def unpack(pool):
     for at, sc in ((k, ks), (v, vs)):
         code = pool[:, :, at] >> (4 * (c % 2)).astype(np.uint8) & 15
         out.append(values(code, pool[:, :, sc][..., ::32]))
+    out.append(2.0 ** (np.repeat(pool[:, :, vs][..., ::32], 32, -1).astype(float) - 127))
     return out
 
 
@@ -88,14 +89,14 @@ def attend(q, pool, table, lens, scale):
     B, T, H, D = q.shape
     heads = pool.shape[1]
     g = H // heads
-    K, V = unpack(pool)
+    K, V, S = unpack(pool)
     out, tol = np.zeros(q.shape), np.zeros(q.shape)
     for b in range(B):
         n = int(lens[b])
         at = np.arange(n)
         page = table[b][at // PAGE]
         inside = (page >= 0) & (page < pool.shape[0])
-        kb, vb = K[np.where(inside, page, 0), :, at % PAGE], V[np.where(inside, page, 0), :, at % PAGE]  # [n, heads, D]
+        kb, vb, sb = (x[np.where(inside, page, 0), :, at % PAGE] for x in (K, V, S))  # [n, heads, D]
         for t in range(T):
             see = inside & (at <= n - T + t)
             if not see.any():
@@ -107,20 +108,24 @@ def attend(q, pool, table, lens, scale):
                 p /= p.sum()
                 out[b, t, h] = p @ v
                 reach = np.abs(k) @ np.abs(q[b, t, h]) * abs(scale)
-                tol[b, t, h] = bound(p, np.abs(v), reach.max(), D)
+                tol[b, t, h] = bound(p, np.abs(v), sb[see, h // g].max(0), reach.max(), D)
     return out, tol
 
 
-def bound(p, v, reach, D):
+def bound(p, v, scale, reach, D):
     """|error| before the output's rounding, from the kernel's arithmetic:
-    weights rounded to f16 (2^-11 each); scores summed in fp32 over D products
-    and D / 32 scale groups, scaled and shifted (each a rounding of at most
-    2^-24 of `reach`, the largest sum of |q k| scale), so a weight is off by
-    twice that many nats against the sum; exp2 and the rescaling of the
-    accumulators good to 2^-18; a value whose scale lies 2^-22 below the
-    largest of its group is dropped."""
+    weights rounded to f16 (2^-11 each, or 2^-31 of the largest where they are
+    subnormal); scores summed in fp32 over D products and D / 32 scale groups,
+    scaled and shifted (each a rounding of at most 2^-24 of `reach`, the
+    largest sum of |q k| scale), so a weight is off by twice that many nats
+    against the sum; exp2 and the rescaling of the accumulators good to 2^-18.
+    Values: a weight is multiplied by 2^(b - E + 7) in f16, b the exponent of
+    the value's scale and E the largest of the group's, which is zero for b
+    <= E - 22: such a value is at most 6 * 2^-22 of the largest scale; a
+    product below 2^-14 is off by 2^-25, when the largest weight times the
+    largest scale is 2^13 or more: 6 * 2^-38 of that scale for each key."""
     rel = 2.0 ** -11 + 2 * (D + 8) * 2.0 ** -24 * reach + 2.0 ** -18
-    return rel * (p @ v) + 2.0 ** -20 * v.max(0)
+    return rel * (p @ v) + 2.0 ** -31 * v.sum(0) + (6 * 2.0 ** -22 + len(p) * 6 * 2.0 ** -38) * scale
 
 
 def random_pool(rng, pages, heads, D, spread=3.0):
