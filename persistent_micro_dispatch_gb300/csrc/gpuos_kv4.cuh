@@ -146,6 +146,13 @@ DEV void kv4_args(const gpuos_devdesc *d, uint32_t rows_per_tile, Kv4Args &a)
     a.npages = d->dims[4];
     a.scale = d->fparam[0] * 1.4426950408889634f;
 }
+/* Query row r of a cache head: token t, query head h g + hh. */
+DEV void kv4_token(const Kv4Args &a, uint32_t r, uint32_t &t, uint32_t &hh)
+{
+    t = a.T == 1 ? 0u : r / a.g;
+    hh = r - t * a.g;
+}
+DEV uint32_t kv4_head(const Kv4Args &a, uint32_t item) { return a.RT == 1 ? item : item / a.RT; }
 /* Pages of a request; a length that its table row cannot hold counts as one
  * unit that does nothing (bad). */
 DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len, bool &bad)
@@ -166,40 +173,62 @@ struct Kv4Pos {
     int32_t len;
     uint64_t first; /* first unit of the item */
 };
-/* All units of the call (every lane). */
-DEV uint64_t kv4_units(const Kv4Args &a)
+/* All units of the call, and (every lane) the length of request `lane`. */
+DEV uint64_t kv4_units(const Kv4Args &a, int32_t &len0)
 {
-    unsigned long long n = 0;
-    for (uint32_t i = lane_id(); i < a.B; i += 32) n += kv4_pages(a, __ldcg(a.lens + i));
+    const uint32_t lane = lane_id();
+    uint32_t n = 0; /* B P < 2^31: page counts fit 32 bits */
+    len0 = 0;
+    for (uint32_t i = lane; i < a.B; i += 128) { /* four loads in flight */
+        int32_t len[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    return n * a.Hkv * a.RT;
+        for (int k = 0; k < 4; k++) len[k] = i + 32u * k < a.B ? __ldcg(a.lens + i + 32u * k) : 0;
+        if (i == lane) len0 = len[0];
+#pragma unroll
+        for (int k = 0; k < 4; k++) n += i + 32u * k < a.B ? kv4_pages(a, len[k]) : 0u;
+    }
+    return (uint64_t)__reduce_add_sync(0xFFFFFFFFu, n) * a.Hkv * a.RT;
 }
+DEV uint64_t kv4_div(uint64_t n, uint32_t d) { return n >> 32 ? n / d : (uint64_t)((uint32_t)n / d); }
+/* W units in n runs that differ by one unit at most: the first W mod n have
+ * one more than the others. */
+struct Kv4Runs {
+    uint64_t base, more; /* units of a run; runs with one more */
+    DEV Kv4Runs(uint64_t W, uint32_t n) : base(kv4_div(W, n)) { more = W - base * n; }
+    DEV uint64_t start(uint64_t run) const { return run * base + (run < more ? run : more); }
+    DEV uint32_t run_of(uint64_t u) const
+    {
+        const uint64_t cut = more * (base + 1);
+        if (u < cut) return (uint32_t)((u | base) >> 32 ? u / (base + 1) : (uint32_t)u / ((uint32_t)base + 1u));
+        const uint64_t v = u - cut;
+        return (uint32_t)(more + ((v | base) >> 32 ? v / base : (uint32_t)v / (uint32_t)base));
+    }
+};
 /* The place of unit u (u < the number of units). */
-DEV void kv4_seek(const Kv4Args &a, uint64_t u, Kv4Pos &p)
+DEV void kv4_seek(const Kv4Args &a, uint64_t u, int32_t len0, Kv4Pos &p)
 {
     const uint32_t lane = lane_id(), HR = a.Hkv * a.RT;
-    unsigned long long base = 0;
+    const uint32_t pg = (uint32_t)kv4_div(u, HR); /* pages of all requests before u's request: at most this */
+    uint32_t base = 0;
     for (uint32_t i0 = 0; i0 < a.B; i0 += 32) {
         const uint32_t i = i0 + lane;
-        const int32_t len = i < a.B ? __ldcg(a.lens + i) : 0;
-        const unsigned long long cnt = i < a.B ? (unsigned long long)kv4_pages(a, len) * HR : 0ull;
-        unsigned long long incl = cnt;
+        const int32_t len = i0 == 0 ? len0 : (i < a.B ? __ldcg(a.lens + i) : 0);
+        const uint32_t cnt = i < a.B ? kv4_pages(a, len) : 0u;
+        uint32_t incl = cnt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
             if (lane >= (uint32_t)o) incl += v;
         }
-        const unsigned long long lo = base + incl - cnt;
-        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, u >= lo && u < lo + cnt);
+        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, pg < base + incl);
         if (bal) {
             const int src = __ffs(bal) - 1;
             p.b = i0 + (uint32_t)src;
             p.len = __shfl_sync(0xFFFFFFFFu, len, src);
             p.np = kv4_pages(a, p.len);
-            const uint64_t lo_b = __shfl_sync(0xFFFFFFFFu, lo, src);
+            const uint64_t lo_b = (uint64_t)(base + __shfl_sync(0xFFFFFFFFu, incl, src) - p.np) * HR;
             const uint64_t off = u - lo_b;
-            p.item = (uint32_t)(off / p.np);
+            p.item = (uint32_t)kv4_div(off, p.np);
             p.page = (uint32_t)(off - (uint64_t)p.item * p.np);
             p.first = lo_b + (uint64_t)p.item * p.np;
             return;
@@ -234,6 +263,7 @@ struct Kv4State {
     float l[NT][2];       /* this lane's part of the running sum */
     float acc[NT][G][2][4];
     uint32_t E[G]; /* largest value-scale exponent met in each group */
+    uint32_t El, bias2; /* E of group lane % G; 22 - El in both halves */
     uint32_t lim[NT][2]; /* keys that the row sees */
     uint32_t min_lim;    /* least of them over the tile's rows */
 };
@@ -241,26 +271,43 @@ struct Kv4State {
 DEV uint32_t kv4_row_limit(const Kv4Args &a, int32_t len, uint32_t r)
 {
     if (r >= a.T * a.g) return (uint32_t)len;
+    if (a.T == 1) return (uint32_t)len;
     const int64_t n = (int64_t)len - (int64_t)a.T + 1 + (int64_t)(r / a.g);
     return n > 0 ? (uint32_t)n : 0u;
 }
 
+/* The item's query rows, as they lie in memory. */
 template <int G, int NT>
-DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, Kv4State<G, NT> &s)
+struct Kv4Query {
+    uint4 raw[NT][G]; /* row 8 nt + i: channels 32 g + 8 j + {0..7} */
+};
+template <int G, int NT>
+DEV void kv4_load_q(const Kv4Args &a, const Kv4Pos &p, Kv4Query<G, NT> &x)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
-    const uint32_t h = p.item / a.RT, r0 = (p.item - h * a.RT) * 8u * NT;
+    const uint32_t h = kv4_head(a, p.item), r0 = (p.item - h * a.RT) * 8u * NT;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
         const uint32_t r = r0 + 8u * nt + i;
-        uint4 raw[G];
         const bool have = r < a.T * a.g;
-        const uint32_t t = r / a.g, hh = r - t * a.g;
+        uint32_t t, hh;
+        kv4_token(a, r, t, hh);
         const uint16_t *qr = a.q + (((uint64_t)p.b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 8u * j;
 #pragma unroll
         for (int g = 0; g < G; g++)
-            raw[g] = have ? __ldcg(reinterpret_cast<const uint4 *>(qr + 32 * g)) : make_uint4(0, 0, 0, 0);
+            x.raw[nt][g] = have ? __ldcg(reinterpret_cast<const uint4 *>(qr + 32 * g)) : make_uint4(0, 0, 0, 0);
+    }
+}
+/* An item's first state. */
+template <int G, int NT>
+DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx, Kv4State<G, NT> &s)
+{
+    const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
+    const uint32_t h = kv4_head(a, p.item), r0 = (p.item - h * a.RT) * 8u * NT;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        const uint4(&raw)[G] = qx.raw[nt];
         float top = 0.0f;
         bool odd = false; /* a NaN or infinity in the row: left as it is */
 #pragma unroll
@@ -312,6 +359,8 @@ DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, Kv4State<G, NT> &s)
     }
 #pragma unroll
     for (int g = 0; g < G; g++) s.E[g] = 0;
+    s.El = 0;
+    s.bias2 = 22u | 22u << 16;
     s.min_lim = kv4_row_limit(a, p.len, r0); /* rows come in order of t */
 }
 
@@ -377,6 +426,7 @@ DEV void kv4_grow(uint32_t base, uint32_t key0, uint32_t &vw, Kv4State<G, NT> &s
         /* 2^(E - e); below 2^-126 nothing is left of it */
         const float up = s.E[g] + 127u > e ? kv4_pow2((int)s.E[g] - (int)e) : 0.0f;
         s.E[g] = e;
+        if (lane % G == (uint32_t)g) s.El = e;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -415,21 +465,14 @@ DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
         const uint32_t word = lane % (8u * G), key0 = word / G * 4u;
         uint32_t vw = kv4_ld4<GLOBAL>(pg + 33u * D + 4u * word);
         if (nv < GPUOS_KV4_PAGE) vw &= kv4_keep(key0, nv);
-        /* E of the lane's group */
-        uint32_t E = s.E[0];
-#pragma unroll
-        for (int g = 1; g < G; g++) E = lane % G == (uint32_t)g ? s.E[g] : E;
-        const uint32_t b02 = vw & 0x00FF00FFu, b13 = vw >> 8 & 0x00FF00FFu;
-        const uint32_t top = __vimax_s16x2_relu(b02, b13);
-        if (__any_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16) > E)) {
+        const uint32_t top = __vimax_s16x2_relu(vw & 0x00FF00FFu, vw >> 8 & 0x00FF00FFu);
+        if (__any_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16) > s.El)) {
             kv4_grow<G, NT>(base, key0, vw, s);
-            E = s.E[0];
-#pragma unroll
-            for (int g = 1; g < G; g++) E = lane % G == (uint32_t)g ? s.E[g] : E;
+            const uint32_t bias = (22u - s.El) & 0xFFFFu;
+            s.bias2 = bias | bias << 16;
         }
-        const uint32_t bias = (22u - E) & 0xFFFFu, bias2 = bias | bias << 16;
-        vs.x = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4140), bias2, 0u) << 10;
-        vs.y = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4342), bias2, 0u) << 10;
+        vs.x = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4140), s.bias2, 0u) << 10;
+        vs.y = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4342), s.bias2, 0u) << 10;
     }
     if (!GLOBAL) {
         __syncwarp(); /* the last page's readers are done */
@@ -640,14 +683,15 @@ DEV void kv4_store(const Kv4Args &a, const Kv4Pos &p, const Kv4State<G, NT> &s)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
-    const uint32_t h = p.item / a.RT, r0 = (p.item - h * a.RT) * 8u * NT;
+    const uint32_t h = kv4_head(a, p.item), r0 = (p.item - h * a.RT) * 8u * NT;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int c = 0; c < 2; c++) {
             const uint32_t r = r0 + 8u * nt + 2u * j + c;
             if (r >= a.T * a.g) continue;
-            const uint32_t t = r / a.g, hh = r - t * a.g;
+            uint32_t t, hh;
+            kv4_token(a, r, t, hh);
             uint16_t *o = a.out + (((uint64_t)p.b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 4u * i;
             const bool none = s.l[nt][c] == 0.0f;
             const float z = kv4_empty(s.lim[nt][c]);
@@ -727,7 +771,7 @@ template <int G, int NT>
 DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT> &s)
 {
     constexpr uint32_t PB = kv4_page_bytes(32u * G);
-    const uint32_t lane = lane_id(), h = p.item / a.RT;
+    const uint32_t lane = lane_id(), h = kv4_head(a, p.item);
     const int32_t *row = a.table + (uint64_t)p.b * a.P;
     const uint64_t stride = (uint64_t)a.Hkv * PB;
     const unsigned char *pool = a.pool + (uint64_t)h * PB;
@@ -819,13 +863,15 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
 {
     Kv4Args a;
     kv4_args(d, 8u * NT, a);
-    const uint64_t W = kv4_units(a);
-    const uint64_t nt = d->ntiles < W ? d->ntiles : W;
+    int32_t len0;
+    const uint64_t W = kv4_units(a, len0);
+    const uint32_t nt = d->ntiles < W ? d->ntiles : (uint32_t)W;
     if (tile >= nt) return GPUOS_ST_OK;
-    uint64_t u = W * tile / nt;
-    const uint64_t u1 = W * (tile + 1ull) / nt;
+    const Kv4Runs runs(W, nt);
+    uint64_t u = runs.start(tile);
+    const uint64_t u1 = runs.start(tile + 1ull);
     Kv4Pos p;
-    kv4_seek(a, u, p);
+    kv4_seek(a, u, len0, p);
     int status = GPUOS_ST_OK;
     while (u < u1) {
         const uint32_t end = (uint32_t)(u1 - u < p.np - p.page ? p.page + (u1 - u) : p.np);
@@ -836,13 +882,15 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
             status = GPUOS_ST_BAD_ARGS; /* the request's rows are left as they were */
         } else {
             Kv4State<G, NT> s;
-            kv4_begin(a, p, s);
+            Kv4Query<G, NT> qx;
+            kv4_load_q(a, p, qx);
+            kv4_begin(a, p, qx, s);
             const int st = p.len ? kv4_run(a, p, end, s) : GPUOS_ST_OK;
             if (st) status = st;
             kv4_finish(s);
             if (begin != 0 || end != p.np) {
-                const uint32_t first = (uint32_t)(((p.first + 1) * nt - 1) / W);
-                const uint32_t F = (uint32_t)(((p.first + p.np) * nt - 1) / W) - first + 1;
+                const uint32_t first = runs.run_of(p.first);
+                const uint32_t F = runs.run_of(p.first + p.np - 1) - first + 1;
                 uint32_t c = tile - first;
                 bool done = true;
                 for (uint32_t step = 1; step < F; step <<= 1) {
@@ -1110,11 +1158,13 @@ struct Kv4Block {
     static_assert(WARP_BYTES % 16 == 0 && FRAG % 16 == 0, "alignment");
 };
 /* What a warp leaves: the state of the item it began in the middle of, and of
- * the item that it does not finish (none: first = ~0). */
+ * the item that it does not finish (none: first unit ~0). */
+struct Kv4Item {
+    uint32_t b, item, np;
+};
 struct Kv4Left {
-    unsigned long long head, tail; /* the item's first unit */
-    uint32_t b, item, np, pad;     /* of the tail, or else of the head */
-    uint32_t hb, hitem, hnp, pad2; /* of the head */
+    unsigned long long head, tail; /* the items' first units */
+    Kv4Item hitem, titem;
 };
 
 template <int G, int NT>
@@ -1134,43 +1184,23 @@ DEV void kv4_part_put(float4 *p4, const Kv4State<G, NT> &s)
 }
 /* One quarter row of the output: element idx of a state's accumulators. */
 template <int G, int NT>
-DEV void kv4_out4(const Kv4Args &a, uint32_t b, uint32_t item, int32_t len, uint32_t idx, float l, float4 v)
+DEV void kv4_out4(const Kv4Args &a, const Kv4Item &it, uint32_t idx, float l, float4 v)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = idx & 31u, r2 = idx >> 5 & 1u, g = idx >> 6 & (G - 1u), nt = idx / (64u * G);
-    const uint32_t h = item / a.RT, r = (item - h * a.RT) * 8u * NT + 8u * nt + 2u * (lane & 3u) + r2;
+    const uint32_t h = kv4_head(a, it.item), r = (it.item - h * a.RT) * 8u * NT + 8u * nt + 2u * (lane & 3u) + r2;
     if (r >= a.T * a.g) return;
-    const uint32_t t = r / a.g, hh = r - t * a.g;
+    uint32_t t, hh;
+    kv4_token(a, r, t, hh);
     if (l == 0.0f) {
-        const float z = kv4_empty(kv4_row_limit(a, len, r));
+        const float z = kv4_empty(kv4_row_limit(a, __ldcg(a.lens + it.b), r));
         v = make_float4(z, z, z, z);
     }
     uint2 w;
     w.x = pack_bf2(v.x, v.y);
     w.y = pack_bf2(v.z, v.w);
-    *reinterpret_cast<uint2 *>(a.out + (((uint64_t)b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 32u * g + 4u * (lane >> 2)) = w;
+    *reinterpret_cast<uint2 *>(a.out + (((uint64_t)it.b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 32u * g + 4u * (lane >> 2)) = w;
 }
-/* m, l of element idx's row in a state. */
-template <int G, int NT>
-DEV float2 kv4_ml(float4 x, uint32_t idx) { return idx >> 5 & 1u ? make_float2(x.z, x.w) : make_float2(x.x, x.y); }
-template <int G, int NT>
-DEV uint32_t kv4_ml_at(uint32_t idx) { return idx / (64u * G) * 4u + (idx & 3u); }
-
-/* Add a state's element to a merge under way: mean v, weight l 2^m. */
-DEV void kv4_fold(float2 ml, float4 x, float &m, float &l, float4 &v)
-{
-    const float mn = fmaxf(m, ml.x);
-    const float ws = l * kv4_ex2(m - mn), wo = ml.y * kv4_ex2(ml.x - mn);
-    const float n = ws + wo, inv = n != 0.0f ? 1.0f / n : 0.0f;
-    const float c0 = ws * inv, c1 = wo * inv;
-    v.x = fmaf(x.x, c1, v.x * c0);
-    v.y = fmaf(x.y, c1, v.y * c0);
-    v.z = fmaf(x.z, c1, v.z * c0);
-    v.w = fmaf(x.w, c1, v.w * c0);
-    m = mn;
-    l = n;
-}
-
 template <int G, int NT>
 __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_attend_kernel(const __grid_constant__ gpuos_devdesc d)
 {
@@ -1179,7 +1209,13 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[C::WARPS][C::NS];
     __shared__ Kv4Left left[C::WARPS];
-    __shared__ uint32_t last[2];
+    __shared__ float weight[2][C::WARPS][8 * NT]; /* of the warps' heads and tails in their items */
+    __shared__ float2 total[2][C::WARPS][8 * NT]; /* those items' (m, l) */
+    __shared__ struct {
+        unsigned long long first;
+        Kv4Item it;
+        uint32_t blk0, last; /* the item's first block; its blocks, if all are here */
+    } shared[2];
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
     unsigned char *mine = sm + warp * C::WARP_BYTES;
     if (lane == 0) {
@@ -1191,18 +1227,25 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     __syncwarp();
     Kv4Args a;
     kv4_args(&d, 8u * NT, a);
-    const uint64_t W = kv4_units(a);
-    /* at least GPUOS_KV4_RUN pages a warp: fewer blocks, and fewer states to merge, when there is little work */
-    uint64_t nblk = (W + C::WARPS * GPUOS_KV4_RUN - 1) / (C::WARPS * GPUOS_KV4_RUN);
-    if (nblk > gridDim.x) nblk = gridDim.x;
+    int32_t len0;
+    const uint64_t W = kv4_units(a, len0);
+    /* Little work: at least GPUOS_KV4_RUN pages a warp, so fewer blocks, and
+     * as many for each item, so that with equal lengths none spans more. */
+    uint32_t nblk = gridDim.x;
+    if (W < (uint64_t)C::WARPS * GPUOS_KV4_RUN * nblk) {
+        const uint32_t items = a.B * a.Hkv * a.RT; /* <= W */
+        nblk = ((uint32_t)W + C::WARPS * GPUOS_KV4_RUN - 1) / (C::WARPS * GPUOS_KV4_RUN);
+        if (nblk > items) nblk = min((nblk + items - 1) / items * items, gridDim.x);
+    }
     if (blockIdx.x >= nblk) return;
-    const uint64_t nt = nblk * C::WARPS;
-    const uint64_t tile = (uint64_t)blockIdx.x * C::WARPS + warp;
-    uint64_t u = W * tile / nt;
-    const uint64_t u1 = W * (tile + 1) / nt;
+    const Kv4Runs runs(W, nblk); /* the blocks' runs, then the warps' */
+    const uint64_t b0 = runs.start(blockIdx.x), b1 = runs.start(blockIdx.x + 1ull);
+    const Kv4Runs mine_of(b1 - b0, C::WARPS);
+    uint64_t u = b0 + mine_of.start(warp);
+    const uint64_t u1 = b0 + mine_of.start(warp + 1u);
     Kv4Pos p;
-    uint32_t used = 0; /* pages taken so far: the ring's position */
-    if (u < u1) kv4_seek(a, u, p);
+    uint32_t slot = 0, parity = 0; /* the ring's position */
+    if (u < u1) kv4_seek(a, u, len0, p);
     while (u < u1) {
         const uint32_t end = (uint32_t)(u1 - u < p.np - p.page ? p.page + (u1 - u) : p.np);
         const uint32_t begin = p.page;
@@ -1210,46 +1253,49 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         (void)kv4_pages(a, p.len, bad);
         if (!bad) { /* else the request's rows are left as they were */
             Kv4State<G, NT> s;
-            const uint32_t h = p.item / a.RT, n = p.len ? end - begin : 0u;
+            const uint32_t h = kv4_head(a, p.item), n = p.len ? end - begin : 0u;
             const int32_t *row = a.table + (uint64_t)p.b * a.P + begin;
             const uint64_t stride = (uint64_t)a.Hkv * PB;
             const unsigned char *pool = a.pool + (uint64_t)h * PB;
             /* page ids, 32 at a time in the lanes; one that is not in the
              * pool stands for no keys (page 0 is read and masked) */
             int32_t ids = lane < n ? __ldcg(row + lane) : 0, ids_next = 0;
-            auto issue = [&](uint32_t k, int32_t id) {
+            Kv4Query<G, NT> qx;
+            kv4_load_q(a, p, qx); /* used after the first pages are on their way */
+            auto issue = [&](uint32_t at, int32_t id) {
                 if (lane == 0) {
-                    const uint32_t slot = (used + k) % NS;
-                    mbar_expect(&bars[warp][slot], PB);
-                    bulk_g2s(mine + slot * PB, pool + (uint64_t)((uint32_t)id < a.npages ? (uint32_t)id : 0u) * stride, PB,
-                             &bars[warp][slot]);
+                    mbar_expect(&bars[warp][at], PB);
+                    bulk_g2s(mine + at * PB, pool + ((uint32_t)id < a.npages ? (uint32_t)id : 0u) * stride, PB, &bars[warp][at]);
                 }
             };
 #pragma unroll
             for (uint32_t k = 0; k < NS; k++) {
                 const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k);
-                if (k < n) issue(k, id);
+                if (k < n) issue(slot + k < NS ? slot + k : slot + k - NS, id);
             }
-            kv4_begin(a, p, s);
+            kv4_begin(a, p, qx, s);
             for (uint32_t k = 0; k < n; k++) {
                 if ((k & 31u) == 0) {
                     if (k) ids = ids_next;
                     ids_next = k + 32u + lane < n ? __ldcg(row + k + 32u + lane) : 0;
                 }
                 const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k & 31u);
-                const uint32_t slot = (used + k) % NS, base = (begin + k) * GPUOS_KV4_PAGE;
+                const uint32_t base = (begin + k) * GPUOS_KV4_PAGE;
                 const uint32_t valid = (uint32_t)id < a.npages ? (uint32_t)p.len : 0u;
-                (void)mbar_wait(&bars[warp][slot], (used + k) / NS & 1u); /* bounded, like every wait */
+                (void)mbar_wait(&bars[warp][slot], parity); /* bounded, like every wait */
                 kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, s);
                 if (k + NS < n) {
                     const uint32_t kn = k + NS;
                     const int32_t nx = __shfl_sync(0xFFFFFFFFu, kn >> 5 != k >> 5 ? ids_next : ids, kn & 31u);
                     __syncwarp(); /* every lane is done with this slot */
                     if (lane == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    issue(kn, nx);
+                    issue(slot, nx);
+                }
+                if (++slot == NS) {
+                    slot = 0;
+                    parity ^= 1u;
                 }
             }
-            used += n;
             kv4_finish(s);
             if (begin == 0 && end == p.np) {
                 kv4_store(a, p, s);
@@ -1260,17 +1306,8 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 __syncwarp();
                 kv4_part_put<G, NT>(reinterpret_cast<float4 *>(tail ? mine : sm + C::WARPS * C::WARP_BYTES + warp * C::FRAG), s);
                 if (lane == 0) {
-                    if (tail) {
-                        left[warp].tail = p.first;
-                        left[warp].b = p.b;
-                        left[warp].item = p.item;
-                        left[warp].np = p.np;
-                    } else {
-                        left[warp].head = p.first;
-                        left[warp].hb = p.b;
-                        left[warp].hitem = p.item;
-                        left[warp].hnp = p.np;
-                    }
+                    (tail ? left[warp].tail : left[warp].head) = p.first;
+                    (tail ? left[warp].titem : left[warp].hitem) = Kv4Item{p.b, p.item, p.np};
                 }
             }
         }
@@ -1278,93 +1315,146 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         kv4_next(a, p);
     }
     __syncthreads();
-    /* the items that warps of this block share, in order: a state that begins
-     * one (or goes on from the last block) and those that follow it */
-    const uint64_t b0 = W * (uint64_t)blockIdx.x / nblk, b1 = W * (blockIdx.x + 1ull) / nblk; /* the block's units */
+    /* The items that warps of this block share, in order: the state that
+     * begins one (a warp's tail; or the block's first head, of an item that
+     * an earlier block began) and the heads that follow it. Lane w looks at
+     * warp w's. First each warp finds the weights of its own two states, row
+     * by row, against the others of their items; then a thread for each four
+     * channels adds the states' means. */
     constexpr uint32_t NE = NT * G * 64u; /* float4s of a state's accumulators */
-    float4 *const ws = reinterpret_cast<float4 *>(reinterpret_cast<float *>(d.aux2) + GPUOS_KV4_MAX_TILES);
-    bool out[2] = {false, false}; /* a state for the workspace: of an item that began earlier; of one that goes on */
-    uint32_t ob[2], oitem[2], onp[2];
-    unsigned long long ofirst[2];
-    bool seen = false;
-    for (uint32_t c = 0; c < 2u * C::WARPS; c++) { /* 2 w: warp w's head, 2 w + 1: its tail */
-        const uint32_t w0 = c >> 1;
-        const bool tail = c & 1u;
-        const unsigned long long first = tail ? left[w0].tail : left[w0].head;
+    const unsigned long long head = lane < C::WARPS ? left[lane].head : ~0ull, tail = lane < C::WARPS ? left[lane].tail : ~0ull;
+    for (uint32_t k = 0; k < 2; k++) {
+        const unsigned long long first = __shfl_sync(0xFFFFFFFFu, k ? tail : head, warp);
         if (first == ~0ull) continue;
-        /* a head goes with the state that an earlier warp of this block left
-         * of its item; only the block's first state can lack one */
-        if (!tail && (first >= b0 || seen)) continue;
-        seen = true;
-        const uint32_t b = tail ? left[w0].b : left[w0].hb, item = tail ? left[w0].item : left[w0].hitem;
-        const uint32_t np = tail ? left[w0].np : left[w0].hnp;
-        const bool begins = tail, ends = first + np <= b1;
-        for (uint32_t idx = threadIdx.x; idx < NE; idx += C::WARPS * 32u) {
-            float m = -FLT_MAX, l = 0.0f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (uint32_t w = w0; w < C::WARPS; w++) {
-                const bool t = w == w0 && tail;
-                if (w > w0 && left[w].head != first) continue;
-                const float4 *st = reinterpret_cast<const float4 *>(t ? sm + w * C::WARP_BYTES : sm + C::WARPS * C::WARP_BYTES + w * C::FRAG);
-                kv4_fold(kv4_ml<G, NT>(st[kv4_ml_at<G, NT>(idx)], idx), st[NT * 4 + idx], m, l, v);
-            }
-            if (begins && ends) {
-                kv4_out4<G, NT>(a, b, item, __ldcg(a.lens + b), idx, l, v);
-            } else {
-                float4 *st = ws + ((uint64_t)blockIdx.x * 2u + (begins ? 1u : 0u)) * (Kv4Part<G, NT>::floats / 4u);
-                __stcg(st + NT * 4 + idx, v);
-                if ((idx & 31u) < 4u && (idx >> 6 & (G - 1u)) == 0u) /* the row's (m, l), once */
-                    __stcg(reinterpret_cast<float2 *>(st + kv4_ml_at<G, NT>(idx)) + (idx >> 5 & 1u), make_float2(m, l));
-            }
+        const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head == first), own = __ballot_sync(0xFFFFFFFFu, tail == first);
+        const uint32_t r = lane % (8u * NT);
+        /* the row's (m, l) in the state of warp w, a tail or a head */
+        auto ml_of = [&](uint32_t w, bool t) {
+            return reinterpret_cast<const float2 *>(t ? sm + w * C::WARP_BYTES : sm + C::WARPS * C::WARP_BYTES + w * C::FRAG)[r];
+        };
+        float M = -FLT_MAX, l = 0.0f;
+        float2 x = make_float2(-FLT_MAX, 0.0f);
+        if (own) x = ml_of((uint32_t)__ffs((int)own) - 1u, true);
+        M = x.x;
+        for (uint32_t hs = heads; hs; hs &= hs - 1u) M = fmaxf(M, ml_of((uint32_t)__ffs((int)hs) - 1u, false).x);
+        l = x.y * kv4_ex2(x.x - M);
+        for (uint32_t hs = heads; hs; hs &= hs - 1u) {
+            const float2 y = ml_of((uint32_t)__ffs((int)hs) - 1u, false);
+            l = fmaf(y.y, kv4_ex2(y.x - M), l);
         }
-        if (!(begins && ends)) {
-            const int k = begins ? 1 : 0;
-            out[k] = true;
-            ob[k] = b;
-            oitem[k] = item;
-            onp[k] = np;
-            ofirst[k] = first;
+        const float2 me = ml_of(warp, k);
+        if (lane < 8u * NT) {
+            weight[k][warp][r] = l != 0.0f ? me.y * kv4_ex2(me.x - M) / l : 0.0f;
+            total[k][warp][r] = make_float2(M, l);
         }
     }
-    if (!out[0] && !out[1]) return;
     __syncthreads();
-    if (threadIdx.x < 2u) {
-        last[threadIdx.x] = 0;
-        if (out[threadIdx.x]) {
-            /* the blocks of an item count at the counter of its first block */
-            const uint64_t first = ofirst[threadIdx.x];
-            const uint32_t blk0 = (uint32_t)(((first + 1) * nblk - 1) / W);
-            const uint32_t F = (uint32_t)(((first + onp[threadIdx.x]) * nblk - 1) / W) - blk0 + 1;
+    const uint32_t orphan = __ballot_sync(0xFFFFFFFFu, head < b0), tails = __ballot_sync(0xFFFFFFFFu, tail != ~0ull);
+    float4 *const ws = reinterpret_cast<float4 *>(reinterpret_cast<float *>(d.aux2) + GPUOS_KV4_MAX_TILES);
+    uint32_t out = 0; /* bit 0: a state of an item that began earlier is in the workspace; bit 1: of one that goes on */
+    uint32_t todo = tails << 1 | (orphan ? 1u : 0u); /* bit 0: the orphan; bit 1 + w: warp w's tail */
+    while (todo) {
+        const uint32_t c = (uint32_t)__ffs((int)todo) - 1u;
+        todo &= todo - 1u;
+        const bool begins = c != 0;
+        const uint32_t w0 = begins ? c - 1u : (uint32_t)__ffs((int)orphan) - 1u;
+        const unsigned long long first = __shfl_sync(0xFFFFFFFFu, begins ? tail : head, w0);
+        const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head == first);
+        const Kv4Item it = begins ? left[w0].titem : left[w0].hitem;
+        const bool whole = begins && first + it.np <= b1;
+        for (uint32_t idx = threadIdx.x; idx < NE; idx += C::WARPS * 32u) {
+            const uint32_t r = idx / (64u * G) * 8u + 2u * (idx & 3u) + (idx >> 5 & 1u); /* the element's row */
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (begins) {
+                const float wt = weight[1][w0][r];
+                const float4 x = reinterpret_cast<const float4 *>(sm + w0 * C::WARP_BYTES)[NT * 4 + idx];
+                v = make_float4(x.x * wt, x.y * wt, x.z * wt, x.w * wt);
+            }
+            for (uint32_t hs = heads; hs; hs &= hs - 1u) {
+                const uint32_t w = (uint32_t)__ffs((int)hs) - 1u;
+                const float wt = weight[0][w][r];
+                const float4 x = reinterpret_cast<const float4 *>(sm + C::WARPS * C::WARP_BYTES + w * C::FRAG)[NT * 4 + idx];
+                v.x = fmaf(x.x, wt, v.x);
+                v.y = fmaf(x.y, wt, v.y);
+                v.z = fmaf(x.z, wt, v.z);
+                v.w = fmaf(x.w, wt, v.w);
+            }
+            const float2 ml = total[begins][w0][r];
+            if (whole) {
+                kv4_out4<G, NT>(a, it, idx, ml.y, v);
+            } else {
+                float4 *st = ws + ((uint64_t)blockIdx.x * 2u + (begins ? 1u : 0u)) * (C::FRAG / 16u);
+                __stcg(st + NT * 4 + idx, v);
+                if ((idx & 31u) < 4u && (idx >> 6 & (G - 1u)) == 0u) /* the row's (m, l), once */
+                    __stcg(reinterpret_cast<float2 *>(st) + r, ml);
+            }
+        }
+        if (!whole) {
+            out |= begins ? 2u : 1u;
+            if (threadIdx.x == 0) {
+                shared[begins].first = first;
+                shared[begins].it = it;
+            }
+        }
+    }
+    if (out == 0) return;
+    __syncthreads();
+    if (lane == 0 && warp < 2u) {
+        /* the blocks of an item count at the counter of its first block */
+        uint32_t last = 0;
+        if (out >> warp & 1u) {
+            const uint64_t first = shared[warp].first;
+            const uint32_t blk0 = runs.run_of(first);
+            const uint32_t F = runs.run_of(first + shared[warp].it.np - 1) - blk0 + 1;
             uint32_t *cnt = kv4_counters(&d) + blk0;
             if (atom_add_acq_rel_gpu32(cnt, 1u) == F - 1) {
                 *cnt = 0; /* left zero for the next call */
-                last[threadIdx.x] = F;
+                last = F;
             }
+            shared[warp].blk0 = blk0;
         }
+        shared[warp].last = last;
     }
     __syncthreads();
     for (int k = 0; k < 2; k++) {
-        const uint32_t F = last[k];
+        const uint32_t F = shared[k].last;
         if (F == 0) continue;
-        const uint32_t blk0 = (uint32_t)(((ofirst[k] + 1) * nblk - 1) / W);
-        const int32_t len = __ldcg(a.lens + ob[k]);
+        const uint32_t blk0 = shared[k].blk0;
         for (uint32_t idx = threadIdx.x; idx < NE; idx += C::WARPS * 32u) {
-            float m = -FLT_MAX, l = 0.0f;
+            const uint32_t r = idx / (64u * G) * 8u + 2u * (idx & 3u) + (idx >> 5 & 1u);
+            float M = -FLT_MAX, l = 0.0f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (uint32_t f0 = 0; f0 < F; f0 += 8) {
-                float4 ml[8], x[8];
+            constexpr uint32_t U = 10;
+            for (uint32_t f0 = 0; f0 < F; f0 += U) { /* a batch's loads are in flight together */
+                float2 ml[U];
+                float4 x[U];
 #pragma unroll
-                for (uint32_t f = 0; f < 8; f++) {
+                for (uint32_t f = 0; f < U; f++) {
                     const uint32_t ff = min(f0 + f, F - 1);
-                    const float4 *st = ws + ((uint64_t)(blk0 + ff) * 2u + (ff == 0 ? 1u : 0u)) * (Kv4Part<G, NT>::floats / 4u);
-                    ml[f] = __ldcg(st + kv4_ml_at<G, NT>(idx));
+                    const float4 *st = ws + ((uint64_t)(blk0 + ff) * 2u + (ff == 0 ? 1u : 0u)) * (C::FRAG / 16u);
+                    ml[f] = __ldcg(reinterpret_cast<const float2 *>(st) + r);
                     x[f] = __ldcg(st + NT * 4 + idx);
                 }
+                float mb = M;
 #pragma unroll
-                for (uint32_t f = 0; f < 8; f++)
-                    if (f0 + f < F) kv4_fold(kv4_ml<G, NT>(ml[f], idx), x[f], m, l, v);
+                for (uint32_t f = 0; f < U; f++) mb = fmaxf(mb, ml[f].x);
+                const float sc = kv4_ex2(M - mb);
+                l *= sc;
+                v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+                M = mb;
+#pragma unroll
+                for (uint32_t f = 0; f < U; f++) {
+                    if (f0 + f >= F) continue; /* duplicates */
+                    const float wt = ml[f].y * kv4_ex2(ml[f].x - M);
+                    l += wt;
+                    v.x = fmaf(x[f].x, wt, v.x);
+                    v.y = fmaf(x[f].y, wt, v.y);
+                    v.z = fmaf(x[f].z, wt, v.z);
+                    v.w = fmaf(x[f].w, wt, v.w);
+                }
             }
-            kv4_out4<G, NT>(a, ob[k], oitem[k], len, idx, l, v);
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            kv4_out4<G, NT>(a, shared[k].it, idx, l, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
         }
     }
 }
