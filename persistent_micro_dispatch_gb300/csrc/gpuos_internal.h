@@ -30,7 +30,9 @@
 #define GPUOS_KV4_TILES 1536              /* KV4 attention tiles (and KV4 row tiles aimed at) */
 #define GPUOS_KV4_MAX_TILES 2048          /* counters at the start of the KV4 workspace */
 #define GPUOS_KV4_MAX_BLOCKS 1024         /* blocks of an eager attention launch at most (workspace) */
-#define GPUOS_KV4_RUN 3                   /* pages of a warp's run at least, if there are as many */
+#ifndef GPUOS_KV4_LEAD
+#define GPUOS_KV4_LEAD 6                  /* units that starting an attention item counts for (a page counts one) */
+#endif
 #define GPUOS_KV4_MAX_PAGES (1u << 26)    /* pages of a pool, and of a table row: slots are below 2^31 */
 #define GPUOS_PAGE_CHUNK 16384            /* bytes of a page-copy tile */
 #define GPUOS_ROW_REG_MAX 4096            /* rows up to this width stay in registers */

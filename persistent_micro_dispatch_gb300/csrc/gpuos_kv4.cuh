@@ -101,11 +101,16 @@ DEV float kv4_ex2(float x)
  * row r sees. The T g query rows of a request that share a cache head
  * (g = H / Hkv; row r = t g + hh) are cut into row tiles of 8 NT rows.
  *
- * Work is counted in units of one page of one (request, head, row tile), a
- * request of length 0 being one unit; the units are numbered in that order
- * and cut into equal runs, one per warp, whatever the requests' lengths. A
- * run that ends inside an item leaves a partial state, merged with its
- * neighbours' (below).
+ * An item is one (request, head, row tile). Work is counted in units of one
+ * page of an item (a request of length 0: one unit), with GPUOS_KV4_LEAD more
+ * before its first page for what an item costs of itself (a warp fetches page
+ * ids, queries and a first page one after another: about 4 us, against 0.6 us
+ * for each further page); the units are numbered in that order and cut into
+ * equal runs, one per warp, whatever the requests' lengths. Measured with 0,
+ * 2, 3, 4, 6 units: 16 ragged requests of 2 to 4,099 tokens 32.5, 23.9, 21.9,
+ * 20.6, 20.2 us; 256 of 30 to 60 tokens 20.6, 17.4, 20.7, 18.2, 14.6; long
+ * ones do not care. A run that ends inside an item leaves a partial state, merged with
+ * its neighbours' (below).
  *
  * Numerics. q is scaled by a power of two for each row to [128, 256) and held
  * in f16: exact for the bf16 values within 2^-21 of the row's largest, and
@@ -169,15 +174,23 @@ DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len)
 /* A warp's place in the work. */
 struct Kv4Pos {
     uint32_t b, item; /* request; head * RT + row tile */
-    uint32_t page, np; /* next page, the request's pages */
+    uint32_t off, np; /* next unit of the item; its pages */
     int32_t len;
-    uint64_t first; /* first unit of the item */
+    uint64_t first; /* the unit of the item's first page */
 };
+/* The next units of an item up to `left`: pages [begin, end), none in the lead. */
+DEV uint32_t kv4_take(const Kv4Pos &p, uint64_t left, uint32_t &begin, uint32_t &end)
+{
+    const uint32_t span = p.np + GPUOS_KV4_LEAD - p.off, n = left < span ? (uint32_t)left : span;
+    begin = p.off > GPUOS_KV4_LEAD ? p.off - GPUOS_KV4_LEAD : 0u;
+    end = p.off + n > GPUOS_KV4_LEAD ? p.off + n - GPUOS_KV4_LEAD : 0u;
+    return n;
+}
 /* All units of the call, and (every lane) the length of request `lane`. */
 DEV uint64_t kv4_units(const Kv4Args &a, int32_t &len0)
 {
     const uint32_t lane = lane_id();
-    uint32_t n = 0; /* B P < 2^31: page counts fit 32 bits */
+    uint32_t n = 0; /* B P < 2^29: the sums fit 32 bits */
     len0 = 0;
     for (uint32_t i = lane; i < a.B; i += 128) { /* four loads in flight */
         int32_t len[4];
@@ -185,7 +198,7 @@ DEV uint64_t kv4_units(const Kv4Args &a, int32_t &len0)
         for (int k = 0; k < 4; k++) len[k] = i + 32u * k < a.B ? __ldcg(a.lens + i + 32u * k) : 0;
         if (i == lane) len0 = len[0];
 #pragma unroll
-        for (int k = 0; k < 4; k++) n += i + 32u * k < a.B ? kv4_pages(a, len[k]) : 0u;
+        for (int k = 0; k < 4; k++) n += i + 32u * k < a.B ? kv4_pages(a, len[k]) + GPUOS_KV4_LEAD : 0u;
     }
     return (uint64_t)__reduce_add_sync(0xFFFFFFFFu, n) * a.Hkv * a.RT;
 }
@@ -213,7 +226,7 @@ DEV void kv4_seek(const Kv4Args &a, uint64_t u, int32_t len0, Kv4Pos &p)
     for (uint32_t i0 = 0; i0 < a.B; i0 += 32) {
         const uint32_t i = i0 + lane;
         const int32_t len = i0 == 0 ? len0 : (i < a.B ? __ldcg(a.lens + i) : 0);
-        const uint32_t cnt = i < a.B ? kv4_pages(a, len) : 0u;
+        const uint32_t cnt = i < a.B ? kv4_pages(a, len) + GPUOS_KV4_LEAD : 0u;
         uint32_t incl = cnt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -226,11 +239,12 @@ DEV void kv4_seek(const Kv4Args &a, uint64_t u, int32_t len0, Kv4Pos &p)
             p.b = i0 + (uint32_t)src;
             p.len = __shfl_sync(0xFFFFFFFFu, len, src);
             p.np = kv4_pages(a, p.len);
-            const uint64_t lo_b = (uint64_t)(base + __shfl_sync(0xFFFFFFFFu, incl, src) - p.np) * HR;
+            const uint32_t span = p.np + GPUOS_KV4_LEAD;
+            const uint64_t lo_b = (uint64_t)(base + __shfl_sync(0xFFFFFFFFu, incl, src) - span) * HR;
             const uint64_t off = u - lo_b;
-            p.item = (uint32_t)kv4_div(off, p.np);
-            p.page = (uint32_t)(off - (uint64_t)p.item * p.np);
-            p.first = lo_b + (uint64_t)p.item * p.np;
+            p.item = (uint32_t)kv4_div(off, span);
+            p.off = (uint32_t)(off - (uint64_t)p.item * span);
+            p.first = lo_b + (uint64_t)p.item * span + GPUOS_KV4_LEAD;
             return;
         }
         base += __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -238,19 +252,21 @@ DEV void kv4_seek(const Kv4Args &a, uint64_t u, int32_t len0, Kv4Pos &p)
     p.b = a.B; /* not reached for u < kv4_units() */
     p.len = 0;
     p.np = 1;
-    p.item = p.page = 0;
+    p.item = p.off = 0;
     p.first = u;
 }
 /* The next item. */
 DEV void kv4_next(const Kv4Args &a, Kv4Pos &p)
 {
     p.first += p.np;
-    p.page = 0;
-    if (++p.item < a.Hkv * a.RT) return;
-    p.item = 0;
-    if (++p.b >= a.B) return;
-    p.len = __ldcg(a.lens + p.b);
-    p.np = kv4_pages(a, p.len);
+    p.off = 0;
+    if (++p.item >= a.Hkv * a.RT) {
+        p.item = 0;
+        if (++p.b >= a.B) return;
+        p.len = __ldcg(a.lens + p.b);
+        p.np = kv4_pages(a, p.len);
+    }
+    p.first += GPUOS_KV4_LEAD;
 }
 
 /* One item's running state in a warp: lane (i, j) holds query rows
@@ -764,11 +780,11 @@ DEV void kv4_part_merge(const float *part, Kv4State<G, NT> &s, bool left)
     }
 }
 
-/* The pages of one run within an item, [p.page, end): into the state. With
+/* The pages of one run within an item, [begin, end): into the state. With
  * staging the pages arrive by bulk copies into the two halves of the warp's
  * buffer in turn. */
 template <int G, int NT>
-DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT> &s)
+DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t begin, uint32_t end, Kv4State<G, NT> &s)
 {
     constexpr uint32_t PB = kv4_page_bytes(32u * G);
     const uint32_t lane = lane_id(), h = kv4_head(a, p.item);
@@ -782,9 +798,9 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT>
     uint32_t phs = staged ? w->phase[0] | w->phase[1] << 1 : 0u;
     /* page ids, 32 at a time in the warp's lanes; one that is not in the pool
      * stands for no keys (page 0 is read and masked) */
-    const uint32_t n = end - p.page;
+    const uint32_t n = end - begin;
     int32_t ids = 0, ids_next = 0;
-    auto load_ids = [&](uint32_t k) { return p.page + k + lane < end ? __ldcg(row + p.page + k + lane) : 0; };
+    auto load_ids = [&](uint32_t k) { return begin + k + lane < end ? __ldcg(row + begin + k + lane) : 0; };
     ids = load_ids(0);
     auto issue = [&](uint32_t k, int32_t id) {
         if (lane == 0) {
@@ -806,7 +822,7 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t end, Kv4State<G, NT>
         const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k & 31u);
         const bool there = (uint32_t)id < a.npages;
         if (!there) status = GPUOS_ST_BAD_ARGS;
-        const uint32_t base = (p.page + k) * GPUOS_KV4_PAGE, valid = there ? (uint32_t)p.len : 0u;
+        const uint32_t base = (begin + k) * GPUOS_KV4_PAGE, valid = there ? (uint32_t)p.len : 0u;
         if (staged) {
             const uint32_t hb = k & 1u;
             if (!mbar_wait(&w->mbar[hb], phs >> hb & 1u)) {
@@ -874,18 +890,18 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
     kv4_seek(a, u, len0, p);
     int status = GPUOS_ST_OK;
     while (u < u1) {
-        const uint32_t end = (uint32_t)(u1 - u < p.np - p.page ? p.page + (u1 - u) : p.np);
-        const uint32_t begin = p.page;
+        uint32_t begin, end;
+        u += kv4_take(p, u1 - u, begin, end);
         bool bad;
         (void)kv4_pages(a, p.len, bad);
         if (bad) {
             status = GPUOS_ST_BAD_ARGS; /* the request's rows are left as they were */
-        } else {
+        } else if (begin < end) {
             Kv4State<G, NT> s;
             Kv4Query<G, NT> qx;
             kv4_load_q(a, p, qx);
             kv4_begin(a, p, qx, s);
-            const int st = p.len ? kv4_run(a, p, end, s) : GPUOS_ST_OK;
+            const int st = p.len ? kv4_run(a, p, begin, end, s) : GPUOS_ST_OK;
             if (st) status = st;
             kv4_finish(s);
             if (begin != 0 || end != p.np) {
@@ -917,7 +933,6 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
                 kv4_store(a, p, s);
             }
         }
-        u += end - begin;
         kv4_next(a, p);
     }
     return status;
@@ -1229,12 +1244,12 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     kv4_args(&d, 8u * NT, a);
     int32_t len0;
     const uint64_t W = kv4_units(a, len0);
-    /* Little work: at least GPUOS_KV4_RUN pages a warp, so fewer blocks, and
-     * as many for each item, so that with equal lengths none spans more. */
+    /* Little work: no more warps than units, and as many blocks for each
+     * item, so that with equal lengths none spans more. */
     uint32_t nblk = gridDim.x;
-    if (W < (uint64_t)C::WARPS * GPUOS_KV4_RUN * nblk) {
-        const uint32_t items = a.B * a.Hkv * a.RT; /* <= W */
-        nblk = ((uint32_t)W + C::WARPS * GPUOS_KV4_RUN - 1) / (C::WARPS * GPUOS_KV4_RUN);
+    if (W < (uint64_t)C::WARPS * nblk) {
+        const uint32_t items = a.B * a.Hkv * a.RT; /* < W */
+        nblk = ((uint32_t)W + C::WARPS - 1) / C::WARPS;
         if (nblk > items) nblk = min((nblk + items - 1) / items * items, gridDim.x);
     }
     if (blockIdx.x >= nblk) return;
@@ -1247,11 +1262,11 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     uint32_t slot = 0, parity = 0; /* the ring's position */
     if (u < u1) kv4_seek(a, u, len0, p);
     while (u < u1) {
-        const uint32_t end = (uint32_t)(u1 - u < p.np - p.page ? p.page + (u1 - u) : p.np);
-        const uint32_t begin = p.page;
+        uint32_t begin, end;
+        u += kv4_take(p, u1 - u, begin, end);
         bool bad;
         (void)kv4_pages(a, p.len, bad);
-        if (!bad) { /* else the request's rows are left as they were */
+        if (!bad && begin < end) { /* (bad: the request's rows are left as they were) */
             Kv4State<G, NT> s;
             const uint32_t h = kv4_head(a, p.item), n = p.len ? end - begin : 0u;
             const int32_t *row = a.table + (uint64_t)p.b * a.P + begin;
@@ -1311,7 +1326,6 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 }
             }
         }
-        u += end - begin;
         kv4_next(a, p);
     }
     __syncthreads();
@@ -1477,8 +1491,9 @@ static int kv4_attend_launch(const gpuos_devdesc &d, void *stream)
     }
     /* no more blocks than the longest requests can fill */
     const uint64_t g = (d.dims[1] & 0xFFFFu) / (d.dims[1] >> 16), T = d.dims[2] >> 16;
-    const uint64_t units = (uint64_t)d.dims[0] * d.dims[3] * (d.dims[1] >> 16) * ((T * g + 8 * NT - 1) / (8 * NT));
-    uint64_t grid = (units + C::WARPS * GPUOS_KV4_RUN - 1) / (C::WARPS * GPUOS_KV4_RUN);
+    const uint64_t units =
+        (uint64_t)d.dims[0] * (d.dims[3] + GPUOS_KV4_LEAD) * (d.dims[1] >> 16) * ((T * g + 8 * NT - 1) / (8 * NT));
+    uint64_t grid = (units + C::WARPS - 1) / C::WARPS;
     if (grid > (uint64_t)sms) grid = (uint64_t)sms;
     if (grid > GPUOS_KV4_MAX_BLOCKS) grid = GPUOS_KV4_MAX_BLOCKS;
     gpuos_kv4_attend_kernel<G, NT><<<(uint32_t)grid, C::WARPS * 32, C::SMEM, (cudaStream_t)stream>>>(d);

@@ -179,9 +179,11 @@ def host_now_ns() -> int:
 
 def eager_run(descs: np.ndarray, stream_ptr: int = 0, stage_bytes: int = 16384) -> None:
     """Launch each descriptor as its own kernel on ``stream_ptr`` (cudaStream_t)."""
-    descs = np.ascontiguousarray(descs, dtype=DESC_DTYPE)
-    check(lib().gpuos_eager_run(descs.ctypes.data, len(descs), stage_bytes, C.c_void_p(stream_ptr)),
-          "gpuos_eager_run")
+    if descs.dtype is not DESC_DTYPE or not descs.flags.c_contiguous:
+        descs = np.ascontiguousarray(descs, dtype=DESC_DTYPE)
+    rc = lib().gpuos_eager_run(descs.ctypes.data, len(descs), stage_bytes, stream_ptr)
+    if rc != OK:
+        check(rc, "gpuos_eager_run")
 
 
 def sdpa_noalloc(q: int, Kc: int, Vc: int, lens: int, out: int, B: int, H: int, D: int, Lcap: int, Lmax: int,

@@ -51,62 +51,64 @@ def new_workspace(device="cuda") -> torch.Tensor:
     return torch.zeros(WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
-def _check(what: str, ok: bool) -> None:
-    if not ok:
-        raise ValueError(what)
+def _refuse(pool: torch.Tensor, *named) -> None:
+    """Raise what is wrong with a call's arguments, each (name, tensor,
+    dtypes, shape; None in the shape: any size)."""
+    for name, t, dtypes, shape in named:
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {t.dtype}, wanted {' or '.join(str(d) for d in dtypes)}")
+        if t.ndim != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple('any' if w is None else w for w in shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: not contiguous")
+        if t.get_device() < 0 or t.device != pool.device:
+            raise ValueError(f"{name}: on {t.device}, wanted the pool's CUDA device")
+        if t.data_ptr() % 16 and name not in ("slots", "table", "lens"):
+            raise ValueError(f"{name}: not 16-byte aligned")
+    raise ValueError(f"pool {tuple(pool.shape)}: 1 to 2^26 pages of 1 to 65535 heads of 34 * 64 or 34 * 128 bytes, wanted")
 
 
-def _tensor(name: str, t: torch.Tensor, dtypes, ndim: int, like: torch.Tensor) -> int:
-    """Device pointer of a contiguous tensor on `like`'s device."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, wanted {' or '.join(str(d) for d in dtypes)}")
-    if t.ndim != ndim:
-        raise ValueError(f"{name}: {t.ndim} dimensions, wanted {ndim}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    if t.device != like.device or t.device.type != "cuda":
-        raise ValueError(f"{name}: on {t.device}, wanted the pool's CUDA device")
-    return t.data_ptr()
-
-
-def _pool(pool: torch.Tensor):
-    p = _tensor("pool", pool, (torch.uint8,), 3, pool)
-    npages, heads, nbytes = pool.shape
-    _check(f"pool: {nbytes} bytes a head and page, wanted 34 * 64 or 34 * 128", nbytes in (34 * 64, 34 * 128))
-    _check("pool: 1 to 2^26 pages and 1 to 65535 heads", 1 <= npages <= 1 << 26 and 1 <= heads <= 65535)
-    _check("pool: not 16-byte aligned", p % 16 == 0)
-    return p, npages, heads, nbytes // 34
-
-
-def _desc(op: str, dtype: int, a=0, b=0, out=0, aux0=0, aux1=0, aux2=0, dims=(), fparam=0.0) -> np.ndarray:
-    dims = tuple(dims) + (0,) * (6 - len(dims))
-    raw = bytearray(_DESC.pack(G.OP[op], dtype, 0, 0, 0, 0, a, b, out, aux0, aux1, aux2, *dims, fparam, 0.0, 0, 0, 0))
+def _desc(op: int, dtype: int, a: int, b: int, out: int, aux0: int, aux1: int, aux2: int, d0: int, d1: int, d2: int,
+          d3: int, d4: int, fparam: float) -> np.ndarray:
+    raw = bytearray(_DESC.pack(op, dtype, 0, 0, 0, 0, a, b, out, aux0, aux1, aux2, d0, d1, d2, d3, d4, 0, fparam, 0.0,
+                               0, 0, 0))
     return np.frombuffer(raw, dtype=G.DESC_DTYPE)
 
 
-def _rows(op: str, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor) -> np.ndarray:
-    pp, npages, heads, D = _pool(pool)
-    kp = _tensor("k", k, _DTYPE, 3, pool)
-    vp = _tensor("v", v, (k.dtype,), 3, pool)
-    sp = _tensor("slots", slots, (torch.int32,), 1, pool)
-    n = slots.shape[0]
-    _check(f"k, v: {tuple(k.shape)} and {tuple(v.shape)}, wanted {(n, heads, D)}", k.shape == v.shape == (n, heads, D))
-    _check("k, v: not 16-byte aligned", kp % 16 == 0 and vp % 16 == 0)
-    if op == "kv4_write":
-        return _desc(op, _DTYPE[k.dtype], a=kp, b=vp, out=pp, aux0=sp, dims=(n, heads, D, npages))
-    return _desc(op, _DTYPE[k.dtype], a=pp, out=kp, aux0=sp, aux1=vp, dims=(n, heads, D, npages))
+_WRITE, _READ, _SDPA, _COPY = (G.OP[n] for n in ("kv4_write", "kv4_read", "kv4_sdpa", "page_copy"))
+_U8, _I32, _BF16 = torch.uint8, torch.int32, torch.bfloat16
+_HEAD_DIM = {34 * 64: 64, 34 * 128: 128}
+
+
+def _rows(op: int, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor) -> np.ndarray:
+    dt, dev, ks, ps = _DTYPE.get(k.dtype), pool.get_device(), k.shape, pool.shape
+    if len(ks) == 3 and len(ps) == 3 and slots.ndim == 1:
+        (n, heads, D), (npages, _, nbytes) = ks, ps
+        kp, vp, pp = k.data_ptr(), v.data_ptr(), pool.data_ptr()
+        if (dt is not None and v.dtype is k.dtype and v.shape == ks and slots.dtype is _I32 and pool.dtype is _U8
+                and slots.shape[0] == n and _HEAD_DIM.get(nbytes) == D and ps[1] == heads and 1 <= npages <= 1 << 26
+                and 1 <= heads <= 65535 and dev >= 0 and k.get_device() == dev and v.get_device() == dev
+                and slots.get_device() == dev and k.is_contiguous() and v.is_contiguous() and slots.is_contiguous()
+                and pool.is_contiguous() and not (kp | vp | pp) & 15):
+            if op == _WRITE:
+                return _desc(op, dt, kp, vp, pp, slots.data_ptr(), 0, 0, n, heads, D, npages, 0, 0.0)
+            return _desc(op, dt, pp, 0, kp, slots.data_ptr(), vp, 0, n, heads, D, npages, 0, 0.0)
+    n, heads = slots.numel(), ps[1] if len(ps) == 3 else None
+    D = _HEAD_DIM.get(ps[2]) if len(ps) == 3 else None
+    _refuse(pool, ("pool", pool, (_U8,), (None, None, None)), ("k", k, tuple(_DTYPE), (n, heads, D)),
+            ("v", v, (k.dtype,), (n, heads, D)), ("slots", slots, (_I32,), (n,)))
 
 
 def write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor) -> np.ndarray:
     """Quantise rows k, v [N, heads, D] (float32 or bfloat16) into the slots
     int32 [N] (page * 32 + key; negative: skipped; distinct) of the pool."""
-    return _rows("kv4_write", k, v, slots, pool)
+    return _rows(_WRITE, k, v, slots, pool)
 
 
 def read(pool: torch.Tensor, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> np.ndarray:
     """The rows held in the slots into k, v [N, heads, D] (float32 or
     bfloat16, both exact); zeros for a negative slot."""
-    return _rows("kv4_read", k, v, slots, pool)
+    return _rows(_READ, k, v, slots, pool)
 
 
 def sdpa(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, out: torch.Tensor,
@@ -116,24 +118,32 @@ def sdpa(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, lens: torch.T
     token t sees keys 0 .. lens[b] - T + t; zeros where that is none. Query
     head h reads cache head h // (H / heads). Descriptors that share a
     workspace must run one after another."""
-    pp, npages, heads, D = _pool(pool)
-    qp = _tensor("q", q, (torch.bfloat16,), 4, pool)
-    op = _tensor("out", out, (torch.bfloat16,), 4, pool)
-    tp = _tensor("table", table, (torch.int32,), 2, pool)
-    lp = _tensor("lens", lens, (torch.int32,), 1, pool)
-    wp = _tensor("workspace", workspace, (torch.uint8,), 1, pool)
-    B, T, H, d = q.shape
-    P = table.shape[1]
-    _check(f"q: {d} channels a head, the pool has {D}", d == D)
-    _check(f"q: {H} heads over the pool's {heads}", 1 <= H <= 65535 and H % heads == 0)
-    _check(f"q: {T} tokens, wanted 1 to {MAX_QUERY_TOKENS}", 1 <= T <= MAX_QUERY_TOKENS)
-    _check("out: not q's shape", out.shape == q.shape)
-    _check("table, lens: not one row and one length a request", table.shape[0] == B and lens.shape[0] == B)
-    _check("table: 1 to 2^26 pages a request", 1 <= P <= 1 << 26)
-    _check("q, out, workspace: not 16-byte aligned", (qp | op | wp) % 16 == 0)
-    _check(f"workspace: {workspace.numel()} bytes, wanted {WORKSPACE_BYTES}", workspace.numel() >= WORKSPACE_BYTES)
-    return _desc("kv4_sdpa", G.BF16, a=qp, b=pp, out=op, aux0=lp, aux1=tp, aux2=wp,
-                 dims=(B, H | heads << 16, D | T << 16, P, npages), fparam=scale)
+    dev, qs, ps, ts = pool.get_device(), q.shape, pool.shape, table.shape
+    if len(qs) == 4 and len(ps) == 3 and len(ts) == 2 and lens.ndim == 1:
+        (B, T, H, D), (npages, heads, nbytes), P = qs, ps, ts[1]
+        qp, pp, op, wp = q.data_ptr(), pool.data_ptr(), out.data_ptr(), workspace.data_ptr()
+        if (q.dtype is _BF16 and out.dtype is _BF16 and pool.dtype is _U8 and table.dtype is _I32 and lens.dtype is _I32
+                and workspace.dtype is _U8 and out.shape == qs and _HEAD_DIM.get(nbytes) == D and ts[0] == B
+                and lens.shape[0] == B and 1 <= npages <= 1 << 26 and 1 <= heads and 1 <= H <= 65535 and H % heads == 0
+                and 1 <= T <= MAX_QUERY_TOKENS and 1 <= P <= 1 << 26 and workspace.numel() >= WORKSPACE_BYTES
+                and dev >= 0 and q.get_device() == dev and out.get_device() == dev and table.get_device() == dev
+                and lens.get_device() == dev and workspace.get_device() == dev and q.is_contiguous()
+                and out.is_contiguous() and pool.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
+                and workspace.is_contiguous() and not (qp | pp | op | wp) & 15):
+            return _desc(_SDPA, G.BF16, qp, pp, op, lens.data_ptr(), table.data_ptr(), wp, B, H | heads << 16, D | T << 16,
+                         P, npages, scale)
+        if len(qs) == 4 and not 1 <= T <= MAX_QUERY_TOKENS:
+            raise ValueError(f"q: {T} tokens a request, wanted 1 to {MAX_QUERY_TOKENS}")
+        if heads and H % heads or not 1 <= H <= 65535:
+            raise ValueError(f"q: {H} heads over the pool's {heads}")
+        if not 1 <= P <= 1 << 26:
+            raise ValueError(f"table: {P} pages a request, wanted 1 to 2^26")
+        if workspace.numel() < WORKSPACE_BYTES:
+            raise ValueError(f"workspace: {workspace.numel()} bytes, wanted {WORKSPACE_BYTES}")
+    B, D = qs[0] if qs else None, _HEAD_DIM.get(ps[2]) if len(ps) == 3 else None
+    _refuse(pool, ("pool", pool, (_U8,), (None, None, None)), ("q", q, (_BF16,), (None, None, None, D)),
+            ("out", out, (_BF16,), tuple(qs)), ("table", table, (_I32,), (B, None)), ("lens", lens, (_I32,), (B,)),
+            ("workspace", workspace, (_U8,), (None,)))
 
 
 def page_copy(pool: torch.Tensor, pairs: torch.Tensor) -> np.ndarray:
@@ -141,13 +151,17 @@ def page_copy(pool: torch.Tensor, pairs: torch.Tensor) -> np.ndarray:
     and every layer l. pool: [layers, npages, ...] of any dtype, a multiple of
     16 bytes a page. Pairs with a negative page are skipped; a source may be
     in several pairs, a destination is in one and is no pair's source."""
-    _check(f"pool: {pool.ndim} dimensions, wanted layers, pages and the page's own", pool.ndim >= 3)
-    pp = _tensor("pool", pool, (pool.dtype,), pool.ndim, pool)
-    ap = _tensor("pairs", pairs, (torch.int32,), 2, pool)
-    layers, npages = pool.shape[:2]
-    nbytes = pool[0, 0].numel() * pool.element_size() if layers and npages else 0
-    _check("pool: no layers, no pages, or pages that are not a multiple of 16 bytes", nbytes > 0 and nbytes % 16 == 0)
-    _check("pool: more than 2^31 - 1 pages or 2^36 bytes a page", npages < 1 << 31 and nbytes < 1 << 36)
-    _check("pairs: wanted [n, 2]", pairs.shape[1] == 2)
-    _check("pool, pairs: not 16- and 8-byte aligned", pp % 16 == 0 and ap % 8 == 0)
-    return _desc("page_copy", G.BF16, a=pp, aux0=ap, dims=(pairs.shape[0], nbytes // 16, npages, layers))
+    ps, dev = pool.shape, pool.get_device()
+    nbytes = pool.element_size()
+    for n in ps[2:]:
+        nbytes *= n
+    pp, ap = pool.data_ptr(), pairs.data_ptr()
+    if (len(ps) >= 3 and ps[0] >= 1 and 1 <= ps[1] < 1 << 31 and 0 < nbytes < 1 << 36 and not nbytes & 15
+            and pairs.dtype is _I32 and pairs.ndim == 2 and pairs.shape[1] == 2 and dev >= 0 and pairs.get_device() == dev
+            and pool.is_contiguous() and pairs.is_contiguous() and not pp & 15 and not ap & 7):
+        return _desc(_COPY, G.BF16, pp, 0, 0, ap, 0, 0, pairs.shape[0], nbytes >> 4, ps[1], ps[0], 0, 0.0)
+    if len(ps) < 3 or not pool.numel() or nbytes & 15 or nbytes >= 1 << 36 or ps[1] >= 1 << 31:
+        raise ValueError(f"pool {tuple(ps)}: wanted [layers, pages, ...], a multiple of 16 bytes a page")
+    if pairs.dtype is _I32 and ap & 7:
+        raise ValueError("pairs: not 8-byte aligned")
+    _refuse(pool, ("pool", pool, (pool.dtype,), tuple(ps)), ("pairs", pairs, (_I32,), (None, 2)))
