@@ -480,7 +480,8 @@ GPUOS_API int gpuos_tile_profile_get(gpuos_ctx *ctx, gpuos_tile_profile *out);
  *                      shortens the chunks when the requests' lengths lens[b]
  *                      leave tiles idle: see the sdpa op body)
  *   vecmat             ceil(N / 8) (eight output columns per tile)
- *   kv4_write, _read   runs of r rows (token, head), r = ceil(N Hkv / 1536) within [4, 64]
+ *   kv4_write, _read   Hkv * ceil(N / t), t = 8 * ceil(Hkv * ceil(N / 8) / 8192) within [8, 64]
+ *                      (t tokens of one head per tile)
  *   kv4_sdpa           min(1536, B * P * Hkv * row tiles) equal runs of pages
  *                      (a row tile: 8 of the T * H / Hkv query rows of a cache head)
  *   page_copy          layers * n * ceil(page bytes / 16384)

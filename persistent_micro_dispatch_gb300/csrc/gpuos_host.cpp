@@ -487,10 +487,10 @@ static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool use
             if (!d->a || !second || !d->out || !d->aux0 || (d->aux0 & 3u)) return GPUOS_EINVAL;
             if (!al16(d->a) || !al16(second) || !al16(d->out)) return GPUOS_EINVAL;
         }
-        const uint64_t rows = (uint64_t)m[0] * m[1];
-        uint64_t per = ceil_div(rows, GPUOS_KV4_TILES);
-        per = per < 4 ? 4 : (per > 64 ? 64 : per);
-        nt = ceil_div(rows, per);
+        /* eight tokens of a head a tile, more once that fills the GPU */
+        uint64_t octets = ceil_div(ceil_div(m[0], 8) * m[1], GPUOS_KV4_ROW_TILES);
+        octets = octets < 1 ? 1 : (octets > 8 ? 8 : octets);
+        nt = ceil_div(m[0], 8 * octets) * m[1];
         break;
     }
     case GPUOS_OP_KV4_SDPA: {

@@ -27,7 +27,8 @@
 #define GPUOS_HEAD_GROUP 4                /* heads per RoPE / KV-write tile */
 #define GPUOS_VM_COLS 8                   /* output columns per vecmat tile (16 bytes of a row) */
 #define GPUOS_KV4_ROWS 8                  /* query rows of a KV4 attention tile (one n8 block of the matrix instruction) */
-#define GPUOS_KV4_TILES 1536              /* KV4 attention tiles (and KV4 row tiles aimed at) */
+#define GPUOS_KV4_TILES 1536              /* KV4 attention tiles */
+#define GPUOS_KV4_ROW_TILES 8192          /* KV4 write and read tiles aimed at */
 #define GPUOS_KV4_MAX_TILES 2048          /* counters at the start of the KV4 workspace */
 #define GPUOS_KV4_MAX_BLOCKS 1024         /* blocks of an eager attention launch at most (workspace) */
 #ifndef GPUOS_KV4_LEAD

@@ -946,164 +946,273 @@ DEV int kv4_sdpa_op(const gpuos_devdesc *d, uint32_t tile)
 
 /* ---------------------------------------------------------------------------
  * Write and read back. Row (n, h) is token n's head h: keys and values of a
- * row go to (come from) slot slots[n] = page * 32 + key. A lane takes eight
- * neighbouring channels: one word of the keys' codes, two half words of the
- * values'. A negative slot is a hole: not written, read as zeros.
+ * row go to (come from) slot slots[n] = page * 32 + key. A negative slot is a
+ * hole: not written, read as zeros.
+ *
+ * A warp takes eight neighbouring tokens of one head at a time, because
+ * neighbours in a prompt are neighbours in a page, and lanes in the order of
+ * the page: for keys lane (token, j) holds channels 32 g + 8 j .. + 7 of every
+ * group g, 4 G contiguous bytes of codes; for values, four tokens at a time,
+ * lane (token, i) holds channels 32 g + 4 i .. + 3, 2 G contiguous bytes. Then
+ * two keys' (four values') pieces fill a 32-byte sector and a row's channels
+ * are moved 64 bytes at a time. Both ops are bound by the rows' bytes: 512
+ * of a bf16 row of 128 channels, keys and values, against 136 of codes.
  *
  * Scale: the least e >= -127 with max |x| <= 6 2^e (at most 125, so that
  * 6 2^e is finite: above it the largest code stands for what is larger).
  * x 2^-e is exact, so a code is the correctly rounded one.
  * ------------------------------------------------------------------------- */
-struct Kv4Row {
-    unsigned char *k, *v, *ks, *vs; /* the lane's key word, first value half word, scale bytes */
-};
+/* The codes of a lane of keys (j) or values (i) of a slot, after the page's. */
 template <int G>
-DEV Kv4Row kv4_row(unsigned char *pool, uint32_t H, uint32_t slot, uint32_t h, uint32_t c8)
+DEV uint32_t kv4_k_at(uint32_t key, uint32_t j)
 {
-    constexpr uint32_t D = 32u * G;
-    const uint32_t key = slot % GPUOS_KV4_PAGE, t = key >> 4, quad = key >> 2 & 3u, r = key & 3u;
-    const uint32_t g = c8 >> 2, x = c8 & 3u; /* channels 32 g + 8 x .. + 7 */
-    unsigned char *pg = pool + ((uint64_t)(slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
-    Kv4Row o;
-    o.k = pg + t * 8u * D + (((quad * 2u + (r & 1u)) * 4u + x) * 2u + (r >> 1)) * 4u * G + 4u * g;
-    o.v = pg + 16u * D + t * 8u * D + ((2u * x * 4u + quad) * 4u + r) * 2u * G + 2u * g; /* the next: + 32 G */
-    o.ks = pg + 32u * D + key * G + g;
-    o.vs = pg + 33u * D + ((t * 4u + quad) * G + g) * 4u + r;
-    return o;
+    return (key >> 4) * 256u * G + ((((key >> 2 & 3u) * 2u + (key & 1u)) * 4u + j) * 2u + (key >> 1 & 1u)) * 4u * G;
 }
-/* Rows of a tile: the host's tiles cut the N H rows into equal runs. */
-DEV void kv4_rows(const gpuos_devdesc *d, uint32_t tile, uint64_t &r0, uint64_t &r1)
+template <int G>
+DEV uint32_t kv4_v_at(uint32_t key, uint32_t i)
 {
-    const uint64_t rows = (uint64_t)d->dims[0] * d->dims[1], per = (rows + d->ntiles - 1) / d->ntiles;
-    r0 = per * tile;
-    r1 = r0 + per < rows ? r0 + per : rows;
+    return 512u * G + (key >> 4) * 256u * G + ((i * 4u + (key >> 2 & 3u)) * 4u + (key & 3u)) * 2u * G;
 }
-template <bool F32>
-DEV void kv4_load8(const void *base, uint64_t e, float (&x)[8])
+/* The value scale byte of group 0 of a slot; group g: + 4 g. */
+template <int G>
+DEV uint32_t kv4_vs_at(uint32_t key) { return 33u * 32u * G + (key >> 2) * 4u * G + (key & 3u); }
+
+/* A tile's tokens: the host's tiles are blocks of tokens (a multiple of
+ * eight) by head. False if the tile has none. */
+DEV bool kv4_tokens(const gpuos_devdesc *d, uint32_t tile, uint32_t &h, uint32_t &n0, uint32_t &n1)
+{
+    const uint32_t N = d->dims[0], H = d->dims[1], blocks = d->ntiles / H;
+    const uint32_t per = (uint32_t)(((uint64_t)N + blocks - 1) / blocks + 7u) & ~7u;
+    const uint32_t blk = tile / H;
+    h = tile - blk * H;
+    if ((uint64_t)blk * per >= N) return false;
+    n0 = blk * per;
+    n1 = N - n0 < per ? N : n0 + per;
+    return true;
+}
+/* C neighbouring values of a row (C a multiple of 4). */
+template <int C, bool F32>
+DEV void kv4_load_row(const void *base, uint64_t e, float (&x)[C])
 {
     if (F32) {
         const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + e);
-        const float4 u = __ldcg(p), v = __ldcg(p + 1);
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+#pragma unroll
+        for (int c = 0; c < C / 4; c++) {
+            const float4 v = __ldcg(p + c);
+            x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
+        }
+    } else if (C == 8) {
+        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + e));
+        x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
+        x[C - 4] = bf_lo(v.z); x[C - 3] = bf_hi(v.z); x[C - 2] = bf_lo(v.w); x[C - 1] = bf_hi(v.w);
     } else {
-        unpack8(__ldcg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + e)), x);
+        const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(base) + e));
+        x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
     }
 }
-/* The scale byte of a group of 32 (four lanes of eight values) and the codes. */
-DEV uint32_t kv4_quantise(float (&x)[8], uint32_t &byte)
+template <int C, bool F32>
+DEV void kv4_store_row(void *base, uint64_t e, const float (&x)[C])
+{
+    if (F32) {
+        float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(base) + e);
+#pragma unroll
+        for (int c = 0; c < C / 4; c++) p[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+    } else if (C == 8) {
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + e) =
+            make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[C - 4], x[C - 3]), pack_bf2(x[C - 2], x[C - 1]));
+    } else {
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(base) + e) =
+            make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
+    }
+}
+/* Codes of C values of a group that LANES neighbouring lanes share, and its
+ * scale byte. */
+template <int C, int LANES>
+DEV uint32_t kv4_quantise(const float (&v)[C], uint32_t &byte)
 {
     float top = 0.0f;
     bool odd = false;
 #pragma unroll
-    for (int c = 0; c < 8; c++) {
-        top = fmaxf(top, fabsf(x[c]));
-        odd |= !(fabsf(x[c]) < INFINITY);
+    for (int c = 0; c < C; c++) {
+        top = fmaxf(top, fabsf(v[c]));
+        odd |= !(fabsf(v[c]) < INFINITY);
     }
     top = odd ? INFINITY : top;
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const uint32_t bits = __float_as_uint(top);
     int e = (int)(bits >> 23) - 129 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
     e = max(-127, min(125, e));
     const float down = kv4_pow2(-e);
-#pragma unroll
-    for (int c = 0; c < 8; c++) x[c] *= down;
     const bool none = top == INFINITY;
+    float x[8];
+#pragma unroll
+    for (int c = 0; c < 8; c++) x[c] = c < C ? v[c] * down : 0.0f;
     byte = none ? 255u : (uint32_t)(e + 127);
     return none ? 0u : kv4_encode8(x);
 }
-template <int G, bool F32>
-DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
-{
-    constexpr uint32_t LPR = 4u * G, RPI = 16u / LPR; /* lanes of a row; rows a step (keys and values each) */
-    const uint32_t H = d->dims[1], lane = lane_id();
-    const uint32_t c8 = lane % LPR, val = lane / LPR & 1u, sub = lane / (2u * LPR);
-    const int32_t *slots = reinterpret_cast<const int32_t *>(d->aux0);
-    const uint32_t nslots = d->dims[3] * GPUOS_KV4_PAGE;
-    uint64_t r0, r1;
-    kv4_rows(d, tile, r0, r1);
-    int status = GPUOS_ST_OK;
-    for (uint64_t r = r0; r < r1; r += RPI) {
-        const uint64_t row = r + sub;
-        const bool have = row < r1;
-        const uint32_t n = have ? (uint32_t)(row / H) : 0u, h = have ? (uint32_t)(row - (uint64_t)n * H) : 0u;
-        const int32_t slot = have ? __ldcg(slots + n) : -1;
-        if (slot >= 0 && (uint32_t)slot >= nslots) status = GPUOS_ST_BAD_ARGS;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (have) kv4_load8<F32>(reinterpret_cast<const void *>(val ? d->b : d->a), row * (32u * G) + 8u * c8, x);
-        uint32_t byte;
-        const uint32_t w = kv4_quantise(x, byte);
-        if (slot >= 0 && (uint32_t)slot < nslots) {
-            const Kv4Row o = kv4_row<G>(reinterpret_cast<unsigned char *>(d->out), H, (uint32_t)slot, h, c8);
-            if (val) {
-                *reinterpret_cast<uint16_t *>(o.v) = (uint16_t)w;
-                *reinterpret_cast<uint16_t *>(o.v + 32u * G) = (uint16_t)(w >> 16);
-                if ((c8 & 3u) == 0) *o.vs = (unsigned char)byte;
-            } else {
-                *reinterpret_cast<uint32_t *>(o.k) = w;
-                if ((c8 & 3u) == 0) *o.ks = (unsigned char)byte;
-            }
-        }
-    }
-    return __any_sync(0xFFFFFFFFu, status != GPUOS_ST_OK) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
-}
-/* Values of eight codes under a scale byte. */
-DEV void kv4_dequantise(uint32_t w, uint32_t byte, float (&x)[8])
+/* Values of C codes (from the lowest nibble of w on) under a scale byte. */
+template <int C>
+DEV void kv4_dequantise(uint32_t w, uint32_t byte, float (&x)[C])
 {
     uint32_t h[4];
     kv4_decode4(w, h);
     float s = __uint_as_float(byte ? byte << 23 : 0x00400000u); /* 2^-127 is a subnormal number */
     if (byte == 255u) s = NAN;
 #pragma unroll
-    for (int c = 0; c < 4; c++) {
+    for (int c = 0; c < C / 2; c++) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[c]));
         x[2 * c] = f.x * s;
         x[2 * c + 1] = f.y * s;
     }
 }
+/* G words (G == 4: 16 bytes; G == 2: 8) */
+template <int G>
+DEV void kv4_ld_words(const unsigned char *p, uint32_t (&w)[G])
+{
+    if (G == 4) {
+        const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(p));
+        w[0] = x.x; w[1] = x.y; w[G - 2] = x.z; w[G - 1] = x.w;
+    } else {
+        const uint2 x = __ldcg(reinterpret_cast<const uint2 *>(p));
+        w[0] = x.x; w[1] = x.y;
+    }
+}
+template <int G, bool F32>
+DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
+{
+    constexpr uint32_t D = 32u * G;
+    const uint32_t H = d->dims[1], lane = lane_id(), j = lane & 3u, i = lane & 7u;
+    const int32_t *slots = reinterpret_cast<const int32_t *>(d->aux0);
+    const uint32_t nslots = d->dims[3] * GPUOS_KV4_PAGE;
+    const void *const ksrc = reinterpret_cast<const void *>(d->a), *const vsrc = reinterpret_cast<const void *>(d->b);
+    unsigned char *const pool = reinterpret_cast<unsigned char *>(d->out);
+    uint32_t h, n0, n1;
+    if (!kv4_tokens(d, tile, h, n0, n1)) return GPUOS_ST_OK;
+    bool bad = false;
+    for (uint32_t n = n0; n < n1; n += 8) {
+        const uint32_t left = n1 - n;
+        const int32_t mine = (lane & 7u) < left ? __ldcg(slots + n + (lane & 7u)) : -1; /* token lane % 8 */
+        bad |= mine >= 0 && (uint32_t)mine >= nslots;
+        float xk[G][8], xv[2][G][4];
+#pragma unroll
+        for (int g = 0; g < G; g++) { /* rows behind the last: the last again */
+            kv4_load_row<8, F32>(ksrc, ((uint64_t)(n + min(lane >> 2, left - 1u)) * H + h) * D + 32u * g + 8u * j, xk[g]);
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+                kv4_load_row<4, F32>(vsrc, ((uint64_t)(n + min(4u * t + (lane >> 3), left - 1u)) * H + h) * D + 32u * g + 4u * i,
+                                     xv[t][g]);
+        }
+        {
+            const int32_t slot = __shfl_sync(0xFFFFFFFFu, mine, lane >> 2);
+            uint32_t w[G], sc = 0;
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                uint32_t byte;
+                w[g] = kv4_quantise<8, 4>(xk[g], byte);
+                sc |= byte << (8 * g);
+            }
+            if ((uint32_t)slot < nslots) {
+                unsigned char *pg = pool + ((uint64_t)((uint32_t)slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
+                const uint32_t key = (uint32_t)slot % GPUOS_KV4_PAGE;
+                if (G == 4) *reinterpret_cast<uint4 *>(pg + kv4_k_at<G>(key, j)) = make_uint4(w[0], w[1], w[G - 2], w[G - 1]);
+                else *reinterpret_cast<uint2 *>(pg + kv4_k_at<G>(key, j)) = make_uint2(w[0], w[1]);
+                if (j == 0) {
+                    if (G == 4) *reinterpret_cast<uint32_t *>(pg + 32u * D + key * G) = sc;
+                    else *reinterpret_cast<uint16_t *>(pg + 32u * D + key * G) = (uint16_t)sc;
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            const int32_t slot = __shfl_sync(0xFFFFFFFFu, mine, 4u * t + (lane >> 3));
+            uint32_t w[G / 2], sc = 0;
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                uint32_t byte;
+                const uint32_t c = kv4_quantise<4, 8>(xv[t][g], byte) & 0xFFFFu;
+                if (g & 1) w[g / 2] |= c << 16;
+                else w[g / 2] = c;
+                if (i == (uint32_t)g) sc = byte;
+            }
+            if ((uint32_t)slot < nslots) {
+                unsigned char *pg = pool + ((uint64_t)((uint32_t)slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
+                const uint32_t key = (uint32_t)slot % GPUOS_KV4_PAGE;
+                if (G == 4) *reinterpret_cast<uint2 *>(pg + kv4_v_at<G>(key, i)) = make_uint2(w[0], w[G / 2 - 1]);
+                else *reinterpret_cast<uint32_t *>(pg + kv4_v_at<G>(key, i)) = w[0];
+                if (i < G) pg[kv4_vs_at<G>(key) + 4u * i] = (unsigned char)sc;
+            }
+        }
+    }
+    return __any_sync(0xFFFFFFFFu, bad) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
+}
 template <int G, bool F32>
 DEV int kv4_read_tile(const gpuos_devdesc *d, uint32_t tile)
 {
-    constexpr uint32_t LPR = 4u * G, RPI = 16u / LPR;
-    const uint32_t H = d->dims[1], lane = lane_id();
-    const uint32_t c8 = lane % LPR, val = lane / LPR & 1u, sub = lane / (2u * LPR);
+    constexpr uint32_t D = 32u * G;
+    const uint32_t H = d->dims[1], lane = lane_id(), j = lane & 3u, i = lane & 7u;
     const int32_t *slots = reinterpret_cast<const int32_t *>(d->aux0);
     const uint32_t nslots = d->dims[3] * GPUOS_KV4_PAGE;
-    uint64_t r0, r1;
-    kv4_rows(d, tile, r0, r1);
-    int status = GPUOS_ST_OK;
-    for (uint64_t r = r0; r < r1; r += RPI) {
-        const uint64_t row = r + sub;
-        if (row >= r1) break;
-        const uint32_t n = (uint32_t)(row / H), h = (uint32_t)(row - (uint64_t)n * H);
-        const int32_t slot = __ldcg(slots + n);
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (slot >= 0 && (uint32_t)slot < nslots) {
-            const Kv4Row o = kv4_row<G>(reinterpret_cast<unsigned char *>(d->a), H, (uint32_t)slot, h, c8);
-            uint32_t w, byte;
-            if (val) {
-                w = (uint32_t)__ldcg(reinterpret_cast<const uint16_t *>(o.v)) |
-                    (uint32_t)__ldcg(reinterpret_cast<const uint16_t *>(o.v + 32u * G)) << 16;
-                byte = __ldcg(o.vs);
-            } else {
-                w = __ldcg(reinterpret_cast<const uint32_t *>(o.k));
-                byte = __ldcg(o.ks);
-            }
-            kv4_dequantise(w, byte, x);
-        } else if (slot >= 0) {
-            status = GPUOS_ST_BAD_ARGS;
+    const unsigned char *const pool = reinterpret_cast<const unsigned char *>(d->a);
+    void *const kdst = reinterpret_cast<void *>(d->out), *const vdst = reinterpret_cast<void *>(d->aux1);
+    uint32_t h, n0, n1;
+    if (!kv4_tokens(d, tile, h, n0, n1)) return GPUOS_ST_OK;
+    bool bad = false;
+    int32_t mine = n0 + (lane & 7u) < n1 ? __ldcg(slots + n0 + (lane & 7u)) : -1; /* token lane % 8 */
+    for (uint32_t n = n0; n < n1; n += 8) {
+        bad |= mine >= 0 && (uint32_t)mine >= nslots;
+        /* every load of the eight tokens is out before the first is used */
+        const int32_t ks = __shfl_sync(0xFFFFFFFFu, mine, lane >> 2);
+        const bool kin = (uint32_t)ks < nslots;
+        uint32_t kw[G], ksc = 0, vw[2][G / 2], vsc[2][G];
+        {
+            const uint32_t slot = kin ? (uint32_t)ks : 0u, key = slot % GPUOS_KV4_PAGE;
+            const unsigned char *pg = pool + ((uint64_t)(slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
+            kv4_ld_words<G>(pg + kv4_k_at<G>(key, j), kw);
+            ksc = G == 4 ? __ldcg(reinterpret_cast<const uint32_t *>(pg + 32u * D + key * G))
+                         : (uint32_t)__ldcg(reinterpret_cast<const uint16_t *>(pg + 32u * D + key * G));
         }
-        const uint64_t e = row * (32u * G) + 8u * c8;
-        if (F32) {
-            float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(val ? d->aux1 : d->out) + e);
-            o[0] = make_float4(x[0], x[1], x[2], x[3]);
-            o[1] = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(val ? d->aux1 : d->out) + e) = pack8(x);
+        bool vin[2];
+        uint32_t vkey[2];
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            const int32_t vs = __shfl_sync(0xFFFFFFFFu, mine, 4u * t + (lane >> 3));
+            vin[t] = (uint32_t)vs < nslots;
+            const uint32_t slot = vin[t] ? (uint32_t)vs : 0u;
+            vkey[t] = slot % GPUOS_KV4_PAGE;
+            const unsigned char *pg = pool + ((uint64_t)(slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
+            if (G == 4) {
+                const uint2 x = __ldcg(reinterpret_cast<const uint2 *>(pg + kv4_v_at<G>(vkey[t], i)));
+                vw[t][0] = x.x;
+                vw[t][G / 2 - 1] = x.y;
+            } else {
+                vw[t][0] = __ldcg(reinterpret_cast<const uint32_t *>(pg + kv4_v_at<G>(vkey[t], i)));
+            }
+            kv4_ld_words<G>(pg + kv4_vs_at<G>(vkey[t] & ~3u), vsc[t]); /* four keys' bytes of each group */
+        }
+        mine = n + 8u + (lane & 7u) < n1 ? __ldcg(slots + n + 8u + (lane & 7u)) : -1;
+        const uint32_t left = n1 - n;
+        if (lane >> 2 < left) {
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                float x[8];
+                kv4_dequantise<8>(kin ? kw[g] : 0u, kin ? ksc >> (8 * g) & 255u : 127u, x);
+                kv4_store_row<8, F32>(kdst, ((uint64_t)(n + (lane >> 2)) * H + h) * D + 32u * g + 8u * j, x);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            if (4u * t + (lane >> 3) >= left) continue;
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                float x[4];
+                const uint32_t w = vw[t][g / 2] >> (16 * (g & 1));
+                kv4_dequantise<4>(vin[t] ? w : 0u, vin[t] ? vsc[t][g] >> (8u * (vkey[t] & 3u)) & 255u : 127u, x);
+                kv4_store_row<4, F32>(vdst, ((uint64_t)(n + 4u * t + (lane >> 3)) * H + h) * D + 32u * g + 4u * i, x);
+            }
         }
     }
-    return __any_sync(0xFFFFFFFFu, status != GPUOS_ST_OK) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
+    return __any_sync(0xFFFFFFFFu, bad) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
 }
 DEV int kv4_write_op(const gpuos_devdesc *d, uint32_t tile)
 {
@@ -1500,18 +1609,23 @@ static int kv4_attend_launch(const gpuos_devdesc &d, void *stream)
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-/* The other ops: one warp a tile, as in the executor. */
+/* The other ops: one warp a tile, as in the executor; four warps a block, so
+ * that a block's limit of 32 an SM leaves room for 64 warps. */
+#define GPUOS_KV4_EAGER_WARPS 4u
 template <int OP>
-__global__ void __launch_bounds__(32) gpuos_kv4_eager_kernel(const __grid_constant__ gpuos_devdesc d)
+__global__ void __launch_bounds__(GPUOS_KV4_EAGER_WARPS * 32) gpuos_kv4_eager_kernel(const __grid_constant__ gpuos_devdesc d)
 {
-    if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_op(&d, blockIdx.x);
-    if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_op(&d, blockIdx.x);
-    if (OP == GPUOS_OP_PAGE_COPY) (void)page_copy_op(&d, blockIdx.x);
+    const uint32_t tile = blockIdx.x * GPUOS_KV4_EAGER_WARPS + (threadIdx.x >> 5);
+    if (tile >= d.ntiles) return;
+    if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_op(&d, tile);
+    if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_op(&d, tile);
+    if (OP == GPUOS_OP_PAGE_COPY) (void)page_copy_op(&d, tile);
 }
 template <int OP>
 static int kv4_tiles_launch(const gpuos_devdesc &d, void *stream)
 {
-    gpuos_kv4_eager_kernel<OP><<<d.ntiles, 32, 0, (cudaStream_t)stream>>>(d);
+    const uint32_t blocks = (d.ntiles + GPUOS_KV4_EAGER_WARPS - 1) / GPUOS_KV4_EAGER_WARPS;
+    gpuos_kv4_eager_kernel<OP><<<blocks, GPUOS_KV4_EAGER_WARPS * 32, 0, (cudaStream_t)stream>>>(d);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 static int kv4_eager_launch(const gpuos_devdesc &d, void *stream)

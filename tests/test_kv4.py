@@ -32,11 +32,12 @@ def _sdpa(G, B=2, H=8, Hkv=2, D=128, T=1, P=4, npages=9, **kw):
 
 def test_tiles(G):
     n = lambda d: G.op_ntiles(d)  # noqa: E731
-    # rows: runs of ceil(rows / 1536) within [4, 64]
+    # rows: eight tokens of a head, up to 64 once that makes more than 8192 tiles
     assert n(_desc(G, "kv4_write", (1, 1, 128, 1))) == 1
-    assert n(_desc(G, "kv4_write", (64, 8, 128, 99))) == 128
-    assert n(_desc(G, "kv4_read", (8192, 8, 64, 999), dtype=0)) == -(-65536 // 43)
-    assert n(_desc(G, "kv4_read", (1 << 20, 8, 64, 1 << 20))) == (1 << 23) // 64
+    assert n(_desc(G, "kv4_write", (65, 8, 128, 99))) == 9 * 8
+    assert n(_desc(G, "kv4_read", (8192, 8, 64, 999), dtype=0)) == 8192
+    assert n(_desc(G, "kv4_read", (8193, 8, 64, 999), dtype=0)) == -(-8193 // 16) * 8
+    assert n(_desc(G, "kv4_read", (1 << 20, 8, 64, 1 << 20))) == (1 << 20) // 64 * 8
     assert n(_desc(G, "kv4_write", (0, 0, 0, 0), a=0, b=0, out=0, aux0=0)) == 1
     # attention: one tile a page of a (request, head, row tile) until 1536
     assert n(_sdpa(G)) == 2 * 2 * 4
