@@ -482,8 +482,10 @@ GPUOS_API int gpuos_tile_profile_get(gpuos_ctx *ctx, gpuos_tile_profile *out);
  *   vecmat             ceil(N / 8) (eight output columns per tile)
  *   kv4_write, _read   Hkv * ceil(N / t), t = 8 * ceil(Hkv * ceil(N / 8) / 8192) within [8, 64]
  *                      (t tokens of one head per tile)
- *   kv4_sdpa           min(1536, B * P * Hkv * row tiles) equal runs of pages
- *                      (a row tile: 8 of the T * H / Hkv query rows of a cache head)
+ *   kv4_sdpa           min(1536, B * (P + 6) * Hkv * row tiles) equal runs of pages
+ *                      (a row tile: 8 of the T * H / Hkv query rows of a cache head;
+ *                      starting a request's head and row tile counts for six pages;
+ *                      the product is below 2^32, EINVAL otherwise)
  *   page_copy          layers * n * ceil(page bytes / 16384)
  *   nop / empty op     1
  * Returns GPUOS_EINVAL for a descriptor the library would reject. */

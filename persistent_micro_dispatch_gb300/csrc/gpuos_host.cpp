@@ -501,14 +501,11 @@ static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool use
         if (m[3] == 0 || m[3] > GPUOS_KV4_MAX_PAGES) return GPUOS_EINVAL;
         if (!d->a || !d->b || !d->out || !d->aux0 || !d->aux1 || !d->aux2) return GPUOS_EINVAL;
         if (!al16(d->a) || !al16(d->b) || !al16(d->out) || !al16(d->aux2) || ((d->aux0 | d->aux1) & 3u)) return GPUOS_EINVAL;
-        /* the table has fewer than 2^29 entries, so sums of pages (and what
-         * an item counts besides) fit 32 bits; items are (request, head, row
-         * tile), which must too; units are pages by (head, row tile): below
-         * 2^50, so that the products that cut them into runs fit 64 bits */
+        /* work is counted in pages (and GPUOS_KV4_LEAD) of each request, head
+         * and row tile, in 32 bits: 2^32 of them would be 9 TB of cache */
         const uint64_t per_page = (uint64_t)Hkv * ceil_div((uint64_t)T * (H / Hkv), GPUOS_KV4_ROWS);
-        if ((uint64_t)m[0] * m[3] >= (1ull << 29) || (uint64_t)m[0] * m[3] > (1ull << 50) / per_page) return GPUOS_EINVAL;
-        if ((uint64_t)m[0] * per_page >= (1ull << 32)) return GPUOS_EINVAL;
-        const uint64_t units = (uint64_t)m[0] * m[3] * per_page;
+        if ((uint64_t)m[0] * per_page >= (1ull << 32) / (m[3] + GPUOS_KV4_LEAD)) return GPUOS_EINVAL;
+        const uint64_t units = (uint64_t)m[0] * (m[3] + GPUOS_KV4_LEAD) * per_page;
         nt = units < GPUOS_KV4_TILES ? units : GPUOS_KV4_TILES;
         break;
     }

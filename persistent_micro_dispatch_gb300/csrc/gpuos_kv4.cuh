@@ -176,21 +176,21 @@ struct Kv4Pos {
     uint32_t b, item; /* request; head * RT + row tile */
     uint32_t off, np; /* next unit of the item; its pages */
     int32_t len;
-    uint64_t first; /* the unit of the item's first page */
+    uint32_t first; /* the unit of the item's first page */
 };
 /* The next units of an item up to `left`: pages [begin, end), none in the lead. */
-DEV uint32_t kv4_take(const Kv4Pos &p, uint64_t left, uint32_t &begin, uint32_t &end)
+DEV uint32_t kv4_take(const Kv4Pos &p, uint32_t left, uint32_t &begin, uint32_t &end)
 {
-    const uint32_t span = p.np + GPUOS_KV4_LEAD - p.off, n = left < span ? (uint32_t)left : span;
+    const uint32_t span = p.np + GPUOS_KV4_LEAD - p.off, n = min(left, span);
     begin = p.off > GPUOS_KV4_LEAD ? p.off - GPUOS_KV4_LEAD : 0u;
     end = p.off + n > GPUOS_KV4_LEAD ? p.off + n - GPUOS_KV4_LEAD : 0u;
     return n;
 }
 /* All units of the call, and (every lane) the length of request `lane`. */
-DEV uint64_t kv4_units(const Kv4Args &a, int32_t &len0)
+DEV uint32_t kv4_units(const Kv4Args &a, int32_t &len0)
 {
     const uint32_t lane = lane_id();
-    uint32_t n = 0; /* B P < 2^29: the sums fit 32 bits */
+    uint32_t n = 0; /* (the host keeps the units that the table can hold below 2^32) */
     len0 = 0;
     for (uint32_t i = lane; i < a.B; i += 128) { /* four loads in flight */
         int32_t len[4];
@@ -200,28 +200,25 @@ DEV uint64_t kv4_units(const Kv4Args &a, int32_t &len0)
 #pragma unroll
         for (int k = 0; k < 4; k++) n += i + 32u * k < a.B ? kv4_pages(a, len[k]) + GPUOS_KV4_LEAD : 0u;
     }
-    return (uint64_t)__reduce_add_sync(0xFFFFFFFFu, n) * a.Hkv * a.RT;
+    return __reduce_add_sync(0xFFFFFFFFu, n) * a.Hkv * a.RT;
 }
-DEV uint64_t kv4_div(uint64_t n, uint32_t d) { return n >> 32 ? n / d : (uint64_t)((uint32_t)n / d); }
 /* W units in n runs that differ by one unit at most: the first W mod n have
  * one more than the others. */
 struct Kv4Runs {
-    uint64_t base, more; /* units of a run; runs with one more */
-    DEV Kv4Runs(uint64_t W, uint32_t n) : base(kv4_div(W, n)) { more = W - base * n; }
-    DEV uint64_t start(uint64_t run) const { return run * base + (run < more ? run : more); }
-    DEV uint32_t run_of(uint64_t u) const
+    uint32_t base, more; /* units of a run; runs with one more */
+    DEV Kv4Runs(uint32_t W, uint32_t n) : base(W / n) { more = W - base * n; }
+    DEV uint32_t start(uint32_t run) const { return run * base + min(run, more); }
+    DEV uint32_t run_of(uint32_t u) const
     {
-        const uint64_t cut = more * (base + 1);
-        if (u < cut) return (uint32_t)((u | base) >> 32 ? u / (base + 1) : (uint32_t)u / ((uint32_t)base + 1u));
-        const uint64_t v = u - cut;
-        return (uint32_t)(more + ((v | base) >> 32 ? v / base : (uint32_t)v / (uint32_t)base));
+        const uint32_t cut = more * (base + 1u);
+        return u < cut ? u / (base + 1u) : more + (u - cut) / base;
     }
 };
 /* The place of unit u (u < the number of units). */
-DEV void kv4_seek(const Kv4Args &a, uint64_t u, int32_t len0, Kv4Pos &p)
+DEV void kv4_seek(const Kv4Args &a, uint32_t u, int32_t len0, Kv4Pos &p)
 {
     const uint32_t lane = lane_id(), HR = a.Hkv * a.RT;
-    const uint32_t pg = (uint32_t)kv4_div(u, HR); /* pages of all requests before u's request: at most this */
+    const uint32_t pg = u / HR; /* pages of all requests before u's request: at most this */
     uint32_t base = 0;
     for (uint32_t i0 = 0; i0 < a.B; i0 += 32) {
         const uint32_t i = i0 + lane;
@@ -240,11 +237,11 @@ DEV void kv4_seek(const Kv4Args &a, uint64_t u, int32_t len0, Kv4Pos &p)
             p.len = __shfl_sync(0xFFFFFFFFu, len, src);
             p.np = kv4_pages(a, p.len);
             const uint32_t span = p.np + GPUOS_KV4_LEAD;
-            const uint64_t lo_b = (uint64_t)(base + __shfl_sync(0xFFFFFFFFu, incl, src) - span) * HR;
-            const uint64_t off = u - lo_b;
-            p.item = (uint32_t)kv4_div(off, span);
-            p.off = (uint32_t)(off - (uint64_t)p.item * span);
-            p.first = lo_b + (uint64_t)p.item * span + GPUOS_KV4_LEAD;
+            const uint32_t lo_b = (base + __shfl_sync(0xFFFFFFFFu, incl, src) - span) * HR;
+            const uint32_t off = u - lo_b;
+            p.item = off / span;
+            p.off = off - p.item * span;
+            p.first = lo_b + p.item * span + GPUOS_KV4_LEAD;
             return;
         }
         base += __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -880,12 +877,12 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
     Kv4Args a;
     kv4_args(d, 8u * NT, a);
     int32_t len0;
-    const uint64_t W = kv4_units(a, len0);
-    const uint32_t nt = d->ntiles < W ? d->ntiles : (uint32_t)W;
+    const uint32_t W = kv4_units(a, len0);
+    const uint32_t nt = min(d->ntiles, W);
     if (tile >= nt) return GPUOS_ST_OK;
     const Kv4Runs runs(W, nt);
-    uint64_t u = runs.start(tile);
-    const uint64_t u1 = runs.start(tile + 1ull);
+    uint32_t u = runs.start(tile);
+    const uint32_t u1 = runs.start(tile + 1u);
     Kv4Pos p;
     kv4_seek(a, u, len0, p);
     int status = GPUOS_ST_OK;
@@ -1282,12 +1279,12 @@ struct Kv4Block {
     static_assert(WARP_BYTES % 16 == 0 && FRAG % 16 == 0, "alignment");
 };
 /* What a warp leaves: the state of the item it began in the middle of, and of
- * the item that it does not finish (none: first unit ~0). */
+ * the item that it does not finish (none: ~0). */
 struct Kv4Item {
     uint32_t b, item, np;
 };
 struct Kv4Left {
-    unsigned long long head, tail; /* the items' first units */
+    uint32_t head, tail; /* the units of the items' first pages */
     Kv4Item hitem, titem;
 };
 
@@ -1336,7 +1333,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     __shared__ float weight[2][C::WARPS][8 * NT]; /* of the warps' heads and tails in their items */
     __shared__ float2 total[2][C::WARPS][8 * NT]; /* those items' (m, l) */
     __shared__ struct {
-        unsigned long long first;
+        uint32_t first;
         Kv4Item it;
         uint32_t blk0, last; /* the item's first block; its blocks, if all are here */
     } shared[2];
@@ -1346,27 +1343,27 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         for (uint32_t k = 0; k < NS; k++)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&bars[warp][k])) : "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        left[warp].head = left[warp].tail = ~0ull;
+        left[warp].head = left[warp].tail = ~0u;
     }
     __syncwarp();
     Kv4Args a;
     kv4_args(&d, 8u * NT, a);
     int32_t len0;
-    const uint64_t W = kv4_units(a, len0);
+    const uint32_t W = kv4_units(a, len0);
     /* Little work: no more warps than units, and as many blocks for each
      * item, so that with equal lengths none spans more. */
     uint32_t nblk = gridDim.x;
-    if (W < (uint64_t)C::WARPS * nblk) {
+    if (W < C::WARPS * nblk) {
         const uint32_t items = a.B * a.Hkv * a.RT; /* < W */
-        nblk = ((uint32_t)W + C::WARPS - 1) / C::WARPS;
+        nblk = (W + C::WARPS - 1) / C::WARPS;
         if (nblk > items) nblk = min((nblk + items - 1) / items * items, gridDim.x);
     }
     if (blockIdx.x >= nblk) return;
     const Kv4Runs runs(W, nblk); /* the blocks' runs, then the warps' */
-    const uint64_t b0 = runs.start(blockIdx.x), b1 = runs.start(blockIdx.x + 1ull);
+    const uint32_t b0 = runs.start(blockIdx.x), b1 = runs.start(blockIdx.x + 1u);
     const Kv4Runs mine_of(b1 - b0, C::WARPS);
-    uint64_t u = b0 + mine_of.start(warp);
-    const uint64_t u1 = b0 + mine_of.start(warp + 1u);
+    uint32_t u = b0 + mine_of.start(warp);
+    const uint32_t u1 = b0 + mine_of.start(warp + 1u);
     Kv4Pos p;
     uint32_t slot = 0, parity = 0; /* the ring's position */
     if (u < u1) kv4_seek(a, u, len0, p);
@@ -1445,34 +1442,40 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
      * by row, against the others of their items; then a thread for each four
      * channels adds the states' means. */
     constexpr uint32_t NE = NT * G * 64u; /* float4s of a state's accumulators */
-    const unsigned long long head = lane < C::WARPS ? left[lane].head : ~0ull, tail = lane < C::WARPS ? left[lane].tail : ~0ull;
+    const uint32_t head = lane < C::WARPS ? left[lane].head : ~0u, tail = lane < C::WARPS ? left[lane].tail : ~0u;
     for (uint32_t k = 0; k < 2; k++) {
-        const unsigned long long first = __shfl_sync(0xFFFFFFFFu, k ? tail : head, warp);
-        if (first == ~0ull) continue;
+        const uint32_t first = __shfl_sync(0xFFFFFFFFu, k ? tail : head, warp);
+        if (first == ~0u) continue;
         const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head == first), own = __ballot_sync(0xFFFFFFFFu, tail == first);
-        const uint32_t r = lane % (8u * NT);
-        /* the row's (m, l) in the state of warp w, a tail or a head */
+        /* lane (q, r): row r of the states of warps q, q + Q, ... */
+        constexpr uint32_t Q = 32u / (8u * NT);
+        static_assert(C::WARPS % Q == 0, "warps in the lanes' turns");
+        const uint32_t r = lane % (8u * NT), q = lane / (8u * NT);
         auto ml_of = [&](uint32_t w, bool t) {
             return reinterpret_cast<const float2 *>(t ? sm + w * C::WARP_BYTES : sm + C::WARPS * C::WARP_BYTES + w * C::FRAG)[r];
         };
-        float M = -FLT_MAX, l = 0.0f;
-        float2 x = make_float2(-FLT_MAX, 0.0f);
-        if (own) x = ml_of((uint32_t)__ffs((int)own) - 1u, true);
-        M = x.x;
-        for (uint32_t hs = heads; hs; hs &= hs - 1u) M = fmaxf(M, ml_of((uint32_t)__ffs((int)hs) - 1u, false).x);
-        l = x.y * kv4_ex2(x.x - M);
-        for (uint32_t hs = heads; hs; hs &= hs - 1u) {
-            const float2 y = ml_of((uint32_t)__ffs((int)hs) - 1u, false);
-            l = fmaf(y.y, kv4_ex2(y.x - M), l);
-        }
+        float2 x[C::WARPS / Q + 1];
+#pragma unroll
+        for (uint32_t w = 0; w < C::WARPS / Q; w++)
+            x[w] = heads >> (w * Q + q) & 1u ? ml_of(w * Q + q, false) : make_float2(-FLT_MAX, 0.0f);
+        x[C::WARPS / Q] = own && q == 0 ? ml_of((uint32_t)__ffs((int)own) - 1u, true) : make_float2(-FLT_MAX, 0.0f);
         const float2 me = ml_of(warp, k);
-        if (lane < 8u * NT) {
+        float M = -FLT_MAX, l = 0.0f;
+#pragma unroll
+        for (uint32_t w = 0; w <= C::WARPS / Q; w++) M = fmaxf(M, x[w].x);
+#pragma unroll
+        for (uint32_t o = 8u * NT; o < 32u; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+#pragma unroll
+        for (uint32_t w = 0; w <= C::WARPS / Q; w++) l = fmaf(x[w].y, kv4_ex2(x[w].x - M), l);
+#pragma unroll
+        for (uint32_t o = 8u * NT; o < 32u; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (q == 0) {
             weight[k][warp][r] = l != 0.0f ? me.y * kv4_ex2(me.x - M) / l : 0.0f;
             total[k][warp][r] = make_float2(M, l);
         }
     }
     __syncthreads();
-    const uint32_t orphan = __ballot_sync(0xFFFFFFFFu, head < b0), tails = __ballot_sync(0xFFFFFFFFu, tail != ~0ull);
+    const uint32_t orphan = __ballot_sync(0xFFFFFFFFu, head < b0), tails = __ballot_sync(0xFFFFFFFFu, tail != ~0u);
     float4 *const ws = reinterpret_cast<float4 *>(reinterpret_cast<float *>(d.aux2) + GPUOS_KV4_MAX_TILES);
     uint32_t out = 0; /* bit 0: a state of an item that began earlier is in the workspace; bit 1: of one that goes on */
     uint32_t todo = tails << 1 | (orphan ? 1u : 0u); /* bit 0: the orphan; bit 1 + w: warp w's tail */
@@ -1481,7 +1484,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         todo &= todo - 1u;
         const bool begins = c != 0;
         const uint32_t w0 = begins ? c - 1u : (uint32_t)__ffs((int)orphan) - 1u;
-        const unsigned long long first = __shfl_sync(0xFFFFFFFFu, begins ? tail : head, w0);
+        const uint32_t first = __shfl_sync(0xFFFFFFFFu, begins ? tail : head, w0);
         const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head == first);
         const Kv4Item it = begins ? left[w0].titem : left[w0].hitem;
         const bool whole = begins && first + it.np <= b1;
@@ -1493,8 +1496,9 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 const float4 x = reinterpret_cast<const float4 *>(sm + w0 * C::WARP_BYTES)[NT * 4 + idx];
                 v = make_float4(x.x * wt, x.y * wt, x.z * wt, x.w * wt);
             }
-            for (uint32_t hs = heads; hs; hs &= hs - 1u) {
-                const uint32_t w = (uint32_t)__ffs((int)hs) - 1u;
+#pragma unroll
+            for (uint32_t w = 0; w < C::WARPS; w++) {
+                if (!(heads >> w & 1u)) continue;
                 const float wt = weight[0][w][r];
                 const float4 x = reinterpret_cast<const float4 *>(sm + C::WARPS * C::WARP_BYTES + w * C::FRAG)[NT * 4 + idx];
                 v.x = fmaf(x.x, wt, v.x);
@@ -1526,7 +1530,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         /* the blocks of an item count at the counter of its first block */
         uint32_t last = 0;
         if (out >> warp & 1u) {
-            const uint64_t first = shared[warp].first;
+            const uint32_t first = shared[warp].first;
             const uint32_t blk0 = runs.run_of(first);
             const uint32_t F = runs.run_of(first + shared[warp].it.np - 1) - blk0 + 1;
             uint32_t *cnt = kv4_counters(&d) + blk0;

@@ -181,7 +181,9 @@ def eager_run(descs: np.ndarray, stream_ptr: int = 0, stage_bytes: int = 16384) 
     """Launch each descriptor as its own kernel on ``stream_ptr`` (cudaStream_t)."""
     if descs.dtype is not DESC_DTYPE or not descs.flags.c_contiguous:
         descs = np.ascontiguousarray(descs, dtype=DESC_DTYPE)
-    rc = lib().gpuos_eager_run(descs.ctypes.data, len(descs), stage_bytes, stream_ptr)
+    n = len(descs)
+    # (a few descriptors are copied: cheaper than numpy's way to their address)
+    rc = lib().gpuos_eager_run(descs.tobytes() if n <= 16 else descs.ctypes.data, n, stage_bytes, stream_ptr)
     if rc != OK:
         check(rc, "gpuos_eager_run")
 

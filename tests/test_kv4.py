@@ -39,9 +39,9 @@ def test_tiles(G):
     assert n(_desc(G, "kv4_read", (8193, 8, 64, 999), dtype=0)) == -(-8193 // 16) * 8
     assert n(_desc(G, "kv4_read", (1 << 20, 8, 64, 1 << 20))) == (1 << 20) // 64 * 8
     assert n(_desc(G, "kv4_write", (0, 0, 0, 0), a=0, b=0, out=0, aux0=0)) == 1
-    # attention: one tile a page of a (request, head, row tile) until 1536
-    assert n(_sdpa(G)) == 2 * 2 * 4
-    assert n(_sdpa(G, H=16, T=2)) == 2 * 2 * 4 * 2  # 16 rows a head: two row tiles
+    # attention: the table's pages and six by (request, head, row tile), until 1536
+    assert n(_sdpa(G)) == 2 * 2 * (4 + 6)
+    assert n(_sdpa(G, H=16, T=2)) == 2 * 2 * (4 + 6) * 2  # 16 rows a head: two row tiles
     assert n(_sdpa(G, B=64, Hkv=8, P=512)) == 1536
     assert n(_sdpa(G, B=0)) == 1
     # pages: 16 KB a tile
@@ -54,7 +54,7 @@ def test_tiles(G):
     dict(D=96), dict(D=0), dict(D=256), dict(T=0), dict(T=33), dict(H=7), dict(H=0), dict(Hkv=0), dict(P=0),
     dict(P=(1 << 26) + 1), dict(npages=0), dict(npages=(1 << 26) + 1), dict(dtype=0), dict(a=0), dict(b=0), dict(out=0),
     dict(aux0=0), dict(aux1=0), dict(aux2=0), dict(a=0x1008), dict(b=0x1004), dict(out=0x1002), dict(aux2=0x1008),
-    dict(aux0=0x1002), dict(aux1=0x1001), dict(B=0xFFFFFFFF, P=1 << 26)])
+    dict(aux0=0x1002), dict(aux1=0x1001), dict(B=0xFFFFFFFF, P=1 << 26), dict(B=1 << 16, Hkv=16, H=16, P=4096)])
 def test_sdpa_refusals(G, bad):
     with pytest.raises(G.GpuosError) as e:
         G.op_ntiles(_sdpa(G, **bad))
