@@ -83,7 +83,7 @@ def build(force: bool = False) -> str:
         # every function of the relocatable build must fit the executor's
         # per-thread register budget (launch bounds: 384 threads, 1 block/SM)
         jobs.append(([NVCC] + ARCH + COMMON + ["-cubin", "-rdc=true", "-maxrregcount", "168", "-Xptxas", "-v",
-                                               dev_src, "-o", EXEC_RDC + ".tmp"],
+                                               "-DGPUOS_EXECUTOR_ONLY", dev_src, "-o", EXEC_RDC + ".tmp"],
                      os.path.join(BUILD, "gpuos_exec_rdc.ptxas.txt")))
     with cf.ThreadPoolExecutor(max_workers=4) as ex:
         list(ex.map(lambda j: _run(*j), jobs))

@@ -2716,6 +2716,9 @@ extern "C" int gpuos_dev_preload(void)
     cudaFuncAttributes a;
     if (cudaFuncGetAttributes(&a, gpuos_executor_kernel) != cudaSuccess) return -1;
     if (cudaFuncGetAttributes(&a, gpuos_eager_kernel) != cudaSuccess) return -1;
+#ifndef GPUOS_EXECUTOR_ONLY
+    if (kv4_preload() != 0) return -1;
+#endif
     return 0;
 }
 
@@ -2725,7 +2728,9 @@ extern "C" int gpuos_dev_eager_launch(const gpuos_desc *d, uint32_t ntiles, uint
     static_assert(sizeof(dd) == sizeof(*d), "layout");
     memcpy(&dd, d, sizeof(dd));
     dd.ntiles = ntiles;
+#ifndef GPUOS_EXECUTOR_ONLY
     if (d->op_id >= GPUOS_OP_KV4_WRITE && d->op_id <= GPUOS_OP_PAGE_COPY) return kv4_eager_launch(dd, stream);
+#endif
     const uint32_t grid = (ntiles + EAGER_WPB - 1) / EAGER_WPB;
     const uint32_t dyn = gpuos_dev_dyn_smem(EAGER_WPB, stage_bytes);
     static uint32_t attr_set = 0;

@@ -1259,6 +1259,7 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
     return GPUOS_ST_OK;
 }
 
+#ifndef GPUOS_EXECUTOR_ONLY /* the relocatable build holds the executor and its ops alone */
 /* ---------------------------------------------------------------------------
  * Attention as a launch of its own (gpuos_eager_run). The runs are those of
  * the executor's tiles, one for each warp, but a block has every SM to itself:
@@ -1351,10 +1352,14 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     int32_t len0;
     const uint32_t W = kv4_units(a, len0);
     /* Little work: no more warps than units, and as many blocks for each
-     * item, so that with equal lengths none spans more. */
-    uint32_t nblk = gridDim.x;
+     * item, so that with equal lengths none spans more. Few items: the last
+     * block of one merges the states of all, so no more of them than the
+     * square root of its units (0.1 us each, against 0.1 us for each page of
+     * the twelve warps; a single head over 131,072 tokens: 152 blocks 29.6
+     * us, 70 blocks 23.5). */
+    const uint32_t items = a.B * a.Hkv * a.RT; /* < W */
+    uint32_t nblk = min(gridDim.x, items * ((uint32_t)sqrtf((float)(W / items)) + 1u));
     if (W < C::WARPS * nblk) {
-        const uint32_t items = a.B * a.Hkv * a.RT; /* < W */
         nblk = (W + C::WARPS - 1) / C::WARPS;
         if (nblk > items) nblk = min((nblk + items - 1) / items * items, gridDim.x);
     }
@@ -1551,8 +1556,12 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
             const uint32_t r = idx / (64u * G) * 8u + 2u * (idx & 3u) + (idx >> 5 & 1u);
             float M = -FLT_MAX, l = 0.0f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr uint32_t U = 10;
-            for (uint32_t f0 = 0; f0 < F; f0 += U) { /* a batch's loads are in flight together */
+            /* two states at a time: this code runs once, from an instruction
+             * cache that does not hold it, and is faster short (unrolled 2,
+             * 4, 6, 10, 20 times, 64 long requests: 79.2, 80.1, 79.7, 80.3,
+             * 84.4 us) */
+            constexpr uint32_t U = 2;
+            for (uint32_t f0 = 0; f0 < F; f0 += U) {
                 float2 ml[U];
                 float4 x[U];
 #pragma unroll
@@ -1645,4 +1654,19 @@ static int kv4_eager_launch(const gpuos_devdesc &d, void *stream)
     if ((d.dims[2] & 0xFFFFu) == 128) return rows <= 8 ? kv4_attend_launch<4, 1>(d, stream) : kv4_attend_launch<4, 2>(d, stream);
     return rows <= 8 ? kv4_attend_launch<2, 1>(d, stream) : kv4_attend_launch<2, 2>(d, stream);
 }
+/* Load the kernels (see gpuos_dev_preload). */
+static int kv4_preload()
+{
+    const void *const all[] = {
+        (const void *)gpuos_kv4_attend_kernel<4, 1>, (const void *)gpuos_kv4_attend_kernel<4, 2>,
+        (const void *)gpuos_kv4_attend_kernel<2, 1>, (const void *)gpuos_kv4_attend_kernel<2, 2>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_WRITE>, (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_READ>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_PAGE_COPY>};
+    for (const void *f : all) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, f) != cudaSuccess) return -1;
+    }
+    return 0;
+}
+#endif /* GPUOS_EXECUTOR_ONLY */
 #endif /* GPUOS_KV4_CUH */

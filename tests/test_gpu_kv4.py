@@ -153,6 +153,50 @@ def test_attention_value_scales_far_apart(runner):
 
 
 @pytest.mark.parametrize("runner", ["eager", "executor"])
+def test_attention_sink(runner):
+    """One key takes nearly all the weight and its value is nothing: the
+    output is what thousands of keys with weights near 2^-20 add up to."""
+    q, pool, table, lens = _attend_case(61, 1, 4, 1, 128, 1, [12001])
+    k0, v0, ks, vs = R.offsets(128, 0, np.arange(128))
+    pool[:, :, 32 * 128:33 * 128] = 121  # the other keys are small
+    pool[table[0, 0], 0, v0] = 0
+    pool[table[0, 0], 0, k0] = 0x22  # every channel 1.0
+    pool[table[0, 0], 0, ks] = 127
+    q[:] = R.bf16(0.5 + np.random.default_rng(1).standard_normal(q.shape) * 0.03)
+    scale = 14.0 / 64  # the sink's score 14, 20 octaves; the others' near 0
+    want, tol = R.attend(q, pool, table, lens, scale)
+    K, V, _ = R.unpack(pool)
+    s = (K[table[0, 0], 0, 0] * q[0, 0, 0]).sum() * scale
+    assert 13 < s < 15 and 1e-5 < np.abs(want).max() < 1e-2
+    _close(_attend(RUNNERS[runner], q, pool, table, lens, scale), want, tol)
+
+
+def test_attention_graphs_share_a_workspace():
+    """Two captured calls with one workspace, replayed one after another."""
+    import torch
+    from persistent_micro_dispatch_gb300 import gpuos as G, kv4
+    ws, st = kv4.new_workspace(), torch.cuda.Stream()
+    graphs, held = [], []
+    for seed, (B, H, heads, D, T, ls) in ((71, (2, 8, 2, 128, 1, [700, 2100])), (72, (1, 24, 1, 64, 1, [5000]))):
+        q, pool, table, lens = _attend_case(seed, B, H, heads, D, T, ls)
+        t = [_dev(q, torch.bfloat16), _dev(pool), _dev(table), _dev(lens)]
+        out = torch.zeros(B, T, H, D, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            G.eager_run(kv4.sdpa(*t, out, ws, 0.1), st.cuda_stream)
+        graphs.append(g)
+        held.append((t, out, R.attend(q, pool, table, lens, 0.1)))
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for _, out, (want, tol) in held:
+        _close(_f64(out), want, tol)
+    assert not ws[:8192].any().item()
+
+
+@pytest.mark.parametrize("runner", ["eager", "executor"])
 def test_attention_stale_rows_and_nan_groups(runner):
     """Scale bytes of 255: behind the last key they are ignored; a visible
     value group gives NaN there and only there; a visible key gives NaN rows."""
