@@ -131,8 +131,9 @@ struct Kv4Args {
     const int32_t *lens;
     const int32_t *table;
     uint16_t *out;
-    uint32_t B, H, Hkv, T, g, RT, P, npages;
+    uint32_t B, H, Hkv, T, g, RT, P, npages, rows; /* (rows: of a row tile) */
     float scale; /* times log2 e */
+    float inv_g; /* 1 / g */
 };
 DEV void kv4_args(const gpuos_devdesc *d, uint32_t rows_per_tile, Kv4Args &a)
 {
@@ -146,23 +147,26 @@ DEV void kv4_args(const gpuos_devdesc *d, uint32_t rows_per_tile, Kv4Args &a)
     a.Hkv = d->dims[1] >> 16;
     a.T = d->dims[2] >> 16;
     a.g = a.H / a.Hkv;
+    a.inv_g = 1.0f / (float)a.g;
+    a.rows = rows_per_tile;
     a.RT = (a.T * a.g + rows_per_tile - 1) / rows_per_tile;
     a.P = d->dims[3];
     a.npages = d->dims[4];
     a.scale = d->fparam[0] * 1.4426950408889634f;
 }
-/* Query row r of a cache head: token t, query head h g + hh. */
+/* Query row r of a cache head: token t = floor(r / g), query head h g + hh.
+ * In floats, without a division's code: r is below 2^21 + 16, so (r + 1/2) / g
+ * is off by less than the 1 / (2 g) that parts it from an integer. */
 DEV void kv4_token(const Kv4Args &a, uint32_t r, uint32_t &t, uint32_t &hh)
 {
-    t = a.T == 1 ? 0u : r / a.g;
+    t = (uint32_t)(((float)r + 0.5f) * a.inv_g);
     hh = r - t * a.g;
 }
-DEV uint32_t kv4_head(const Kv4Args &a, uint32_t item) { return a.RT == 1 ? item : item / a.RT; }
 /* Pages of a request; a length that its table row cannot hold counts as one
  * unit that does nothing (bad). */
 DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len, bool &bad)
 {
-    bad = len < 0 || (uint64_t)len > (uint64_t)a.P * GPUOS_KV4_PAGE;
+    bad = (uint32_t)len > a.P * GPUOS_KV4_PAGE; /* (at most 2^31; a negative length is above) */
     return bad || len == 0 ? 1u : ((uint32_t)len + GPUOS_KV4_PAGE - 1u) / GPUOS_KV4_PAGE;
 }
 DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len)
@@ -173,7 +177,7 @@ DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len)
 
 /* A warp's place in the work. */
 struct Kv4Pos {
-    uint32_t b, item; /* request; head * RT + row tile */
+    uint32_t b, h, r0; /* request, head, first row of the row tile */
     uint32_t off, np; /* next unit of the item; its pages */
     int32_t len;
     uint32_t first; /* the unit of the item's first page */
@@ -192,6 +196,7 @@ DEV uint32_t kv4_units(const Kv4Args &a, int32_t &len0)
     const uint32_t lane = lane_id();
     uint32_t n = 0; /* (the host keeps the units that the table can hold below 2^32) */
     len0 = 0;
+#pragma unroll 1
     for (uint32_t i = lane; i < a.B; i += 128) { /* four loads in flight */
         int32_t len[4];
 #pragma unroll
@@ -220,6 +225,7 @@ DEV void kv4_seek(const Kv4Args &a, uint32_t u, int32_t len0, Kv4Pos &p)
     const uint32_t lane = lane_id(), HR = a.Hkv * a.RT;
     const uint32_t pg = u / HR; /* pages of all requests before u's request: at most this */
     uint32_t base = 0;
+#pragma unroll 1
     for (uint32_t i0 = 0; i0 < a.B; i0 += 32) {
         const uint32_t i = i0 + lane;
         const int32_t len = i0 == 0 ? len0 : (i < a.B ? __ldcg(a.lens + i) : 0);
@@ -239,9 +245,11 @@ DEV void kv4_seek(const Kv4Args &a, uint32_t u, int32_t len0, Kv4Pos &p)
             const uint32_t span = p.np + GPUOS_KV4_LEAD;
             const uint32_t lo_b = (base + __shfl_sync(0xFFFFFFFFu, incl, src) - span) * HR;
             const uint32_t off = u - lo_b;
-            p.item = off / span;
-            p.off = off - p.item * span;
-            p.first = lo_b + p.item * span + GPUOS_KV4_LEAD;
+            const uint32_t item = off / span;
+            p.off = off - item * span;
+            p.first = lo_b + item * span + GPUOS_KV4_LEAD;
+            p.h = a.RT == 1 ? item : item / a.RT;
+            p.r0 = (item - p.h * a.RT) * a.rows;
             return;
         }
         base += __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -249,7 +257,7 @@ DEV void kv4_seek(const Kv4Args &a, uint32_t u, int32_t len0, Kv4Pos &p)
     p.b = a.B; /* not reached for u < kv4_units() */
     p.len = 0;
     p.np = 1;
-    p.item = p.off = 0;
+    p.h = p.r0 = p.off = 0;
     p.first = u;
 }
 /* The next item. */
@@ -257,8 +265,14 @@ DEV void kv4_next(const Kv4Args &a, Kv4Pos &p)
 {
     p.first += p.np;
     p.off = 0;
-    if (++p.item >= a.Hkv * a.RT) {
-        p.item = 0;
+    p.r0 += a.rows;
+    if (p.r0 < a.T * a.g) {
+        p.first += GPUOS_KV4_LEAD;
+        return;
+    }
+    p.r0 = 0;
+    if (++p.h >= a.Hkv) {
+        p.h = 0;
         if (++p.b >= a.B) return;
         p.len = __ldcg(a.lens + p.b);
         p.np = kv4_pages(a, p.len);
@@ -277,6 +291,7 @@ struct Kv4State {
     float acc[NT][G][2][4];
     uint32_t E[G]; /* largest value-scale exponent met in each group */
     uint32_t El, bias2; /* E of group lane % G; 22 - El in both halves */
+    uint32_t nan; /* bit 2 NT g + 2 nt + c: row (nt, c) saw a NaN among group g's values */
     uint32_t lim[NT][2]; /* keys that the row sees */
     uint32_t min_lim;    /* least of them over the tile's rows */
 };
@@ -284,9 +299,9 @@ struct Kv4State {
 DEV uint32_t kv4_row_limit(const Kv4Args &a, int32_t len, uint32_t r)
 {
     if (r >= a.T * a.g) return (uint32_t)len;
-    if (a.T == 1) return (uint32_t)len;
-    const int64_t n = (int64_t)len - (int64_t)a.T + 1 + (int64_t)(r / a.g);
-    return n > 0 ? (uint32_t)n : 0u;
+    uint32_t t, hh;
+    kv4_token(a, r, t, hh);
+    return (uint32_t)max(len - (int32_t)(a.T - 1u - t), 0);
 }
 
 /* The item's query rows, as they lie in memory. */
@@ -299,7 +314,7 @@ DEV void kv4_load_q(const Kv4Args &a, const Kv4Pos &p, Kv4Query<G, NT> &x)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
-    const uint32_t h = kv4_head(a, p.item), r0 = (p.item - h * a.RT) * 8u * NT;
+    const uint32_t h = p.h, r0 = p.r0;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
         const uint32_t r = r0 + 8u * nt + i;
@@ -317,29 +332,22 @@ template <int G, int NT>
 DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx, Kv4State<G, NT> &s)
 {
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
-    const uint32_t h = kv4_head(a, p.item), r0 = (p.item - h * a.RT) * 8u * NT;
+    const uint32_t h = p.h, r0 = p.r0;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
         const uint4(&raw)[G] = qx.raw[nt];
-        float top = 0.0f;
-        bool odd = false; /* a NaN or infinity in the row: left as it is */
+        /* the largest magnitude, as bf16 bits: those of positive numbers are
+         * in order, infinity and NaN (the row is left as it is) on top */
+        uint32_t w = 0;
 #pragma unroll
-        for (int g = 0; g < G; g++) {
-            float x[8];
-            unpack8(raw[g], x);
-#pragma unroll
-            for (int c = 0; c < 8; c++) {
-                top = fmaxf(top, fabsf(x[c]));
-                odd |= !(fabsf(x[c]) < INFINITY);
-            }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const uint32_t oddrow = __ballot_sync(0xFFFFFFFFu, odd) >> (4u * i) & 15u;
-        /* k: top 2^-k in [128, 256); both 2^k and 2^-k stay normal numbers */
-        int k = (int)(__float_as_uint(top) >> 23) - 127 - 7;
-        if (oddrow || top == 0.0f) k = 0;
-        k = max(-126, min(126, k));
+        for (int g = 0; g < G; g++)
+            w = __vmaxu2(w, __vmaxu2(__vmaxu2(raw[g].x & 0x7FFF7FFFu, raw[g].y & 0x7FFF7FFFu),
+                                     __vmaxu2(raw[g].z & 0x7FFF7FFFu, raw[g].w & 0x7FFF7FFFu)));
+        w = max(w & 0xFFFFu, w >> 16);
+        w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1));
+        w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 2));
+        /* k: the largest times 2^-k is in [128, 256); both 2^k and 2^-k stay normal numbers */
+        const int k = w == 0 || w >= 0x7F80u ? 0 : max(-126, (int)(w >> 7) - 127 - 7);
         /* the factor stays positive: a negative scale turns q, one of zero
          * (or a product with 2^k below every number) empties it */
         float down = kv4_pow2(-k), f = fabsf(a.scale) * kv4_pow2(k);
@@ -350,10 +358,9 @@ DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx,
         }
 #pragma unroll
         for (int g = 0; g < G; g++) {
-            float x[8];
-            unpack8(raw[g], x);
+            const uint32_t x[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
-            for (int c = 0; c < 4; c++) s.q[nt][g][c] = kv4_pack_h2(x[2 * c] * down, x[2 * c + 1] * down);
+            for (int c = 0; c < 4; c++) s.q[nt][g][c] = kv4_pack_h2(bf_lo(x[c]) * down, bf_hi(x[c]) * down);
         }
         s.f[nt][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * j);
         s.f[nt][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * j + 4);
@@ -372,7 +379,7 @@ DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx,
     }
 #pragma unroll
     for (int g = 0; g < G; g++) s.E[g] = 0;
-    s.El = 0;
+    s.El = s.nan = 0;
     s.bias2 = 22u | 22u << 16;
     s.min_lim = kv4_row_limit(a, p.len, r0); /* rows come in order of t */
 }
@@ -407,28 +414,24 @@ DEV uint32_t kv4_keep(uint32_t key0, uint32_t n)
  * first page, then with each new largest). E grows, the accumulators follow.
  * vw: the lane's word of value scales, group lane % G, keys key0 .. key0 + 3
  * of the page, already without what lies behind the last key. A scale of 255
- * makes NaN what the rows that see the key hold of the group, and is dropped
- * from vw. */
+ * is noted for the rows that see the key, and dropped from vw. */
 template <int G, int NT>
 DEV void kv4_grow(uint32_t base, uint32_t key0, uint32_t &vw, Kv4State<G, NT> &s)
 {
     const uint32_t lane = lane_id();
     const uint32_t nan = __vcmpeq4(vw, 0xFFFFFFFFu);
     if (__any_sync(0xFFFFFFFFu, nan != 0u)) {
-#pragma unroll
-        for (int g = 0; g < G; g++) {
+#pragma unroll 1
+        for (uint32_t g = 0; g < G; g++) {
             /* the page's first such key of the group */
             uint32_t lo = GPUOS_KV4_PAGE;
-            if (nan && lane % G == (uint32_t)g) lo = key0 + ((uint32_t)__ffs((int)nan) - 1u) / 8u;
+            if (nan && lane % G == g) lo = key0 + ((uint32_t)__ffs((int)nan) - 1u) / 8u;
             lo = __reduce_min_sync(0xFFFFFFFFu, lo);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                for (int c = 0; c < 4; c++)
-                    if (lo < GPUOS_KV4_PAGE && base + lo < s.lim[nt][c & 1]) {
-                        s.acc[nt][g][0][c] = NAN;
-                        s.acc[nt][g][1][c] = NAN;
-                    }
+                for (int c = 0; c < 2; c++)
+                    if (lo < GPUOS_KV4_PAGE && base + lo < s.lim[nt][c]) s.nan |= 1u << (2u * NT * g + 2 * nt + c);
         }
         vw &= ~nan;
     }
@@ -665,6 +668,7 @@ DEV void kv4_finish(Kv4State<G, NT> &s)
 {
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
+        float inv[2];
 #pragma unroll
         for (int r = 0; r < 2; r++) {
             float l = s.l[nt][r];
@@ -672,19 +676,29 @@ DEV void kv4_finish(Kv4State<G, NT> &s)
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
             s.l[nt][r] = l;
+            inv[r] = l != 0.0f ? 1.0f / l : 0.0f;
         }
 #pragma unroll
         for (int g = 0; g < G; g++) {
             /* 2^(E - 127 - 7) in two factors (E - 134 may be below -126) */
             const int e = (int)s.E[g] - 134, e1 = e / 2;
-            const float p1 = kv4_pow2(e1), p2 = kv4_pow2(e - e1);
+            const float p2 = kv4_pow2(e - e1);
 #pragma unroll
             for (int c = 0; c < 4; c++) {
-                const float l = s.l[nt][c & 1], inv = l != 0.0f ? 1.0f / l : 0.0f;
-                s.acc[nt][g][0][c] = s.acc[nt][g][0][c] * inv * p1 * p2;
-                s.acc[nt][g][1][c] = s.acc[nt][g][1][c] * inv * p1 * p2;
+                const float x = inv[c & 1] * kv4_pow2(e1);
+                s.acc[nt][g][0][c] = s.acc[nt][g][0][c] * x * p2;
+                s.acc[nt][g][1][c] = s.acc[nt][g][1][c] * x * p2;
             }
         }
+    }
+    if (__any_sync(0xFFFFFFFFu, s.nan != 0u)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int g = 0; g < G; g++)
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    if (s.nan >> (2 * NT * g + 2 * nt + (c & 1)) & 1u) s.acc[nt][g][0][c] = s.acc[nt][g][1][c] = NAN;
     }
 }
 /* Rows that see no key are zero; the sum of a row that sees some is zero only
@@ -696,7 +710,7 @@ DEV void kv4_store(const Kv4Args &a, const Kv4Pos &p, const Kv4State<G, NT> &s)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
-    const uint32_t h = kv4_head(a, p.item), r0 = (p.item - h * a.RT) * 8u * NT;
+    const uint32_t h = p.h, r0 = p.r0;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -784,7 +798,7 @@ template <int G, int NT>
 DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t begin, uint32_t end, Kv4State<G, NT> &s)
 {
     constexpr uint32_t PB = kv4_page_bytes(32u * G);
-    const uint32_t lane = lane_id(), h = kv4_head(a, p.item);
+    const uint32_t lane = lane_id(), h = p.h;
     const int32_t *row = a.table + (uint64_t)p.b * a.P;
     const uint64_t stride = (uint64_t)a.Hkv * PB;
     const unsigned char *pool = a.pool + (uint64_t)h * PB;
@@ -811,6 +825,7 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t begin, uint32_t end,
         issue(0, __shfl_sync(0xFFFFFFFFu, ids, 0));
         if (n > 1) issue(1, __shfl_sync(0xFFFFFFFFu, ids, 1));
     }
+#pragma unroll 1
     for (uint32_t k = 0; k < n; k++) {
         if ((k & 31u) == 0) {
             if (k) ids = ids_next;
@@ -886,6 +901,7 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
     Kv4Pos p;
     kv4_seek(a, u, len0, p);
     int status = GPUOS_ST_OK;
+#pragma unroll 1
     while (u < u1) {
         uint32_t begin, end;
         u += kv4_take(p, u1 - u, begin, end);
@@ -906,6 +922,7 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
                 const uint32_t F = runs.run_of(p.first + p.np - 1) - first + 1;
                 uint32_t c = tile - first;
                 bool done = true;
+#pragma unroll 1
                 for (uint32_t step = 1; step < F; step <<= 1) {
                     const uint32_t other = c ^ step;
                     if (other < F) {
@@ -1087,6 +1104,7 @@ DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
     uint32_t h, n0, n1;
     if (!kv4_tokens(d, tile, h, n0, n1)) return GPUOS_ST_OK;
     bool bad = false;
+#pragma unroll 1
     for (uint32_t n = n0; n < n1; n += 8) {
         const uint32_t left = n1 - n;
         const int32_t mine = (lane & 7u) < left ? __ldcg(slots + n + (lane & 7u)) : -1; /* token lane % 8 */
@@ -1156,6 +1174,7 @@ DEV int kv4_read_tile(const gpuos_devdesc *d, uint32_t tile)
     if (!kv4_tokens(d, tile, h, n0, n1)) return GPUOS_ST_OK;
     bool bad = false;
     int32_t mine = n0 + (lane & 7u) < n1 ? __ldcg(slots + n0 + (lane & 7u)) : -1; /* token lane % 8 */
+#pragma unroll 1
     for (uint32_t n = n0; n < n1; n += 8) {
         bad |= mine >= 0 && (uint32_t)mine >= nslots;
         /* every load of the eight tokens is out before the first is used */
@@ -1247,6 +1266,7 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
     uint4 *dst = pool + (uint64_t)sd.y * p16;
     const uint32_t m = p16 - c0 < C ? p16 - c0 : C;
     constexpr int U = 8;
+#pragma unroll 1
     for (uint32_t i0 = lane_id(); i0 < m; i0 += 32u * U) {
         uint4 v[U];
 #pragma unroll
@@ -1282,7 +1302,7 @@ struct Kv4Block {
 /* What a warp leaves: the state of the item it began in the middle of, and of
  * the item that it does not finish (none: ~0). */
 struct Kv4Item {
-    uint32_t b, item, np;
+    uint32_t b, h, r0, np;
 };
 struct Kv4Left {
     uint32_t head, tail; /* the units of the items' first pages */
@@ -1310,7 +1330,7 @@ DEV void kv4_out4(const Kv4Args &a, const Kv4Item &it, uint32_t idx, float l, fl
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = idx & 31u, r2 = idx >> 5 & 1u, g = idx >> 6 & (G - 1u), nt = idx / (64u * G);
-    const uint32_t h = kv4_head(a, it.item), r = (it.item - h * a.RT) * 8u * NT + 8u * nt + 2u * (lane & 3u) + r2;
+    const uint32_t r = it.r0 + 8u * nt + 2u * (lane & 3u) + r2;
     if (r >= a.T * a.g) return;
     uint32_t t, hh;
     kv4_token(a, r, t, hh);
@@ -1321,7 +1341,7 @@ DEV void kv4_out4(const Kv4Args &a, const Kv4Item &it, uint32_t idx, float l, fl
     uint2 w;
     w.x = pack_bf2(v.x, v.y);
     w.y = pack_bf2(v.z, v.w);
-    *reinterpret_cast<uint2 *>(a.out + (((uint64_t)it.b * a.T + t) * a.H + (uint64_t)h * a.g + hh) * D + 32u * g + 4u * (lane >> 2)) = w;
+    *reinterpret_cast<uint2 *>(a.out + (((uint64_t)it.b * a.T + t) * a.H + (uint64_t)it.h * a.g + hh) * D + 32u * g + 4u * (lane >> 2)) = w;
 }
 template <int G, int NT>
 __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_attend_kernel(const __grid_constant__ gpuos_devdesc d)
@@ -1372,6 +1392,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     Kv4Pos p;
     uint32_t slot = 0, parity = 0; /* the ring's position */
     if (u < u1) kv4_seek(a, u, len0, p);
+#pragma unroll 1
     while (u < u1) {
         uint32_t begin, end;
         u += kv4_take(p, u1 - u, begin, end);
@@ -1379,10 +1400,10 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         (void)kv4_pages(a, p.len, bad);
         if (!bad && begin < end) { /* (bad: the request's rows are left as they were) */
             Kv4State<G, NT> s;
-            const uint32_t h = kv4_head(a, p.item), n = p.len ? end - begin : 0u;
+            const uint32_t n = p.len ? end - begin : 0u;
             const int32_t *row = a.table + (uint64_t)p.b * a.P + begin;
             const uint64_t stride = (uint64_t)a.Hkv * PB;
-            const unsigned char *pool = a.pool + (uint64_t)h * PB;
+            const unsigned char *pool = a.pool + (uint64_t)p.h * PB;
             /* page ids, 32 at a time in the lanes; one that is not in the
              * pool stands for no keys (page 0 is read and masked) */
             int32_t ids = lane < n ? __ldcg(row + lane) : 0, ids_next = 0;
@@ -1400,6 +1421,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 if (k < n) issue(slot + k < NS ? slot + k : slot + k - NS, id);
             }
             kv4_begin(a, p, qx, s);
+#pragma unroll 1
             for (uint32_t k = 0; k < n; k++) {
                 if ((k & 31u) == 0) {
                     if (k) ids = ids_next;
@@ -1433,7 +1455,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 kv4_part_put<G, NT>(reinterpret_cast<float4 *>(tail ? mine : sm + C::WARPS * C::WARP_BYTES + warp * C::FRAG), s);
                 if (lane == 0) {
                     (tail ? left[warp].tail : left[warp].head) = p.first;
-                    (tail ? left[warp].titem : left[warp].hitem) = Kv4Item{p.b, p.item, p.np};
+                    (tail ? left[warp].titem : left[warp].hitem) = Kv4Item{p.b, p.h, p.r0, p.np};
                 }
             }
         }
@@ -1448,6 +1470,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
      * channels adds the states' means. */
     constexpr uint32_t NE = NT * G * 64u; /* float4s of a state's accumulators */
     const uint32_t head = lane < C::WARPS ? left[lane].head : ~0u, tail = lane < C::WARPS ? left[lane].tail : ~0u;
+#pragma unroll 1
     for (uint32_t k = 0; k < 2; k++) {
         const uint32_t first = __shfl_sync(0xFFFFFFFFu, k ? tail : head, warp);
         if (first == ~0u) continue;
@@ -1484,6 +1507,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     float4 *const ws = reinterpret_cast<float4 *>(reinterpret_cast<float *>(d.aux2) + GPUOS_KV4_MAX_TILES);
     uint32_t out = 0; /* bit 0: a state of an item that began earlier is in the workspace; bit 1: of one that goes on */
     uint32_t todo = tails << 1 | (orphan ? 1u : 0u); /* bit 0: the orphan; bit 1 + w: warp w's tail */
+#pragma unroll 1
     while (todo) {
         const uint32_t c = (uint32_t)__ffs((int)todo) - 1u;
         todo &= todo - 1u;
@@ -1501,7 +1525,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 const float4 x = reinterpret_cast<const float4 *>(sm + w0 * C::WARP_BYTES)[NT * 4 + idx];
                 v = make_float4(x.x * wt, x.y * wt, x.z * wt, x.w * wt);
             }
-#pragma unroll
+#pragma unroll 4
             for (uint32_t w = 0; w < C::WARPS; w++) {
                 if (!(heads >> w & 1u)) continue;
                 const float wt = weight[0][w][r];
@@ -1548,6 +1572,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         shared[warp].last = last;
     }
     __syncthreads();
+#pragma unroll 1
     for (int k = 0; k < 2; k++) {
         const uint32_t F = shared[k].last;
         if (F == 0) continue;
