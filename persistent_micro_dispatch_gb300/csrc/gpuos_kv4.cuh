@@ -1004,26 +1004,45 @@ DEV bool kv4_tokens(const gpuos_devdesc *d, uint32_t tile, uint32_t &h, uint32_t
     n1 = N - n0 < per ? N : n0 + per;
     return true;
 }
-/* C neighbouring values of a row (C a multiple of 4). */
+/* C neighbouring values of a row (4 or 8), as they lie in memory. */
 template <int C, bool F32>
-DEV void kv4_load_row(const void *base, uint64_t e, float (&x)[C])
-{
-    if (F32) {
-        const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + e);
+struct Kv4Raw {
+    static constexpr int N = F32 ? C : C / 2;
+    uint32_t w[N];
+    DEV void load(const void *base, uint64_t e)
+    {
+        const unsigned char *p = reinterpret_cast<const unsigned char *>(base) + e * (F32 ? 4u : 2u);
+        if (N == 2) {
+            const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(p));
+            w[0] = v.x; w[1] = v.y;
+        } else {
 #pragma unroll
-        for (int c = 0; c < C / 4; c++) {
-            const float4 v = __ldcg(p + c);
-            x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
+            for (int c = 0; c < N; c += 4) {
+                const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(p) + c / 4);
+                w[c] = v.x; w[c + 1] = v.y; w[(c + 2) % N] = v.z; w[(c + 3) % N] = v.w;
+            }
         }
-    } else if (C == 8) {
-        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + e));
-        x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
-        x[C - 4] = bf_lo(v.z); x[C - 3] = bf_hi(v.z); x[C - 2] = bf_lo(v.w); x[C - 1] = bf_hi(v.w);
-    } else {
-        const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(base) + e));
-        x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
     }
-}
+    DEV float value(int c) const
+    {
+        if (F32) return __uint_as_float(w[c % N]);
+        return c & 1 ? bf_hi(w[c / 2]) : bf_lo(w[c / 2]);
+    }
+    /* The largest magnitude, as the bits of an fp32 number: those of positive
+     * numbers are in order, infinity and NaN on top. */
+    DEV uint32_t top() const
+    {
+        uint32_t m = 0;
+        if (F32) {
+#pragma unroll
+            for (int c = 0; c < N; c++) m = max(m, w[c] & 0x7FFFFFFFu);
+            return m;
+        }
+#pragma unroll
+        for (int c = 0; c < N; c++) m = __vmaxu2(m, w[c] & 0x7FFF7FFFu);
+        return max(m << 16, m & 0xFFFF0000u);
+    }
+};
 template <int C, bool F32>
 DEV void kv4_store_row(void *base, uint64_t e, const float (&x)[C])
 {
@@ -1041,27 +1060,19 @@ DEV void kv4_store_row(void *base, uint64_t e, const float (&x)[C])
 }
 /* Codes of C values of a group that LANES neighbouring lanes share, and its
  * scale byte. */
-template <int C, int LANES>
-DEV uint32_t kv4_quantise(const float (&v)[C], uint32_t &byte)
+template <int C, int LANES, bool F32>
+DEV uint32_t kv4_quantise(const Kv4Raw<C, F32> &v, uint32_t &byte)
 {
-    float top = 0.0f;
-    bool odd = false;
+    uint32_t bits = v.top();
 #pragma unroll
-    for (int c = 0; c < C; c++) {
-        top = fmaxf(top, fabsf(v[c]));
-        odd |= !(fabsf(v[c]) < INFINITY);
-    }
-    top = odd ? INFINITY : top;
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const uint32_t bits = __float_as_uint(top);
+    for (int o = 1; o < LANES; o <<= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
     int e = (int)(bits >> 23) - 129 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
     e = max(-127, min(125, e));
     const float down = kv4_pow2(-e);
-    const bool none = top == INFINITY;
+    const bool none = bits >= 0x7F800000u;
     float x[8];
 #pragma unroll
-    for (int c = 0; c < 8; c++) x[c] = c < C ? v[c] * down : 0.0f;
+    for (int c = 0; c < 8; c++) x[c] = c < C ? v.value(c) * down : 0.0f;
     byte = none ? 255u : (uint32_t)(e + 127);
     return none ? 0u : kv4_encode8(x);
 }
@@ -1109,14 +1120,14 @@ DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
         const uint32_t left = n1 - n;
         const int32_t mine = (lane & 7u) < left ? __ldcg(slots + n + (lane & 7u)) : -1; /* token lane % 8 */
         bad |= mine >= 0 && (uint32_t)mine >= nslots;
-        float xk[G][8], xv[2][G][4];
+        Kv4Raw<8, F32> xk[G];
+        Kv4Raw<4, F32> xv[2][G];
 #pragma unroll
         for (int g = 0; g < G; g++) { /* rows behind the last: the last again */
-            kv4_load_row<8, F32>(ksrc, ((uint64_t)(n + min(lane >> 2, left - 1u)) * H + h) * D + 32u * g + 8u * j, xk[g]);
+            xk[g].load(ksrc, ((uint64_t)(n + min(lane >> 2, left - 1u)) * H + h) * D + 32u * g + 8u * j);
 #pragma unroll
             for (int t = 0; t < 2; t++)
-                kv4_load_row<4, F32>(vsrc, ((uint64_t)(n + min(4u * t + (lane >> 3), left - 1u)) * H + h) * D + 32u * g + 4u * i,
-                                     xv[t][g]);
+                xv[t][g].load(vsrc, ((uint64_t)(n + min(4u * t + (lane >> 3), left - 1u)) * H + h) * D + 32u * g + 4u * i);
         }
         {
             const int32_t slot = __shfl_sync(0xFFFFFFFFu, mine, lane >> 2);
@@ -1124,7 +1135,7 @@ DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
 #pragma unroll
             for (int g = 0; g < G; g++) {
                 uint32_t byte;
-                w[g] = kv4_quantise<8, 4>(xk[g], byte);
+                w[g] = kv4_quantise<8, 4, F32>(xk[g], byte);
                 sc |= byte << (8 * g);
             }
             if ((uint32_t)slot < nslots) {
@@ -1145,7 +1156,7 @@ DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
 #pragma unroll
             for (int g = 0; g < G; g++) {
                 uint32_t byte;
-                const uint32_t c = kv4_quantise<4, 8>(xv[t][g], byte) & 0xFFFFu;
+                const uint32_t c = kv4_quantise<4, 8, F32>(xv[t][g], byte) & 0xFFFFu;
                 if (g & 1) w[g / 2] |= c << 16;
                 else w[g / 2] = c;
                 if (i == (uint32_t)g) sc = byte;
@@ -1291,7 +1302,7 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
 template <int G, int NT>
 struct Kv4Block {
     static constexpr uint32_t WARPS = NT == 1 ? 12 : 8; /* 168 and 255 registers a thread */
-    static constexpr uint32_t NS = NT == 1 ? 3 : 4;
+    static constexpr uint32_t NS = 2; /* (three: 0.5 to 2 % slower; a page is 4,352 bytes, 104 KB in flight an SM) */
     static constexpr uint32_t PB = 34u * 32u * G;
     static constexpr uint32_t FRAG = Kv4Part<G, NT>::floats * 4u;
     static constexpr uint32_t WARP_BYTES = NS * PB + GPUOS_KV4_SCRATCH;
@@ -1648,30 +1659,39 @@ static int kv4_attend_launch(const gpuos_devdesc &d, void *stream)
 }
 
 /* The other ops: one warp a tile, as in the executor; four warps a block, so
- * that a block's limit of 32 an SM leaves room for 64 warps. */
+ * that a block's limit of 32 an SM leaves room for 64 warps; a kernel for each
+ * type and head dimension, so that each has its own registers. */
 #define GPUOS_KV4_EAGER_WARPS 4u
-template <int OP>
+template <int OP, int G, bool F32>
 __global__ void __launch_bounds__(GPUOS_KV4_EAGER_WARPS * 32) gpuos_kv4_eager_kernel(const __grid_constant__ gpuos_devdesc d)
 {
     const uint32_t tile = blockIdx.x * GPUOS_KV4_EAGER_WARPS + (threadIdx.x >> 5);
     if (tile >= d.ntiles) return;
-    if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_op(&d, tile);
-    if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_op(&d, tile);
+    if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_tile<G, F32>(&d, tile);
+    if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_tile<G, F32>(&d, tile);
     if (OP == GPUOS_OP_PAGE_COPY) (void)page_copy_op(&d, tile);
 }
-template <int OP>
+template <int OP, int G, bool F32>
 static int kv4_tiles_launch(const gpuos_devdesc &d, void *stream)
 {
     const uint32_t blocks = (d.ntiles + GPUOS_KV4_EAGER_WARPS - 1) / GPUOS_KV4_EAGER_WARPS;
-    gpuos_kv4_eager_kernel<OP><<<blocks, GPUOS_KV4_EAGER_WARPS * 32, 0, (cudaStream_t)stream>>>(d);
+    gpuos_kv4_eager_kernel<OP, G, F32><<<blocks, GPUOS_KV4_EAGER_WARPS * 32, 0, (cudaStream_t)stream>>>(d);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+template <int OP>
+static int kv4_rows_launch(const gpuos_devdesc &d, void *stream)
+{
+    if (d.dims[0] == 0) return 0;
+    if (d.dims[2] == 128)
+        return d.dtype == GPUOS_F32 ? kv4_tiles_launch<OP, 4, true>(d, stream) : kv4_tiles_launch<OP, 4, false>(d, stream);
+    return d.dtype == GPUOS_F32 ? kv4_tiles_launch<OP, 2, true>(d, stream) : kv4_tiles_launch<OP, 2, false>(d, stream);
 }
 static int kv4_eager_launch(const gpuos_devdesc &d, void *stream)
 {
     switch (d.op_id) {
-    case GPUOS_OP_KV4_WRITE: return kv4_tiles_launch<GPUOS_OP_KV4_WRITE>(d, stream);
-    case GPUOS_OP_KV4_READ: return kv4_tiles_launch<GPUOS_OP_KV4_READ>(d, stream);
-    case GPUOS_OP_PAGE_COPY: return kv4_tiles_launch<GPUOS_OP_PAGE_COPY>(d, stream);
+    case GPUOS_OP_KV4_WRITE: return kv4_rows_launch<GPUOS_OP_KV4_WRITE>(d, stream);
+    case GPUOS_OP_KV4_READ: return kv4_rows_launch<GPUOS_OP_KV4_READ>(d, stream);
+    case GPUOS_OP_PAGE_COPY: return kv4_tiles_launch<GPUOS_OP_PAGE_COPY, 4, false>(d, stream);
     default: break;
     }
     if (d.dims[0] == 0) return 0;
@@ -1685,8 +1705,15 @@ static int kv4_preload()
     const void *const all[] = {
         (const void *)gpuos_kv4_attend_kernel<4, 1>, (const void *)gpuos_kv4_attend_kernel<4, 2>,
         (const void *)gpuos_kv4_attend_kernel<2, 1>, (const void *)gpuos_kv4_attend_kernel<2, 2>,
-        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_WRITE>, (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_READ>,
-        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_PAGE_COPY>};
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_WRITE, 4, false>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_WRITE, 4, true>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_WRITE, 2, false>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_WRITE, 2, true>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_READ, 4, false>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_READ, 4, true>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_READ, 2, false>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_KV4_READ, 2, true>,
+        (const void *)gpuos_kv4_eager_kernel<GPUOS_OP_PAGE_COPY, 4, false>};
     for (const void *f : all) {
         cudaFuncAttributes at;
         if (cudaFuncGetAttributes(&at, f) != cudaSuccess) return -1;
