@@ -1058,23 +1058,38 @@ DEV void kv4_store_row(void *base, uint64_t e, const float (&x)[C])
             make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
     }
 }
-/* Codes of C values of a group that LANES neighbouring lanes share, and its
- * scale byte. */
-template <int C, int LANES, bool F32>
-DEV uint32_t kv4_quantise(const Kv4Raw<C, F32> &v, uint32_t &byte)
+/* The scales of a row's G groups, C values of each in every one of LANES
+ * neighbouring lanes: byte is that of the lane's group (lane % LANES) * G /
+ * LANES, down[g] what values of group g are multiplied by (0: a group with a
+ * NaN or infinity). The maxima are split among the lanes as they are reduced,
+ * so that a lane works out one scale, not G. */
+template <int C, int LANES, int G, bool F32>
+DEV void kv4_scales(const Kv4Raw<C, F32> (&v)[G], uint32_t &byte, float (&down)[G])
 {
-    uint32_t bits = v.top();
+    const uint32_t lane = lane_id();
+    uint32_t t[G];
 #pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
-    int e = (int)(bits >> 23) - 129 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    e = max(-127, min(125, e));
-    const float down = kv4_pow2(-e);
-    const bool none = bits >= 0x7F800000u;
-    float x[8];
+    for (int g = 0; g < G; g++) t[g] = v[g].top();
+    int o = LANES;
 #pragma unroll
-    for (int c = 0; c < 8; c++) x[c] = c < C ? v.value(c) * down : 0.0f;
-    byte = none ? 255u : (uint32_t)(e + 127);
-    return none ? 0u : kv4_encode8(x);
+    for (int n = G; n > 1; n >>= 1) { /* the upper half of the groups goes to the lanes with bit o */
+        o >>= 1;
+        const bool up = lane & (uint32_t)o;
+#pragma unroll
+        for (int g = 0; g < n / 2; g++) {
+            const uint32_t keep = up ? t[g + n / 2] : t[g], give = up ? t[g] : t[g + n / 2];
+            t[g] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+        }
+    }
+#pragma unroll
+    for (o >>= 1; o > 0; o >>= 1) t[0] = max(t[0], __shfl_xor_sync(0xFFFFFFFFu, t[0], o));
+    /* e = floor(log2 top) - 2, and one more above 1.5 * 2^floor(log2 top) */
+    const uint32_t x = (t[0] + 0x3FFFFFu) >> 23;
+    const bool none = t[0] >= 0x7F800000u;
+    byte = none ? 255u : min(max(x, 2u) - 2u, 252u);
+    const float mine = none ? 0.0f : __uint_as_float((254u - byte) << 23); /* 2^-e */
+#pragma unroll
+    for (int g = 0; g < G; g++) down[g] = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~(LANES - 1u)) + (uint32_t)g * (LANES / G));
 }
 /* Values of C codes (from the lowest nibble of w on) under a scale byte. */
 template <int C>
@@ -1131,42 +1146,44 @@ DEV int kv4_write_tile(const gpuos_devdesc *d, uint32_t tile)
         }
         {
             const int32_t slot = __shfl_sync(0xFFFFFFFFu, mine, lane >> 2);
-            uint32_t w[G], sc = 0;
+            uint32_t w[G], byte;
+            float down[G];
+            kv4_scales<8, 4, G, F32>(xk, byte, down);
 #pragma unroll
             for (int g = 0; g < G; g++) {
-                uint32_t byte;
-                w[g] = kv4_quantise<8, 4, F32>(xk[g], byte);
-                sc |= byte << (8 * g);
+                float x[8];
+#pragma unroll
+                for (int c = 0; c < 8; c++) x[c] = xk[g].value(c) * down[g];
+                w[g] = down[g] != 0.0f ? kv4_encode8(x) : 0u;
             }
             if ((uint32_t)slot < nslots) {
                 unsigned char *pg = pool + ((uint64_t)((uint32_t)slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
                 const uint32_t key = (uint32_t)slot % GPUOS_KV4_PAGE;
                 if (G == 4) *reinterpret_cast<uint4 *>(pg + kv4_k_at<G>(key, j)) = make_uint4(w[0], w[1], w[G - 2], w[G - 1]);
                 else *reinterpret_cast<uint2 *>(pg + kv4_k_at<G>(key, j)) = make_uint2(w[0], w[1]);
-                if (j == 0) {
-                    if (G == 4) *reinterpret_cast<uint32_t *>(pg + 32u * D + key * G) = sc;
-                    else *reinterpret_cast<uint16_t *>(pg + 32u * D + key * G) = (uint16_t)sc;
-                }
+                if (j % (4u / G) == 0) pg[32u * D + key * G + j / (4u / G)] = (unsigned char)byte;
             }
         }
 #pragma unroll
         for (int t = 0; t < 2; t++) {
             const int32_t slot = __shfl_sync(0xFFFFFFFFu, mine, 4u * t + (lane >> 3));
-            uint32_t w[G / 2], sc = 0;
+            uint32_t w[G / 2], byte;
+            float down[G];
+            kv4_scales<4, 8, G, F32>(xv[t], byte, down);
 #pragma unroll
-            for (int g = 0; g < G; g++) {
-                uint32_t byte;
-                const uint32_t c = kv4_quantise<4, 8, F32>(xv[t][g], byte) & 0xFFFFu;
-                if (g & 1) w[g / 2] |= c << 16;
-                else w[g / 2] = c;
-                if (i == (uint32_t)g) sc = byte;
+            for (int g = 0; g < G; g += 2) {
+                float x[8];
+#pragma unroll
+                for (int c = 0; c < 8; c++) x[c] = xv[t][g + c / 4].value(c % 4) * down[g + c / 4];
+                const uint32_t c2 = kv4_encode8(x);
+                w[g / 2] = (down[g] != 0.0f ? c2 & 0xFFFFu : 0u) | (down[g + 1] != 0.0f ? c2 & 0xFFFF0000u : 0u);
             }
             if ((uint32_t)slot < nslots) {
                 unsigned char *pg = pool + ((uint64_t)((uint32_t)slot / GPUOS_KV4_PAGE) * H + h) * kv4_page_bytes(D);
                 const uint32_t key = (uint32_t)slot % GPUOS_KV4_PAGE;
                 if (G == 4) *reinterpret_cast<uint2 *>(pg + kv4_v_at<G>(key, i)) = make_uint2(w[0], w[G / 2 - 1]);
                 else *reinterpret_cast<uint32_t *>(pg + kv4_v_at<G>(key, i)) = w[0];
-                if (i < G) pg[kv4_vs_at<G>(key) + 4u * i] = (unsigned char)sc;
+                if (i % (8u / G) == 0) pg[kv4_vs_at<G>(key) + 4u * (i / (8u / G))] = (unsigned char)byte;
             }
         }
     }
