@@ -754,40 +754,66 @@ DEV void kv4_part_store(float *part, const Kv4State<G, NT> &s)
                        make_float4(s.acc[nt][g][0][r], s.acc[nt][g][0][r + 2], s.acc[nt][g][1][r], s.acc[nt][g][1][r + 2]));
     }
 }
-/* s := the merge of s and the stored state; `left`: s comes first (the order
- * of the arithmetic is that of the keys, whoever does it). */
+/* A request's head and row tile. */
+struct Kv4Item {
+    uint32_t b, h, r0, np;
+};
+/* Four channels of the output: element idx of a state's accumulators. */
 template <int G, int NT>
-DEV void kv4_part_merge(const float *part, Kv4State<G, NT> &s, bool left)
+DEV void kv4_out4(const Kv4Args &a, const Kv4Item &it, uint32_t idx, float l, float4 v)
+{
+    constexpr uint32_t D = 32u * G;
+    const uint32_t lane = idx & 31u, r2 = idx >> 5 & 1u, g = idx >> 6 & (G - 1u), nt = idx / (64u * G);
+    const uint32_t r = it.r0 + 8u * nt + 2u * (lane & 3u) + r2;
+    if (r >= a.T * a.g) return;
+    uint32_t t, hh;
+    kv4_token(a, r, t, hh);
+    if (l == 0.0f) {
+        const float z = kv4_empty(kv4_row_limit(a, __ldcg(a.lens + it.b), r));
+        v = make_float4(z, z, z, z);
+    }
+    uint2 w;
+    w.x = pack_bf2(v.x, v.y);
+    w.y = pack_bf2(v.z, v.w);
+    *reinterpret_cast<uint2 *>(a.out + (((uint64_t)it.b * a.T + t) * a.H + (uint64_t)it.h * a.g + hh) * D + 32u * g + 4u * (lane >> 2)) = w;
+}
+/* Two stored states, the left one's keys first, into a third place or (dst
+ * null) the output. Nothing of a state stays in registers: this is the
+ * executor's path, whose worker keeps what a tile leaves it. */
+template <int G, int NT>
+DEV void kv4_part_merge(const Kv4Args &a, const Kv4Item &it, const float *left, const float *right, float *dst)
 {
     const uint32_t lane = lane_id(), j = lane & 3u;
-    const float4 *p4 = reinterpret_cast<const float4 *>(part);
+    const float4 *x4 = reinterpret_cast<const float4 *>(left), *y4 = reinterpret_cast<const float4 *>(right);
+    float4 *d4 = reinterpret_cast<float4 *>(dst);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-        const float4 ml = __ldcg(p4 + nt * 4 + j);
-        float4 x[G][2];
-#pragma unroll
-        for (int g = 0; g < G; g++)
-#pragma unroll
-            for (int r = 0; r < 2; r++) x[g][r] = __ldcg(p4 + NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane);
+        const float4 p = __ldcg(x4 + nt * 4 + j), q = __ldcg(y4 + nt * 4 + j);
+        __syncwarp(); /* dst may be one of them: every lane has read its rows' (m, l) */
+        float wx[2], wy[2], m[2], l[2];
 #pragma unroll
         for (int r = 0; r < 2; r++) {
-            const float mo = r ? ml.z : ml.x, lo = r ? ml.w : ml.y;
-            const float mn = fmaxf(s.m[nt][r], mo);
-            const float ws = s.l[nt][r] * kv4_ex2(s.m[nt][r] - mn), wo = lo * kv4_ex2(mo - mn);
-            const float l = left ? ws + wo : wo + ws, inv = l != 0.0f ? 1.0f / l : 0.0f;
-            const float a0 = ws * inv, b0 = wo * inv;
-            s.m[nt][r] = mn;
-            s.l[nt][r] = l;
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-                const float o4[4] = {x[g][r].x, x[g][r].y, x[g][r].z, x[g][r].w};
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    float &v = s.acc[nt][g][c >> 1][r + 2 * (c & 1)];
-                    v = left ? fmaf(o4[c], b0, v * a0) : fmaf(v, a0, o4[c] * b0);
-                }
-            }
+            const float mx = r ? p.z : p.x, lx = r ? p.w : p.y, my = r ? q.z : q.x, ly = r ? q.w : q.y;
+            m[r] = fmaxf(mx, my);
+            wx[r] = lx * kv4_ex2(mx - m[r]);
+            wy[r] = ly * kv4_ex2(my - m[r]);
+            l[r] = wx[r] + wy[r];
+            const float inv = l[r] != 0.0f ? 1.0f / l[r] : 0.0f;
+            wx[r] *= inv;
+            wy[r] *= inv;
         }
+        if (dst && lane < 4) __stcg(d4 + nt * 4 + j, make_float4(m[0], l[0], m[1], l[1]));
+#pragma unroll 2
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const uint32_t idx = ((uint32_t)(nt * G + g) * 2u + r) * 32u + lane;
+                const float4 x = __ldcg(x4 + NT * 4 + idx), y = __ldcg(y4 + NT * 4 + idx);
+                const float4 v = make_float4(fmaf(y.x, wy[r], x.x * wx[r]), fmaf(y.y, wy[r], x.y * wx[r]),
+                                             fmaf(y.z, wy[r], x.z * wx[r]), fmaf(y.w, wy[r], x.w * wx[r]));
+                if (dst) __stcg(d4 + NT * 4 + idx, v);
+                else kv4_out4<G, NT>(a, it, idx, l[r], v);
+            }
     }
 }
 
@@ -920,29 +946,26 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
             if (begin != 0 || end != p.np) {
                 const uint32_t first = runs.run_of(p.first);
                 const uint32_t F = runs.run_of(p.first + p.np - 1) - first + 1;
+                auto slot = [&](uint32_t at) { return kv4_slot<G, NT>(d, first + at, at == 0); };
                 uint32_t c = tile - first;
-                bool done = true;
+                kv4_part_store<G, NT>(slot(c), s);
 #pragma unroll 1
                 for (uint32_t step = 1; step < F; step <<= 1) {
                     const uint32_t other = c ^ step;
                     if (other < F) {
                         uint32_t *cnt = kv4_counters(d) + first + (c | step);
-                        kv4_part_store<G, NT>(kv4_slot<G, NT>(d, first + c, c == 0), s);
                         __syncwarp();
                         uint32_t old = 0;
                         if (lane_id() == 0) old = atom_add_acq_rel_gpu32(cnt, 1u);
                         old = __shfl_sync(0xFFFFFFFFu, old, 0);
-                        if (old == 0) {
-                            done = false;
-                            break;
-                        }
+                        if (old == 0) break; /* the other half's last tile goes on */
                         __syncwarp();
-                        kv4_part_merge<G, NT>(kv4_slot<G, NT>(d, first + other, other == 0), s, c < other);
                         if (lane_id() == 0) *cnt = 0; /* left zero for the next call */
+                        kv4_part_merge<G, NT>(a, Kv4Item{p.b, p.h, p.r0, p.np}, slot(c & ~step), slot(c | step),
+                                              step << 1 < F ? slot(c & ~step) : nullptr);
                     }
                     c &= ~step;
                 }
-                if (done) kv4_store(a, p, s);
             } else {
                 kv4_store(a, p, s);
             }
@@ -1329,9 +1352,6 @@ struct Kv4Block {
 };
 /* What a warp leaves: the state of the item it began in the middle of, and of
  * the item that it does not finish (none: ~0). */
-struct Kv4Item {
-    uint32_t b, h, r0, np;
-};
 struct Kv4Left {
     uint32_t head, tail; /* the units of the items' first pages */
     Kv4Item hitem, titem;
@@ -1351,25 +1371,6 @@ DEV void kv4_part_put(float4 *p4, const Kv4State<G, NT> &s)
                 p4[NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane] =
                     make_float4(s.acc[nt][g][0][r], s.acc[nt][g][0][r + 2], s.acc[nt][g][1][r], s.acc[nt][g][1][r + 2]);
     }
-}
-/* One quarter row of the output: element idx of a state's accumulators. */
-template <int G, int NT>
-DEV void kv4_out4(const Kv4Args &a, const Kv4Item &it, uint32_t idx, float l, float4 v)
-{
-    constexpr uint32_t D = 32u * G;
-    const uint32_t lane = idx & 31u, r2 = idx >> 5 & 1u, g = idx >> 6 & (G - 1u), nt = idx / (64u * G);
-    const uint32_t r = it.r0 + 8u * nt + 2u * (lane & 3u) + r2;
-    if (r >= a.T * a.g) return;
-    uint32_t t, hh;
-    kv4_token(a, r, t, hh);
-    if (l == 0.0f) {
-        const float z = kv4_empty(kv4_row_limit(a, __ldcg(a.lens + it.b), r));
-        v = make_float4(z, z, z, z);
-    }
-    uint2 w;
-    w.x = pack_bf2(v.x, v.y);
-    w.y = pack_bf2(v.z, v.w);
-    *reinterpret_cast<uint2 *>(a.out + (((uint64_t)it.b * a.T + t) * a.H + (uint64_t)it.h * a.g + hh) * D + 32u * g + 4u * (lane >> 2)) = w;
 }
 template <int G, int NT>
 __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_attend_kernel(const __grid_constant__ gpuos_devdesc d)
