@@ -803,17 +803,25 @@ DEV void kv4_part_merge(const Kv4Args &a, const Kv4Item &it, const float *left, 
             wy[r] *= inv;
         }
         if (dst && lane < 4) __stcg(d4 + nt * 4 + j, make_float4(m[0], l[0], m[1], l[1]));
-#pragma unroll 2
-        for (int g = 0; g < G; g++)
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const uint32_t idx = ((uint32_t)(nt * G + g) * 2u + r) * 32u + lane;
-                const float4 x = __ldcg(x4 + NT * 4 + idx), y = __ldcg(y4 + NT * 4 + idx);
-                const float4 v = make_float4(fmaf(y.x, wy[r], x.x * wx[r]), fmaf(y.y, wy[r], x.y * wx[r]),
-                                             fmaf(y.z, wy[r], x.z * wx[r]), fmaf(y.w, wy[r], x.w * wx[r]));
+        for (int g0 = 0; g0 < G; g0 += 2) {
+            float4 x[4], y[4]; /* both states of two groups in flight (the stores may be to one of them) */
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uint32_t idx = ((uint32_t)(nt * G + g0) * 2u + k) * 32u + lane;
+                x[k] = __ldcg(x4 + NT * 4 + idx);
+                y[k] = __ldcg(y4 + NT * 4 + idx);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uint32_t idx = ((uint32_t)(nt * G + g0) * 2u + k) * 32u + lane;
+                const int r = k & 1;
+                const float4 v = make_float4(fmaf(y[k].x, wy[r], x[k].x * wx[r]), fmaf(y[k].y, wy[r], x[k].y * wx[r]),
+                                             fmaf(y[k].z, wy[r], x[k].z * wx[r]), fmaf(y[k].w, wy[r], x[k].w * wx[r]));
                 if (dst) __stcg(d4 + NT * 4 + idx, v);
                 else kv4_out4<G, NT>(a, it, idx, l[r], v);
             }
+        }
     }
 }
 
