@@ -511,7 +511,9 @@ GPUOS_API size_t gpuos_kv4_pool_bytes(uint32_t npages, uint32_t Hkv, uint32_t D)
  * take smaller tiles than in the executor (te within [4096 (GELU: 1024),
  * 4096 (f32) or 8192 (bf16)], the rule above otherwise): a launch runs one
  * op, so its tiles are all its parallelism. With stage_bytes
- * of shared-memory staging per warp as in gpuos_config. Deps are implied by
+ * of shared-memory staging per warp as in gpuos_config. The 4-bit cache's ops
+ * launch kernels of their own (attention: at most one block per SM; the others:
+ * four of the rule's tiles a block) and do not use stage_bytes. Deps are implied by
  * stream order. Does not synchronize. Errors: EINVAL (as gpuos_submit),
  * ECUDA. */
 GPUOS_API int gpuos_eager_run(const gpuos_desc *d, uint32_t count, uint32_t stage_bytes, void *stream);
