@@ -109,7 +109,7 @@ enum {
      * held a NaN or an infinity, and reads as NaN). Slot s is key s % 32 of page s / 32. Pages
      * are caller-owned like every tensor; so are the tables that say which are in use. */
     GPUOS_OP_KV4_WRITE = 14, /* rows a=k[N][Hkv][D], b=v, f32|bf16, quantised into slots aux0 =
-                               i32[N] of pool `out`; dims = {N, Hkv, D, npages}. e is the least
+                               i32[N] of pool `out`; dims = {N, Hkv, D, npages}, N < 2^31. e is the least
                                exponent >= -127 (at most 125) with max|x| <= 6 * 2^e, codes are
                                the nearest, ties to the even code. A negative slot is skipped.
                                The slots of one descriptor are distinct (of two rows for one slot

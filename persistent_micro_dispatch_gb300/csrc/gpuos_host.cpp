@@ -483,7 +483,7 @@ static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool use
         const bool rd = d->op_id == GPUOS_OP_KV4_READ;
         if (m[0]) {
             const uint64_t second = rd ? d->aux1 : d->b;
-            if (!kv4_sizes_ok(m[1], m[2], m[3])) return GPUOS_EINVAL;
+            if (!kv4_sizes_ok(m[1], m[2], m[3]) || m[0] > GPUOS_KV4_MAX_ROWS) return GPUOS_EINVAL;
             if (!d->a || !second || !d->out || !d->aux0 || (d->aux0 & 3u)) return GPUOS_EINVAL;
             if (!al16(d->a) || !al16(second) || !al16(d->out)) return GPUOS_EINVAL;
         }

@@ -35,6 +35,7 @@
 #define GPUOS_KV4_LEAD 6                  /* units that starting an attention item counts for (a page counts one) */
 #endif
 #define GPUOS_KV4_MAX_PAGES (1u << 26)    /* pages of a pool, and of a table row: slots are below 2^31 */
+#define GPUOS_KV4_MAX_ROWS 0x7FFFFFFFu    /* tokens of a KV4 write or read */
 #define GPUOS_PAGE_CHUNK 16384            /* bytes of a page-copy tile */
 #define GPUOS_ROW_REG_MAX 4096            /* rows up to this width stay in registers */
 #define GPUOS_MAX_WPB 12

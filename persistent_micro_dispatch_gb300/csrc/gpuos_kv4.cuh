@@ -122,8 +122,7 @@ DEV float kv4_ex2(float x)
  * multiplied there by 2^(b - E + 7), b the value's scale exponent and E the
  * largest met so far in its group: exact unless the product falls below
  * 2^-14, that is 2^-27 of the largest; a scale 2^-22 below E counts as zero.
- * The softmax's
- * reference and sum and the output accumulators are fp32.
+ * The softmax's reference and sum and the output accumulators are fp32.
  * ------------------------------------------------------------------------- */
 struct Kv4Args {
     const uint16_t *q;
@@ -166,7 +165,7 @@ DEV void kv4_token(const Kv4Args &a, uint32_t r, uint32_t &t, uint32_t &hh)
  * unit that does nothing (bad). */
 DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len, bool &bad)
 {
-    bad = (uint32_t)len > a.P * GPUOS_KV4_PAGE; /* (at most 2^31; a negative length is above) */
+    bad = len < 0 || (uint32_t)len > a.P * GPUOS_KV4_PAGE;
     return bad || len == 0 ? 1u : ((uint32_t)len + GPUOS_KV4_PAGE - 1u) / GPUOS_KV4_PAGE;
 }
 DEV uint32_t kv4_pages(const Kv4Args &a, int32_t len)
@@ -927,7 +926,7 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
     kv4_args(d, 8u * NT, a);
     int32_t len0;
     const uint32_t W = kv4_units(a, len0);
-    const uint32_t nt = min(d->ntiles, W);
+    const uint32_t nt = min(min(d->ntiles, W), (uint32_t)GPUOS_KV4_TILES); /* (what the workspace holds) */
     if (tile >= nt) return GPUOS_ST_OK;
     const Kv4Runs runs(W, nt);
     uint32_t u = runs.start(tile);
@@ -983,10 +982,19 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
     return status;
 }
 
+/* The executor's entries check sizes again: an alias of an op (a user op id)
+ * is not checked on the host. */
 DEV int kv4_sdpa_op(const gpuos_devdesc *d, uint32_t tile)
 {
     if (d->dims[0] == 0) return GPUOS_ST_OK;
-    return (d->dims[2] & 0xFFFFu) == 128 ? kv4_sdpa_tile<4, 1>(d, tile) : kv4_sdpa_tile<2, 1>(d, tile);
+    const uint32_t H = d->dims[1] & 0xFFFFu, Hkv = d->dims[1] >> 16, D = d->dims[2] & 0xFFFFu, T = d->dims[2] >> 16;
+    const uint32_t P = d->dims[3], npages = d->dims[4];
+    if (Hkv == 0 || H == 0 || H % Hkv || T == 0 || T > GPUOS_KV4_MAX_T || P == 0 || P > GPUOS_KV4_MAX_PAGES ||
+        npages == 0 || npages > GPUOS_KV4_MAX_PAGES || (D != 64 && D != 128))
+        return GPUOS_ST_BAD_ARGS;
+    const uint32_t HR = Hkv * ((T * (H / Hkv) + GPUOS_KV4_ROWS - 1u) / GPUOS_KV4_ROWS); /* below 2^31 */
+    if ((uint64_t)d->dims[0] * HR >= (1ull << 32) / (P + GPUOS_KV4_LEAD)) return GPUOS_ST_BAD_ARGS;
+    return D == 128 ? kv4_sdpa_tile<4, 1>(d, tile) : kv4_sdpa_tile<2, 1>(d, tile);
 }
 
 /* ---------------------------------------------------------------------------
@@ -1292,9 +1300,16 @@ DEV int kv4_read_tile(const gpuos_devdesc *d, uint32_t tile)
     }
     return __any_sync(0xFFFFFFFFu, bad) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
 }
+DEV bool kv4_rows_ok(const gpuos_devdesc *d)
+{
+    return d->dims[0] <= GPUOS_KV4_MAX_ROWS && d->dims[1] != 0 && d->dims[1] <= 0xFFFFu &&
+           (d->dims[2] == 64 || d->dims[2] == 128) && d->dims[3] != 0 && d->dims[3] <= GPUOS_KV4_MAX_PAGES &&
+           d->dtype <= GPUOS_BF16 && d->ntiles >= d->dims[1];
+}
 DEV int kv4_write_op(const gpuos_devdesc *d, uint32_t tile)
 {
     if (d->dims[0] == 0) return GPUOS_ST_OK;
+    if (!kv4_rows_ok(d)) return GPUOS_ST_BAD_ARGS;
     const bool f32 = d->dtype == GPUOS_F32;
     if (d->dims[2] == 128) return f32 ? kv4_write_tile<4, true>(d, tile) : kv4_write_tile<4, false>(d, tile);
     return f32 ? kv4_write_tile<2, true>(d, tile) : kv4_write_tile<2, false>(d, tile);
@@ -1302,6 +1317,7 @@ DEV int kv4_write_op(const gpuos_devdesc *d, uint32_t tile)
 DEV int kv4_read_op(const gpuos_devdesc *d, uint32_t tile)
 {
     if (d->dims[0] == 0) return GPUOS_ST_OK;
+    if (!kv4_rows_ok(d)) return GPUOS_ST_BAD_ARGS;
     const bool f32 = d->dtype == GPUOS_F32;
     if (d->dims[2] == 128) return f32 ? kv4_read_tile<4, true>(d, tile) : kv4_read_tile<4, false>(d, tile);
     return f32 ? kv4_read_tile<2, true>(d, tile) : kv4_read_tile<2, false>(d, tile);

@@ -15,7 +15,8 @@ library, has the dense cache update and attention that these stand beside.
     gpuos.eager_run(kv4.write(k, v, slots, pool), stream)
     gpuos.eager_run(kv4.sdpa(q, pool, table, lens, out, ws, D ** -0.5), stream)
 
-Nothing here reads device memory. Slots, page tables, lengths and pairs that
+Nothing here reads device memory or computes gradients. Launch with the
+tensors' device current, on one of its streams. Slots, page tables, lengths and pairs that
 point outside the pool are found by the kernels: such an entry is skipped
 (attention: the page counts as no keys; a request whose length does not fit
 its table row keeps its output rows as they were), and the executor reports

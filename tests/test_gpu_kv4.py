@@ -505,6 +505,44 @@ def test_serving_steps(runner):
     assert np.array_equal(pool.cpu().numpy(), ref)
 
 
+def test_aliased_ops_check_their_sizes():
+    """An alias is a user op: the host passes its sizes and tile count on, and
+    the op itself refuses what it cannot do."""
+    import torch
+    from persistent_micro_dispatch_gb300 import gpuos as G, kv4
+    from workloads.device import warm_torch
+    q, pool, table, lens = _attend_case(81, 2, 4, 2, 64, 1, [700, 33])
+    t = [_dev(q, torch.bfloat16), _dev(pool), _dev(table), _dev(lens)]
+    out, ws = torch.zeros_like(t[0]), kv4.new_workspace()
+    k = torch.ones(3, 2, 64, device="cuda")
+    s = _dev(np.array([0, 1, 2], np.int32))
+    good = kv4.sdpa(*t, out, ws, 0.1)
+    bad = [good.copy() for _ in range(6)] + [kv4.read(t[1], s, k.clone(), k.clone()) for _ in range(3)]
+    for d, (at, v) in zip(bad, [(1, 4), (1, 4 | 3 << 16), (2, 96 | 1 << 16), (2, 64), (3, 0), (4, 0), (1, 0), (2, 96), (3, 0)]):
+        d["dims"][0, at] = v
+    good["ntiles"] = 5000  # more than the workspace holds states for
+    d = np.concatenate([good] + bad)
+    d["op_id"] = [90] * 7 + [91] * 3
+    d["ntiles"][1:] = 4
+    d["flags"] = G.FLAG_DEP_REL
+    d["dep"][1:, 0] = 1
+    warm_torch()
+    torch.cuda.synchronize()
+    ex = G.Executor()
+    try:
+        ex.alias_op(90, G.OP["kv4_sdpa"])
+        ex.alias_op(91, G.OP["kv4_read"])
+        hist = ex.set_history(0, len(d))
+        ex.submit_batch(d)
+        rc = ex.sync(raise_on_error=False, timeout_ms=60_000)
+    finally:
+        assert ex.shutdown() == G.OK
+    assert rc == G.EDEVICE and hist["status"].tolist() == [0] + [2] * 9
+    want, tol = R.attend(q, pool, table, lens, 0.1)
+    _close(_f64(out), want, tol)
+    assert not ws[:8192].any().item()
+
+
 def test_binding_refusals():
     import torch
     from persistent_micro_dispatch_gb300 import kv4

@@ -64,7 +64,7 @@ def test_sdpa_refusals(G, bad):
 @pytest.mark.parametrize("op", ["kv4_write", "kv4_read"])
 @pytest.mark.parametrize("bad", [
     dict(dims=(1, 0, 128, 1)), dict(dims=(1, 65536, 128, 1)), dict(dims=(1, 1, 100, 1)), dict(dims=(1, 1, 128, 0)),
-    dict(dims=(1, 1, 128, (1 << 26) + 1)), dict(dtype=2), dict(a=0), dict(out=0), dict(aux0=0), dict(aux0=0x1002),
+    dict(dims=(1, 1, 128, (1 << 26) + 1)), dict(dims=(1 << 31, 1, 128, 1)), dict(dtype=2), dict(a=0), dict(out=0), dict(aux0=0), dict(aux0=0x1002),
     dict(a=0x1004), dict(out=0x1008), dict(second=0), dict(second=0x1008)])
 def test_row_refusals(G, op, bad):
     bad = dict(bad)
