@@ -1643,6 +1643,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         const uint32_t F = shared[k].last;
         if (F == 0) continue;
         const uint32_t blk0 = shared[k].blk0;
+#pragma unroll
         for (uint32_t idx = threadIdx.x; idx < NE; idx += C::WARPS * 32u) {
             const uint32_t r = idx / (64u * G) * 8u + 2u * (idx & 3u) + (idx >> 5 & 1u);
             float M = -FLT_MAX, l = 0.0f;
@@ -1750,9 +1751,18 @@ static int kv4_eager_launch(const gpuos_devdesc &d, void *stream)
     default: break;
     }
     if (d.dims[0] == 0) return 0;
+    /* Row tiles of eight or of sixteen rows. Sixteen read and convert a page
+     * half as often; eight leave room for twelve warps an SM instead of eight,
+     * which is better while a warp has few pages: sixteen rows a head, 4 heads
+     * of 64 over 4 x 3,000 tokens 12.5 us by sixteens, 9.4 by eights; 8 x
+     * 8,000 20.7, 19.9; 8 x 20,000 33.5, 37.5; 32 x 8,000 44.9, 54.2. They
+     * cross near nine pages for each of 1,824 warps; the lengths are on the
+     * device, so the table's width stands for them. */
     const uint32_t rows = (d.dims[2] >> 16) * ((d.dims[1] & 0xFFFFu) / (d.dims[1] >> 16));
-    if ((d.dims[2] & 0xFFFFu) == 128) return rows <= 8 ? kv4_attend_launch<4, 1>(d, stream) : kv4_attend_launch<4, 2>(d, stream);
-    return rows <= 8 ? kv4_attend_launch<2, 1>(d, stream) : kv4_attend_launch<2, 2>(d, stream);
+    const uint64_t pages = (uint64_t)d.dims[0] * d.dims[3] * (d.dims[1] >> 16) * ((rows + 7u) / 8u);
+    const bool eights = rows <= 8 || pages < 16384u;
+    if ((d.dims[2] & 0xFFFFu) == 128) return eights ? kv4_attend_launch<4, 1>(d, stream) : kv4_attend_launch<4, 2>(d, stream);
+    return eights ? kv4_attend_launch<2, 1>(d, stream) : kv4_attend_launch<2, 2>(d, stream);
 }
 /* Load the kernels (see gpuos_dev_preload). */
 static int kv4_preload()

@@ -107,6 +107,7 @@ CASES = [
     (4, 8, 2, 128, 4, [0, 4, 65, 3]),
     (40, 2, 1, 64, 1, list(range(40))),   # more than a warp's lanes of requests
     (1, 4, 1, 128, 1, [20011]),           # long: many partial states
+    (3, 24, 1, 128, 5, [1500, 97, 3]),    # 120 rows
     (3, 32, 4, 128, 2, [3000, 7, 1023]),
 ]
 
@@ -118,6 +119,20 @@ def test_attention(case, runner):
     x = _attend_case(hash(case[:5]) & 0xFFFF, B, H, heads, D, T, lens, spare=B % 3)
     want, tol = R.attend(*x, D ** -0.5)
     _close(_attend(RUNNERS[runner], *x, D ** -0.5), want, tol)
+
+
+@pytest.mark.parametrize("D,H,T,lens", [(128, 16, 1, [9000, 31, 0, 4097]), (64, 11, 3, [2, 700, 5000, 33]), (128, 64, 7, [1200, 5, 33])])
+def test_attention_wide_tables(D, H, T, lens):
+    """Tables wide enough for the launch to take sixteen rows at a time,
+    whatever the lengths."""
+    q, pool, table, lens = _attend_case(91, len(lens), H, 1, D, T, lens)
+    wide = np.full((len(lens), 16384), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    want, tol = R.attend(q, pool, table, lens, D ** -0.5)
+    for t in (table, wide):
+        _close(_attend(_eager, q, pool, t, lens, D ** -0.5), want, tol)
+    first = _attend(_eager, q, pool, wide, lens, 0.1)
+    assert np.array_equal(_attend(_eager, q, pool, wide, lens, 0.1), first)
 
 
 @pytest.mark.parametrize("runner", ["eager", "executor"])
