@@ -1327,7 +1327,7 @@ DEV int kv4_read_op(const gpuos_devdesc *d, uint32_t tile)
  * Page copy: pool[layer][dst] = pool[layer][src] for every (src, dst) pair and
  * layer, GPUOS_PAGE_CHUNK bytes a tile, eight 16-byte loads in flight a lane.
  * Bound by memory: 611 pages of 128 KB in 4 layers 87.5 us, 6.6 TB/s; 15 of
- * 34 KB in 32 layers 6.1 us, a launch and its ramp.
+ * 34 KB in 32 layers 5.7 us, a launch and its ramp.
  * ------------------------------------------------------------------------- */
 DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
 {
@@ -1369,13 +1369,39 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
  * merges them in the order of the keys.
  *
  * Bound by memory while pages stream: 64 requests of 2,000 to 16,383 tokens
- * (32 heads over 8, D = 128) 80.5 us, 5.4 TB/s over the launch and 6.7 in its
+ * (32 heads over 8, D = 128) 80.3 us, 5.4 TB/s over the launch and 6.7 in its
  * middle (a page's 517 instructions take 150 of the 187 cycles that its bytes
- * take an SM); one of 131,071 (64 heads over 8) 35.9 us; one of 1,000 8.4 us,
+ * take an SM); one of 131,071 (64 heads over 8) 35.1 us; one of 1,000 8.2 us,
  * which is a chain of loads (lengths, page ids, page) and merges. Twelve warps
  * of 168 registers: sixteen of 128 were 2 to 10 % slower, eight 16 % on the
  * long case; they only win where latency is all (1,000 tokens: 8.0 us).
  * ------------------------------------------------------------------------- */
+/* These kernels are launched with programmatic stream serialisation: their
+ * blocks may start as soon as those of the stream's previous kernel have
+ * ended, and wait here, before anything else, until its writes are visible.
+ * That takes 2 us off a launch that follows another in a stream (8 requests of
+ * 32 heads 18.5 -> 16.7 us a call, one of 131,071 tokens 36.7 -> 34.3). Every
+ * thread of every block waits, whether it has work or not: a kernel that ended
+ * without would let the next one pass the one before it. */
+DEV void kv4_after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+static int kv4_launch(void (*kernel)(const gpuos_devdesc), uint32_t blocks, uint32_t threads, uint32_t smem, void *stream,
+                      const gpuos_devdesc &d)
+{
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(blocks);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = (cudaStream_t)stream;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, kernel, d) == cudaSuccess) return 0;
+    (void)cudaGetLastError(); /* reported here */
+    return -1;
+}
+
 template <int G, int NT>
 struct Kv4Block {
     static constexpr uint32_t WARPS = NT == 1 ? 12 : 8; /* 168 and 255 registers a thread */
@@ -1426,6 +1452,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     } shared[2];
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
     unsigned char *mine = sm + warp * C::WARP_BYTES;
+    kv4_after_previous();
     if (lane == 0) {
         for (uint32_t k = 0; k < NS; k++)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&bars[warp][k])) : "memory");
@@ -1710,8 +1737,7 @@ static int kv4_attend_launch(const gpuos_devdesc &d, void *stream)
     uint64_t grid = (units + C::WARPS - 1) / C::WARPS;
     if (grid > (uint64_t)sms) grid = (uint64_t)sms;
     if (grid > GPUOS_KV4_MAX_BLOCKS) grid = GPUOS_KV4_MAX_BLOCKS;
-    gpuos_kv4_attend_kernel<G, NT><<<(uint32_t)grid, C::WARPS * 32, C::SMEM, (cudaStream_t)stream>>>(d);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return kv4_launch(gpuos_kv4_attend_kernel<G, NT>, (uint32_t)grid, C::WARPS * 32, C::SMEM, stream, d);
 }
 
 /* The other ops: one warp a tile, as in the executor; four warps a block, so
@@ -1722,6 +1748,7 @@ template <int OP, int G, bool F32>
 __global__ void __launch_bounds__(GPUOS_KV4_EAGER_WARPS * 32) gpuos_kv4_eager_kernel(const __grid_constant__ gpuos_devdesc d)
 {
     const uint32_t tile = blockIdx.x * GPUOS_KV4_EAGER_WARPS + (threadIdx.x >> 5);
+    kv4_after_previous();
     if (tile >= d.ntiles) return;
     if (OP == GPUOS_OP_KV4_WRITE) (void)kv4_write_tile<G, F32>(&d, tile);
     if (OP == GPUOS_OP_KV4_READ) (void)kv4_read_tile<G, F32>(&d, tile);
@@ -1731,8 +1758,7 @@ template <int OP, int G, bool F32>
 static int kv4_tiles_launch(const gpuos_devdesc &d, void *stream)
 {
     const uint32_t blocks = (d.ntiles + GPUOS_KV4_EAGER_WARPS - 1) / GPUOS_KV4_EAGER_WARPS;
-    gpuos_kv4_eager_kernel<OP, G, F32><<<blocks, GPUOS_KV4_EAGER_WARPS * 32, 0, (cudaStream_t)stream>>>(d);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return kv4_launch(gpuos_kv4_eager_kernel<OP, G, F32>, blocks, GPUOS_KV4_EAGER_WARPS * 32, 0, stream, d);
 }
 template <int OP>
 static int kv4_rows_launch(const gpuos_devdesc &d, void *stream)

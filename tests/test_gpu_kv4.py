@@ -335,6 +335,40 @@ def test_attention_far_pages():
         assert np.array_equal(_f64(y), R.values(*R.quantise(_f64(x))))
 
 
+def test_launches_wait_for_their_predecessors():
+    """A chain of short and long launches on one stream, ordinary kernels
+    among them: each op sees what every earlier one wrote, also past a launch
+    between them that has nothing to do."""
+    import torch
+    from persistent_micro_dispatch_gb300 import gpuos as G, kv4
+    rng = np.random.default_rng(5)
+    heads, D, n = 8, 128, 40_000
+    pool = kv4.new_pool(n // 32, heads, D)
+    k = _dev(R.bf16(rng.standard_normal((n, heads, D))), torch.bfloat16)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    hole = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    one = torch.empty(1, heads, D, dtype=torch.bfloat16, device="cuda")
+    src, a, b = torch.empty_like(k), torch.empty_like(k), torch.empty_like(k)
+    pairs = _dev(np.array([[i, n // 32 - 1 - i] for i in range(n // 64)], np.int32))
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for r in range(8):
+            torch.mul(k, float(2 ** r), out=src)  # an ordinary kernel, then ours
+            G.eager_run(kv4.write(src, src, slots, pool), st.cuda_stream)
+            G.eager_run(kv4.read(pool, hole, one, one), st.cuda_stream)
+            G.eager_run(kv4.page_copy(pool.view(1, n // 32, -1), pairs), st.cuda_stream)
+            G.eager_run(kv4.read(pool, hole, one, one), st.cuda_stream)
+            G.eager_run(kv4.read(pool, slots, a, b), st.cuda_stream)
+            got = a.clone()  # ours, then an ordinary kernel
+            want = R.values(*R.quantise(_f64(k[:32 * 4]) * 2.0 ** r))
+            st.synchronize()
+            assert np.array_equal(_f64(got[:128]), want)
+            m = torch.arange(n, device="cuda").view(-1, 32)
+            m[n // 32 - n // 64:] = m[:n // 64].flip(0)
+            assert torch.equal(got, got[m.flatten()])
+
+
 def _rows(rng, n, heads, D, f32):
     x = rng.standard_normal((n, heads, D)) * np.exp(2 * rng.standard_normal((n, heads, D // 32))).repeat(32, -1)
     return x.astype(np.float32).astype(np.float64) if f32 else R.bf16(x)
