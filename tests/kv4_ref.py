@@ -1,4 +1,4 @@
-"""The 4-bit paged cache in 64 bits, from its definition (numpy): the checker
+"""The 4-bit paged cache in 64 bits, from its definition (numpy): the reference
 of the KV4 ops' tests. It shares no code with the library."""
 import numpy as np
 
@@ -125,7 +125,7 @@ def bound(p, v, scale, reach, D):
     product below 2^-14 is off by 2^-25, when the largest weight times the
     largest scale is 2^13 or more: 6 * 2^-38 of that scale for each key."""
     rel = 2.0 ** -11 + 2 * (D + 8) * 2.0 ** -24 * reach + 2.0 ** -18
-    return rel * (p @ v) + 2.0 ** -31 * v.sum(0) + (6 * 2.0 ** -22 + len(p) * 6 * 2.0 ** -38) * scale
+    return rel * (p @ v) + 2.0 ** -31 * v.sum(0) + (6 * 2.0 ** -22 + len(v) * 6 * 2.0 ** -38) * scale
 
 
 def random_pool(rng, pages, heads, D, spread=3.0):

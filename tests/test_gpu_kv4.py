@@ -106,6 +106,7 @@ CASES = [
     (2, 5, 1, 64, 32, [40, 17]),          # 160 rows
     (4, 8, 2, 128, 4, [0, 4, 65, 3]),
     (40, 2, 1, 64, 1, list(range(40))),   # more than a warp's lanes of requests
+    (201, 3, 3, 64, 1, [7 * i % 90 for i in range(201)]),
     (1, 4, 1, 128, 1, [20011]),           # long: many partial states
     (3, 24, 1, 128, 5, [1500, 97, 3]),    # 120 rows
     (3, 32, 4, 128, 2, [3000, 7, 1023]),
@@ -133,6 +134,56 @@ def test_attention_wide_tables(D, H, T, lens):
         _close(_attend(_eager, q, pool, t, lens, D ** -0.5), want, tol)
     first = _attend(_eager, q, pool, wide, lens, 0.1)
     assert np.array_equal(_attend(_eager, q, pool, wide, lens, 0.1), first)
+
+
+@pytest.mark.parametrize("runner", ["eager", "executor"])
+def test_attention_most_heads(runner):
+    """65,535 query heads over one cache head, two tokens: 131,070 rows."""
+    q, pool, table, lens = _attend_case(101, 1, 65535, 1, 64, 2, [40])
+    K, V, S = R.unpack(pool)
+    at = np.arange(40)
+    k, v, sc = (x[table[0, at // 32], 0, at % 32] for x in (K, V, S))
+    want, tol = np.zeros(q.shape), np.zeros(q.shape)
+    for t in range(2):
+        n = 39 + t
+        s = q[0, t] @ k[:n].T * 0.1
+        p = np.exp(s - s.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        want[0, t] = p @ v[:n]
+        reach = (np.abs(q[0, t]) @ np.abs(k[:n]).T * 0.1).max()
+        tol[0, t] = R.bound(p, np.abs(v[:n]), sc[:n].max(0), reach, 64)
+    _close(_attend(RUNNERS[runner], q, pool, table, lens, 0.1), want, tol)
+
+
+def test_first_call_captured():
+    """The first call of a process may be inside a capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from persistent_micro_dispatch_gb300 import gpuos as G, kv4
+q = torch.randn(2, 1, 4, 128, device="cuda").bfloat16()
+pool, ws, out = kv4.new_pool(8, 2, 128), kv4.new_workspace(), torch.zeros_like(q)
+k = torch.randn(70, 2, 128, device="cuda").bfloat16()
+slots = torch.arange(70, device="cuda", dtype=torch.int32)
+table = torch.tensor([[0, 1, 2], [0, -1, -1]], device="cuda", dtype=torch.int32)
+lens = torch.tensor([70, 1], device="cuda", dtype=torch.int32)
+pairs = torch.tensor([[0, 5]], device="cuda", dtype=torch.int32)
+st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g, stream=st):
+    for d in (kv4.write(k, k, slots, pool), kv4.page_copy(pool.view(1, 8, -1), pairs),
+              kv4.sdpa(q, pool, table, lens, out, ws, 0.1), kv4.read(pool, slots, k, k)):
+        G.eager_run(d, st.cuda_stream)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out[1, 0, 0], k[0, 0]) and torch.equal(out[1, 0, 3], k[0, 1]) and torch.equal(pool[5], pool[0])
+print("captured ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert "captured ok" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("runner", ["eager", "executor"])

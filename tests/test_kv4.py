@@ -1,5 +1,5 @@
 """The 4-bit paged cache without a GPU: the tiling rules and refusals of its
-ops, the binding's checks, and the checker's own pins."""
+ops, the binding's checks, and the reference's own pins."""
 import numpy as np
 import pytest
 import torch
@@ -121,7 +121,7 @@ def test_page_layout_is_a_bijection(D):
     assert (k[:, ::2] == k[:, 1::2]).all() and (v[:, ::2] == v[:, 1::2]).all()
 
 
-def test_checker_quantises_by_the_definition():
+def test_reference_quantises_by_the_definition():
     x = np.zeros((1, 32))
     x[0, :8] = [6.0, 5.0, 2.5, 0.25, 0.75, -0.0, -3.5, 1.25]
     code, byte = R.quantise(x)
