@@ -1839,15 +1839,20 @@ __device__ __noinline__ int op_rope(const gpuos_devdesc *d, uint32_t t) { return
 __device__ __noinline__ int op_kv_write(const gpuos_devdesc *d, uint32_t t) { return kv_tile(d, t); }
 __device__ __noinline__ int op_sdpa(const gpuos_devdesc *d, uint32_t t) { return sdpa_tile(d, t); }
 __device__ __noinline__ int op_vecmat(const gpuos_devdesc *d, uint32_t t) { return vecmat_tile(d, t); }
-__device__ __noinline__ int op_kv4_write(const gpuos_devdesc *d, uint32_t t) { return kv4_write_op(d, t); }
-__device__ __noinline__ int op_kv4_read(const gpuos_devdesc *d, uint32_t t) { return kv4_read_op(d, t); }
-__device__ __noinline__ int op_kv4_sdpa(const gpuos_devdesc *d, uint32_t t) { return kv4_sdpa_op(d, t); }
-__device__ __noinline__ int op_page_copy(const gpuos_devdesc *d, uint32_t t) { return page_copy_op(d, t); }
+/* The 4-bit cache's entries. The names are chosen for their place: functions
+ * lie in the image in the order of their mangled names, and with these four
+ * among the others (op_kv4_write, ...) instead of behind them the mixed
+ * pipeline, which waits on the ops' code, ran 1.3 % slower (126.0 against
+ * 127.6 K ops/s, two runs each; without the four 128.0). */
+__device__ __noinline__ int op_xwrite(const gpuos_devdesc *d, uint32_t t) { return kv4_write_op(d, t); }
+__device__ __noinline__ int op_x_read(const gpuos_devdesc *d, uint32_t t) { return kv4_read_op(d, t); }
+__device__ __noinline__ int op_x_sdpa(const gpuos_devdesc *d, uint32_t t) { return kv4_sdpa_op(d, t); }
+__device__ __noinline__ int op_x_copy(const gpuos_devdesc *d, uint32_t t) { return page_copy_op(d, t); }
 
 __device__ gpuos_op_fn g_builtin_ops[GPUOS_OP_BUILTIN_COUNT] = {
     op_nop, op_add, op_mul, op_relu, op_gelu, op_softmax, op_layernorm,
     op_rowsum, op_rowmax, op_rowmin, op_rope, op_kv_write, op_sdpa, op_vecmat,
-    op_kv4_write, op_kv4_read, op_kv4_sdpa, op_page_copy,
+    op_xwrite, op_x_read, op_x_sdpa, op_x_copy,
 };
 
 /* The body of built-in op `kind`, inlined (the eager kernel). */

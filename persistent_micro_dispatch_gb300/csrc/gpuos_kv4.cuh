@@ -330,8 +330,7 @@ DEV void kv4_load_q(const Kv4Args &a, const Kv4Pos &p, Kv4Query<G, NT> &x)
 template <int G, int NT>
 DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx, Kv4State<G, NT> &s)
 {
-    const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
-    const uint32_t h = p.h, r0 = p.r0;
+    const uint32_t j = lane_id() & 3u, r0 = p.r0;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
         const uint4(&raw)[G] = qx.raw[nt];
@@ -1075,14 +1074,9 @@ struct Kv4Raw {
     DEV uint32_t top() const
     {
         uint32_t m = 0;
-        if (F32) {
 #pragma unroll
-            for (int c = 0; c < N; c++) m = max(m, w[c] & 0x7FFFFFFFu);
-            return m;
-        }
-#pragma unroll
-        for (int c = 0; c < N; c++) m = __vmaxu2(m, w[c] & 0x7FFF7FFFu);
-        return max(m << 16, m & 0xFFFF0000u);
+        for (int c = 0; c < N; c++) m = F32 ? max(m, w[c] & 0x7FFFFFFFu) : __vmaxu2(m, w[c] & 0x7FFF7FFFu);
+        return F32 ? m : max(m << 16, m & 0xFFFF0000u);
     }
 };
 template <int C, bool F32>
