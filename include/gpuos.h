@@ -513,8 +513,9 @@ GPUOS_API size_t gpuos_kv4_pool_bytes(uint32_t npages, uint32_t Hkv, uint32_t D)
  * op, so its tiles are all its parallelism. With stage_bytes
  * of shared-memory staging per warp as in gpuos_config. The 4-bit cache's ops
  * launch kernels of their own (attention: at most one block per SM; the others:
- * four of the rule's tiles a block) and do not use stage_bytes. Deps are implied by
- * stream order. Does not synchronize. Errors: EINVAL (as gpuos_submit),
+ * four of the rule's tiles a block), do not use stage_bytes, and may be given their
+ * SMs as the stream's previous kernel ends: they wait on the device until its writes
+ * are visible. Deps are implied by stream order. Does not synchronize. Errors: EINVAL (as gpuos_submit),
  * ECUDA. */
 GPUOS_API int gpuos_eager_run(const gpuos_desc *d, uint32_t count, uint32_t stage_bytes, void *stream);
 

@@ -31,9 +31,7 @@
 #define GPUOS_KV4_ROW_TILES 8192          /* KV4 write and read tiles aimed at */
 #define GPUOS_KV4_MAX_TILES 2048          /* counters at the start of the KV4 workspace */
 #define GPUOS_KV4_MAX_BLOCKS 1024         /* blocks of an eager attention launch at most (workspace) */
-#ifndef GPUOS_KV4_LEAD
 #define GPUOS_KV4_LEAD 6                  /* units that starting an attention item counts for (a page counts one) */
-#endif
 #define GPUOS_KV4_MAX_PAGES (1u << 26)    /* pages of a pool, and of a table row: slots are below 2^31 */
 #define GPUOS_KV4_MAX_ROWS 0x7FFFFFFFu    /* tokens of a KV4 write or read */
 #define GPUOS_PAGE_CHUNK 16384            /* bytes of a page-copy tile */

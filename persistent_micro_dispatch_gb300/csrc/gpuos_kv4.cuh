@@ -389,12 +389,6 @@ DEV uint4 kv4_ld16(const unsigned char *p)
     return *reinterpret_cast<const uint4 *>(p);
 }
 template <bool GLOBAL>
-DEV uint2 kv4_ld8(const unsigned char *p)
-{
-    if (GLOBAL) return __ldcg(reinterpret_cast<const uint2 *>(p));
-    return *reinterpret_cast<const uint2 *>(p);
-}
-template <bool GLOBAL>
 DEV uint32_t kv4_ld4(const unsigned char *p)
 {
     if (GLOBAL) return __ldcg(reinterpret_cast<const uint32_t *>(p));
@@ -736,22 +730,31 @@ template <int G, int NT>
 struct Kv4Part {
     static constexpr uint32_t floats = NT * 16u + NT * G * 256u;
 };
-template <int G, int NT>
-DEV void kv4_part_store(float *part, const Kv4State<G, NT> &s)
+static_assert(4u * (GPUOS_KV4_MAX_TILES + 2u * GPUOS_KV4_TILES * Kv4Part<4, 1>::floats) <= GPUOS_KV4_WORKSPACE &&
+                  4u * (GPUOS_KV4_MAX_TILES + 2u * GPUOS_KV4_MAX_BLOCKS * Kv4Part<4, 2>::floats) <= GPUOS_KV4_WORKSPACE &&
+                  GPUOS_KV4_TILES <= GPUOS_KV4_MAX_TILES && GPUOS_KV4_MAX_BLOCKS <= GPUOS_KV4_MAX_TILES,
+              "the workspace holds every tile's and block's states and counters");
+template <bool GLOBAL, int G, int NT>
+DEV void kv4_part_store(void *part, const Kv4State<G, NT> &s)
 {
-    const uint32_t lane = lane_id(), j = lane & 3u;
+    const uint32_t lane = lane_id();
     float4 *p4 = reinterpret_cast<float4 *>(part);
+    auto put = [&](uint32_t at, float4 v) {
+        if (GLOBAL) __stcg(p4 + at, v);
+        else p4[at] = v;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-        if (lane < 4) __stcg(p4 + nt * 4 + j, make_float4(s.m[nt][0], s.l[nt][0], s.m[nt][1], s.l[nt][1]));
+        if (lane < 4) put(nt * 4 + lane, make_float4(s.m[nt][0], s.l[nt][0], s.m[nt][1], s.l[nt][1]));
 #pragma unroll
         for (int g = 0; g < G; g++)
 #pragma unroll
             for (int r = 0; r < 2; r++)
-                __stcg(p4 + NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane,
-                       make_float4(s.acc[nt][g][0][r], s.acc[nt][g][0][r + 2], s.acc[nt][g][1][r], s.acc[nt][g][1][r + 2]));
+                put(NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane,
+                    make_float4(s.acc[nt][g][0][r], s.acc[nt][g][0][r + 2], s.acc[nt][g][1][r], s.acc[nt][g][1][r + 2]));
     }
 }
+
 /* A request's head and row tile. */
 struct Kv4Item {
     uint32_t b, h, r0, np;
@@ -954,7 +957,7 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
                 const uint32_t F = runs.run_of(p.first + p.np - 1) - first + 1;
                 auto slot = [&](uint32_t at) { return kv4_slot<G, NT>(d, first + at, at == 0); };
                 uint32_t c = tile - first;
-                kv4_part_store<G, NT>(slot(c), s);
+                kv4_part_store<true>(slot(c), s);
 #pragma unroll 1
                 for (uint32_t step = 1; step < F; step <<= 1) {
                     const uint32_t other = c ^ step;
@@ -1415,21 +1418,6 @@ struct Kv4Left {
 };
 
 template <int G, int NT>
-DEV void kv4_part_put(float4 *p4, const Kv4State<G, NT> &s)
-{
-    const uint32_t lane = lane_id();
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++) {
-        if (lane < 4) p4[nt * 4 + lane] = make_float4(s.m[nt][0], s.l[nt][0], s.m[nt][1], s.l[nt][1]);
-#pragma unroll
-        for (int g = 0; g < G; g++)
-#pragma unroll
-            for (int r = 0; r < 2; r++)
-                p4[NT * 4 + ((nt * G + g) * 2 + r) * 32 + lane] =
-                    make_float4(s.acc[nt][g][0][r], s.acc[nt][g][0][r + 2], s.acc[nt][g][1][r], s.acc[nt][g][1][r + 2]);
-    }
-}
-template <int G, int NT>
 __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_attend_kernel(const __grid_constant__ gpuos_devdesc d)
 {
     using C = Kv4Block<G, NT>;
@@ -1539,7 +1527,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                  * warp's run, and takes the place of the pages */
                 const bool tail = begin == 0;
                 __syncwarp();
-                kv4_part_put<G, NT>(reinterpret_cast<float4 *>(tail ? mine : sm + C::WARPS * C::WARP_BYTES + warp * C::FRAG), s);
+                kv4_part_store<false>(tail ? mine : sm + C::WARPS * C::WARP_BYTES + warp * C::FRAG, s);
                 if (lane == 0) {
                     (tail ? left[warp].tail : left[warp].head) = p.first;
                     (tail ? left[warp].titem : left[warp].hitem) = Kv4Item{p.b, p.h, p.r0, p.np};
