@@ -984,8 +984,9 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
     return status;
 }
 
-/* The executor's entries check sizes again: an alias of an op (a user op id)
- * is not checked on the host. */
+/* The executor's entries check sizes and alignment again: an alias of an op (a
+ * user op id) is not checked on the host. */
+DEV bool kv4_aligned(uint64_t p, uint32_t to) { return p != 0 && (p & (to - 1u)) == 0; }
 DEV int kv4_sdpa_op(const gpuos_devdesc *d, uint32_t tile)
 {
     if (d->dims[0] == 0) return GPUOS_ST_OK;
@@ -993,6 +994,9 @@ DEV int kv4_sdpa_op(const gpuos_devdesc *d, uint32_t tile)
     const uint32_t P = d->dims[3], npages = d->dims[4];
     if (Hkv == 0 || H == 0 || H % Hkv || T == 0 || T > GPUOS_KV4_MAX_T || P == 0 || P > GPUOS_KV4_MAX_PAGES ||
         npages == 0 || npages > GPUOS_KV4_MAX_PAGES || (D != 64 && D != 128))
+        return GPUOS_ST_BAD_ARGS;
+    if (!kv4_aligned(d->a, 16) || !kv4_aligned(d->b, 16) || !kv4_aligned(d->out, 16) || !kv4_aligned(d->aux2, 16) ||
+        !kv4_aligned(d->aux0, 4) || !kv4_aligned(d->aux1, 4))
         return GPUOS_ST_BAD_ARGS;
     const uint32_t HR = Hkv * ((T * (H / Hkv) + GPUOS_KV4_ROWS - 1u) / GPUOS_KV4_ROWS); /* below 2^31 */
     if ((uint64_t)d->dims[0] * HR >= (1ull << 32) / (P + GPUOS_KV4_LEAD)) return GPUOS_ST_BAD_ARGS;
@@ -1297,16 +1301,17 @@ DEV int kv4_read_tile(const gpuos_devdesc *d, uint32_t tile)
     }
     return __any_sync(0xFFFFFFFFu, bad) ? GPUOS_ST_BAD_ARGS : GPUOS_ST_OK;
 }
-DEV bool kv4_rows_ok(const gpuos_devdesc *d)
+DEV bool kv4_rows_ok(const gpuos_devdesc *d, uint64_t second)
 {
-    return d->dims[0] <= GPUOS_KV4_MAX_ROWS && d->dims[1] != 0 && d->dims[1] <= 0xFFFFu &&
+    return kv4_aligned(d->a, 16) && kv4_aligned(second, 16) && kv4_aligned(d->out, 16) && kv4_aligned(d->aux0, 4) &&
+           d->dims[0] <= GPUOS_KV4_MAX_ROWS && d->dims[1] != 0 && d->dims[1] <= 0xFFFFu &&
            (d->dims[2] == 64 || d->dims[2] == 128) && d->dims[3] != 0 && d->dims[3] <= GPUOS_KV4_MAX_PAGES &&
            d->dtype <= GPUOS_BF16 && d->ntiles >= d->dims[1];
 }
 DEV int kv4_write_op(const gpuos_devdesc *d, uint32_t tile)
 {
     if (d->dims[0] == 0) return GPUOS_ST_OK;
-    if (!kv4_rows_ok(d)) return GPUOS_ST_BAD_ARGS;
+    if (!kv4_rows_ok(d, d->b)) return GPUOS_ST_BAD_ARGS;
     const bool f32 = d->dtype == GPUOS_F32;
     if (d->dims[2] == 128) return f32 ? kv4_write_tile<4, true>(d, tile) : kv4_write_tile<4, false>(d, tile);
     return f32 ? kv4_write_tile<2, true>(d, tile) : kv4_write_tile<2, false>(d, tile);
@@ -1314,7 +1319,7 @@ DEV int kv4_write_op(const gpuos_devdesc *d, uint32_t tile)
 DEV int kv4_read_op(const gpuos_devdesc *d, uint32_t tile)
 {
     if (d->dims[0] == 0) return GPUOS_ST_OK;
-    if (!kv4_rows_ok(d)) return GPUOS_ST_BAD_ARGS;
+    if (!kv4_rows_ok(d, d->aux1)) return GPUOS_ST_BAD_ARGS;
     const bool f32 = d->dtype == GPUOS_F32;
     if (d->dims[2] == 128) return f32 ? kv4_read_tile<4, true>(d, tile) : kv4_read_tile<4, false>(d, tile);
     return f32 ? kv4_read_tile<2, true>(d, tile) : kv4_read_tile<2, false>(d, tile);
@@ -1329,9 +1334,10 @@ DEV int kv4_read_op(const gpuos_devdesc *d, uint32_t tile)
 DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
 {
     const uint32_t n = d->dims[0], p16 = d->dims[1], npages = d->dims[2], layers = d->dims[3];
-    if (n == 0 || p16 == 0 || layers == 0) return GPUOS_ST_OK;
+    if (n == 0) return GPUOS_ST_OK;
+    if (p16 == 0 || layers == 0 || !kv4_aligned(d->a, 16) || !kv4_aligned(d->aux0, 8)) return GPUOS_ST_BAD_ARGS;
     constexpr uint32_t C = GPUOS_PAGE_CHUNK / 16u;
-    const uint32_t nc = (p16 + C - 1) / C;
+    const uint32_t nc = p16 / C + (p16 % C != 0);
     const uint32_t pair = tile / nc, c0 = (tile - pair * nc) * C;
     const uint32_t layer = pair / n, k = pair - layer * n;
     if (layer >= layers) return GPUOS_ST_OK;

@@ -616,13 +616,31 @@ def test_aliased_ops_check_their_sizes():
     out, ws = torch.zeros_like(t[0]), kv4.new_workspace()
     k = torch.ones(3, 2, 64, device="cuda")
     s = _dev(np.array([0, 1, 2], np.int32))
+    pairs = _dev(np.array([[0, 1], [0, 1]], np.int32))
     good = kv4.sdpa(*t, out, ws, 0.1)
-    bad = [good.copy() for _ in range(6)] + [kv4.read(t[1], s, k.clone(), k.clone()) for _ in range(3)]
-    for d, (at, v) in zip(bad, [(1, 4), (1, 4 | 3 << 16), (2, 96 | 1 << 16), (2, 64), (3, 0), (4, 0), (1, 0), (2, 96), (3, 0)]):
-        d["dims"][0, at] = v
-    good["ntiles"] = 5000  # more than the workspace holds states for
+    reads, copies = kv4.read(t[1], s, k, k), kv4.page_copy(t[1][None], pairs)
+    bad = []
+
+    def refused(alias, desc, dim=None, value=0, field=None, shift=0):
+        d = desc.copy()
+        d["op_id"] = alias
+        if dim is not None:
+            d["dims"][0, dim] = value
+        if field:
+            d[field] = d[field] + shift if shift else 0
+        bad.append(d)
+
+    for dim, value in ((1, 4), (1, 4 | 3 << 16), (2, 96 | 1 << 16), (2, 64), (3, 0), (4, 0)):
+        refused(90, good, dim, value)
+    for field, shift in (("a", 8), ("b", 2), ("out", 1), ("aux0", 2), ("aux1", 1), ("aux2", 8), ("b", 0)):
+        refused(90, good, field=field, shift=shift)
+    for dim, value in ((1, 0), (2, 96), (3, 0)):
+        refused(91, reads, dim, value)
+    refused(91, reads, field="aux1", shift=4)
+    for dim, field, shift in ((1, None, 0), (3, None, 0), (None, "a", 0), (None, "aux0", 4)):
+        refused(92, copies, dim, 0, field, shift)
+    good["op_id"], good["ntiles"] = 90, 5000  # more tiles than the workspace holds states for
     d = np.concatenate([good] + bad)
-    d["op_id"] = [90] * 7 + [91] * 3
     d["ntiles"][1:] = 4
     d["flags"] = G.FLAG_DEP_REL
     d["dep"][1:, 0] = 1
@@ -632,12 +650,13 @@ def test_aliased_ops_check_their_sizes():
     try:
         ex.alias_op(90, G.OP["kv4_sdpa"])
         ex.alias_op(91, G.OP["kv4_read"])
+        ex.alias_op(92, G.OP["page_copy"])
         hist = ex.set_history(0, len(d))
         ex.submit_batch(d)
         rc = ex.sync(raise_on_error=False, timeout_ms=60_000)
     finally:
         assert ex.shutdown() == G.OK
-    assert rc == G.EDEVICE and hist["status"].tolist() == [0] + [2] * 9
+    assert rc == G.EDEVICE and hist["status"].tolist() == [0] + [2] * len(bad)
     want, tol = R.attend(q, pool, table, lens, 0.1)
     _close(_f64(out), want, tol)
     assert not ws[:8192].any().item()
