@@ -178,10 +178,13 @@ def host_now_ns() -> int:
 
 
 def eager_run(descs: np.ndarray, stream_ptr: int = 0, stage_bytes: int = 16384) -> None:
-    """Launch each descriptor as its own kernel on ``stream_ptr`` (cudaStream_t)."""
-    if descs.dtype is not DESC_DTYPE or not descs.flags.c_contiguous:
-        descs = np.ascontiguousarray(descs, dtype=DESC_DTYPE)
-    n = len(descs)
+    """Launch each descriptor as its own kernel on ``stream_ptr`` (cudaStream_t).
+    descs: an array of records, one record, or a list of them."""
+    # (the common case, a 1-d array of records, is taken as it is; a lone
+    # record's len() is its number of fields, so anything else goes to numpy)
+    if type(descs) is not np.ndarray or descs.dtype is not DESC_DTYPE or descs.ndim != 1 or not descs.flags.c_contiguous:
+        descs = np.ascontiguousarray(descs, dtype=DESC_DTYPE).reshape(-1)
+    n = descs.size
     # (a few descriptors are copied: cheaper than numpy's way to their address)
     rc = lib().gpuos_eager_run(descs.tobytes() if n <= 16 else descs.ctypes.data, n, stage_bytes, stream_ptr)
     if rc != OK:
