@@ -121,7 +121,11 @@ enum {
                                aux1 = table i32[B][P]; a=q[B][T][H][D], out alike, bf16; b = pool;
                                aux0 = lens i32[B], 0 <= lens[b] <= 32 P (the T new tokens
                                included); query head h reads cache head h / (H / Hkv); a query that
-                               sees no key gives zeros; aux2 = workspace of GPUOS_KV4_WORKSPACE
+                               sees no key gives zeros. A weight is held to 2^-11 of itself, or to
+                               2^-25 of what weighs most in the row (weight times value, by groups of
+                               32 channels), however far apart the values' sizes are and whatever
+                               keys that the query does not see hold; below 2^-140 of the largest it
+                               is nothing. aux2 = workspace of GPUOS_KV4_WORKSPACE
                                bytes (below); dims = {B, H | Hkv << 16, D | T << 16, P, npages},
                                T <= 32, H % Hkv == 0; fparam[0] = scale */
     GPUOS_OP_PAGE_COPY = 17, /* a[l][dst] = a[l][src] for the pairs aux0 = i32[n][2] of {src, dst}

@@ -116,12 +116,17 @@ DEV float kv4_ex2(float x)
  * in f16: exact for the bf16 values within 2^-21 of the row's largest, and
  * off by at most 2^-32 of it below. Codes are exact in f16; the products are
  * summed in fp32 for each scale group, and the groups' sums are scaled and
- * added in fp32. Weights p, the largest 2^6 to 2^8, are rounded to f16 (11
- * bits; bf16's 8 would show in a bf16 output; one 2^-20 of the largest still
- * has them all, below that the error is at most 2^-31 of the largest), and
- * multiplied there by 2^(b - E + 7), b the value's scale exponent and E the
- * largest met so far in its group: exact unless the product falls below
- * 2^-14, that is 2^-27 of the largest; a scale 2^-22 below E counts as zero.
+ * added in fp32. Weights p, the largest 2^14 to 2^15, are rounded to f16 (11
+ * bits; bf16's 8 would show in a bf16 output; one 2^-28 of the largest still
+ * has them all) and multiplied there by 2^(b - E), b the value's scale byte
+ * and E a byte of the group's choosing, which is also the accumulators' unit.
+ * A page is taken that way only if E - 12 <= b <= E for all its keys. Then
+ * the product is off by 2^-25 at most where it is not exact, and the key that
+ * set the softmax's reference weighs 2^14 with b >= E - 12: what is lost is
+ * 6 * 2^-27 of the largest p 2^b that the row has met, for each key, whatever
+ * the other rows and the hidden keys hold. Any other page (kv4_page_slow)
+ * multiplies p 2^(b - x) in fp32, x the row's own largest p 2^b in the page,
+ * before it rounds to f16, and sets E anew.
  * The softmax's reference and sum and the output accumulators are fp32.
  * ------------------------------------------------------------------------- */
 struct Kv4Args {
@@ -288,8 +293,9 @@ struct Kv4State {
     float m[NT][2];       /* the reference that scores are taken against, equal in the lanes of a row */
     float l[NT][2];       /* this lane's part of the running sum */
     float acc[NT][G][2][4];
-    uint32_t E[G]; /* largest value-scale exponent met in each group */
-    uint32_t El, bias2; /* E of group lane % G; 22 - El in both halves */
+    uint32_t E[G]; /* the unit of each group's accumulators: 2^(E - 127) */
+    uint32_t open; /* bit g: group g's window of scales is in use (a row may have no weight that bears it out) */
+    uint32_t nlo, factor; /* of group lane % G: 12 - E in both halves (closed: no byte passes); 15 - E in both f16 exponents */
     uint32_t nan; /* bit 2 NT g + 2 nt + c: row (nt, c) saw a NaN among group g's values */
     uint32_t lim[NT][2]; /* keys that the row sees */
     uint32_t min_lim;    /* least of them over the tile's rows */
@@ -301,6 +307,19 @@ DEV uint32_t kv4_row_limit(const Kv4Args &a, int32_t len, uint32_t r)
     uint32_t t, hh;
     kv4_token(a, r, t, hh);
     return (uint32_t)max(len - (int32_t)(a.T - 1u - t), 0);
+}
+
+/* The lane's part of the window of scales, from E and open. */
+template <int G, int NT>
+DEV void kv4_window(Kv4State<G, NT> &s)
+{
+    const uint32_t mine = lane_id() % G;
+    uint32_t e = s.E[0];
+#pragma unroll
+    for (int g = 1; g < G; g++) e = mine == (uint32_t)g ? s.E[g] : e;
+    const uint32_t lo = s.open >> mine & 1u ? (12u - e) & 0xFFFFu : 0x4000u;
+    s.nlo = lo | lo << 16;
+    s.factor = (15u - e) * 0x04000400u;
 }
 
 /* The item's query rows, as they lie in memory. */
@@ -377,8 +396,9 @@ DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx,
     }
 #pragma unroll
     for (int g = 0; g < G; g++) s.E[g] = 0;
-    s.El = s.nan = 0;
-    s.bias2 = 22u | 22u << 16;
+    s.nan = 0;
+    s.open = (1u << G) - 1u;
+    kv4_window(s);
     s.min_lim = kv4_row_limit(a, p.len, r0); /* rows come in order of t */
 }
 
@@ -402,65 +422,331 @@ DEV uint32_t kv4_keep(uint32_t key0, uint32_t n)
     return (1u << (8u * (n - key0))) - 1u;
 }
 
-/* The page's largest value scale of a group exceeds s.E (rare: at a run's
- * first page, then with each new largest). E grows, the accumulators follow.
- * vw: the lane's word of value scales, group lane % G, keys key0 .. key0 + 3
- * of the page, already without what lies behind the last key. A scale of 255
- * is noted for the rows that see the key, and dropped from vw. */
-template <int G, int NT>
-DEV void kv4_grow(uint32_t base, uint32_t key0, uint32_t &vw, Kv4State<G, NT> &s)
+/* 2^n for |n| up to 250 in two factors, as 2^n itself may leave fp32's range. */
+DEV float2 kv4_pow2x2(int n)
 {
+    n = min(max(n, -250), 250);
+    return make_float2(kv4_pow2(n / 2), kv4_pow2(n - n / 2));
+}
+/* x 2^n of a number x >= 0 (0 below 2^-126), by its exponent; NaN stays */
+DEV float kv4_shift(float x, int n)
+{
+    const uint32_t u = __float_as_uint(x);
+    const int e = (int)(u >> 23);
+    return e != 0 && e + n > 0 || e >= 255 ? __uint_as_float(e >= 255 ? u : u + ((uint32_t)n << 23)) : 0.0f;
+}
+/* floor(log2 |x|) of a number's bits, sign taken off; below 2^-126: -127 */
+DEV int kv4_log2(uint32_t bits) { return (int)(bits >> 23) - 127; }
+/* A word or byte of a page, which lies in shared or global memory (volatile:
+ * never from L1, which other ops' writes pass by). */
+DEV uint32_t kv4_any32(const unsigned char *p) { return *reinterpret_cast<const volatile uint32_t *>(p); }
+DEV uint32_t kv4_any8(const unsigned char *p) { return *reinterpret_cast<const volatile unsigned char *>(p); }
+/* Largest (least) of the lanes that hold a row's keys; of all rows. */
+DEV int kv4_max_keys(int x)
+{
+    x = max(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+    x = max(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+    return max(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+}
+
+/* The lane's word of value scales, keys key0 .. key0 + 3: what lies behind the
+ * page's nv keys becomes the window's largest byte (its weights are zero). */
+template <int G, int NT>
+DEV uint32_t kv4_fill(uint32_t vw, uint32_t key0, uint32_t nv, const Kv4State<G, NT> &s)
+{
+    const uint32_t keep = kv4_keep(key0, nv);
+    return (vw & keep) | (min(12u - (uint32_t)(int)(int16_t)s.nlo, 255u) * 0x01010101u & ~keep);
+}
+/* Does any lane's word hold a byte outside E - 12 .. E? (The larger of byte -
+ * (E - 12), mod 2^16, and 12, is 12 for the others.) */
+template <int G, int NT>
+DEV bool kv4_outside(uint32_t vw, const Kv4State<G, NT> &s)
+{
+    const uint32_t lo = __viaddmax_u16x2(__byte_perm(vw, 0u, 0x4140), s.nlo, 0x000C000Cu);
+    return __any_sync(0xFFFFFFFFu, __viaddmax_u16x2(__byte_perm(vw, 0u, 0x4342), s.nlo, lo) != 0x000C000Cu);
+}
+
+/* A page holds value scales outside its groups' windows (vw: the lane's word
+ * of them). Before the first weight the windows are free: each is laid four
+ * octaves above the largest scale of the keys that every row sees (of all
+ * keys, where that is none), and its twelve octaves hold most pages. False if
+ * the page does not fit all the same. */
+template <int G, int NT>
+DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, Kv4State<G, NT> &s)
+{
+    float any = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) any = fmaxf(any, fmaxf(s.l[nt][0], s.l[nt][1]));
+    if (__any_sync(0xFFFFFFFFu, any != 0.0f)) return false;
     const uint32_t lane = lane_id();
-    const uint32_t nan = __vcmpeq4(vw, 0xFFFFFFFFu);
-    if (__any_sync(0xFFFFFFFFu, nan != 0u)) {
-#pragma unroll 1
-        for (uint32_t g = 0; g < G; g++) {
-            /* the page's first such key of the group */
-            uint32_t lo = GPUOS_KV4_PAGE;
-            if (nan && lane % G == g) lo = key0 + ((uint32_t)__ffs((int)nan) - 1u) / 8u;
-            lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                for (int c = 0; c < 2; c++)
-                    if (lo < GPUOS_KV4_PAGE && base + lo < s.lim[nt][c]) s.nan |= 1u << (2u * NT * g + 2 * nt + c);
-        }
-        vw &= ~nan;
-    }
-    uint32_t x = max(max(vw & 255u, vw >> 8 & 255u), max(vw >> 16 & 255u, vw >> 24));
+    const uint32_t all = s.min_lim > base ? min(nv, s.min_lim - base) : nv;
+    const uint32_t x = vw & kv4_keep(key0, all);
+    const uint32_t top = max(max(x & 255u, x >> 8 & 255u), max(x >> 16 & 255u, x >> 24));
 #pragma unroll
     for (int g = 0; g < G; g++) {
-        const uint32_t e = max(s.E[g], __reduce_max_sync(0xFFFFFFFFu, lane % G == (uint32_t)g ? x : 0u));
-        /* 2^(E - e); below 2^-126 nothing is left of it */
-        const float up = s.E[g] + 127u > e ? kv4_pow2((int)s.E[g] - (int)e) : 0.0f;
-        s.E[g] = e;
-        if (lane % G == (uint32_t)g) s.El = e;
+        const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, lane % G == (uint32_t)g ? top : 0u);
+        if (t != 0u && t != 255u) s.E[g] = t + 4u; /* (acc is zero) */
+    }
+    kv4_window(s);
+    vw = kv4_fill(vw, key0, nv, s);
+    return !kv4_outside(vw, s);
+}
+
+/* A page whose value scales lie too far apart, or too far from what the rows
+ * have met, for weights in f16 under one unit: as kv4_page, but each row's
+ * products p 2^b are formed in fp32 and rounded to f16 against their own
+ * largest, 2^x. Then the window of scales is laid anew: four octaves above
+ * the scale of what the page's heaviest keys hold, but never so high that its
+ * unit is more than 2^12 above what some row has weighed (cap), because that
+ * is what bounds the error of the pages that follow; if the accumulators'
+ * range asks for more, the window is closed and every page comes here. (Rows
+ * of one tile that heed values more than 2^150 apart in one group: the smaller
+ * are lost.) A call whose every page comes here took 603 us instead of 80 (64
+ * requests of 2,000 to 16,383 tokens, scales random over 40 octaves); out of
+ * line, so that the common path keeps its registers. */
+template <int G, int NT>
+__device__ __noinline__ void kv4_page_slow(const unsigned char *pg, uint32_t base, uint32_t nv, uint32_t rows, Kv4State<G, NT> *s)
+{
+    constexpr uint32_t D = 32u * G;
+    constexpr int NONE = -100000;
+    const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
+    const uint32_t k0 = 4u * (i >> 1) + (i & 1u); /* keys 16 t + k0 + {0, 2} */
+    float sc[2][NT][4];
+    uint32_t lim[NT][2]; /* (behind the last row: sees nothing) */
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) lim[nt][r] = 8u * nt + 2u * j + r < rows ? s->lim[nt][r] : 0u;
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) sc[t][nt][c] = 0.0f;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+#pragma unroll 1
+        for (uint32_t g = 0; g < G; g++) {
+            const unsigned char *kp = pg + (uint32_t)t * 8u * D + lane * 8u * G + 4u * g;
+            const unsigned char *ks = pg + 32u * D + (16u * t + k0) * G + g;
+            uint32_t x0[4], x1[4];
+            kv4_decode4(kv4_any32(kp), x0);
+            kv4_decode4(kv4_any32(kp + 4u * G), x1);
+            const float f0 = __uint_as_float(kv4_any8(ks) << 23), f1 = __uint_as_float(kv4_any8(ks + 2u * G) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                kv4_mma(c, x0[0], x1[0], x0[1], x1[1], s->q[nt][g][0], s->q[nt][g][1]);
+                kv4_mma(c, x0[2], x1[2], x0[3], x1[3], s->q[nt][g][2], s->q[nt][g][3]);
+                sc[t][nt][0] = fmaf(c[0], f0, sc[t][nt][0]);
+                sc[t][nt][1] = fmaf(c[1], f0, sc[t][nt][1]);
+                sc[t][nt][2] = fmaf(c[2], f1, sc[t][nt][2]);
+                sc[t][nt][3] = fmaf(c[3], f1, sc[t][nt][3]);
+            }
+        }
+    }
+    /* weights, and for each row: whether it had weight before this page, the
+     * octaves that its reference rose and what that leaves of what is
+     * accumulated, its largest weight here */
+    float rise[NT][2], fall[NT][2];
+    bool before[NT][2], lost[NT][2]; /* lost: not a number */
+    int heavy[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const uint32_t key = 16u * t + k0 + 2u * h;
+                    float &x = sc[t][nt][r + 2 * h];
+                    x = key < nv && base + key < lim[nt][r] ? x * s->f[nt][r] : -INFINITY;
+                    mx = fmaxf(mx, x);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            const float m0 = s->m[nt][r], m = mx - 15.0f > m0 ? mx - 14.0f : m0;
+            const float alpha = kv4_ex2(m0 - m), l0 = s->l[nt][r];
+            before[nt][r] = kv4_max_keys(l0 != 0.0f) != 0;
+            lost[nt][r] = kv4_max_keys(l0 != l0) != 0;
+            rise[nt][r] = m - m0;
+            float l = l0 * alpha;
+            uint32_t top = 0;
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float &x = sc[t][nt][r + 2 * h];
+                    x = kv4_ex2(x - m);
+                    l += x;
+                    top = max(top, __float_as_uint(x) & 0x7FFFFFFFu);
+                }
+            heavy[nt][r] = kv4_log2((uint32_t)kv4_max_keys((int)top));
+            s->m[nt][r] = m;
+            s->l[nt][r] = l;
+            fall[nt][r] = alpha;
+        }
+#pragma unroll 1
+    for (uint32_t g = 0; g < G; g++) {
+        uint32_t b[2][2]; /* scale bytes of the lane's keys */
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t key = 16u * t + k0 + 2u * h;
+                b[t][h] = kv4_any8(pg + 33u * D + (key >> 2) * 4u * G + (key & 3u) + 4u * g);
+            }
+        int x[NT][2], cap = -NONE, top = NONE, like = NONE;
+        uint32_t pb[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            float w[2][4];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                int most = NONE, nan = 0;
+#pragma unroll
+                for (int t = 0; t < 2; t++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t key = 16u * t + k0 + 2u * h, p = __float_as_uint(sc[t][nt][r + 2 * h]);
+                        const bool see = key < nv && base + key < lim[nt][r];
+                        if (b[t][h] == 255u) nan |= see;
+                        else if (p != 0u && p < 0x7F800000u) most = max(most, kv4_log2(p) + (int)b[t][h]);
+                    }
+                x[nt][r] = most = kv4_max_keys(most);
+                if (kv4_max_keys(nan)) s->nan |= 1u << (2u * NT * g + 2u * nt + r);
+#pragma unroll
+                for (int t = 0; t < 2; t++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const float p = sc[t][nt][r + 2 * h];
+                        w[t][r + 2 * h] = b[t][h] == 255u ? 0.0f : (most == NONE ? p : kv4_shift(p, (int)b[t][h] - most + 14));
+                    }
+                /* the largest p 2^b that the row is known to have met is at
+                 * least 2^(E - 12) if the window was open, and 2^(x - 14) */
+                if (lim[nt][r] == 0u || lost[nt][r] || !(before[nt][r] || most != NONE)) continue;
+                const int old = before[nt][r] && (s->open >> g & 1u) ? (int)s->E[g] - (int)fminf(ceilf(rise[nt][r]), 4096.0f) : NONE;
+                cap = min(cap, max(old, most == NONE ? NONE : most - 2));
+                top = max(top, most);
+                if (most != NONE) like = max(like, most - heavy[nt][r]);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                pb[t][nt][0] = kv4_trans8x8(kv4_pack_h2(w[t][0], w[t][1]));
+                pb[t][nt][1] = kv4_trans8x8(kv4_pack_h2(w[t][2], w[t][3]));
+            }
+        }
+        float c[NT][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
             for (int u = 0; u < 2; u++)
 #pragma unroll
-                for (int c = 0; c < 4; c++) s.acc[nt][g][u][c] *= up;
+                for (int k = 0; k < 4; k++) c[nt][u][k] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            /* two neighbouring channels a byte: 16 bits of the word that holds groups g & ~1 and g | 1 */
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                v[k] = kv4_any32(pg + 16u * D + (uint32_t)t * 8u * D + lane * 8u * G + (k * (G / 2) + (g >> 1)) * 4u) >> (16u * (g & 1u));
+            uint32_t e01[4], o01[4], e23[4], o23[4];
+            kv4_decode4((v[0] & 0x0F0Fu) | ((v[1] << 4) & 0xF0F0u), e01);
+            kv4_decode4(((v[0] >> 4) & 0x0F0Fu) | (v[1] & 0xF0F0u), o01);
+            kv4_decode4((v[2] & 0x0F0Fu) | ((v[3] << 4) & 0xF0F0u), e23);
+            kv4_decode4(((v[2] >> 4) & 0x0F0Fu) | (v[3] & 0xF0F0u), o23);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                kv4_mma(c[nt][0], e01[0], o01[0], e23[0], o23[0], pb[t][nt][0], pb[t][nt][1]);
+                kv4_mma(c[nt][1], e01[1], o01[1], e23[1], o23[1], pb[t][nt][0], pb[t][nt][1]);
+            }
+        }
+        /* over the rows: the lanes j of each i */
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            cap = min(cap, __shfl_xor_sync(0xFFFFFFFFu, cap, o));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            like = max(like, __shfl_xor_sync(0xFFFFFFFFu, like, o));
+        }
+        float acc[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int k = 0; k < 4; k++) acc[nt][u][k] = s->acc[nt][g][u][k] * fall[nt][k & 1];
+        const int E = (int)s->E[g];
+        int unit = E;
+        if (top != NONE) {
+            /* accumulators of 2^-90 to 2^90 leave room for what follows */
+            uint32_t big = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const uint32_t a = __float_as_uint(acc[nt][k >> 2][k & 3]) & 0x7FFFFFFFu;
+                    big = max(big, a < 0x7F800000u ? a : 0u);
+                }
+            big = __reduce_max_sync(0xFFFFFFFFu, big);
+            int least = top - 74;
+            if (big != 0u) least = max(least, E + kv4_log2(big) - 90);
+            unit = min(like + 4, cap);
+            unit = min(max(unit < least ? max(E, least) : unit, 1), 300);
+            s->E[g] = (uint32_t)unit;
+            s->open = unit <= cap ? s->open | 1u << g : s->open & ~(1u << g);
+        }
+        const float2 old = kv4_pow2x2(E - unit);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const float2 add = kv4_pow2x2(x[nt][r] == NONE ? 0 : x[nt][r] - 14 - unit);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int u = k >> 1, v = r + 2 * (k & 1);
+                    s->acc[nt][g][u][v] = acc[nt][u][v] * old.x * old.y + c[nt][u][v] * add.x * add.y;
+                }
+            }
     }
+    kv4_window(*s);
+}
+
+/* The state in a copy, so that it stays in registers where this is not called;
+ * rows: the tile's query rows. */
+template <int G, int NT>
+DEV void kv4_page_rare(const unsigned char *pg, uint32_t base, uint32_t nv, uint32_t rows, Kv4State<G, NT> &s)
+{
+    Kv4State<G, NT> copy = s;
+    kv4_page_slow<G, NT>(pg, base, nv, rows, &copy);
+    s = copy;
+}
+/* Existing keys of the page that begins with key `base`. */
+DEV uint32_t kv4_existing(uint32_t base, uint32_t valid)
+{
+    return valid > base ? min(valid - base, (uint32_t)GPUOS_KV4_PAGE) : 0u;
 }
 
 /* One page: keys [base, base + 32) of the item, of which those below `valid`
  * exist (the rest of a request's last page holds anything). `scratch` (768
  * bytes of the warp's) passes the scales from the lane that converts a word
  * of them to the lanes that use them; without it (GLOBAL: the page is in
- * global memory, there is no staging) they pass by shuffles. */
+ * global memory, there is no staging) they pass by shuffles. False: nothing is
+ * done, the page has to go the slow way (kv4_page_rare). */
 template <int G, int NT, bool GLOBAL>
-DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base, uint32_t valid, Kv4State<G, NT> &s)
+DEV bool kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base, uint32_t valid, Kv4State<G, NT> &s)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
-    const uint32_t nv = valid > base ? min(valid - base, (uint32_t)GPUOS_KV4_PAGE) : 0u; /* existing keys of the page */
+    const uint32_t nv = kv4_existing(base, valid);
 
     /* ---- scales. Key scales: lane = key, G bytes -> G floats 2^(byte - 127)
      * (byte 0 gives 0: such a group's values are below 2^-124; 255 gives
      * infinity, and NaN with the zero codes that the write leaves beside it).
      * Value scales: lane = word ((key / 4) G + group) -> four f16, 2^(byte -
-     * E + 7): exponent field byte - E + 22, zero below 1. ---- */
+     * E): exponent field byte - E + 15, 3 to 15 for the bytes of the window;
+     * with any other byte the page goes the slow way. ---- */
     float kf[G];
     {
         const uint32_t w = G == 4 ? kv4_ld4<GLOBAL>(pg + 32u * D + 4u * lane)
@@ -472,15 +758,10 @@ DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
     {
         const uint32_t word = lane % (8u * G), key0 = word / G * 4u;
         uint32_t vw = kv4_ld4<GLOBAL>(pg + 33u * D + 4u * word);
-        if (nv < GPUOS_KV4_PAGE) vw &= kv4_keep(key0, nv);
-        const uint32_t top = __vimax_s16x2_relu(vw & 0x00FF00FFu, vw >> 8 & 0x00FF00FFu);
-        if (__any_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16) > s.El)) {
-            kv4_grow<G, NT>(base, key0, vw, s);
-            const uint32_t bias = (22u - s.El) & 0xFFFFu;
-            s.bias2 = bias | bias << 16;
-        }
-        vs.x = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4140), s.bias2, 0u) << 10;
-        vs.y = __viaddmax_s16x2(__byte_perm(vw, 0u, 0x4342), s.bias2, 0u) << 10;
+        if (nv < GPUOS_KV4_PAGE) vw = kv4_fill(vw, key0, nv, s);
+        if (kv4_outside(vw, s) && !kv4_fit<G, NT>(base, nv, key0, vw, s)) return false;
+        vs.x = __byte_perm(vw, 0u, 0x4140) * 1024u + s.factor;
+        vs.y = __byte_perm(vw, 0u, 0x4342) * 1024u + s.factor;
     }
     if (!GLOBAL) {
         __syncwarp(); /* the last page's readers are done */
@@ -556,9 +837,9 @@ DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
                 }
     }
 
-    /* ---- online softmax. Weights are 2^(score - m), m a reference 7 below
+    /* ---- online softmax. Weights are 2^(score - m), m a reference 14 below
      * the largest score when it was last set: it is set anew (and what is
-     * accumulated rescaled) only when a score comes 8 above it. ---- */
+     * accumulated rescaled) only when a score comes 15 above it. ---- */
     float high[NT][2];
     bool over = false;
 #pragma unroll
@@ -566,7 +847,7 @@ DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
 #pragma unroll
         for (int r = 0; r < 2; r++) {
             high[nt][r] = fmaxf(fmaxf(sc[0][nt][r], sc[0][nt][r + 2]), fmaxf(sc[1][nt][r], sc[1][nt][r + 2]));
-            over |= fmaf(high[nt][r], s.f[nt][r], -8.0f) > s.m[nt][r];
+            over |= fmaf(high[nt][r], s.f[nt][r], -15.0f) > s.m[nt][r];
         }
     if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
@@ -577,7 +858,7 @@ DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-                const float mn = fmaxf(s.m[nt][r], mx - 7.0f);
+                const float mn = fmaxf(s.m[nt][r], mx - 14.0f);
                 const float alpha = kv4_ex2(s.m[nt][r] - mn); /* 0 from the first reference, -FLT_MAX */
                 s.m[nt][r] = mn;
                 s.l[nt][r] *= alpha;
@@ -651,6 +932,7 @@ DEV void kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
             }
         }
     }
+    return true;
 }
 
 /* End of a run within an item: l summed over the lanes of a row, acc brought
@@ -672,8 +954,8 @@ DEV void kv4_finish(Kv4State<G, NT> &s)
         }
 #pragma unroll
         for (int g = 0; g < G; g++) {
-            /* 2^(E - 127 - 7) in two factors (E - 134 may be below -126) */
-            const int e = (int)s.E[g] - 134, e1 = e / 2;
+            /* 2^(E - 127) in two factors (E may be 0, or above 254) */
+            const int e = (int)s.E[g] - 127, e1 = e / 2;
             const float p2 = kv4_pow2(e - e1);
 #pragma unroll
             for (int c = 0; c < 4; c++) {
@@ -826,17 +1108,20 @@ DEV void kv4_part_merge(const Kv4Args &a, const Kv4Item &it, const float *left, 
     }
 }
 
-/* The pages of one run within an item, [begin, end): into the state. With
- * staging the pages arrive by bulk copies into the two halves of the warp's
- * buffer in turn. */
+/* The pages of one run within an item, [first, end): into the state, up to one
+ * that has to go the slow way; first is then that page, and end otherwise (the
+ * call that the slow way takes is the caller's: within this loop it cost 3 %).
+ * With staging the pages arrive by bulk copies into the two halves of the
+ * warp's buffer in turn. */
 template <int G, int NT>
-DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t begin, uint32_t end, Kv4State<G, NT> &s)
+DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t &first, uint32_t end, Kv4State<G, NT> &s)
 {
     constexpr uint32_t PB = kv4_page_bytes(32u * G);
     const uint32_t lane = lane_id(), h = p.h;
     const int32_t *row = a.table + (uint64_t)p.b * a.P;
     const uint64_t stride = (uint64_t)a.Hkv * PB;
     const unsigned char *pool = a.pool + (uint64_t)h * PB;
+    const uint32_t begin = first;
     const bool staged = stage_hdr()->stage_bytes >= 2u * PB + GPUOS_KV4_SCRATCH;
     WarpStage *w = warp_stage();
     unsigned char *buf = warp_stage_buf();
@@ -846,6 +1131,7 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t begin, uint32_t end,
      * stands for no keys (page 0 is read and masked) */
     const uint32_t n = end - begin;
     int32_t ids = 0, ids_next = 0;
+    first = end;
     auto load_ids = [&](uint32_t k) { return begin + k + lane < end ? __ldcg(row + begin + k + lane) : 0; };
     ids = load_ids(0);
     auto issue = [&](uint32_t k, int32_t id) {
@@ -885,7 +1171,15 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t begin, uint32_t end,
                 break;
             }
             phs ^= 1u << hb;
-            kv4_page<G, NT, false>(buf + hb * PB, buf + 2u * PB, base, valid, s);
+            if (!kv4_page<G, NT, false>(buf + hb * PB, buf + 2u * PB, base, valid, s)) {
+                first = begin + k;
+                if (k + 1 < n) { /* (the other half's copy is out) */
+                    if (!mbar_wait(&w->mbar[hb ^ 1u], phs >> (hb ^ 1u) & 1u) && !mbar_wait(&w->mbar[hb ^ 1u], phs >> (hb ^ 1u) & 1u))
+                        status = GPUOS_ST_COPY_TIMEOUT;
+                    phs ^= 1u << (hb ^ 1u);
+                }
+                break;
+            }
             if (k + 2 < n) {
                 const int32_t nx = (k & 31u) < 30u ? __shfl_sync(0xFFFFFFFFu, ids, (k + 2) & 31u)
                                                    : __shfl_sync(0xFFFFFFFFu, ids_next, (k + 2) & 31u);
@@ -894,7 +1188,10 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t begin, uint32_t end,
                 issue(k + 2, nx);
             }
         } else {
-            kv4_page<G, NT, true>(pool + (uint64_t)(there ? (uint32_t)id : 0u) * stride, nullptr, base, valid, s);
+            if (!kv4_page<G, NT, true>(pool + (uint64_t)(there ? (uint32_t)id : 0u) * stride, nullptr, base, valid, s)) {
+                first = begin + k;
+                break;
+            }
         }
     }
     if (staged) {
@@ -949,8 +1246,17 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
             Kv4Query<G, NT> qx;
             kv4_load_q(a, p, qx);
             kv4_begin(a, p, qx, s);
-            const int st = p.len ? kv4_run(a, p, begin, end, s) : GPUOS_ST_OK;
-            if (st) status = st;
+#pragma unroll 1
+            for (uint32_t at = begin; p.len && at < end;) {
+                const int st = kv4_run(a, p, at, end, s);
+                if (st) status = st;
+                if (at < end) {
+                    const uint32_t id = (uint32_t)__ldcg(a.table + (uint64_t)p.b * a.P + at), base = at * GPUOS_KV4_PAGE;
+                    kv4_page_rare(a.pool + ((uint64_t)(id < a.npages ? id : 0u) * a.Hkv + p.h) * kv4_page_bytes(32u * G), base,
+                                  kv4_existing(base, id < a.npages ? (uint32_t)p.len : 0u), a.T * a.g - p.r0, s);
+                    at++;
+                }
+            }
             kv4_finish(s);
             if (begin != 0 || end != p.np) {
                 const uint32_t first = runs.run_of(p.first);
@@ -1512,7 +1818,8 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 const uint32_t base = (begin + k) * GPUOS_KV4_PAGE;
                 const uint32_t valid = (uint32_t)id < a.npages ? (uint32_t)p.len : 0u;
                 (void)mbar_wait(&bars[warp][slot], parity); /* bounded, like every wait */
-                kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, s);
+                if (!kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, s))
+                    kv4_page_rare(mine + slot * PB, base, kv4_existing(base, valid), a.T * a.g - p.r0, s);
                 if (k + NS < n) {
                     const uint32_t kn = k + NS;
                     const int32_t nx = __shfl_sync(0xFFFFFFFFu, kn >> 5 != k >> 5 ? ids_next : ids, kn & 31u);
@@ -1580,7 +1887,11 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         for (uint32_t o = 8u * NT; o < 32u; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
         if (q == 0) {
             weight[k][warp][r] = l != 0.0f ? me.y * kv4_ex2(me.x - M) / l : 0.0f;
-            total[k][warp][r] = make_float2(M, l);
+            /* 2^-46: a weight is 2^15 at most and the keys are 2^31, so that
+             * the blocks' sum of values under such weights stays in fp32
+             * where the values do (scaled here, not there: that code runs
+             * cold, and one more instruction in its loop cost 0.3 to 1 us) */
+            total[k][warp][r] = make_float2(M, l * 0x1p-46f);
         }
     }
     __syncthreads();
