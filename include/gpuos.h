@@ -125,7 +125,9 @@ enum {
                                2^-25 of what weighs most in the row (weight times value, by groups of
                                32 channels), however far apart the values' sizes are and whatever
                                keys that the query does not see hold; below 2^-140 of the largest it
-                               is nothing. aux2 = workspace of GPUOS_KV4_WORKSPACE
+                               is nothing. Scores are held in fp32, a query channel to 2^-18 of the
+                               largest of its 32. A score or output beyond fp32 gives NaN or an
+                               infinity. aux2 = workspace of GPUOS_KV4_WORKSPACE
                                bytes (below); dims = {B, H | Hkv << 16, D | T << 16, P, npages},
                                T <= 32, H % Hkv == 0; fparam[0] = scale */
     GPUOS_OP_PAGE_COPY = 17, /* a[l][dst] = a[l][src] for the pairs aux0 = i32[n][2] of {src, dst}

@@ -34,6 +34,7 @@
 #include <atomic>
 
 #define GPUOS_KV4_SCRATCH 768u /* bytes of a warp's converted scales */
+#define GPUOS_KV4_WIDE 0x80000000u
 
 DEV constexpr uint32_t kv4_page_bytes(uint32_t D) { return 34u * D; }
 
@@ -113,21 +114,24 @@ DEV float kv4_ex2(float x)
  * its neighbours' (below).
  *
  * Numerics. q is scaled by a power of two for each row to [128, 256) and held
- * in f16: exact for the bf16 values within 2^-21 of the row's largest, and
- * off by at most 2^-32 of it below. Codes are exact in f16; the products are
- * summed in fp32 for each scale group, and the groups' sums are scaled and
- * added in fp32. Weights p, the largest 2^14 to 2^15, are rounded to f16 (11
- * bits; bf16's 8 would show in a bf16 output; one 2^-28 of the largest still
- * has them all) and multiplied there by 2^(b - E), b the value's scale byte
- * and E a byte of the group's choosing, which is also the accumulators' unit.
- * A page is taken that way only if E - 12 <= b <= E for all its keys. Then
- * the product is off by 2^-25 at most where it is not exact, and the key that
- * set the softmax's reference weighs 2^14 with b >= E - 12: what is lost is
- * 6 * 2^-27 of the largest p 2^b that the row has met, for each key, whatever
- * the other rows and the hidden keys hold. Any other page (kv4_page_slow)
- * multiplies p 2^(b - x) in fp32, x the row's own largest p 2^b in the page,
- * before it rounds to f16, and sets E anew.
- * The softmax's reference and sum and the output accumulators are fp32.
+ * in f16: exact for the bf16 values within 2^-21 of the row's largest, and off
+ * by at most 2^-32 of it below. If a group of 32 channels has its largest
+ * 2^14 below the row's, every page goes the slow way (below), where each group
+ * has a power of its own; what is lost is 2^-18 of a group's largest at most.
+ * Codes are exact in f16; the products are summed in fp32 for each scale
+ * group, and the groups' sums are scaled and added in fp32. Weights p, the
+ * largest 2^14 to 2^15, are rounded to f16 (11 bits; bf16's 8 would show in a
+ * bf16 output; one 2^-28 of the largest still has them all) and multiplied
+ * there by 2^(b - E), b the value's scale byte and E a byte of the group's
+ * choosing, which is also the accumulators' unit. A page is taken that way
+ * only if E - 12 <= b <= E for all its keys. Then the product is off by 2^-25
+ * at most where it is not exact, and the key that set the softmax's reference
+ * weighs 2^14 with b >= E - 12: what is lost is 6 * 2^-27 of the largest p 2^b
+ * that the row has met, for each key, whatever the other rows and the hidden
+ * keys hold. Any other page goes the slow way (kv4_page_slow): it multiplies
+ * p 2^(b - x) in fp32, x the row's own largest p 2^b in the page, before it
+ * rounds to f16, and sets E anew. The softmax's reference and sum and the
+ * output accumulators are fp32.
  * ------------------------------------------------------------------------- */
 struct Kv4Args {
     const uint16_t *q;
@@ -294,7 +298,8 @@ struct Kv4State {
     float l[NT][2];       /* this lane's part of the running sum */
     float acc[NT][G][2][4];
     uint32_t E[G]; /* the unit of each group's accumulators: 2^(E - 127) */
-    uint32_t open; /* bit g: group g's window of scales is in use (a row may have no weight that bears it out) */
+    uint32_t open; /* bit g: group g's window of scales is in use (a row may have no weight that bears it out);
+                      GPUOS_KV4_WIDE: none is, whatever the other bits say */
     uint32_t nlo, factor; /* of group lane % G: 12 - E in both halves (closed: no byte passes); 15 - E in both f16 exponents */
     uint32_t nan; /* bit 2 NT g + 2 nt + c: row (nt, c) saw a NaN among group g's values */
     uint32_t lim[NT][2]; /* keys that the row sees */
@@ -317,11 +322,23 @@ DEV void kv4_window(Kv4State<G, NT> &s)
     uint32_t e = s.E[0];
 #pragma unroll
     for (int g = 1; g < G; g++) e = mine == (uint32_t)g ? s.E[g] : e;
-    const uint32_t lo = s.open >> mine & 1u ? (12u - e) & 0xFFFFu : 0x4000u;
+    const uint32_t lo = s.open >> mine & ~(s.open / GPUOS_KV4_WIDE) & 1u ? (12u - e) & 0xFFFFu : 0x4000u;
     s.nlo = lo | lo << 16;
     s.factor = (15u - e) * 0x04000400u;
 }
 
+/* Where the lane's part of a tile's query row begins (channel 8 j); null
+ * behind the last row. */
+template <int G>
+DEV const uint16_t *kv4_q_row(const Kv4Args &a, const Kv4Pos &p, uint32_t row)
+{
+    const uint32_t r = p.r0 + row;
+    uint32_t t, hh;
+    kv4_token(a, r, t, hh);
+    return r < a.T * a.g
+               ? a.q + (((uint64_t)p.b * a.T + t) * a.H + (uint64_t)p.h * a.g + hh) * (32u * G) + 8u * (lane_id() & 3u)
+               : nullptr;
+}
 /* The item's query rows, as they lie in memory. */
 template <int G, int NT>
 struct Kv4Query {
@@ -350,24 +367,38 @@ template <int G, int NT>
 DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx, Kv4State<G, NT> &s)
 {
     const uint32_t j = lane_id() & 3u, r0 = p.r0;
+    bool wide = false;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
         const uint4(&raw)[G] = qx.raw[nt];
-        /* the largest magnitude, as bf16 bits: those of positive numbers are
-         * in order, infinity and NaN (the row is left as it is) on top */
-        uint32_t w = 0;
+        /* each group's largest magnitude (two groups a word), as bf16 bits:
+         * those of positive numbers are in order, infinity and NaN (the row
+         * is left as it is) on top */
+        uint32_t w = 0, least = 0xFFFFFFFFu; /* (less one, so that an empty group is the most) */
 #pragma unroll
-        for (int g = 0; g < G; g++)
-            w = __vmaxu2(w, __vmaxu2(__vmaxu2(raw[g].x & 0x7FFF7FFFu, raw[g].y & 0x7FFF7FFFu),
-                                     __vmaxu2(raw[g].z & 0x7FFF7FFFu, raw[g].w & 0x7FFF7FFFu)));
+        for (int g = 0; g < G; g += 2) {
+            uint32_t m[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                m[h] = __vmaxu2(__vmaxu2(raw[g + h].x & 0x7FFF7FFFu, raw[g + h].y & 0x7FFF7FFFu),
+                                __vmaxu2(raw[g + h].z & 0x7FFF7FFFu, raw[g + h].w & 0x7FFF7FFFu));
+            uint32_t top = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+            top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            w = __vmaxu2(w, top);
+            least = __viaddmin_u16x2(top, 0xFFFFFFFFu, least);
+        }
         w = max(w & 0xFFFFu, w >> 16);
-        w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1));
-        w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 2));
+        least = min(least & 0xFFFFu, least >> 16) + 1u;
         /* k: the largest times 2^-k is in [128, 256); both 2^k and 2^-k stay normal numbers */
         const int k = w == 0 || w >= 0x7F80u ? 0 : max(-126, (int)(w >> 7) - 127 - 7);
         /* the factor stays positive: a negative scale turns q, one of zero
-         * (or a product with 2^k below every number) empties it */
+         * empties it */
         float down = kv4_pow2(-k), f = fabsf(a.scale) * kv4_pow2(k);
+        /* a group 2^14 below the largest has lost bits in f16, a factor that
+         * is no normal number has too, and under a large one the least keys
+         * count: every page goes the slow way */
+        wide |= least + (14u << 7) < w || ((f < FLT_MIN || f > 0x1p80f) && a.scale != 0.0f);
         if (a.scale < 0.0f) down = -down;
         if (f == 0.0f) {
             down = 0.0f;
@@ -397,7 +428,7 @@ DEV void kv4_begin(const Kv4Args &a, const Kv4Pos &p, const Kv4Query<G, NT> &qx,
 #pragma unroll
     for (int g = 0; g < G; g++) s.E[g] = 0;
     s.nan = 0;
-    s.open = (1u << G) - 1u;
+    s.open = __any_sync(0xFFFFFFFFu, wide) ? GPUOS_KV4_WIDE : (1u << G) - 1u;
     kv4_window(s);
     s.min_lim = kv4_row_limit(a, p.len, r0); /* rows come in order of t */
 }
@@ -441,7 +472,7 @@ DEV int kv4_log2(uint32_t bits) { return (int)(bits >> 23) - 127; }
  * never from L1, which other ops' writes pass by). */
 DEV uint32_t kv4_any32(const unsigned char *p) { return *reinterpret_cast<const volatile uint32_t *>(p); }
 DEV uint32_t kv4_any8(const unsigned char *p) { return *reinterpret_cast<const volatile unsigned char *>(p); }
-/* Largest (least) of the lanes that hold a row's keys; of all rows. */
+/* Largest of the lanes that hold a row's keys. */
 DEV int kv4_max_keys(int x)
 {
     x = max(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
@@ -457,22 +488,24 @@ DEV uint32_t kv4_fill(uint32_t vw, uint32_t key0, uint32_t nv, const Kv4State<G,
     const uint32_t keep = kv4_keep(key0, nv);
     return (vw & keep) | (min(12u - (uint32_t)(int)(int16_t)s.nlo, 255u) * 0x01010101u & ~keep);
 }
-/* Does any lane's word hold a byte outside E - 12 .. E? (The larger of byte -
- * (E - 12), mod 2^16, and 12, is 12 for the others.) */
+/* Does any lane's word hold a byte outside E - 12 .. E (the larger of byte -
+ * (E - 12), mod 2^16, and 12, is 12 for the others), or its key a scale too
+ * large (far)? */
 template <int G, int NT>
-DEV bool kv4_outside(uint32_t vw, const Kv4State<G, NT> &s)
+DEV bool kv4_outside(uint32_t vw, uint32_t far, const Kv4State<G, NT> &s)
 {
     const uint32_t lo = __viaddmax_u16x2(__byte_perm(vw, 0u, 0x4140), s.nlo, 0x000C000Cu);
-    return __any_sync(0xFFFFFFFFu, __viaddmax_u16x2(__byte_perm(vw, 0u, 0x4342), s.nlo, lo) != 0x000C000Cu);
+    const uint32_t x = __viaddmax_u16x2(__byte_perm(vw, 0u, 0x4342), s.nlo, lo) ^ 0x000C000Cu;
+    return __any_sync(0xFFFFFFFFu, (x | far) != 0u);
 }
 
 /* A page holds value scales outside its groups' windows (vw: the lane's word
- * of them). Before the first weight the windows are free: each is laid four
- * octaves above the largest scale of the keys that every row sees (of all
- * keys, where that is none), and its twelve octaves hold most pages. False if
- * the page does not fit all the same. */
+ * of them), or key scales too large (far). Before the first weight the windows
+ * are free: each is laid four octaves above the largest scale of the keys that
+ * every row sees (of all keys, where that is none), and its twelve octaves
+ * hold most pages. False if the page does not fit all the same. */
 template <int G, int NT>
-DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, Kv4State<G, NT> &s)
+DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, uint32_t far, Kv4State<G, NT> &s)
 {
     float any = 0.0f;
 #pragma unroll
@@ -489,23 +522,27 @@ DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, Kv4Sta
     }
     kv4_window(s);
     vw = kv4_fill(vw, key0, nv, s);
-    return !kv4_outside(vw, s);
+    return !kv4_outside(vw, far, s);
 }
 
 /* A page whose value scales lie too far apart, or too far from what the rows
- * have met, for weights in f16 under one unit: as kv4_page, but each row's
- * products p 2^b are formed in fp32 and rounded to f16 against their own
- * largest, 2^x. Then the window of scales is laid anew: four octaves above
- * the scale of what the page's heaviest keys hold, but never so high that its
- * unit is more than 2^12 above what some row has weighed (cap), because that
- * is what bounds the error of the pages that follow; if the accumulators'
- * range asks for more, the window is closed and every page comes here. (Rows
- * of one tile that heed values more than 2^150 apart in one group: the smaller
- * are lost.) A call whose every page comes here took 603 us instead of 80 (64
+ * have met, for weights in f16 under one unit, or whose keys are so large that
+ * their products with a query scaled to 128 may leave fp32 although the scores
+ * do not, or a query whose groups lie far apart (s->q[nt][0] says where it
+ * lies): as kv4_page, but each group of a query row has its own power of
+ * two, which meets the key's scale and the factor's in one exponent, and each
+ * row's products p 2^b are formed in fp32 and rounded to f16 against their own
+ * largest, 2^x. Then the window of scales is laid anew: four octaves above the
+ * scale of what the page's heaviest keys hold, but never so high that its unit
+ * is more than 2^12 above what some row has weighed (cap), because that is
+ * what bounds the error of the pages that follow; if the accumulators' range
+ * asks for more, the window is closed and every page comes here. (Rows of one
+ * tile that heed values more than 2^150 apart in one group: the smaller are
+ * lost.) A call whose every page comes here took 740 us instead of 81 (64
  * requests of 2,000 to 16,383 tokens, scales random over 40 octaves); out of
  * line, so that the common path keeps its registers. */
 template <int G, int NT>
-__device__ __noinline__ void kv4_page_slow(const unsigned char *pg, uint32_t base, uint32_t nv, uint32_t rows, Kv4State<G, NT> *s)
+__device__ __noinline__ void kv4_page_slow(const unsigned char *pg, uint32_t base, uint32_t nv, uint32_t rows, float scale, Kv4State<G, NT> *s)
 {
     constexpr uint32_t D = 32u * G;
     constexpr int NONE = -100000;
@@ -522,25 +559,53 @@ __device__ __noinline__ void kv4_page_slow(const unsigned char *pg, uint32_t bas
 #pragma unroll
             for (int c = 0; c < 4; c++) sc[t][nt][c] = 0.0f;
     }
+    const uint16_t *row[NT];
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
+    for (int nt = 0; nt < NT; nt++)
+        row[nt] = reinterpret_cast<const uint16_t *>((uint64_t)s->q[nt][0][1] << 32 | s->q[nt][0][0]);
+    /* scale = rest 2^es; an infinity or NaN is all rest, zero all exponent */
+    const uint32_t sb = __float_as_uint(scale) & 0x7FFFFFFFu;
+    const int es = sb == 0u ? -4096 : (sb >= 0x7F800000u ? 0 : max(kv4_log2(sb), -126));
+    const float rest = sb == 0u ? 1.0f : scale * kv4_pow2(-max(es, -126));
 #pragma unroll 1
-        for (uint32_t g = 0; g < G; g++) {
+    for (uint32_t g = 0; g < G; g++) {
+        uint32_t q[NT][4];
+        int kg[NT][2]; /* of rows 2 j, 2 j + 1 */
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const uint4 raw = row[nt] ? __ldcg(reinterpret_cast<const uint4 *>(row[nt] + 32u * g)) : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+            uint32_t w = 0;
+#pragma unroll
+            for (int c = 0; c < 4; c++) w = __vmaxu2(w, x[c] & 0x7FFF7FFFu);
+            w = max(w & 0xFFFFu, w >> 16);
+            w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1));
+            w = max(w, __shfl_xor_sync(0xFFFFFFFFu, w, 2));
+            const int k = w == 0 || w >= 0x7F80u ? 0 : max(-126, (int)(w >> 7) - 127 - 7);
+            const float down = kv4_pow2(-k);
+#pragma unroll
+            for (int c = 0; c < 4; c++) q[nt][c] = kv4_pack_h2(bf_lo(x[c]) * down, bf_hi(x[c]) * down);
+            kg[nt][0] = __shfl_sync(0xFFFFFFFFu, k, 8 * j) + es - 127;
+            kg[nt][1] = __shfl_sync(0xFFFFFFFFu, k, 8 * j + 4) + es - 127;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
             const unsigned char *kp = pg + (uint32_t)t * 8u * D + lane * 8u * G + 4u * g;
             const unsigned char *ks = pg + 32u * D + (16u * t + k0) * G + g;
             uint32_t x0[4], x1[4];
             kv4_decode4(kv4_any32(kp), x0);
             kv4_decode4(kv4_any32(kp + 4u * G), x1);
-            const float f0 = __uint_as_float(kv4_any8(ks) << 23), f1 = __uint_as_float(kv4_any8(ks + 2u * G) << 23);
+            const uint32_t b[2] = {kv4_any8(ks), kv4_any8(ks + 2u * G)};
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
                 float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                kv4_mma(c, x0[0], x1[0], x0[1], x1[1], s->q[nt][g][0], s->q[nt][g][1]);
-                kv4_mma(c, x0[2], x1[2], x0[3], x1[3], s->q[nt][g][2], s->q[nt][g][3]);
-                sc[t][nt][0] = fmaf(c[0], f0, sc[t][nt][0]);
-                sc[t][nt][1] = fmaf(c[1], f0, sc[t][nt][1]);
-                sc[t][nt][2] = fmaf(c[2], f1, sc[t][nt][2]);
-                sc[t][nt][3] = fmaf(c[3], f1, sc[t][nt][3]);
+                kv4_mma(c, x0[0], x1[0], x0[1], x1[1], q[nt][0], q[nt][1]);
+                kv4_mma(c, x0[2], x1[2], x0[3], x1[3], q[nt][2], q[nt][3]);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float2 f = kv4_pow2x2((int)b[k >> 1] + kg[nt][k & 1]);
+                    sc[t][nt][k] += b[k >> 1] == 255u ? NAN : c[k] * f.x * f.y;
+                }
             }
         }
     }
@@ -561,7 +626,7 @@ __device__ __noinline__ void kv4_page_slow(const unsigned char *pg, uint32_t bas
                 for (int h = 0; h < 2; h++) {
                     const uint32_t key = 16u * t + k0 + 2u * h;
                     float &x = sc[t][nt][r + 2 * h];
-                    x = key < nv && base + key < lim[nt][r] ? x * s->f[nt][r] : -INFINITY;
+                    x = key < nv && base + key < lim[nt][r] ? x * rest : -INFINITY;
                     mx = fmaxf(mx, x);
                 }
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
@@ -713,13 +778,24 @@ __device__ __noinline__ void kv4_page_slow(const unsigned char *pg, uint32_t bas
     kv4_window(*s);
 }
 
-/* The state in a copy, so that it stays in registers where this is not called;
- * rows: the tile's query rows. */
+/* The state in a copy, so that it stays in registers where this is not called. */
 template <int G, int NT>
-DEV void kv4_page_rare(const unsigned char *pg, uint32_t base, uint32_t nv, uint32_t rows, Kv4State<G, NT> &s)
+DEV void kv4_page_rare(const Kv4Args &a, const Kv4Pos &p, const unsigned char *pg, uint32_t base, uint32_t nv, Kv4State<G, NT> &s)
 {
     Kv4State<G, NT> copy = s;
-    kv4_page_slow<G, NT>(pg, base, nv, rows, &copy);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) { /* (the page's path reads the query itself) */
+        const uint64_t at = (uint64_t)kv4_q_row<G>(a, p, 8u * nt + (lane_id() >> 2));
+        copy.q[nt][0][0] = (uint32_t)at;
+        copy.q[nt][0][1] = (uint32_t)(at >> 32);
+    }
+    kv4_page_slow<G, NT>(pg, base, nv, a.T * a.g - p.r0, a.scale, &copy);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) copy.q[nt][g][c] = s.q[nt][g][c];
     s = copy;
 }
 /* Existing keys of the page that begins with key `base`. */
@@ -742,24 +818,28 @@ DEV bool kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
     const uint32_t nv = kv4_existing(base, valid);
 
     /* ---- scales. Key scales: lane = key, G bytes -> G floats 2^(byte - 127)
-     * (byte 0 gives 0: such a group's values are below 2^-124; 255 gives
-     * infinity, and NaN with the zero codes that the write leaves beside it).
+     * (byte 0 gives 0: with a factor up to 2^80 such a group would add 2^-30
+     * to a score). Above 191 (255 among them) the page goes the slow way;
+     * below, a sum of D products with queries up to 256 stays under 2^82.
      * Value scales: lane = word ((key / 4) G + group) -> four f16, 2^(byte -
      * E): exponent field byte - E + 15, 3 to 15 for the bytes of the window;
      * with any other byte the page goes the slow way. ---- */
     float kf[G];
+    uint32_t far;
     {
         const uint32_t w = G == 4 ? kv4_ld4<GLOBAL>(pg + 32u * D + 4u * lane)
                                   : kv4_ld4<GLOBAL>(pg + 32u * D + 4u * (lane >> 1)) >> (16u * (lane & 1u));
 #pragma unroll
-        for (int g = 0; g < G; g++) kf[g] = __uint_as_float((g < 3 ? w << (23 - 8 * g) : w >> 1) & 0x7F800000u);
+        for (int g = 0; g < G; g++)
+            kf[g] = __uint_as_float((g < 3 ? w << (23 - 8 * g) : w >> 1) & 0x7F800000u);
+        far = lane < nv ? w & w << 1 & (G == 4 ? 0x80808080u : 0x8080u) : 0u;
     }
     uint2 vs;
     {
         const uint32_t word = lane % (8u * G), key0 = word / G * 4u;
         uint32_t vw = kv4_ld4<GLOBAL>(pg + 33u * D + 4u * word);
         if (nv < GPUOS_KV4_PAGE) vw = kv4_fill(vw, key0, nv, s);
-        if (kv4_outside(vw, s) && !kv4_fit<G, NT>(base, nv, key0, vw, s)) return false;
+        if (kv4_outside(vw, far, s) && !kv4_fit<G, NT>(base, nv, key0, vw, far, s)) return false;
         vs.x = __byte_perm(vw, 0u, 0x4140) * 1024u + s.factor;
         vs.y = __byte_perm(vw, 0u, 0x4342) * 1024u + s.factor;
     }
@@ -1252,8 +1332,8 @@ DEV int kv4_sdpa_tile(const gpuos_devdesc *d, uint32_t tile)
                 if (st) status = st;
                 if (at < end) {
                     const uint32_t id = (uint32_t)__ldcg(a.table + (uint64_t)p.b * a.P + at), base = at * GPUOS_KV4_PAGE;
-                    kv4_page_rare(a.pool + ((uint64_t)(id < a.npages ? id : 0u) * a.Hkv + p.h) * kv4_page_bytes(32u * G), base,
-                                  kv4_existing(base, id < a.npages ? (uint32_t)p.len : 0u), a.T * a.g - p.r0, s);
+                    kv4_page_rare(a, p, a.pool + ((uint64_t)(id < a.npages ? id : 0u) * a.Hkv + p.h) * kv4_page_bytes(32u * G), base,
+                                  kv4_existing(base, id < a.npages ? (uint32_t)p.len : 0u), s);
                     at++;
                 }
             }
@@ -1808,18 +1888,9 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 if (k < n) issue(slot + k < NS ? slot + k : slot + k - NS, id);
             }
             kv4_begin(a, p, qx, s);
-#pragma unroll 1
-            for (uint32_t k = 0; k < n; k++) {
-                if ((k & 31u) == 0) {
-                    if (k) ids = ids_next;
-                    ids_next = k + 32u + lane < n ? __ldcg(row + k + 32u + lane) : 0;
-                }
-                const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k & 31u);
-                const uint32_t base = (begin + k) * GPUOS_KV4_PAGE;
-                const uint32_t valid = (uint32_t)id < a.npages ? (uint32_t)p.len : 0u;
-                (void)mbar_wait(&bars[warp][slot], parity); /* bounded, like every wait */
-                if (!kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, s))
-                    kv4_page_rare(mine + slot * PB, base, kv4_existing(base, valid), a.T * a.g - p.r0, s);
+            uint32_t k = 0;
+            /* the page's slot takes the next page but one */
+            auto follow = [&]() {
                 if (k + NS < n) {
                     const uint32_t kn = k + NS;
                     const int32_t nx = __shfl_sync(0xFFFFFFFFu, kn >> 5 != k >> 5 ? ids_next : ids, kn & 31u);
@@ -1830,6 +1901,29 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                 if (++slot == NS) {
                     slot = 0;
                     parity ^= 1u;
+                }
+                k++;
+            };
+#pragma unroll 1
+            while (k < n) { /* (the slow way's call stands outside the loop over pages: 2 % of the batch case) */
+                uint32_t base, valid;
+                bool done;
+#pragma unroll 1
+                do {
+                    if ((k & 31u) == 0) {
+                        if (k) ids = ids_next;
+                        ids_next = k + 32u + lane < n ? __ldcg(row + k + 32u + lane) : 0;
+                    }
+                    const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k & 31u);
+                    base = (begin + k) * GPUOS_KV4_PAGE;
+                    valid = (uint32_t)id < a.npages ? (uint32_t)p.len : 0u;
+                    (void)mbar_wait(&bars[warp][slot], parity); /* bounded, like every wait */
+                    done = kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, s);
+                    if (done) follow();
+                } while (done && k < n);
+                if (!done) {
+                    kv4_page_rare(a, p, mine + slot * PB, base, kv4_existing(base, valid), s);
+                    follow();
                 }
             }
             kv4_finish(s);

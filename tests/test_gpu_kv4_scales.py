@@ -224,3 +224,72 @@ def test_nan_groups_among_far_scales(run):
     got = _attend(RUNNERS[run], q, pool, table, lens, 0.125)
     assert np.array_equal(np.isnan(got), nan)
     _close(got[~nan], want[~nan], tol[~nan])
+
+
+@pytest.mark.parametrize("run", WAYS)
+@pytest.mark.parametrize("T,H", [(1, 4), (2, 24)])
+@pytest.mark.parametrize("up", [60, 66, 100, 112, 118])
+@pytest.mark.parametrize("scale", [1.0, 0.125, 0.001])
+def test_large_keys_under_small_queries(run, T, H, up, scale):
+    """Keys 2^up times their common size, queries 2^-up times theirs: scores
+    of order one, as they are without."""
+    D = 64
+    q, pool, table, lens = _attend_case(41, 3, H, 1, D, T, [70, 33, 1 + T])
+    was = pool[:, :, 32 * D:33 * D].astype(int)
+    pool[:, :, 32 * D:33 * D] = (was + up).clip(0, 252)
+    q = R.bf16(q * 2.0 ** -up / scale * 0.125)
+    want, tol = _want(q, pool, table, lens, scale)
+    assert 0.01 < np.abs(want).max() < 100
+    _check(run, q, pool, table, lens, scale)
+
+
+@pytest.mark.parametrize("run", WAYS)
+@pytest.mark.parametrize("byte", [0, 1, 9])
+def test_small_keys_under_large_queries(run, byte):
+    """Key scales from 2^-127 on: a code of them is not zero."""
+    D = 64
+    q, pool, table, lens = _attend_case(43, 2, 4, 2, D, 1, [70, 33])
+    pool[:, :, 32 * D:33 * D] = byte
+    q = R.bf16(q * 2.0 ** 120)
+    K, _, _ = R.unpack(pool)
+    scale = 2.0 ** (7 - byte)
+    x = K[table[0, 0], 0] @ q[0, 0, 0] * scale
+    assert 2 < np.abs(x).max() < 60
+    _check(run, q, pool, table, lens, scale)
+
+
+@pytest.mark.parametrize("run", WAYS)
+def test_key_sizes_apart(run):
+    """One group of every key is 2^90 times the others, under query channels
+    that are small there; some keys in pages of common ones."""
+    D = 64
+    q, pool, table, lens = _attend_case(47, 2, 4, 1, D, 1, [100, 300])
+    q[..., 32:] *= 2.0 ** -90
+    q = R.bf16(q)
+    for b, n in enumerate(lens):
+        for at in range(5, n, 7):
+            ks = R.offsets(D, at % 32, 32)[2]
+            pool[table[b, at // 32], 0, ks] += 90
+    _check(run, q, pool, table, lens, 0.125)
+
+
+@pytest.mark.parametrize("run", WAYS)
+@pytest.mark.parametrize("code", [0, 1, 7, 9, 15])
+def test_key_scale_of_nan_beside_any_code(run, code):
+    """A key scale of 255 is NaN whatever the codes are, for the rows that see
+    the key; behind the last key it is nothing."""
+    D, T = 64, 2
+    q, pool, table, lens = _attend_case(53, 3, 4, 2, D, T, [40, 50, 70])
+    clean = pool.copy()
+    for page, key, h in ((table[0, 1], 39 - 32, 0), (table[1, 0], 4, 1), (table[2, 2], 70 - 64, 0)):
+        k, _, ks, _ = R.offsets(D, key, np.arange(32))
+        pool[page, h, k] = code | code << 4
+        pool[page, h, ks] = 255
+        clean[page, h, k], clean[page, h, ks] = 0, 127
+    want, tol = _want(q, clean, table, lens, 0.125)
+    nan = np.zeros(q.shape, bool)
+    nan[0, 1, :2] = True  # the last key: the last token alone sees it
+    nan[1, :, 2:] = True
+    got = _attend(RUNNERS[run], q, pool, table, lens, 0.125)
+    assert np.array_equal(np.isnan(got), nan)
+    _close(got[~nan], want[~nan], tol[~nan])
