@@ -1882,6 +1882,10 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                     bulk_g2s(mine + at * PB, pool + ((uint32_t)id < a.npages ? (uint32_t)id : 0u) * stride, PB, &bars[warp][at]);
                 }
             };
+            /* every lane is done with the last item's pages, whose slots these
+             * copies take (ordinary reads, then asynchronous writes) */
+            __syncwarp();
+            if (lane == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
             for (uint32_t k = 0; k < NS; k++) {
                 const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k);
