@@ -521,7 +521,9 @@ GPUOS_API size_t gpuos_kv4_pool_bytes(uint32_t npages, uint32_t Hkv, uint32_t D)
  * launch kernels of their own (attention: at most one block per SM; the others:
  * four of the rule's tiles a block), do not use stage_bytes, and may be given their
  * SMs as the stream's previous kernel ends: they wait on the device until its writes
- * are visible. Deps are implied by stream order. Does not synchronize. Errors: EINVAL (as gpuos_submit),
+ * are visible. A launch has no status: where the executor would report one, entries
+ * are skipped alike, and attention whose copy of a page does not land in time gives
+ * NaN. Deps are implied by stream order. Does not synchronize. Errors: EINVAL (as gpuos_submit),
  * ECUDA. */
 GPUOS_API int gpuos_eager_run(const gpuos_desc *d, uint32_t count, uint32_t stage_bytes, void *stream);
 

@@ -490,13 +490,13 @@ DEV uint32_t kv4_fill(uint32_t vw, uint32_t key0, uint32_t nv, const Kv4State<G,
 }
 /* Does any lane's word hold a byte outside E - 12 .. E (the larger of byte -
  * (E - 12), mod 2^16, and 12, is 12 for the others), or its key a scale too
- * large (far)? */
+ * large (far), or has the page not come for it (here)? */
 template <int G, int NT>
-DEV bool kv4_outside(uint32_t vw, uint32_t far, const Kv4State<G, NT> &s)
+DEV bool kv4_outside(uint32_t vw, uint32_t far, bool here, const Kv4State<G, NT> &s)
 {
     const uint32_t lo = __viaddmax_u16x2(__byte_perm(vw, 0u, 0x4140), s.nlo, 0x000C000Cu);
     const uint32_t x = __viaddmax_u16x2(__byte_perm(vw, 0u, 0x4342), s.nlo, lo) ^ 0x000C000Cu;
-    return __any_sync(0xFFFFFFFFu, (x | far) != 0u);
+    return __any_sync(0xFFFFFFFFu, (x | far) != 0u || !here);
 }
 
 /* A page holds value scales outside its groups' windows (vw: the lane's word
@@ -505,7 +505,7 @@ DEV bool kv4_outside(uint32_t vw, uint32_t far, const Kv4State<G, NT> &s)
  * every row sees (of all keys, where that is none), and its twelve octaves
  * hold most pages. False if the page does not fit all the same. */
 template <int G, int NT>
-DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, uint32_t far, Kv4State<G, NT> &s)
+DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, uint32_t far, bool here, Kv4State<G, NT> &s)
 {
     float any = 0.0f;
 #pragma unroll
@@ -522,7 +522,7 @@ DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, uint32
     }
     kv4_window(s);
     vw = kv4_fill(vw, key0, nv, s);
-    return !kv4_outside(vw, far, s);
+    return !kv4_outside(vw, far, here, s);
 }
 
 /* A page whose value scales lie too far apart, or too far from what the rows
@@ -809,9 +809,10 @@ DEV uint32_t kv4_existing(uint32_t base, uint32_t valid)
  * bytes of the warp's) passes the scales from the lane that converts a word
  * of them to the lanes that use them; without it (GLOBAL: the page is in
  * global memory, there is no staging) they pass by shuffles. False: nothing is
- * done, the page has to go the slow way (kv4_page_rare). */
+ * done, as the page has to go the slow way (kv4_page_rare), or has not come
+ * (here, as each lane found it: the limit of their waits may part them). */
 template <int G, int NT, bool GLOBAL>
-DEV bool kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base, uint32_t valid, Kv4State<G, NT> &s)
+DEV bool kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base, uint32_t valid, bool here, Kv4State<G, NT> &s)
 {
     constexpr uint32_t D = 32u * G;
     const uint32_t lane = lane_id(), i = lane >> 2, j = lane & 3u;
@@ -839,7 +840,7 @@ DEV bool kv4_page(const unsigned char *pg, unsigned char *scratch, uint32_t base
         const uint32_t word = lane % (8u * G), key0 = word / G * 4u;
         uint32_t vw = kv4_ld4<GLOBAL>(pg + 33u * D + 4u * word);
         if (nv < GPUOS_KV4_PAGE) vw = kv4_fill(vw, key0, nv, s);
-        if (kv4_outside(vw, far, s) && !kv4_fit<G, NT>(base, nv, key0, vw, far, s)) return false;
+        if (kv4_outside(vw, far, here, s) && !kv4_fit<G, NT>(base, nv, key0, vw, far, here, s)) return false;
         vs.x = __byte_perm(vw, 0u, 0x4140) * 1024u + s.factor;
         vs.y = __byte_perm(vw, 0u, 0x4342) * 1024u + s.factor;
     }
@@ -1238,26 +1239,22 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t &first, uint32_t end
         const uint32_t base = (begin + k) * GPUOS_KV4_PAGE, valid = there ? (uint32_t)p.len : 0u;
         if (staged) {
             const uint32_t hb = k & 1u;
-            if (!mbar_wait(&w->mbar[hb], phs >> hb & 1u)) {
-                /* leave no copy in flight: wait once more (bounded) for this
-                 * half and for the other one if it has a copy out */
-                mbar_wait(&w->mbar[hb], phs >> hb & 1u);
-                phs ^= 1u << hb;
-                if (k + 1 < n) {
-                    mbar_wait(&w->mbar[hb ^ 1u], phs >> (hb ^ 1u) & 1u);
-                    phs ^= 1u << (hb ^ 1u);
-                }
-                status = GPUOS_ST_COPY_TIMEOUT;
-                break;
-            }
+            const bool here = mbar_wait(&w->mbar[hb], phs >> hb & 1u);
             phs ^= 1u << hb;
-            if (!kv4_page<G, NT, false>(buf + hb * PB, buf + 2u * PB, base, valid, s)) {
-                first = begin + k;
-                if (k + 1 < n) { /* (the other half's copy is out) */
-                    if (!mbar_wait(&w->mbar[hb ^ 1u], phs >> (hb ^ 1u) & 1u) && !mbar_wait(&w->mbar[hb ^ 1u], phs >> (hb ^ 1u) & 1u))
-                        status = GPUOS_ST_COPY_TIMEOUT;
+            if (!kv4_page<G, NT, false>(buf + hb * PB, buf + 2u * PB, base, valid, here, s)) {
+                /* leave no copy in flight: wait (once more, bounded) for this
+                 * half if its copy has not landed, and for the other one if
+                 * it has a copy out */
+                bool lost = __any_sync(0xFFFFFFFFu, !here);
+                if (lost) (void)mbar_wait(&w->mbar[hb], ~(phs >> hb) & 1u);
+                if (k + 1 < n) {
+                    const uint32_t ph = phs >> (hb ^ 1u) & 1u;
+                    if (!mbar_wait(&w->mbar[hb ^ 1u], ph) && !mbar_wait(&w->mbar[hb ^ 1u], ph)) lost = true;
                     phs ^= 1u << (hb ^ 1u);
                 }
+                lost = __any_sync(0xFFFFFFFFu, lost);
+                if (lost) status = GPUOS_ST_COPY_TIMEOUT;
+                else first = begin + k;
                 break;
             }
             if (k + 2 < n) {
@@ -1268,7 +1265,7 @@ DEV int kv4_run(const Kv4Args &a, const Kv4Pos &p, uint32_t &first, uint32_t end
                 issue(k + 2, nx);
             }
         } else {
-            if (!kv4_page<G, NT, true>(pool + (uint64_t)(there ? (uint32_t)id : 0u) * stride, nullptr, base, valid, s)) {
+            if (!kv4_page<G, NT, true>(pool + (uint64_t)(there ? (uint32_t)id : 0u) * stride, nullptr, base, valid, true, s)) {
                 first = begin + k;
                 break;
             }
@@ -1858,6 +1855,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
     const uint32_t u1 = b0 + mine_of.start(warp + 1u);
     Kv4Pos p;
     uint32_t slot = 0, parity = 0; /* the ring's position */
+    bool lost = false; /* a page did not arrive: what this warp has yet to do is NaN */
     if (u < u1) kv4_seek(a, u, len0, p);
 #pragma unroll 1
     while (u < u1) {
@@ -1867,7 +1865,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
         (void)kv4_pages(a, p.len, bad);
         if (!bad && begin < end) { /* (bad: the request's rows are left as they were) */
             Kv4State<G, NT> s;
-            const uint32_t n = p.len ? end - begin : 0u;
+            const uint32_t n = p.len && !lost ? end - begin : 0u;
             const int32_t *row = a.table + (uint64_t)p.b * a.P + begin;
             const uint64_t stride = (uint64_t)a.Hkv * PB;
             const unsigned char *pool = a.pool + (uint64_t)p.h * PB;
@@ -1911,7 +1909,7 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
 #pragma unroll 1
             while (k < n) { /* (the slow way's call stands outside the loop over pages: 2 % of the batch case) */
                 uint32_t base, valid;
-                bool done;
+                bool done = true;
 #pragma unroll 1
                 do {
                     if ((k & 31u) == 0) {
@@ -1921,14 +1919,34 @@ __global__ void __launch_bounds__(Kv4Block<G, NT>::WARPS * 32, 1) gpuos_kv4_atte
                     const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, k & 31u);
                     base = (begin + k) * GPUOS_KV4_PAGE;
                     valid = (uint32_t)id < a.npages ? (uint32_t)p.len : 0u;
-                    (void)mbar_wait(&bars[warp][slot], parity); /* bounded, like every wait */
-                    done = kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, s);
+                    /* bounded, like every wait; lanes poll for themselves, and the limit may part them */
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars[warp][slot], parity))) {
+                        lost = true;
+                        break;
+                    }
+                    done = kv4_page<G, NT, false>(mine + slot * PB, mine + NS * PB, base, valid, true, s);
                     if (done) follow();
                 } while (done && k < n);
+                if (lost) {
+                    /* no copy is left in flight: each is waited for once
+                     * more, and none is issued again */
+                    for (uint32_t c = 0; c < NS && k + c < n; c++) {
+                        (void)mbar_wait(&bars[warp][slot], parity);
+                        if (++slot == NS) {
+                            slot = 0;
+                            parity ^= 1u;
+                        }
+                    }
+                    break;
+                }
                 if (!done) {
                     kv4_page_rare(a, p, mine + slot * PB, base, kv4_existing(base, valid), s);
                     follow();
                 }
+            }
+            if (lost) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) s.l[nt][0] = s.l[nt][1] = NAN;
             }
             kv4_finish(s);
             if (begin == 0 && end == p.np) {
