@@ -264,7 +264,8 @@ typedef struct gpuos_stats_t {
 } gpuos_stats_t;
 
 /* Where the executor's worker warps spent their time, per op id (device
- * clock, summed over warps). Bucket b < GPUOS_OP_BUILTIN_COUNT is op id b;
+ * clock, summed over warps), since the executor's last launch: a hand-off
+ * starts every bucket anew, as it does gpuos_stats' per-warp counters. Bucket b < GPUOS_OP_BUILTIN_COUNT is op id b;
  * bucket GPUOS_OP_BUILTIN_COUNT gathers every user op id. */
 #define GPUOS_PROF_BUCKETS 32
 #define GPUOS_PROF_FIELDS 4

@@ -2609,11 +2609,14 @@ DEV void worker(const gpuos_exec_params &p, gpuos_devdesc *sd, uint32_t gw, uint
             const uint32_t bk = sd->op_id < GPUOS_OP_BUILTIN_COUNT ? sd->op_id : GPUOS_OP_BUILTIN_COUNT;
             const uint64_t t_fin = globaltimer();
             const uint64_t add[GPUOS_PROF_FIELDS] = {count, t_body - t_deps, t_fin - t_body, t_deps - t_found};
-            if (bk < GPUOS_PROF_SMEM_BUCKETS) {
+            /* (the 4-bit cache's read back, attention and page copy, whose
+             * tiles are long, go to the row itself) */
+            const uint32_t sk = bk == GPUOS_OP_BUILTIN_COUNT ? GPUOS_PROF_SMEM_BUCKETS - 1 : bk;
+            if (bk < GPUOS_PROF_SMEM_BUCKETS - 1 || bk == GPUOS_OP_BUILTIN_COUNT) {
 #pragma unroll
                 for (int f = 0; f < GPUOS_PROF_FIELDS; f++) {
-                    const uint64_t v = sprof[f * GPUOS_PROF_SMEM_BUCKETS + bk] + add[f];
-                    sprof[f * GPUOS_PROF_SMEM_BUCKETS + bk] = v;
+                    const uint64_t v = sprof[f * GPUOS_PROF_SMEM_BUCKETS + sk] + add[f];
+                    sprof[f * GPUOS_PROF_SMEM_BUCKETS + sk] = v;
                     ws[GPUOS_WS_PROF + f * GPUOS_PROF_BUCKETS + bk] = v;
                 }
             } else {
@@ -2650,8 +2653,11 @@ extern "C" __global__ void __launch_bounds__(GPUOS_MAX_WPB * 32, 1) gpuos_execut
     __shared__ uint64_t s_prof[GPUOS_MAX_WPB][GPUOS_PROF_FIELDS * GPUOS_PROF_SMEM_BUCKETS]; /* tile profiles */
     const uint32_t warp = threadIdx.x >> 5;
     for (uint32_t i = threadIdx.x & 31u; i < GPUOS_PROF_FIELDS * GPUOS_PROF_SMEM_BUCKETS; i += 32) s_prof[warp][i] = 0;
-    stage_init(p.stage_bytes); /* (its block barriers also order the clearing above) */
     const uint32_t gw = blockIdx.x * (blockDim.x >> 5) + warp;
+    /* the warp's row in memory too: every bucket counts from this launch on */
+    for (uint32_t i = threadIdx.x & 31u; i < GPUOS_PROF_FIELDS * GPUOS_PROF_BUCKETS; i += 32)
+        p.warp_stats[(uint64_t)gw * GPUOS_WS_N + GPUOS_WS_PROF + i] = 0;
+    stage_init(p.stage_bytes); /* (its block barriers also order the clearing above) */
     /* Blocks 0 .. S-1 each hold one sequencer warp and nothing else (unless
      * there is only one block): worker warps beside a sequencer would share
      * its issue slots and load/store pipe, and sequencers on one SM slowed

@@ -43,8 +43,9 @@
  * sequencer's table copy, per-warp tile profiles */
 #define GPUOS_EXEC_STATIC_SMEM \
     (GPUOS_MAX_WPB * 128 + 256 * 8 + GPUOS_MAX_WPB * GPUOS_PROF_FIELDS * GPUOS_PROF_SMEM_BUCKETS * 8)
-/* buckets kept in shared memory (more would take what the largest staging
- * buffers need); the others are added to in the warp's row */
+/* buckets kept in shared memory, the last for the user ops (more would take
+ * what the largest staging buffers need); the others are added to in the
+ * warp's row */
 #define GPUOS_PROF_SMEM_BUCKETS 16
 #define GPUOS_MAX_REGS 168 /* registers per thread: 65536 / (12 warps x 32), in steps of 8 */
 #define GPUOS_TILE_MAX (1u << 30)          /* tiles per descriptor */
