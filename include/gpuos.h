@@ -146,9 +146,14 @@ enum {
 #define GPUOS_KV4_PAGE 32u /* tokens of a page of the 4-bit cache */
 #define GPUOS_KV4_MAX_T 32u /* query tokens of a request in one KV4_SDPA */
 /* Workspace of KV4_SDPA, whatever its sizes: 16-byte aligned, its first 8 KiB
- * zero before the first use; every descriptor leaves them zero. Descriptors
- * (launches, replayed graphs) that share a workspace run one after another. */
+ * zero before the first use; a descriptor that runs leaves them zero. One that
+ * does not run to its end (it completed with GPUOS_ST_DEP_TIMEOUT or
+ * GPUOS_ST_ABORTED, or its executor died) may leave some raised, and the next
+ * one with that workspace would then join states that are not its own: zero
+ * the first GPUOS_KV4_COUNTERS bytes again before it. Descriptors (launches,
+ * replayed graphs) that share a workspace run one after another. */
 #define GPUOS_KV4_WORKSPACE (32u << 20)
+#define GPUOS_KV4_COUNTERS 8192u
 
 /* descriptor flags */
 #define GPUOS_FLAG_FENCE 1u   /* start only after every earlier descriptor completed */

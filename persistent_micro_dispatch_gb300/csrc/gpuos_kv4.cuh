@@ -1095,7 +1095,7 @@ struct Kv4Part {
 };
 static_assert(4u * (GPUOS_KV4_MAX_TILES + 2u * GPUOS_KV4_TILES * Kv4Part<4, 1>::floats) <= GPUOS_KV4_WORKSPACE &&
                   4u * (GPUOS_KV4_MAX_TILES + 2u * GPUOS_KV4_MAX_BLOCKS * Kv4Part<4, 2>::floats) <= GPUOS_KV4_WORKSPACE &&
-                  GPUOS_KV4_TILES <= GPUOS_KV4_MAX_TILES && GPUOS_KV4_MAX_BLOCKS <= GPUOS_KV4_MAX_TILES,
+                  4u * GPUOS_KV4_MAX_TILES == GPUOS_KV4_COUNTERS && GPUOS_KV4_TILES <= GPUOS_KV4_MAX_TILES && GPUOS_KV4_MAX_BLOCKS <= GPUOS_KV4_MAX_TILES,
               "the workspace holds every tile's and block's states and counters");
 template <bool GLOBAL, int G, int NT>
 DEV void kv4_part_store(void *part, const Kv4State<G, NT> &s)

@@ -33,6 +33,7 @@ from . import gpuos as G
 
 PAGE = 32
 WORKSPACE_BYTES = 32 << 20
+COUNTER_BYTES = 8192  # of the workspace: zero before each attention
 MAX_QUERY_TOKENS = 32
 
 _DESC = struct.Struct("<HBBI2Q6Q6I2f3Q")
@@ -50,6 +51,14 @@ def new_pool(npages: int, heads: int, head_dim: int, device="cuda") -> torch.Ten
 def new_workspace(device="cuda") -> torch.Tensor:
     """The attention's workspace, for one descriptor at a time."""
     return torch.zeros(WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def reset_workspace(workspace: torch.Tensor) -> None:
+    """Make a workspace fit for use again after an attention that did not run
+    to its end (status 3, a dependency's wait ran out, or 4, the executor was
+    leaving): what it left would be joined to the next one's states. Runs on
+    the current stream."""
+    workspace[:COUNTER_BYTES].zero_()
 
 
 def _refuse(pool: torch.Tensor, *named) -> None:
