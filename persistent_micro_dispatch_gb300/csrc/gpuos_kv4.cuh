@@ -1725,8 +1725,9 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
     const uint32_t layer = pair / n, k = pair - layer * n;
     if (layer >= layers) return GPUOS_ST_OK;
     const int2 sd = __ldcg(reinterpret_cast<const int2 *>(d->aux0) + k);
-    if (sd.x < 0 || sd.y < 0 || sd.x == sd.y) return GPUOS_ST_OK;
+    if (sd.x < 0 || sd.y < 0) return GPUOS_ST_OK;
     if ((uint32_t)sd.x >= npages || (uint32_t)sd.y >= npages) return GPUOS_ST_BAD_ARGS;
+    if (sd.x == sd.y) return GPUOS_ST_OK;
     uint4 *pool = reinterpret_cast<uint4 *>(d->a) + (uint64_t)layer * npages * p16 + c0;
     const uint4 *src = pool + (uint64_t)sd.x * p16;
     uint4 *dst = pool + (uint64_t)sd.y * p16;
