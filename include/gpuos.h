@@ -106,35 +106,43 @@ enum {
      * head; the pool is [npages][Hkv][34 D] bytes (gpuos_kv4_pool_bytes), D = 64 or 128, 16-byte
      * aligned. Each run of 32 channels of a token is 32 codes of 4 bits (sign, and one of
      * {0, .5, 1, 1.5, 2, 3, 4, 6}) under one scale byte e + 127: value = code * 2^e (255: the run
-     * held a NaN or an infinity, and reads as NaN). Slot s is key s % 32 of page s / 32. Pages
-     * are caller-owned like every tensor; so are the tables that say which are in use. */
+     * held a NaN or an infinity, and reads as NaN, whatever its codes). Slot s is key s % 32 of
+     * page s / 32. Pages are caller-owned like every tensor; so are the tables that say which
+     * are in use. Slots, pages, lengths and pairs are checked on the device: what lies outside
+     * the pool (or a length outside 0 .. 32 P) is never followed, and gives status
+     * GPUOS_ST_BAD_ARGS where there is a status. */
     GPUOS_OP_KV4_WRITE = 14, /* rows a=k[N][Hkv][D], b=v, f32|bf16, quantised into slots aux0 =
                                i32[N] of pool `out`; dims = {N, Hkv, D, npages}, N < 2^31. e is the least
                                exponent >= -127 (at most 125) with max|x| <= 6 * 2^e, codes are
-                               the nearest, ties to the even code. A negative slot is skipped.
+                               the nearest, ties to the even code. A negative slot is skipped, one
+                               outside the pool too.
                                The slots of one descriptor are distinct (of two rows for one slot
                                either, or parts of both, may stay) */
     GPUOS_OP_KV4_READ = 15,  /* the inverse: slots aux0 of pool a -> out=k[N][Hkv][D], aux1=v,
-                               f32|bf16 (exact in both); a negative slot gives zeros; dims as above */
+                               f32|bf16 (exact in both); a negative slot gives zeros, one outside
+                               the pool too; dims as above */
     GPUOS_OP_KV4_SDPA = 16,  /* attention of T query tokens a request over the cache: out[b][t][h] =
                                softmax(scale q.K^T) V over keys 0 .. lens[b] - T + t of the pages
                                aux1 = table i32[B][P]; a=q[B][T][H][D], out alike, bf16; b = pool;
                                aux0 = lens i32[B], 0 <= lens[b] <= 32 P (the T new tokens
-                               included); query head h reads cache head h / (H / Hkv); a query that
-                               sees no key gives zeros. A weight is held to 2^-11 of itself, or to
-                               2^-25 of what weighs most in the row (weight times value, by groups of
-                               32 channels), however far apart the values' sizes are and whatever
-                               keys that the query does not see hold; below 2^-140 of the largest it
-                               is nothing. Scores are held in fp32, a query channel to 2^-18 of the
-                               largest of its 32. A score or output beyond fp32 gives NaN or an
-                               infinity. aux2 = workspace of GPUOS_KV4_WORKSPACE
-                               bytes (below); dims = {B, H | Hkv << 16, D | T << 16, P, npages},
-                               T <= 32, H % Hkv == 0; fparam[0] = scale */
+                               included); query head h reads cache head h / (H / Hkv). A query that
+                               sees no key gives zeros; one with positions to see, but every page
+                               of them outside the pool, NaN (a page outside is left out); a request
+                               of a length outside its table keeps its output rows. A weight is held
+                               to 2^-11 of itself, or to 2^-24 of what weighs most in the row
+                               (weight times value, by groups of 32 channels), however far apart
+                               the values' sizes are and whatever keys that the query does not see
+                               hold; below 2^-140 of the largest it is nothing. Scores are held in
+                               fp32, a query channel to 2^-18 of the largest of its 32; a score or
+                               an output beyond fp32 gives NaN or an infinity. aux2 = workspace of
+                               GPUOS_KV4_WORKSPACE bytes (below); dims = {B, H | Hkv << 16,
+                               D | T << 16, P, npages}, T <= 32, H % Hkv == 0; fparam[0] = scale */
     GPUOS_OP_PAGE_COPY = 17, /* a[l][dst] = a[l][src] for the pairs aux0 = i32[n][2] of {src, dst}
                                and every layer l of pool a[layers][npages][16 * page16] bytes (any
                                paged cache, this one or another); dims = {n, page16, npages,
-                               layers}. Pairs with a negative page are skipped; a source may be in
-                               several pairs; a destination is in one, and is no pair's source */
+                               layers}. Pairs with a negative page are skipped, those with one
+                               outside the pool too; a source may be in several pairs; a destination
+                               is in one, and is no pair's source */
     GPUOS_OP_BUILTIN_COUNT = 18,
     GPUOS_OP_USER_FIRST = 64, /* ids >= this are free for gpuos_register_op */
     GPUOS_MAX_OPS = 256

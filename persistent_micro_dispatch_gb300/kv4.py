@@ -16,11 +16,14 @@ library, has the dense cache update and attention that these stand beside.
     gpuos.eager_run(kv4.sdpa(q, pool, table, lens, out, ws, D ** -0.5), stream)
 
 Nothing here reads device memory or computes gradients. Launch with the
-tensors' device current, on one of its streams. Slots, page tables, lengths and pairs that
-point outside the pool are found by the kernels: such an entry is skipped
-(attention: the page counts as no keys; a request whose length does not fit
-its table row keeps its output rows as they were), and the executor reports
-status 2 (bad arguments) for the descriptor.
+tensors' device current, on one of its streams. Slots, page tables, lengths and
+pairs that point outside the pool are found by the kernels, and the executor
+reports status 2 (bad arguments) for the descriptor; a launch reports nothing.
+Of such an entry, a written row is skipped, a row read back is zeros, a pair is
+skipped, a page's keys are left out of the attention (a query that has
+positions to see, but none of whose pages is in the pool, is NaN), and a
+request whose length does not fit its table row keeps its output rows as they
+were.
 """
 from __future__ import annotations
 

@@ -293,3 +293,45 @@ def test_key_scale_of_nan_beside_any_code(run, code):
     got = _attend(RUNNERS[run], q, pool, table, lens, 0.125)
     assert np.array_equal(np.isnan(got), nan)
     _close(got[~nan], want[~nan], tol[~nan])
+
+
+def test_far_scales_after_a_handoff():
+    """The slow way of a page in an executor that was linked anew with a
+    module of user ops."""
+    import torch
+    from persistent_micro_dispatch_gb300 import gpuos as G, kv4
+    from tests.test_gpu_kv4 import _dev, _f64
+    from tests.test_gpu_protocol import _NEG_SRC
+    from workloads.device import warm_torch
+    rng = np.random.default_rng(61)
+    q, pool, table, lens = _attend_case(3, 4, 12, 1, 128, 2, [97, 64, 2000, 9])
+    pool[:, :, 33 * 128:] = rng.integers(67, 188, pool[:, :, 33 * 128:].shape)
+    t = [_dev(q, torch.bfloat16), _dev(pool), _dev(table), _dev(lens)]
+    out, ws = torch.zeros_like(t[0]), kv4.new_workspace()
+    img = G.compile_op(_NEG_SRC, "neg.cu")
+    warm_torch()
+    torch.cuda.synchronize()
+    ex = G.Executor()
+    try:
+        ex.register_op(90, img, "op_neg_ptr")
+        assert ex.stats()["handoffs"] == 1
+        ex.submit(kv4.sdpa(*t, out, ws, 0.1))
+        ex.sync(timeout_ms=30_000)
+    finally:
+        assert ex.shutdown() == G.OK
+    want, tol = _want(q, pool, table, lens, 0.1)
+    _close(_f64(out), want, tol)
+
+
+@pytest.mark.parametrize("run", WAYS)
+def test_pages_outside_among_far_scales(run):
+    """A page that is not in the pool is left out, between pages that go the
+    slow way; one request has none in the pool."""
+    q, pool, table, lens = _plain_pool(67, 2, 4, 1, 64, 1, [200, 64], lo=60)
+    table[0, 2], table[0, 4], table[1, :2] = -7, pool.shape[0], 1 << 20
+    got = _attend(RUNNERS[run], q, pool, table, lens, 0.125, **({"expect": [2]} if run != "eager" else {}))
+    inside = table.copy()
+    inside[0, :5] = table[0, [0, 1, 3, 5, 6]]  # the last page has 8 keys, and stays last
+    want, tol = _want(q[:1], pool, inside[:1], np.array([200 - 64]), 0.125)
+    _close(got[:1], want, tol)
+    assert np.isnan(got[1]).all()
