@@ -1839,11 +1839,13 @@ __device__ __noinline__ int op_rope(const gpuos_devdesc *d, uint32_t t) { return
 __device__ __noinline__ int op_kv_write(const gpuos_devdesc *d, uint32_t t) { return kv_tile(d, t); }
 __device__ __noinline__ int op_sdpa(const gpuos_devdesc *d, uint32_t t) { return sdpa_tile(d, t); }
 __device__ __noinline__ int op_vecmat(const gpuos_devdesc *d, uint32_t t) { return vecmat_tile(d, t); }
-/* The 4-bit cache's entries. The names are chosen for their place: functions
- * lie in the image in the order of their mangled names, and with these four
- * among the others (op_kv4_write, ...) instead of behind them the mixed
- * pipeline, which waits on the ops' code, ran 1.3 % slower (126.0 against
- * 127.6 K ops/s, two runs each; without the four 128.0). */
+/* The 4-bit cache's entries. The names (and op_x_slow's, which attention
+ * calls) are chosen for their place: functions lie in the image in the order
+ * of their mangled names, and the other ops' code is waited for. With the four
+ * among the others (op_kv4_write, ...) the variable-shape stream ran 52.7
+ * against 53.8 M descriptors/s and the mixed pipeline 126.0 against 126.6 K
+ * ops/s; with attention's slow path in front of all, 126.6 against 127.2 K
+ * (three runs each, in turn, that differ by 0.1 K). */
 __device__ __noinline__ int op_xwrite(const gpuos_devdesc *d, uint32_t t) { return kv4_write_op(d, t); }
 __device__ __noinline__ int op_x_read(const gpuos_devdesc *d, uint32_t t) { return kv4_read_op(d, t); }
 __device__ __noinline__ int op_x_sdpa(const gpuos_devdesc *d, uint32_t t) { return kv4_sdpa_op(d, t); }

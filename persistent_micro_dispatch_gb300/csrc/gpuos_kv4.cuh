@@ -128,7 +128,7 @@ DEV float kv4_ex2(float x)
  * at most where it is not exact, and the key that set the softmax's reference
  * weighs 2^14 with b >= E - 12: what is lost is 6 * 2^-27 of the largest p 2^b
  * that the row has met, for each key, whatever the other rows and the hidden
- * keys hold. Any other page goes the slow way (kv4_page_slow): it multiplies
+ * keys hold. Any other page goes the slow way (op_x_slow): it multiplies
  * p 2^(b - x) in fp32, x the row's own largest p 2^b in the page, before it
  * rounds to f16, and sets E anew. The softmax's reference and sum and the
  * output accumulators are fp32.
@@ -540,9 +540,10 @@ DEV bool kv4_fit(uint32_t base, uint32_t nv, uint32_t key0, uint32_t &vw, uint32
  * tile that heed values more than 2^150 apart in one group: the smaller are
  * lost.) A call whose every page comes here took 740 us instead of 81 (64
  * requests of 2,000 to 16,383 tokens, scales random over 40 octaves); out of
- * line, so that the common path keeps its registers. */
+ * line, so that the common path keeps its registers, and named for its place
+ * among the cache's ops behind the others (see op_xwrite). */
 template <int G, int NT>
-__device__ __noinline__ void kv4_page_slow(const unsigned char *pg, uint32_t base, uint32_t nv, uint32_t rows, float scale, Kv4State<G, NT> *s)
+__device__ __noinline__ void op_x_slow(const unsigned char *pg, uint32_t base, uint32_t nv, uint32_t rows, float scale, Kv4State<G, NT> *s)
 {
     constexpr uint32_t D = 32u * G;
     constexpr int NONE = -100000;
@@ -789,7 +790,7 @@ DEV void kv4_page_rare(const Kv4Args &a, const Kv4Pos &p, const unsigned char *p
         copy.q[nt][0][0] = (uint32_t)at;
         copy.q[nt][0][1] = (uint32_t)(at >> 32);
     }
-    kv4_page_slow<G, NT>(pg, base, nv, a.T * a.g - p.r0, a.scale, &copy);
+    op_x_slow<G, NT>(pg, base, nv, a.T * a.g - p.r0, a.scale, &copy);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
