@@ -107,11 +107,15 @@ DEV float kv4_ex2(float x)
  * before its first page for what an item costs of itself (a warp fetches page
  * ids, queries and a first page one after another: about 4 us, against 0.6 us
  * for each further page); the units are numbered in that order and cut into
- * equal runs, one per warp, whatever the requests' lengths. Measured with 0,
- * 2, 3, 4, 6 units: 16 ragged requests of 2 to 4,099 tokens 32.5, 23.9, 21.9,
- * 20.6, 20.2 us; 256 of 30 to 60 tokens 20.6, 17.4, 20.7, 18.2, 14.6; long
- * ones do not care. A run that ends inside an item leaves a partial state, merged with
- * its neighbours' (below).
+ * equal runs, one per warp, whatever the requests' lengths. Without, 16 ragged
+ * requests of 2 to 4,099 tokens took 32.5 us, 256 of 30 to 60 tokens 20.6, in
+ * an early form; now, with 3, 4, 6, 8, 12 units, the same two (32 heads over
+ * 4) 12.3, 12.3, 12.4, 12.2, 11.5 and 12.8, 14.5, 14.0, 12.6, 11.6 us; 64 of
+ * 200 to 1,500 (32 over 8) 22.3, 22.1, 22.5, 22.9, 24.0; one of 100 7.7, 7.8,
+ * 8.0, 5.5, 7.1; 33 of 1 to 3,001 (14 over 2, D = 64) 10.0, 10.0, 10.4, 10.1,
+ * 9.8; 8 of 20,000 38.0, 38.2, 38.1, 38.5, 38.4. Six is in the middle, not a
+ * best: short requests want more, medium ones fewer. A run that ends inside an
+ * item leaves a partial state, merged with its neighbours' (below).
  *
  * Numerics. q is scaled by a power of two for each row to [128, 256) and held
  * in f16: exact for the bf16 values within 2^-21 of the row's largest, and off
@@ -2195,15 +2199,26 @@ static int kv4_eager_launch(const gpuos_devdesc &d, void *stream)
     }
     if (d.dims[0] == 0) return 0;
     /* Row tiles of eight or of sixteen rows. Sixteen read and convert a page
-     * half as often; eight leave room for twelve warps an SM instead of eight,
-     * which is better while a warp has few pages: sixteen rows a head, 4 heads
-     * of 64 over 4 x 3,000 tokens 12.5 us by sixteens, 9.4 by eights; 8 x
-     * 8,000 20.7, 19.9; 8 x 20,000 33.5, 37.5; 32 x 8,000 44.9, 54.2. They
-     * cross near nine pages for each of 1,824 warps; the lengths are on the
-     * device, so the table's width stands for them. */
-    const uint32_t rows = (d.dims[2] >> 16) * ((d.dims[1] & 0xFFFFu) / (d.dims[1] >> 16));
-    const uint64_t pages = (uint64_t)d.dims[0] * d.dims[3] * (d.dims[1] >> 16) * ((rows + 7u) / 8u);
-    const bool eights = rows <= 8 || pages < 16384u;
+     * half as often; eight leave room for twelve warps an SM instead of eight
+     * (D = 128) and waste less of a last tile. Device us by eights, by
+     * sixteens, 4 cache heads:
+     *   D    rows  4 x 1,000    4 x 3,000    8 x 8,000    8 x 20,000   32 x 8,000
+     *   64   16     8.3   8.0    9.8   9.4   15.6  14.8   27.0  23.1   38.1  30.7
+     *   64   24     8.5   8.5   10.3  11.0   19.5  19.7   36.2  36.2   53.5  53.0
+     *   64   40     9.3   9.5   11.7  11.4   27.1  25.7   54.7  49.3   83.4  74.9
+     *   64   128   13.2  11.5   20.1  17.4   68.7  53.1    157   117    247   185
+     *   128  16     8.7  10.4   11.3  12.4   20.2  20.9   37.2  34.0   54.4  46.2
+     *   128  24     9.1  10.7   12.2  14.9   26.0  28.4   50.8  53.7   77.1  80.4
+     *   128  32    10.4  10.7   13.3  15.3   31.4  28.6   64.7  54.2   99.3  80.8
+     *   128  56    11.6  12.7   16.7  17.9   48.7  45.2    106  95.8    167   150
+     * So three tiles of eight (four halves of two sixteens) are by eights; D =
+     * 64 by sixteens; D = 128 by sixteens from about nine pages for each of
+     * 1,824 warps on. The lengths are on the device, so the table's width
+     * stands for them: requests much shorter than their table allows are taken
+     * for long ones (16 of 2 to 4,099 tokens, 32 rows: 17.3 us, 16.2 by eights). */
+    const uint32_t rows = (d.dims[2] >> 16) * ((d.dims[1] & 0xFFFFu) / (d.dims[1] >> 16)), tiles = (rows + 7u) / 8u;
+    const uint64_t pages = (uint64_t)d.dims[0] * d.dims[3] * (d.dims[1] >> 16) * tiles;
+    const bool eights = tiles == 1u || tiles == 3u || ((d.dims[2] & 0xFFFFu) == 128u && pages < 16384u);
     if ((d.dims[2] & 0xFFFFu) == 128) return eights ? kv4_attend_launch<4, 1>(d, stream) : kv4_attend_launch<4, 2>(d, stream);
     return eights ? kv4_attend_launch<2, 1>(d, stream) : kv4_attend_launch<2, 2>(d, stream);
 }
