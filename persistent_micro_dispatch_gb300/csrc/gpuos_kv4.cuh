@@ -1404,9 +1404,10 @@ DEV int kv4_sdpa_op(const gpuos_devdesc *d, uint32_t tile)
  * two keys' (four values') pieces fill a 32-byte sector and a row's channels
  * are moved 64 bytes at a time. Both ops move the rows' bytes: 512 of a bf16
  * row of 128 channels, keys and values, against 136 of codes. 8,192 tokens of
- * 8 heads are written in 9.6 us (4.4 TB/s; 580 instructions for eight rows,
- * the ALU pipe at 72 %, so conversion bounds the write), 163,840 read back in
- * 154 us (6.26 TB/s, memory).
+ * 8 heads are written in 9.6 us (4.4 TB/s; 192,512 of them in 134: no one
+ * thing is full there, the ALU pipe 72 %, issue 70 %, memory 54 %, with 40 %
+ * of the warps that an SM holds; 580 instructions for eight rows), 163,840
+ * read back in 154 us (6.26 TB/s, memory).
  *
  * Scale: the least e >= -127 with max |x| <= 6 2^e (at most 125, so that
  * 6 2^e is finite: above it the largest code stands for what is larger).
@@ -1761,9 +1762,9 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
  * merges them in the order of the keys.
  *
  * Bound by memory while pages stream: 64 requests of 2,000 to 16,383 tokens
- * (32 heads over 8, D = 128) 80.3 us, 5.4 TB/s over the launch and 6.7 in its
+ * (32 heads over 8, D = 128) 81 us, 5.4 TB/s over the launch and 6.7 in its
  * middle (a page's 517 instructions take 150 of the 187 cycles that its bytes
- * take an SM); one of 131,071 (64 heads over 8) 35.1 us; one of 1,000 8.2 us,
+ * take an SM); one of 131,071 (64 heads over 8) 34.8 us; one of 1,000 8.4 us,
  * which is a chain of loads (lengths, page ids, page) and merges. Twelve warps
  * of 168 registers: sixteen of 128 were 2 to 10 % slower, eight 16 % on the
  * long case; they only win where latency is all (1,000 tokens: 8.0 us).
@@ -1771,8 +1772,7 @@ DEV int page_copy_op(const gpuos_devdesc *d, uint32_t tile)
 /* These kernels are launched with programmatic stream serialisation: their
  * blocks may start as soon as those of the stream's previous kernel have
  * ended, and wait here, before anything else, until its writes are visible.
- * That takes 2 us off a launch that follows another in a stream (8 requests of
- * 32 heads 18.5 -> 16.7 us a call, one of 131,071 tokens 36.7 -> 34.3). Every
+ * That takes 2 us off a launch that follows another in a stream. Every
  * thread of every block waits, whether it has work or not: a kernel that ended
  * without would let the next one pass the one before it. */
 DEV void kv4_after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
