@@ -136,19 +136,20 @@ class ClockSampler:
 # descriptors it processed, reported only while the sources are unchanged.
 TRAFFIC_SOURCES = ("persistent_micro_dispatch_gb300/csrc/gpuos_device.cu",
                    "persistent_micro_dispatch_gb300/csrc/gpuos_internal.h")
+TRAFFIC_INCLUDES = ("persistent_micro_dispatch_gb300/csrc/gpuos_kv4.cuh",)  # by gpuos_device.cu
 TRAFFIC = {
-    "c2": dict(bytes=251_875_840, descs=4096, sources="59f0042f3e66b557"),
-    "c2l": dict(bytes=1_089_941_760, descs=400, sources="59f0042f3e66b557"),
-    "c3": dict(bytes=417_755_392, descs=2048, sources="59f0042f3e66b557"),
-    "c4": dict(bytes=31_051_235_584, descs=600, sources="59f0042f3e66b557"),
-    "c5": dict(bytes=492_626_176, descs=224, sources="59f0042f3e66b557"),
+    "c2": dict(bytes=252_671_744, descs=4096, sources="2a920200555672ad"),
+    "c2l": dict(bytes=1_088_947_456, descs=400, sources="2a920200555672ad"),
+    "c3": dict(bytes=415_183_360, descs=2048, sources="2a920200555672ad"),
+    "c4": dict(bytes=31_080_491_264, descs=600, sources="2a920200555672ad"),
+    "c5": dict(bytes=494_220_544, descs=224, sources="2a920200555672ad"),
 }
 
 
 def sources_digest() -> str:
     import hashlib
     h = hashlib.sha256()
-    for f in TRAFFIC_SOURCES:
+    for f in TRAFFIC_SOURCES + TRAFFIC_INCLUDES:
         with open(os.path.join(ROOT, f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
