@@ -61,6 +61,8 @@ def reset_workspace(workspace: torch.Tensor) -> None:
     to its end (status 3, a dependency's wait ran out, or 4, the executor was
     leaving): what it left would be joined to the next one's states. Runs on
     the current stream."""
+    if workspace.dtype is not torch.uint8 or workspace.ndim != 1 or workspace.numel() < WORKSPACE_BYTES:
+        raise ValueError(f"workspace: {workspace.dtype} {tuple(workspace.shape)}, wanted uint8 ({WORKSPACE_BYTES},)")
     workspace[:COUNTER_BYTES].zero_()
 
 

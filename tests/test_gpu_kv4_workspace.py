@@ -14,6 +14,17 @@ def test_counter_bytes_are_the_headers():
     assert int(re.search(r"#define GPUOS_KV4_COUNTERS (\d+)u", text).group(1)) == kv4.COUNTER_BYTES
 
 
+def test_reset_refuses_what_is_no_workspace():
+    import torch
+    from persistent_micro_dispatch_gb300 import kv4
+    ws = kv4.new_workspace(device="cpu").fill_(7)
+    for bad in (ws[:-1], ws.view(torch.int32), ws.view(2, -1), torch.zeros(8192, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            kv4.reset_workspace(bad)
+    kv4.reset_workspace(ws)
+    assert not ws[:kv4.COUNTER_BYTES].any() and (ws[kv4.COUNTER_BYTES:] == 7).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("runner", ["eager", "executor"])
 def test_reset_after_an_abandoned_attention(runner):
