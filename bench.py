@@ -136,7 +136,8 @@ class ClockSampler:
 # descriptors it processed, reported only while the sources are unchanged.
 TRAFFIC_SOURCES = ("persistent_micro_dispatch_gb300/csrc/gpuos_device.cu",
                    "persistent_micro_dispatch_gb300/csrc/gpuos_internal.h")
-TRAFFIC_INCLUDES = ("persistent_micro_dispatch_gb300/csrc/gpuos_kv4.cuh",)  # by gpuos_device.cu
+TRAFFIC_INCLUDES = ("persistent_micro_dispatch_gb300/csrc/gpuos_kv4.cuh",  # by gpuos_device.cu
+                    "persistent_micro_dispatch_gb300/csrc/gpuos_choose.cuh")
 TRAFFIC = {
     "c2": dict(bytes=252_671_744, descs=4096, sources="2a920200555672ad"),
     "c2l": dict(bytes=1_088_947_456, descs=400, sources="2a920200555672ad"),

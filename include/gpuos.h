@@ -143,7 +143,52 @@ enum {
                                layers}. Pairs with a negative page are skipped, those with one
                                outside the pool too; a source may be in several pairs; a destination
                                is in one, and is no pair's source */
-    GPUOS_OP_BUILTIN_COUNT = 18,
+    /* What a decode step chooses: the next token's logits made ready, the best tokens of a row,
+     * the experts of a token, and the experts' order. Rows of logits lie `ld` elements apart. */
+    GPUOS_OP_LOGITS_ADJUST = 18, /* a[B][V] -> out[B][V], f32|bf16 (both of one type; out may be a
+                               itself, rows alike), for request b under aux0 = gpuos_logits_request[B]
+                               (16-byte aligned) and its first `length` tokens of b = i32[B][Lcap]:
+                               x of a token that it has had becomes x / repetition (x > 0) or
+                               x * repetition; frequency * c + presence is taken off where c, its
+                               count after the first `prompt` tokens, is not 0; the value that
+                               aux2 = gpuos_logits_bias[B][Nb] lists for it in the request's first
+                               `biases` entries is added (of several, the last one's; a negative token
+                               is no entry); the sum is divided by the temperature (if above 0); and
+                               tokens whose bit in row `mask` of aux1 = u32[M][ceil(V / 32)] is 0 get
+                               -infinity, whatever they held. Arithmetic in fp32, one rounding to the
+                               type. Tokens outside the vocabulary are passed over. A request whose
+                               record does not fit (length outside 0 .. Lcap, prompt outside 0 ..
+                               length, mask >= M, biases outside 0 .. Nb) keeps its output row and gives
+                               status GPUOS_ST_BAD_ARGS. b, aux1, aux2 may be 0 with Lcap, M, Nb 0;
+                               dims = {B, V, ld of a, ld of out, Lcap <= 2^28, M | Nb << 16} */
+    GPUOS_OP_LOGITS_TOP = 19, /* the K best of each row of a[B][V], f32|bf16: out = ids i32[B][K], by
+                               value, then by id; aux0 = f32[B][K] their log-probabilities x - lse;
+                               aux1 = lse f32[B], the log of the row's sum of exp(x) (0: not wanted).
+                               A NaN counts as -infinity; a row of nothing else has lse -infinity and
+                               log-probabilities -infinity. aux2 = workspace of
+                               GPUOS_CHOOSE_WORKSPACE bytes (below); dims = {B, V, ld, K},
+                               1 <= K <= min(V, 64) */
+    GPUOS_OP_EXPERT_ROUTE = 20, /* a = router logits [N][E], f32|bf16 -> out = ids i32[N][K], the K best
+                               experts of each token, and aux0 = their weights f32[N][K]. A score is
+                               softmax or sigmoid of the logit; the choice goes by score + b[e] (b =
+                               f32[E] or 0), the weight by the score alone. With G > 1 groups of E / G
+                               neighbouring experts, only the `keep` best groups are chosen from, by their
+                               best member or the sum of their two best. Ties go to the lower expert (or
+                               group); the choice is that of 64-bit arithmetic. Weights are divided by
+                               their sum if asked, then multiplied by fparam[0]. A NaN logit counts as
+                               -infinity (score 0); weights of sum 0 stay 0. aux1 = i32[1] on the device
+                               (0: none): tokens from there on are padding, with ids -1 and weights 0.
+                               dims = {N, E <= 1024, ld, K <= 32, G | keep << 16, GPUOS_ROUTE_* flags},
+                               G <= 32, E % G == 0, K <= keep * (E / G) */
+    GPUOS_OP_EXPERT_COUNT = 21, /* the pairs of each expert in runs of a = ids i32[P], into aux2 = workspace
+                               (GPUOS_CHOOSE_WORKSPACE bytes), for the EXPERT_PLACE after it; dims =
+                               {P < 2^31, E <= 1024}. Up to GPUOS_PLAN_ONE pairs need none */
+    GPUOS_OP_EXPERT_PLACE = 22, /* pairs a = ids i32[P] in the experts' order: out = order i32[P], pair
+                               numbers by expert, within one in their order, -1 behind the last; b =
+                               place i32[P], where each pair went (-1: its id is not in 0 .. E - 1);
+                               aux0 = offsets i32[E + 1], where each expert's pairs begin. aux2 and dims
+                               as for EXPERT_COUNT, which has run on them before if P > GPUOS_PLAN_ONE */
+    GPUOS_OP_BUILTIN_COUNT = 23,
     GPUOS_OP_USER_FIRST = 64, /* ids >= this are free for gpuos_register_op */
     GPUOS_MAX_OPS = 256
 };
@@ -162,6 +207,34 @@ enum {
  * replayed graphs) that share a workspace run one after another. */
 #define GPUOS_KV4_WORKSPACE (32u << 20)
 #define GPUOS_KV4_COUNTERS 8192u
+
+/* One request's settings for LOGITS_ADJUST. */
+typedef struct gpuos_logits_request {
+    float repetition, presence, frequency; /* 1, 0, 0: no penalties */
+    float temperature;                     /* not above 0: the logits are not divided */
+    int32_t prompt, length;                /* its tokens so far, the first `prompt` of them the prompt */
+    int32_t mask;                          /* its row of the masks; negative: none */
+    int32_t biases;                        /* its entries of the biases */
+} gpuos_logits_request;
+typedef struct gpuos_logits_bias {
+    int32_t token; /* negative: no entry */
+    float value;
+} gpuos_logits_bias;
+
+/* EXPERT_ROUTE flags (dims[5]) */
+#define GPUOS_ROUTE_SIGMOID 1u /* scores are sigmoids (else the row's softmax) */
+#define GPUOS_ROUTE_TOP2 2u    /* a group counts by the sum of its two best (else by its best) */
+#define GPUOS_ROUTE_NORM 4u    /* weights are divided by their sum */
+
+/* Workspace of LOGITS_TOP and of the experts' plan, whatever the sizes: 16-byte
+ * aligned, its first GPUOS_CHOOSE_COUNTERS bytes zero before the first use; a
+ * descriptor that runs to its end leaves them zero (after GPUOS_ST_DEP_TIMEOUT or
+ * GPUOS_ST_ABORTED zero them again). Descriptors (launches, replayed graphs)
+ * that share a workspace run one after another; an EXPERT_COUNT and its
+ * EXPERT_PLACE with nothing of the workspace's between them. */
+#define GPUOS_CHOOSE_WORKSPACE (2u << 20)
+#define GPUOS_CHOOSE_COUNTERS 8192u
+#define GPUOS_PLAN_ONE 4096u /* pairs of a plan that EXPERT_PLACE counts by itself */
 
 /* descriptor flags */
 #define GPUOS_FLAG_FENCE 1u   /* start only after every earlier descriptor completed */
@@ -507,6 +580,11 @@ GPUOS_API int gpuos_tile_profile_get(gpuos_ctx *ctx, gpuos_tile_profile *out);
  *                      starting a request's head and row tile counts for six pages;
  *                      the product is below 2^32, EINVAL otherwise)
  *   page_copy          layers * n * ceil(page bytes / 16384)
+ *   logits_adjust      B * ceil((V + 7) / 4096) (4,096 tokens of one row per tile)
+ *   logits_top         B * s, s = min(floor(2048 / B), ceil((V + 7) / 1024)) or 1: runs of
+ *                      round_up(ceil((V + 7) / s), 256) tokens of one row
+ *   expert_route       ceil(N / 8) (eight tokens per tile)
+ *   expert_count, _place  1 up to GPUOS_PLAN_ONE pairs, else min(64, ceil(P / 2048)) equal runs of pairs
  *   nop / empty op     1
  * Returns GPUOS_EINVAL for a descriptor the library would reject. */
 GPUOS_API int gpuos_op_ntiles(const gpuos_desc *d, uint32_t *ntiles);

@@ -63,7 +63,8 @@ def executor_regs(log_path=None) -> int:
 
 def build(force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    headers = [os.path.join(CSRC, "gpuos_internal.h"), os.path.join(CSRC, "gpuos_kv4.cuh"), os.path.join(INCLUDE, "gpuos.h")]
+    headers = [os.path.join(CSRC, "gpuos_internal.h"), os.path.join(CSRC, "gpuos_kv4.cuh"),
+               os.path.join(CSRC, "gpuos_choose.cuh"), os.path.join(INCLUDE, "gpuos.h")]
     objs = []
     jobs = []
     for src in SOURCES:

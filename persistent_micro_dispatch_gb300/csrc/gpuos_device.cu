@@ -1824,6 +1824,7 @@ DEV int vecmat_tile(const gpuos_devdesc *d, uint32_t tile)
 
 /* ---- table entries ----------------------------------------------------------- */
 #include "gpuos_kv4.cuh"
+#include "gpuos_choose.cuh"
 
 __device__ __noinline__ int op_nop(const gpuos_devdesc *, uint32_t) { return GPUOS_ST_OK; }
 __device__ __noinline__ int op_add(const gpuos_devdesc *d, uint32_t t) { return ew_dispatch<EW_ADD>(d, t); }
@@ -1850,11 +1851,18 @@ __device__ __noinline__ int op_xwrite(const gpuos_devdesc *d, uint32_t t) { retu
 __device__ __noinline__ int op_x_read(const gpuos_devdesc *d, uint32_t t) { return kv4_read_op(d, t); }
 __device__ __noinline__ int op_x_sdpa(const gpuos_devdesc *d, uint32_t t) { return kv4_sdpa_op(d, t); }
 __device__ __noinline__ int op_x_copy(const gpuos_devdesc *d, uint32_t t) { return page_copy_op(d, t); }
+/* What a decode step chooses: behind them, for the same reason. */
+__device__ __noinline__ int op_y_adjs(const gpuos_devdesc *d, uint32_t t) { return adjust_op(d, t); }
+__device__ __noinline__ int op_y_tops(const gpuos_devdesc *d, uint32_t t) { return top_op(d, t); }
+__device__ __noinline__ int op_y_rout(const gpuos_devdesc *d, uint32_t t) { return route_op(d, t); }
+__device__ __noinline__ int op_y_cnts(const gpuos_devdesc *d, uint32_t t) { return plan_count_op(d, t); }
+__device__ __noinline__ int op_y_plac(const gpuos_devdesc *d, uint32_t t) { return plan_place_op(d, t); }
 
 __device__ gpuos_op_fn g_builtin_ops[GPUOS_OP_BUILTIN_COUNT] = {
     op_nop, op_add, op_mul, op_relu, op_gelu, op_softmax, op_layernorm,
     op_rowsum, op_rowmax, op_rowmin, op_rope, op_kv_write, op_sdpa, op_vecmat,
     op_xwrite, op_x_read, op_x_sdpa, op_x_copy,
+    op_y_adjs, op_y_tops, op_y_rout, op_y_cnts, op_y_plac,
 };
 
 /* The body of built-in op `kind`, inlined (the eager kernel). */
@@ -2730,7 +2738,7 @@ extern "C" int gpuos_dev_preload(void)
     if (cudaFuncGetAttributes(&a, gpuos_executor_kernel) != cudaSuccess) return -1;
     if (cudaFuncGetAttributes(&a, gpuos_eager_kernel) != cudaSuccess) return -1;
 #ifndef GPUOS_EXECUTOR_ONLY
-    if (kv4_preload() != 0) return -1;
+    if (kv4_preload() != 0 || choose_preload() != 0) return -1;
 #endif
     return 0;
 }
@@ -2743,6 +2751,7 @@ extern "C" int gpuos_dev_eager_launch(const gpuos_desc *d, uint32_t ntiles, uint
     dd.ntiles = ntiles;
 #ifndef GPUOS_EXECUTOR_ONLY
     if (d->op_id >= GPUOS_OP_KV4_WRITE && d->op_id <= GPUOS_OP_PAGE_COPY) return kv4_eager_launch(dd, stream);
+    if (d->op_id >= GPUOS_OP_LOGITS_ADJUST && d->op_id <= GPUOS_OP_EXPERT_PLACE) return choose_eager_launch(dd, stream);
 #endif
     const uint32_t grid = (ntiles + EAGER_WPB - 1) / EAGER_WPB;
     const uint32_t dyn = gpuos_dev_dyn_smem(EAGER_WPB, stage_bytes);

@@ -518,6 +518,29 @@ static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool use
             nt = (uint64_t)m[0] * m[3] * chunks;
         }
         break;
+    case GPUOS_OP_LOGITS_ADJUST:
+        if (m[0] && m[1]) {
+            if (!gpuos_adjust_ok(d->dtype, d->a, d->b, d->out, d->aux0, d->aux1, d->aux2, m)) return GPUOS_EINVAL;
+            nt = (uint64_t)m[0] * gpuos_adjust_chunks(m[1]);
+        }
+        break;
+    case GPUOS_OP_LOGITS_TOP:
+        if (m[0]) {
+            if (!gpuos_top_ok(d->dtype, d->a, d->out, d->aux0, d->aux1, d->aux2, m)) return GPUOS_EINVAL;
+            nt = (uint64_t)m[0] * gpuos_top_split(m[0], m[1]);
+        }
+        break;
+    case GPUOS_OP_EXPERT_ROUTE:
+        if (m[0]) {
+            if (!gpuos_route_ok(d->dtype, d->a, d->b, d->out, d->aux0, d->aux1, m)) return GPUOS_EINVAL;
+            nt = ceil_div(m[0], GPUOS_ROUTE_ROWS);
+        }
+        break;
+    case GPUOS_OP_EXPERT_COUNT:
+    case GPUOS_OP_EXPERT_PLACE:
+        if (!gpuos_plan_ok(d->op_id == GPUOS_OP_EXPERT_PLACE, d->a, d->b, d->out, d->aux0, d->aux2, m)) return GPUOS_EINVAL;
+        nt = gpuos_plan_tiles(m[0]);
+        break;
     default:
         if (d->op_id < GPUOS_OP_USER_FIRST && d->op_id >= GPUOS_OP_BUILTIN_COUNT) return GPUOS_EINVAL;
         if (!user_op_known) return GPUOS_EINVAL;

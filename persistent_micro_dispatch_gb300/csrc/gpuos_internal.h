@@ -35,6 +35,82 @@
 #define GPUOS_KV4_MAX_PAGES (1u << 26)    /* pages of a pool, and of a table row: slots are below 2^31 */
 #define GPUOS_KV4_MAX_ROWS 0x7FFFFFFFu    /* tokens of a KV4 write or read */
 #define GPUOS_PAGE_CHUNK 16384            /* bytes of a page-copy tile */
+#define GPUOS_ADJUST_CHUNK 4096           /* tokens of a logits-adjust tile (16 KB of counters) */
+#define GPUOS_ADJUST_MAX_L (1u << 28)     /* tokens of a request's history (a counter has 29 bits) */
+#define GPUOS_TOP_MAX_K 64                /* best tokens of a row at most (two for each lane) */
+#define GPUOS_TOP_TILES 2048              /* tiles of a split logits-top at most: counters and partial states */
+#define GPUOS_TOP_RUN 1024                /* tokens of a logits-top tile at least */
+#define GPUOS_TOP_PART (16u + 8u * GPUOS_TOP_MAX_K) /* bytes of a tile's partial state: {max, sum}, K entries */
+#define GPUOS_ROUTE_MAX_E 1024            /* experts */
+#define GPUOS_ROUTE_MAX_K 32              /* experts of a token (one for each lane) */
+#define GPUOS_ROUTE_ROWS 8                /* tokens of an expert-route tile */
+#define GPUOS_PLAN_RUN 2048               /* pairs of an expert-count tile at least */
+#define GPUOS_PLAN_TILES 64               /* expert-count tiles at most (each reads the others' counts) */
+#define GPUOS_PLAN_OFFSET (GPUOS_CHOOSE_COUNTERS + GPUOS_TOP_TILES * GPUOS_TOP_PART) /* the counts' place in the workspace */
+/* How the choosing ops are cut into tiles; the host sets ntiles by these, and
+ * the device (whose descriptors may be an alias's, which the host does not
+ * check) goes by them too. */
+#ifdef __CUDACC__
+#define GPUOS_HD __host__ __device__
+#else
+#define GPUOS_HD
+#endif
+static inline GPUOS_HD uint32_t gpuos_adjust_chunks(uint32_t V)
+{
+    return (uint32_t)(((uint64_t)V + 7u + GPUOS_ADJUST_CHUNK - 1u) / GPUOS_ADJUST_CHUNK);
+}
+static inline GPUOS_HD uint32_t gpuos_top_split(uint32_t B, uint32_t V)
+{
+    const uint32_t most = (uint32_t)(((uint64_t)V + 7u + GPUOS_TOP_RUN - 1u) / GPUOS_TOP_RUN);
+    const uint32_t want = B ? GPUOS_TOP_TILES / B : 1u;
+    return want < 1u ? 1u : (want < most ? want : most);
+}
+static inline GPUOS_HD uint32_t gpuos_plan_tiles(uint32_t P)
+{
+    if (P <= GPUOS_PLAN_ONE) return 1u;
+    const uint32_t n = (P + GPUOS_PLAN_RUN - 1u) / GPUOS_PLAN_RUN;
+    return n < GPUOS_PLAN_TILES ? n : GPUOS_PLAN_TILES;
+}
+/* What the choosing ops' descriptors have to hold, checked on the host and
+ * (aliases) on the device: types, pointers and their alignment, sizes. */
+static inline GPUOS_HD bool gpuos_rows_ok(uint32_t dtype, uint64_t a, uint32_t n, uint32_t ld)
+{
+    return (dtype == GPUOS_F32 || dtype == GPUOS_BF16) && a != 0 && (a & (dtype == GPUOS_F32 ? 3u : 1u)) == 0 && n != 0 &&
+           n < 0x7FFFFF00u && ld >= n;
+}
+static inline GPUOS_HD bool gpuos_adjust_ok(uint32_t dtype, uint64_t a, uint64_t tokens, uint64_t out, uint64_t requests,
+                                            uint64_t masks, uint64_t biases, const uint32_t *m)
+{
+    if (!gpuos_rows_ok(dtype, a, m[1], m[2]) || !gpuos_rows_ok(dtype, out, m[1], m[3])) return false;
+    if (a == out && m[2] != m[3]) return false;
+    if (requests == 0 || (requests & 15u) || (tokens & 3u) || (masks & 3u) || (biases & 7u)) return false;
+    return m[4] <= GPUOS_ADJUST_MAX_L && (tokens || m[4] == 0) && (masks || (m[5] & 0xFFFFu) == 0) &&
+           (biases || (m[5] >> 16) == 0);
+}
+static inline GPUOS_HD bool gpuos_top_ok(uint32_t dtype, uint64_t a, uint64_t ids, uint64_t logp, uint64_t lse, uint64_t ws,
+                                         const uint32_t *m)
+{
+    return gpuos_rows_ok(dtype, a, m[1], m[2]) && ids && logp && ws && ((ids | logp | lse) & 3u) == 0 && (ws & 15u) == 0 &&
+           m[3] >= 1 && m[3] <= GPUOS_TOP_MAX_K && m[3] <= m[1];
+}
+static inline GPUOS_HD bool gpuos_route_ok(uint32_t dtype, uint64_t a, uint64_t bias, uint64_t ids, uint64_t weights,
+                                           uint64_t rows, const uint32_t *m)
+{
+    const uint32_t E = m[1], K = m[3], G = m[4] & 0xFFFFu, keep = m[4] >> 16;
+    if (!gpuos_rows_ok(dtype, a, E, m[2]) || !ids || !weights || ((bias | ids | weights | rows) & 3u)) return false;
+    if (E > GPUOS_ROUTE_MAX_E || K == 0 || K > GPUOS_ROUTE_MAX_K || m[5] > 7u) return false;
+    if (G == 0 || G > 32u || E % G || keep == 0 || keep > G) return false;
+    return K <= keep * (E / G) && !((m[5] & GPUOS_ROUTE_TOP2) && E / G < 2u);
+}
+static inline GPUOS_HD bool gpuos_plan_ok(bool place_op, uint64_t ids, uint64_t place, uint64_t order, uint64_t offsets, uint64_t ws,
+                                          const uint32_t *m)
+{
+    if (m[0] > 0x7FFFFF00u || m[1] == 0 || m[1] > GPUOS_ROUTE_MAX_E || ws == 0 || (ws & 15u)) return false;
+    if (m[0] && (!ids || (ids & 3u))) return false;
+    if (!place_op) return true;
+    if (!offsets || ((offsets | place | order) & 3u)) return false;
+    return m[0] == 0 || (place && order);
+}
 #define GPUOS_ROW_REG_MAX 4096            /* rows up to this width stay in registers */
 #define GPUOS_MAX_WPB 12
 #define GPUOS_MAX_SEQ 4 /* sequencer warps at most */
