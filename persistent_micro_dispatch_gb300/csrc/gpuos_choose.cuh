@@ -787,8 +787,7 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
         for (int i = 0; i < VPL; i++)
             if (lane + 32u * i < a.E && !(kept >> ((lane + 32u * i) / a.size) & 1u)) key[i] = 0u;
     }
-    uint32_t id = 0, before = 0;
-    float xb = 0.0f, bb = 0.0f; /* the last one's logit and bias */
+    uint32_t id = 0, before = 0, e_before = 0;
     const uint32_t rounds = a.K + (a.bias ? 1u : 0u);
 #pragma unroll 1
     for (uint32_t k = 0; k < rounds; k++) {
@@ -807,9 +806,9 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
         if (a.bias) {
             /* values that may have swapped, unless they are of equal logits and biases */
             if (k && choose_unkey(before) - choose_unkey(win) <= unsure) {
-                if (!(route_logit(d, a, n, e) == xb && __ldcg(a.bias + e) == bb)) sure = false;
+                if (!(route_logit(d, a, n, e) == route_logit(d, a, n, e_before) && __ldcg(a.bias + e) == __ldcg(a.bias + e_before))) sure = false;
             }
-            before = win, xb = route_logit(d, a, n, e), bb = __ldcg(a.bias + e);
+            before = win, e_before = e;
         }
         if (lane == k && k < a.K) id = e;
     }
@@ -995,39 +994,861 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
 }
 
 #ifndef GPUOS_EXECUTOR_ONLY
-template <int OP>
-__global__ void __launch_bounds__(32) gpuos_choose_eager_kernel(const __grid_constant__ gpuos_devdesc d)
+/* As kv4_launch, with a grid of two dimensions. */
+static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d)
 {
-    stage_init(16384);
-    kv4_after_previous();
-    if (OP == GPUOS_OP_LOGITS_ADJUST) (void)adjust_op(&d, blockIdx.x);
-    if (OP == GPUOS_OP_LOGITS_TOP) (void)top_op(&d, blockIdx.x);
-    if (OP == GPUOS_OP_EXPERT_ROUTE) (void)route_op(&d, blockIdx.x);
-    if (OP == GPUOS_OP_EXPERT_COUNT) (void)plan_count_op(&d, blockIdx.x);
-    if (OP == GPUOS_OP_EXPERT_PLACE) (void)plan_place_op(&d, blockIdx.x);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = blocks;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = (cudaStream_t)stream;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, kernel, d) == cudaSuccess) return 0;
+    (void)cudaGetLastError(); /* reported here */
+    return -1;
 }
-template <int OP>
-static int choose_tiles_launch(const gpuos_devdesc &d, void *stream)
+
+/* ---------------------------------------------------------------------------
+ * Logits adjusted, launched: a block takes 16 places for each of its threads
+ * of one row. A thread's logits and mask words are on their way while the
+ * block counts the request's tokens.
+ * ------------------------------------------------------------------------- */
+template <bool F32>
+struct AdjustRaw {
+    static constexpr int N = F32 ? 3 : 2; /* vectors that eight elements lie in, whatever their start */
+    uint4 v[N];
+};
+/* Eight elements of the input from place `at` of the output's, all inside the
+ * row, out of the vectors that hold them; `r`: elements before the first. */
+template <bool F32>
+DEV void adjust_raw(const ChooseRow<F32> &in, uint32_t from, uint32_t r, bool here, AdjustRaw<F32> &raw)
 {
-    return kv4_launch(gpuos_choose_eager_kernel<OP>, d.ntiles, 32, gpuos_dev_dyn_smem(1, 16384), stream, d);
+    constexpr uint32_t PER = F32 ? 4u : 8u;
+#pragma unroll
+    for (int k = 0; k < AdjustRaw<F32>::N; k++) {
+        const uint32_t first = from + PER * k;
+        /* the last vector is needed only if the elements do not start at a boundary */
+        const bool need = here && (k + 1 < AdjustRaw<F32>::N || r) && first < in.hi;
+        raw.v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (!need) continue;
+        if (first >= in.lo && first + PER <= in.hi) {
+            raw.v[k] = *in.vec(first);
+        } else { /* the row's ends: nothing outside is read */
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (uint32_t j = 0; j < PER; j++) {
+                if (first + j < in.lo || first + j >= in.hi) continue;
+                if (F32) w[j & 3u] = reinterpret_cast<const uint32_t *>(in.base)[first + j];
+                else w[(j >> 1) & 3u] |= (uint32_t)reinterpret_cast<const uint16_t *>(in.base)[first + j] << 16 * (j & 1u);
+            }
+            raw.v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+template <bool F32>
+DEV void adjust_unpack(const AdjustRaw<F32> &raw, uint32_t r, float (&x)[8])
+{
+    uint32_t w[F32 ? 12 : 8];
+#pragma unroll
+    for (int k = 0; k < AdjustRaw<F32>::N; k++) w[4 * k] = raw.v[k].x, w[4 * k + 1] = raw.v[k].y, w[4 * k + 2] = raw.v[k].z, w[4 * k + 3] = raw.v[k].w;
+    if (F32) {
+        if (r & 2u)
+#pragma unroll
+            for (int i = 0; i < 9; i++) w[i] = w[i + 2];
+        if (r & 1u)
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = w[i + 1];
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = __uint_as_float(w[i]);
+    } else {
+        if (r & 4u)
+#pragma unroll
+            for (int i = 0; i < 6; i++) w[i] = w[i + 2];
+        if (r & 2u)
+#pragma unroll
+            for (int i = 0; i < 5; i++) w[i] = w[i + 1];
+        if (r & 1u)
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[2 * i] = bf_lo(w[i]), x[2 * i + 1] = bf_hi(w[i]);
+    }
+}
+
+template <bool F32, int THREADS>
+__global__ void __launch_bounds__(THREADS) gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    constexpr uint32_t CHUNK = THREADS * 16u;
+    extern __shared__ __align__(16) uint32_t adjust_ctr[]; /* CHUNK counters */
+    __shared__ int32_t listed[THREADS];
+    kv4_after_previous();
+    const uint32_t V = d.dims[1], b = blockIdx.y, t = threadIdx.x;
+    AdjustArgs a;
+    const bool fits = adjust_args(&d, b, a);
+    const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
+    const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi);
+    if (!fits || lo >= hi) return;
+    const uint32_t shift = in.lo - out.lo, r = shift & (F32 ? 3u : 7u); /* (modulo 2^32, like the places) */
+    AdjustRaw<F32> raw[2];
+    uint32_t bits[2];
+#pragma unroll
+    for (uint32_t k = 0; k < 2; k++) {
+        const uint32_t at = from + (k * THREADS + t) * 8u;
+        adjust_raw(in, at + shift - r, r, at < hi, raw[k]); /* (places before 0 wrap round, and are not in the row) */
+        bits[k] = at < hi ? adjust_bits(a, (int32_t)at - (int32_t)out.lo, V) : 0u;
+    }
+    const bool counted = a.penal || a.q.biases > 0;
+    if (counted) {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; k++) reinterpret_cast<uint4 *>(adjust_ctr)[k * THREADS + t] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        if (a.penal) {
+            const uint32_t n = (uint32_t)a.q.length, prompt = (uint32_t)a.q.prompt;
+#pragma unroll 1
+            for (uint32_t i0 = t; i0 < n; i0 += 8u * THREADS) {
+                int32_t tok[8];
+#pragma unroll
+                for (uint32_t k = 0; k < 8; k++) tok[k] = i0 + k * THREADS < n ? a.tokens[i0 + k * THREADS] : -1;
+#pragma unroll
+                for (uint32_t k = 0; k < 8; k++) {
+                    const uint32_t at = (uint32_t)tok[k] + out.lo - from;
+                    if ((uint32_t)tok[k] >= V || at >= CHUNK) continue;
+                    if (i0 + k * THREADS < prompt) atomicOr(adjust_ctr + at, GPUOS_ADJUST_HAD);
+                    else atomicAdd(adjust_ctr + at, 1u);
+                }
+            }
+        }
+        for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
+            const uint32_t token = (uint32_t)__ldg(&a.bias[i].x), at = token + out.lo - from;
+            if (i < THREADS) listed[i] = (int32_t)token;
+            if (token < V && at < CHUNK) atomicOr(adjust_ctr + at, GPUOS_ADJUST_LISTED);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 2; k++) {
+        const uint32_t at = from + (k * THREADS + t) * 8u;
+        if (at >= hi) continue;
+        float x[8];
+        adjust_unpack(raw[k], r, x);
+        uint32_t skip = 0, w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        if (counted) {
+            const uint4 w0 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t)];
+            const uint4 w1 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t) + 1];
+            w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) {
+            if ((w[j] & GPUOS_ADJUST_LISTED) || at + j < lo || at + j >= hi) skip |= 1u << j;
+            x[j] = bits[k] >> j & 1u ? adjust_penalty(a, x[j], w[j]) * a.inv_temp : -INFINITY;
+        }
+        if (skip == 0) {
+            uint4 *o = const_cast<uint4 *>(out.vec(at));
+            if (F32) {
+                o[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+                o[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+            } else {
+                o[0] = pack8(x);
+            }
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++)
+                if (!(skip >> j & 1u)) out.put(at + j, x[j]);
+        }
+    }
+    /* listed tokens: nobody has written them (out may be the input) */
+    for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
+        const int2 e = a.bias[i];
+        const uint32_t at = (uint32_t)e.x + out.lo;
+        if ((uint32_t)e.x >= V || at < from || at - from >= CHUNK) continue;
+        bool again = false; /* listed again further on: the later entry counts */
+        for (uint32_t k = i + 1; k < min((uint32_t)a.q.biases, (uint32_t)THREADS); k++) again |= listed[k] == e.x;
+        if (again || ((uint32_t)a.q.biases > THREADS && adjust_again(a, max(i, THREADS - 1u), e.x))) continue;
+        const float y = (adjust_penalty(a, in.one(at + shift), adjust_ctr[at - from]) + __int_as_float(e.y)) * a.inv_temp;
+        out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
+    }
+}
+template <bool F32, int THREADS>
+static int adjust_launch(const gpuos_devdesc &d, void *stream)
+{
+    constexpr uint32_t CHUNK = THREADS * 16u;
+    const uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + CHUNK - 1u) / CHUNK);
+    gpuos_devdesc e = d;
+    /* (rows beyond the grid's second dimension: launches of their own) */
+    for (uint32_t row = 0; row < d.dims[0]; row += 65535u) {
+        e.dims[0] = min(d.dims[0] - row, 65535u);
+        const uint64_t size = F32 ? 4u : 2u;
+        e.a = d.a + (uint64_t)row * d.dims[2] * size;
+        e.out = d.out + (uint64_t)row * d.dims[3] * size;
+        e.b = d.b + (uint64_t)row * d.dims[4] * 4u;
+        e.aux0 = d.aux0 + (uint64_t)row * sizeof(gpuos_logits_request);
+        e.aux2 = d.aux2 + (uint64_t)row * (d.dims[5] >> 16) * sizeof(gpuos_logits_bias);
+        if (choose_launch(gpuos_adjust_kernel<F32, THREADS>, dim3(chunks, e.dims[0]), THREADS, CHUNK * 4u, stream, e) != 0) return -1;
+    }
+    return 0;
+}
+template <bool F32>
+static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
+{
+    return adjust_launch<F32, 512>(d, stream);
+}
+
+/* ---------------------------------------------------------------------------
+ * The best tokens, launched: a block takes a run of a row, a unit of 32
+ * elements a thread at a time. Elements that may be among the K best are
+ * gathered: those not below the K-th best of the threads' own best, which is a
+ * bound from below and tight enough that a few more than K come together from
+ * a whole run. Their ranks, by comparing all with all, are the answer's order.
+ * ------------------------------------------------------------------------- */
+#define GPUOS_TOPB_THREADS 256
+#define GPUOS_TOPB_BLOCKS 1216u /* eight for each SM */
+#define GPUOS_TOPB_UNIT (GPUOS_TOPB_THREADS * 8u * GPUOS_TOP_UNIT)
+/* a unit adds at most K threads' elements (32 each) to those before it */
+#define GPUOS_TOPB_FEW 256u
+#define GPUOS_TOPB_ROOM (GPUOS_TOPB_FEW + GPUOS_TOP_MAX_K * 8u * GPUOS_TOP_UNIT)
+
+struct TopBlock {
+    uint64_t got[GPUOS_TOPB_ROOM];
+    uint64_t best[GPUOS_TOPB_THREADS];
+    uint64_t sorted[GPUOS_TOP_MAX_K];
+    uint64_t bar; /* an element has to be above it */
+    float2 part[GPUOS_TOPB_THREADS / 32];
+    uint32_t count, last;
+};
+/* How many of n entries are above x. */
+DEV uint32_t top_rank(const uint64_t *e, uint32_t n, uint64_t x)
+{
+    uint32_t r = 0;
+#pragma unroll 4
+    for (uint32_t i = 0; i < n; i++) r += e[i] > x;
+    return r;
+}
+/* The K best of the gathered ones, in order, into `sorted` (0 where there are
+ * none); every thread. */
+DEV void top_sort(TopBlock &s, uint32_t K)
+{
+    const uint32_t t = threadIdx.x;
+    __syncthreads();
+    const uint32_t n = s.count;
+    if (t < K) s.sorted[t] = 0;
+    __syncthreads();
+    for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) {
+        const uint64_t x = s.got[i];
+        const uint32_t r = top_rank(s.got, n, x);
+        if (r < K) s.sorted[r] = x;
+    }
+    __syncthreads();
+}
+/* The block's row state from the threads' (m, l); every thread has it after. */
+DEV void top_block_softmax(TopBlock &s, float &m, float &l)
+{
+    top_softmax(m, l);
+    if (lane_id() == 0) s.part[threadIdx.x >> 5] = make_float2(m, l);
+    __syncthreads();
+    const uint32_t w = lane_id() & (GPUOS_TOPB_THREADS / 32u - 1u);
+    m = s.part[w].x, l = lane_id() < GPUOS_TOPB_THREADS / 32u ? s.part[w].y : 0.0f;
+    top_softmax(m, l);
+}
+DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s, float m, float l)
+{
+    const uint32_t K = d.dims[3], t = threadIdx.x;
+    const float ls = logf(l); /* (-infinity if nothing but -infinity was there) */
+    if (t < K) {
+        const float x = choose_unkey((uint32_t)(s.sorted[t] >> 32));
+        reinterpret_cast<uint32_t *>(d.out)[(uint64_t)row * K + t] = GPUOS_FULL - (uint32_t)s.sorted[t];
+        reinterpret_cast<float *>(d.aux0)[(uint64_t)row * K + t] = x == -INFINITY ? x : x - m - ls;
+    }
+    if (d.aux1 && t == 0) reinterpret_cast<float *>(d.aux1)[row] = m + ls;
+}
+template <bool F32>
+__global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    __shared__ TopBlock s;
+    const uint32_t V = d.dims[1], K = d.dims[3], t = threadIdx.x, S = d.ntiles / d.dims[0]; /* (runs of a row) */
+    const uint32_t row = blockIdx.x / S, part = blockIdx.x - row * S;
+    kv4_after_previous();
+    const ChooseRow<F32> r(d.a, row, d.dims[2], V);
+    const uint32_t run = ((V + 7u + S - 1u) / S + 255u) & ~255u, from = part * run;
+    const uint32_t lo = max(from, r.lo), hi = min(from + run, r.hi);
+    const float none = __int_as_float(0x7FFFFFFF); /* NaN: not an element */
+    float m = -FLT_MAX, l = 0.0f;
+    if (t == 0) s.count = 0, s.bar = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (uint32_t u0 = from; u0 < hi; u0 += GPUOS_TOPB_UNIT) {
+        float x[GPUOS_TOP_UNIT][8], unit = -INFINITY;
+#pragma unroll
+        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) choose_load8(r, u0 + (u * GPUOS_TOPB_THREADS + t) * 8u, lo, hi, none, x[u]);
+#pragma unroll
+        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
+            const uint32_t at = u0 + (u * GPUOS_TOPB_THREADS + t) * 8u;
+            const bool whole = at >= lo && at + 8u <= hi;
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++) {
+                /* a NaN among the logits counts as -infinity */
+                if (whole || (at + j >= lo && at + j < hi)) x[u][j] = fmaxf(x[u][j], -INFINITY);
+                unit = fmaxf(unit, x[u][j]);
+            }
+        }
+        if (unit > m) {
+            const float M = fminf(unit, FLT_MAX); /* (an infinite maximum: the sum is infinite) */
+            l *= choose_exp(m - M);
+            m = M;
+        }
+        float sum[GPUOS_TOP_UNIT]; /* (sums of sums: a rounding for each unit, not for each element) */
+#pragma unroll
+        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
+            sum[u] = 0.0f;
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++) {
+                /* the difference first: the lowest of the type's values is a mask too */
+                float e;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((fmaxf(x[u][j], -INFINITY) - m) * 1.4426950408889634f));
+                sum[u] += e;
+            }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        /* this thread's best, the first of equal ones */
+        uint64_t mine = 0;
+        uint64_t bar = s.bar;
+        if (bar == 0 || unit > choose_unkey((uint32_t)(bar >> 32))) { /* (an equal one behind the bar's is not above it) */
+            uint32_t at = GPUOS_FULL;
+#pragma unroll
+            for (int u = GPUOS_TOP_UNIT - 1; u >= 0; u--)
+#pragma unroll
+                for (int j = 7; j >= 0; j--)
+                    if (x[u][j] == unit) at = u0 + (u * GPUOS_TOPB_THREADS + t) * 8u + j - r.lo;
+            if (at != GPUOS_FULL) mine = top_entry(unit, at); /* (none of its elements is there) */
+        }
+        const uint32_t above = (uint32_t)__syncthreads_count(mine > bar);
+        if (above == 0) continue;
+        if (above > K) {
+            s.best[t] = mine;
+            __syncthreads();
+            if (mine > bar && top_rank(s.best, GPUOS_TOPB_THREADS, mine) == K) s.bar = mine; /* (K others' are above it) */
+            __syncthreads();
+            bar = s.bar;
+        }
+        if (mine > bar) {
+#pragma unroll
+            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; j++) {
+                    if (!(x[u][j] >= choose_unkey((uint32_t)(bar >> 32))) && bar) continue;
+                    const uint64_t e = x[u][j] == x[u][j] ? top_entry(x[u][j], u0 + (u * GPUOS_TOPB_THREADS + t) * 8u + j - r.lo) : 0ull;
+                    if (e > bar) s.got[atomicAdd(&s.count, 1u)] = e;
+                }
+        }
+        __syncthreads();
+        if (s.count > GPUOS_TOPB_FEW) { /* make room: the K best so far, and a better bar */
+            top_sort(s, K);
+            if (t < K) s.got[t] = s.sorted[t];
+            if (t == 0) s.count = K, s.bar = max(s.bar, s.sorted[K - 1]);
+            __syncthreads();
+        }
+    }
+    top_sort(s, K);
+    top_block_softmax(s, m, l);
+    if (S == 1) {
+        top_block_write(d, row, s, m, l);
+        return;
+    }
+    /* the row's last block joins the runs' states */
+    unsigned char *p = top_part(&d, blockIdx.x);
+    if (t < K) __stcg(reinterpret_cast<unsigned long long *>(p + 16) + t, (unsigned long long)s.sorted[t]);
+    if (t == 0) __stcg(reinterpret_cast<float2 *>(p), make_float2(m, l));
+    __syncthreads();
+    if (t == 0) {
+        uint32_t *ctr = reinterpret_cast<uint32_t *>(d.aux2) + row;
+        s.last = atom_add_acq_rel_gpu32(ctr, 1u) == S - 1u;
+        if (s.last) *ctr = 0; /* left zero for the next call */
+        s.count = 0;
+    }
+    __syncthreads();
+    if (!s.last) return;
+    m = -FLT_MAX, l = 0.0f;
+    if (t < S) {
+        const float2 ms = __ldcg(reinterpret_cast<const float2 *>(top_part(&d, row * S + t)));
+        m = ms.x, l = ms.y;
+    }
+    for (uint32_t i = t; i < S * K; i += GPUOS_TOPB_THREADS) {
+        const uint64_t e = __ldcg(reinterpret_cast<const unsigned long long *>(top_part(&d, row * S + i / K) + 16) + i % K);
+        if (e) s.got[atomicAdd(&s.count, 1u)] = e;
+    }
+    top_sort(s, K);
+    top_block_softmax(s, m, l);
+    top_block_write(d, row, s, m, l);
+}
+
+template <bool F32>
+static int top_launch(const gpuos_devdesc &d, void *stream)
+{
+    /* runs of a row: as many as fill the GPU, but none below a unit; what a row's
+     * last block can join, and the workspace holds */
+    gpuos_devdesc e = d;
+    const uint32_t B = d.dims[0];
+    uint32_t S = (uint32_t)(((uint64_t)d.dims[1] + 7u + GPUOS_TOPB_UNIT - 1u) / GPUOS_TOPB_UNIT);
+    const uint32_t fill = (GPUOS_TOPB_BLOCKS + B - 1u) / B;
+    S = min(min(S, fill), min(32u, GPUOS_TOP_TILES / min(B, (uint32_t)GPUOS_TOP_TILES)));
+    e.ntiles = B * S;
+    return choose_launch(gpuos_top_kernel<F32>, dim3(e.ntiles), GPUOS_TOPB_THREADS, 0, stream, e);
+}
+
+/* ---------------------------------------------------------------------------
+ * The experts of a token, launched: sixteen lanes a token, neighbouring
+ * experts in a lane, so that a group is one lane's or a few neighbours'. What
+ * may be among the K best are the values not below the (K + 1)-th best of the
+ * lanes' own best; they are gathered, and ranked by comparing all with all.
+ * ------------------------------------------------------------------------- */
+#define GPUOS_ROUTEB_THREADS 128
+#define GPUOS_ROUTEB_BLOCKS 1824u /* at most: twelve for each SM */
+#define GPUOS_ROUTEB_LANES 16u
+#define GPUOS_ROUTEB_ROOM 128u /* gathered values of a token at most; more: the token goes the general way */
+#define GPUOS_ROUTEB_MAX_K 15u
+struct RouteGot {
+    uint64_t e; /* value and expert, as one number to compare by */
+    float x;    /* the logit */
+    float pad;
+};
+struct RouteToken {
+    RouteGot got[GPUOS_ROUTEB_ROOM];
+    RouteGot best[GPUOS_ROUTEB_LANES];
+    uint32_t count, pad[3];
+};
+/* Over a token's sixteen lanes. */
+DEV uint32_t half_min(uint32_t v)
+{
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) v = min(v, __shfl_xor_sync(GPUOS_FULL, v, o));
+    return v;
+}
+DEV float half_max(float v)
+{
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(GPUOS_FULL, v, o));
+    return v;
+}
+DEV float half_sum(float v)
+{
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) v += __shfl_xor_sync(GPUOS_FULL, v, o);
+    return v;
+}
+/* The n-th largest (1 <= n <= 16) of the half's keys. */
+DEV uint32_t half_nth(uint32_t key, uint32_t n)
+{
+    const uint32_t lane = lane_id() & 15u;
+#pragma unroll
+    for (uint32_t size = 2; size <= 16; size <<= 1)
+#pragma unroll
+        for (uint32_t o = size >> 1; o; o >>= 1) {
+            const uint32_t other = __shfl_xor_sync(GPUOS_FULL, key, (int)o);
+            const bool down = (lane & size) == 0 || size == 16, first = (lane & o) == 0;
+            key = down == first ? max(key, other) : min(key, other);
+        }
+    return __shfl_sync(GPUOS_FULL, key, (int)((lane_id() & 16u) + n - 1u));
+}
+/* ... of two keys of each lane, a >= b: those above it are counted. */
+DEV uint32_t half_nth2(uint32_t a, uint32_t b, uint32_t n)
+{
+    uint32_t above_a = 0, above_b = 0;
+#pragma unroll
+    for (int o = 0; o < 16; o++) {
+        const uint32_t x = __shfl_xor_sync(GPUOS_FULL, a, o), y = __shfl_xor_sync(GPUOS_FULL, b, o);
+        above_a += (x > a) + (y > a);
+        above_b += (x > b) + (y > b);
+    }
+    /* (equal keys leave gaps: the least that fewer than n are above) */
+    return half_min(above_b < n ? b : (above_a < n ? a : GPUOS_FULL));
+}
+/* For choosing only: fewer instructions, and off by at most 2^-21 of itself and
+ * 2^-23 (1 + |x|) where x is negative. */
+DEV float route_sigmoid_fast(float x)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(x * -1.4426950408889634f, 126.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+/* VPL >= values a lane; P = how many it has; VEC: they are whole 16-byte vectors */
+template <bool F32, int VPL, bool VEC>
+__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS) gpuos_route_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    __shared__ RouteToken tokens[GPUOS_ROUTEB_THREADS / GPUOS_ROUTEB_LANES];
+    const uint32_t lane = lane_id(), sub = lane & 15u, warp = threadIdx.x >> 5;
+    RouteToken &s = tokens[warp * 2u + (lane >> 4)];
+    kv4_after_previous();
+    RouteArgs a;
+    route_args(&d, a);
+    const uint32_t rows = a.rows ? (uint32_t)max(__ldg(a.rows), 0) : a.N;
+    const uint32_t P = (a.E + 15u) / 16u, first = sub * P; /* this lane's experts */
+    const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, top2 = a.flags & GPUOS_ROUTE_TOP2;
+    const bool summed = a.G > 1 && top2; /* (groups go by scores, experts without a bias by logits) */
+    const uint32_t step = gridDim.x * (GPUOS_ROUTEB_THREADS / 16u);
+#pragma unroll 1
+    for (uint32_t n0 = (blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + warp) * 2u; n0 < a.N; n0 += step) {
+        const uint32_t n = min(n0 + (lane >> 4), a.N - 1u); /* (the last token's lanes may do it twice) */
+        const bool pad = n >= rows;
+        const unsigned char *row = reinterpret_cast<const unsigned char *>(d.a) + ((uint64_t)n * a.ld + first) * (F32 ? 4u : 2u);
+        float x[VPL];
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += F32 ? 4 : 8) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row) + i / (F32 ? 4 : 8));
+                if (F32) {
+                    x[i] = __uint_as_float(v.x), x[i + 1] = __uint_as_float(v.y), x[i + 2] = __uint_as_float(v.z), x[i + 3] = __uint_as_float(v.w);
+                } else {
+                    float f[8];
+                    unpack8(v, f);
+#pragma unroll
+                    for (int j = 0; j < 8 && i + j < VPL; j++) x[i + j] = f[j];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                x[i] = -INFINITY;
+                if (i < (int)P && first + i < a.E)
+                    x[i] = F32 ? __ldg(reinterpret_cast<const float *>(row) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(row) + i));
+            }
+        }
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) x[i] = fmaxf(x[i], -INFINITY), most = fmaxf(most, x[i]);
+        most = fminf(half_max(most), FLT_MAX);
+        float inv = 1.0f; /* (a softmax whose scores are only divided by one another does without its sum) */
+        if (!sigmoid && (a.bias || summed || !(a.flags & GPUOS_ROUTE_NORM))) {
+            float total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) total += route_score(false, x[i], most, 1.0f);
+            total = half_sum(total);
+            inv = total > 0.0f ? 1.0f / total : 0.0f;
+        }
+        uint32_t key[VPL];
+        float wide = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            float c = x[i];
+            if (a.bias) c = sigmoid ? (x[i] == -INFINITY ? 0.0f : route_sigmoid_fast(x[i])) : route_score(false, x[i], most, inv);
+            const bool here = VEC || (i < (int)P && first + i < a.E);
+            if (a.bias && here) {
+                c = fmaxf(c + __ldg(a.bias + first + i), -INFINITY);
+                if (fabsf(c) <= FLT_MAX) wide = fmaxf(wide, fabsf(c));
+            }
+            key[i] = here ? choose_key(c) : 0u;
+        }
+        /* what two values may differ by and yet be the other way round */
+        const float low = fminf(most, 0.0f);
+        const float unsure = route_score(sigmoid, most, most, inv) * (sigmoid ? 0x1.4p-20f - low * 0x1p-21f : 0x1p-18f) + half_max(wide) * 0x1p-22f;
+        bool sure = !sigmoid || most >= -60.0f || most == -INFINITY;
+        uint32_t one = 0, two = 0; /* the lane's two best */
+#pragma unroll
+        for (int i = 0; i < VPL; i++) two = max(two, min(one, key[i])), one = max(one, key[i]);
+        if (a.G > 1) {
+            uint32_t g1 = one, g2 = two;
+            const uint32_t span = 16u / a.G, g = sub / span; /* (lanes of a group) */
+            for (uint32_t o = 1; o < span; o <<= 1) {
+                const uint32_t o1 = __shfl_xor_sync(GPUOS_FULL, g1, (int)o), o2 = __shfl_xor_sync(GPUOS_FULL, g2, (int)o);
+                g2 = max(min(g1, o1), max(g2, o2));
+                g1 = max(g1, o1);
+            }
+            uint32_t mine = g1;
+            if (top2) {
+                float v1 = choose_unkey(g1), v2 = choose_unkey(g2);
+                if (!a.bias) v1 = route_score(sigmoid, v1, most, inv), v2 = route_score(sigmoid, v2, most, inv);
+                mine = choose_key(v1 + v2);
+            }
+            uint32_t rank = 0, next = 0;
+            for (uint32_t k = 0; k < a.G; k++) {
+                const uint32_t v = __shfl_sync(GPUOS_FULL, mine, (int)((lane & 16u) + k * span));
+                const bool ahead = v > mine || (v == mine && k < g);
+                rank += ahead;
+                if (!ahead && k != g) next = max(next, v); /* the best behind this one */
+            }
+            if ((a.bias || top2) && rank == a.keep - 1u && a.keep < a.G && choose_unkey(mine) - choose_unkey(next) <= 2.0f * unsure) sure = false;
+            if (rank >= a.keep) {
+                one = two = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; i++) key[i] = 0u;
+            }
+        }
+        /* the (K + 1)-th best of the lanes' best, or of their two best where groups are shut (1: all that is there) */
+        const uint32_t bar = max(a.G > 1 ? half_nth2(one, two, a.K + 1u) : half_nth(one, a.K + 1u), 1u);
+        if (sub == 0) s.count = 0;
+        __syncwarp();
+        if (one >= bar) {
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                if (key[i] < bar) continue;
+                const uint32_t at = atomicAdd(&s.count, 1u);
+                if (at < GPUOS_ROUTEB_ROOM) {
+                    s.got[at].e = (uint64_t)key[i] << 32 | (GPUOS_FULL - (first + i));
+                    s.got[at].x = x[i];
+                }
+            }
+        }
+        __syncwarp();
+        const uint32_t count = s.count;
+        if (count > GPUOS_ROUTEB_ROOM) sure = false;
+        const uint32_t have = min(count, GPUOS_ROUTEB_ROOM);
+        for (uint32_t i = sub; i < have; i += 16u) {
+            const RouteGot c = s.got[i];
+            uint32_t rank = 0;
+            for (uint32_t k = 0; k < have; k++) rank += s.got[k].e > c.e;
+            if (rank <= a.K) s.best[rank] = c; /* (K <= 15) */
+        }
+        __syncwarp();
+        const RouteGot c = s.best[sub];
+        const uint32_t id = GPUOS_FULL - (uint32_t)c.e;
+        if (a.bias && sub < a.K && sub + 1u < have) {
+            /* values that may have swapped, unless they are of equal logits and biases */
+            const RouteGot o = s.best[sub + 1u];
+            if (choose_unkey((uint32_t)(c.e >> 32)) - choose_unkey((uint32_t)(o.e >> 32)) <= unsure &&
+                !(c.x == o.x && __ldg(a.bias + id) == __ldg(a.bias + (GPUOS_FULL - (uint32_t)o.e))))
+                sure = false;
+        }
+        if (sigmoid && sub < a.K && c.x < -80.0f && c.x != -INFINITY) sure = false; /* (its weight may be all that is seen) */
+        float w = sub < a.K ? route_score(sigmoid, c.x, most, inv) : 0.0f;
+        if (a.flags & GPUOS_ROUTE_NORM) {
+            const float sum = half_sum(w);
+            if (sum != 0.0f) w /= sum;
+        }
+        const uint32_t again = __ballot_sync(GPUOS_FULL, !sure && !pad);
+        if (sub < a.K && !(again >> (lane & 16u) & 0xFFFFu)) {
+            a.ids[(uint64_t)n * a.K + sub] = pad ? GPUOS_FULL : id;
+            a.weights[(uint64_t)n * a.K + sub] = pad ? 0.0f : w * a.scale;
+        }
+        if (again & 0xFFFFu) op_y_sure(&d, n0);
+        if (again >> 16 && n0 + 1u < a.N) op_y_sure(&d, n0 + 1u);
+        __syncwarp();
+    }
+}
+/* The general way: a warp a token. */
+template <int VPL>
+__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS) gpuos_route_any_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    kv4_after_previous();
+    const uint32_t step = gridDim.x * (GPUOS_ROUTEB_THREADS / 32u);
+    for (uint32_t n = blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + (threadIdx.x >> 5); n < d.dims[0]; n += step) route_tile<VPL>(&d, n, 1u);
+}
+
+template <bool F32, int VPL>
+static int route_launch(const gpuos_devdesc &d, void *stream)
+{
+    const uint32_t tokens = GPUOS_ROUTEB_THREADS / 16u, size = F32 ? 4u : 2u;
+    const uint64_t blocks = ((uint64_t)d.dims[0] + tokens - 1u) / tokens;
+    const uint32_t grid = (uint32_t)min(blocks, (uint64_t)GPUOS_ROUTEB_BLOCKS);
+    const bool vec = d.dims[1] == 16u * VPL && (VPL * size) % 16u == 0 && (d.a & 15u) == 0 && ((uint64_t)d.dims[2] * size & 15u) == 0;
+    if constexpr (VPL * (F32 ? 4 : 2) % 16 == 0) {
+        if (vec) return choose_launch(gpuos_route_kernel<F32, VPL, true>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
+    }
+    return choose_launch(gpuos_route_kernel<F32, VPL, false>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
+}
+template <bool F32>
+static int route_launch_of(const gpuos_devdesc &d, void *stream)
+{
+    const uint32_t E = d.dims[1], G = d.dims[4] & 0xFFFFu;
+    /* sixteen lanes have to hold whole groups or equal parts of one */
+    if (d.dims[3] <= GPUOS_ROUTEB_MAX_K && E <= 512u && (G == 1u || (16u % G == 0 && E % 16u == 0))) {
+        if (E <= 64u) return route_launch<F32, 4>(d, stream);
+        if (E <= 128u) return route_launch<F32, 8>(d, stream);
+        if (E <= 256u) return route_launch<F32, 16>(d, stream);
+        return route_launch<F32, 32>(d, stream);
+    }
+    const uint32_t grid = (uint32_t)min(((uint64_t)d.dims[0] + 3u) / 4u, (uint64_t)GPUOS_ROUTEB_BLOCKS);
+    if (E <= 256u) return choose_launch(gpuos_route_any_kernel<8>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
+    return choose_launch(gpuos_route_any_kernel<32>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
+}
+
+/* ---------------------------------------------------------------------------
+ * The experts' order, launched: a block takes a run, 4,096 pairs at a time, a
+ * warp 128 of them. Within a warp's 32 pairs, equal ids find each other by
+ * match; over its four steps, over the warps and over the runs, counts say what
+ * comes before.
+ * ------------------------------------------------------------------------- */
+#define GPUOS_PLANB_THREADS 1024u
+#define GPUOS_PLANB_WARPS 32u
+#define GPUOS_PLANB_STEPS 4u
+#define GPUOS_PLANB_PAIRS (GPUOS_PLANB_THREADS * GPUOS_PLANB_STEPS)
+static_assert(GPUOS_PLANB_PAIRS >= GPUOS_PLAN_ONE, "a plan of one run is one turn");
+
+__global__ void __launch_bounds__(GPUOS_PLANB_THREADS) gpuos_plan_count_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    __shared__ uint32_t count[GPUOS_ROUTE_MAX_E];
+    PlanRun p;
+    plan_run(&d, blockIdx.x, p);
+    const uint32_t t = threadIdx.x;
+    count[t] = 0;
+    kv4_after_previous();
+    __syncthreads();
+#pragma unroll 1
+    for (uint32_t i = p.lo + t; i < p.hi; i += GPUOS_PLANB_PAIRS) {
+        int32_t id[GPUOS_PLANB_STEPS];
+#pragma unroll
+        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) id[k] = i + k * GPUOS_PLANB_THREADS < p.hi ? __ldg(p.ids + i + k * GPUOS_PLANB_THREADS) : -1;
+#pragma unroll
+        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++)
+            if ((uint32_t)id[k] < p.E) atomicAdd(count + id[k], 1u);
+    }
+    __syncthreads();
+    if (t < p.E) p.counts[blockIdx.x * p.E + t] = count[t];
+}
+/* The sum of the threads' values before this one's, and of all. */
+DEV uint32_t plan_scan(uint32_t v, uint32_t *warps, uint32_t &total)
+{
+    const uint32_t lane = lane_id(), w = threadIdx.x >> 5;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(GPUOS_FULL, incl, o);
+        if (lane >= (uint32_t)o) incl += x;
+    }
+    if (lane == 31) warps[w] = incl;
+    __syncthreads();
+    uint32_t s = warps[lane];
+    const uint32_t own = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(GPUOS_FULL, s, o);
+        if (lane >= (uint32_t)o) s += x;
+    }
+    total = __shfl_sync(GPUOS_FULL, s, 31);
+    return __shfl_sync(GPUOS_FULL, s - own, (int)w) + incl - v;
+}
+__global__ void __launch_bounds__(GPUOS_PLANB_THREADS) gpuos_plan_place_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    extern __shared__ __align__(16) uint16_t plan_before[]; /* [32 warps][E]: the warps' pairs, then those of the warps before */
+    __shared__ uint32_t base[GPUOS_ROUTE_MAX_E], warps[32], part[2][GPUOS_PLANB_THREADS];
+    PlanRun p;
+    plan_run(&d, blockIdx.x, p);
+    const uint32_t t = threadIdx.x, lane = lane_id(), w = t >> 5;
+    int32_t *const order = reinterpret_cast<int32_t *>(d.out), *const place = reinterpret_cast<int32_t *>(d.b);
+    uint32_t *const offsets = reinterpret_cast<uint32_t *>(d.aux0);
+    uint16_t *const mine = plan_before + w * p.E;
+    kv4_after_previous();
+    uint32_t total = 0;
+    if (p.T > 1) {
+        /* pairs of each expert in the runs before this one, and in all */
+        const uint32_t parts = GPUOS_PLANB_THREADS / p.E, q = t / p.E, e = t - q * p.E;
+        uint32_t all = 0, before = 0;
+        if (q < parts) {
+#pragma unroll 8
+            for (uint32_t k = q; k < p.T; k += parts) {
+                const uint32_t c = __ldcg(p.counts + k * p.E + e);
+                all += c;
+                before += k < blockIdx.x ? c : 0u;
+            }
+        }
+        part[0][t] = all, part[1][t] = before;
+        __syncthreads();
+        all = before = 0;
+        if (t < p.E)
+            for (uint32_t k = 0; k < parts; k++) all += part[0][k * p.E + t], before += part[1][k * p.E + t];
+        const uint32_t at = plan_scan(all, warps, total);
+        if (t < p.E) {
+            base[t] = at + before;
+            if (blockIdx.x == 0) offsets[t] = at;
+        }
+    }
+#pragma unroll 1
+    for (uint32_t i0 = p.lo; i0 < p.hi || (p.T == 1 && i0 == 0); i0 += GPUOS_PLANB_PAIRS) {
+        int32_t id[GPUOS_PLANB_STEPS];
+        uint32_t rank[GPUOS_PLANB_STEPS];
+        const uint32_t i = i0 + w * (32u * GPUOS_PLANB_STEPS) + lane;
+#pragma unroll
+        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) id[k] = i + 32u * k < p.hi ? __ldg(p.ids + i + 32u * k) : -1;
+        for (uint32_t k = t; k < GPUOS_PLANB_WARPS * p.E / 2u; k += GPUOS_PLANB_THREADS) reinterpret_cast<uint32_t *>(plan_before)[k] = 0u;
+        __syncthreads();
+#pragma unroll
+        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) {
+            const bool here = (uint32_t)id[k] < p.E;
+            const uint32_t peers = __match_any_sync(GPUOS_FULL, here ? id[k] : -1);
+            const uint32_t below = (uint32_t)__popc(peers & ((1u << lane) - 1u));
+            rank[k] = here ? mine[id[k]] + below : 0u;
+            __syncwarp();
+            if (here && below == 0) mine[id[k]] = (uint16_t)(rank[k] + (uint32_t)__popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        uint32_t sum = 0;
+        if (t < p.E) {
+#pragma unroll
+            for (uint32_t k = 0; k < GPUOS_PLANB_WARPS; k++) {
+                const uint32_t c = plan_before[k * p.E + t];
+                plan_before[k * p.E + t] = (uint16_t)sum;
+                sum += c;
+            }
+        }
+        if (p.T == 1) { /* (one turn: its counts are all) */
+            const uint32_t at = plan_scan(sum, warps, total);
+            if (t < p.E) base[t] = offsets[t] = at;
+        }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) {
+            const uint32_t at = i + 32u * k;
+            if (at >= p.hi) continue;
+            const bool here = (uint32_t)id[k] < p.E;
+            const uint32_t to = here ? base[id[k]] + mine[id[k]] + rank[k] : 0u;
+            place[at] = here ? (int32_t)to : -1;
+            if (here) order[to] = (int32_t)at;
+            if (at >= total) order[at] = -1; /* (behind the last pair) */
+        }
+        __syncthreads();
+        if (t < p.E) base[t] += sum;
+    }
+    if (blockIdx.x == 0 && t == 0) offsets[p.E] = total;
+}
+
+static int plan_launch(const gpuos_devdesc &d, void *stream)
+{
+    if (d.op_id == GPUOS_OP_EXPERT_COUNT)
+        return d.ntiles == 1 ? 0 : choose_launch(gpuos_plan_count_kernel, dim3(d.ntiles), GPUOS_PLANB_THREADS, 0, stream, d);
+    const uint32_t smem = (GPUOS_PLANB_WARPS * d.dims[1] * 2u + 15u) & ~15u;
+    if (smem > 32768u) { /* more than a block has unasked: once per device */
+        static std::atomic<bool> known[64];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+        if (!known[dev].load(std::memory_order_relaxed)) {
+            if (cudaFuncSetAttribute(gpuos_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)(GPUOS_PLANB_WARPS * GPUOS_ROUTE_MAX_E * 2u)) != cudaSuccess)
+                return -1;
+            known[dev].store(true, std::memory_order_relaxed);
+        }
+    }
+    return choose_launch(gpuos_plan_place_kernel, dim3(d.ntiles), GPUOS_PLANB_THREADS, smem, stream, d);
 }
 static int choose_eager_launch(const gpuos_devdesc &d, void *stream)
 {
+    const bool f32 = d.dtype == GPUOS_F32;
+    if (d.op_id == GPUOS_OP_EXPERT_COUNT || d.op_id == GPUOS_OP_EXPERT_PLACE) return plan_launch(d, stream);
+    if (d.dims[0] == 0 || d.dims[1] == 0) return 0;
     switch (d.op_id) {
-    case GPUOS_OP_LOGITS_ADJUST: return choose_tiles_launch<GPUOS_OP_LOGITS_ADJUST>(d, stream);
-    case GPUOS_OP_LOGITS_TOP: return choose_tiles_launch<GPUOS_OP_LOGITS_TOP>(d, stream);
-    case GPUOS_OP_EXPERT_ROUTE: return choose_tiles_launch<GPUOS_OP_EXPERT_ROUTE>(d, stream);
-    case GPUOS_OP_EXPERT_COUNT: return choose_tiles_launch<GPUOS_OP_EXPERT_COUNT>(d, stream);
-    default: return choose_tiles_launch<GPUOS_OP_EXPERT_PLACE>(d, stream);
+    case GPUOS_OP_LOGITS_ADJUST: return f32 ? adjust_launch_of<true>(d, stream) : adjust_launch_of<false>(d, stream);
+    case GPUOS_OP_LOGITS_TOP: return f32 ? top_launch<true>(d, stream) : top_launch<false>(d, stream);
+    default: return f32 ? route_launch_of<true>(d, stream) : route_launch_of<false>(d, stream);
     }
 }
 /* Load the kernels (see gpuos_dev_preload). */
 static int choose_preload()
 {
     const void *const all[] = {
-        (const void *)gpuos_choose_eager_kernel<GPUOS_OP_LOGITS_ADJUST>, (const void *)gpuos_choose_eager_kernel<GPUOS_OP_LOGITS_TOP>,
-        (const void *)gpuos_choose_eager_kernel<GPUOS_OP_EXPERT_ROUTE>, (const void *)gpuos_choose_eager_kernel<GPUOS_OP_EXPERT_COUNT>,
-        (const void *)gpuos_choose_eager_kernel<GPUOS_OP_EXPERT_PLACE>};
+        (const void *)gpuos_adjust_kernel<true, 512>, (const void *)gpuos_adjust_kernel<false, 512>,
+        (const void *)gpuos_top_kernel<true>, (const void *)gpuos_top_kernel<false>,
+        (const void *)gpuos_route_kernel<true, 4, true>, (const void *)gpuos_route_kernel<true, 8, true>,
+        (const void *)gpuos_route_kernel<true, 16, true>, (const void *)gpuos_route_kernel<true, 32, true>,
+        (const void *)gpuos_route_kernel<true, 4, false>, (const void *)gpuos_route_kernel<true, 8, false>,
+        (const void *)gpuos_route_kernel<true, 16, false>, (const void *)gpuos_route_kernel<true, 32, false>,
+        (const void *)gpuos_route_kernel<false, 8, true>,
+        (const void *)gpuos_route_kernel<false, 16, true>, (const void *)gpuos_route_kernel<false, 32, true>,
+        (const void *)gpuos_route_kernel<false, 4, false>, (const void *)gpuos_route_kernel<false, 8, false>,
+        (const void *)gpuos_route_kernel<false, 16, false>, (const void *)gpuos_route_kernel<false, 32, false>,
+        (const void *)gpuos_route_any_kernel<8>, (const void *)gpuos_route_any_kernel<32>,
+        (const void *)gpuos_plan_count_kernel, (const void *)gpuos_plan_place_kernel};
     for (const void *f : all) {
         cudaFuncAttributes at;
         if (cudaFuncGetAttributes(&at, f) != cudaSuccess) return -1;

@@ -240,6 +240,13 @@ def test_top_of_odd_rows(case, kind, run):
         _check_top(run, _top_rows(B + V, B, V, f32, kind), f32, pad, K)
 
 
+@pytest.mark.parametrize("kind", ["plain", "up", "masked"])
+def test_top_of_whole_rows(kind):
+    """More rows than a launch cuts up: a block goes through all of a row."""
+    _check_top("eager", _top_rows(1, 1300, 20001, True, kind), True, 0, 64)
+    _check_top("executor", _top_rows(1, 1300, 20001, False, kind), False, 3, 33)
+
+
 @pytest.mark.parametrize("run", ["eager", "executor"])
 def test_top_of_an_infinite_logit(run):
     """+infinity is the best; the row's lse is infinite, the others' log-probabilities -infinity."""
