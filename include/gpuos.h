@@ -155,8 +155,8 @@ enum {
                                `biases` entries is added (of several, the last one's; a negative token
                                is no entry); the sum is divided by the temperature (if above 0); and
                                tokens whose bit in row `mask` of aux1 = u32[M][ceil(V / 32)] is 0 get
-                               -infinity, whatever they held. Arithmetic in fp32, one rounding to the
-                               type. Tokens outside the vocabulary are passed over. A request whose
+                               -infinity, whatever they held. Arithmetic in fp32 (factors are divided by
+                               the temperature first), one rounding to the type. Tokens outside the vocabulary are passed over. A request whose
                                record does not fit (length outside 0 .. Lcap, prompt outside 0 ..
                                length, mask >= M, biases outside 0 .. Nb) keeps its output row and gives
                                status GPUOS_ST_BAD_ARGS. b, aux1, aux2 may be 0 with Lcap, M, Nb 0;

@@ -79,7 +79,8 @@ struct AdjustArgs {
     const int32_t *tokens;
     const uint32_t *mask; /* its row; null: none */
     const int2 *bias;
-    float inv_rep, inv_temp;
+    /* divided by the temperature: 1, 1 / repetition, repetition, frequency, presence */
+    float plain, above, below, frequency, presence;
     bool penal;
 };
 /* The settings of request b; false if its record does not fit. */
@@ -99,21 +100,23 @@ DEV bool adjust_args(const gpuos_devdesc *d, uint32_t b, AdjustArgs &a)
     a.tokens = reinterpret_cast<const int32_t *>(d->b) + (uint64_t)b * Lcap;
     a.bias = reinterpret_cast<const int2 *>(d->aux2) + (uint64_t)b * Nb;
     a.mask = a.q.mask < 0 ? nullptr : reinterpret_cast<const uint32_t *>(d->aux1) + (uint64_t)(uint32_t)a.q.mask * ((V + 31u) / 32u);
-    a.inv_rep = 1.0f / a.q.repetition;
-    a.inv_temp = a.q.temperature > 0.0f ? 1.0f / a.q.temperature : 1.0f;
+    a.plain = a.q.temperature > 0.0f ? 1.0f / a.q.temperature : 1.0f;
+    a.above = a.plain / a.q.repetition;
+    a.below = a.plain * a.q.repetition;
+    a.frequency = a.plain * a.q.frequency;
+    a.presence = a.plain * a.q.presence;
     a.penal = a.q.length > 0 && !(a.q.repetition == 1.0f && a.q.presence == 0.0f && a.q.frequency == 0.0f);
     return (uint32_t)a.q.length <= Lcap && (uint32_t)a.q.prompt <= (uint32_t)a.q.length && (a.q.mask < 0 || (uint32_t)a.q.mask < M) &&
            (uint32_t)a.q.biases <= Nb;
 }
-/* (A product with 1 / repetition or 1 / temperature, rounded, is off by 2^-23
- * of itself where the quotient is by 2^-24: a division is ten times the code,
- * and a rounding to bf16 costs 2^-8 afterwards.) */
+/* x under a token's counter, divided by the temperature: a factor for each
+ * request and side, and one multiply-add. (The factors' roundings, 2^-24 each,
+ * stand where quotients' would; a division is ten times the code.) */
 DEV float adjust_penalty(const AdjustArgs &a, float x, uint32_t w)
 {
     const uint32_t c = w & GPUOS_ADJUST_COUNT;
-    float y = w & (GPUOS_ADJUST_COUNT | GPUOS_ADJUST_HAD) ? (x > 0.0f ? x * a.inv_rep : x * a.q.repetition) : x;
-    if (c) y -= fmaf(a.q.frequency, (float)c, a.q.presence);
-    return y;
+    const float f = w & (GPUOS_ADJUST_COUNT | GPUOS_ADJUST_HAD) ? (x > 0.0f ? a.above : a.below) : a.plain;
+    return fmaf(x, f, c ? -fmaf(a.frequency, (float)c, a.presence) : 0.0f);
 }
 /* The mask's bits of eight tokens from v (some of which may lie outside the
  * vocabulary); all ones without a mask. */
@@ -219,7 +222,7 @@ DEV int adjust_tile(const gpuos_devdesc *d, uint32_t tile)
             for (uint32_t j = 0; j < 8; j++) {
                 uint32_t w = counted ? (room ? ctr[at - w0 + j] : mine[j]) : 0u;
                 if (w & GPUOS_ADJUST_LISTED || at + j < v0 || at + j >= w1) skip |= 1u << j;
-                x[j] = bits >> j & 1u ? adjust_penalty(a, x[j], w) * a.inv_temp : -INFINITY;
+                x[j] = bits >> j & 1u ? adjust_penalty(a, x[j], w) : -INFINITY;
             }
             if (skip == 0) {
                 uint4 *o = const_cast<uint4 *>(out.vec(at));
@@ -254,7 +257,7 @@ DEV int adjust_tile(const gpuos_devdesc *d, uint32_t tile)
                 }
             }
             if (here && !adjust_again(a, i, e.x)) {
-                const float y = (adjust_penalty(a, in.one(at + shift), w) + __int_as_float(e.y)) * a.inv_temp;
+                const float y = fmaf(__int_as_float(e.y), a.plain, adjust_penalty(a, in.one(at + shift), w));
                 out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
             }
         }
@@ -994,22 +997,33 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
 }
 
 #ifndef GPUOS_EXECUTOR_ONLY
-/* As kv4_launch, with a grid of two dimensions. */
-static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d)
+#define GPUOS_ADJUSTB_LONG 8192u
+/* As kv4_launch, with a grid of two dimensions and clusters. */
+static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d,
+                         uint32_t cluster = 1)
 {
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t c = {};
     c.gridDim = blocks;
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = (cudaStream_t)stream;
-    c.attrs = &at;
-    c.numAttrs = 1;
+    c.attrs = at;
+    c.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&c, kernel, d) == cudaSuccess) return 0;
     (void)cudaGetLastError(); /* reported here */
     return -1;
+}
+/* Every thread of the cluster's blocks; what each wrote before, also to the
+ * others' shared memory, is seen after. */
+DEV void choose_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 /* ---------------------------------------------------------------------------
@@ -1017,22 +1031,24 @@ static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint3
  * of one row. A thread's logits and mask words are on their way while the
  * block counts the request's tokens.
  * ------------------------------------------------------------------------- */
-template <bool F32>
+template <bool F32, bool SAME>
 struct AdjustRaw {
-    static constexpr int N = F32 ? 3 : 2; /* vectors that eight elements lie in, whatever their start */
+    /* vectors that eight elements lie in: whole ones (SAME: the input's rows lie
+     * as the output's do), or whatever their start */
+    static constexpr int N = (F32 ? 2 : 1) + (SAME ? 0 : 1);
     uint4 v[N];
 };
-/* Eight elements of the input from place `at` of the output's, all inside the
- * row, out of the vectors that hold them; `r`: elements before the first. */
-template <bool F32>
-DEV void adjust_raw(const ChooseRow<F32> &in, uint32_t from, uint32_t r, bool here, AdjustRaw<F32> &raw)
+/* The vectors of the input from place `from`, the first of which has `r`
+ * elements that are not wanted. */
+template <bool F32, bool SAME>
+DEV void adjust_raw(const ChooseRow<F32> &in, uint32_t from, uint32_t r, bool here, AdjustRaw<F32, SAME> &raw)
 {
     constexpr uint32_t PER = F32 ? 4u : 8u;
 #pragma unroll
-    for (int k = 0; k < AdjustRaw<F32>::N; k++) {
+    for (int k = 0; k < AdjustRaw<F32, SAME>::N; k++) {
         const uint32_t first = from + PER * k;
         /* the last vector is needed only if the elements do not start at a boundary */
-        const bool need = here && (k + 1 < AdjustRaw<F32>::N || r) && first < in.hi;
+        const bool need = here && (SAME || k + 1 < AdjustRaw<F32, SAME>::N || r) && first < in.hi;
         raw.v[k] = make_uint4(0u, 0u, 0u, 0u);
         if (!need) continue;
         if (first >= in.lo && first + PER <= in.hi) {
@@ -1049,37 +1065,37 @@ DEV void adjust_raw(const ChooseRow<F32> &in, uint32_t from, uint32_t r, bool he
         }
     }
 }
-template <bool F32>
-DEV void adjust_unpack(const AdjustRaw<F32> &raw, uint32_t r, float (&x)[8])
+template <bool F32, bool SAME>
+DEV void adjust_unpack(const AdjustRaw<F32, SAME> &raw, uint32_t r, float (&x)[8])
 {
-    uint32_t w[F32 ? 12 : 8];
+    constexpr int N = AdjustRaw<F32, SAME>::N;
+    uint32_t w[4 * N];
 #pragma unroll
-    for (int k = 0; k < AdjustRaw<F32>::N; k++) w[4 * k] = raw.v[k].x, w[4 * k + 1] = raw.v[k].y, w[4 * k + 2] = raw.v[k].z, w[4 * k + 3] = raw.v[k].w;
+    for (int k = 0; k < N; k++) w[4 * k] = raw.v[k].x, w[4 * k + 1] = raw.v[k].y, w[4 * k + 2] = raw.v[k].z, w[4 * k + 3] = raw.v[k].w;
+    if (!SAME) {
+        if (!F32 && r & 4u)
+#pragma unroll
+            for (int i = 0; i + 2 < 4 * N; i++) w[i] = w[i + 2];
+        if (r & 2u)
+#pragma unroll
+            for (int i = 0; i + (F32 ? 2 : 1) < 4 * N; i++) w[i] = w[i + (F32 ? 2 : 1)];
+        if (r & 1u)
+#pragma unroll
+            for (int i = 0; i + 1 < 4 * N; i++) w[i] = F32 ? w[i + 1] : __funnelshift_r(w[i], w[i + 1], 16);
+    }
     if (F32) {
-        if (r & 2u)
 #pragma unroll
-            for (int i = 0; i < 9; i++) w[i] = w[i + 2];
-        if (r & 1u)
-#pragma unroll
-            for (int i = 0; i < 8; i++) w[i] = w[i + 1];
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = __uint_as_float(w[i]);
+        for (int i = 0; i < 8; i++) x[i] = __uint_as_float(w[i % (4 * N)]);
     } else {
-        if (r & 4u)
-#pragma unroll
-            for (int i = 0; i < 6; i++) w[i] = w[i + 2];
-        if (r & 2u)
-#pragma unroll
-            for (int i = 0; i < 5; i++) w[i] = w[i + 1];
-        if (r & 1u)
-#pragma unroll
-            for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
 #pragma unroll
         for (int i = 0; i < 4; i++) x[2 * i] = bf_lo(w[i]), x[2 * i + 1] = bf_hi(w[i]);
     }
 }
 
-template <bool F32, int THREADS>
+/* (CLUSTER blocks of a row's neighbouring chunks count together: each looks at
+ * its share of the request's tokens, and adds to the counter of whichever has
+ * the token, in that block's shared memory) */
+template <bool F32, bool SAME, int THREADS, int CLUSTER>
 __global__ void __launch_bounds__(THREADS) gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
 {
     constexpr uint32_t CHUNK = THREADS * 16u;
@@ -1088,46 +1104,62 @@ __global__ void __launch_bounds__(THREADS) gpuos_adjust_kernel(const __grid_cons
     kv4_after_previous();
     const uint32_t V = d.dims[1], b = blockIdx.y, t = threadIdx.x;
     AdjustArgs a;
-    const bool fits = adjust_args(&d, b, a);
+    if (!adjust_args(&d, b, a)) return; /* (all of a row's blocks) */
     const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
-    const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi);
-    if (!fits || lo >= hi) return;
-    const uint32_t shift = in.lo - out.lo, r = shift & (F32 ? 3u : 7u); /* (modulo 2^32, like the places) */
-    AdjustRaw<F32> raw[2];
-    uint32_t bits[2];
+    const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi); /* (a cluster's last may be empty) */
+    const uint32_t shift = in.lo - out.lo, r = SAME ? 0u : shift & (F32 ? 3u : 7u); /* (modulo 2^32, like the places) */
+    AdjustRaw<F32, SAME> raw[2];
+    uint32_t bits[2] = {0xFFu, 0xFFu};
 #pragma unroll
     for (uint32_t k = 0; k < 2; k++) {
         const uint32_t at = from + (k * THREADS + t) * 8u;
         adjust_raw(in, at + shift - r, r, at < hi, raw[k]); /* (places before 0 wrap round, and are not in the row) */
-        bits[k] = at < hi ? adjust_bits(a, (int32_t)at - (int32_t)out.lo, V) : 0u;
+        if (a.mask && at < hi) bits[k] = adjust_bits(a, (int32_t)at - (int32_t)out.lo, V);
     }
     const bool counted = a.penal || a.q.biases > 0;
     if (counted) {
 #pragma unroll
         for (uint32_t k = 0; k < 4; k++) reinterpret_cast<uint4 *>(adjust_ctr)[k * THREADS + t] = make_uint4(0u, 0u, 0u, 0u);
-        __syncthreads();
+        uint32_t rank = 0; /* in the cluster */
+        if (CLUSTER > 1) {
+            asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+            choose_cluster_sync();
+        } else {
+            __syncthreads();
+        }
         if (a.penal) {
             const uint32_t n = (uint32_t)a.q.length, prompt = (uint32_t)a.q.prompt;
+            const uint32_t begin = from - rank * CHUNK, mine = smem_addr(adjust_ctr); /* (the cluster's first place) */
 #pragma unroll 1
-            for (uint32_t i0 = t; i0 < n; i0 += 8u * THREADS) {
+            for (uint32_t i0 = rank * THREADS + t; i0 < n; i0 += 8u * THREADS * CLUSTER) {
                 int32_t tok[8];
 #pragma unroll
-                for (uint32_t k = 0; k < 8; k++) tok[k] = i0 + k * THREADS < n ? a.tokens[i0 + k * THREADS] : -1;
+                for (uint32_t k = 0; k < 8; k++) tok[k] = i0 + k * THREADS * CLUSTER < n ? a.tokens[i0 + k * THREADS * CLUSTER] : -1;
 #pragma unroll
                 for (uint32_t k = 0; k < 8; k++) {
-                    const uint32_t at = (uint32_t)tok[k] + out.lo - from;
-                    if ((uint32_t)tok[k] >= V || at >= CHUNK) continue;
-                    if (i0 + k * THREADS < prompt) atomicOr(adjust_ctr + at, GPUOS_ADJUST_HAD);
-                    else atomicAdd(adjust_ctr + at, 1u);
+                    const uint32_t at = (uint32_t)tok[k] + out.lo - begin;
+                    if ((uint32_t)tok[k] >= V || at >= CHUNK * CLUSTER) continue;
+                    const bool had = i0 + k * THREADS * CLUSTER < prompt;
+                    if (CLUSTER > 1) {
+                        uint32_t remote;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(mine + at % CHUNK * 4u), "r"(at / CHUNK));
+                        if (had) asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(remote), "r"(GPUOS_ADJUST_HAD) : "memory");
+                        else asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(remote), "r"(1u) : "memory");
+                    } else if (had) {
+                        atomicOr(adjust_ctr + at, GPUOS_ADJUST_HAD);
+                    } else {
+                        atomicAdd(adjust_ctr + at, 1u);
+                    }
                 }
             }
         }
         for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
-            const uint32_t token = (uint32_t)__ldg(&a.bias[i].x), at = token + out.lo - from;
+            const uint32_t token = (uint32_t)a.bias[i].x, at = token + out.lo - from;
             if (i < THREADS) listed[i] = (int32_t)token;
             if (token < V && at < CHUNK) atomicOr(adjust_ctr + at, GPUOS_ADJUST_LISTED);
         }
-        __syncthreads();
+        if (CLUSTER > 1) choose_cluster_sync();
+        else __syncthreads();
     }
 #pragma unroll
     for (uint32_t k = 0; k < 2; k++) {
@@ -1135,18 +1167,25 @@ __global__ void __launch_bounds__(THREADS) gpuos_adjust_kernel(const __grid_cons
         if (at >= hi) continue;
         float x[8];
         adjust_unpack(raw[k], r, x);
-        uint32_t skip = 0, w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
         if (counted) {
-            const uint4 w0 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t)];
-            const uint4 w1 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t) + 1];
-            w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+            w0 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t)];
+            w1 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t) + 1];
         }
+        const uint32_t any = (w0.x | w0.y | w0.z | w0.w) | (w1.x | w1.y | w1.z | w1.w);
+        if (any) {
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (uint32_t j = 0; j < 8; j++) {
-            if ((w[j] & GPUOS_ADJUST_LISTED) || at + j < lo || at + j >= hi) skip |= 1u << j;
-            x[j] = bits[k] >> j & 1u ? adjust_penalty(a, x[j], w[j]) * a.inv_temp : -INFINITY;
+            for (uint32_t j = 0; j < 8; j++) x[j] = adjust_penalty(a, x[j], w[j]);
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++) x[j] *= a.plain;
         }
-        if (skip == 0) {
+        if (a.mask) {
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++) x[j] = bits[k] & 1u << j ? x[j] : -INFINITY;
+        }
+        if (!(any & GPUOS_ADJUST_LISTED) && at >= lo && at + 8u <= hi) {
             uint4 *o = const_cast<uint4 *>(out.vec(at));
             if (F32) {
                 o[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -1155,9 +1194,10 @@ __global__ void __launch_bounds__(THREADS) gpuos_adjust_kernel(const __grid_cons
                 o[0] = pack8(x);
             }
         } else {
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (uint32_t j = 0; j < 8; j++)
-                if (!(skip >> j & 1u)) out.put(at + j, x[j]);
+                if (!(w[j] & GPUOS_ADJUST_LISTED) && at + j >= lo && at + j < hi) out.put(at + j, x[j]);
         }
     }
     /* listed tokens: nobody has written them (out may be the input) */
@@ -1168,15 +1208,16 @@ __global__ void __launch_bounds__(THREADS) gpuos_adjust_kernel(const __grid_cons
         bool again = false; /* listed again further on: the later entry counts */
         for (uint32_t k = i + 1; k < min((uint32_t)a.q.biases, (uint32_t)THREADS); k++) again |= listed[k] == e.x;
         if (again || ((uint32_t)a.q.biases > THREADS && adjust_again(a, max(i, THREADS - 1u), e.x))) continue;
-        const float y = (adjust_penalty(a, in.one(at + shift), adjust_ctr[at - from]) + __int_as_float(e.y)) * a.inv_temp;
+        const float y = fmaf(__int_as_float(e.y), a.plain, adjust_penalty(a, in.one(at + shift), adjust_ctr[at - from]));
         out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
     }
 }
-template <bool F32, int THREADS>
+template <bool F32, bool SAME, int THREADS, int CLUSTER>
 static int adjust_launch(const gpuos_devdesc &d, void *stream)
 {
     constexpr uint32_t CHUNK = THREADS * 16u;
-    const uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + CHUNK - 1u) / CHUNK);
+    uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + CHUNK - 1u) / CHUNK);
+    chunks = (chunks + CLUSTER - 1u) / CLUSTER * CLUSTER;
     gpuos_devdesc e = d;
     /* (rows beyond the grid's second dimension: launches of their own) */
     for (uint32_t row = 0; row < d.dims[0]; row += 65535u) {
@@ -1187,37 +1228,50 @@ static int adjust_launch(const gpuos_devdesc &d, void *stream)
         e.b = d.b + (uint64_t)row * d.dims[4] * 4u;
         e.aux0 = d.aux0 + (uint64_t)row * sizeof(gpuos_logits_request);
         e.aux2 = d.aux2 + (uint64_t)row * (d.dims[5] >> 16) * sizeof(gpuos_logits_bias);
-        if (choose_launch(gpuos_adjust_kernel<F32, THREADS>, dim3(chunks, e.dims[0]), THREADS, CHUNK * 4u, stream, e) != 0) return -1;
+        if (choose_launch(gpuos_adjust_kernel<F32, SAME, THREADS, CLUSTER>, dim3(chunks, e.dims[0]), THREADS, CHUNK * 4u, stream, e, CLUSTER) != 0)
+            return -1;
     }
     return 0;
+}
+template <bool F32, bool SAME>
+static int adjust_launch_by(const gpuos_devdesc &d, void *stream)
+{
+    if (d.dims[4] > GPUOS_ADJUSTB_LONG) return adjust_launch<F32, SAME, 512, 4>(d, stream);
+    return adjust_launch<F32, SAME, 512, 1>(d, stream);
 }
 template <bool F32>
 static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
 {
-    return adjust_launch<F32, 512>(d, stream);
+    const uint64_t size = F32 ? 4u : 2u;
+    const bool same = ((d.a ^ d.out) & 15u) == 0 && (((uint64_t)d.dims[2] - d.dims[3]) * size & 15u) == 0;
+    return same ? adjust_launch_by<F32, true>(d, stream) : adjust_launch_by<F32, false>(d, stream);
 }
 
 /* ---------------------------------------------------------------------------
  * The best tokens, launched: a block takes a run of a row, a unit of 32
- * elements a thread at a time. Elements that may be among the K best are
- * gathered: those not below the K-th best of the threads' own best, which is a
- * bound from below and tight enough that a few more than K come together from
- * a whole run. Their ranks, by comparing all with all, are the answer's order.
+ * elements a thread at a time. The first unit gives a bar that at least K of
+ * its elements reach; what reaches it in the run is gathered, a few times K
+ * elements, and ranked by comparing all with all. Nothing waits between units.
+ * The softmax's sum is kept in base 2 under a maximum of the thread's own:
+ * one multiply-add, one exponential and one sum an element.
  * ------------------------------------------------------------------------- */
 #define GPUOS_TOPB_THREADS 256
-#define GPUOS_TOPB_BLOCKS 1216u /* eight for each SM */
+#define GPUOS_TOPB_WARPS (GPUOS_TOPB_THREADS / 32)
+#define GPUOS_TOPB_SLOTS 456u /* blocks that run at a time: three for each SM */
+#define GPUOS_TOPB_FIXED 12288u /* elements that a block's start and end cost as much as */
 #define GPUOS_TOPB_UNIT (GPUOS_TOPB_THREADS * 8u * GPUOS_TOP_UNIT)
-/* a unit adds at most K threads' elements (32 each) to those before it */
 #define GPUOS_TOPB_FEW 256u
+/* (the slow gathering: a unit adds at most K threads' 32 elements to the few before it) */
 #define GPUOS_TOPB_ROOM (GPUOS_TOPB_FEW + GPUOS_TOP_MAX_K * 8u * GPUOS_TOP_UNIT)
 
 struct TopBlock {
     uint64_t got[GPUOS_TOPB_ROOM];
+    uint64_t few[GPUOS_TOPB_FEW];
     uint64_t best[GPUOS_TOPB_THREADS];
     uint64_t sorted[GPUOS_TOP_MAX_K];
-    uint64_t bar; /* an element has to be above it */
-    float2 part[GPUOS_TOPB_THREADS / 32];
-    uint32_t count, last;
+    uint64_t bar; /* an entry has to be above it */
+    float2 part[GPUOS_TOPB_WARPS];
+    uint32_t count, left, last;
 };
 /* How many of n entries are above x. */
 DEV uint32_t top_rank(const uint64_t *e, uint32_t n, uint64_t x)
@@ -1227,18 +1281,57 @@ DEV uint32_t top_rank(const uint64_t *e, uint32_t n, uint64_t x)
     for (uint32_t i = 0; i < n; i++) r += e[i] > x;
     return r;
 }
-/* The K best of the gathered ones, in order, into `sorted` (0 where there are
- * none); every thread. */
-DEV void top_sort(TopBlock &s, uint32_t K)
+/* A bar that at least K of the threads' entries are above (0: there are not K,
+ * or not K in the warps' eight best): the K-th of the warps' eight best, less
+ * one. Every thread. */
+DEV uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
+{
+    const uint32_t t = threadIdx.x, lane = lane_id();
+    uint64_t keep = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; i < min(K, 8u); i++) {
+        const uint32_t hi = __reduce_max_sync(GPUOS_FULL, (uint32_t)(mine >> 32));
+        const uint32_t lo = __reduce_max_sync(GPUOS_FULL, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+        const uint64_t top = (uint64_t)hi << 32 | lo;
+        if (mine == top) mine = 0;
+        if (lane == i) keep = top;
+    }
+    __syncthreads(); /* (the last use of best and bar is over) */
+    if (lane < 8) s.best[(t >> 5) * 8u + lane] = keep;
+    if (t == 0) s.bar = 0;
+    __syncthreads();
+    if (t < GPUOS_TOPB_WARPS * 8u) {
+        const uint64_t x = s.best[t];
+        if (x && top_rank(s.best, GPUOS_TOPB_WARPS * 8u, x) == K - 1u) s.bar = x - 1u;
+    }
+    __syncthreads();
+    return s.bar;
+}
+/* The K best of the n gathered ones, in order, into `sorted` (0 where there
+ * are none); every thread, after a barrier. */
+DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K)
 {
     const uint32_t t = threadIdx.x;
-    __syncthreads();
-    const uint32_t n = s.count;
+    const uint64_t *from = s.got;
+    if (n > 64u) { /* first those that reach a bar of their own */
+        uint64_t mine = 0;
+        for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) mine = max(mine, s.got[i]);
+        if (t == 0) s.left = 0;
+        const uint64_t bar = top_bar(s, mine, K);
+        for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) {
+            const uint64_t x = s.got[i];
+            if (x <= bar) continue;
+            const uint32_t at = atomicAdd(&s.left, 1u);
+            if (at < GPUOS_TOPB_FEW) s.few[at] = x;
+        }
+        __syncthreads();
+        if (s.left <= GPUOS_TOPB_FEW) n = s.left, from = s.few;
+    }
     if (t < K) s.sorted[t] = 0;
     __syncthreads();
     for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) {
-        const uint64_t x = s.got[i];
-        const uint32_t r = top_rank(s.got, n, x);
+        const uint64_t x = from[i];
+        const uint32_t r = top_rank(from, n, x);
         if (r < K) s.sorted[r] = x;
     }
     __syncthreads();
@@ -1249,9 +1342,10 @@ DEV void top_block_softmax(TopBlock &s, float &m, float &l)
     top_softmax(m, l);
     if (lane_id() == 0) s.part[threadIdx.x >> 5] = make_float2(m, l);
     __syncthreads();
-    const uint32_t w = lane_id() & (GPUOS_TOPB_THREADS / 32u - 1u);
-    m = s.part[w].x, l = lane_id() < GPUOS_TOPB_THREADS / 32u ? s.part[w].y : 0.0f;
+    const uint32_t w = lane_id() & (GPUOS_TOPB_WARPS - 1u);
+    m = s.part[w].x, l = lane_id() < GPUOS_TOPB_WARPS ? s.part[w].y : 0.0f;
     top_softmax(m, l);
+    __syncthreads();
 }
 DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s, float m, float l)
 {
@@ -1264,66 +1358,57 @@ DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s
     }
     if (d.aux1 && t == 0) reinterpret_cast<float *>(d.aux1)[row] = m + ls;
 }
+/* A unit's elements in this thread; -infinity outside [lo, hi), and for a NaN
+ * if `clean`. */
 template <bool F32>
-__global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const __grid_constant__ gpuos_devdesc d)
+DEV void top_load(const ChooseRow<F32> &r, uint32_t u0, uint32_t lo, uint32_t hi, float (&x)[GPUOS_TOP_UNIT][8])
 {
-    __shared__ TopBlock s;
-    const uint32_t V = d.dims[1], K = d.dims[3], t = threadIdx.x, S = d.ntiles / d.dims[0]; /* (runs of a row) */
-    const uint32_t row = blockIdx.x / S, part = blockIdx.x - row * S;
-    kv4_after_previous();
-    const ChooseRow<F32> r(d.a, row, d.dims[2], V);
-    const uint32_t run = ((V + 7u + S - 1u) / S + 255u) & ~255u, from = part * run;
-    const uint32_t lo = max(from, r.lo), hi = min(from + run, r.hi);
-    const float none = __int_as_float(0x7FFFFFFF); /* NaN: not an element */
-    float m = -FLT_MAX, l = 0.0f;
-    if (t == 0) s.count = 0, s.bar = 0;
+#pragma unroll
+    for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+        choose_load8(r, u0 + (u * GPUOS_TOPB_THREADS + threadIdx.x) * 8u, lo, hi, -INFINITY, x[u]);
+}
+DEV uint32_t top_place(uint32_t u0, uint32_t u, uint32_t j) { return u0 + (u * GPUOS_TOPB_THREADS + threadIdx.x) * 8u + j; }
+/* The thread's best of a unit (0: it has none). */
+DEV uint64_t top_mine(const float (&x)[GPUOS_TOP_UNIT][8], uint32_t u0, uint32_t lo, uint32_t hi, uint32_t row_lo)
+{
+    float most = -INFINITY;
+#pragma unroll
+    for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) most = fmaxf(most, x[u][j]);
+    uint32_t at = GPUOS_FULL; /* the first of equal ones that is there */
+#pragma unroll
+    for (int u = GPUOS_TOP_UNIT - 1; u >= 0; u--)
+#pragma unroll
+        for (int j = 7; j >= 0; j--) {
+            const uint32_t p = top_place(u0, u, j);
+            if (fmaxf(x[u][j], -INFINITY) == most && p >= lo && p < hi) at = p;
+        }
+    return at == GPUOS_FULL ? 0ull : top_entry(most, at - row_lo);
+}
+DEV void top_push(TopBlock &s, uint64_t bar, float x, uint32_t p, uint32_t lo, uint32_t hi, uint32_t row_lo)
+{
+    const uint64_t e = top_entry(fmaxf(x, -INFINITY), p - row_lo);
+    if (e <= bar || p < lo || p >= hi) return;
+    const uint32_t at = atomicAdd(&s.count, 1u);
+    if (at < GPUOS_TOPB_ROOM) s.got[at] = e;
+}
+/* Gathering when the bar let more pass than there is room for (rows that rise,
+ * or lie in few places): the bar rises with each unit, exactly, so that no
+ * more than K threads' elements pass, and what is gathered is cut to the K
+ * best. Returns how many there are; every thread. */
+template <bool F32>
+__device__ __noinline__ uint32_t top_gather_slow(TopBlock &s, const ChooseRow<F32> r, uint32_t from, uint32_t lo, uint32_t hi, uint32_t K)
+{
+    const uint32_t t = threadIdx.x;
+    uint64_t bar = 0;
     __syncthreads();
+    if (t == 0) s.count = 0;
 #pragma unroll 1
     for (uint32_t u0 = from; u0 < hi; u0 += GPUOS_TOPB_UNIT) {
-        float x[GPUOS_TOP_UNIT][8], unit = -INFINITY;
-#pragma unroll
-        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) choose_load8(r, u0 + (u * GPUOS_TOPB_THREADS + t) * 8u, lo, hi, none, x[u]);
-#pragma unroll
-        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
-            const uint32_t at = u0 + (u * GPUOS_TOPB_THREADS + t) * 8u;
-            const bool whole = at >= lo && at + 8u <= hi;
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++) {
-                /* a NaN among the logits counts as -infinity */
-                if (whole || (at + j >= lo && at + j < hi)) x[u][j] = fmaxf(x[u][j], -INFINITY);
-                unit = fmaxf(unit, x[u][j]);
-            }
-        }
-        if (unit > m) {
-            const float M = fminf(unit, FLT_MAX); /* (an infinite maximum: the sum is infinite) */
-            l *= choose_exp(m - M);
-            m = M;
-        }
-        float sum[GPUOS_TOP_UNIT]; /* (sums of sums: a rounding for each unit, not for each element) */
-#pragma unroll
-        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
-            sum[u] = 0.0f;
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++) {
-                /* the difference first: the lowest of the type's values is a mask too */
-                float e;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((fmaxf(x[u][j], -INFINITY) - m) * 1.4426950408889634f));
-                sum[u] += e;
-            }
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        /* this thread's best, the first of equal ones */
-        uint64_t mine = 0;
-        uint64_t bar = s.bar;
-        if (bar == 0 || unit > choose_unkey((uint32_t)(bar >> 32))) { /* (an equal one behind the bar's is not above it) */
-            uint32_t at = GPUOS_FULL;
-#pragma unroll
-            for (int u = GPUOS_TOP_UNIT - 1; u >= 0; u--)
-#pragma unroll
-                for (int j = 7; j >= 0; j--)
-                    if (x[u][j] == unit) at = u0 + (u * GPUOS_TOPB_THREADS + t) * 8u + j - r.lo;
-            if (at != GPUOS_FULL) mine = top_entry(unit, at); /* (none of its elements is there) */
-        }
+        float x[GPUOS_TOP_UNIT][8];
+        top_load(r, u0, lo, hi, x);
+        const uint64_t mine = top_mine(x, u0, lo, hi, r.lo);
         const uint32_t above = (uint32_t)__syncthreads_count(mine > bar);
         if (above == 0) continue;
         if (above > K) {
@@ -1333,25 +1418,124 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
             __syncthreads();
             bar = s.bar;
         }
-        if (mine > bar) {
+        if (mine > bar)
+#pragma unroll
+            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; j++) top_push(s, bar, x[u][j], top_place(u0, u, j), lo, hi, r.lo);
+        __syncthreads();
+        const uint32_t n = s.count;
+        if (n > GPUOS_TOPB_FEW) { /* the K best so far, and the bar at the last of them */
+            top_sort(s, n, K);
+            if (t < K) s.got[t] = s.sorted[t];
+            if (t == 0) s.count = K;
+            bar = max(bar, s.sorted[K - 1]);
+        }
+    }
+    __syncthreads();
+    return s.count;
+}
+template <bool F32>
+__global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    __shared__ TopBlock s;
+    const uint32_t V = d.dims[1], K = d.dims[3], t = threadIdx.x, S = d.ntiles / d.dims[0]; /* (runs of a row) */
+    const uint32_t row = blockIdx.x / S, part = blockIdx.x - row * S;
+    constexpr float L2E = 1.44269504f; /* (its error is the same for every element: 1e-8 of their distance from the maximum) */
+    kv4_after_previous();
+    const ChooseRow<F32> r(d.a, row, d.dims[2], V);
+    const uint32_t run = ((V + 7u + S - 1u) / S + 255u) & ~255u, from = part * run;
+    const uint32_t lo = max(from, r.lo), hi = min(from + run, r.hi);
+    /* sum of 2^(L2E x - ml), ml = L2E m rounded; and, of units whose largest is
+     * so far from 0 that rounding would tell, the sum of e^(x - far_m) */
+    float m = -2e6f, ml = -2e6f * L2E, l = 0.0f, far_m = -FLT_MAX, far_l = 0.0f;
+    uint64_t bar = 0;
+    float barf = -INFINITY;
+    if (t == 0) s.count = 0;
+#pragma unroll 1
+    for (uint32_t u0 = from; u0 < hi; u0 += GPUOS_TOPB_UNIT) {
+        float x[GPUOS_TOP_UNIT][8], most[GPUOS_TOP_UNIT];
+        top_load(r, u0, lo, hi, x);
+#pragma unroll
+        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
+            most[u] = -INFINITY; /* (a maximum passes a NaN over) */
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++) most[u] = fmaxf(most[u], x[u][j]);
+        }
+        const float unit = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+        float sum[GPUOS_TOP_UNIT]; /* (sums of sums: a rounding for each unit, not for each element) */
+        if (fabsf(unit) <= 1e6f) {
+            if (unit > m) {
+                const float to = unit * L2E;
+                float f;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(ml - to));
+                l *= f;
+                m = unit, ml = to;
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
+                sum[u] = 0.0f;
+#pragma unroll
+                for (uint32_t j = 0; j < 8; j++) {
+                    float e;
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x[u][j], L2E, -ml)));
+                    sum[u] += e;
+                }
+            }
+            float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (!(all == all)) { /* a NaN among the logits counts as -infinity */
+                all = 0.0f;
+#pragma unroll
+                for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; j++) {
+                        float e;
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(fmaxf(x[u][j], -INFINITY), L2E, -ml)));
+                        all += e;
+                    }
+            }
+            l += all;
+        } else if (unit != -INFINITY) {
+            const float to = fmaxf(far_m, fminf(unit, FLT_MAX)); /* (an infinite maximum: the sum is infinite) */
+            far_l *= choose_exp(far_m - to);
+            far_m = to;
 #pragma unroll
             for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
 #pragma unroll
                 for (uint32_t j = 0; j < 8; j++) {
-                    if (!(x[u][j] >= choose_unkey((uint32_t)(bar >> 32))) && bar) continue;
-                    const uint64_t e = x[u][j] == x[u][j] ? top_entry(x[u][j], u0 + (u * GPUOS_TOPB_THREADS + t) * 8u + j - r.lo) : 0ull;
-                    if (e > bar) s.got[atomicAdd(&s.count, 1u)] = e;
+                    float e;
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((fmaxf(x[u][j], -INFINITY) - far_m) * L2E));
+                    far_l += e;
                 }
         }
-        __syncthreads();
-        if (s.count > GPUOS_TOPB_FEW) { /* make room: the K best so far, and a better bar */
-            top_sort(s, K);
-            if (t < K) s.got[t] = s.sorted[t];
-            if (t == 0) s.count = K, s.bar = max(s.bar, s.sorted[K - 1]);
-            __syncthreads();
+        if (u0 == from) {
+            bar = top_bar(s, top_mine(x, u0, lo, hi, r.lo), K);
+            barf = bar ? choose_unkey((uint32_t)(bar >> 32)) : -INFINITY; /* (that bar's value itself may pass) */
+        }
+        if (u0 == from ? unit >= barf : unit > barf || bar == 0) { /* (an equal one in a later unit comes after) */
+#pragma unroll
+            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
+                if (!(most[u] >= barf)) continue;
+#pragma unroll
+                for (uint32_t j = 0; j < 8; j++)
+                    if (!(x[u][j] < barf)) top_push(s, bar, x[u][j], top_place(u0, u, j), lo, hi, r.lo);
+            }
         }
     }
-    top_sort(s, K);
+    if (l > 0.0f) { /* both sums under one maximum */
+        float f;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(-fmaf(m, L2E, -ml)));
+        l *= f;
+        const float M = fmaxf(m, far_m);
+        l = l * choose_exp(m - M) + far_l * choose_exp(far_m - M);
+        m = M;
+    } else {
+        m = far_m, l = far_l;
+    }
+    __syncthreads();
+    uint32_t n = s.count;
+    if (n > GPUOS_TOPB_ROOM) n = top_gather_slow(s, r, from, lo, hi, K);
+    top_sort(s, n, K);
     top_block_softmax(s, m, l);
     if (S == 1) {
         top_block_write(d, row, s, m, l);
@@ -1366,7 +1550,6 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
         uint32_t *ctr = reinterpret_cast<uint32_t *>(d.aux2) + row;
         s.last = atom_add_acq_rel_gpu32(ctr, 1u) == S - 1u;
         if (s.last) *ctr = 0; /* left zero for the next call */
-        s.count = 0;
     }
     __syncthreads();
     if (!s.last) return;
@@ -1375,11 +1558,10 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
         const float2 ms = __ldcg(reinterpret_cast<const float2 *>(top_part(&d, row * S + t)));
         m = ms.x, l = ms.y;
     }
-    for (uint32_t i = t; i < S * K; i += GPUOS_TOPB_THREADS) {
-        const uint64_t e = __ldcg(reinterpret_cast<const unsigned long long *>(top_part(&d, row * S + i / K) + 16) + i % K);
-        if (e) s.got[atomicAdd(&s.count, 1u)] = e;
-    }
-    top_sort(s, K);
+    for (uint32_t i = t; i < S * K; i += GPUOS_TOPB_THREADS) /* (entries that are not there are 0, and below all others) */
+        s.got[i] = __ldcg(reinterpret_cast<const unsigned long long *>(top_part(&d, row * S + i / K) + 16) + i % K);
+    __syncthreads();
+    top_sort(s, S * K, K);
     top_block_softmax(s, m, l);
     top_block_write(d, row, s, m, l);
 }
@@ -1387,45 +1569,37 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
 template <bool F32>
 static int top_launch(const gpuos_devdesc &d, void *stream)
 {
-    /* runs of a row: as many as fill the GPU, but none below a unit; what a row's
-     * last block can join, and the workspace holds */
+    /* runs of a row: the number with the least elements one after another, if
+     * as many blocks as there are slots run at a time; none below a unit, no
+     * more than a row's last block can join and the workspace holds */
     gpuos_devdesc e = d;
-    const uint32_t B = d.dims[0];
-    uint32_t S = (uint32_t)(((uint64_t)d.dims[1] + 7u + GPUOS_TOPB_UNIT - 1u) / GPUOS_TOPB_UNIT);
-    const uint32_t fill = (GPUOS_TOPB_BLOCKS + B - 1u) / B;
-    S = min(min(S, fill), min(32u, GPUOS_TOP_TILES / min(B, (uint32_t)GPUOS_TOP_TILES)));
-    e.ntiles = B * S;
+    const uint64_t B = d.dims[0], V = d.dims[1];
+    const uint64_t most = min(min((V + 7u + GPUOS_TOPB_UNIT - 1u) / GPUOS_TOPB_UNIT, (uint64_t)32u), GPUOS_TOP_TILES / B);
+    uint64_t S = 1, least = ~0ull;
+    for (uint64_t n = 1; n <= most || n == 1; n++) {
+        const uint64_t cost = (B * n + GPUOS_TOPB_SLOTS - 1u) / GPUOS_TOPB_SLOTS * (V / n + GPUOS_TOPB_FIXED);
+        if (cost < least) least = cost, S = n;
+    }
+    e.ntiles = (uint32_t)(B * S);
     return choose_launch(gpuos_top_kernel<F32>, dim3(e.ntiles), GPUOS_TOPB_THREADS, 0, stream, e);
 }
 
 /* ---------------------------------------------------------------------------
  * The experts of a token, launched: sixteen lanes a token, neighbouring
  * experts in a lane, so that a group is one lane's or a few neighbours'. What
- * may be among the K best are the values not below the (K + 1)-th best of the
- * lanes' own best; they are gathered, and ranked by comparing all with all.
+ * may be among the K best are the values that reach a bar which K + 1 of the
+ * lanes' own best reach; they are gathered, and ranked by comparing all with
+ * all. Values are floats to the end; NaN is what may not be chosen.
  * ------------------------------------------------------------------------- */
 #define GPUOS_ROUTEB_THREADS 128
-#define GPUOS_ROUTEB_BLOCKS 1824u /* at most: twelve for each SM */
-#define GPUOS_ROUTEB_LANES 16u
-#define GPUOS_ROUTEB_ROOM 128u /* gathered values of a token at most; more: the token goes the general way */
+#define GPUOS_ROUTEB_BLOCKS 1216u /* at most: eight for each SM, that run at a time */
+#define GPUOS_ROUTEB_ROOM 128u /* gathered values of a token at most; more: the token goes the sure way */
 #define GPUOS_ROUTEB_MAX_K 15u
-struct RouteGot {
-    uint64_t e; /* value and expert, as one number to compare by */
-    float x;    /* the logit */
-    float pad;
-};
 struct RouteToken {
-    RouteGot got[GPUOS_ROUTEB_ROOM];
-    RouteGot best[GPUOS_ROUTEB_LANES];
-    uint32_t count, pad[3];
+    uint64_t got[GPUOS_ROUTEB_ROOM]; /* value and expert, as one number to compare by */
+    uint64_t best[16];
 };
 /* Over a token's sixteen lanes. */
-DEV uint32_t half_min(uint32_t v)
-{
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) v = min(v, __shfl_xor_sync(GPUOS_FULL, v, o));
-    return v;
-}
 DEV float half_max(float v)
 {
 #pragma unroll
@@ -1438,187 +1612,194 @@ DEV float half_sum(float v)
     for (int o = 1; o < 16; o <<= 1) v += __shfl_xor_sync(GPUOS_FULL, v, o);
     return v;
 }
-/* The n-th largest (1 <= n <= 16) of the half's keys. */
-DEV uint32_t half_nth(uint32_t key, uint32_t n)
+/* The lanes' values from the largest down. */
+DEV float half_sort(float v)
 {
     const uint32_t lane = lane_id() & 15u;
 #pragma unroll
     for (uint32_t size = 2; size <= 16; size <<= 1)
 #pragma unroll
         for (uint32_t o = size >> 1; o; o >>= 1) {
-            const uint32_t other = __shfl_xor_sync(GPUOS_FULL, key, (int)o);
+            const float other = __shfl_xor_sync(GPUOS_FULL, v, (int)o);
             const bool down = (lane & size) == 0 || size == 16, first = (lane & o) == 0;
-            key = down == first ? max(key, other) : min(key, other);
+            v = down == first ? fmaxf(v, other) : fminf(v, other);
         }
-    return __shfl_sync(GPUOS_FULL, key, (int)((lane_id() & 16u) + n - 1u));
+    return v;
 }
-/* ... of two keys of each lane, a >= b: those above it are counted. */
-DEV uint32_t half_nth2(uint32_t a, uint32_t b, uint32_t n)
-{
-    uint32_t above_a = 0, above_b = 0;
-#pragma unroll
-    for (int o = 0; o < 16; o++) {
-        const uint32_t x = __shfl_xor_sync(GPUOS_FULL, a, o), y = __shfl_xor_sync(GPUOS_FULL, b, o);
-        above_a += (x > a) + (y > a);
-        above_b += (x > b) + (y > b);
-    }
-    /* (equal keys leave gaps: the least that fewer than n are above) */
-    return half_min(above_b < n ? b : (above_a < n ? a : GPUOS_FULL));
-}
-/* For choosing only: fewer instructions, and off by at most 2^-21 of itself and
- * 2^-23 (1 + |x|) where x is negative. */
+/* For choosing only: few instructions, and off by at most 2^-21 of itself and
+ * |x| 2^-23 of itself where x is negative. */
 DEV float route_sigmoid_fast(float x)
 {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(x * -1.4426950408889634f, 126.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(x * -1.44269504f, 126.0f)));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
-/* VPL >= values a lane; P = how many it has; VEC: they are whole 16-byte vectors */
+/* VPL >= values a lane; VEC: as many, and whole 16-byte vectors */
 template <bool F32, int VPL, bool VEC>
-__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS) gpuos_route_kernel(const __grid_constant__ gpuos_devdesc d)
+__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos_route_kernel(const __grid_constant__ gpuos_devdesc d)
 {
-    __shared__ RouteToken tokens[GPUOS_ROUTEB_THREADS / GPUOS_ROUTEB_LANES];
+    __shared__ RouteToken tokens[GPUOS_ROUTEB_THREADS / 16];
+    const float none = __int_as_float(0x7FFFFFFF);
     const uint32_t lane = lane_id(), sub = lane & 15u, warp = threadIdx.x >> 5;
     RouteToken &s = tokens[warp * 2u + (lane >> 4)];
     kv4_after_previous();
     RouteArgs a;
     route_args(&d, a);
     const uint32_t rows = a.rows ? (uint32_t)max(__ldg(a.rows), 0) : a.N;
-    const uint32_t P = (a.E + 15u) / 16u, first = sub * P; /* this lane's experts */
-    const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, top2 = a.flags & GPUOS_ROUTE_TOP2;
-    const bool summed = a.G > 1 && top2; /* (groups go by scores, experts without a bias by logits) */
+    const uint32_t P = VEC ? (uint32_t)VPL : (a.E + 15u) / 16u, first = sub * P; /* this lane's experts */
+    const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, summed = a.G > 1 && a.flags & GPUOS_ROUTE_TOP2, biased = a.bias != nullptr;
+    const bool norm = a.flags & GPUOS_ROUTE_NORM;
+    const uint32_t span = 16u / a.G, group = sub / span; /* lanes of a group */
+    /* of K + 1 that reach the bar, how many are lanes' best, and lanes' second best */
+    const uint32_t live = a.keep * span, ones = min(live, a.G > 1 ? (2u * a.K + 4u) / 3u : a.K + 1u), twos = a.K + 1u - ones;
+    float bias[VPL], wide = 0.0f;
+    if (biased) {
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            bias[i] = VEC || (i < (int)P && first + i < a.E) ? fmaxf(__ldg(a.bias + first + i), -INFINITY) : 0.0f;
+            if (fabsf(bias[i]) <= FLT_MAX) wide = fmaxf(wide, fabsf(bias[i]));
+        }
+        wide = half_max(wide) + 1.0f; /* no value is larger */
+    }
     const uint32_t step = gridDim.x * (GPUOS_ROUTEB_THREADS / 16u);
 #pragma unroll 1
     for (uint32_t n0 = (blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + warp) * 2u; n0 < a.N; n0 += step) {
-        const uint32_t n = min(n0 + (lane >> 4), a.N - 1u); /* (the last token's lanes may do it twice) */
+        const uint32_t n = min(n0 + (lane >> 4), a.N - 1u); /* (the last token may be done twice) */
         const bool pad = n >= rows;
         const unsigned char *row = reinterpret_cast<const unsigned char *>(d.a) + ((uint64_t)n * a.ld + first) * (F32 ? 4u : 2u);
-        float x[VPL];
+        float c[VPL]; /* what is chosen by */
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < VPL; i += F32 ? 4 : 8) {
                 const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row) + i / (F32 ? 4 : 8));
                 if (F32) {
-                    x[i] = __uint_as_float(v.x), x[i + 1] = __uint_as_float(v.y), x[i + 2] = __uint_as_float(v.z), x[i + 3] = __uint_as_float(v.w);
+                    c[i] = __uint_as_float(v.x), c[i + 1] = __uint_as_float(v.y), c[i + 2] = __uint_as_float(v.z), c[i + 3] = __uint_as_float(v.w);
                 } else {
                     float f[8];
                     unpack8(v, f);
 #pragma unroll
-                    for (int j = 0; j < 8 && i + j < VPL; j++) x[i + j] = f[j];
+                    for (int j = 0; j < 8 && i + j < VPL; j++) c[i + j] = f[j];
                 }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; i++) {
-                x[i] = -INFINITY;
+                c[i] = -INFINITY;
                 if (i < (int)P && first + i < a.E)
-                    x[i] = F32 ? __ldg(reinterpret_cast<const float *>(row) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(row) + i));
+                    c[i] = F32 ? __ldg(reinterpret_cast<const float *>(row) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(row) + i));
             }
         }
         float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) x[i] = fmaxf(x[i], -INFINITY), most = fmaxf(most, x[i]);
+        for (int i = 0; i < VPL; i++) c[i] = fmaxf(c[i], -INFINITY), most = fmaxf(most, c[i]); /* (a NaN counts as -infinity) */
         most = fminf(half_max(most), FLT_MAX);
         float inv = 1.0f; /* (a softmax whose scores are only divided by one another does without its sum) */
-        if (!sigmoid && (a.bias || summed || !(a.flags & GPUOS_ROUTE_NORM))) {
+        if (!sigmoid && (biased || summed || !norm)) {
             float total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < VPL; i++) total += route_score(false, x[i], most, 1.0f);
+            for (int i = 0; i < VPL; i++) total += route_score(false, c[i], most, 1.0f);
             total = half_sum(total);
             inv = total > 0.0f ? 1.0f / total : 0.0f;
         }
-        uint32_t key[VPL];
-        float wide = 0.0f;
+        if (biased) {
 #pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            float c = x[i];
-            if (a.bias) c = sigmoid ? (x[i] == -INFINITY ? 0.0f : route_sigmoid_fast(x[i])) : route_score(false, x[i], most, inv);
-            const bool here = VEC || (i < (int)P && first + i < a.E);
-            if (a.bias && here) {
-                c = fmaxf(c + __ldg(a.bias + first + i), -INFINITY);
-                if (fabsf(c) <= FLT_MAX) wide = fmaxf(wide, fabsf(c));
-            }
-            key[i] = here ? choose_key(c) : 0u;
+            for (int i = 0; i < VPL; i++) c[i] = (sigmoid ? route_sigmoid_fast(c[i]) : route_score(false, c[i], most, inv)) + bias[i];
         }
-        /* what two values may differ by and yet be the other way round */
+        /* What two values may differ by and yet be the other way round: twice a
+         * value's error. A sigmoid's is 2^-21 of itself (ex2 2^-22, the reciprocal
+         * and a sum) and, where x < 0, 1.5 |x| 2^-24 of itself (its argument's
+         * rounding); |x| s(x) is at most (1 + |most|) s(most) there. A softmax's
+         * 2^-19 (its sum's errors too). A sum with the bias: 2^-24 more of itself. */
         const float low = fminf(most, 0.0f);
-        const float unsure = route_score(sigmoid, most, most, inv) * (sigmoid ? 0x1.4p-20f - low * 0x1p-21f : 0x1p-18f) + half_max(wide) * 0x1p-22f;
+        const float unsure = (sigmoid ? route_sigmoid_fast(most) * (0x1.8p-20f - low * 0x1p-21f) : inv * 0x1p-18f) + wide * 0x1p-22f;
         bool sure = !sigmoid || most >= -60.0f || most == -INFINITY;
-        uint32_t one = 0, two = 0; /* the lane's two best */
+        if (!VEC) {
 #pragma unroll
-        for (int i = 0; i < VPL; i++) two = max(two, min(one, key[i])), one = max(one, key[i]);
-        if (a.G > 1) {
-            uint32_t g1 = one, g2 = two;
-            const uint32_t span = 16u / a.G, g = sub / span; /* (lanes of a group) */
-            for (uint32_t o = 1; o < span; o <<= 1) {
-                const uint32_t o1 = __shfl_xor_sync(GPUOS_FULL, g1, (int)o), o2 = __shfl_xor_sync(GPUOS_FULL, g2, (int)o);
-                g2 = max(min(g1, o1), max(g2, o2));
-                g1 = max(g1, o1);
-            }
-            uint32_t mine = g1;
-            if (top2) {
-                float v1 = choose_unkey(g1), v2 = choose_unkey(g2);
-                if (!a.bias) v1 = route_score(sigmoid, v1, most, inv), v2 = route_score(sigmoid, v2, most, inv);
-                mine = choose_key(v1 + v2);
-            }
-            uint32_t rank = 0, next = 0;
-            for (uint32_t k = 0; k < a.G; k++) {
-                const uint32_t v = __shfl_sync(GPUOS_FULL, mine, (int)((lane & 16u) + k * span));
-                const bool ahead = v > mine || (v == mine && k < g);
-                rank += ahead;
-                if (!ahead && k != g) next = max(next, v); /* the best behind this one */
-            }
-            if ((a.bias || top2) && rank == a.keep - 1u && a.keep < a.G && choose_unkey(mine) - choose_unkey(next) <= 2.0f * unsure) sure = false;
-            if (rank >= a.keep) {
-                one = two = 0;
-#pragma unroll
-                for (int i = 0; i < VPL; i++) key[i] = 0u;
-            }
+            for (int i = 0; i < VPL; i++)
+                if (i >= (int)P || first + i >= a.E) c[i] = none;
         }
-        /* the (K + 1)-th best of the lanes' best, or of their two best where groups are shut (1: all that is there) */
-        const uint32_t bar = max(a.G > 1 ? half_nth2(one, two, a.K + 1u) : half_nth(one, a.K + 1u), 1u);
-        if (sub == 0) s.count = 0;
-        __syncwarp();
-        if (one >= bar) {
+        float one = -INFINITY, two = -INFINITY; /* the lane's two best */
+#pragma unroll
+        for (int i = 0; i < VPL; i++) two = fmaxf(two, fminf(one, c[i] == c[i] ? c[i] : -INFINITY)), one = fmaxf(one, c[i]);
+        bool shut = false;
+        if (a.G > 1) {
+            float g1 = one, g2 = two;
+            for (uint32_t o = 1; o < span; o <<= 1) {
+                const float o1 = __shfl_xor_sync(GPUOS_FULL, g1, (int)o), o2 = __shfl_xor_sync(GPUOS_FULL, g2, (int)o);
+                g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
+                g1 = fmaxf(g1, o1);
+            }
+            float mine = g1;
+            if (summed) mine = biased ? g1 + g2 : route_score(sigmoid, g1, most, inv) + route_score(sigmoid, g2, most, inv);
+            uint32_t rank = 0;
+            float next = -INFINITY; /* the best behind this group */
+            for (uint32_t k = 0; k < a.G; k++) {
+                const float v = __shfl_sync(GPUOS_FULL, mine, (int)((lane & 16u) + k * span));
+                const bool ahead = v > mine || (v == mine && k < group);
+                rank += ahead;
+                if (!ahead && k != group) next = fmaxf(next, v);
+            }
+            if ((biased || summed) && rank == a.keep - 1u && a.keep < a.G && mine - next <= 2.0f * unsure) sure = false;
+            shut = rank >= a.keep;
+            if (shut) one = two = -INFINITY;
+        }
+        float bar = __shfl_sync(GPUOS_FULL, half_sort(one), (int)((lane & 16u) + ones - 1u));
+        if (twos) {
+            const float b = __shfl_sync(GPUOS_FULL, half_sort(two), (int)((lane & 16u) + min(twos, 16u) - 1u));
+            bar = twos <= live ? fminf(bar, b) : -INFINITY;
+        }
+        uint32_t count = 0; /* of this lane's that reach it */
+#pragma unroll
+        for (int i = 0; i < VPL; i++) count += c[i] >= bar;
+        if (shut) count = 0;
+        uint32_t have = count;
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(GPUOS_FULL, have, o, 16);
+            if (sub >= (uint32_t)o) have += v;
+        }
+        uint32_t at = have - count;
+        have = __shfl_sync(GPUOS_FULL, have, 15, 16);
+        if (have > GPUOS_ROUTEB_ROOM) sure = false, have = GPUOS_ROUTEB_ROOM;
+        if (count) {
 #pragma unroll
             for (int i = 0; i < VPL; i++) {
-                if (key[i] < bar) continue;
-                const uint32_t at = atomicAdd(&s.count, 1u);
-                if (at < GPUOS_ROUTEB_ROOM) {
-                    s.got[at].e = (uint64_t)key[i] << 32 | (GPUOS_FULL - (first + i));
-                    s.got[at].x = x[i];
-                }
+                if (!(c[i] >= bar)) continue;
+                if (at < GPUOS_ROUTEB_ROOM) s.got[at] = top_entry(c[i], first + i);
+                at++;
             }
         }
         __syncwarp();
-        const uint32_t count = s.count;
-        if (count > GPUOS_ROUTEB_ROOM) sure = false;
-        const uint32_t have = min(count, GPUOS_ROUTEB_ROOM);
         for (uint32_t i = sub; i < have; i += 16u) {
-            const RouteGot c = s.got[i];
+            const uint64_t e = s.got[i];
             uint32_t rank = 0;
-            for (uint32_t k = 0; k < have; k++) rank += s.got[k].e > c.e;
-            if (rank <= a.K) s.best[rank] = c; /* (K <= 15) */
+#pragma unroll 4
+            for (uint32_t k = 0; k < have; k++) rank += s.got[k] > e;
+            if (rank <= a.K) s.best[rank] = e; /* (K <= 15) */
         }
         __syncwarp();
-        const RouteGot c = s.best[sub];
-        const uint32_t id = GPUOS_FULL - (uint32_t)c.e;
-        if (a.bias && sub < a.K && sub + 1u < have) {
+        const bool chosen = sub < a.K;
+        const uint64_t e = s.best[chosen ? sub : 0u];
+        const uint32_t id = GPUOS_FULL - (uint32_t)e;
+        const uint64_t logit = (uint64_t)n * a.ld + id;
+        const float x = fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + logit) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + logit)), -INFINITY);
+        if (biased && chosen && sub + 1u < have) {
             /* values that may have swapped, unless they are of equal logits and biases */
-            const RouteGot o = s.best[sub + 1u];
-            if (choose_unkey((uint32_t)(c.e >> 32)) - choose_unkey((uint32_t)(o.e >> 32)) <= unsure &&
-                !(c.x == o.x && __ldg(a.bias + id) == __ldg(a.bias + (GPUOS_FULL - (uint32_t)o.e))))
-                sure = false;
+            const uint64_t o = s.best[sub + 1u];
+            if (choose_unkey((uint32_t)(e >> 32)) - choose_unkey((uint32_t)(o >> 32)) <= unsure) {
+                const uint32_t other = GPUOS_FULL - (uint32_t)o;
+                if (!(x == route_logit(&d, a, n, other) && __ldg(a.bias + id) == __ldg(a.bias + other))) sure = false;
+            }
         }
-        if (sigmoid && sub < a.K && c.x < -80.0f && c.x != -INFINITY) sure = false; /* (its weight may be all that is seen) */
-        float w = sub < a.K ? route_score(sigmoid, c.x, most, inv) : 0.0f;
-        if (a.flags & GPUOS_ROUTE_NORM) {
+        if (sigmoid && chosen && x < -80.0f && x != -INFINITY) sure = false; /* (its weight may be all that is seen) */
+        float w = chosen ? route_score(sigmoid, x, most, inv) : 0.0f;
+        if (norm) {
             const float sum = half_sum(w);
             if (sum != 0.0f) w /= sum;
         }
         const uint32_t again = __ballot_sync(GPUOS_FULL, !sure && !pad);
-        if (sub < a.K && !(again >> (lane & 16u) & 0xFFFFu)) {
+        if (chosen && !(again >> (lane & 16u) & 0xFFFFu)) {
             a.ids[(uint64_t)n * a.K + sub] = pad ? GPUOS_FULL : id;
             a.weights[(uint64_t)n * a.K + sub] = pad ? 0.0f : w * a.scale;
         }
@@ -1837,7 +2018,9 @@ static int choose_eager_launch(const gpuos_devdesc &d, void *stream)
 static int choose_preload()
 {
     const void *const all[] = {
-        (const void *)gpuos_adjust_kernel<true, 512>, (const void *)gpuos_adjust_kernel<false, 512>,
+        (const void *)gpuos_adjust_kernel<true, true, 512, 1>, (const void *)gpuos_adjust_kernel<true, true, 512, 4>,
+        (const void *)gpuos_adjust_kernel<true, false, 512, 1>, (const void *)gpuos_adjust_kernel<true, false, 512, 4>, (const void *)gpuos_adjust_kernel<false, true, 512, 1>, (const void *)gpuos_adjust_kernel<false, true, 512, 4>,
+        (const void *)gpuos_adjust_kernel<false, false, 512, 1>, (const void *)gpuos_adjust_kernel<false, false, 512, 4>,
         (const void *)gpuos_top_kernel<true>, (const void *)gpuos_top_kernel<false>,
         (const void *)gpuos_route_kernel<true, 4, true>, (const void *)gpuos_route_kernel<true, 8, true>,
         (const void *)gpuos_route_kernel<true, 16, true>, (const void *)gpuos_route_kernel<true, 32, true>,

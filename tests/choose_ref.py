@@ -16,9 +16,9 @@ def bf16(x):
     return np.where(np.isnan(x), x, r)
 
 
-def _fp32(x):
-    """x with what fp32 cannot hold infinite, as its arithmetic leaves it."""
-    return np.where(np.abs(x) >= 3.4028235677973366e38, np.copysign(np.inf, x), x)
+def _held(x, f32):
+    """x with what the type cannot hold infinite (beyond its largest and half a step)."""
+    return np.where(np.abs(x) >= (3.4028235677973366e38 if f32 else 3.3961775292304e38), np.copysign(np.inf, x), x)
 
 
 def adjust(logits, settings, tokens, bias, mask, f32):
@@ -34,19 +34,17 @@ def adjust(logits, settings, tokens, bias, mask, f32):
         c = np.bincount(own, minlength=V).astype(np.float64)
         x = logits[b].astype(np.float64)
         with np.errstate(all="ignore"):
-            y = _fp32(np.where(seen, np.where(x > 0, x / rep, x * rep), x))
+            y = np.where(seen, np.where(x > 0, x / rep, x * rep), x)
             off = np.where(c > 0, freq * c + pres, 0.0)
             add = np.zeros(V)
             for e in (bias[b, :s["biases"]] if bias is not None else []):
                 if 0 <= e["token"] < V:
                     add[e["token"]] = e["value"]
             t = temp if temp > 0 else 1.0
-            # roundings, each 2^-24 of a part: 1 / rep and the product (or one), the penalty's, the difference's, the
-            # sum's, 1 / temperature and the product
+            # roundings, each 2^-24 of a part: 1 / temperature, that over (or times) rep, frequency, presence; the penalty's;
+            # the multiply-adds'
             part = np.abs(y) + np.abs(off) + np.abs(add)
-            y = _fp32(_fp32(_fp32(y - off) + add) / t)
-            if not f32:  # (the largest bfloat16 and half a step)
-                y = np.where(np.abs(y) >= 3.3961775292304e38, np.copysign(np.inf, y), y)
+            y = _held((y - off + add) / t, f32)
             near = 8 * 2.0 ** -24 * part / t
             tol[b] = np.where(np.isfinite(y), near + HALF_STEP[f32] * (np.abs(y) + near) + 2.0 ** -133, 0.0)
         if s["mask"] >= 0:
