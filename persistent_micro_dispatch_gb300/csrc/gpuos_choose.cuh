@@ -660,9 +660,9 @@ __device__ __noinline__ void op_y_sure(const gpuos_devdesc *d, uint32_t n)
     double inv = 0.0;
     if (!sigmoid) {
         double total = 0.0;
-#pragma unroll 1
+#pragma unroll 2
         for (uint32_t i = 0; i < V; i++)
-            if (lane + 32u * i < a.E) total += route_score(false, (double)route_logit(d, a, n, lane + 32u * i), (double)most, 1.0);
+            total += lane + 32u * i < a.E ? route_score(false, (double)route_logit(d, a, n, lane + 32u * i), (double)most, 1.0) : 0.0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(GPUOS_FULL, total, o);
         inv = total > 0.0 ? 1.0 / total : 0.0;
@@ -1019,6 +1019,16 @@ static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint3
     (void)cudaGetLastError(); /* reported here */
     return -1;
 }
+/* Let a kernel have more shared memory than 48 KB, once for each device. */
+static int choose_smem(const void *kernel, uint32_t bytes, std::atomic<bool> (&known)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+    if (known[dev].load(std::memory_order_relaxed)) return 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return -1;
+    known[dev].store(true, std::memory_order_relaxed);
+    return 0;
+}
 /* Every thread of the cluster's blocks; what each wrote before, also to the
  * others' shared memory, is seen after. */
 DEV void choose_cluster_sync()
@@ -1096,24 +1106,28 @@ DEV void adjust_unpack(const AdjustRaw<F32, SAME> &raw, uint32_t r, float (&x)[8
  * its share of the request's tokens, and adds to the counter of whichever has
  * the token, in that block's shared memory) */
 template <bool F32, bool SAME, int THREADS, int CLUSTER>
-__global__ void __launch_bounds__(THREADS) gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
+__global__ void __launch_bounds__(THREADS, 1280 / THREADS) gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
 {
     constexpr uint32_t CHUNK = THREADS * 16u;
     extern __shared__ __align__(16) uint32_t adjust_ctr[]; /* CHUNK counters */
     __shared__ int32_t listed[THREADS];
     kv4_after_previous();
     const uint32_t V = d.dims[1], b = blockIdx.y, t = threadIdx.x;
-    AdjustArgs a;
-    if (!adjust_args(&d, b, a)) return; /* (all of a row's blocks) */
     const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
     const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi); /* (a cluster's last may be empty) */
     const uint32_t shift = in.lo - out.lo, r = SAME ? 0u : shift & (F32 ? 3u : 7u); /* (modulo 2^32, like the places) */
     AdjustRaw<F32, SAME> raw[2];
-    uint32_t bits[2] = {0xFFu, 0xFFu};
 #pragma unroll
     for (uint32_t k = 0; k < 2; k++) {
         const uint32_t at = from + (k * THREADS + t) * 8u;
         adjust_raw(in, at + shift - r, r, at < hi, raw[k]); /* (places before 0 wrap round, and are not in the row) */
+    }
+    AdjustArgs a;
+    if (!adjust_args(&d, b, a)) return; /* (all of a row's blocks) */
+    uint32_t bits[2] = {0xFFu, 0xFFu};
+#pragma unroll
+    for (uint32_t k = 0; k < 2; k++) {
+        const uint32_t at = from + (k * THREADS + t) * 8u;
         if (a.mask && at < hi) bits[k] = adjust_bits(a, (int32_t)at - (int32_t)out.lo, V);
     }
     const bool counted = a.penal || a.q.biases > 0;
@@ -1218,6 +1232,8 @@ static int adjust_launch(const gpuos_devdesc &d, void *stream)
     constexpr uint32_t CHUNK = THREADS * 16u;
     uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + CHUNK - 1u) / CHUNK);
     chunks = (chunks + CLUSTER - 1u) / CLUSTER * CLUSTER;
+    static std::atomic<bool> known[64];
+    if (CHUNK * 4u > 32768u && choose_smem((const void *)gpuos_adjust_kernel<F32, SAME, THREADS, CLUSTER>, CHUNK * 4u, known) != 0) return -1;
     gpuos_devdesc e = d;
     /* (rows beyond the grid's second dimension: launches of their own) */
     for (uint32_t row = 0; row < d.dims[0]; row += 65535u) {
@@ -1236,8 +1252,8 @@ static int adjust_launch(const gpuos_devdesc &d, void *stream)
 template <bool F32, bool SAME>
 static int adjust_launch_by(const gpuos_devdesc &d, void *stream)
 {
-    if (d.dims[4] > GPUOS_ADJUSTB_LONG) return adjust_launch<F32, SAME, 512, 4>(d, stream);
-    return adjust_launch<F32, SAME, 512, 1>(d, stream);
+    if (d.dims[4] > GPUOS_ADJUSTB_LONG) return adjust_launch<F32, SAME, 1024, 1>(d, stream);
+    return adjust_launch<F32, SAME, 256, 1>(d, stream);
 }
 template <bool F32>
 static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
@@ -1289,7 +1305,7 @@ DEV uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
     const uint32_t t = threadIdx.x, lane = lane_id();
     uint64_t keep = 0;
 #pragma unroll 1
-    for (uint32_t i = 0; i < min(K, 8u); i++) {
+    for (uint32_t i = 0; i < min(K, min((K + 23u) / 8u, 8u)); i++) {
         const uint32_t hi = __reduce_max_sync(GPUOS_FULL, (uint32_t)(mine >> 32));
         const uint32_t lo = __reduce_max_sync(GPUOS_FULL, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
         const uint64_t top = (uint64_t)hi << 32 | lo;
@@ -1313,7 +1329,7 @@ DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K)
 {
     const uint32_t t = threadIdx.x;
     const uint64_t *from = s.got;
-    if (n > 64u) { /* first those that reach a bar of their own */
+    if (n > 192u) { /* first those that reach a bar of their own */
         uint64_t mine = 0;
         for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) mine = max(mine, s.got[i]);
         if (t == 0) s.left = 0;
@@ -1598,6 +1614,7 @@ static int top_launch(const gpuos_devdesc &d, void *stream)
 struct RouteToken {
     uint64_t got[GPUOS_ROUTEB_ROOM]; /* value and expert, as one number to compare by */
     uint64_t best[16];
+    double exact[GPUOS_ROUTEB_ROOM];
 };
 /* Over a token's sixteen lanes. */
 DEV float half_max(float v)
@@ -1634,6 +1651,37 @@ DEV float route_sigmoid_fast(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(x * -1.44269504f, 126.0f)));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
+}
+/* A token whose groups are sure, but not its experts: all that may be among
+ * them are gathered, and are ranked again by values in 64 bits (sigmoid scores
+ * and biases; the token's lanes, `have` alike in them). Lane `sub` has the
+ * token's expert of that rank after. */
+DEV uint32_t route_refine(const gpuos_devdesc *d, const RouteArgs &a, RouteToken &s, uint32_t n, uint32_t have, uint32_t lanes)
+{
+    const uint32_t sub = lane_id() & 15u;
+#pragma unroll 1
+    for (uint32_t i = sub; i < have; i += 16u) {
+        const uint32_t id = GPUOS_FULL - (uint32_t)s.got[i];
+        s.exact[i] = route_score(true, (double)route_logit(d, a, n, id), 0.0, 0.0) + (double)fmaxf(__ldg(a.bias + id), -INFINITY);
+    }
+    __syncwarp(lanes);
+#pragma unroll 1
+    for (uint32_t i = sub; i < have; i += 16u) {
+        const uint32_t low = (uint32_t)s.got[i];
+        const double x = s.exact[i];
+        uint32_t rank = 0;
+#pragma unroll 1
+        for (uint32_t k = 0; k < have; k++) rank += s.exact[k] > x || (s.exact[k] == x && (uint32_t)s.got[k] > low);
+        if (rank < 16u) s.best[rank] = low;
+    }
+    __syncwarp(lanes);
+    return GPUOS_FULL - (uint32_t)s.best[sub];
+}
+__device__ __noinline__ uint32_t op_y_fine(const gpuos_devdesc *d, RouteToken *s, uint32_t n, uint32_t have, uint32_t lanes)
+{
+    RouteArgs a;
+    route_args(d, a);
+    return route_refine(d, a, *s, n, have, lanes);
 }
 /* VPL >= values a lane; VEC: as many, and whole 16-byte vectors */
 template <bool F32, int VPL, bool VEC>
@@ -1749,6 +1797,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
             const float b = __shfl_sync(GPUOS_FULL, half_sort(two), (int)((lane & 16u) + min(twos, 16u) - 1u));
             bar = twos <= live ? fminf(bar, b) : -INFINITY;
         }
+        if (biased) bar -= unsure; /* (what may be the other way round is gathered too) */
         uint32_t count = 0; /* of this lane's that reach it */
 #pragma unroll
         for (int i = 0; i < VPL; i++) count += c[i] >= bar;
@@ -1781,16 +1830,32 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
         __syncwarp();
         const bool chosen = sub < a.K;
         const uint64_t e = s.best[chosen ? sub : 0u];
-        const uint32_t id = GPUOS_FULL - (uint32_t)e;
-        const uint64_t logit = (uint64_t)n * a.ld + id;
-        const float x = fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + logit) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + logit)), -INFINITY);
-        if (biased && chosen && sub + 1u < have) {
-            /* values that may have swapped, unless they are of equal logits and biases */
-            const uint64_t o = s.best[sub + 1u];
-            if (choose_unkey((uint32_t)(e >> 32)) - choose_unkey((uint32_t)(o >> 32)) <= unsure) {
+        uint32_t id = GPUOS_FULL - (uint32_t)e;
+        auto logit = [&](uint32_t k) {
+            const uint64_t i = (uint64_t)n * a.ld + k;
+            return fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + i)), -INFINITY);
+        };
+        float x = logit(id);
+        if (biased) {
+            bool near = false;
+            if (chosen && sub + 1u < have) {
+                /* values that may have swapped, unless they are of equal logits and biases */
+                const uint64_t o = s.best[sub + 1u];
                 const uint32_t other = GPUOS_FULL - (uint32_t)o;
-                if (!(x == route_logit(&d, a, n, other) && __ldg(a.bias + id) == __ldg(a.bias + other))) sure = false;
+                near = choose_unkey((uint32_t)(e >> 32)) - choose_unkey((uint32_t)(o >> 32)) <= unsure &&
+                       !(x == logit(other) && __ldg(a.bias + id) == __ldg(a.bias + other));
             }
+            const uint32_t lanes = 0xFFFFu << (lane & 16u);
+            if (__ballot_sync(GPUOS_FULL, near && sure) & lanes) {
+                if (sigmoid) {
+                    __syncwarp(lanes); /* (best has been read) */
+                    const uint32_t fine = op_y_fine(&d, &s, n, have, lanes);
+                    if (chosen) id = fine, x = logit(id);
+                } else {
+                    sure = false;
+                }
+            }
+            __syncwarp();
         }
         if (sigmoid && chosen && x < -80.0f && x != -INFINITY) sure = false; /* (its weight may be all that is seen) */
         float w = chosen ? route_score(sigmoid, x, most, inv) : 0.0f;
@@ -1990,17 +2055,8 @@ static int plan_launch(const gpuos_devdesc &d, void *stream)
     if (d.op_id == GPUOS_OP_EXPERT_COUNT)
         return d.ntiles == 1 ? 0 : choose_launch(gpuos_plan_count_kernel, dim3(d.ntiles), GPUOS_PLANB_THREADS, 0, stream, d);
     const uint32_t smem = (GPUOS_PLANB_WARPS * d.dims[1] * 2u + 15u) & ~15u;
-    if (smem > 32768u) { /* more than a block has unasked: once per device */
-        static std::atomic<bool> known[64];
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
-        if (!known[dev].load(std::memory_order_relaxed)) {
-            if (cudaFuncSetAttribute(gpuos_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)(GPUOS_PLANB_WARPS * GPUOS_ROUTE_MAX_E * 2u)) != cudaSuccess)
-                return -1;
-            known[dev].store(true, std::memory_order_relaxed);
-        }
-    }
+    static std::atomic<bool> known[64];
+    if (smem > 32768u && choose_smem((const void *)gpuos_plan_place_kernel, GPUOS_PLANB_WARPS * GPUOS_ROUTE_MAX_E * 2u, known) != 0) return -1;
     return choose_launch(gpuos_plan_place_kernel, dim3(d.ntiles), GPUOS_PLANB_THREADS, smem, stream, d);
 }
 static int choose_eager_launch(const gpuos_devdesc &d, void *stream)
@@ -2018,9 +2074,9 @@ static int choose_eager_launch(const gpuos_devdesc &d, void *stream)
 static int choose_preload()
 {
     const void *const all[] = {
-        (const void *)gpuos_adjust_kernel<true, true, 512, 1>, (const void *)gpuos_adjust_kernel<true, true, 512, 4>,
-        (const void *)gpuos_adjust_kernel<true, false, 512, 1>, (const void *)gpuos_adjust_kernel<true, false, 512, 4>, (const void *)gpuos_adjust_kernel<false, true, 512, 1>, (const void *)gpuos_adjust_kernel<false, true, 512, 4>,
-        (const void *)gpuos_adjust_kernel<false, false, 512, 1>, (const void *)gpuos_adjust_kernel<false, false, 512, 4>,
+        (const void *)gpuos_adjust_kernel<true, true, 256, 1>, (const void *)gpuos_adjust_kernel<true, true, 1024, 1>,
+        (const void *)gpuos_adjust_kernel<true, false, 256, 1>, (const void *)gpuos_adjust_kernel<true, false, 1024, 1>, (const void *)gpuos_adjust_kernel<false, true, 256, 1>, (const void *)gpuos_adjust_kernel<false, true, 1024, 1>,
+        (const void *)gpuos_adjust_kernel<false, false, 256, 1>, (const void *)gpuos_adjust_kernel<false, false, 1024, 1>,
         (const void *)gpuos_top_kernel<true>, (const void *)gpuos_top_kernel<false>,
         (const void *)gpuos_route_kernel<true, 4, true>, (const void *)gpuos_route_kernel<true, 8, true>,
         (const void *)gpuos_route_kernel<true, 16, true>, (const void *)gpuos_route_kernel<true, 32, true>,
