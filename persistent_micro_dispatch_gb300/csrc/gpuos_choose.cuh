@@ -643,50 +643,48 @@ DEV uint32_t route_groups(const RouteArgs &a, Key &mine, Key &edge)
     }
     return kept;
 }
-/* One token's choice and weights in 64 bits. Few tokens come here, so it is
- * short: values in local memory, loops that are not unrolled. */
+/* One token's choice and weights in 64 bits. Few tokens come here, but a
+ * launch ends with the last of them: its exponentials run side by side. */
+template <int VPL>
 __device__ __noinline__ void op_y_sure(const gpuos_devdesc *d, uint32_t n)
 {
     RouteArgs a;
     route_args(d, a);
-    const uint32_t lane = lane_id(), V = (a.E + 31u) / 32u;
-    const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, top2 = a.flags & GPUOS_ROUTE_TOP2;
-    double c[GPUOS_ROUTE_MAX_E / 32];
+    const uint32_t lane = lane_id();
+    const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, top2 = a.flags & GPUOS_ROUTE_TOP2, scored = a.bias || top2;
+    uint64_t key[VPL]; /* what groups go by, in order; 0: no expert */
     float most = -INFINITY;
-#pragma unroll 1
-    for (uint32_t i = 0; i < V; i++)
+#pragma unroll
+    for (int i = 0; i < VPL; i++)
         if (lane + 32u * i < a.E) most = fmaxf(most, route_logit(d, a, n, lane + 32u * i));
     most = fminf(warp_max(most), FLT_MAX);
     double inv = 0.0;
     if (!sigmoid) {
         double total = 0.0;
-#pragma unroll 2
-        for (uint32_t i = 0; i < V; i++)
+#pragma unroll 4
+        for (int i = 0; i < VPL; i++)
             total += lane + 32u * i < a.E ? route_score(false, (double)route_logit(d, a, n, lane + 32u * i), (double)most, 1.0) : 0.0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(GPUOS_FULL, total, o);
         inv = total > 0.0 ? 1.0 / total : 0.0;
     }
-#pragma unroll 1
-    for (uint32_t i = 0; i < V; i++) {
+#pragma unroll
+    for (int i = 0; i < VPL; i++) {
         const uint32_t e = lane + 32u * i;
-        c[i] = 0.0;
-        if (e >= a.E) continue;
-        c[i] = (double)route_logit(d, a, n, e); /* without a bias the scores' order is the logits' */
-        if (a.bias || top2) c[i] = route_score(sigmoid, c[i], (double)most, inv);
-        if (a.bias) c[i] += (double)__ldcg(a.bias + e);
-        if (!(c[i] == c[i])) c[i] = -INFINITY;
+        const bool here = e < a.E;
+        double c = here ? (double)route_logit(d, a, n, e) : 0.0; /* without a bias the scores' order is the logits' */
+        if (scored) c = route_score(sigmoid, c, (double)most, inv);
+        if (a.bias && here) c += (double)fmaxf(__ldcg(a.bias + e), -INFINITY);
+        key[i] = here ? route_key(c) : 0ull;
     }
-    uint32_t kept = GPUOS_FULL;
     if (a.G > 1) {
         uint64_t mine = 0, edge;
 #pragma unroll 1
         for (uint32_t g = 0; g < a.G; g++) {
             uint64_t one = 0, two = 0;
-#pragma unroll 1
-            for (uint32_t i = 0; i < V; i++) {
-                const uint32_t e = lane + 32u * i - g * a.size;
-                const uint64_t k = e < a.size ? route_key(c[i]) : 0;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const uint64_t k = lane + 32u * i - g * a.size < a.size ? key[i] : 0ull;
                 two = max(two, min(one, k));
                 one = max(one, k);
             }
@@ -698,23 +696,31 @@ __device__ __noinline__ void op_y_sure(const gpuos_devdesc *d, uint32_t n)
             }
             if (lane == g) mine = best;
         }
-        kept = route_groups(a, mine, edge);
+        const uint32_t kept = route_groups(a, mine, edge);
+#pragma unroll
+        for (int i = 0; i < VPL; i++)
+            if (lane + 32u * i < a.E && !(kept >> ((lane + 32u * i) / a.size) & 1u)) key[i] = 0ull;
     }
-    uint32_t id = 0, taken = 0;
+    if (top2 && !a.bias) {
+#pragma unroll
+        for (int i = 0; i < VPL; i++)
+            if (key[i]) key[i] = route_key((double)route_logit(d, a, n, lane + 32u * i));
+    }
+    uint32_t id = 0;
 #pragma unroll 1
     for (uint32_t k = 0; k < a.K; k++) {
         uint64_t best = 0;
         uint32_t at = 0;
-#pragma unroll 1
-        for (uint32_t i = 0; i < V; i++) {
-            const uint32_t e = lane + 32u * i;
-            if (e >= a.E || taken >> i & 1u || !(kept >> (a.G > 1 ? e / a.size : 0u) & 1u)) continue;
-            const uint64_t key = a.bias || !top2 ? route_key(c[i]) : route_key((double)route_logit(d, a, n, e));
-            if (key > best) best = key, at = i;
-        }
+#pragma unroll
+        for (int i = VPL - 1; i >= 0; i--)
+            if (key[i] >= best) best = key[i], at = (uint32_t)i;
         const uint64_t win = route_max(best);
         const uint32_t e = __reduce_min_sync(GPUOS_FULL, best == win ? lane + 32u * at : GPUOS_FULL);
-        if (lane == (e & 31u)) taken |= 1u << (e >> 5);
+        if (lane == (e & 31u)) {
+#pragma unroll
+            for (int i = 0; i < VPL; i++)
+                if (i == (int)(e >> 5)) key[i] = 0ull;
+        }
         if (lane == k) id = e;
     }
     const double got = lane < a.K ? route_score(sigmoid, (double)route_logit(d, a, n, id), (double)most, inv) : 0.0;
@@ -837,7 +843,7 @@ DEV void route_tile(const gpuos_devdesc *d, uint32_t first, uint32_t count)
                 __stcg(a.weights + (uint64_t)n * a.K + lane, 0.0f);
             }
         } else if (!route_token<VPL>(d, a, n)) {
-            op_y_sure(d, n);
+            op_y_sure<VPL>(d, n);
         }
     }
 }
@@ -1615,6 +1621,8 @@ struct RouteToken {
     uint64_t got[GPUOS_ROUTEB_ROOM]; /* value and expert, as one number to compare by */
     uint64_t best[16];
     double exact[GPUOS_ROUTEB_ROOM];
+    float logit[GPUOS_ROUTEB_ROOM], best_logit[16];
+    uint16_t id[GPUOS_ROUTEB_ROOM];
 };
 /* Over a token's sixteen lanes. */
 DEV float half_max(float v)
@@ -1769,7 +1777,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
         }
         float one = -INFINITY, two = -INFINITY; /* the lane's two best */
 #pragma unroll
-        for (int i = 0; i < VPL; i++) two = fmaxf(two, fminf(one, c[i] == c[i] ? c[i] : -INFINITY)), one = fmaxf(one, c[i]);
+        for (int i = 0; i < VPL; i++) two = fmaxf(two, fminf(one, VEC || c[i] == c[i] ? c[i] : -INFINITY)), one = fmaxf(one, c[i]);
         bool shut = false;
         if (a.G > 1) {
             float g1 = one, g2 = two;
@@ -1782,6 +1790,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
             if (summed) mine = biased ? g1 + g2 : route_score(sigmoid, g1, most, inv) + route_score(sigmoid, g2, most, inv);
             uint32_t rank = 0;
             float next = -INFINITY; /* the best behind this group */
+#pragma unroll 4
             for (uint32_t k = 0; k < a.G; k++) {
                 const float v = __shfl_sync(GPUOS_FULL, mine, (int)((lane & 16u) + k * span));
                 const bool ahead = v > mine || (v == mine && k < group);
@@ -1798,10 +1807,11 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
             bar = twos <= live ? fminf(bar, b) : -INFINITY;
         }
         if (biased) bar -= unsure; /* (what may be the other way round is gathered too) */
-        uint32_t count = 0; /* of this lane's that reach it */
+        uint32_t reach = 0; /* this lane's that reach it */
 #pragma unroll
-        for (int i = 0; i < VPL; i++) count += c[i] >= bar;
-        if (shut) count = 0;
+        for (int i = 0; i < VPL; i++) reach |= c[i] >= bar ? 1u << i : 0u;
+        if (shut) reach = 0;
+        const uint32_t count = (uint32_t)__popc(reach);
         uint32_t have = count;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) {
@@ -1811,13 +1821,21 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
         uint32_t at = have - count;
         have = __shfl_sync(GPUOS_FULL, have, 15, 16);
         if (have > GPUOS_ROUTEB_ROOM) sure = false, have = GPUOS_ROUTEB_ROOM;
-        if (count) {
-#pragma unroll
-            for (int i = 0; i < VPL; i++) {
-                if (!(c[i] >= bar)) continue;
-                if (at < GPUOS_ROUTEB_ROOM) s.got[at] = top_entry(c[i], first + i);
-                at++;
-            }
+        for (; reach; reach &= reach - 1u, at++)
+            if (at < GPUOS_ROUTEB_ROOM) s.id[at] = (uint16_t)(first + (uint32_t)__ffs((int)reach) - 1u);
+        __syncwarp();
+        auto logit = [&](uint32_t k) {
+            const uint64_t i = (uint64_t)n * a.ld + k;
+            return fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + i)), -INFINITY);
+        };
+        /* (their values again: cheaper than to keep a lane's values in reach of any index) */
+        for (uint32_t i = sub; i < have; i += 16u) {
+            const uint32_t id = s.id[i];
+            const float x = logit(id);
+            float v = x;
+            if (biased) v = (sigmoid ? route_sigmoid_fast(x) : route_score(false, x, most, inv)) + fmaxf(__ldg(a.bias + id), -INFINITY);
+            s.got[i] = top_entry(v, id);
+            s.logit[i] = x;
         }
         __syncwarp();
         for (uint32_t i = sub; i < have; i += 16u) {
@@ -1825,25 +1843,20 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
             uint32_t rank = 0;
 #pragma unroll 4
             for (uint32_t k = 0; k < have; k++) rank += s.got[k] > e;
-            if (rank <= a.K) s.best[rank] = e; /* (K <= 15) */
+            if (rank <= a.K) s.best[rank] = e, s.best_logit[rank] = s.logit[i]; /* (K <= 15) */
         }
         __syncwarp();
         const bool chosen = sub < a.K;
         const uint64_t e = s.best[chosen ? sub : 0u];
         uint32_t id = GPUOS_FULL - (uint32_t)e;
-        auto logit = [&](uint32_t k) {
-            const uint64_t i = (uint64_t)n * a.ld + k;
-            return fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + i)), -INFINITY);
-        };
-        float x = logit(id);
+        float x = s.best_logit[chosen ? sub : 0u];
         if (biased) {
             bool near = false;
             if (chosen && sub + 1u < have) {
                 /* values that may have swapped, unless they are of equal logits and biases */
                 const uint64_t o = s.best[sub + 1u];
-                const uint32_t other = GPUOS_FULL - (uint32_t)o;
                 near = choose_unkey((uint32_t)(e >> 32)) - choose_unkey((uint32_t)(o >> 32)) <= unsure &&
-                       !(x == logit(other) && __ldg(a.bias + id) == __ldg(a.bias + other));
+                       !(x == s.best_logit[sub + 1u] && __ldg(a.bias + id) == __ldg(a.bias + (GPUOS_FULL - (uint32_t)o)));
             }
             const uint32_t lanes = 0xFFFFu << (lane & 16u);
             if (__ballot_sync(GPUOS_FULL, near && sure) & lanes) {
@@ -1868,8 +1881,8 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
             a.ids[(uint64_t)n * a.K + sub] = pad ? GPUOS_FULL : id;
             a.weights[(uint64_t)n * a.K + sub] = pad ? 0.0f : w * a.scale;
         }
-        if (again & 0xFFFFu) op_y_sure(&d, n0);
-        if (again >> 16 && n0 + 1u < a.N) op_y_sure(&d, n0 + 1u);
+        if (again & 0xFFFFu) op_y_sure<VPL <= 16 ? 8 : 32>(&d, n0);
+        if (again >> 16 && n0 + 1u < a.N) op_y_sure<VPL <= 16 ? 8 : 32>(&d, n0 + 1u);
         __syncwarp();
     }
 }
