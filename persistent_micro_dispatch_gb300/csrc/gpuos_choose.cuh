@@ -1607,46 +1607,48 @@ static int top_launch(const gpuos_devdesc &d, void *stream)
 }
 
 /* ---------------------------------------------------------------------------
- * The experts of a token, launched: sixteen lanes a token, neighbouring
+ * The experts of a token, launched: eight or sixteen lanes a token, neighbouring
  * experts in a lane, so that a group is one lane's or a few neighbours'. What
  * may be among the K best are the values that reach a bar which K + 1 of the
- * lanes' own best reach; they are gathered, and ranked by comparing all with
- * all. Values are floats to the end; NaN is what may not be chosen.
+ * lanes' best and second best reach; they are gathered, and ranked by comparing
+ * all with all. Values are floats to the end; NaN is what may not be chosen.
  * ------------------------------------------------------------------------- */
 #define GPUOS_ROUTEB_THREADS 128
-#define GPUOS_ROUTEB_BLOCKS 1216u /* at most: eight for each SM, that run at a time */
-#define GPUOS_ROUTEB_ROOM 128u /* gathered values of a token at most; more: the token goes the sure way */
+#define GPUOS_ROUTEB_ROOM 64u /* gathered values of a token at most; more: the token goes the sure way */
 #define GPUOS_ROUTEB_MAX_K 15u
 struct RouteToken {
     uint64_t got[GPUOS_ROUTEB_ROOM]; /* value and expert, as one number to compare by */
+    float2 fine[GPUOS_ROUTEB_ROOM];  /* the value as a sum of two floats */
     uint64_t best[16];
-    double exact[GPUOS_ROUTEB_ROOM];
     float logit[GPUOS_ROUTEB_ROOM], best_logit[16];
     uint16_t id[GPUOS_ROUTEB_ROOM];
 };
-/* Over a token's sixteen lanes. */
-DEV float half_max(float v)
+/* Over a token's L lanes. */
+template <int L>
+DEV float lanes_max(float v)
 {
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(GPUOS_FULL, v, o));
+    for (int o = 1; o < L; o <<= 1) v = fmaxf(v, __shfl_xor_sync(GPUOS_FULL, v, o));
     return v;
 }
-DEV float half_sum(float v)
+template <int L>
+DEV float lanes_sum(float v)
 {
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) v += __shfl_xor_sync(GPUOS_FULL, v, o);
+    for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(GPUOS_FULL, v, o);
     return v;
 }
 /* The lanes' values from the largest down. */
-DEV float half_sort(float v)
+template <int L>
+DEV float lanes_sort(float v)
 {
-    const uint32_t lane = lane_id() & 15u;
+    const uint32_t lane = lane_id() & (L - 1);
 #pragma unroll
-    for (uint32_t size = 2; size <= 16; size <<= 1)
+    for (uint32_t size = 2; size <= L; size <<= 1)
 #pragma unroll
         for (uint32_t o = size >> 1; o; o >>= 1) {
             const float other = __shfl_xor_sync(GPUOS_FULL, v, (int)o);
-            const bool down = (lane & size) == 0 || size == 16, first = (lane & o) == 0;
+            const bool down = (lane & size) == 0 || size == L, first = (lane & o) == 0;
             v = down == first ? fmaxf(v, other) : fminf(v, other);
         }
     return v;
@@ -1660,68 +1662,136 @@ DEV float route_sigmoid_fast(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
-/* A token whose groups are sure, but not its experts: all that may be among
- * them are gathered, and are ranked again by values in 64 bits (sigmoid scores
- * and biases; the token's lanes, `have` alike in them). Lane `sub` has the
- * token's expert of that rank after. */
-DEV uint32_t route_refine(const gpuos_devdesc *d, const RouteArgs &a, RouteToken &s, uint32_t n, uint32_t have, uint32_t lanes)
+/* Sums of two floats, x = h + l: Dekker's and Knuth's error-free sums, and
+ * products with the fused multiply-add ("double-double" arithmetic). */
+DEV float2 pair_sum(float a, float b)
 {
-    const uint32_t sub = lane_id() & 15u;
+    const float h = __fadd_rn(a, b), z = __fsub_rn(h, a);
+    return make_float2(h, __fadd_rn(__fsub_rn(a, __fsub_rn(h, z)), __fsub_rn(b, z)));
+}
+DEV float2 pair_add(float2 a, float2 b)
+{
+    const float2 s = pair_sum(a.x, b.x);
+    return pair_sum(s.x, __fadd_rn(s.y, __fadd_rn(a.y, b.y)));
+}
+DEV float2 pair_mul(float2 a, float2 b)
+{
+    const float h = __fmul_rn(a.x, b.x);
+    const float l = __fmaf_rn(a.x, b.y, __fmaf_rn(a.y, b.x, __fmaf_rn(a.x, b.x, -h)));
+    return pair_sum(h, l);
+}
+/* 1 / (1 + e^-x) for |x| <= 80, off by less than 2^-42: e^-x = 2^n e^r with
+ * |r| <= ln 2 / 2, e^r by its power series (terms from r^7 / 7! on, below 2^-22,
+ * in one float), the quotient by one step of Newton's. */
+DEV float2 route_sigmoid_fine(float x)
+{
+    const float t = fminf(fmaxf(-x, -80.0f), 80.0f), n = rintf(t * 1.44269504f);
+    /* ln 2 = 0x1.62ep-1 + 0x1.0bfbe8p-15 + 0x1.cf79acp-40 - ...: the first product is exact */
+    float2 r = pair_sum(__fmaf_rn(-n, 0x1.62ep-1f, t), 0.0f);
+    const float m = __fmul_rn(-n, 0x1.0bfbe8p-15f);
+    r = pair_add(r, make_float2(m, __fmaf_rn(-n, 0x1.cf79acp-40f, __fmaf_rn(-n, 0x1.0bfbe8p-15f, -m))));
+    const float y = r.x;
+    float tail = 1.0f / 479001600.0f;
+    tail = fmaf(tail, y, 1.0f / 39916800.0f);
+    tail = fmaf(tail, y, 1.0f / 3628800.0f);
+    tail = fmaf(tail, y, 1.0f / 362880.0f);
+    tail = fmaf(tail, y, 1.0f / 40320.0f);
+    tail = fmaf(tail, y, 1.0f / 5040.0f);
+    /* 1 / 720, 1 / 120, 1 / 24, 1 / 6 as sums of two floats */
+    float2 p = pair_add(make_float2(0x1.6c16c2p-10f, -0x1.27d27ep-35f), pair_sum(__fmul_rn(tail, y), 0.0f));
+    p = pair_add(make_float2(0x1.111112p-7f, -0x1.dddddep-32f), pair_mul(p, r));
+    p = pair_add(make_float2(0x1.555556p-5f, -0x1.555556p-30f), pair_mul(p, r));
+    p = pair_add(make_float2(0x1.555556p-3f, -0x1.555556p-28f), pair_mul(p, r));
+    p = pair_add(make_float2(0.5f, 0.0f), pair_mul(p, r));
+    p = pair_add(make_float2(1.0f, 0.0f), pair_mul(p, r));
+    p = pair_add(make_float2(1.0f, 0.0f), pair_mul(p, r));
+    const float f = kv4_pow2((int)n);
+    const float2 q = pair_add(make_float2(1.0f, 0.0f), make_float2(p.x * f, p.y * f));
+    const float g = __frcp_rn(q.x);
+    const float e = __fmaf_rn(-g, q.y, __fmaf_rn(-g, q.x, 1.0f));
+    return pair_sum(g, __fmul_rn(g, e));
+}
+/* What two values of that kind, or sums of two, may differ by and yet be the
+ * other way round. */
+DEV float pair_unsure(float wide) { return (1.0f + wide) * 0x1p-39f; }
+DEV float pair_less(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); } /* a - b, to a part in 2^24 */
+struct RouteKind { /* (what the ways below need of the call) */
+    const float *bias;
+    uint32_t have, lanes;
+    float wide;
+};
+/* A token whose groups are sure, but not its experts: all that may be among
+ * them are gathered, and are ranked again by finer values (sigmoid scores and
+ * biases). Every lane of the token; false if that does not tell either. Only
+ * values of equal logits and biases may be equal. */
+__device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, uint32_t K, const RouteKind q)
+{
 #pragma unroll 1
-    for (uint32_t i = sub; i < have; i += 16u) {
-        const uint32_t id = GPUOS_FULL - (uint32_t)s.got[i];
-        s.exact[i] = route_score(true, (double)route_logit(d, a, n, id), 0.0, 0.0) + (double)fmaxf(__ldg(a.bias + id), -INFINITY);
+    for (uint32_t i = sub; i < q.have; i += L) {
+        const float x = s->logit[i], b = fmaxf(__ldg(q.bias + s->id[i]), -INFINITY);
+        s->fine[i] = x == -INFINITY ? make_float2(b, 0.0f) : (fabsf(b) <= FLT_MAX ? pair_add(route_sigmoid_fine(x), make_float2(b, 0.0f)) : make_float2(b, 0.0f));
     }
-    __syncwarp(lanes);
+    __syncwarp(q.lanes);
+    bool told = true;
 #pragma unroll 1
-    for (uint32_t i = sub; i < have; i += 16u) {
-        const uint32_t low = (uint32_t)s.got[i];
-        const double x = s.exact[i];
+    for (uint32_t i = sub; i < q.have; i += L) {
+        const float2 v = s->fine[i];
+        const uint32_t id = s->id[i];
+        const float x = s->logit[i], b = fmaxf(__ldg(q.bias + id), -INFINITY);
         uint32_t rank = 0;
 #pragma unroll 1
-        for (uint32_t k = 0; k < have; k++) rank += s.exact[k] > x || (s.exact[k] == x && (uint32_t)s.got[k] > low);
-        if (rank < 16u) s.best[rank] = low;
+        for (uint32_t k = 0; k < q.have; k++) {
+            if (k == i) continue;
+            const float2 o = s->fine[k];
+            const float more = pair_less(o, v);
+            const bool alike = s->logit[k] == x && fmaxf(__ldg(q.bias + s->id[k]), -INFINITY) == b;
+            if (alike ? s->id[k] < id : more > 0.0f || o.x > v.x) rank++; /* (an infinite one's difference is NaN) */
+            if (!alike && fabsf(more) <= pair_unsure(q.wide)) told = false;
+        }
+        if (rank < 16u) s->best[rank] = s->got[i], s->best_logit[rank] = x;
     }
-    __syncwarp(lanes);
-    return GPUOS_FULL - (uint32_t)s.best[sub];
-}
-__device__ __noinline__ uint32_t op_y_fine(const gpuos_devdesc *d, RouteToken *s, uint32_t n, uint32_t have, uint32_t lanes)
-{
-    RouteArgs a;
-    route_args(d, a);
-    return route_refine(d, a, *s, n, have, lanes);
+    __syncwarp(q.lanes);
+    (void)K;
+    return told;
 }
 /* VPL >= values a lane; VEC: as many, and whole 16-byte vectors */
-template <bool F32, int VPL, bool VEC>
-__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos_route_kernel(const __grid_constant__ gpuos_devdesc d)
+template <bool F32, int L, int VPL, bool VEC>
+__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 6) gpuos_route_kernel(const __grid_constant__ gpuos_devdesc d)
 {
-    __shared__ RouteToken tokens[GPUOS_ROUTEB_THREADS / 16];
+    __shared__ RouteToken tokens[GPUOS_ROUTEB_THREADS / L];
+    __shared__ __align__(16) float biases[L][VPL + 4]; /* (four more: the lanes' vectors lie in different banks) */
+    constexpr uint32_t TOKENS = 32 / L; /* of a warp */
     const float none = __int_as_float(0x7FFFFFFF);
-    const uint32_t lane = lane_id(), sub = lane & 15u, warp = threadIdx.x >> 5;
-    RouteToken &s = tokens[warp * 2u + (lane >> 4)];
+    const uint32_t lane = lane_id(), sub = lane & (L - 1), own = lane & ~(uint32_t)(L - 1), warp = threadIdx.x >> 5;
+    const uint32_t lanes = (L == 32 ? GPUOS_FULL : (1u << L) - 1u) << own;
+    RouteToken &s = tokens[threadIdx.x / L];
     kv4_after_previous();
     RouteArgs a;
     route_args(&d, a);
     const uint32_t rows = a.rows ? (uint32_t)max(__ldg(a.rows), 0) : a.N;
-    const uint32_t P = VEC ? (uint32_t)VPL : (a.E + 15u) / 16u, first = sub * P; /* this lane's experts */
+    const uint32_t P = VEC ? (uint32_t)VPL : (a.E + L - 1u) / L, first = sub * P; /* this lane's experts */
     const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, summed = a.G > 1 && a.flags & GPUOS_ROUTE_TOP2, biased = a.bias != nullptr;
     const bool norm = a.flags & GPUOS_ROUTE_NORM;
-    const uint32_t span = 16u / a.G, group = sub / span; /* lanes of a group */
+    const uint32_t span = L / a.G, group = sub / span; /* lanes of a group */
     /* of K + 1 that reach the bar, how many are lanes' best, and lanes' second best */
-    const uint32_t live = a.keep * span, ones = min(live, a.G > 1 ? (2u * a.K + 4u) / 3u : a.K + 1u), twos = a.K + 1u - ones;
-    float bias[VPL], wide = 0.0f;
+    const uint32_t live = a.keep * span, ones = min(live, a.G == 1 && a.K < L ? a.K + 1u : (2u * a.K + 4u) / 3u), twos = a.K + 1u - ones;
+    float wide = 0.0f;
     if (biased) {
-#pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            bias[i] = VEC || (i < (int)P && first + i < a.E) ? fmaxf(__ldg(a.bias + first + i), -INFINITY) : 0.0f;
-            if (fabsf(bias[i]) <= FLT_MAX) wide = fmaxf(wide, fabsf(bias[i]));
+        for (uint32_t i = threadIdx.x; i < L * P; i += GPUOS_ROUTEB_THREADS) {
+            const float b = i < a.E ? fmaxf(__ldg(a.bias + i), -INFINITY) : 0.0f;
+            biases[i / P][i % P] = b;
         }
-        wide = half_max(wide) + 1.0f; /* no value is larger */
+        __syncthreads();
+        for (uint32_t i = sub; i < a.E; i += L) {
+            const float b = fabsf(biases[i / P][i % P]);
+            if (b <= FLT_MAX) wide = fmaxf(wide, b);
+        }
+        wide = lanes_max<L>(wide) + 1.0f; /* no value is larger */
     }
-    const uint32_t step = gridDim.x * (GPUOS_ROUTEB_THREADS / 16u);
+    const uint32_t step = gridDim.x * (GPUOS_ROUTEB_THREADS / L);
 #pragma unroll 1
-    for (uint32_t n0 = (blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + warp) * 2u; n0 < a.N; n0 += step) {
-        const uint32_t n = min(n0 + (lane >> 4), a.N - 1u); /* (the last token may be done twice) */
+    for (uint32_t n0 = (blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + warp) * TOKENS; n0 < a.N; n0 += step) {
+        const uint32_t n = min(n0 + lane / L, a.N - 1u); /* (the last token may be done twice) */
         const bool pad = n >= rows;
         const unsigned char *row = reinterpret_cast<const unsigned char *>(d.a) + ((uint64_t)n * a.ld + first) * (F32 ? 4u : 2u);
         float c[VPL]; /* what is chosen by */
@@ -1749,18 +1819,18 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
         float most = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VPL; i++) c[i] = fmaxf(c[i], -INFINITY), most = fmaxf(most, c[i]); /* (a NaN counts as -infinity) */
-        most = fminf(half_max(most), FLT_MAX);
+        most = fminf(lanes_max<L>(most), FLT_MAX);
         float inv = 1.0f; /* (a softmax whose scores are only divided by one another does without its sum) */
         if (!sigmoid && (biased || summed || !norm)) {
             float total = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPL; i++) total += route_score(false, c[i], most, 1.0f);
-            total = half_sum(total);
+            total = lanes_sum<L>(total);
             inv = total > 0.0f ? 1.0f / total : 0.0f;
         }
         if (biased) {
 #pragma unroll
-            for (int i = 0; i < VPL; i++) c[i] = (sigmoid ? route_sigmoid_fast(c[i]) : route_score(false, c[i], most, inv)) + bias[i];
+            for (int i = 0; i < VPL; i++) c[i] = (sigmoid ? route_sigmoid_fast(c[i]) : route_score(false, c[i], most, inv)) + biases[sub][i];
         }
         /* What two values may differ by and yet be the other way round: twice a
          * value's error. A sigmoid's is 2^-21 of itself (ex2 2^-22, the reciprocal
@@ -1792,18 +1862,61 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
             float next = -INFINITY; /* the best behind this group */
 #pragma unroll 4
             for (uint32_t k = 0; k < a.G; k++) {
-                const float v = __shfl_sync(GPUOS_FULL, mine, (int)((lane & 16u) + k * span));
+                const float v = __shfl_sync(GPUOS_FULL, mine, (int)(own + k * span));
                 const bool ahead = v > mine || (v == mine && k < group);
                 rank += ahead;
                 if (!ahead && k != group) next = fmaxf(next, v);
             }
-            if ((biased || summed) && rank == a.keep - 1u && a.keep < a.G && mine - next <= 2.0f * unsure) sure = false;
+            const bool near = (biased || summed) && rank == a.keep - 1u && a.keep < a.G && mine - next <= 2.0f * unsure;
+            if (__any_sync(GPUOS_FULL, near)) {
+                if (sigmoid && biased) {
+                    /* the groups' values again, finer: of what may be their best, which are few */
+                    float2 f1 = make_float2(-INFINITY, 0.0f), f2 = f1;
+                    const float from = (summed ? g2 : g1) - unsure;
+#pragma unroll 1
+                    for (uint32_t i = 0; i < P; i++) {
+                        if (first + i >= a.E) break;
+                        const uint64_t at = (uint64_t)n * a.ld + first + i;
+                        const float x = fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + at) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + at)), -INFINITY);
+                        const float b = biases[sub][i];
+                        if (!(route_sigmoid_fast(x) + b >= from)) continue;
+                        float2 v = make_float2(b, 0.0f);
+                        if (x != -INFINITY && fabsf(b) <= FLT_MAX) v = pair_add(route_sigmoid_fine(x), v);
+                        if (v.x > f1.x || (v.x == f1.x && v.y > f1.y)) f2 = f1, f1 = v;
+                        else if (v.x > f2.x || (v.x == f2.x && v.y > f2.y)) f2 = v;
+                    }
+                    __syncwarp();
+                    auto more = [](float2 p, float2 q) { return p.x > q.x || (p.x == q.x && p.y > q.y); };
+                    for (uint32_t o = 1; o < span; o <<= 1) {
+                        float2 o1 = make_float2(__shfl_xor_sync(GPUOS_FULL, f1.x, (int)o), __shfl_xor_sync(GPUOS_FULL, f1.y, (int)o));
+                        float2 o2 = make_float2(__shfl_xor_sync(GPUOS_FULL, f2.x, (int)o), __shfl_xor_sync(GPUOS_FULL, f2.y, (int)o));
+                        if (more(o1, f1)) {
+                            const float2 x1 = f1, x2 = f2;
+                            f1 = o1, f2 = o2, o1 = x1, o2 = x2;
+                        }
+                        if (more(o1, f2)) f2 = o1;
+                    }
+                    float2 value = f1;
+                    if (summed) value = f2.x == -INFINITY || fabsf(f1.x) > FLT_MAX ? make_float2(f1.x + f2.x, 0.0f) : pair_add(f1, f2);
+                    rank = 0;
+                    bool told = true;
+                    for (uint32_t k = 0; k < a.G; k++) {
+                        const float2 v = make_float2(__shfl_sync(GPUOS_FULL, value.x, (int)(own + k * span)), __shfl_sync(GPUOS_FULL, value.y, (int)(own + k * span)));
+                        if (k == group) continue;
+                        rank += more(v, value) || (v.x == value.x && v.y == value.y && k < group);
+                        if (fabsf(pair_less(v, value)) <= 2.0f * pair_unsure(wide)) told = false;
+                    }
+                    if (!told) sure = false;
+                } else if (near) {
+                    sure = false;
+                }
+            }
             shut = rank >= a.keep;
             if (shut) one = two = -INFINITY;
         }
-        float bar = __shfl_sync(GPUOS_FULL, half_sort(one), (int)((lane & 16u) + ones - 1u));
+        float bar = __shfl_sync(GPUOS_FULL, lanes_sort<L>(one), (int)(own + ones - 1u));
         if (twos) {
-            const float b = __shfl_sync(GPUOS_FULL, half_sort(two), (int)((lane & 16u) + min(twos, 16u) - 1u));
+            const float b = __shfl_sync(GPUOS_FULL, lanes_sort<L>(two), (int)(own + min(twos, (uint32_t)L) - 1u));
             bar = twos <= live ? fminf(bar, b) : -INFINITY;
         }
         if (biased) bar -= unsure; /* (what may be the other way round is gathered too) */
@@ -1814,31 +1927,28 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
         const uint32_t count = (uint32_t)__popc(reach);
         uint32_t have = count;
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(GPUOS_FULL, have, o, 16);
+        for (int o = 1; o < L; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(GPUOS_FULL, have, o, L);
             if (sub >= (uint32_t)o) have += v;
         }
         uint32_t at = have - count;
-        have = __shfl_sync(GPUOS_FULL, have, 15, 16);
+        have = __shfl_sync(GPUOS_FULL, have, L - 1, L);
         if (have > GPUOS_ROUTEB_ROOM) sure = false, have = GPUOS_ROUTEB_ROOM;
         for (; reach; reach &= reach - 1u, at++)
             if (at < GPUOS_ROUTEB_ROOM) s.id[at] = (uint16_t)(first + (uint32_t)__ffs((int)reach) - 1u);
         __syncwarp();
-        auto logit = [&](uint32_t k) {
-            const uint64_t i = (uint64_t)n * a.ld + k;
-            return fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + i)), -INFINITY);
-        };
         /* (their values again: cheaper than to keep a lane's values in reach of any index) */
-        for (uint32_t i = sub; i < have; i += 16u) {
+        for (uint32_t i = sub; i < have; i += L) {
             const uint32_t id = s.id[i];
-            const float x = logit(id);
+            const uint64_t k = (uint64_t)n * a.ld + id;
+            const float x = fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + k) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + k)), -INFINITY);
             float v = x;
             if (biased) v = (sigmoid ? route_sigmoid_fast(x) : route_score(false, x, most, inv)) + fmaxf(__ldg(a.bias + id), -INFINITY);
             s.got[i] = top_entry(v, id);
             s.logit[i] = x;
         }
         __syncwarp();
-        for (uint32_t i = sub; i < have; i += 16u) {
+        for (uint32_t i = sub; i < have; i += L) {
             const uint64_t e = s.got[i];
             uint32_t rank = 0;
 #pragma unroll 4
@@ -1847,42 +1957,42 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 5) gpuos
         }
         __syncwarp();
         const bool chosen = sub < a.K;
-        const uint64_t e = s.best[chosen ? sub : 0u];
-        uint32_t id = GPUOS_FULL - (uint32_t)e;
-        float x = s.best_logit[chosen ? sub : 0u];
+        const uint32_t mine = chosen ? sub : 0u;
         if (biased) {
             bool near = false;
             if (chosen && sub + 1u < have) {
                 /* values that may have swapped, unless they are of equal logits and biases */
-                const uint64_t o = s.best[sub + 1u];
+                const uint64_t e = s.best[sub], o = s.best[sub + 1u];
                 near = choose_unkey((uint32_t)(e >> 32)) - choose_unkey((uint32_t)(o >> 32)) <= unsure &&
-                       !(x == s.best_logit[sub + 1u] && __ldg(a.bias + id) == __ldg(a.bias + (GPUOS_FULL - (uint32_t)o)));
+                       !(s.best_logit[sub] == s.best_logit[sub + 1u] && __ldg(a.bias + (GPUOS_FULL - (uint32_t)e)) == __ldg(a.bias + (GPUOS_FULL - (uint32_t)o)));
             }
-            const uint32_t lanes = 0xFFFFu << (lane & 16u);
-            if (__ballot_sync(GPUOS_FULL, near && sure) & lanes) {
+            const uint32_t who = __ballot_sync(GPUOS_FULL, near);
+            if (who & lanes) {
                 if (sigmoid) {
                     __syncwarp(lanes); /* (best has been read) */
-                    const uint32_t fine = op_y_fine(&d, &s, n, have, lanes);
-                    if (chosen) id = fine, x = logit(id);
+                    if (!op_y_fine(&s, sub, L, a.K, RouteKind{a.bias, have, lanes, wide})) sure = false;
                 } else {
                     sure = false;
                 }
             }
             __syncwarp();
         }
+        const uint32_t id = GPUOS_FULL - (uint32_t)s.best[mine];
+        const float x = s.best_logit[mine];
         if (sigmoid && chosen && x < -80.0f && x != -INFINITY) sure = false; /* (its weight may be all that is seen) */
         float w = chosen ? route_score(sigmoid, x, most, inv) : 0.0f;
         if (norm) {
-            const float sum = half_sum(w);
-            if (sum != 0.0f) w /= sum;
+            const float sum = lanes_sum<L>(w);
+            if (sum != 0.0f) w = __fdividef(w, sum);
         }
-        const uint32_t again = __ballot_sync(GPUOS_FULL, !sure && !pad);
-        if (chosen && !(again >> (lane & 16u) & 0xFFFFu)) {
+        uint32_t again = __ballot_sync(GPUOS_FULL, !sure && !pad);
+        if (chosen && !(again & lanes)) {
             a.ids[(uint64_t)n * a.K + sub] = pad ? GPUOS_FULL : id;
             a.weights[(uint64_t)n * a.K + sub] = pad ? 0.0f : w * a.scale;
         }
-        if (again & 0xFFFFu) op_y_sure<VPL <= 16 ? 8 : 32>(&d, n0);
-        if (again >> 16 && n0 + 1u < a.N) op_y_sure<VPL <= 16 ? 8 : 32>(&d, n0 + 1u);
+#pragma unroll 1
+        for (uint32_t k = 0; again && k < TOKENS; k++, again = L == 32 ? 0u : again >> L)
+            if (again & ((1u << L) - 1u) && n0 + k < a.N) op_y_sure<L * VPL <= 256 ? 8 : 32>(&d, n0 + k);
         __syncwarp();
     }
 }
@@ -1895,30 +2005,35 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS) gpuos_route_any_kernel(c
     for (uint32_t n = blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + (threadIdx.x >> 5); n < d.dims[0]; n += step) route_tile<VPL>(&d, n, 1u);
 }
 
-template <bool F32, int VPL>
+template <bool F32, int L, int VPL>
 static int route_launch(const gpuos_devdesc &d, void *stream)
 {
-    const uint32_t tokens = GPUOS_ROUTEB_THREADS / 16u, size = F32 ? 4u : 2u;
+    const uint32_t tokens = GPUOS_ROUTEB_THREADS / L, size = F32 ? 4u : 2u;
     const uint64_t blocks = ((uint64_t)d.dims[0] + tokens - 1u) / tokens;
-    const uint32_t grid = (uint32_t)min(blocks, (uint64_t)GPUOS_ROUTEB_BLOCKS);
-    const bool vec = d.dims[1] == 16u * VPL && (VPL * size) % 16u == 0 && (d.a & 15u) == 0 && ((uint64_t)d.dims[2] * size & 15u) == 0;
-    if constexpr (VPL * (F32 ? 4 : 2) % 16 == 0) {
-        if (vec) return choose_launch(gpuos_route_kernel<F32, VPL, true>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
-    }
-    return choose_launch(gpuos_route_kernel<F32, VPL, false>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
+    const uint32_t grid = (uint32_t)min(blocks, (uint64_t)(VPL <= 16 ? 1216u : 912u)); /* as many as run at a time */
+    const bool vec = d.dims[1] == L * VPL && (VPL * size) % 16u == 0 && (d.a & 15u) == 0 && ((uint64_t)d.dims[2] * size & 15u) == 0;
+    if (vec) return choose_launch(gpuos_route_kernel<F32, L, VPL, true>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
+    return choose_launch(gpuos_route_kernel<F32, L, VPL, false>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
 }
 template <bool F32>
 static int route_launch_of(const gpuos_devdesc &d, void *stream)
 {
-    const uint32_t E = d.dims[1], G = d.dims[4] & 0xFFFFu;
-    /* sixteen lanes have to hold whole groups or equal parts of one */
-    if (d.dims[3] <= GPUOS_ROUTEB_MAX_K && E <= 512u && (G == 1u || (16u % G == 0 && E % 16u == 0))) {
-        if (E <= 64u) return route_launch<F32, 4>(d, stream);
-        if (E <= 128u) return route_launch<F32, 8>(d, stream);
-        if (E <= 256u) return route_launch<F32, 16>(d, stream);
-        return route_launch<F32, 32>(d, stream);
+    const uint32_t E = d.dims[1], K = d.dims[3], G = d.dims[4] & 0xFFFFu, keep = d.dims[4] >> 16;
+    /* a token's lanes have to hold whole groups or equal parts of one, and two
+     * values of each open lane have to be enough for a bar, or all fit */
+    auto fits = [&](uint32_t L) {
+        return (G == 1u || (L % G == 0 && E % L == 0)) && (K + 1u <= 2u * keep * (L / G) || keep * (E / G) <= GPUOS_ROUTEB_ROOM);
+    };
+    if (K <= 8u && E <= 256u && fits(8)) {
+        if (E <= 64u) return route_launch<F32, 8, 8>(d, stream);
+        if (E <= 128u) return route_launch<F32, 8, 16>(d, stream);
+        return route_launch<F32, 8, 32>(d, stream);
     }
-    const uint32_t grid = (uint32_t)min(((uint64_t)d.dims[0] + 3u) / 4u, (uint64_t)GPUOS_ROUTEB_BLOCKS);
+    if (K <= GPUOS_ROUTEB_MAX_K && E <= 512u && fits(16)) {
+        if (E <= 256u) return route_launch<F32, 16, 16>(d, stream);
+        return route_launch<F32, 16, 32>(d, stream);
+    }
+    const uint32_t grid = (uint32_t)min(((uint64_t)d.dims[0] + 3u) / 4u, (uint64_t)1216u);
     if (E <= 256u) return choose_launch(gpuos_route_any_kernel<8>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
     return choose_launch(gpuos_route_any_kernel<32>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
 }
@@ -2091,14 +2206,16 @@ static int choose_preload()
         (const void *)gpuos_adjust_kernel<true, false, 256, 1>, (const void *)gpuos_adjust_kernel<true, false, 1024, 1>, (const void *)gpuos_adjust_kernel<false, true, 256, 1>, (const void *)gpuos_adjust_kernel<false, true, 1024, 1>,
         (const void *)gpuos_adjust_kernel<false, false, 256, 1>, (const void *)gpuos_adjust_kernel<false, false, 1024, 1>,
         (const void *)gpuos_top_kernel<true>, (const void *)gpuos_top_kernel<false>,
-        (const void *)gpuos_route_kernel<true, 4, true>, (const void *)gpuos_route_kernel<true, 8, true>,
-        (const void *)gpuos_route_kernel<true, 16, true>, (const void *)gpuos_route_kernel<true, 32, true>,
-        (const void *)gpuos_route_kernel<true, 4, false>, (const void *)gpuos_route_kernel<true, 8, false>,
-        (const void *)gpuos_route_kernel<true, 16, false>, (const void *)gpuos_route_kernel<true, 32, false>,
-        (const void *)gpuos_route_kernel<false, 8, true>,
-        (const void *)gpuos_route_kernel<false, 16, true>, (const void *)gpuos_route_kernel<false, 32, true>,
-        (const void *)gpuos_route_kernel<false, 4, false>, (const void *)gpuos_route_kernel<false, 8, false>,
-        (const void *)gpuos_route_kernel<false, 16, false>, (const void *)gpuos_route_kernel<false, 32, false>,
+        (const void *)gpuos_route_kernel<true, 8, 8, true>, (const void *)gpuos_route_kernel<true, 8, 8, false>,
+        (const void *)gpuos_route_kernel<true, 8, 16, true>, (const void *)gpuos_route_kernel<true, 8, 16, false>,
+        (const void *)gpuos_route_kernel<true, 8, 32, true>, (const void *)gpuos_route_kernel<true, 8, 32, false>,
+        (const void *)gpuos_route_kernel<true, 16, 16, true>, (const void *)gpuos_route_kernel<true, 16, 16, false>,
+        (const void *)gpuos_route_kernel<true, 16, 32, true>, (const void *)gpuos_route_kernel<true, 16, 32, false>,
+        (const void *)gpuos_route_kernel<false, 8, 8, true>, (const void *)gpuos_route_kernel<false, 8, 8, false>,
+        (const void *)gpuos_route_kernel<false, 8, 16, true>, (const void *)gpuos_route_kernel<false, 8, 16, false>,
+        (const void *)gpuos_route_kernel<false, 8, 32, true>, (const void *)gpuos_route_kernel<false, 8, 32, false>,
+        (const void *)gpuos_route_kernel<false, 16, 16, true>, (const void *)gpuos_route_kernel<false, 16, 16, false>,
+        (const void *)gpuos_route_kernel<false, 16, 32, true>, (const void *)gpuos_route_kernel<false, 16, 32, false>,
         (const void *)gpuos_route_any_kernel<8>, (const void *)gpuos_route_any_kernel<32>,
         (const void *)gpuos_plan_count_kernel, (const void *)gpuos_plan_place_kernel};
     for (const void *f : all) {
