@@ -108,30 +108,29 @@ def _refuse(like: torch.Tensor, *named) -> None:
 
 def _rows(name: str, x: torch.Tensor):
     """Type, rows, columns, row distance and address of logits."""
-    dt = _DTYPE.get(x.dtype)
+    dt, shape = _DTYPE.get(x.dtype), x.shape
+    if dt is not None and len(shape) == 2 and x.get_device() >= 0:
+        n, cols = shape
+        ld, step = (cols, 1) if x.is_contiguous() or n < 2 else x.stride()
+        if n < 2:
+            step = x.stride(1)
+        if (step == 1 or cols == 1) and 1 <= cols <= ld < 1 << 32 and cols < 0x7FFFFF00 and n < 1 << 31:
+            return dt, n, cols, ld, x.data_ptr()
     if dt is None:
         raise TypeError(f"{name}: dtype {x.dtype}, wanted torch.float32 or torch.bfloat16")
     if x.ndim != 2 or not x.shape[1]:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted (rows, columns)")
     if x.get_device() < 0:
         raise ValueError(f"{name}: on {x.device}, wanted a CUDA device")
-    n, cols = x.shape
-    ld, step = x.stride()
-    if n < 2:
-        ld = cols
-    if (step != 1 and cols > 1) or not cols <= ld < 1 << 32 or cols >= 0x7FFFFF00 or n >= 1 << 31:
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, strides {x.stride()}, wanted rows that lie one behind the other")
-    return dt, n, cols, ld, x.data_ptr()
+    raise ValueError(f"{name}: shape {tuple(x.shape)}, strides {x.stride()}, wanted rows that lie one behind the other")
 
 
-def _desc(op, dtype, a, b, out, aux0, aux1, aux2, d0, d1, d2, d3, d4, d5, fparam=0.0, flags=0, dep=0) -> np.ndarray:
-    raw = bytearray(_DESC.pack(op, dtype, flags, 0, dep, 0, a, b, out, aux0, aux1, aux2, d0, d1, d2, d3, d4, d5, fparam, 0.0,
-                               0, 0, 0))
-    return np.frombuffer(raw, dtype=G.DESC_DTYPE)
-
-
-def _fit(t: torch.Tensor, dtype, shape, dev: int) -> bool:
-    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+def _desc(*records) -> np.ndarray:
+    """Descriptors of (op, dtype, flags, dep, a, b, out, aux0, aux1, aux2, dims..., fparam)."""
+    raw = bytearray()
+    for op, dt, flags, dep, a, b, out, x0, x1, x2, d0, d1, d2, d3, d4, d5, f in records:
+        raw += _DESC.pack(op, dt, flags, 0, dep, 0, a, b, out, x0, x1, x2, d0, d1, d2, d3, d4, d5, f, 0.0, 0, 0, 0)
+    return np.frombuffer(raw, G.DESC_DTYPE)
 
 
 def adjust(logits: torch.Tensor, out: torch.Tensor, settings: torch.Tensor, tokens: Optional[torch.Tensor] = None,
@@ -145,18 +144,25 @@ def adjust(logits: torch.Tensor, out: torch.Tensor, settings: torch.Tensor, toke
     bit v % 32 of word v // 32) is 0."""
     dt, B, V, ld, a = _rows("logits", logits)
     dt2, B2, V2, ldo, o = _rows("out", out)
-    dev = logits.get_device()
+    dev, sp = logits.get_device(), settings.data_ptr()
     L = M = n = tp = mp = bp = 0
-    ok = dt2 == dt and B2 == B and V2 == V and out.get_device() == dev and _fit(settings, _I32, (B, 8), dev) and not settings.data_ptr() & 15
+    ok = (dt2 == dt and B2 == B and V2 == V and out.get_device() == dev and settings.dtype is _I32 and settings.shape == (B, 8)
+          and settings.get_device() == dev and settings.is_contiguous() and not sp & 15)
     if tokens is not None:
-        L, tp = tokens.shape[-1] if tokens.ndim else 0, tokens.data_ptr()
-        ok = ok and _fit(tokens, _I32, (B, L), dev) and L <= 1 << 28
+        ts, tp = tokens.shape, tokens.data_ptr()
+        L = ts[-1] if ts else 0
+        ok = (ok and len(ts) == 2 and ts[0] == B and L <= 1 << 28 and tokens.dtype is _I32 and tokens.get_device() == dev
+              and tokens.is_contiguous())
     if mask is not None:
-        M, mp = mask.shape[0] if mask.ndim else 0, mask.data_ptr()
-        ok = ok and _fit(mask, _I32, (M, (V + 31) // 32), dev) and M < 1 << 16
+        ms, mp = mask.shape, mask.data_ptr()
+        M = ms[0] if ms else 0
+        ok = (ok and len(ms) == 2 and ms[1] == V + 31 >> 5 and M < 1 << 16 and mask.dtype is _I32 and mask.get_device() == dev
+              and mask.is_contiguous())
     if bias is not None:
-        n, bp = bias.shape[1] if bias.ndim == 3 else 0, bias.data_ptr()
-        ok = ok and _fit(bias, _I32, (B, n, 2), dev) and n < 1 << 16 and not bp & 7
+        bs, bp = bias.shape, bias.data_ptr()
+        n = bs[1] if len(bs) == 3 else 0
+        ok = (ok and len(bs) == 3 and bs[0] == B and bs[2] == 2 and n < 1 << 16 and bias.dtype is _I32 and bias.get_device() == dev
+              and bias.is_contiguous() and not bp & 7)
     if not ok or (a == o and ld != ldo):
         if dt2 != dt or (B2, V2) != (B, V) or out.get_device() != dev:
             raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, wanted {logits.dtype} {(B, V)} on {logits.device}")
@@ -165,7 +171,7 @@ def adjust(logits: torch.Tensor, out: torch.Tensor, settings: torch.Tensor, toke
         _refuse(logits, ("settings", settings, (_I32,), (B, 8), 16), ("tokens", tokens, (_I32,), (B, None), 4),
                 ("mask", mask, (_I32,), (None, (V + 31) // 32), 4), ("bias", bias, (_I32,), (B, None, 2), 8))
         raise ValueError(f"{L} tokens, {M} masks and {n} biases: at most 2^28, 65535 and 65535")
-    return _desc(_ADJUST, dt, a, tp, o, settings.data_ptr(), mp, bp, B, V, ld, ldo, L, M | n << 16)
+    return _desc((_ADJUST, dt, 0, 0, a, tp, o, sp, mp, bp, B, V, ld, ldo, L, M | n << 16, 0.0))
 
 
 def top(logits: torch.Tensor, ids: torch.Tensor, logprobs: torch.Tensor, lse: Optional[torch.Tensor],
@@ -176,16 +182,20 @@ def top(logits: torch.Tensor, ids: torch.Tensor, logprobs: torch.Tensor, lse: Op
     wanted). Descriptors that share a workspace must run one after another."""
     dt, B, V, ld, a = _rows("logits", logits)
     dev, K = logits.get_device(), ids.shape[-1] if ids.ndim else 0
-    if not (1 <= K <= MAX_TOP and K <= V and _fit(ids, _I32, (B, K), dev) and _fit(logprobs, _F32, (B, K), dev)
-            and (lse is None or _fit(lse, _F32, (B,), dev)) and _fit(workspace, _U8, workspace.shape[:1], dev)
-            and workspace.numel() >= WORKSPACE_BYTES and not workspace.data_ptr() & 15):
+    shape, wp = (B, K), workspace.data_ptr()
+    if not (1 <= K <= MAX_TOP and K <= V and ids.dtype is _I32 and ids.shape == shape and logprobs.dtype is _F32
+            and logprobs.shape == shape and ids.get_device() == dev and logprobs.get_device() == dev and ids.is_contiguous()
+            and logprobs.is_contiguous()
+            and (lse is None or (lse.dtype is _F32 and lse.shape == (B,) and lse.get_device() == dev and lse.is_contiguous()))
+            and workspace.dtype is _U8 and workspace.ndim == 1 and workspace.numel() >= WORKSPACE_BYTES
+            and workspace.get_device() == dev and workspace.is_contiguous() and not wp & 15):
         if not 1 <= K <= min(MAX_TOP, V):
             raise ValueError(f"ids: {K} of {V} tokens a row, wanted 1 to {min(MAX_TOP, V)}")
         _refuse(logits, ("ids", ids, (_I32,), (B, None), 4), ("logprobs", logprobs, (_F32,), (B, K), 4), ("lse", lse, (_F32,), (B,), 4),
                 ("workspace", workspace, (_U8,), (None,), 16))
         raise ValueError(f"workspace: {workspace.numel()} bytes, wanted {WORKSPACE_BYTES}")
-    return _desc(_TOP, dt, a, 0, ids.data_ptr(), logprobs.data_ptr(), 0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                 B, V, ld, K, 0, 0)
+    return _desc((_TOP, dt, 0, 0, a, 0, ids.data_ptr(), logprobs.data_ptr(), 0 if lse is None else lse.data_ptr(), wp, B, V, ld, K, 0, 0,
+                  0.0))
 
 
 def experts(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, *, sigmoid: bool = False,
@@ -201,10 +211,13 @@ def experts(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, *, s
     padding, with ids -1 and weights 0."""
     dt, N, E, ld, a = _rows("logits", logits)
     dev, K = logits.get_device(), ids.shape[-1] if ids.ndim else 0
+    shape = (N, K)
     if not (E <= MAX_EXPERTS and 1 <= K <= MAX_EXPERTS_PER_TOKEN and 1 <= groups <= 32 and E % groups == 0 and 1 <= keep <= groups
-            and K <= keep * (E // groups) and not (top2 and E // groups < 2) and _fit(ids, _I32, (N, K), dev)
-            and _fit(weights, _F32, (N, K), dev) and (bias is None or _fit(bias, _F32, (E,), dev))
-            and (rows is None or _fit(rows, _I32, (1,), dev))):
+            and K <= keep * (E // groups) and not (top2 and E // groups < 2) and ids.dtype is _I32 and ids.shape == shape
+            and weights.dtype is _F32 and weights.shape == shape and ids.get_device() == dev and weights.get_device() == dev
+            and ids.is_contiguous() and weights.is_contiguous()
+            and (bias is None or (bias.dtype is _F32 and bias.shape == (E,) and bias.get_device() == dev and bias.is_contiguous()))
+            and (rows is None or (rows.dtype is _I32 and rows.shape == (1,) and rows.get_device() == dev))):
         if not 1 <= E <= MAX_EXPERTS or not 1 <= groups <= 32 or E % groups or not 1 <= keep <= groups or (top2 and E // groups < 2):
             raise ValueError(f"{E} experts in {groups} groups of which {keep}: wanted at most {MAX_EXPERTS} in 1 to 32 equal groups"
                              + (" of two or more" if top2 else ""))
@@ -212,9 +225,9 @@ def experts(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, *, s
             raise ValueError(f"ids: {K} experts a token, wanted 1 to {min(MAX_EXPERTS_PER_TOKEN, keep * (E // groups))}")
         _refuse(logits, ("ids", ids, (_I32,), (N, None), 4), ("weights", weights, (_F32,), (N, K), 4), ("bias", bias, (_F32,), (E,), 4),
                 ("rows", rows, (_I32,), (1,), 4))
-    return _desc(_ROUTE, dt, a, 0 if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                 0 if rows is None else rows.data_ptr(), 0, N, E, ld, K, groups | keep << 16,
-                 (_FLAGS_SIGMOID if sigmoid else 0) | (_FLAGS_TOP2 if top2 else 0) | (_FLAGS_NORM if normalise else 0), scale)
+    return _desc((_ROUTE, dt, 0, 0, a, 0 if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                  0 if rows is None else rows.data_ptr(), 0, N, E, ld, K, groups | keep << 16,
+                  (_FLAGS_SIGMOID if sigmoid else 0) | (_FLAGS_TOP2 if top2 else 0) | (_FLAGS_NORM if normalise else 0), scale))
 
 
 def plan(ids: torch.Tensor, order: torch.Tensor, place: torch.Tensor, offsets: torch.Tensor, workspace: torch.Tensor) -> np.ndarray:
@@ -225,10 +238,13 @@ def plan(ids: torch.Tensor, order: torch.Tensor, place: torch.Tensor, offsets: t
     record, or two (a count and a placement that depends on the record before
     it) for more than 4,096 pairs. Descriptors that share a workspace must run
     one after another, these two with nothing between that shares it."""
-    dev, P, E = ids.get_device(), ids.numel(), offsets.numel() - 1
-    if not (dev >= 0 and ids.dtype is _I32 and ids.is_contiguous() and P < 0x7FFFFF00 and 1 <= E <= MAX_EXPERTS
-            and _fit(order, _I32, (P,), dev) and _fit(place, _I32, ids.shape, dev) and _fit(offsets, _I32, (E + 1,), dev)
-            and _fit(workspace, _U8, workspace.shape[:1], dev) and workspace.numel() >= WORKSPACE_BYTES and not workspace.data_ptr() & 15):
+    dev, P, E, ws = ids.get_device(), ids.numel(), offsets.numel() - 1, workspace.data_ptr()
+    if not (dev >= 0 and ids.dtype is _I32 and order.dtype is _I32 and place.dtype is _I32 and offsets.dtype is _I32
+            and P < 0x7FFFFF00 and 1 <= E <= MAX_EXPERTS and order.numel() == P and order.ndim == offsets.ndim == 1
+            and place.shape == ids.shape and order.get_device() == dev and place.get_device() == dev and offsets.get_device() == dev
+            and ids.is_contiguous() and order.is_contiguous() and place.is_contiguous() and offsets.is_contiguous()
+            and workspace.dtype is _U8 and workspace.ndim == 1 and workspace.numel() >= WORKSPACE_BYTES
+            and workspace.get_device() == dev and workspace.is_contiguous() and not ws & 15):
         if dev < 0:
             raise ValueError(f"ids: on {ids.device}, wanted a CUDA device")
         _refuse(ids, ("ids", ids, (_I32,), tuple(ids.shape), 4), ("order", order, (_I32,), (P,), 4),
@@ -237,9 +253,8 @@ def plan(ids: torch.Tensor, order: torch.Tensor, place: torch.Tensor, offsets: t
         if not 1 <= E <= MAX_EXPERTS or P >= 0x7FFFFF00:
             raise ValueError(f"{P} pairs of {E} experts: wanted below 2^31 of 1 to {MAX_EXPERTS}")
         raise ValueError(f"workspace: {workspace.numel()} bytes, wanted {WORKSPACE_BYTES}")
-    a, ws = ids.data_ptr(), workspace.data_ptr()
+    a = ids.data_ptr()
+    place_it = (_PLACE, 0, 0, 0, a, place.data_ptr(), order.data_ptr(), offsets.data_ptr(), 0, ws, P, E, 0, 0, 0, 0, 0.0)
     if P <= PLAN_ONE:
-        return _desc(_PLACE, 0, a, place.data_ptr(), order.data_ptr(), offsets.data_ptr(), 0, ws, P, E, 0, 0, 0, 0)
-    return np.concatenate((_desc(_COUNT, 0, a, 0, 0, 0, 0, ws, P, E, 0, 0, 0, 0),
-                           _desc(_PLACE, 0, a, place.data_ptr(), order.data_ptr(), offsets.data_ptr(), 0, ws, P, E, 0, 0, 0, 0, 0.0,
-                                 G.FLAG_DEP_REL, 1)))
+        return _desc(place_it)
+    return _desc((_COUNT, 0, 0, 0, a, 0, 0, 0, 0, ws, P, E, 0, 0, 0, 0, 0.0), (_PLACE, 0, G.FLAG_DEP_REL, 1) + place_it[4:])

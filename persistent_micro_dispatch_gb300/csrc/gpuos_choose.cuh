@@ -1610,12 +1610,13 @@ static int top_launch(const gpuos_devdesc &d, void *stream)
  * The experts of a token, launched: eight or sixteen lanes a token, neighbouring
  * experts in a lane, so that a group is one lane's or a few neighbours'. What
  * may be among the K best are the values that reach a bar which K + 1 of the
- * lanes' best and second best reach; they are gathered, and ranked by comparing
+ * lanes' best three reach; they are gathered, and ranked by comparing
  * all with all. Values are floats to the end; NaN is what may not be chosen.
  * ------------------------------------------------------------------------- */
 #define GPUOS_ROUTEB_THREADS 128
 #define GPUOS_ROUTEB_ROOM 64u /* gathered values of a token at most; more: the token goes the sure way */
 #define GPUOS_ROUTEB_MAX_K 15u
+#define GPUOS_ROUTEB_BLOCKS 1216u /* at most, eight for each SM: as many as run at a time */
 struct RouteToken {
     uint64_t got[GPUOS_ROUTEB_ROOM]; /* value and expert, as one number to compare by */
     float2 fine[GPUOS_ROUTEB_ROOM];  /* the value as a sum of two floats */
@@ -1715,8 +1716,8 @@ DEV float2 route_sigmoid_fine(float x)
  * other way round. */
 DEV float pair_unsure(float wide) { return (1.0f + wide) * 0x1p-39f; }
 DEV float pair_less(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); } /* a - b, to a part in 2^24 */
-struct RouteKind { /* (what the ways below need of the call) */
-    const float *bias;
+struct RouteKind {
+    const float *bias; /* (in shared memory, none NaN) */
     uint32_t have, lanes;
     float wide;
 };
@@ -1724,11 +1725,11 @@ struct RouteKind { /* (what the ways below need of the call) */
  * them are gathered, and are ranked again by finer values (sigmoid scores and
  * biases). Every lane of the token; false if that does not tell either. Only
  * values of equal logits and biases may be equal. */
-__device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, uint32_t K, const RouteKind q)
+__device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, const RouteKind q)
 {
 #pragma unroll 1
     for (uint32_t i = sub; i < q.have; i += L) {
-        const float x = s->logit[i], b = fmaxf(__ldg(q.bias + s->id[i]), -INFINITY);
+        const float x = s->logit[i], b = q.bias[s->id[i]];
         s->fine[i] = x == -INFINITY ? make_float2(b, 0.0f) : (fabsf(b) <= FLT_MAX ? pair_add(route_sigmoid_fine(x), make_float2(b, 0.0f)) : make_float2(b, 0.0f));
     }
     __syncwarp(q.lanes);
@@ -1737,29 +1738,29 @@ __device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, 
     for (uint32_t i = sub; i < q.have; i += L) {
         const float2 v = s->fine[i];
         const uint32_t id = s->id[i];
-        const float x = s->logit[i], b = fmaxf(__ldg(q.bias + id), -INFINITY);
+        const float x = s->logit[i], b = q.bias[id];
         uint32_t rank = 0;
 #pragma unroll 1
         for (uint32_t k = 0; k < q.have; k++) {
             if (k == i) continue;
             const float2 o = s->fine[k];
             const float more = pair_less(o, v);
-            const bool alike = s->logit[k] == x && fmaxf(__ldg(q.bias + s->id[k]), -INFINITY) == b;
+            const bool alike = s->logit[k] == x && q.bias[s->id[k]] == b;
             if (alike ? s->id[k] < id : more > 0.0f || o.x > v.x) rank++; /* (an infinite one's difference is NaN) */
             if (!alike && fabsf(more) <= pair_unsure(q.wide)) told = false;
         }
         if (rank < 16u) s->best[rank] = s->got[i], s->best_logit[rank] = x;
     }
     __syncwarp(q.lanes);
-    (void)K;
     return told;
 }
 /* VPL >= values a lane; VEC: as many, and whole 16-byte vectors */
 template <bool F32, int L, int VPL, bool VEC>
-__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 6) gpuos_route_kernel(const __grid_constant__ gpuos_devdesc d)
+__global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos_route_kernel(const __grid_constant__ gpuos_devdesc d)
 {
     __shared__ RouteToken tokens[GPUOS_ROUTEB_THREADS / L];
     __shared__ __align__(16) float biases[L][VPL + 4]; /* (four more: the lanes' vectors lie in different banks) */
+    __shared__ float flat[L * VPL]; /* ... in the experts' order */
     constexpr uint32_t TOKENS = 32 / L; /* of a warp */
     const float none = __int_as_float(0x7FFFFFFF);
     const uint32_t lane = lane_id(), sub = lane & (L - 1), own = lane & ~(uint32_t)(L - 1), warp = threadIdx.x >> 5;
@@ -1773,19 +1774,17 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 6) gpuos
     const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, summed = a.G > 1 && a.flags & GPUOS_ROUTE_TOP2, biased = a.bias != nullptr;
     const bool norm = a.flags & GPUOS_ROUTE_NORM;
     const uint32_t span = L / a.G, group = sub / span; /* lanes of a group */
-    /* of K + 1 that reach the bar, how many are lanes' best, and lanes' second best */
-    const uint32_t live = a.keep * span, ones = min(live, a.G == 1 && a.K < L ? a.K + 1u : (2u * a.K + 4u) / 3u), twos = a.K + 1u - ones;
+    /* of K + 1 that reach the bar, how many are lanes' best, second and third
+     * best (in random order six of nine are the first, and two the second) */
+    const uint32_t live = a.keep * span, ones = min(live, (2u * a.K + 4u) / 3u), twos = min(live, a.K + 1u - ones), threes = a.K + 1u - ones - twos;
     float wide = 0.0f;
     if (biased) {
         for (uint32_t i = threadIdx.x; i < L * P; i += GPUOS_ROUTEB_THREADS) {
             const float b = i < a.E ? fmaxf(__ldg(a.bias + i), -INFINITY) : 0.0f;
-            biases[i / P][i % P] = b;
+            biases[i / P][i % P] = flat[i] = b;
         }
         __syncthreads();
-        for (uint32_t i = sub; i < a.E; i += L) {
-            const float b = fabsf(biases[i / P][i % P]);
-            if (b <= FLT_MAX) wide = fmaxf(wide, b);
-        }
+        for (uint32_t i = sub; i < a.E; i += L) wide = fmaxf(wide, fabsf(flat[i]) <= FLT_MAX ? fabsf(flat[i]) : 0.0f);
         wide = lanes_max<L>(wide) + 1.0f; /* no value is larger */
     }
     const uint32_t step = gridDim.x * (GPUOS_ROUTEB_THREADS / L);
@@ -1845,9 +1844,21 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 6) gpuos
             for (int i = 0; i < VPL; i++)
                 if (i >= (int)P || first + i >= a.E) c[i] = none;
         }
-        float one = -INFINITY, two = -INFINITY; /* the lane's two best */
+        /* the lane's best three, or nearly: of its even and its odd values the best two */
+        float one, two, three;
+        {
+            float p1 = -INFINITY, p2 = -INFINITY, q1 = -INFINITY, q2 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) two = fmaxf(two, fminf(one, VEC || c[i] == c[i] ? c[i] : -INFINITY)), one = fmaxf(one, c[i]);
+            for (int i = 0; i < VPL; i += 2) {
+                const float p = VEC || c[i] == c[i] ? c[i] : -INFINITY, q = VEC || c[i + 1] == c[i + 1] ? c[i + 1] : -INFINITY;
+                p2 = fmaxf(p2, fminf(p1, p)), p1 = fmaxf(p1, p);
+                q2 = fmaxf(q2, fminf(q1, q)), q1 = fmaxf(q1, q);
+            }
+            one = fmaxf(p1, q1);
+            const float r = fminf(p1, q1), t = fmaxf(p2, q2);
+            two = fmaxf(r, t);
+            three = fmaxf(fminf(r, t), fminf(p2, q2));
+        }
         bool shut = false;
         if (a.G > 1) {
             float g1 = one, g2 = two;
@@ -1912,12 +1923,13 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 6) gpuos
                 }
             }
             shut = rank >= a.keep;
-            if (shut) one = two = -INFINITY;
+            if (shut) one = two = three = -INFINITY;
         }
         float bar = __shfl_sync(GPUOS_FULL, lanes_sort<L>(one), (int)(own + ones - 1u));
-        if (twos) {
-            const float b = __shfl_sync(GPUOS_FULL, lanes_sort<L>(two), (int)(own + min(twos, (uint32_t)L) - 1u));
-            bar = twos <= live ? fminf(bar, b) : -INFINITY;
+        if (twos) bar = fminf(bar, __shfl_sync(GPUOS_FULL, lanes_sort<L>(two), (int)(own + twos - 1u)));
+        if (threes) {
+            const float b = __shfl_sync(GPUOS_FULL, lanes_sort<L>(three), (int)(own + min(threes, (uint32_t)L) - 1u));
+            bar = threes <= live ? fminf(bar, b) : -INFINITY;
         }
         if (biased) bar -= unsure; /* (what may be the other way round is gathered too) */
         uint32_t reach = 0; /* this lane's that reach it */
@@ -1943,7 +1955,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 6) gpuos
             const uint64_t k = (uint64_t)n * a.ld + id;
             const float x = fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + k) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + k)), -INFINITY);
             float v = x;
-            if (biased) v = (sigmoid ? route_sigmoid_fast(x) : route_score(false, x, most, inv)) + fmaxf(__ldg(a.bias + id), -INFINITY);
+            if (biased) v = (sigmoid ? route_sigmoid_fast(x) : route_score(false, x, most, inv)) + flat[id];
             s.got[i] = top_entry(v, id);
             s.logit[i] = x;
         }
@@ -1964,13 +1976,13 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 6) gpuos
                 /* values that may have swapped, unless they are of equal logits and biases */
                 const uint64_t e = s.best[sub], o = s.best[sub + 1u];
                 near = choose_unkey((uint32_t)(e >> 32)) - choose_unkey((uint32_t)(o >> 32)) <= unsure &&
-                       !(s.best_logit[sub] == s.best_logit[sub + 1u] && __ldg(a.bias + (GPUOS_FULL - (uint32_t)e)) == __ldg(a.bias + (GPUOS_FULL - (uint32_t)o)));
+                       !(s.best_logit[sub] == s.best_logit[sub + 1u] && flat[GPUOS_FULL - (uint32_t)e] == flat[GPUOS_FULL - (uint32_t)o]);
             }
             const uint32_t who = __ballot_sync(GPUOS_FULL, near);
             if (who & lanes) {
                 if (sigmoid) {
                     __syncwarp(lanes); /* (best has been read) */
-                    if (!op_y_fine(&s, sub, L, a.K, RouteKind{a.bias, have, lanes, wide})) sure = false;
+                    if (!op_y_fine(&s, sub, L, RouteKind{flat, have, lanes, wide})) sure = false;
                 } else {
                     sure = false;
                 }
@@ -2010,7 +2022,7 @@ static int route_launch(const gpuos_devdesc &d, void *stream)
 {
     const uint32_t tokens = GPUOS_ROUTEB_THREADS / L, size = F32 ? 4u : 2u;
     const uint64_t blocks = ((uint64_t)d.dims[0] + tokens - 1u) / tokens;
-    const uint32_t grid = (uint32_t)min(blocks, (uint64_t)(VPL <= 16 ? 1216u : 912u)); /* as many as run at a time */
+    const uint32_t grid = (uint32_t)min(blocks, (uint64_t)GPUOS_ROUTEB_BLOCKS);
     const bool vec = d.dims[1] == L * VPL && (VPL * size) % 16u == 0 && (d.a & 15u) == 0 && ((uint64_t)d.dims[2] * size & 15u) == 0;
     if (vec) return choose_launch(gpuos_route_kernel<F32, L, VPL, true>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
     return choose_launch(gpuos_route_kernel<F32, L, VPL, false>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
@@ -2019,21 +2031,20 @@ template <bool F32>
 static int route_launch_of(const gpuos_devdesc &d, void *stream)
 {
     const uint32_t E = d.dims[1], K = d.dims[3], G = d.dims[4] & 0xFFFFu, keep = d.dims[4] >> 16;
-    /* a token's lanes have to hold whole groups or equal parts of one, and two
+    /* a token's lanes have to hold whole groups or equal parts of one, and three
      * values of each open lane have to be enough for a bar, or all fit */
     auto fits = [&](uint32_t L) {
-        return (G == 1u || (L % G == 0 && E % L == 0)) && (K + 1u <= 2u * keep * (L / G) || keep * (E / G) <= GPUOS_ROUTEB_ROOM);
+        return (G == 1u || (L % G == 0 && E % L == 0)) && (K + 1u <= 3u * keep * (L / G) || keep * (E / G) <= GPUOS_ROUTEB_ROOM);
     };
-    if (K <= 8u && E <= 256u && fits(8)) {
+    if (K <= 8u && E <= 128u && fits(8)) {
         if (E <= 64u) return route_launch<F32, 8, 8>(d, stream);
-        if (E <= 128u) return route_launch<F32, 8, 16>(d, stream);
-        return route_launch<F32, 8, 32>(d, stream);
+        return route_launch<F32, 8, 16>(d, stream);
     }
     if (K <= GPUOS_ROUTEB_MAX_K && E <= 512u && fits(16)) {
         if (E <= 256u) return route_launch<F32, 16, 16>(d, stream);
         return route_launch<F32, 16, 32>(d, stream);
     }
-    const uint32_t grid = (uint32_t)min(((uint64_t)d.dims[0] + 3u) / 4u, (uint64_t)1216u);
+    const uint32_t grid = (uint32_t)min(((uint64_t)d.dims[0] + 3u) / 4u, (uint64_t)GPUOS_ROUTEB_BLOCKS);
     if (E <= 256u) return choose_launch(gpuos_route_any_kernel<8>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
     return choose_launch(gpuos_route_any_kernel<32>, dim3(grid), GPUOS_ROUTEB_THREADS, 0, stream, d);
 }
@@ -2208,12 +2219,10 @@ static int choose_preload()
         (const void *)gpuos_top_kernel<true>, (const void *)gpuos_top_kernel<false>,
         (const void *)gpuos_route_kernel<true, 8, 8, true>, (const void *)gpuos_route_kernel<true, 8, 8, false>,
         (const void *)gpuos_route_kernel<true, 8, 16, true>, (const void *)gpuos_route_kernel<true, 8, 16, false>,
-        (const void *)gpuos_route_kernel<true, 8, 32, true>, (const void *)gpuos_route_kernel<true, 8, 32, false>,
         (const void *)gpuos_route_kernel<true, 16, 16, true>, (const void *)gpuos_route_kernel<true, 16, 16, false>,
         (const void *)gpuos_route_kernel<true, 16, 32, true>, (const void *)gpuos_route_kernel<true, 16, 32, false>,
         (const void *)gpuos_route_kernel<false, 8, 8, true>, (const void *)gpuos_route_kernel<false, 8, 8, false>,
         (const void *)gpuos_route_kernel<false, 8, 16, true>, (const void *)gpuos_route_kernel<false, 8, 16, false>,
-        (const void *)gpuos_route_kernel<false, 8, 32, true>, (const void *)gpuos_route_kernel<false, 8, 32, false>,
         (const void *)gpuos_route_kernel<false, 16, 16, true>, (const void *)gpuos_route_kernel<false, 16, 16, false>,
         (const void *)gpuos_route_kernel<false, 16, 32, true>, (const void *)gpuos_route_kernel<false, 16, 32, false>,
         (const void *)gpuos_route_any_kernel<8>, (const void *)gpuos_route_any_kernel<32>,
