@@ -168,7 +168,8 @@ enum {
                                log-probabilities -infinity. aux2 = workspace of
                                GPUOS_CHOOSE_WORKSPACE bytes (below); dims = {B, V, ld, K},
                                1 <= K <= min(V, 64) */
-    GPUOS_OP_EXPERT_ROUTE = 20, /* a = router logits [N][E], f32|bf16 -> out = ids i32[N][K], the K best
+    GPUOS_OP_RESERVED = 20, /* no op: refused wherever an id is given */
+    GPUOS_OP_EXPERT_ROUTE = 21, /* a = router logits [N][E], f32|bf16 -> out = ids i32[N][K], the K best
                                experts of each token, and aux0 = their weights f32[N][K]. A score is
                                softmax or sigmoid of the logit; the choice goes by score + b[e] (b =
                                f32[E] or 0), the weight by the score alone. With G > 1 groups of E / G
@@ -180,15 +181,15 @@ enum {
                                (0: none): tokens from there on are padding, with ids -1 and weights 0.
                                dims = {N, E <= 1024, ld, K <= 32, G | keep << 16, GPUOS_ROUTE_* flags},
                                G <= 32, E % G == 0, K <= keep * (E / G) */
-    GPUOS_OP_EXPERT_COUNT = 21, /* the pairs of each expert in runs of a = ids i32[P], into aux2 = workspace
+    GPUOS_OP_EXPERT_COUNT = 22, /* the pairs of each expert in runs of a = ids i32[P], into aux2 = workspace
                                (GPUOS_CHOOSE_WORKSPACE bytes), for the EXPERT_PLACE after it; dims =
                                {P < 2^31, E <= 1024}. Up to GPUOS_PLAN_ONE pairs need none */
-    GPUOS_OP_EXPERT_PLACE = 22, /* pairs a = ids i32[P] in the experts' order: out = order i32[P], pair
+    GPUOS_OP_EXPERT_PLACE = 23, /* pairs a = ids i32[P] in the experts' order: out = order i32[P], pair
                                numbers by expert, within one in their order, -1 behind the last; b =
                                place i32[P], where each pair went (-1: its id is not in 0 .. E - 1);
                                aux0 = offsets i32[E + 1], where each expert's pairs begin. aux2 and dims
                                as for EXPERT_COUNT, which has run on them before if P > GPUOS_PLAN_ONE */
-    GPUOS_OP_BUILTIN_COUNT = 23,
+    GPUOS_OP_BUILTIN_COUNT = 24,
     GPUOS_OP_USER_FIRST = 64, /* ids >= this are free for gpuos_register_op */
     GPUOS_MAX_OPS = 256
 };

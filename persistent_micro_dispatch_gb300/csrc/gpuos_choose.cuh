@@ -1270,21 +1270,32 @@ static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
 }
 
 /* ---------------------------------------------------------------------------
- * The best tokens, launched: a block takes a run of a row, a unit of 32
- * elements a thread at a time. The first unit gives a bar that at least K of
- * its elements reach; what reaches it in the run is gathered, a few times K
- * elements, and ranked by comparing all with all. Nothing waits between units.
- * The softmax's sum is kept in base 2 under a maximum of the thread's own:
- * one multiply-add, one exponential and one sum an element.
+ * The best tokens, launched: a block takes a run of a row, which bulk copies
+ * bring into a ring of shared memory, 16 KB a unit. The first unit gives a bar
+ * that at least K of its elements reach; what reaches it in the run is
+ * gathered, a few times K elements, and ranked by comparing all with all.
+ * Warps wait for copies, not for each other, between units. The softmax's sum
+ * is kept in base 2 under a maximum of the thread's own: one multiply-add, one
+ * exponential and one sum an element.
  * ------------------------------------------------------------------------- */
 #define GPUOS_TOPB_THREADS 256
 #define GPUOS_TOPB_WARPS (GPUOS_TOPB_THREADS / 32)
 #define GPUOS_TOPB_SLOTS 456u /* blocks that run at a time: three for each SM */
 #define GPUOS_TOPB_FIXED 12288u /* elements that a block's start and end cost as much as */
-#define GPUOS_TOPB_UNIT (GPUOS_TOPB_THREADS * 8u * GPUOS_TOP_UNIT)
+#define GPUOS_TOPB_BYTES 16384u /* of a unit */
+#define GPUOS_TOPB_STAGES 3u
 #define GPUOS_TOPB_FEW 256u
 /* (the slow gathering: a unit adds at most K threads' 32 elements to the few before it) */
-#define GPUOS_TOPB_ROOM (GPUOS_TOPB_FEW + GPUOS_TOP_MAX_K * 8u * GPUOS_TOP_UNIT)
+#define GPUOS_TOPB_ROOM (GPUOS_TOPB_FEW + GPUOS_TOP_MAX_K * 32u)
+template <bool F32>
+struct TopUnit {
+    static constexpr uint32_t PER = F32 ? 4u : 8u; /* elements of a vector */
+    static constexpr uint32_t N = GPUOS_TOPB_BYTES / (F32 ? 4u : 2u); /* elements */
+    static constexpr int G = N / GPUOS_TOPB_THREADS / 8; /* eights of a thread */
+    /* the place of a thread's element (u, j) from the unit's first: neighbouring
+     * threads have neighbouring vectors */
+    static DEV uint32_t at(uint32_t u, uint32_t j) { return (((8u / PER) * u + j / PER) * GPUOS_TOPB_THREADS + threadIdx.x) * PER + j % PER; }
+};
 
 struct TopBlock {
     uint64_t got[GPUOS_TOPB_ROOM];
@@ -1380,30 +1391,49 @@ DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s
     }
     if (d.aux1 && t == 0) reinterpret_cast<float *>(d.aux1)[row] = m + ls;
 }
-/* A unit's elements in this thread; -infinity outside [lo, hi), and for a NaN
- * if `clean`. */
+/* A unit's elements in this thread, -infinity outside [lo, hi): those at places
+ * [b0, b1) (whole vectors) out of `stage`, which begins at u0; the others, of
+ * which a row's ends have a few, from the row. */
 template <bool F32>
-DEV void top_load(const ChooseRow<F32> &r, uint32_t u0, uint32_t lo, uint32_t hi, float (&x)[GPUOS_TOP_UNIT][8])
+DEV void top_load(const ChooseRow<F32> &r, const unsigned char *stage, uint32_t u0, uint32_t b0, uint32_t b1, uint32_t lo, uint32_t hi,
+                  float (&x)[TopUnit<F32>::G][8])
 {
+    using U = TopUnit<F32>;
 #pragma unroll
-    for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
-        choose_load8(r, u0 + (u * GPUOS_TOPB_THREADS + threadIdx.x) * 8u, lo, hi, -INFINITY, x[u]);
+    for (uint32_t u = 0; u < U::G; u++)
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j += U::PER) {
+            const uint32_t p = u0 + U::at(u, j);
+            if (p >= b0 && p < b1) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(stage + U::at(u, j) * (F32 ? 4u : 2u));
+                if (F32) {
+                    x[u][j & 4u] = __uint_as_float(v.x), x[u][(j & 4u) + 1] = __uint_as_float(v.y), x[u][(j & 4u) + 2] = __uint_as_float(v.z),
+                    x[u][(j & 4u) + 3] = __uint_as_float(v.w);
+                } else {
+                    unpack8(v, x[u]);
+                }
+            } else {
+#pragma unroll
+                for (uint32_t k = 0; k < U::PER; k++) x[u][(j + k) & 7u] = p + k >= lo && p + k < hi ? r.one(p + k) : -INFINITY;
+            }
+        }
 }
-DEV uint32_t top_place(uint32_t u0, uint32_t u, uint32_t j) { return u0 + (u * GPUOS_TOPB_THREADS + threadIdx.x) * 8u + j; }
 /* The thread's best of a unit (0: it has none). */
-DEV uint64_t top_mine(const float (&x)[GPUOS_TOP_UNIT][8], uint32_t u0, uint32_t lo, uint32_t hi, uint32_t row_lo)
+template <bool F32>
+DEV uint64_t top_mine(const float (&x)[TopUnit<F32>::G][8], uint32_t u0, uint32_t lo, uint32_t hi, uint32_t row_lo)
 {
+    using U = TopUnit<F32>;
     float most = -INFINITY;
 #pragma unroll
-    for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+    for (uint32_t u = 0; u < U::G; u++)
 #pragma unroll
         for (uint32_t j = 0; j < 8; j++) most = fmaxf(most, x[u][j]);
-    uint32_t at = GPUOS_FULL; /* the first of equal ones that is there */
+    uint32_t at = GPUOS_FULL; /* the first of equal ones that is there (places rise with u and j) */
 #pragma unroll
-    for (int u = GPUOS_TOP_UNIT - 1; u >= 0; u--)
+    for (int u = U::G - 1; u >= 0; u--)
 #pragma unroll
         for (int j = 7; j >= 0; j--) {
-            const uint32_t p = top_place(u0, u, j);
+            const uint32_t p = u0 + U::at(u, j);
             if (fmaxf(x[u][j], -INFINITY) == most && p >= lo && p < hi) at = p;
         }
     return at == GPUOS_FULL ? 0ull : top_entry(most, at - row_lo);
@@ -1427,10 +1457,10 @@ __device__ __noinline__ uint32_t top_gather_slow(TopBlock &s, const ChooseRow<F3
     __syncthreads();
     if (t == 0) s.count = 0;
 #pragma unroll 1
-    for (uint32_t u0 = from; u0 < hi; u0 += GPUOS_TOPB_UNIT) {
-        float x[GPUOS_TOP_UNIT][8];
-        top_load(r, u0, lo, hi, x);
-        const uint64_t mine = top_mine(x, u0, lo, hi, r.lo);
+    for (uint32_t u0 = from; u0 < hi; u0 += TopUnit<F32>::N) {
+        float x[TopUnit<F32>::G][8];
+        top_load(r, nullptr, u0, 0u, 0u, lo, hi, x); /* (element by element: nothing here is often) */
+        const uint64_t mine = top_mine<F32>(x, u0, lo, hi, r.lo);
         const uint32_t above = (uint32_t)__syncthreads_count(mine > bar);
         if (above == 0) continue;
         if (above > K) {
@@ -1442,9 +1472,9 @@ __device__ __noinline__ uint32_t top_gather_slow(TopBlock &s, const ChooseRow<F3
         }
         if (mine > bar)
 #pragma unroll
-            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+            for (uint32_t u = 0; u < TopUnit<F32>::G; u++)
 #pragma unroll
-                for (uint32_t j = 0; j < 8; j++) top_push(s, bar, x[u][j], top_place(u0, u, j), lo, hi, r.lo);
+                for (uint32_t j = 0; j < 8; j++) top_push(s, bar, x[u][j], u0 + TopUnit<F32>::at(u, j), lo, hi, r.lo);
         __syncthreads();
         const uint32_t n = s.count;
         if (n > GPUOS_TOPB_FEW) { /* the K best so far, and the bar at the last of them */
@@ -1457,64 +1487,97 @@ __device__ __noinline__ uint32_t top_gather_slow(TopBlock &s, const ChooseRow<F3
     __syncthreads();
     return s.count;
 }
+DEV float top_ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 template <bool F32>
 __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const __grid_constant__ gpuos_devdesc d)
 {
+    using U = TopUnit<F32>;
+    extern __shared__ __align__(128) unsigned char top_ring[];
     __shared__ TopBlock s;
+    __shared__ __align__(8) unsigned long long full[GPUOS_TOPB_STAGES], empty[GPUOS_TOPB_STAGES];
     const uint32_t V = d.dims[1], K = d.dims[3], t = threadIdx.x, S = d.ntiles / d.dims[0]; /* (runs of a row) */
     const uint32_t row = blockIdx.x / S, part = blockIdx.x - row * S;
     constexpr float L2E = 1.44269504f; /* (its error is the same for every element: 1e-8 of their distance from the maximum) */
-    kv4_after_previous();
     const ChooseRow<F32> r(d.a, row, d.dims[2], V);
     const uint32_t run = ((V + 7u + S - 1u) / S + 255u) & ~255u, from = part * run;
     const uint32_t lo = max(from, r.lo), hi = min(from + run, r.hi);
+    const uint32_t units = hi > from ? (hi - from + U::N - 1u) / U::N : 0u;
+    /* the whole vectors of a unit, [first, second) */
+    auto whole = [&](uint32_t u0) {
+        const uint32_t b0 = max(u0, (lo + U::PER - 1u) & ~(U::PER - 1u));
+        return make_uint2(b0, max(b0, min(u0 + U::N, hi & ~(U::PER - 1u))));
+    };
+    auto copy = [&](uint32_t i) { /* one thread */
+        const uint32_t u0 = from + i * U::N, at = i % GPUOS_TOPB_STAGES;
+        const uint2 b = whole(u0);
+        const uint32_t bytes = (b.y - b.x) * (F32 ? 4u : 2u);
+        if (bytes == 0) {
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&full[at])) : "memory");
+            return;
+        }
+        mbar_expect(&full[at], bytes);
+        bulk_g2s(top_ring + at * GPUOS_TOPB_BYTES + (b.x - u0) * (F32 ? 4u : 2u), r.vec(b.x), bytes, &full[at]);
+    };
+    if (t == 0) {
+        s.count = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < GPUOS_TOPB_STAGES; k++) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[k])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[k])), "n"(GPUOS_TOPB_WARPS) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    kv4_after_previous();
+    if (t == 0)
+        for (uint32_t i = 0; i < min(units, GPUOS_TOPB_STAGES); i++) copy(i);
+    __syncthreads();
     /* sum of 2^(L2E x - ml), ml = L2E m rounded; and, of units whose largest is
      * so far from 0 that rounding would tell, the sum of e^(x - far_m) */
     float m = -2e6f, ml = -2e6f * L2E, l = 0.0f, far_m = -FLT_MAX, far_l = 0.0f;
     uint64_t bar = 0;
     float barf = -INFINITY;
-    if (t == 0) s.count = 0;
+    bool lost = false; /* a copy did not arrive (bounded, like every wait): the row's numbers are NaN */
 #pragma unroll 1
-    for (uint32_t u0 = from; u0 < hi; u0 += GPUOS_TOPB_UNIT) {
-        float x[GPUOS_TOP_UNIT][8], most[GPUOS_TOP_UNIT];
-        top_load(r, u0, lo, hi, x);
+    for (uint32_t i = 0; i < units; i++) {
+        const uint32_t u0 = from + i * U::N, at = i % GPUOS_TOPB_STAGES, turn = i / GPUOS_TOPB_STAGES & 1u;
+        const uint2 b = whole(u0);
+        float x[U::G][8], most[U::G], unit = -INFINITY;
+        if (!mbar_wait(&full[at], turn)) lost = true;
+        top_load(r, top_ring + at * GPUOS_TOPB_BYTES, u0, b.x, b.y, lo, hi, x);
 #pragma unroll
-        for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
+        for (uint32_t u = 0; u < U::G; u++) {
             most[u] = -INFINITY; /* (a maximum passes a NaN over) */
 #pragma unroll
             for (uint32_t j = 0; j < 8; j++) most[u] = fmaxf(most[u], x[u][j]);
+            unit = fmaxf(unit, most[u]);
         }
-        const float unit = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-        float sum[GPUOS_TOP_UNIT]; /* (sums of sums: a rounding for each unit, not for each element) */
+        __syncwarp(); /* this warp has its elements */
+        if (lane_id() == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[at])) : "memory");
         if (fabsf(unit) <= 1e6f) {
             if (unit > m) {
                 const float to = unit * L2E;
-                float f;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(ml - to));
-                l *= f;
+                l *= top_ex2(ml - to);
                 m = unit, ml = to;
             }
+            float all = 0.0f; /* (sums of sums: a rounding for each unit, not for each element) */
 #pragma unroll
-            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
-                sum[u] = 0.0f;
+            for (uint32_t u = 0; u < U::G; u++) {
+                float sum = 0.0f;
 #pragma unroll
-                for (uint32_t j = 0; j < 8; j++) {
-                    float e;
-                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x[u][j], L2E, -ml)));
-                    sum[u] += e;
-                }
+                for (uint32_t j = 0; j < 8; j++) sum += top_ex2(fmaf(x[u][j], L2E, -ml));
+                all += sum;
             }
-            float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (!(all == all)) { /* a NaN among the logits counts as -infinity */
                 all = 0.0f;
 #pragma unroll
-                for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+                for (uint32_t u = 0; u < U::G; u++)
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; j++) {
-                        float e;
-                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(fmaxf(x[u][j], -INFINITY), L2E, -ml)));
-                        all += e;
-                    }
+                    for (uint32_t j = 0; j < 8; j++) all += top_ex2(fmaf(fmaxf(x[u][j], -INFINITY), L2E, -ml));
             }
             l += all;
         } else if (unit != -INFINITY) {
@@ -1522,27 +1585,30 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
             far_l *= choose_exp(far_m - to);
             far_m = to;
 #pragma unroll
-            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++)
+            for (uint32_t u = 0; u < U::G; u++)
 #pragma unroll
-                for (uint32_t j = 0; j < 8; j++) {
-                    float e;
-                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((fmaxf(x[u][j], -INFINITY) - far_m) * L2E));
-                    far_l += e;
-                }
+                for (uint32_t j = 0; j < 8; j++) far_l += top_ex2((fmaxf(x[u][j], -INFINITY) - far_m) * L2E);
         }
-        if (u0 == from) {
-            bar = top_bar(s, top_mine(x, u0, lo, hi, r.lo), K);
+        if (i == 0) {
+            bar = top_bar(s, top_mine<F32>(x, u0, lo, hi, r.lo), K);
             barf = bar ? choose_unkey((uint32_t)(bar >> 32)) : -INFINITY; /* (that bar's value itself may pass) */
         }
-        if (u0 == from ? unit >= barf : unit > barf || bar == 0) { /* (an equal one in a later unit comes after) */
+        if (i == 0 ? unit >= barf : unit > barf || bar == 0) { /* (an equal one in a later unit comes after) */
 #pragma unroll
-            for (uint32_t u = 0; u < GPUOS_TOP_UNIT; u++) {
+            for (uint32_t u = 0; u < U::G; u++) {
                 if (!(most[u] >= barf)) continue;
 #pragma unroll
                 for (uint32_t j = 0; j < 8; j++)
-                    if (!(x[u][j] < barf)) top_push(s, bar, x[u][j], top_place(u0, u, j), lo, hi, r.lo);
+                    if (!(x[u][j] < barf)) top_push(s, bar, x[u][j], u0 + U::at(u, j), lo, hi, r.lo);
             }
         }
+        /* the unit's place takes the next but two, once all warps have left it; the warps take turns at that */
+        if (t == 32u * (i % GPUOS_TOPB_WARPS) && i + GPUOS_TOPB_STAGES < units) {
+            if (!mbar_wait(&empty[at], turn)) lost = true;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            copy(i + GPUOS_TOPB_STAGES);
+        }
+        __syncwarp();
     }
     if (l > 0.0f) { /* both sums under one maximum */
         float f;
@@ -1554,7 +1620,7 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
     } else {
         m = far_m, l = far_l;
     }
-    __syncthreads();
+    if (__syncthreads_or(lost)) l = __int_as_float(0x7FFFFFFF);
     uint32_t n = s.count;
     if (n > GPUOS_TOPB_ROOM) n = top_gather_slow(s, r, from, lo, hi, K);
     top_sort(s, n, K);
@@ -1596,14 +1662,16 @@ static int top_launch(const gpuos_devdesc &d, void *stream)
      * more than a row's last block can join and the workspace holds */
     gpuos_devdesc e = d;
     const uint64_t B = d.dims[0], V = d.dims[1];
-    const uint64_t most = min(min((V + 7u + GPUOS_TOPB_UNIT - 1u) / GPUOS_TOPB_UNIT, (uint64_t)32u), GPUOS_TOP_TILES / B);
+    const uint64_t most = min(min((V + 7u + TopUnit<F32>::N - 1u) / TopUnit<F32>::N, (uint64_t)32u), GPUOS_TOP_TILES / B);
     uint64_t S = 1, least = ~0ull;
     for (uint64_t n = 1; n <= most || n == 1; n++) {
         const uint64_t cost = (B * n + GPUOS_TOPB_SLOTS - 1u) / GPUOS_TOPB_SLOTS * (V / n + GPUOS_TOPB_FIXED);
         if (cost < least) least = cost, S = n;
     }
     e.ntiles = (uint32_t)(B * S);
-    return choose_launch(gpuos_top_kernel<F32>, dim3(e.ntiles), GPUOS_TOPB_THREADS, 0, stream, e);
+    static std::atomic<bool> known[64];
+    if (choose_smem((const void *)gpuos_top_kernel<F32>, GPUOS_TOPB_STAGES * GPUOS_TOPB_BYTES, known) != 0) return -1;
+    return choose_launch(gpuos_top_kernel<F32>, dim3(e.ntiles), GPUOS_TOPB_THREADS, GPUOS_TOPB_STAGES * GPUOS_TOPB_BYTES, stream, e);
 }
 
 /* ---------------------------------------------------------------------------

@@ -1862,7 +1862,7 @@ __device__ gpuos_op_fn g_builtin_ops[GPUOS_OP_BUILTIN_COUNT] = {
     op_nop, op_add, op_mul, op_relu, op_gelu, op_softmax, op_layernorm,
     op_rowsum, op_rowmax, op_rowmin, op_rope, op_kv_write, op_sdpa, op_vecmat,
     op_xwrite, op_x_read, op_x_sdpa, op_x_copy,
-    op_y_adjs, op_y_tops, op_y_rout, op_y_cnts, op_y_plac,
+    op_y_adjs, op_y_tops, nullptr /* (20 is reserved) */, op_y_rout, op_y_cnts, op_y_plac,
 };
 
 /* The body of built-in op `kind`, inlined (the eager kernel). */

@@ -530,6 +530,7 @@ static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool use
             nt = (uint64_t)m[0] * gpuos_top_split(m[0], m[1]);
         }
         break;
+    case GPUOS_OP_RESERVED: return GPUOS_EINVAL;
     case GPUOS_OP_EXPERT_ROUTE:
         if (m[0]) {
             if (!gpuos_route_ok(d->dtype, d->a, d->b, d->out, d->aux0, d->aux1, m)) return GPUOS_EINVAL;
@@ -1558,7 +1559,7 @@ int gpuos_load_module(gpuos_ctx *c, const void *image, size_t len)
 int gpuos_register_op(gpuos_ctx *c, uint16_t op_id, const void *image, size_t len, const char *sym)
 {
     if (!c || !image || !len || !sym || op_id >= GPUOS_MAX_OPS || op_id == GPUOS_OP_NOP) return GPUOS_EINVAL;
-    if (op_id >= GPUOS_OP_BUILTIN_COUNT && op_id < GPUOS_OP_USER_FIRST) return GPUOS_EINVAL;
+    if ((op_id >= GPUOS_OP_BUILTIN_COUNT && op_id < GPUOS_OP_USER_FIRST) || op_id == GPUOS_OP_RESERVED) return GPUOS_EINVAL;
     if (!c->accepting) return GPUOS_ESTOPPED;
     if (find_module(c, image, len, fnv1a(image, len)) < 0) {
         /* not linked into the executor: linked at the launch, or, with the
@@ -1589,7 +1590,7 @@ int gpuos_register_op(gpuos_ctx *c, uint16_t op_id, const void *image, size_t le
 int gpuos_alias_op(gpuos_ctx *c, uint16_t op_id, uint16_t source_op)
 {
     if (!c || op_id >= GPUOS_MAX_OPS || source_op >= GPUOS_MAX_OPS || op_id == GPUOS_OP_NOP) return GPUOS_EINVAL;
-    if (op_id >= GPUOS_OP_BUILTIN_COUNT && op_id < GPUOS_OP_USER_FIRST) return GPUOS_EINVAL;
+    if ((op_id >= GPUOS_OP_BUILTIN_COUNT && op_id < GPUOS_OP_USER_FIRST) || op_id == GPUOS_OP_RESERVED) return GPUOS_EINVAL;
     if (!c->accepting) return GPUOS_ESTOPPED;
     const uint64_t v = c->table_host[c->version & 1u][source_op];
     if (v == 0) return GPUOS_EINVAL;

@@ -22,7 +22,7 @@ OK, EINVAL, EAGAIN, ETIMEDOUT, EDEVICE, ECUDA, ESTOPPED, ENOMEM, EBUSY, ETOOBIG,
 ST_OK, ST_BAD_OP, ST_BAD_ARGS, ST_DEP_TIMEOUT, ST_ABORTED, ST_BAD_DESC, ST_COPY_TIMEOUT = 0, 1, 2, 3, 4, 5, 6
 OP = dict(nop=0, add=1, mul=2, relu=3, gelu=4, softmax=5, layernorm=6, rowsum=7, rowmax=8, rowmin=9,
           rope=10, kv_write=11, sdpa=12, vecmat=13, kv4_write=14, kv4_read=15, kv4_sdpa=16, page_copy=17,
-          logits_adjust=18, logits_top=19, expert_route=20, expert_count=21, expert_place=22)
+          logits_adjust=18, logits_top=19, expert_route=21, expert_count=22, expert_place=23)
 OP_USER_FIRST = 64
 F32, BF16 = 0, 1
 DTYPE = {"f32": F32, "bf16": BF16}

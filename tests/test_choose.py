@@ -1,7 +1,5 @@
 """What a decode step chooses, without a GPU: the tiling rules and refusals of
 its ops, the binding's checks, and the reference's own pins."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -90,6 +88,16 @@ def test_pointer_and_type_refusals(G, op, field, value):
     with pytest.raises(G.GpuosError) as e:
         G.op_ntiles(_desc(G, op, GOOD[op], **kw, **({"dtype": value} if field == "dtype" else {})))
     assert e.value.code == G.EINVAL
+
+
+def test_the_reserved_id_is_no_op(G):
+    assert 20 not in G.OP.values()
+    d = G.make_descs(1)
+    d["op_id"] = 20
+    with pytest.raises(G.GpuosError) as e:
+        G.op_ntiles(d)
+    assert e.value.code == G.EINVAL
+    assert G.lib().gpuos_eager_run(d.ctypes.data, 1, 0, None) == G.EINVAL
 
 
 def test_in_place_needs_rows_alike(G):
