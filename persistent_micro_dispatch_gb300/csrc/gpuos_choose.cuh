@@ -1270,10 +1270,12 @@ static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
 }
 
 /* ---------------------------------------------------------------------------
- * The best tokens, launched: a block takes a run of a row, which bulk copies
- * bring into a ring of shared memory, 16 KB a unit. The first unit gives a bar
- * that at least K of its elements reach; what reaches it in the run is
- * gathered, a few times K elements, and ranked by comparing all with all.
+ * The best tokens, launched. The rows one behind the other are cut into equal
+ * runs, one for each block, so that all end together; a row, or what a run has
+ * of it, is a piece. Bulk copies bring a run into a ring of shared memory, 4,096
+ * elements a unit. A piece's first unit gives a bar that at least K of its elements
+ * reach; what reaches it is gathered, a few times K elements, and ranked by
+ * comparing all with all; now and then the K best so far give a better bar.
  * Warps wait for copies, not for each other, between units. The softmax's sum
  * is kept in base 2 under a maximum of the thread's own: one multiply-add, one
  * exponential and one sum an element.
@@ -1281,16 +1283,19 @@ static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
 #define GPUOS_TOPB_THREADS 256
 #define GPUOS_TOPB_WARPS (GPUOS_TOPB_THREADS / 32)
 #define GPUOS_TOPB_SLOTS 456u /* blocks that run at a time: three for each SM */
-#define GPUOS_TOPB_FIXED 12288u /* elements that a block's start and end cost as much as */
-#define GPUOS_TOPB_BYTES 16384u /* of a unit */
+#define GPUOS_TOPB_FIXED 48u /* cells (of 256 elements) that a piece's start and end cost as much as */
+#define GPUOS_TOPB_UNIT 4096u /* elements: sixteen a thread */
 #define GPUOS_TOPB_STAGES 3u
 #define GPUOS_TOPB_FEW 256u
-/* (the slow gathering: a unit adds at most K threads' 32 elements to the few before it) */
-#define GPUOS_TOPB_ROOM (GPUOS_TOPB_FEW + GPUOS_TOP_MAX_K * 32u)
+static_assert(2u * GPUOS_TOPB_SLOTS <= GPUOS_TOP_TILES, "two pieces of each block in the workspace");
+/* (the slow gathering: a unit adds at most K threads' 16 elements to the few before it) */
+#define GPUOS_TOPB_ROOM (GPUOS_TOPB_FEW + GPUOS_TOP_MAX_K * 16u)
+#define GPUOS_TOPB_JOIN (35u * GPUOS_TOP_MAX_K) /* entries of a row's pieces */
+static_assert(GPUOS_TOPB_JOIN >= GPUOS_TOPB_ROOM, "one array for both");
 template <bool F32>
 struct TopUnit {
     static constexpr uint32_t PER = F32 ? 4u : 8u; /* elements of a vector */
-    static constexpr uint32_t N = GPUOS_TOPB_BYTES / (F32 ? 4u : 2u); /* elements */
+    static constexpr uint32_t N = GPUOS_TOPB_UNIT, BYTES = N * (F32 ? 4u : 2u);
     static constexpr int G = N / GPUOS_TOPB_THREADS / 8; /* eights of a thread */
     /* the place of a thread's element (u, j) from the unit's first: neighbouring
      * threads have neighbouring vectors */
@@ -1298,21 +1303,33 @@ struct TopUnit {
 };
 
 struct TopBlock {
-    uint64_t got[GPUOS_TOPB_ROOM];
-    uint64_t few[GPUOS_TOPB_FEW];
-    uint64_t best[GPUOS_TOPB_THREADS];
+    /* (eight more of each: a list's end is filled with entries below all others) */
+    __align__(16) uint64_t got[GPUOS_TOPB_JOIN + 8u];
+    __align__(16) uint64_t few[GPUOS_TOPB_FEW + 8u];
+    __align__(16) uint64_t best[GPUOS_TOPB_THREADS];
     uint64_t sorted[GPUOS_TOP_MAX_K];
     uint64_t bar; /* an entry has to be above it */
     float2 part[GPUOS_TOPB_WARPS];
     uint32_t count, left, last;
 };
-/* How many of n entries are above x. */
+/* How many of n entries (a multiple of eight) are above x. */
 DEV uint32_t top_rank(const uint64_t *e, uint32_t n, uint64_t x)
 {
     uint32_t r = 0;
 #pragma unroll 4
-    for (uint32_t i = 0; i < n; i++) r += e[i] > x;
+    for (uint32_t i = 0; i < n; i += 8) {
+        ulonglong2 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) v[k] = reinterpret_cast<const ulonglong2 *>(e + i)[k];
+#pragma unroll
+        for (int k = 0; k < 4; k++) r += (v[k].x > x) + (v[k].y > x);
+    }
     return r;
+}
+DEV uint32_t top_fill(uint64_t *e, uint32_t n) /* (before a barrier) */
+{
+    if (threadIdx.x < 8u) e[n + threadIdx.x] = 0;
+    return (n + 7u) & ~7u;
 }
 /* A bar that at least K of the threads' entries are above (0: there are not K,
  * or not K in the warps' eight best): the K-th of the warps' eight best, less
@@ -1345,7 +1362,7 @@ DEV uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
 DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K)
 {
     const uint32_t t = threadIdx.x;
-    const uint64_t *from = s.got;
+    uint64_t *from = s.got;
     if (n > 192u) { /* first those that reach a bar of their own */
         uint64_t mine = 0;
         for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) mine = max(mine, s.got[i]);
@@ -1361,10 +1378,11 @@ DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K)
         if (s.left <= GPUOS_TOPB_FEW) n = s.left, from = s.few;
     }
     if (t < K) s.sorted[t] = 0;
+    const uint32_t n8 = top_fill(from, n);
     __syncthreads();
     for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) {
         const uint64_t x = from[i];
-        const uint32_t r = top_rank(from, n, x);
+        const uint32_t r = top_rank(from, n8, x);
         if (r < K) s.sorted[r] = x;
     }
     __syncthreads();
@@ -1383,7 +1401,9 @@ DEV void top_block_softmax(TopBlock &s, float &m, float &l)
 DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s, float m, float l)
 {
     const uint32_t K = d.dims[3], t = threadIdx.x;
-    const float ls = logf(l); /* (-infinity if nothing but -infinity was there) */
+    float ls; /* (-infinity if nothing but -infinity was there) */
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(ls) : "f"(l));
+    ls *= 0.693147181f;
     if (t < K) {
         const float x = choose_unkey((uint32_t)(s.sorted[t] >> 32));
         reinterpret_cast<uint32_t *>(d.out)[(uint64_t)row * K + t] = GPUOS_FULL - (uint32_t)s.sorted[t];
@@ -1428,14 +1448,21 @@ DEV uint64_t top_mine(const float (&x)[TopUnit<F32>::G][8], uint32_t u0, uint32_
     for (uint32_t u = 0; u < U::G; u++)
 #pragma unroll
         for (uint32_t j = 0; j < 8; j++) most = fmaxf(most, x[u][j]);
-    uint32_t at = GPUOS_FULL; /* the first of equal ones that is there (places rise with u and j) */
+    uint32_t at = GPUOS_FULL; /* the first of equal ones (places rise with u and j) */
 #pragma unroll
-    for (int u = U::G - 1; u >= 0; u--)
-#pragma unroll
-        for (int j = 7; j >= 0; j--) {
-            const uint32_t p = u0 + U::at(u, j);
-            if (fmaxf(x[u][j], -INFINITY) == most && p >= lo && p < hi) at = p;
+    for (int i = 8 * U::G - 1; i >= 0; i--)
+        if (x[i >> 3][i & 7] == most) at = u0 + U::at((uint32_t)i >> 3, (uint32_t)i & 7u);
+    if (most == -INFINITY) { /* which stands for what is not there too */
+        at = GPUOS_FULL;
+#pragma unroll 1
+        for (uint32_t i = 0; i < 8u * U::G; i++) {
+            const uint32_t p = u0 + U::at(i >> 3, i & 7u);
+            if (p >= lo && p < hi) {
+                at = p;
+                break;
+            }
         }
+    }
     return at == GPUOS_FULL ? 0ull : top_entry(most, at - row_lo);
 }
 DEV void top_push(TopBlock &s, uint64_t bar, float x, uint32_t p, uint32_t lo, uint32_t hi, uint32_t row_lo)
@@ -1493,185 +1520,288 @@ DEV float top_ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+/* The rows' cells (256 elements each; their number is below 2^32) in runs: S
+ * runs of each row, or runs across rows that differ by one at most, of which
+ * the first `more` have one more. */
+struct TopRuns {
+    uint32_t S, base, more, cells;
+    DEV TopRuns(const gpuos_devdesc &d, uint32_t cells_of_a_row)
+        : S((uint32_t)d.dep[0]), base((uint32_t)d.dep[1]), more((uint32_t)(d.dep[1] >> 32)), cells(cells_of_a_row)
+    {
+    }
+    DEV uint32_t start(uint32_t run) const
+    {
+        if (S == 0) return run * base + min(run, more);
+        const uint32_t row = run / S;
+        return row * cells + (run - row * S) * cells / S; /* (a row has fewer than 2^23 cells, and S is at most 32) */
+    }
+    DEV uint32_t run_of(uint32_t u) const /* (only across rows) */
+    {
+        const uint32_t cut = more * (base + 1u);
+        return u < cut ? u / (base + 1u) : more + (u - cut) / base;
+    }
+};
+/* A place in a run: a row and, of it, the units from u0 on, up to `end`. */
+struct TopCursor {
+    uint32_t cell; /* the piece's first */
+    uint32_t row, u0, end;
+};
+template <bool F32>
+struct TopWork {
+    const gpuos_devdesc &d;
+    uint32_t V, cells; /* of a row */
+    uint32_t last;     /* the run's end */
+    /* the piece that begins at a cell */
+    DEV void piece(uint32_t cell, TopCursor &c) const
+    {
+        c.cell = cell;
+        c.row = cell / cells;
+        const uint32_t begin = c.row * cells;
+        c.u0 = (cell - begin) * 256u;
+        c.end = min(cells, last - begin) * 256u;
+    }
+    /* the next unit; false: the run is over */
+    DEV bool next(TopCursor &c) const
+    {
+        c.u0 += TopUnit<F32>::N;
+        if (c.u0 < c.end) return true;
+        const uint32_t cell = c.row * cells + c.end / 256u;
+        if (cell >= last) return false;
+        piece(cell, c);
+        return true;
+    }
+};
 template <bool F32>
 __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const __grid_constant__ gpuos_devdesc d)
 {
     using U = TopUnit<F32>;
+    constexpr uint32_t ST = GPUOS_TOPB_STAGES, SIZE = F32 ? 4u : 2u;
     extern __shared__ __align__(128) unsigned char top_ring[];
     __shared__ TopBlock s;
-    __shared__ __align__(8) unsigned long long full[GPUOS_TOPB_STAGES], empty[GPUOS_TOPB_STAGES];
-    const uint32_t V = d.dims[1], K = d.dims[3], t = threadIdx.x, S = d.ntiles / d.dims[0]; /* (runs of a row) */
-    const uint32_t row = blockIdx.x / S, part = blockIdx.x - row * S;
+    __shared__ __align__(8) unsigned long long full[ST], empty[ST];
+    const uint32_t V = d.dims[1], K = d.dims[3], t = threadIdx.x;
     constexpr float L2E = 1.44269504f; /* (its error is the same for every element: 1e-8 of their distance from the maximum) */
-    const ChooseRow<F32> r(d.a, row, d.dims[2], V);
-    const uint32_t run = ((V + 7u + S - 1u) / S + 255u) & ~255u, from = part * run;
-    const uint32_t lo = max(from, r.lo), hi = min(from + run, r.hi);
-    const uint32_t units = hi > from ? (hi - from + U::N - 1u) / U::N : 0u;
+    const uint32_t cells = (V + 7u + 255u) / 256u; /* (a row may begin seven elements behind its first vector) */
+    const TopRuns runs(d, cells);
+    const TopWork<F32> work{d, V, cells, runs.start(blockIdx.x + 1u)};
     /* the whole vectors of a unit, [first, second) */
-    auto whole = [&](uint32_t u0) {
+    auto whole = [&](const ChooseRow<F32> &r, uint32_t u0, uint32_t lo, uint32_t hi) {
         const uint32_t b0 = max(u0, (lo + U::PER - 1u) & ~(U::PER - 1u));
         return make_uint2(b0, max(b0, min(u0 + U::N, hi & ~(U::PER - 1u))));
     };
-    auto copy = [&](uint32_t i) { /* one thread */
-        const uint32_t u0 = from + i * U::N, at = i % GPUOS_TOPB_STAGES;
-        const uint2 b = whole(u0);
-        const uint32_t bytes = (b.y - b.x) * (F32 ? 4u : 2u);
+    auto copy = [&](const TopCursor &c, uint32_t at) { /* one thread */
+        const ChooseRow<F32> r(d.a, c.row, d.dims[2], V);
+        const uint2 b = whole(r, c.u0, max(c.u0, r.lo), min(c.end, r.hi));
+        const uint32_t bytes = (b.y - b.x) * SIZE;
         if (bytes == 0) {
             asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&full[at])) : "memory");
             return;
         }
         mbar_expect(&full[at], bytes);
-        bulk_g2s(top_ring + at * GPUOS_TOPB_BYTES + (b.x - u0) * (F32 ? 4u : 2u), r.vec(b.x), bytes, &full[at]);
+        bulk_g2s(top_ring + at * U::BYTES + (b.x - c.u0) * SIZE, r.vec(b.x), bytes, &full[at]);
     };
     if (t == 0) {
-        s.count = 0;
 #pragma unroll
-        for (uint32_t k = 0; k < GPUOS_TOPB_STAGES; k++) {
+        for (uint32_t k = 0; k < ST; k++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[k])) : "memory");
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[k])), "n"(GPUOS_TOPB_WARPS) : "memory");
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    kv4_after_previous();
-    if (t == 0)
-        for (uint32_t i = 0; i < min(units, GPUOS_TOPB_STAGES); i++) copy(i);
     __syncthreads();
-    /* sum of 2^(L2E x - ml), ml = L2E m rounded; and, of units whose largest is
-     * so far from 0 that rounding would tell, the sum of e^(x - far_m) */
-    float m = -2e6f, ml = -2e6f * L2E, l = 0.0f, far_m = -FLT_MAX, far_l = 0.0f;
-    uint64_t bar = 0;
-    float barf = -INFINITY;
-    bool lost = false; /* a copy did not arrive (bounded, like every wait): the row's numbers are NaN */
+    kv4_after_previous();
+    TopCursor c, ahead; /* the unit that is worked on, and the one whose copy is issued next */
+    work.piece(runs.start(blockIdx.x), c);
+    ahead = c;
+    bool more = true; /* there is such a one */
+#pragma unroll
+    for (uint32_t k = 0; k < ST; k++) {
+        if (more && t == 32u * k) copy(ahead, k);
+        more = more && work.next(ahead);
+    }
+    uint32_t at = 0, turn = 0, n_unit = 0; /* the ring's position */
+    bool lost = false; /* a copy did not arrive (bounded, like every wait): the numbers are NaN from there on */
 #pragma unroll 1
-    for (uint32_t i = 0; i < units; i++) {
-        const uint32_t u0 = from + i * U::N, at = i % GPUOS_TOPB_STAGES, turn = i / GPUOS_TOPB_STAGES & 1u;
-        const uint2 b = whole(u0);
-        float x[U::G][8], most[U::G], unit = -INFINITY;
-        if (!mbar_wait(&full[at], turn)) lost = true;
-        top_load(r, top_ring + at * GPUOS_TOPB_BYTES, u0, b.x, b.y, lo, hi, x);
-#pragma unroll
-        for (uint32_t u = 0; u < U::G; u++) {
-            most[u] = -INFINITY; /* (a maximum passes a NaN over) */
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++) most[u] = fmaxf(most[u], x[u][j]);
-            unit = fmaxf(unit, most[u]);
-        }
-        __syncwarp(); /* this warp has its elements */
-        if (lane_id() == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[at])) : "memory");
-        if (fabsf(unit) <= 1e6f) {
-            if (unit > m) {
-                const float to = unit * L2E;
-                l *= top_ex2(ml - to);
-                m = unit, ml = to;
-            }
-            float all = 0.0f; /* (sums of sums: a rounding for each unit, not for each element) */
+    while (true) {
+        const ChooseRow<F32> r(d.a, c.row, d.dims[2], V);
+        const uint32_t from = c.u0, lo = max(from, r.lo), hi = min(c.end, r.hi), row = c.row;
+        const uint32_t first = c.cell;
+        /* sum of 2^(L2E x - ml), ml = L2E m rounded; and, of units whose largest is
+         * so far from 0 that rounding would tell, the sum of e^(x - far_m) */
+        float m = -2e6f, ml = -2e6f * L2E, l = 0.0f, far_m = -FLT_MAX, far_l = 0.0f;
+        uint64_t bar = 0;
+        float barf = -INFINITY;
+        __syncthreads(); /* (the last piece is done with what it gathered) */
+        if (t == 0) s.count = 0;
+        bool again; /* this piece has a further unit */
+#pragma unroll 1
+        do {
+            const uint32_t u0 = c.u0;
+            const uint2 b = whole(r, u0, lo, hi);
+            float x[U::G][8], most[U::G], unit = -INFINITY;
+            if (!mbar_wait(&full[at], turn)) lost = true;
+            top_load(r, top_ring + at * U::BYTES, u0, b.x, b.y, lo, hi, x);
 #pragma unroll
             for (uint32_t u = 0; u < U::G; u++) {
-                float sum = 0.0f;
+                most[u] = -INFINITY; /* (a maximum passes a NaN over) */
 #pragma unroll
-                for (uint32_t j = 0; j < 8; j++) sum += top_ex2(fmaf(x[u][j], L2E, -ml));
-                all += sum;
+                for (uint32_t j = 0; j < 8; j++) most[u] = fmaxf(most[u], x[u][j]);
+                unit = fmaxf(unit, most[u]);
             }
-            if (!(all == all)) { /* a NaN among the logits counts as -infinity */
-                all = 0.0f;
+            if (fabsf(unit) <= 1e6f) {
+                if (unit > m) {
+                    const float to = unit * L2E;
+                    l *= top_ex2(ml - to);
+                    m = unit, ml = to;
+                }
+                float all = 0.0f; /* (sums of sums: a rounding for each unit, not for each element) */
+#pragma unroll
+                for (uint32_t u = 0; u < U::G; u++) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; j++) sum += top_ex2(fmaf(x[u][j], L2E, -ml));
+                    all += sum;
+                }
+                if (!(all == all)) { /* a NaN among the logits counts as -infinity */
+                    all = 0.0f;
+#pragma unroll
+                    for (uint32_t u = 0; u < U::G; u++)
+#pragma unroll
+                        for (uint32_t j = 0; j < 8; j++) all += top_ex2(fmaf(fmaxf(x[u][j], -INFINITY), L2E, -ml));
+                }
+                l += all;
+            } else if (unit != -INFINITY) {
+                const float to = fmaxf(far_m, fminf(unit, FLT_MAX)); /* (an infinite maximum: the sum is infinite) */
+                far_l *= choose_exp(far_m - to);
+                far_m = to;
 #pragma unroll
                 for (uint32_t u = 0; u < U::G; u++)
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; j++) all += top_ex2(fmaf(fmaxf(x[u][j], -INFINITY), L2E, -ml));
+                    for (uint32_t j = 0; j < 8; j++) far_l += top_ex2((fmaxf(x[u][j], -INFINITY) - far_m) * L2E);
             }
-            l += all;
-        } else if (unit != -INFINITY) {
-            const float to = fmaxf(far_m, fminf(unit, FLT_MAX)); /* (an infinite maximum: the sum is infinite) */
-            far_l *= choose_exp(far_m - to);
-            far_m = to;
+            if (u0 == from) {
+                bar = top_bar(s, top_mine<F32>(x, u0, lo, hi, r.lo), K);
+                barf = bar ? choose_unkey((uint32_t)(bar >> 32)) : -INFINITY; /* (that bar's value itself may pass) */
+            }
+            if (u0 == from ? unit >= barf : unit > barf || bar == 0) { /* (an equal one in a later unit comes after) */
+                uint32_t reach = 0;
 #pragma unroll
-            for (uint32_t u = 0; u < U::G; u++)
-#pragma unroll
-                for (uint32_t j = 0; j < 8; j++) far_l += top_ex2((fmaxf(x[u][j], -INFINITY) - far_m) * L2E);
+                for (uint32_t i = 0; i < 8u * U::G; i++) reach |= !(x[i >> 3][i & 7u] < barf) ? 1u << i : 0u;
+#pragma unroll 1
+                for (; reach; reach &= reach - 1u) { /* (few: read again, so that no array needs an index) */
+                    const uint32_t k = (uint32_t)__ffs((int)reach) - 1u, o = U::at(k >> 3, k & 7u), p = u0 + o;
+                    float v = 0.0f;
+                    if (p >= b.x && p < b.y) {
+                        const unsigned char *e = top_ring + at * U::BYTES + o * SIZE;
+                        v = F32 ? *reinterpret_cast<const float *>(e) : bf1(*reinterpret_cast<const uint16_t *>(e));
+                    } else if (p >= lo && p < hi) {
+                        v = r.one(p);
+                    }
+                    top_push(s, bar, v, p, lo, hi, r.lo);
+                }
+            }
+            __syncwarp(); /* this warp is done with its elements */
+            if (lane_id() == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[at])) : "memory");
+            /* the unit's place takes the unit ahead, once all warps have left it; the warps take turns at that */
+            if (more) {
+                if (t == 32u * (n_unit % GPUOS_TOPB_WARPS)) {
+                    if (!mbar_wait(&empty[at], turn)) lost = true;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    copy(ahead, at);
+                }
+                more = work.next(ahead);
+            }
+            __syncwarp();
+            if (++at == ST) at = 0, turn ^= 1u;
+            n_unit++;
+            again = u0 + U::N < c.end;
+            c.u0 = u0 + U::N;
+            const uint32_t nth = (u0 - from) / U::N;
+            if (again && ((nth == 3u && c.end - u0 > 8u * U::N) || (nth & 7u) == 7u)) { /* a better bar, if some were gathered */
+                __syncthreads();
+                const uint32_t n = s.count;
+                if (n > K && n <= GPUOS_TOPB_ROOM && (nth == 3u || n > 64u + K)) {
+                    top_sort(s, n, K);
+                    if (t < K) s.got[t] = s.sorted[t];
+                    if (t == 0) s.count = K;
+                    bar = max(bar, s.sorted[K - 1u]);
+                    barf = choose_unkey((uint32_t)(bar >> 32));
+                }
+                __syncthreads();
+            }
+        } while (again);
+        if (l > 0.0f) { /* both sums under one maximum */
+            l *= top_ex2(-fmaf(m, L2E, -ml));
+            const float M = fmaxf(m, far_m);
+            l = l * choose_exp(m - M) + far_l * choose_exp(far_m - M);
+            m = M;
+        } else {
+            m = far_m, l = far_l;
         }
-        if (i == 0) {
-            bar = top_bar(s, top_mine<F32>(x, u0, lo, hi, r.lo), K);
-            barf = bar ? choose_unkey((uint32_t)(bar >> 32)) : -INFINITY; /* (that bar's value itself may pass) */
-        }
-        if (i == 0 ? unit >= barf : unit > barf || bar == 0) { /* (an equal one in a later unit comes after) */
-#pragma unroll
-            for (uint32_t u = 0; u < U::G; u++) {
-                if (!(most[u] >= barf)) continue;
-#pragma unroll
-                for (uint32_t j = 0; j < 8; j++)
-                    if (!(x[u][j] < barf)) top_push(s, bar, x[u][j], u0 + U::at(u, j), lo, hi, r.lo);
+        if (__syncthreads_or(lost)) l = __int_as_float(0x7FFFFFFF);
+        uint32_t n = s.count;
+        if (n > GPUOS_TOPB_ROOM) n = top_gather_slow(s, r, from, lo, hi, K);
+        top_sort(s, n, K);
+        top_block_softmax(s, m, l);
+        const uint32_t row0 = row * cells, end = row0 + c.end / 256u;
+        if (first == row0 && end == row0 + cells) {
+            top_block_write(d, row, s, m, l);
+        } else {
+            /* the row's last block joins the pieces: a block's first piece is in its
+             * place 0, a later one (which begins a row) in 1; they are counted at
+             * the row's first block */
+            const uint32_t blk0 = runs.S ? row * runs.S : runs.run_of(row0), F = runs.S ? runs.S : runs.run_of(row0 + cells - 1u) - blk0 + 1u;
+            unsigned char *p = top_part(&d, blockIdx.x * 2u + (blockIdx.x == blk0 ? 1u : 0u));
+            if (t < K) __stcg(reinterpret_cast<unsigned long long *>(p + 16) + t, (unsigned long long)s.sorted[t]);
+            if (t == 0) __stcg(reinterpret_cast<float2 *>(p), make_float2(m, l));
+            __syncthreads();
+            if (t == 0) {
+                uint32_t *ctr = reinterpret_cast<uint32_t *>(d.aux2) + blk0;
+                s.last = atom_add_acq_rel_gpu32(ctr, 1u) == F - 1u;
+                if (s.last) *ctr = 0; /* left zero for the next call */
+            }
+            __syncthreads();
+            if (s.last) {
+                auto part = [&](uint32_t f) { return top_part(&d, (blk0 + f) * 2u + (f == 0 ? 1u : 0u)); };
+                m = -FLT_MAX, l = 0.0f;
+                if (t < F) {
+                    const float2 ms = __ldcg(reinterpret_cast<const float2 *>(part(t)));
+                    m = ms.x, l = ms.y;
+                }
+                for (uint32_t i = t; i < F * K; i += GPUOS_TOPB_THREADS) /* (entries that are not there are 0, and below all others) */
+                    s.got[i] = __ldcg(reinterpret_cast<const unsigned long long *>(part(i / K) + 16) + i % K);
+                __syncthreads();
+                top_sort(s, F * K, K);
+                top_block_softmax(s, m, l);
+                top_block_write(d, row, s, m, l);
             }
         }
-        /* the unit's place takes the next but two, once all warps have left it; the warps take turns at that */
-        if (t == 32u * (i % GPUOS_TOPB_WARPS) && i + GPUOS_TOPB_STAGES < units) {
-            if (!mbar_wait(&empty[at], turn)) lost = true;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            copy(i + GPUOS_TOPB_STAGES);
-        }
-        __syncwarp();
+        if (end >= work.last) break;
+        work.piece(end, c);
     }
-    if (l > 0.0f) { /* both sums under one maximum */
-        float f;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(-fmaf(m, L2E, -ml)));
-        l *= f;
-        const float M = fmaxf(m, far_m);
-        l = l * choose_exp(m - M) + far_l * choose_exp(far_m - M);
-        m = M;
-    } else {
-        m = far_m, l = far_l;
-    }
-    if (__syncthreads_or(lost)) l = __int_as_float(0x7FFFFFFF);
-    uint32_t n = s.count;
-    if (n > GPUOS_TOPB_ROOM) n = top_gather_slow(s, r, from, lo, hi, K);
-    top_sort(s, n, K);
-    top_block_softmax(s, m, l);
-    if (S == 1) {
-        top_block_write(d, row, s, m, l);
-        return;
-    }
-    /* the row's last block joins the runs' states */
-    unsigned char *p = top_part(&d, blockIdx.x);
-    if (t < K) __stcg(reinterpret_cast<unsigned long long *>(p + 16) + t, (unsigned long long)s.sorted[t]);
-    if (t == 0) __stcg(reinterpret_cast<float2 *>(p), make_float2(m, l));
-    __syncthreads();
-    if (t == 0) {
-        uint32_t *ctr = reinterpret_cast<uint32_t *>(d.aux2) + row;
-        s.last = atom_add_acq_rel_gpu32(ctr, 1u) == S - 1u;
-        if (s.last) *ctr = 0; /* left zero for the next call */
-    }
-    __syncthreads();
-    if (!s.last) return;
-    m = -FLT_MAX, l = 0.0f;
-    if (t < S) {
-        const float2 ms = __ldcg(reinterpret_cast<const float2 *>(top_part(&d, row * S + t)));
-        m = ms.x, l = ms.y;
-    }
-    for (uint32_t i = t; i < S * K; i += GPUOS_TOPB_THREADS) /* (entries that are not there are 0, and below all others) */
-        s.got[i] = __ldcg(reinterpret_cast<const unsigned long long *>(top_part(&d, row * S + i / K) + 16) + i % K);
-    __syncthreads();
-    top_sort(s, S * K, K);
-    top_block_softmax(s, m, l);
-    top_block_write(d, row, s, m, l);
 }
 
 template <bool F32>
 static int top_launch(const gpuos_devdesc &d, void *stream)
 {
-    /* runs of a row: the number with the least elements one after another, if
-     * as many blocks as there are slots run at a time; none below a unit, no
-     * more than a row's last block can join and the workspace holds */
+    /* Runs: as many as run at a time, and none below a unit or a 32nd of a row
+     * (what a row's last block can join). Whole rows, or as many equal runs of
+     * each as fit, are one piece for each block; other runs balance better but
+     * have more pieces, each of which has a start and an end. */
+    const uint64_t B = d.dims[0], cells = ((uint64_t)d.dims[1] + 7u + 255u) / 256u, unit = GPUOS_TOPB_UNIT / 256u;
+    const uint64_t most = min(min((uint64_t)GPUOS_TOPB_SLOTS, 32u * B), B * ((cells + unit - 1u) / unit));
+    if (B * cells >= 1ull << 32) return -1; /* (elements for 500 GB) */
     gpuos_devdesc e = d;
-    const uint64_t B = d.dims[0], V = d.dims[1];
-    const uint64_t most = min(min((V + 7u + TopUnit<F32>::N - 1u) / TopUnit<F32>::N, (uint64_t)32u), GPUOS_TOP_TILES / B);
-    uint64_t S = 1, least = ~0ull;
-    for (uint64_t n = 1; n <= most || n == 1; n++) {
-        const uint64_t cost = (B * n + GPUOS_TOPB_SLOTS - 1u) / GPUOS_TOPB_SLOTS * (V / n + GPUOS_TOPB_FIXED);
-        if (cost < least) least = cost, S = n;
+    uint64_t grid = most;
+    e.dep[0] = 0;
+    if (B <= most) {
+        const uint64_t S = most / B, even = cells / S + GPUOS_TOPB_FIXED, uneven = B * cells / most + 2u * GPUOS_TOPB_FIXED;
+        if (even <= uneven) grid = B * S, e.dep[0] = S;
     }
-    e.ntiles = (uint32_t)(B * S);
+    e.dep[1] = B * cells / grid | (B * cells % grid) << 32;
     static std::atomic<bool> known[64];
-    if (choose_smem((const void *)gpuos_top_kernel<F32>, GPUOS_TOPB_STAGES * GPUOS_TOPB_BYTES, known) != 0) return -1;
-    return choose_launch(gpuos_top_kernel<F32>, dim3(e.ntiles), GPUOS_TOPB_THREADS, GPUOS_TOPB_STAGES * GPUOS_TOPB_BYTES, stream, e);
+    if (choose_smem((const void *)gpuos_top_kernel<F32>, GPUOS_TOPB_STAGES * TopUnit<F32>::BYTES, known) != 0) return -1;
+    return choose_launch(gpuos_top_kernel<F32>, dim3((uint32_t)grid), GPUOS_TOPB_THREADS, GPUOS_TOPB_STAGES * TopUnit<F32>::BYTES, stream, e);
 }
 
 /* ---------------------------------------------------------------------------

@@ -91,7 +91,8 @@ static inline GPUOS_HD bool gpuos_top_ok(uint32_t dtype, uint64_t a, uint64_t id
                                          const uint32_t *m)
 {
     return gpuos_rows_ok(dtype, a, m[1], m[2]) && ids && logp && ws && ((ids | logp | lse) & 3u) == 0 && (ws & 15u) == 0 &&
-           m[3] >= 1 && m[3] <= GPUOS_TOP_MAX_K && m[3] <= m[1];
+           m[3] >= 1 && m[3] <= GPUOS_TOP_MAX_K && m[3] <= m[1] &&
+           (uint64_t)m[0] * (((uint64_t)m[1] + 262u) / 256u) < 1ull << 32; /* (runs of 256 tokens are counted in 32 bits) */
 }
 static inline GPUOS_HD bool gpuos_route_ok(uint32_t dtype, uint64_t a, uint64_t bias, uint64_t ids, uint64_t weights,
                                            uint64_t rows, const uint32_t *m)

@@ -241,8 +241,9 @@ def test_top_of_odd_rows(case, kind, run):
 
 
 @pytest.mark.parametrize("kind", ["plain", "up", "masked"])
-def test_top_of_whole_rows(kind):
-    """More rows than a launch cuts up: a block goes through all of a row."""
+def test_top_of_many_rows(kind):
+    """More rows than a launch has blocks: runs of several rows, and pieces of rows."""
+    _check_top("eager", _top_rows(2, 460, 9000, False, kind), False, 1, 7)
     _check_top("eager", _top_rows(1, 1300, 20001, True, kind), True, 0, 64)
     _check_top("executor", _top_rows(1, 1300, 20001, False, kind), False, 3, 33)
 
