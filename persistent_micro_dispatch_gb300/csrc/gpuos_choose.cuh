@@ -100,8 +100,8 @@ DEV bool adjust_args(const gpuos_devdesc *d, uint32_t b, AdjustArgs &a)
     a.tokens = reinterpret_cast<const int32_t *>(d->b) + (uint64_t)b * Lcap;
     a.bias = reinterpret_cast<const int2 *>(d->aux2) + (uint64_t)b * Nb;
     a.mask = a.q.mask < 0 ? nullptr : reinterpret_cast<const uint32_t *>(d->aux1) + (uint64_t)(uint32_t)a.q.mask * ((V + 31u) / 32u);
-    a.plain = a.q.temperature > 0.0f ? 1.0f / a.q.temperature : 1.0f;
-    a.above = a.plain / a.q.repetition;
+    a.plain = a.q.temperature > 0.0f ? rcp_approx(a.q.temperature) : 1.0f;
+    a.above = a.plain * rcp_approx(a.q.repetition);
     a.below = a.plain * a.q.repetition;
     a.frequency = a.plain * a.q.frequency;
     a.presence = a.plain * a.q.presence;
@@ -110,8 +110,9 @@ DEV bool adjust_args(const gpuos_devdesc *d, uint32_t b, AdjustArgs &a)
            (uint32_t)a.q.biases <= Nb;
 }
 /* x under a token's counter, divided by the temperature: a factor for each
- * request and side, and one multiply-add. (The factors' roundings, 2^-24 each,
- * stand where quotients' would; a division is ten times the code.) */
+ * request and side, and one multiply-add. (The factors are off by 5 x 2^-24 at
+ * most, two hardware reciprocals of 2^-23 and a product; divisions would be ten
+ * times the code, for each thread.) */
 DEV float adjust_penalty(const AdjustArgs &a, float x, uint32_t w)
 {
     const uint32_t c = w & GPUOS_ADJUST_COUNT;
@@ -1004,23 +1005,20 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
 
 #ifndef GPUOS_EXECUTOR_ONLY
 #define GPUOS_ADJUSTB_LONG 8192u
-/* As kv4_launch, with a grid of two dimensions and clusters. */
-static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d,
-                         uint32_t cluster = 1)
+#define GPUOS_ADJUSTB_MANY (4u << 20)
+/* As kv4_launch, with a grid of two dimensions. */
+static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d)
 {
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = cluster;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
     c.gridDim = blocks;
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = (cudaStream_t)stream;
-    c.attrs = at;
-    c.numAttrs = cluster > 1 ? 2 : 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
     if (cudaLaunchKernelEx(&c, kernel, d) == cudaSuccess) return 0;
     (void)cudaGetLastError(); /* reported here */
     return -1;
@@ -1035,13 +1033,6 @@ static int choose_smem(const void *kernel, uint32_t bytes, std::atomic<bool> (&k
     known[dev].store(true, std::memory_order_relaxed);
     return 0;
 }
-/* Every thread of the cluster's blocks; what each wrote before, also to the
- * others' shared memory, is seen after. */
-DEV void choose_cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 /* ---------------------------------------------------------------------------
  * Logits adjusted, launched: a block takes 16 places for each of its threads
  * of one row. A thread's logits and mask words are on their way while the
@@ -1108,13 +1099,10 @@ DEV void adjust_unpack(const AdjustRaw<F32, SAME> &raw, uint32_t r, float (&x)[8
     }
 }
 
-/* (CLUSTER blocks of a row's neighbouring chunks count together: each looks at
- * its share of the request's tokens, and adds to the counter of whichever has
- * the token, in that block's shared memory) */
-template <bool F32, bool SAME, int THREADS, int CLUSTER>
-__global__ void __launch_bounds__(THREADS, 1280 / THREADS) gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
+template <bool F32, bool SAME, int THREADS, int VECS>
+__global__ void __launch_bounds__(THREADS, (VECS == 2 ? 1280 : 1024) / THREADS) gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
 {
-    constexpr uint32_t CHUNK = THREADS * 16u;
+    constexpr uint32_t CHUNK = THREADS * VECS * 8u;
     extern __shared__ __align__(16) uint32_t adjust_ctr[]; /* CHUNK counters */
     __shared__ int32_t listed[THREADS];
     kv4_after_previous();
@@ -1122,55 +1110,56 @@ __global__ void __launch_bounds__(THREADS, 1280 / THREADS) gpuos_adjust_kernel(c
     const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
     const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi); /* (a cluster's last may be empty) */
     const uint32_t shift = in.lo - out.lo, r = SAME ? 0u : shift & (F32 ? 3u : 7u); /* (modulo 2^32, like the places) */
-    AdjustRaw<F32, SAME> raw[2];
+    AdjustRaw<F32, SAME> raw[VECS];
 #pragma unroll
-    for (uint32_t k = 0; k < 2; k++) {
+    for (uint32_t k = 0; k < VECS; k++) {
         const uint32_t at = from + (k * THREADS + t) * 8u;
-        adjust_raw(in, at + shift - r, r, at < hi, raw[k]); /* (places before 0 wrap round, and are not in the row) */
+        if (SAME && at >= lo && at + 8u <= hi) {
+#pragma unroll
+            for (uint32_t v = 0; v < AdjustRaw<F32, SAME>::N; v++) raw[k].v[v] = in.vec(at)[v];
+        } else {
+            adjust_raw(in, at + shift - r, r, at < hi, raw[k]); /* (places before 0 wrap round, and are not in the row) */
+        }
     }
+    /* the first tokens too, whether the request has had them or not: their loads
+     * need not wait for the record's */
+    constexpr uint32_t EARLY = 4;
+    const uint32_t Lcap = d.dims[4];
+    int32_t early[EARLY];
+#pragma unroll
+    for (uint32_t k = 0; k < EARLY; k++)
+        early[k] = k * THREADS + t < Lcap ? reinterpret_cast<const int32_t *>(d.b)[(uint64_t)b * Lcap + k * THREADS + t] : -1;
     AdjustArgs a;
     if (!adjust_args(&d, b, a)) return; /* (all of a row's blocks) */
-    uint32_t bits[2] = {0xFFu, 0xFFu};
+    uint32_t bits[VECS];
 #pragma unroll
-    for (uint32_t k = 0; k < 2; k++) {
+    for (uint32_t k = 0; k < VECS; k++) {
         const uint32_t at = from + (k * THREADS + t) * 8u;
-        if (a.mask && at < hi) bits[k] = adjust_bits(a, (int32_t)at - (int32_t)out.lo, V);
+        bits[k] = 0xFFu;
+        if (a.mask && at < hi) bits[k] = out.lo == 0 ? a.mask[at >> 5] >> (at & 31u) : adjust_bits(a, (int32_t)at - (int32_t)out.lo, V);
     }
     const bool counted = a.penal || a.q.biases > 0;
     if (counted) {
 #pragma unroll
-        for (uint32_t k = 0; k < 4; k++) reinterpret_cast<uint4 *>(adjust_ctr)[k * THREADS + t] = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t rank = 0; /* in the cluster */
-        if (CLUSTER > 1) {
-            asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-            choose_cluster_sync();
-        } else {
-            __syncthreads();
-        }
+        for (uint32_t k = 0; k < 2 * VECS; k++) reinterpret_cast<uint4 *>(adjust_ctr)[k * THREADS + t] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
         if (a.penal) {
             const uint32_t n = (uint32_t)a.q.length, prompt = (uint32_t)a.q.prompt;
-            const uint32_t begin = from - rank * CHUNK, mine = smem_addr(adjust_ctr); /* (the cluster's first place) */
+            auto mark = [&](int32_t token, uint32_t i) {
+                const uint32_t at = (uint32_t)token + out.lo - from;
+                if ((uint32_t)token >= V || at >= CHUNK || i >= n) return;
+                if (i < prompt) atomicOr(adjust_ctr + at, GPUOS_ADJUST_HAD);
+                else atomicAdd(adjust_ctr + at, 1u);
+            };
+#pragma unroll
+            for (uint32_t k = 0; k < EARLY; k++) mark(early[k], k * THREADS + t);
 #pragma unroll 1
-            for (uint32_t i0 = rank * THREADS + t; i0 < n; i0 += 8u * THREADS * CLUSTER) {
+            for (uint32_t i0 = EARLY * THREADS + t; i0 < n; i0 += 8u * THREADS) {
                 int32_t tok[8];
 #pragma unroll
-                for (uint32_t k = 0; k < 8; k++) tok[k] = i0 + k * THREADS * CLUSTER < n ? a.tokens[i0 + k * THREADS * CLUSTER] : -1;
+                for (uint32_t k = 0; k < 8; k++) tok[k] = i0 + k * THREADS < n ? a.tokens[i0 + k * THREADS] : -1;
 #pragma unroll
-                for (uint32_t k = 0; k < 8; k++) {
-                    const uint32_t at = (uint32_t)tok[k] + out.lo - begin;
-                    if ((uint32_t)tok[k] >= V || at >= CHUNK * CLUSTER) continue;
-                    const bool had = i0 + k * THREADS * CLUSTER < prompt;
-                    if (CLUSTER > 1) {
-                        uint32_t remote;
-                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(mine + at % CHUNK * 4u), "r"(at / CHUNK));
-                        if (had) asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(remote), "r"(GPUOS_ADJUST_HAD) : "memory");
-                        else asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(remote), "r"(1u) : "memory");
-                    } else if (had) {
-                        atomicOr(adjust_ctr + at, GPUOS_ADJUST_HAD);
-                    } else {
-                        atomicAdd(adjust_ctr + at, 1u);
-                    }
-                }
+                for (uint32_t k = 0; k < 8; k++) mark(tok[k], i0 + k * THREADS);
             }
         }
         for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
@@ -1178,11 +1167,10 @@ __global__ void __launch_bounds__(THREADS, 1280 / THREADS) gpuos_adjust_kernel(c
             if (i < THREADS) listed[i] = (int32_t)token;
             if (token < V && at < CHUNK) atomicOr(adjust_ctr + at, GPUOS_ADJUST_LISTED);
         }
-        if (CLUSTER > 1) choose_cluster_sync();
-        else __syncthreads();
+        __syncthreads();
     }
 #pragma unroll
-    for (uint32_t k = 0; k < 2; k++) {
+    for (uint32_t k = 0; k < VECS; k++) {
         const uint32_t at = from + (k * THREADS + t) * 8u;
         if (at >= hi) continue;
         float x[8];
@@ -1232,14 +1220,13 @@ __global__ void __launch_bounds__(THREADS, 1280 / THREADS) gpuos_adjust_kernel(c
         out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
     }
 }
-template <bool F32, bool SAME, int THREADS, int CLUSTER>
+template <bool F32, bool SAME, int THREADS, int VECS>
 static int adjust_launch(const gpuos_devdesc &d, void *stream)
 {
-    constexpr uint32_t CHUNK = THREADS * 16u;
-    uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + CHUNK - 1u) / CHUNK);
-    chunks = (chunks + CLUSTER - 1u) / CLUSTER * CLUSTER;
+    constexpr uint32_t CHUNK = THREADS * VECS * 8u;
+    const uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + CHUNK - 1u) / CHUNK);
     static std::atomic<bool> known[64];
-    if (CHUNK * 4u > 32768u && choose_smem((const void *)gpuos_adjust_kernel<F32, SAME, THREADS, CLUSTER>, CHUNK * 4u, known) != 0) return -1;
+    if (CHUNK * 4u > 32768u && choose_smem((const void *)gpuos_adjust_kernel<F32, SAME, THREADS, VECS>, CHUNK * 4u, known) != 0) return -1;
     gpuos_devdesc e = d;
     /* (rows beyond the grid's second dimension: launches of their own) */
     for (uint32_t row = 0; row < d.dims[0]; row += 65535u) {
@@ -1250,16 +1237,16 @@ static int adjust_launch(const gpuos_devdesc &d, void *stream)
         e.b = d.b + (uint64_t)row * d.dims[4] * 4u;
         e.aux0 = d.aux0 + (uint64_t)row * sizeof(gpuos_logits_request);
         e.aux2 = d.aux2 + (uint64_t)row * (d.dims[5] >> 16) * sizeof(gpuos_logits_bias);
-        if (choose_launch(gpuos_adjust_kernel<F32, SAME, THREADS, CLUSTER>, dim3(chunks, e.dims[0]), THREADS, CHUNK * 4u, stream, e, CLUSTER) != 0)
-            return -1;
+        if (choose_launch(gpuos_adjust_kernel<F32, SAME, THREADS, VECS>, dim3(chunks, e.dims[0]), THREADS, CHUNK * 4u, stream, e) != 0) return -1;
     }
     return 0;
 }
 template <bool F32, bool SAME>
 static int adjust_launch_by(const gpuos_devdesc &d, void *stream)
 {
-    if (d.dims[4] > GPUOS_ADJUSTB_LONG) return adjust_launch<F32, SAME, 1024, 1>(d, stream);
-    return adjust_launch<F32, SAME, 256, 1>(d, stream);
+    if (d.dims[4] > GPUOS_ADJUSTB_LONG) return adjust_launch<F32, SAME, 1024, 2>(d, stream);
+    if ((uint64_t)d.dims[0] * d.dims[1] > GPUOS_ADJUSTB_MANY) return adjust_launch<F32, SAME, 256, 4>(d, stream);
+    return adjust_launch<F32, SAME, 256, 2>(d, stream);
 }
 template <bool F32>
 static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
@@ -2411,9 +2398,10 @@ static int choose_eager_launch(const gpuos_devdesc &d, void *stream)
 static int choose_preload()
 {
     const void *const all[] = {
-        (const void *)gpuos_adjust_kernel<true, true, 256, 1>, (const void *)gpuos_adjust_kernel<true, true, 1024, 1>,
-        (const void *)gpuos_adjust_kernel<true, false, 256, 1>, (const void *)gpuos_adjust_kernel<true, false, 1024, 1>, (const void *)gpuos_adjust_kernel<false, true, 256, 1>, (const void *)gpuos_adjust_kernel<false, true, 1024, 1>,
-        (const void *)gpuos_adjust_kernel<false, false, 256, 1>, (const void *)gpuos_adjust_kernel<false, false, 1024, 1>,
+        (const void *)gpuos_adjust_kernel<true, true, 256, 2>, (const void *)gpuos_adjust_kernel<true, true, 256, 4>, (const void *)gpuos_adjust_kernel<true, true, 1024, 2>,
+        (const void *)gpuos_adjust_kernel<true, false, 256, 2>, (const void *)gpuos_adjust_kernel<true, false, 256, 4>, (const void *)gpuos_adjust_kernel<true, false, 1024, 2>,
+        (const void *)gpuos_adjust_kernel<false, true, 256, 2>, (const void *)gpuos_adjust_kernel<false, true, 256, 4>, (const void *)gpuos_adjust_kernel<false, true, 1024, 2>,
+        (const void *)gpuos_adjust_kernel<false, false, 256, 2>, (const void *)gpuos_adjust_kernel<false, false, 256, 4>, (const void *)gpuos_adjust_kernel<false, false, 1024, 2>,
         (const void *)gpuos_top_kernel<true>, (const void *)gpuos_top_kernel<false>,
         (const void *)gpuos_route_kernel<true, 8, 8, true>, (const void *)gpuos_route_kernel<true, 8, 8, false>,
         (const void *)gpuos_route_kernel<true, 8, 16, true>, (const void *)gpuos_route_kernel<true, 8, 16, false>,
