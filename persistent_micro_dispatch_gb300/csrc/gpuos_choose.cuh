@@ -1004,21 +1004,27 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
 }
 
 #ifndef GPUOS_EXECUTOR_ONLY
-#define GPUOS_ADJUSTB_LONG 8192u
+#define GPUOS_ADJUSTB_THREADS 256u
+#define GPUOS_ADJUSTB_LONG 16384u
+#define GPUOS_ADJUSTL_FEW 304u
 #define GPUOS_ADJUSTB_MANY (4u << 20)
-/* As kv4_launch, with a grid of two dimensions. */
-static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d)
+/* As kv4_launch, with a grid of two dimensions and clusters. */
+static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d,
+                         uint32_t cluster = 1)
 {
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t c = {};
     c.gridDim = blocks;
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = (cudaStream_t)stream;
-    c.attrs = &at;
-    c.numAttrs = 1;
+    c.attrs = at;
+    c.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&c, kernel, d) == cudaSuccess) return 0;
     (void)cudaGetLastError(); /* reported here */
     return -1;
@@ -1099,28 +1105,90 @@ DEV void adjust_unpack(const AdjustRaw<F32, SAME> &raw, uint32_t r, float (&x)[8
     }
 }
 
-template <bool F32, bool SAME, int THREADS, int VECS>
-__global__ void __launch_bounds__(THREADS, (VECS == 2 ? 1280 : 1024) / THREADS) gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
+/* The vectors of a thread's eight places at `at`. */
+template <bool F32, bool SAME>
+DEV void adjust_load(const ChooseRow<F32> &in, uint32_t at, uint32_t shift, uint32_t r, uint32_t lo, uint32_t hi, AdjustRaw<F32, SAME> &raw)
 {
-    constexpr uint32_t CHUNK = THREADS * VECS * 8u;
-    extern __shared__ __align__(16) uint32_t adjust_ctr[]; /* CHUNK counters */
+    if (SAME && at >= lo && at + 8u <= hi) {
+#pragma unroll
+        for (uint32_t v = 0; v < AdjustRaw<F32, SAME>::N; v++) raw.v[v] = in.vec(at)[v];
+    } else {
+        adjust_raw(in, at + shift - r, r, at < hi, raw); /* (places before 0 wrap round, and are not in the row) */
+    }
+}
+/* Eight places with their counters and mask bits, done and written but for
+ * those that are listed or not in [lo, hi). */
+template <bool F32, bool SAME>
+DEV void adjust_eight(const AdjustArgs &a, const ChooseRow<F32> &out, const AdjustRaw<F32, SAME> &raw, uint32_t r, const uint4 &w0, const uint4 &w1,
+                      uint32_t bits, uint32_t at, uint32_t lo, uint32_t hi)
+{
+    float x[8];
+    adjust_unpack(raw, r, x);
+    const uint32_t any = (w0.x | w0.y | w0.z | w0.w) | (w1.x | w1.y | w1.z | w1.w);
+    if (any) {
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) x[j] = adjust_penalty(a, x[j], w[j]);
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) x[j] *= a.plain;
+    }
+    if (a.mask) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) x[j] = bits & 1u << j ? x[j] : -INFINITY;
+    }
+    if (!(any & GPUOS_ADJUST_LISTED) && at >= lo && at + 8u <= hi) {
+        uint4 *o = const_cast<uint4 *>(out.vec(at));
+        if (F32) {
+            o[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            o[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+        } else {
+            o[0] = pack8(x);
+        }
+    } else {
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++)
+            if (!(w[j] & GPUOS_ADJUST_LISTED) && at + j >= lo && at + j < hi) out.put(at + j, x[j]);
+    }
+}
+DEV uint32_t adjust_mask(const AdjustArgs &a, uint32_t at, uint32_t lo, uint32_t V)
+{
+    if (!a.mask) return 0xFFu;
+    return lo == 0 ? a.mask[at >> 5] >> (at & 31u) : adjust_bits(a, (int32_t)at - (int32_t)lo, V);
+}
+/* The listed tokens of places [from, to): nobody has written them (out may be
+ * the input). `listed`: the first THREADS entries' tokens; counter(place). */
+template <bool F32, int THREADS, typename Counter>
+DEV void adjust_listed(const AdjustArgs &a, const ChooseRow<F32> &in, const ChooseRow<F32> &out, uint32_t V, uint32_t shift, uint32_t from, uint32_t to,
+                       const int32_t *listed, const Counter &counter)
+{
+    for (uint32_t i = threadIdx.x; i < (uint32_t)a.q.biases; i += THREADS) {
+        const int2 e = a.bias[i];
+        const uint32_t at = (uint32_t)e.x + out.lo;
+        if ((uint32_t)e.x >= V || at < from || at >= to) continue;
+        bool again = false; /* listed again further on: the later entry counts */
+        for (uint32_t k = i + 1; k < min((uint32_t)a.q.biases, (uint32_t)THREADS); k++) again |= listed[k] == e.x;
+        if (again || ((uint32_t)a.q.biases > THREADS && adjust_again(a, max(i, THREADS - 1u), e.x))) continue;
+        const float y = fmaf(__int_as_float(e.y), a.plain, adjust_penalty(a, in.one(at + shift), counter(at)));
+        out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
+    }
+}
+template <bool F32, bool SAME, int VECS>
+__global__ void __launch_bounds__(GPUOS_ADJUSTB_THREADS, (VECS == 2 ? 1280 : 1024) / GPUOS_ADJUSTB_THREADS)
+    gpuos_adjust_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    constexpr uint32_t THREADS = GPUOS_ADJUSTB_THREADS, CHUNK = THREADS * VECS * 8u;
+    __shared__ __align__(16) uint32_t ctr[CHUNK];
     __shared__ int32_t listed[THREADS];
     kv4_after_previous();
     const uint32_t V = d.dims[1], b = blockIdx.y, t = threadIdx.x;
     const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
-    const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi); /* (a cluster's last may be empty) */
+    const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi);
     const uint32_t shift = in.lo - out.lo, r = SAME ? 0u : shift & (F32 ? 3u : 7u); /* (modulo 2^32, like the places) */
     AdjustRaw<F32, SAME> raw[VECS];
 #pragma unroll
-    for (uint32_t k = 0; k < VECS; k++) {
-        const uint32_t at = from + (k * THREADS + t) * 8u;
-        if (SAME && at >= lo && at + 8u <= hi) {
-#pragma unroll
-            for (uint32_t v = 0; v < AdjustRaw<F32, SAME>::N; v++) raw[k].v[v] = in.vec(at)[v];
-        } else {
-            adjust_raw(in, at + shift - r, r, at < hi, raw[k]); /* (places before 0 wrap round, and are not in the row) */
-        }
-    }
+    for (uint32_t k = 0; k < VECS; k++) adjust_load(in, from + (k * THREADS + t) * 8u, shift, r, lo, hi, raw[k]);
     /* the first tokens too, whether the request has had them or not: their loads
      * need not wait for the record's */
     constexpr uint32_t EARLY = 4;
@@ -1135,21 +1203,20 @@ __global__ void __launch_bounds__(THREADS, (VECS == 2 ? 1280 : 1024) / THREADS) 
 #pragma unroll
     for (uint32_t k = 0; k < VECS; k++) {
         const uint32_t at = from + (k * THREADS + t) * 8u;
-        bits[k] = 0xFFu;
-        if (a.mask && at < hi) bits[k] = out.lo == 0 ? a.mask[at >> 5] >> (at & 31u) : adjust_bits(a, (int32_t)at - (int32_t)out.lo, V);
+        bits[k] = at < hi ? adjust_mask(a, at, out.lo, V) : 0u;
     }
     const bool counted = a.penal || a.q.biases > 0;
     if (counted) {
 #pragma unroll
-        for (uint32_t k = 0; k < 2 * VECS; k++) reinterpret_cast<uint4 *>(adjust_ctr)[k * THREADS + t] = make_uint4(0u, 0u, 0u, 0u);
+        for (uint32_t k = 0; k < 2 * VECS; k++) reinterpret_cast<uint4 *>(ctr)[k * THREADS + t] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
         if (a.penal) {
             const uint32_t n = (uint32_t)a.q.length, prompt = (uint32_t)a.q.prompt;
             auto mark = [&](int32_t token, uint32_t i) {
                 const uint32_t at = (uint32_t)token + out.lo - from;
                 if ((uint32_t)token >= V || at >= CHUNK || i >= n) return;
-                if (i < prompt) atomicOr(adjust_ctr + at, GPUOS_ADJUST_HAD);
-                else atomicAdd(adjust_ctr + at, 1u);
+                if (i < prompt) atomicOr(ctr + at, GPUOS_ADJUST_HAD);
+                else atomicAdd(ctr + at, 1u);
             };
 #pragma unroll
             for (uint32_t k = 0; k < EARLY; k++) mark(early[k], k * THREADS + t);
@@ -1165,7 +1232,7 @@ __global__ void __launch_bounds__(THREADS, (VECS == 2 ? 1280 : 1024) / THREADS) 
         for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
             const uint32_t token = (uint32_t)a.bias[i].x, at = token + out.lo - from;
             if (i < THREADS) listed[i] = (int32_t)token;
-            if (token < V && at < CHUNK) atomicOr(adjust_ctr + at, GPUOS_ADJUST_LISTED);
+            if (token < V && at < CHUNK) atomicOr(ctr + at, GPUOS_ADJUST_LISTED);
         }
         __syncthreads();
     }
@@ -1173,80 +1240,128 @@ __global__ void __launch_bounds__(THREADS, (VECS == 2 ? 1280 : 1024) / THREADS) 
     for (uint32_t k = 0; k < VECS; k++) {
         const uint32_t at = from + (k * THREADS + t) * 8u;
         if (at >= hi) continue;
-        float x[8];
-        adjust_unpack(raw[k], r, x);
         uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
-        if (counted) {
-            w0 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t)];
-            w1 = reinterpret_cast<const uint4 *>(adjust_ctr)[2 * (k * THREADS + t) + 1];
-        }
-        const uint32_t any = (w0.x | w0.y | w0.z | w0.w) | (w1.x | w1.y | w1.z | w1.w);
-        if (any) {
-            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++) x[j] = adjust_penalty(a, x[j], w[j]);
-        } else {
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++) x[j] *= a.plain;
-        }
-        if (a.mask) {
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++) x[j] = bits[k] & 1u << j ? x[j] : -INFINITY;
-        }
-        if (!(any & GPUOS_ADJUST_LISTED) && at >= lo && at + 8u <= hi) {
-            uint4 *o = const_cast<uint4 *>(out.vec(at));
-            if (F32) {
-                o[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-                o[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
-            } else {
-                o[0] = pack8(x);
-            }
-        } else {
-            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-            for (uint32_t j = 0; j < 8; j++)
-                if (!(w[j] & GPUOS_ADJUST_LISTED) && at + j >= lo && at + j < hi) out.put(at + j, x[j]);
-        }
+        if (counted) w0 = reinterpret_cast<const uint4 *>(ctr)[2 * (k * THREADS + t)], w1 = reinterpret_cast<const uint4 *>(ctr)[2 * (k * THREADS + t) + 1];
+        adjust_eight(a, out, raw[k], r, w0, w1, bits[k], at, lo, hi);
     }
-    /* listed tokens: nobody has written them (out may be the input) */
-    for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
-        const int2 e = a.bias[i];
-        const uint32_t at = (uint32_t)e.x + out.lo;
-        if ((uint32_t)e.x >= V || at < from || at - from >= CHUNK) continue;
-        bool again = false; /* listed again further on: the later entry counts */
-        for (uint32_t k = i + 1; k < min((uint32_t)a.q.biases, (uint32_t)THREADS); k++) again |= listed[k] == e.x;
-        if (again || ((uint32_t)a.q.biases > THREADS && adjust_again(a, max(i, THREADS - 1u), e.x))) continue;
-        const float y = fmaf(__int_as_float(e.y), a.plain, adjust_penalty(a, in.one(at + shift), adjust_ctr[at - from]));
-        out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
-    }
+    adjust_listed<F32, (int)THREADS>(a, in, out, V, shift, lo, hi, listed, [&](uint32_t at) { return ctr[at - from]; });
 }
-template <bool F32, bool SAME, int THREADS, int VECS>
-static int adjust_launch(const gpuos_devdesc &d, void *stream)
+/* Long histories: eight blocks of neighbouring chunks, a cluster, share them.
+ * Each counts an eighth of the tokens, for all eight chunks, in 16 bits (15 and
+ * the prompt's flag); a thread then adds up its places' eight counters out of
+ * the eight blocks' shared memory. (Adds to another block's counters instead
+ * took 57 us where one block looking at all tokens took 27, and this 9: eight
+ * requests of 20,000 to 131,071 tokens over 32,000.) */
+#define GPUOS_ADJUSTL_BLOCKS 8u
+#define GPUOS_ADJUSTL_THREADS 512u
+DEV void choose_cluster_sync()
 {
-    constexpr uint32_t CHUNK = THREADS * VECS * 8u;
-    const uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + CHUNK - 1u) / CHUNK);
-    static std::atomic<bool> known[64];
-    if (CHUNK * 4u > 32768u && choose_smem((const void *)gpuos_adjust_kernel<F32, SAME, THREADS, VECS>, CHUNK * 4u, known) != 0) return -1;
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <bool F32, bool SAME>
+__global__ void __launch_bounds__(GPUOS_ADJUSTL_THREADS) gpuos_adjust_long_kernel(const __grid_constant__ gpuos_devdesc d)
+{
+    constexpr uint32_t THREADS = GPUOS_ADJUSTL_THREADS, CHUNK = THREADS * 8u, N = GPUOS_ADJUSTL_BLOCKS;
+    extern __shared__ __align__(16) uint32_t adjust_half[]; /* N CHUNK counters of 16 bits */
+    __shared__ uint32_t has_bias[CHUNK / 32]; /* of this block's chunk */
+    __shared__ int32_t listed[THREADS];
+    kv4_after_previous();
+    const uint32_t V = d.dims[1], b = blockIdx.y, t = threadIdx.x, rank = blockIdx.x % N;
+    const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
+    const uint32_t from = blockIdx.x * CHUNK, lo = max(from, out.lo), hi = min(from + CHUNK, out.hi); /* (a cluster's last may be empty) */
+    const uint32_t shift = in.lo - out.lo, r = SAME ? 0u : shift & (F32 ? 3u : 7u);
+    AdjustArgs a;
+    if (!adjust_args(&d, b, a)) return; /* (all of a row's blocks) */
+    const uint32_t at = from + t * 8u, begin = from - rank * CHUNK; /* (the cluster's first place) */
+    AdjustRaw<F32, SAME> raw;
+    adjust_load(in, at, shift, r, lo, hi, raw);
+    const uint32_t bits = at < hi ? adjust_mask(a, at, out.lo, V) : 0u;
+#pragma unroll
+    for (uint32_t k = 0; k < N; k++) reinterpret_cast<uint4 *>(adjust_half)[k * THREADS + t] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < CHUNK / 32) has_bias[t] = 0u;
+    __syncthreads();
+    if (a.penal) {
+        const uint32_t n = (uint32_t)a.q.length, prompt = (uint32_t)a.q.prompt;
+#pragma unroll 1
+        for (uint32_t i0 = rank * THREADS + t; i0 < n; i0 += 16u * THREADS * N) {
+            int32_t tok[16];
+#pragma unroll
+            for (uint32_t k = 0; k < 16; k++) tok[k] = i0 + k * THREADS * N < n ? a.tokens[i0 + k * THREADS * N] : -1;
+#pragma unroll
+            for (uint32_t k = 0; k < 16; k++) {
+                const uint32_t p = (uint32_t)tok[k] + out.lo - begin;
+                if ((uint32_t)tok[k] >= V || p >= CHUNK * N) continue;
+                if (i0 + k * THREADS * N < prompt) atomicOr(adjust_half + (p >> 1), 0x8000u << 16 * (p & 1u));
+                else atomicAdd(adjust_half + (p >> 1), 1u << 16 * (p & 1u));
+            }
+        }
+    }
+    for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
+        const uint32_t token = (uint32_t)a.bias[i].x, p = token + out.lo - from;
+        if (i < THREADS) listed[i] = (int32_t)token;
+        if (token < V && p < CHUNK) atomicOr(has_bias + (p >> 5), 1u << (p & 31u));
+    }
+    choose_cluster_sync();
+    const uint32_t mine = smem_addr(adjust_half) + (rank * CHUNK + t * 8u) * 2u;
+    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+    for (uint32_t k = 0; k < N; k++) {
+        uint32_t remote;
+        uint4 v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(mine), "r"(k));
+        asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(remote) : "memory");
+        const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (uint32_t j = 0; j < 8; j++) {
+            const uint32_t c = h[j >> 1] >> 16 * (j & 1u);
+            w[j] = (w[j] + (c & 0x7FFFu)) | (c & 0x8000u) << 16;
+        }
+    }
+    /* nobody reads another block's counters from here on: the sums go in their place */
+    choose_cluster_sync();
+    const uint32_t flags = at < hi ? has_bias[t >> 2] >> 8 * (t & 3u) : 0u;
+    uint32_t *const sums = adjust_half;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; j++) sums[t * 8u + j] = w[j];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; j++) w[j] |= flags >> j & 1u ? GPUOS_ADJUST_LISTED : 0u;
+    if (at < hi) adjust_eight(a, out, raw, r, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), bits, at, lo, hi);
+    __syncthreads();
+    adjust_listed<F32, (int)THREADS>(a, in, out, V, shift, lo, hi, listed, [&](uint32_t p) { return sums[p - from]; });
+}
+/* A kernel whose blocks take `chunk` places each, and of a row a multiple of `cluster`. */
+static int adjust_launch(void (*kernel)(const gpuos_devdesc), uint32_t threads, uint32_t chunk, uint32_t smem, uint32_t cluster, uint32_t size,
+                         const gpuos_devdesc &d, void *stream)
+{
+    uint32_t chunks = (uint32_t)(((uint64_t)d.dims[1] + 7u + chunk - 1u) / chunk);
+    chunks = (chunks + cluster - 1u) / cluster * cluster;
     gpuos_devdesc e = d;
     /* (rows beyond the grid's second dimension: launches of their own) */
     for (uint32_t row = 0; row < d.dims[0]; row += 65535u) {
         e.dims[0] = min(d.dims[0] - row, 65535u);
-        const uint64_t size = F32 ? 4u : 2u;
         e.a = d.a + (uint64_t)row * d.dims[2] * size;
         e.out = d.out + (uint64_t)row * d.dims[3] * size;
         e.b = d.b + (uint64_t)row * d.dims[4] * 4u;
         e.aux0 = d.aux0 + (uint64_t)row * sizeof(gpuos_logits_request);
         e.aux2 = d.aux2 + (uint64_t)row * (d.dims[5] >> 16) * sizeof(gpuos_logits_bias);
-        if (choose_launch(gpuos_adjust_kernel<F32, SAME, THREADS, VECS>, dim3(chunks, e.dims[0]), THREADS, CHUNK * 4u, stream, e) != 0) return -1;
+        if (choose_launch(kernel, dim3(chunks, e.dims[0]), threads, smem, stream, e, cluster) != 0) return -1;
     }
     return 0;
 }
 template <bool F32, bool SAME>
 static int adjust_launch_by(const gpuos_devdesc &d, void *stream)
 {
-    if (d.dims[4] > GPUOS_ADJUSTB_LONG) return adjust_launch<F32, SAME, 1024, 2>(d, stream);
-    if ((uint64_t)d.dims[0] * d.dims[1] > GPUOS_ADJUSTB_MANY) return adjust_launch<F32, SAME, 256, 4>(d, stream);
-    return adjust_launch<F32, SAME, 256, 2>(d, stream);
+    constexpr int MANY = F32 ? 3 : 4; /* eights a thread of a large call: what registers hold */
+    constexpr uint32_t T = GPUOS_ADJUSTB_THREADS, TL = GPUOS_ADJUSTL_THREADS, N = GPUOS_ADJUSTL_BLOCKS, size = F32 ? 4u : 2u;
+    /* (a block's share is an eighth and 512 more at most: below 2^15) */
+    if (d.dims[4] > GPUOS_ADJUSTB_LONG && d.dims[4] <= 0x7000u * N && (uint64_t)d.dims[0] * ((d.dims[1] + 7u) / (TL * 8u) + 1u) <= GPUOS_ADJUSTL_FEW) {
+        static std::atomic<bool> known[64];
+        constexpr uint32_t smem = TL * 8u * N * 2u;
+        if (choose_smem((const void *)gpuos_adjust_long_kernel<F32, SAME>, smem, known) != 0) return -1;
+        return adjust_launch(gpuos_adjust_long_kernel<F32, SAME>, TL, TL * 8u, smem, N, size, d, stream);
+    }
+    if ((uint64_t)d.dims[0] * d.dims[1] > GPUOS_ADJUSTB_MANY) return adjust_launch(gpuos_adjust_kernel<F32, SAME, MANY>, T, T * 8u * MANY, 0, 1, size, d, stream);
+    return adjust_launch(gpuos_adjust_kernel<F32, SAME, 2>, T, T * 16u, 0, 1, size, d, stream);
 }
 template <bool F32>
 static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
@@ -2398,10 +2513,10 @@ static int choose_eager_launch(const gpuos_devdesc &d, void *stream)
 static int choose_preload()
 {
     const void *const all[] = {
-        (const void *)gpuos_adjust_kernel<true, true, 256, 2>, (const void *)gpuos_adjust_kernel<true, true, 256, 4>, (const void *)gpuos_adjust_kernel<true, true, 1024, 2>,
-        (const void *)gpuos_adjust_kernel<true, false, 256, 2>, (const void *)gpuos_adjust_kernel<true, false, 256, 4>, (const void *)gpuos_adjust_kernel<true, false, 1024, 2>,
-        (const void *)gpuos_adjust_kernel<false, true, 256, 2>, (const void *)gpuos_adjust_kernel<false, true, 256, 4>, (const void *)gpuos_adjust_kernel<false, true, 1024, 2>,
-        (const void *)gpuos_adjust_kernel<false, false, 256, 2>, (const void *)gpuos_adjust_kernel<false, false, 256, 4>, (const void *)gpuos_adjust_kernel<false, false, 1024, 2>,
+        (const void *)gpuos_adjust_kernel<true, true, 2>, (const void *)gpuos_adjust_kernel<true, true, 3>, (const void *)gpuos_adjust_long_kernel<true, true>,
+        (const void *)gpuos_adjust_kernel<true, false, 2>, (const void *)gpuos_adjust_kernel<true, false, 3>, (const void *)gpuos_adjust_long_kernel<true, false>,
+        (const void *)gpuos_adjust_kernel<false, true, 2>, (const void *)gpuos_adjust_kernel<false, true, 4>, (const void *)gpuos_adjust_long_kernel<false, true>,
+        (const void *)gpuos_adjust_kernel<false, false, 2>, (const void *)gpuos_adjust_kernel<false, false, 4>, (const void *)gpuos_adjust_long_kernel<false, false>,
         (const void *)gpuos_top_kernel<true>, (const void *)gpuos_top_kernel<false>,
         (const void *)gpuos_route_kernel<true, 8, 8, true>, (const void *)gpuos_route_kernel<true, 8, 8, false>,
         (const void *)gpuos_route_kernel<true, 8, 16, true>, (const void *)gpuos_route_kernel<true, 8, 16, false>,
