@@ -585,7 +585,7 @@ GPUOS_API int gpuos_tile_profile_get(gpuos_ctx *ctx, gpuos_tile_profile *out);
  *   logits_top         B * s, s = min(floor(2048 / B), ceil((V + 7) / 1024)) or 1: runs of
  *                      round_up(ceil((V + 7) / s), 256) tokens of one row
  *   expert_route       ceil(N / 8) (eight tokens per tile)
- *   expert_count, _place  1 up to GPUOS_PLAN_ONE pairs, else min(64, ceil(P / 2048)) equal runs of pairs
+ *   expert_count, _place  1 up to GPUOS_PLAN_ONE pairs, else min(96, ceil(P / 2048)) equal runs of pairs
  *   nop / empty op     1
  * Returns GPUOS_EINVAL for a descriptor the library would reject. */
 GPUOS_API int gpuos_op_ntiles(const gpuos_desc *d, uint32_t *ntiles);

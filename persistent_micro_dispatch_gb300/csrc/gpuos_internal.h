@@ -45,7 +45,7 @@
 #define GPUOS_ROUTE_MAX_K 32              /* experts of a token (one for each lane) */
 #define GPUOS_ROUTE_ROWS 8                /* tokens of an expert-route tile */
 #define GPUOS_PLAN_RUN 2048               /* pairs of an expert-count tile at least */
-#define GPUOS_PLAN_TILES 64               /* expert-count tiles at most (each reads the others' counts) */
+#define GPUOS_PLAN_TILES 96               /* expert-count tiles at most (each reads the others' counts) */
 #define GPUOS_PLAN_OFFSET (GPUOS_CHOOSE_COUNTERS + GPUOS_TOP_TILES * GPUOS_TOP_PART) /* the counts' place in the workspace */
 /* How the choosing ops are cut into tiles; the host sets ntiles by these, and
  * the device (whose descriptors may be an alias's, which the host does not
