@@ -582,9 +582,9 @@ GPUOS_API int gpuos_tile_profile_get(gpuos_ctx *ctx, gpuos_tile_profile *out);
  *                      the product is below 2^32, EINVAL otherwise)
  *   page_copy          layers * n * ceil(page bytes / 16384)
  *   logits_adjust      B * ceil((V + 7) / 4096) (4,096 tokens of one row per tile)
- *   logits_top         B * s, s = min(floor(2048 / B), ceil((V + 7) / 1024)) or 1: runs of
+ *   logits_top         B * s, s = min(floor(1536 / B), ceil((V + 7) / 1024)) or 1: runs of
  *                      round_up(ceil((V + 7) / s), 256) tokens of one row
- *   expert_route       ceil(N / 8) (eight tokens per tile)
+ *   expert_route       ceil(N / r), r = ceil(N / 1536) within [1, 8] (r tokens per tile)
  *   expert_count, _place  1 up to GPUOS_PLAN_ONE pairs, else min(96, ceil(P / 2048)) equal runs of pairs
  *   nop / empty op     1
  * Returns GPUOS_EINVAL for a descriptor the library would reject. */

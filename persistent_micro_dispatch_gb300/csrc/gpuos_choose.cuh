@@ -191,15 +191,15 @@ DEV int adjust_tile(const gpuos_devdesc *d, uint32_t tile)
             if (a.penal) {
                 const uint32_t n = (uint32_t)a.q.length;
 #pragma unroll 1
-                for (uint32_t i0 = 0; i0 < n; i0 += 256) {
-                    int32_t t[8];
+                for (uint32_t i0 = 0; i0 < n; i0 += 32 * 24) { /* (a warp alone: what it waits for is the time) */
+                    int32_t t[24];
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; k++) {
+                    for (uint32_t k = 0; k < 24; k++) {
                         const uint32_t i = i0 + k * 32u + lane;
                         t[k] = i < n ? __ldcg(a.tokens + i) : -1;
                     }
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; k++)
+                    for (uint32_t k = 0; k < 24; k++)
                         mark(t[k], true, i0 + k * 32u + lane < (uint32_t)a.q.prompt ? GPUOS_ADJUST_HAD : 0u);
                 }
             }
@@ -519,24 +519,31 @@ DEV int top_tile(const gpuos_devdesc *d, uint32_t tile)
         m = M;
     }
     top_softmax(m, s);
+    constexpr uint32_t LISTS = 8 / KL; /* whose loads are out together */
 #pragma unroll 1
-    for (uint32_t i = 0; i < S; i++) {
-        if (i == part) continue;
-        const unsigned long long *q = reinterpret_cast<const unsigned long long *>(top_part(d, row * S + i) + 16);
-        uint64_t e[KL];
+    for (uint32_t i0 = 0; i0 < S; i0 += LISTS) {
+        uint64_t e[LISTS][KL];
 #pragma unroll
-        for (int k = 0; k < KL; k++) e[k] = lane + 32u * k < K ? __ldcg(q + lane + 32 * k) : 0ull;
+        for (uint32_t i = 0; i < LISTS; i++) {
+            const bool here = i0 + i < S && i0 + i != part;
+            const unsigned long long *q = reinterpret_cast<const unsigned long long *>(top_part(d, row * S + (here ? i0 + i : part)) + 16);
 #pragma unroll
-        for (int k = 0; k < KL; k++) {
-            uint32_t left = __ballot_sync(GPUOS_FULL, e[k] > st.list.last);
-            while (left) {
-                const int src = __ffs((int)left) - 1;
-                left &= left - 1u;
-                const uint64_t c = shfl64(e[k], src);
-                if (c <= st.list.last) break; /* (they come in order) */
-                st.list.insert(c, K);
-            }
+            for (int k = 0; k < KL; k++) e[i][k] = here && lane + 32u * k < K ? __ldcg(q + lane + 32 * k) : 0ull;
         }
+#pragma unroll
+        for (uint32_t i = 0; i < LISTS; i++)
+#pragma unroll
+            for (int k = 0; k < KL; k++) {
+                uint32_t left = __ballot_sync(GPUOS_FULL, e[i][k] > st.list.last);
+#pragma unroll 1
+                while (left) {
+                    const int src = __ffs((int)left) - 1;
+                    left &= left - 1u;
+                    const uint64_t c = shfl64(e[i][k], src);
+                    if (c <= st.list.last) break; /* (they come in order) */
+                    st.list.insert(c, K);
+                }
+            }
     }
     top_write(d, row, st.list, m, s);
     return GPUOS_ST_OK;
@@ -772,16 +779,8 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
     bool sure = !sigmoid || most >= -60.0f || most == -INFINITY;
     if (a.G > 1) {
         uint32_t mine = 0, edge; /* lane g: group g's value */
-#pragma unroll 1
-        for (uint32_t g = 0; g < a.G; g++) {
-            uint32_t one = 0, two = 0;
-#pragma unroll
-            for (int i = 0; i < VPL; i++) {
-                const uint32_t e = lane + 32u * i - g * a.size;
-                const uint32_t k = e < a.size ? key[i] : 0u;
-                two = max(two, min(one, k));
-                one = max(one, k);
-            }
+        uint32_t one = 0, two = 0, g = 0;
+        auto close = [&]() { /* the group's value from the lanes' two best of it */
             uint32_t best = route_max(one);
             if (top2) {
                 const uint32_t owner = (uint32_t)__ffs((int)__ballot_sync(GPUOS_FULL, one == best)) - 1u;
@@ -790,6 +789,28 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
                 best = choose_key(v1 + v2);
             }
             if (lane == g) mine = best;
+            one = two = 0, g++;
+        };
+        if (a.size % 32u == 0) { /* a group is whole rounds of the lanes */
+            uint32_t left = a.size / 32u;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                if (32u * i >= a.E) break;
+                two = max(two, min(one, key[i]));
+                one = max(one, key[i]);
+                if (--left == 0) close(), left = a.size / 32u;
+            }
+        } else {
+#pragma unroll 1
+            while (g < a.G) {
+#pragma unroll
+                for (int i = 0; i < VPL; i++) {
+                    const uint32_t k = lane + 32u * i - g * a.size < a.size ? key[i] : 0u;
+                    two = max(two, min(one, k));
+                    one = max(one, k);
+                }
+                close();
+            }
         }
         const uint32_t kept = route_groups(a, mine, edge);
         if (a.keep < a.G && (a.bias || top2) && choose_unkey(edge) - choose_unkey(route_max(mine)) <= 2.0f * unsure) sure = false;
@@ -853,11 +874,12 @@ DEV int route_op(const gpuos_devdesc *d, uint32_t tile)
     const uint32_t *m = d->dims;
     if (m[0] == 0) return GPUOS_ST_OK;
     if (!gpuos_route_ok(d->dtype, d->a, d->b, d->out, d->aux0, d->aux1, m) ||
-        (m[0] - 1u) / GPUOS_ROUTE_ROWS + 1u != d->ntiles)
+        (m[0] - 1u) / gpuos_route_rows(m[0]) + 1u != d->ntiles)
         return GPUOS_ST_BAD_ARGS;
     if (tile >= d->ntiles) return GPUOS_ST_OK;
-    if (m[1] <= 256) route_tile<8>(d, tile * GPUOS_ROUTE_ROWS, GPUOS_ROUTE_ROWS);
-    else route_tile<32>(d, tile * GPUOS_ROUTE_ROWS, GPUOS_ROUTE_ROWS);
+    const uint32_t rows = gpuos_route_rows(m[0]);
+    if (m[1] <= 256) route_tile<8>(d, tile * rows, rows);
+    else route_tile<32>(d, tile * rows, rows);
     return GPUOS_ST_OK;
 }
 
@@ -984,10 +1006,17 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
     if (tile == 0 && lane == 0) __stcg(offsets + p.E, begin);
     __threadfence_block();
     __syncwarp();
+    int32_t ahead[8] = {-1, -1, -1, -1, -1, -1, -1, -1};
 #pragma unroll 1
     for (uint32_t i0 = p.lo; i0 < p.hi; i0 += 32) {
-        const uint32_t i = i0 + lane;
-        const int32_t id = i < p.hi ? __ldcg(p.ids + i) : -1;
+        const uint32_t i = i0 + lane, step = (i0 - p.lo) / 32u % 8u;
+        if (step == 0) { /* eight steps' ids at a time */
+#pragma unroll
+            for (uint32_t k = 0; k < 8; k++) ahead[k] = i + 32u * k < p.hi ? __ldcg(p.ids + i + 32u * k) : -1;
+        }
+        const int32_t id = ahead[0];
+#pragma unroll
+        for (uint32_t k = 0; k < 7; k++) ahead[k] = ahead[k + 1];
         const bool here = (uint32_t)id < p.E;
         const uint32_t peers = __match_any_sync(GPUOS_FULL, here ? id : -1);
         const uint32_t lead = (uint32_t)__ffs((int)peers) - 1u;

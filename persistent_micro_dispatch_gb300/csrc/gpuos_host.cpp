@@ -534,7 +534,7 @@ static int validate_and_tile(const gpuos_desc *d, uint32_t *ntiles_out, bool use
     case GPUOS_OP_EXPERT_ROUTE:
         if (m[0]) {
             if (!gpuos_route_ok(d->dtype, d->a, d->b, d->out, d->aux0, d->aux1, m)) return GPUOS_EINVAL;
-            nt = ceil_div(m[0], GPUOS_ROUTE_ROWS);
+            nt = ceil_div(m[0], gpuos_route_rows(m[0]));
         }
         break;
     case GPUOS_OP_EXPERT_COUNT:

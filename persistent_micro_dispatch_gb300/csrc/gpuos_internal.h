@@ -38,12 +38,14 @@
 #define GPUOS_ADJUST_CHUNK 4096           /* tokens of a logits-adjust tile (16 KB of counters) */
 #define GPUOS_ADJUST_MAX_L (1u << 28)     /* tokens of a request's history (a counter has 29 bits) */
 #define GPUOS_TOP_MAX_K 64                /* best tokens of a row at most (two for each lane) */
-#define GPUOS_TOP_TILES 2048              /* tiles of a split logits-top at most: counters and partial states */
+#define GPUOS_TOP_TILES 2048              /* partial states of a logits-top, and counters */
+#define GPUOS_TOP_SPLIT 1536              /* tiles of a split logits-top at most (one wave of the default executor) */
 #define GPUOS_TOP_RUN 1024                /* tokens of a logits-top tile at least */
 #define GPUOS_TOP_PART (16u + 8u * GPUOS_TOP_MAX_K) /* bytes of a tile's partial state: {max, sum}, K entries */
 #define GPUOS_ROUTE_MAX_E 1024            /* experts */
 #define GPUOS_ROUTE_MAX_K 32              /* experts of a token (one for each lane) */
-#define GPUOS_ROUTE_ROWS 8                /* tokens of an expert-route tile */
+#define GPUOS_ROUTE_ROWS 8                /* tokens of an expert-route tile at most */
+#define GPUOS_ROUTE_TILES 1536            /* ... of which there are more than one in each beyond so many tiles */
 #define GPUOS_PLAN_RUN 2048               /* pairs of an expert-count tile at least */
 #define GPUOS_PLAN_TILES 96               /* expert-count tiles at most (each reads the others' counts) */
 #define GPUOS_PLAN_OFFSET (GPUOS_CHOOSE_COUNTERS + GPUOS_TOP_TILES * GPUOS_TOP_PART) /* the counts' place in the workspace */
@@ -62,8 +64,13 @@ static inline GPUOS_HD uint32_t gpuos_adjust_chunks(uint32_t V)
 static inline GPUOS_HD uint32_t gpuos_top_split(uint32_t B, uint32_t V)
 {
     const uint32_t most = (uint32_t)(((uint64_t)V + 7u + GPUOS_TOP_RUN - 1u) / GPUOS_TOP_RUN);
-    const uint32_t want = B ? GPUOS_TOP_TILES / B : 1u;
+    const uint32_t want = B ? GPUOS_TOP_SPLIT / B : 1u;
     return want < 1u ? 1u : (want < most ? want : most);
+}
+static inline GPUOS_HD uint32_t gpuos_route_rows(uint32_t N)
+{
+    const uint32_t r = N / GPUOS_ROUTE_TILES + (N % GPUOS_ROUTE_TILES != 0);
+    return r < 1u ? 1u : (r < GPUOS_ROUTE_ROWS ? r : GPUOS_ROUTE_ROWS);
 }
 static inline GPUOS_HD uint32_t gpuos_plan_tiles(uint32_t P)
 {

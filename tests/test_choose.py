@@ -41,15 +41,17 @@ def test_tiles(G):
     assert n("logits_adjust", (2, 4090, 4090, 4090, 0, 0)) == 4
     assert n("logits_adjust", (3, 128000, 128000, 128000, 0, 0), dtype=0) == 3 * 32
     assert n("logits_adjust", (0, 5, 5, 5)) == n("logits_adjust", (5, 0, 0, 0)) == 1
-    # 1,024 tokens a tile, and 2,048 tiles at most while rows are cut
+    # 1,024 tokens a tile, and 1,536 tiles at most while rows are cut
     assert n("logits_top", (1, 1000, 1000, 1)) == 1
     assert n("logits_top", (1, 1018, 1018, 1)) == 2
-    assert n("logits_top", (64, 128000, 128000, 20)) == 64 * 32
-    assert n("logits_top", (65, 128000, 128000, 20)) == 65 * 31
-    assert n("logits_top", (1025, 128000, 128000, 20)) == 1025
+    assert n("logits_top", (1, 128000, 128000, 20)) == 126
+    assert n("logits_top", (64, 128000, 128000, 20)) == 64 * 24
+    assert n("logits_top", (65, 128000, 128000, 20)) == 65 * 23
+    assert n("logits_top", (769, 128000, 128000, 20)) == 769
     assert n("logits_top", (5000, 128000, 128000, 20)) == 5000
     assert n("logits_top", (0, 0, 0, 0)) == 1
-    assert n("expert_route", (17, 64, 64, 8, 1 | 1 << 16, 0)) == 3
+    route = lambda N: n("expert_route", (N, 64, 64, 8, 1 | 1 << 16, 0))  # noqa: E731
+    assert [route(N) for N in (1, 17, 1536, 1537, 4608, 12288, 12289, 32768)] == [1, 17, 1536, 769, 1536, 1536, 1537, 4096]
     assert n("expert_route", (0, 0, 0, 0)) == 1
     for op in ("expert_count", "expert_place"):
         assert n(op, (4096, 64)) == 1 and n(op, (4097, 64)) == 3 and n(op, (1 << 20, 64)) == 96 and n(op, (0, 64)) == 1
