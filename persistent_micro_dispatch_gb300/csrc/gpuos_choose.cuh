@@ -1023,7 +1023,7 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
         uint32_t at = 0;
         if (here && lane == lead) at = plan_add(ctr + id, (uint32_t)__popc(peers), shared);
         at = __shfl_sync(GPUOS_FULL, at, (int)lead) + (uint32_t)__popc(peers & ((1u << lane) - 1u));
-        if (here) __stcg(order + at, (int32_t)i);
+        if (here && at < p.P) __stcg(order + at, (int32_t)i); /* (counts that are not of these pairs: nothing outside is written) */
         if (i < p.hi) __stcg(place + i, here ? (int32_t)at : -1);
         if (i < p.hi && i >= begin) __stcg(order + i, -1); /* (places behind the last pair) */
         __syncwarp();
@@ -2099,7 +2099,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
     kv4_after_previous();
     RouteArgs a;
     route_args(&d, a);
-    const uint32_t rows = a.rows ? (uint32_t)max(__ldg(a.rows), 0) : a.N;
+    const uint32_t rows = a.rows ? (uint32_t)max(*a.rows, 0) : a.N;
     const uint32_t P = VEC ? (uint32_t)VPL : (a.E + L - 1u) / L, first = sub * P; /* this lane's experts */
     const bool sigmoid = a.flags & GPUOS_ROUTE_SIGMOID, summed = a.G > 1 && a.flags & GPUOS_ROUTE_TOP2, biased = a.bias != nullptr;
     const bool norm = a.flags & GPUOS_ROUTE_NORM;
@@ -2110,7 +2110,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
     float wide = 0.0f;
     if (biased) {
         for (uint32_t i = threadIdx.x; i < L * P; i += GPUOS_ROUTEB_THREADS) {
-            const float b = i < a.E ? fmaxf(__ldg(a.bias + i), -INFINITY) : 0.0f;
+            const float b = i < a.E ? fmaxf(a.bias[i], -INFINITY) : 0.0f;
             biases[i / P][i % P] = flat[i] = b;
         }
         __syncthreads();
@@ -2127,7 +2127,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < VPL; i += F32 ? 4 : 8) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row) + i / (F32 ? 4 : 8));
+                const uint4 v = reinterpret_cast<const uint4 *>(row)[i / (F32 ? 4 : 8)];
                 if (F32) {
                     c[i] = __uint_as_float(v.x), c[i + 1] = __uint_as_float(v.y), c[i + 2] = __uint_as_float(v.z), c[i + 3] = __uint_as_float(v.w);
                 } else {
@@ -2142,7 +2142,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
             for (int i = 0; i < VPL; i++) {
                 c[i] = -INFINITY;
                 if (i < (int)P && first + i < a.E)
-                    c[i] = F32 ? __ldg(reinterpret_cast<const float *>(row) + i) : bf1(__ldg(reinterpret_cast<const uint16_t *>(row) + i));
+                    c[i] = F32 ? reinterpret_cast<const float *>(row)[i] : bf1(reinterpret_cast<const uint16_t *>(row)[i]);
             }
         }
         float most = -INFINITY;
@@ -2218,7 +2218,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
                     for (uint32_t i = 0; i < P; i++) {
                         if (first + i >= a.E) break;
                         const uint64_t at = (uint64_t)n * a.ld + first + i;
-                        const float x = fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + at) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + at)), -INFINITY);
+                        const float x = fmaxf(F32 ? reinterpret_cast<const float *>(d.a)[at] : bf1(reinterpret_cast<const uint16_t *>(d.a)[at]), -INFINITY);
                         const float b = biases[sub][i];
                         if (!(route_sigmoid_fast(x) + b >= from)) continue;
                         float2 v = make_float2(b, 0.0f);
@@ -2283,7 +2283,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         for (uint32_t i = sub; i < have; i += L) {
             const uint32_t id = s.id[i];
             const uint64_t k = (uint64_t)n * a.ld + id;
-            const float x = fmaxf(F32 ? __ldg(reinterpret_cast<const float *>(d.a) + k) : bf1(__ldg(reinterpret_cast<const uint16_t *>(d.a) + k)), -INFINITY);
+            const float x = fmaxf(F32 ? reinterpret_cast<const float *>(d.a)[k] : bf1(reinterpret_cast<const uint16_t *>(d.a)[k]), -INFINITY);
             float v = x;
             if (biased) v = (sigmoid ? route_sigmoid_fast(x) : route_score(false, x, most, inv)) + flat[id];
             s.got[i] = top_entry(v, id);
@@ -2404,7 +2404,7 @@ __global__ void __launch_bounds__(GPUOS_PLANB_THREADS) gpuos_plan_count_kernel(c
     for (uint32_t i = p.lo + t; i < p.hi; i += GPUOS_PLANB_PAIRS) {
         int32_t id[GPUOS_PLANB_STEPS];
 #pragma unroll
-        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) id[k] = i + k * GPUOS_PLANB_THREADS < p.hi ? __ldg(p.ids + i + k * GPUOS_PLANB_THREADS) : -1;
+        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) id[k] = i + k * GPUOS_PLANB_THREADS < p.hi ? p.ids[i + k * GPUOS_PLANB_THREADS] : -1;
 #pragma unroll
         for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++)
             if ((uint32_t)id[k] < p.E) atomicAdd(count + id[k], 1u);
@@ -2477,7 +2477,7 @@ __global__ void __launch_bounds__(GPUOS_PLANB_THREADS) gpuos_plan_place_kernel(c
         const uint32_t turn = min(p.hi - i0, GPUOS_PLANB_PAIRS), steps = (turn + GPUOS_PLANB_THREADS - 1u) / GPUOS_PLANB_THREADS;
         const uint32_t i = i0 + w * steps * 32u + lane;
 #pragma unroll
-        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) id[k] = k < steps && i + 32u * k < p.hi ? __ldg(p.ids + i + 32u * k) : -1;
+        for (uint32_t k = 0; k < GPUOS_PLANB_STEPS; k++) id[k] = k < steps && i + 32u * k < p.hi ? p.ids[i + 32u * k] : -1;
         for (uint32_t k = t; k < GPUOS_PLANB_WARPS * p.E / 2u; k += GPUOS_PLANB_THREADS) reinterpret_cast<uint32_t *>(plan_before)[k] = 0u;
         __syncthreads();
 #pragma unroll
@@ -2518,7 +2518,7 @@ __global__ void __launch_bounds__(GPUOS_PLANB_THREADS) gpuos_plan_place_kernel(c
             const bool here = (uint32_t)id[k] < p.E;
             const uint32_t to = here ? base[id[k]] + mine[id[k]] + rank[k] : 0u;
             place[at] = here ? (int32_t)to : -1;
-            if (here) order[to] = (int32_t)at;
+            if (here && to < p.P) order[to] = (int32_t)at; /* (counts that are not of these pairs: nothing outside is written) */
             if (at >= total) order[at] = -1; /* (behind the last pair) */
         }
         __syncthreads();

@@ -307,6 +307,37 @@ def test_reset_after_an_abandoned_call(run):
         assert (ids.cpu().numpy() == R.top(x, 20)[0]).all()
 
 
+@pytest.mark.parametrize("run", ["eager", "executor"])
+def test_a_placement_without_its_count(run):
+    """Counts that are not of these pairs give a wrong order, and nothing outside it."""
+    import torch
+    from persistent_micro_dispatch_gb300 import choose
+    rng = np.random.default_rng(3)
+    ids = _dev(rng.integers(0, 16, 9000).astype(np.int32))
+    for fill in (0, 1000, 2 ** 31 - 1, -1):
+        ws = choose.new_workspace()
+        ws.view(torch.int32)[choose.COUNTER_BYTES // 4:] = fill
+        guard = torch.full((9000 + 20000,), -9, dtype=torch.int32, device="cuda")
+        place, offsets = torch.zeros_like(ids), torch.zeros(17, dtype=torch.int32, device="cuda")
+        d = choose.plan(ids, guard[10000:19000], place, offsets, ws)[1:].copy()
+        d["flags"], d["dep"] = 0, 0
+        RUNNERS[run](d)
+        assert (guard[:10000] == -9).all() and (guard[19000:] == -9).all()
+
+
+def test_adjust_of_more_rows_than_a_grid_holds():
+    import torch
+    from persistent_micro_dispatch_gb300 import choose
+    B, V = 65537 + 60, 40
+    x, s, tokens, bias, mask = _adjust_case(1, B, V, 6, 2, 3, True)
+    t, kw = _adjust_args(s, tokens, bias, mask)
+    logits, out = _dev(x), torch.zeros(B, V, device="cuda")
+    RUNNERS["eager"](choose.adjust(logits, out, t, **kw))
+    at = np.r_[0:40, 65500:B]
+    want, tol = R.adjust(x[at], s[at], tokens[at], bias[at], mask, True)
+    _close(_f64(out)[at], want, tol)
+
+
 def test_aliased_ops_check_their_sizes():
     """An alias is a user op: the host passes its sizes and tile count on, and
     the op itself refuses what it cannot do."""
