@@ -227,6 +227,10 @@ typedef struct gpuos_logits_bias {
 #define GPUOS_ROUTE_TOP2 2u    /* a group counts by the sum of its two best (else by its best) */
 #define GPUOS_ROUTE_NORM 4u    /* weights are divided by their sum */
 
+/* (Through an alias these ops go by the same rule of tiles: ntiles has to be what
+ * gpuos_op_ntiles gives for the op itself, anything else is
+ * GPUOS_ST_BAD_ARGS.) */
+
 /* Workspace of LOGITS_TOP and of the experts' plan, whatever the sizes: 16-byte
  * aligned, its first GPUOS_CHOOSE_COUNTERS bytes zero before the first use; a
  * descriptor that runs to its end leaves them zero (after GPUOS_ST_DEP_TIMEOUT or
@@ -614,7 +618,9 @@ GPUOS_API size_t gpuos_kv4_pool_bytes(uint32_t npages, uint32_t Hkv, uint32_t D)
  * launch kernels of their own (attention: at most one block per SM; the others:
  * four of the rule's tiles a block), do not use stage_bytes, and may be given their
  * SMs as the stream's previous kernel ends: they wait on the device until its writes
- * are visible. A launch has no status: where the executor would report one, entries
+ * are visible. So do the ops of a decode step's choices (logits_adjust to
+ * expert_place), whose kernels go by sizes, not by the rule's tiles. A launch has no
+ * status: where the executor would report one, entries
  * are skipped alike, and attention whose copy of a page does not land in time gives
  * NaN. Deps are implied by stream order. Does not synchronize. Errors: EINVAL (as gpuos_submit),
  * ECUDA. */

@@ -2,6 +2,15 @@
  * What a decode step chooses (included by gpuos_device.cu, whose memory, bf16
  * and staging helpers it uses): logits adjusted for the next token, the best
  * tokens of a row, the experts of a token, and the experts' order.
+ *
+ * Each op has a body for one warp (a tile of the executor), first, and kernels
+ * of its own for launches, behind them. Everything is bound by memory or by
+ * latency; there are no products of matrices. The bodies need no shared memory,
+ * and use the warp's staging buffer for counters where there is one.
+ *
+ * Times are of one GB300 (measured copy bandwidth 6.8 TB/s), device time of
+ * launches one after another in a CUDA graph, unless they say executor (there:
+ * first tile to done).
  */
 #ifndef GPUOS_CHOOSE_CUH
 #define GPUOS_CHOOSE_CUH
@@ -68,7 +77,9 @@ DEV float choose_unkey(uint32_t k) { return __uint_as_float(k ^ ((uint32_t)((int
  * is bound by memory; what a token's penalty needs, its count among the
  * request's tokens, comes from counters of the tile's window of the
  * vocabulary in shared memory, filled by one look at the request's tokens.
- * A counter holds the count after the prompt and two flags.
+ * A counter holds the count after the prompt and two flags. Executor: one
+ * request over 128,000 tokens 21 us, 256 of them (f32) 131; a request's 100,000
+ * tokens are one warp's work in each tile, 200 us.
  * ------------------------------------------------------------------------- */
 #define GPUOS_ADJUST_HAD 0x80000000u    /* in the prompt */
 #define GPUOS_ADJUST_LISTED 0x40000000u /* has a bias: written after the others */
@@ -285,7 +296,8 @@ DEV int adjust_op(const gpuos_devdesc *d, uint32_t tile)
  * The best tokens of a row, with the row's log-sum-exp. One pass over the row:
  * a warp holds the K best so far in its lanes, in order, and the softmax's
  * running maximum and sum; a group of eight elements whose largest is not above
- * the K-th best costs one comparison.
+ * the K-th best costs one comparison. Executor: one row of 32,000, K = 1, 9.7 us;
+ * 64 of 128,000 in bf16, K = 20, 86; 509 of 128,000 in f32, K = 5, 176.
  *
  * An entry is one 64-bit number: the value's place among the floats, then the
  * token's from above, so that one comparison orders by value, then by token.
@@ -1035,9 +1047,23 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
 
 #ifndef GPUOS_EXECUTOR_ONLY
 #define GPUOS_ADJUSTB_THREADS 256u
-#define GPUOS_ADJUSTB_LONG 12288u
-#define GPUOS_ADJUSTL_FEW 304u
-#define GPUOS_ADJUSTB_MANY (4u << 20)
+/* From which length of history on (the tokens' row, which the host knows) eight
+ * blocks share it: direct and shared, us, bf16:
+ *   tokens       8,000        12,000       16,000       24,000        48,000
+ *   8 x 32,000   5.0   6.3    6.4   6.4    7.7   6.4    10.5   6.6    18.4   6.7
+ *   1 x 128,000  5.0   6.3    6.4   6.4    7.7   6.4    10.4   6.4    18.3   6.7
+ *   8 x 128,000  6.2  12.0    7.6  12.1    9.0  12.1    11.9  12.3    20.0  12.6
+ * (64, 32 and 256 blocks that share; 2,048 of them, 64 x 128,000 with 16,000
+ * tokens, take 69 us against 18). */
+#define GPUOS_ADJUSTL_LONG 12288u   /* as long as each block has an SM ... */
+#define GPUOS_ADJUSTL_LONGER 24576u /* ... or half of one */
+#define GPUOS_ADJUSTL_FEW 152u
+/* Elements from which on a thread takes three eights (f32) or four (bf16)
+ * instead of two: two and more, us, rows of 128,000:
+ *   rows   4            16           32           64             128
+ *   f32    4.9   5.0    6.0   6.3    9.1   8.9    17.6   17.7    28.8   28.3   (256: 57, 53)
+ *   bf16   4.7   5.6    6.0   6.1    7.6   7.0    13.5   13.3    23.5   22.2 */
+#define GPUOS_ADJUSTB_MANY 4000000u
 /* As kv4_launch, with a grid of two dimensions and clusters. */
 static int choose_launch(void (*kernel)(const gpuos_devdesc), dim3 blocks, uint32_t threads, uint32_t smem, void *stream, const gpuos_devdesc &d,
                          uint32_t cluster = 1)
@@ -1070,9 +1096,17 @@ static int choose_smem(const void *kernel, uint32_t bytes, std::atomic<bool> (&k
     return 0;
 }
 /* ---------------------------------------------------------------------------
- * Logits adjusted, launched: a block takes 16 places for each of its threads
- * of one row. A thread's logits and mask words are on their way while the
- * block counts the request's tokens.
+ * Logits adjusted, launched: a block takes 16 places of one row for each of its
+ * threads, or more in large calls (below). A thread's logits, the first tokens
+ * and the record are on their way at once, so that a block waits for memory
+ * about twice: for those, and for the mask's words.
+ *
+ * 256 rows of 128,000 in f32 (up to 4,000 tokens, 16 biases, masks for three in
+ * four) 53 us, 5.0 TB/s; without tokens, biases and masks 42.5, 6.2 TB/s; 512
+ * rows in bf16 63 us, 4.2 TB/s: beside memory it is then bound by instructions
+ * (23 for an element, issue slots 60 % used) and by blocks that wait for their
+ * slowest warp's tokens. One row of 128,000 3.2 us, 33 rows of 50,001 whose
+ * input lies otherwise than the output 5.1: latency.
  * ------------------------------------------------------------------------- */
 template <bool F32, bool SAME>
 struct AdjustRaw {
@@ -1279,9 +1313,9 @@ __global__ void __launch_bounds__(GPUOS_ADJUSTB_THREADS, (VECS == 2 ? 1280 : 102
 /* Long histories: eight blocks of neighbouring chunks, a cluster, share them.
  * Each counts an eighth of the tokens, for all eight chunks, in 16 bits (15 and
  * the prompt's flag); a thread then adds up its places' eight counters out of
- * the eight blocks' shared memory. (Adds to another block's counters instead
- * took 57 us where one block looking at all tokens took 27, and this 9: eight
- * requests of 20,000 to 131,071 tokens over 32,000.) */
+ * the eight blocks' shared memory. Eight requests of 20,000 to 131,071 tokens
+ * over 32,000: 8.1 us; blocks of 1,024 threads that each look at all tokens
+ * 15 to 18; adds to the other blocks' counters from afar, instead of sums, 57. */
 #define GPUOS_ADJUSTL_BLOCKS 8u
 #define GPUOS_ADJUSTL_THREADS 512u
 DEV void choose_cluster_sync()
@@ -1383,8 +1417,9 @@ static int adjust_launch_by(const gpuos_devdesc &d, void *stream)
 {
     constexpr int MANY = F32 ? 3 : 4; /* eights a thread of a large call: what registers hold */
     constexpr uint32_t T = GPUOS_ADJUSTB_THREADS, TL = GPUOS_ADJUSTL_THREADS, N = GPUOS_ADJUSTL_BLOCKS, size = F32 ? 4u : 2u;
-    /* (a block's share is an eighth and 512 more at most: below 2^15) */
-    if (d.dims[4] > GPUOS_ADJUSTB_LONG && d.dims[4] <= 0x7000u * N && (uint64_t)d.dims[0] * ((d.dims[1] + 7u) / (TL * 8u) + 1u) <= GPUOS_ADJUSTL_FEW) {
+    const uint64_t sharing = (uint64_t)d.dims[0] * ((d.dims[1] + 7u) / (TL * 8u) + 1u); /* blocks */
+    const bool longer = sharing <= GPUOS_ADJUSTL_FEW ? d.dims[4] > GPUOS_ADJUSTL_LONG : sharing <= 2u * GPUOS_ADJUSTL_FEW && d.dims[4] > GPUOS_ADJUSTL_LONGER;
+    if (longer && d.dims[4] <= 0x7000u * N) { /* (a block's share is an eighth and 512 more at most: below 2^15) */
         static std::atomic<bool> known[64];
         constexpr uint32_t smem = TL * 8u * N * 2u;
         if (choose_smem((const void *)gpuos_adjust_long_kernel<F32, SAME>, smem, known) != 0) return -1;
@@ -1411,6 +1446,15 @@ static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
  * Warps wait for copies, not for each other, between units. The softmax's sum
  * is kept in base 2 under a maximum of the thread's own: one multiply-add, one
  * exponential and one sum an element.
+ *
+ * Bound by memory while units stream (a block's 16 KB in 2,050 cycles with three
+ * blocks an SM, 7 TB/s); a piece's start and end take it about 5 us (first copy
+ * 1, bar 1, ranks 0.5, sums 0.5, a part's way to the row's last block 1 to 2,
+ * joining 2), which the SM's other two blocks cover only in part. 456 rows of
+ * 128,000 in f32, K = 5: 43.5 us, 5.4 TB/s (K = 1: 41); 509 rows, whose runs
+ * cross rows, 55.5, 4.7 TB/s (three equal runs for each row, 4 waves: 62); 64
+ * rows in bf16, K = 20: 16; one row of 32,000, K = 1: 6.1. Loads to registers
+ * instead of the ring took the same time while they were the only change.
  * ------------------------------------------------------------------------- */
 #define GPUOS_TOPB_THREADS 256
 #define GPUOS_TOPB_WARPS (GPUOS_TOPB_THREADS / 32)
@@ -1942,6 +1986,14 @@ static int top_launch(const gpuos_devdesc &d, void *stream)
  * may be among the K best are the values that reach a bar which K + 1 of the
  * lanes' best three reach; they are gathered, and ranked by comparing
  * all with all. Values are floats to the end; NaN is what may not be chosen.
+ *
+ * 32,768 tokens of 256 experts (f32, sigmoid, bias, four of eight groups by their
+ * two best, K = 8): 32 us against 5.3 of memory: 1,100 warp instructions for two
+ * tokens, issue slots 65 % used, the half-rate pipe of minima, maxima and
+ * comparisons 53 %. Without bias and groups 18 us. 65,536 of 64 experts 16.1 us.
+ * Where values are near, 1 token in 1,000 here, sums of two floats tell them
+ * apart (with 64-bit arithmetic instead the launch took 45 us, its last tokens
+ * 15 of them). A kernel for each kind of score and bias would save 6 % of it.
  * ------------------------------------------------------------------------- */
 #define GPUOS_ROUTEB_THREADS 128
 #define GPUOS_ROUTEB_ROOM 64u /* gathered values of a token at most; more: the token goes the sure way */
@@ -2046,7 +2098,7 @@ DEV float2 route_sigmoid_fine(float x)
  * other way round. */
 DEV float pair_unsure(float wide) { return (1.0f + wide) * 0x1p-39f; }
 DEV float pair_less(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); } /* a - b, to a part in 2^24 */
-struct RouteKind {
+struct RouteGathered {
     const float *bias; /* (in shared memory, none NaN) */
     uint32_t have, lanes;
     float wide;
@@ -2055,7 +2107,7 @@ struct RouteKind {
  * them are gathered, and are ranked again by finer values (sigmoid scores and
  * biases). Every lane of the token; false if that does not tell either. Only
  * values of equal logits and biases may be equal. */
-__device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, const RouteKind q)
+__device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, const RouteGathered q)
 {
 #pragma unroll 1
     for (uint32_t i = sub; i < q.have; i += L) {
@@ -2094,7 +2146,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
     constexpr uint32_t TOKENS = 32 / L; /* of a warp */
     const float none = __int_as_float(0x7FFFFFFF);
     const uint32_t lane = lane_id(), sub = lane & (L - 1), own = lane & ~(uint32_t)(L - 1), warp = threadIdx.x >> 5;
-    const uint32_t lanes = (L == 32 ? GPUOS_FULL : (1u << L) - 1u) << own;
+    const uint32_t lanes = ((1u << L) - 1u) << own;
     RouteToken &s = tokens[threadIdx.x / L];
     kv4_after_previous();
     RouteArgs a;
@@ -2312,7 +2364,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
             if (who & lanes) {
                 if (sigmoid) {
                     __syncwarp(lanes); /* (best has been read) */
-                    if (!op_y_fine(&s, sub, L, RouteKind{flat, have, lanes, wide})) sure = false;
+                    if (!op_y_fine(&s, sub, L, RouteGathered{flat, have, lanes, wide})) sure = false;
                 } else {
                     sure = false;
                 }
@@ -2333,7 +2385,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
             a.weights[(uint64_t)n * a.K + sub] = pad ? 0.0f : w * a.scale;
         }
 #pragma unroll 1
-        for (uint32_t k = 0; again && k < TOKENS; k++, again = L == 32 ? 0u : again >> L)
+        for (uint32_t k = 0; again && k < TOKENS; k++, again >>= L)
             if (again & ((1u << L) - 1u) && n0 + k < a.N) op_y_sure<L * VPL <= 256 ? 8 : 32>(&d, n0 + k);
         __syncwarp();
     }
@@ -2366,6 +2418,12 @@ static int route_launch_of(const gpuos_devdesc &d, void *stream)
     auto fits = [&](uint32_t L) {
         return (G == 1u || (L % G == 0 && E % L == 0)) && (K + 1u <= 3u * keep * (L / G) || keep * (E / G) <= GPUOS_ROUTEB_ROOM);
     };
+    /* eight lanes and sixteen, us, no bias, one group:
+     *   tokens      64           4,096        65,536
+     *   E = 32      3.2   3.4    3.9   4.5    14.9   34.0
+     *   E = 64      3.5   3.6    4.5   5.1    16.1   34.9
+     *   E = 128     4.1   4.1    5.7   5.6    21.6   39.0
+     *   E = 256 (32,768 tokens)               19.1   18.1, with bias and groups 43 and 32 */
     if (K <= 8u && E <= 128u && fits(8)) {
         if (E <= 64u) return route_launch<F32, 8, 8>(d, stream);
         return route_launch<F32, 8, 16>(d, stream);
@@ -2383,7 +2441,9 @@ static int route_launch_of(const gpuos_devdesc &d, void *stream)
  * The experts' order, launched: a block takes a run, 4,096 pairs at a time, a
  * warp up to 128 of them. Within a warp's 32 pairs, equal ids find each other
  * by votes on their bits; over its steps, over the warps and over the runs,
- * counts say what comes before.
+ * counts say what comes before. Latency: 512 pairs of 256 experts 3.4 us, one
+ * launch; 262,144 pairs 9.4, two launches of 96 blocks (64 runs: 9.5 where these
+ * took 8.8), of which the second reads the counts of all runs (96 KB a block).
  * ------------------------------------------------------------------------- */
 #define GPUOS_PLANB_THREADS 1024u
 #define GPUOS_PLANB_WARPS 32u
