@@ -42,6 +42,7 @@ from .kv4 import _DESC
 
 WORKSPACE_BYTES = 2 << 20
 COUNTER_BYTES = 8192  # of the workspace: zero before each use
+MAX_BIASES = 1024
 MAX_TOP = 64
 MAX_EXPERTS = 1024
 MAX_EXPERTS_PER_TOKEN = 32
@@ -138,8 +139,8 @@ def adjust(logits: torch.Tensor, out: torch.Tensor, settings: torch.Tensor, toke
     """Logits [B, V] under each request's settings into out [B, V] (of the same
     type; it may be the logits themselves, but not overlap them otherwise):
     penalties for the tokens int32 [B, L] that it has had (its first ``length``
-    of them), biases for listed tokens (int32 [B, n, 2]: a token, and the bits
-    of a float32; its first ``biases``), the temperature, and -infinity for the
+    of them), biases for listed tokens (int32 [B, n <= 1024, 2]: a token, and the
+    bits of a float32; its first ``biases``), the temperature, and -infinity for the
     tokens whose bit in its row of the mask (int32 [M, ceil(V / 32)], token v at
     bit v % 32 of word v // 32) is 0."""
     dt, B, V, ld, a = _rows("logits", logits)
@@ -161,7 +162,7 @@ def adjust(logits: torch.Tensor, out: torch.Tensor, settings: torch.Tensor, toke
     if bias is not None:
         bs, bp = bias.shape, bias.data_ptr()
         n = bs[1] if len(bs) == 3 else 0
-        ok = (ok and len(bs) == 3 and bs[0] == B and bs[2] == 2 and n < 1 << 16 and bias.dtype is _I32 and bias.get_device() == dev
+        ok = (ok and len(bs) == 3 and bs[0] == B and bs[2] == 2 and n <= MAX_BIASES and bias.dtype is _I32 and bias.get_device() == dev
               and bias.is_contiguous() and not bp & 7)
     if not ok or (a == o and ld != ldo):
         if dt2 != dt or (B2, V2) != (B, V) or out.get_device() != dev:
@@ -170,7 +171,7 @@ def adjust(logits: torch.Tensor, out: torch.Tensor, settings: torch.Tensor, toke
             raise ValueError(f"out: the logits' own memory with rows {ldo} apart, wanted {ld}")
         _refuse(logits, ("settings", settings, (_I32,), (B, 8), 16), ("tokens", tokens, (_I32,), (B, None), 4),
                 ("mask", mask, (_I32,), (None, (V + 31) // 32), 4), ("bias", bias, (_I32,), (B, None, 2), 8))
-        raise ValueError(f"{L} tokens, {M} masks and {n} biases: at most 2^28, 65535 and 65535")
+        raise ValueError(f"{L} tokens, {M} masks and {n} biases: at most 2^28, 65535 and {MAX_BIASES}")
     return _desc((_ADJUST, dt, 0, 0, a, tp, o, sp, mp, bp, B, V, ld, ldo, L, M | n << 16, 0.0))
 
 

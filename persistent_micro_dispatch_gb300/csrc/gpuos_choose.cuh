@@ -142,12 +142,19 @@ DEV uint32_t adjust_bits(const AdjustArgs &a, int32_t v, uint32_t V)
     return __funnelshift_r(lo, hi, (uint32_t)v & 31u);
 }
 DEV bool adjust_allowed(const AdjustArgs &a, uint32_t v) { return !a.mask || (__ldcg(a.mask + (v >> 5)) >> (v & 31u) & 1u); }
-/* Entry i's token is listed again behind it: the later entry counts. */
+/* Each lane's entry i, of this token, is listed again behind it: the later
+ * entry counts. Every lane of the warp. */
 DEV bool adjust_again(const AdjustArgs &a, uint32_t i, int32_t token)
 {
-    for (uint32_t k = i + 1; k < (uint32_t)a.q.biases; k++)
-        if (__ldcg(&a.bias[k].x) == token) return true;
-    return false;
+    const uint32_t n = (uint32_t)a.q.biases;
+    bool again = false;
+#pragma unroll 1
+    for (uint32_t k0 = i & ~31u; k0 < n; k0 += 32) {
+        const int32_t t = k0 + lane_id() < n ? __ldcg(&a.bias[k0 + lane_id()].x) : -1;
+#pragma unroll 1
+        for (uint32_t k = 0; k < 32 && k0 + k < n; k++) again |= __shfl_sync(GPUOS_FULL, t, (int)k) == token && k0 + k > i;
+    }
+    return again;
 }
 
 /* One warp's tile: GPUOS_ADJUST_CHUNK places of one row. */
@@ -268,7 +275,9 @@ DEV int adjust_tile(const gpuos_devdesc *d, uint32_t tile)
                     if ((k & 7u) == j) w = o;
                 }
             }
-            if (here && !adjust_again(a, i, e.x)) {
+            if (!__any_sync(GPUOS_FULL, here)) continue;
+            const bool again = adjust_again(a, i, e.x); /* (i0 is alike in the lanes, and a multiple of 32) */
+            if (here && !again) {
                 const float y = fmaf(__int_as_float(e.y), a.plain, adjust_penalty(a, in.one(at + shift), w));
                 out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
             }
@@ -1222,7 +1231,7 @@ DEV uint32_t adjust_mask(const AdjustArgs &a, uint32_t at, uint32_t lo, uint32_t
     return lo == 0 ? a.mask[at >> 5] >> (at & 31u) : adjust_bits(a, (int32_t)at - (int32_t)lo, V);
 }
 /* The listed tokens of places [from, to): nobody has written them (out may be
- * the input). `listed`: the first THREADS entries' tokens; counter(place). */
+ * the input). `listed`: the entries' tokens; counter(place). */
 template <bool F32, int THREADS, typename Counter>
 DEV void adjust_listed(const AdjustArgs &a, const ChooseRow<F32> &in, const ChooseRow<F32> &out, uint32_t V, uint32_t shift, uint32_t from, uint32_t to,
                        const int32_t *listed, const Counter &counter)
@@ -1232,8 +1241,8 @@ DEV void adjust_listed(const AdjustArgs &a, const ChooseRow<F32> &in, const Choo
         const uint32_t at = (uint32_t)e.x + out.lo;
         if ((uint32_t)e.x >= V || at < from || at >= to) continue;
         bool again = false; /* listed again further on: the later entry counts */
-        for (uint32_t k = i + 1; k < min((uint32_t)a.q.biases, (uint32_t)THREADS); k++) again |= listed[k] == e.x;
-        if (again || ((uint32_t)a.q.biases > THREADS && adjust_again(a, max(i, THREADS - 1u), e.x))) continue;
+        for (uint32_t k = i + 1; k < (uint32_t)a.q.biases; k++) again |= listed[k] == e.x;
+        if (again) continue;
         const float y = fmaf(__int_as_float(e.y), a.plain, adjust_penalty(a, in.one(at + shift), counter(at)));
         out.put(at, adjust_allowed(a, (uint32_t)e.x) ? y : -INFINITY);
     }
@@ -1244,7 +1253,7 @@ __global__ void __launch_bounds__(GPUOS_ADJUSTB_THREADS, (VECS == 2 ? 1280 : 102
 {
     constexpr uint32_t THREADS = GPUOS_ADJUSTB_THREADS, CHUNK = THREADS * VECS * 8u;
     __shared__ __align__(16) uint32_t ctr[CHUNK];
-    __shared__ int32_t listed[THREADS];
+    __shared__ int32_t listed[GPUOS_ADJUST_MAX_BIAS];
     kv4_after_previous();
     const uint32_t V = d.dims[1], b = blockIdx.y, t = threadIdx.x;
     const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
@@ -1295,7 +1304,7 @@ __global__ void __launch_bounds__(GPUOS_ADJUSTB_THREADS, (VECS == 2 ? 1280 : 102
         }
         for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
             const uint32_t token = (uint32_t)a.bias[i].x, at = token + out.lo - from;
-            if (i < THREADS) listed[i] = (int32_t)token;
+            listed[i] = (int32_t)token;
             if (token < V && at < CHUNK) atomicOr(ctr + at, GPUOS_ADJUST_LISTED);
         }
         __syncthreads();
@@ -1328,7 +1337,7 @@ __global__ void __launch_bounds__(GPUOS_ADJUSTL_THREADS) gpuos_adjust_long_kerne
     constexpr uint32_t THREADS = GPUOS_ADJUSTL_THREADS, CHUNK = THREADS * 8u, N = GPUOS_ADJUSTL_BLOCKS;
     extern __shared__ __align__(16) uint32_t adjust_half[]; /* N CHUNK counters of 16 bits */
     __shared__ uint32_t has_bias[CHUNK / 32]; /* of this block's chunk */
-    __shared__ int32_t listed[THREADS];
+    __shared__ int32_t listed[GPUOS_ADJUST_MAX_BIAS];
     kv4_after_previous();
     const uint32_t V = d.dims[1], b = blockIdx.y, t = threadIdx.x, rank = blockIdx.x % N;
     const ChooseRow<F32> in(d.a, b, d.dims[2], V), out(d.out, b, d.dims[3], V);
@@ -1362,7 +1371,7 @@ __global__ void __launch_bounds__(GPUOS_ADJUSTL_THREADS) gpuos_adjust_long_kerne
     }
     for (uint32_t i = t; i < (uint32_t)a.q.biases; i += THREADS) {
         const uint32_t token = (uint32_t)a.bias[i].x, p = token + out.lo - from;
-        if (i < THREADS) listed[i] = (int32_t)token;
+        listed[i] = (int32_t)token;
         if (token < V && p < CHUNK) atomicOr(has_bias + (p >> 5), 1u << (p & 31u));
     }
     choose_cluster_sync();

@@ -37,6 +37,7 @@
 #define GPUOS_PAGE_CHUNK 16384            /* bytes of a page-copy tile */
 #define GPUOS_ADJUST_CHUNK 4096           /* tokens of a logits-adjust tile (16 KB of counters) */
 #define GPUOS_ADJUST_MAX_L (1u << 28)     /* tokens of a request's history (a counter has 29 bits) */
+#define GPUOS_ADJUST_MAX_BIAS 1024        /* listed biases of a request (a block holds their tokens) */
 #define GPUOS_TOP_MAX_K 64                /* best tokens of a row at most (two for each lane) */
 #define GPUOS_TOP_TILES 2048              /* partial states of a logits-top, and counters */
 #define GPUOS_TOP_SPLIT 1536              /* tiles of a split logits-top at most (one wave of the default executor) */
@@ -92,7 +93,7 @@ static inline GPUOS_HD bool gpuos_adjust_ok(uint32_t dtype, uint64_t a, uint64_t
     if (a == out && m[2] != m[3]) return false;
     if (requests == 0 || (requests & 15u) || (tokens & 3u) || (masks & 3u) || (biases & 7u)) return false;
     return m[4] <= GPUOS_ADJUST_MAX_L && (tokens || m[4] == 0) && (masks || (m[5] & 0xFFFFu) == 0) &&
-           (biases || (m[5] >> 16) == 0);
+           (m[5] >> 16) <= GPUOS_ADJUST_MAX_BIAS && (biases || (m[5] >> 16) == 0);
 }
 static inline GPUOS_HD bool gpuos_top_ok(uint32_t dtype, uint64_t a, uint64_t ids, uint64_t logp, uint64_t lse, uint64_t ws,
                                          const uint32_t *m)
@@ -106,7 +107,7 @@ static inline GPUOS_HD bool gpuos_route_ok(uint32_t dtype, uint64_t a, uint64_t 
 {
     const uint32_t E = m[1], K = m[3], G = m[4] & 0xFFFFu, keep = m[4] >> 16;
     if (!gpuos_rows_ok(dtype, a, E, m[2]) || !ids || !weights || ((bias | ids | weights | rows) & 3u)) return false;
-    if (E > GPUOS_ROUTE_MAX_E || K == 0 || K > GPUOS_ROUTE_MAX_K || m[5] > 7u) return false;
+    if (m[0] > 0x7FFFFF00u || E > GPUOS_ROUTE_MAX_E || K == 0 || K > GPUOS_ROUTE_MAX_K || m[5] > 7u) return false;
     if (G == 0 || G > 32u || E % G || keep == 0 || keep > G) return false;
     return K <= keep * (E / G) && !((m[5] & GPUOS_ROUTE_TOP2) && E / G < 2u);
 }

@@ -58,10 +58,10 @@ def test_tiles(G):
 
 
 @pytest.mark.parametrize("op,at,value", [
-    *[("logits_adjust", i, v) for i, v in ((1, 0x7FFFFF00), (2, 999), (3, 999), (4, (1 << 28) + 1), (0, 1 << 31))],
+    *[("logits_adjust", i, v) for i, v in ((1, 0x7FFFFF00), (2, 999), (3, 999), (4, (1 << 28) + 1), (0, 1 << 31), (5, 1 | 1025 << 16))],
     *[("logits_top", i, v) for i, v in ((1, 0), (1, 19), (1, 0x7FFFFF00), (2, 999), (3, 0), (3, 65))],
     *[("expert_route", i, v) for i, v in (
-        (1, 0), (1, 63), (1, 1032), (2, 63), (3, 0), (3, 33), (4, 8), (4, 4 << 16), (4, 7 | 4 << 16), (4, 8 | 9 << 16),
+        (0, 0x7FFFFF01), (1, 0), (1, 63), (1, 1032), (2, 63), (3, 0), (3, 33), (4, 8), (4, 4 << 16), (4, 7 | 4 << 16), (4, 8 | 9 << 16),
         (4, 64 | 64 << 16), (4, 16 | 1 << 16), (5, 8))],
     *[(op, i, v) for op in ("expert_count", "expert_place") for i, v in ((0, 0x7FFFFF01), (1, 0), (1, 1025))],
 ])

@@ -98,7 +98,7 @@ ADJUST = [
     # B, V, pad in, pad out, L, biases, masks
     (1, 1, 0, 0, 1, 1, 1), (1, 7, 0, 0, 0, 0, 0), (3, 9, 1, 3, 5, 3, 2), (4, 33, 0, 0, 300, 8, 2), (5, 256, 8, 8, 64, 0, 3),
     (2, 4096, 0, 0, 1000, 40, 1), (3, 4089, 0, 7, 257, 5, 2), (3, 5001, 47, 0, 700, 70, 3), (2, 33003, 1, 1, 3000, 3, 2),
-    (2, 32000, 0, 0, 5000, 0, 0), (3, 33003, 1, 0, 9000, 40, 2), (2, 70000, 8, 8, 20000, 600, 1), (1, 2001, 0, 0, 300000, 3, 1), (6, 8200, 56, 56, 31, 33, 4), (33, 1000, 0, 1, 17, 2, 1),
+    (2, 32000, 0, 0, 5000, 0, 0), (3, 33003, 1, 0, 9000, 40, 2), (2, 70000, 8, 8, 20000, 600, 1), (2, 3000, 0, 0, 40, 1024, 1), (1, 2001, 0, 0, 300000, 3, 1), (6, 8200, 56, 56, 31, 33, 4), (33, 1000, 0, 1, 17, 2, 1),
 ]
 
 

@@ -412,7 +412,7 @@ def test_binding_refusals():
             ("out", x[:, 1:], ValueError), ("out", x.cpu(), ValueError), ("settings", choose.new_settings(2), ValueError),
             ("settings", choose.new_settings(B).float(), TypeError), ("settings", flat[1:].view(B, 8), ValueError), ("tokens", i32(2, 4), ValueError),
             ("tokens", i32(B, 4).long(), TypeError), ("tokens", i32(4, B).t(), ValueError), ("tokens", i32(B), ValueError), ("bias", i32(B, 2), ValueError),
-            ("bias", i32(B, 2, 3), ValueError), ("bias", flat[1:13].view(B, 2, 2), ValueError), ("bias", i32(B, 1 << 16, 2), ValueError),
+            ("bias", i32(B, 2, 3), ValueError), ("bias", flat[1:13].view(B, 2, 2), ValueError), ("bias", i32(B, 1025, 2), ValueError),
             ("mask", i32(1, 3), ValueError), ("mask", i32(4), ValueError), ("mask", i32(1 << 16, 4), ValueError), ("mask", i32(1, 4).cpu(), ValueError)]:
         with pytest.raises(err):
             choose.adjust(**{**good, name: bad})
