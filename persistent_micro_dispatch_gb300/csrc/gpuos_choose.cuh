@@ -1472,6 +1472,8 @@ static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
 #define GPUOS_TOPB_UNIT 4096u /* elements: sixteen a thread */
 #define GPUOS_TOPB_STAGES 3u
 #define GPUOS_TOPB_FEW 256u
+#define GPUOS_TOPB_PLAIN 192u /* entries that are ranked without a bar before */
+#define GPUOS_TOPB_SOME 512u /* ... that a bar lets pass (lists: K, and 56 more of eight) */
 static_assert(2u * GPUOS_TOPB_SLOTS <= GPUOS_TOP_TILES, "two pieces of each block in the workspace");
 /* (the slow gathering: a unit adds at most K threads' 16 elements to the few before it) */
 #define GPUOS_TOPB_ROOM (GPUOS_TOPB_FEW + GPUOS_TOP_MAX_K * 16u)
@@ -1490,7 +1492,7 @@ struct TopUnit {
 struct TopBlock {
     /* (eight more of each: a list's end is filled with entries below all others) */
     __align__(16) uint64_t got[GPUOS_TOPB_JOIN + 8u];
-    __align__(16) uint64_t few[GPUOS_TOPB_FEW + 8u];
+    __align__(16) uint64_t few[GPUOS_TOPB_SOME + 8u];
     __align__(16) uint64_t best[GPUOS_TOPB_THREADS];
     uint64_t sorted[GPUOS_TOP_MAX_K];
     uint64_t bar; /* an entry has to be above it */
@@ -1516,22 +1518,34 @@ DEV uint32_t top_fill(uint64_t *e, uint32_t n) /* (before a barrier) */
     if (threadIdx.x < 8u) e[n + threadIdx.x] = 0;
     return (n + 7u) & ~7u;
 }
-/* A bar that at least K of the threads' entries are above (0: there are not K,
- * or not K in the warps' eight best): the K-th of the warps' eight best, less
- * one. Every thread. */
+/* A bar that at least K of the threads' entries are above (0: there are not
+ * K): the K-th of them less one; or, for few, the K-th of the warps' best few
+ * less one, which takes a third of the time. Every thread. */
+DEV uint64_t top_bar_exact(TopBlock &s, uint64_t mine, uint32_t K)
+{
+    const uint32_t t = threadIdx.x;
+    __syncthreads(); /* (the last use of best and bar is over) */
+    s.best[t] = mine;
+    if (t == 0) s.bar = 0;
+    __syncthreads();
+    if (mine && top_rank(s.best, GPUOS_TOPB_THREADS, mine) == K - 1u) s.bar = mine - 1u;
+    __syncthreads();
+    return s.bar;
+}
 DEV uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
 {
+    if (K > 32u) return top_bar_exact(s, mine, K); /* (the warps' eight best are 64: their K-th lets far too many pass) */
     const uint32_t t = threadIdx.x, lane = lane_id();
     uint64_t keep = 0;
 #pragma unroll 1
-    for (uint32_t i = 0; i < min(K, min((K + 23u) / 8u, 8u)); i++) {
+    for (uint32_t i = 0; i < min(K, (K + 23u) / 8u); i++) {
         const uint32_t hi = __reduce_max_sync(GPUOS_FULL, (uint32_t)(mine >> 32));
         const uint32_t lo = __reduce_max_sync(GPUOS_FULL, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
         const uint64_t top = (uint64_t)hi << 32 | lo;
         if (mine == top) mine = 0;
         if (lane == i) keep = top;
     }
-    __syncthreads(); /* (the last use of best and bar is over) */
+    __syncthreads();
     if (lane < 8) s.best[(t >> 5) * 8u + lane] = keep;
     if (t == 0) s.bar = 0;
     __syncthreads();
@@ -1543,24 +1557,32 @@ DEV uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
     return s.bar;
 }
 /* The K best of the n gathered ones, in order, into `sorted` (0 where there
- * are none); every thread, after a barrier. */
-DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K)
+ * are none); every thread, after a barrier. `lists`: they are so many lists of K
+ * in order (0: they are in none). */
+DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K, uint32_t lists = 0)
 {
     const uint32_t t = threadIdx.x;
     uint64_t *from = s.got;
-    if (n > 192u) { /* first those that reach a bar of their own */
-        uint64_t mine = 0;
-        for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) mine = max(mine, s.got[i]);
+    if (n > GPUOS_TOPB_PLAIN) { /* first those that reach a bar of their own */
+        uint64_t mine = 0, bar;
         if (t == 0) s.left = 0;
-        const uint64_t bar = top_bar(s, mine, K);
+        if (lists) { /* of the lists' first 256 entries: their K-th lets little more pass than K (one row of
+                      * 128,000, 32 lists, K = 64: 13 us; the best of every 256th entry instead: 107) */
+            const uint32_t f = t % lists, k = t / lists;
+            if (k < min(K, GPUOS_TOPB_THREADS / lists)) mine = s.got[f * K + k];
+            bar = top_bar_exact(s, mine, K);
+        } else {
+            for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) mine = max(mine, s.got[i]);
+            bar = top_bar(s, mine, K);
+        }
         for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) {
             const uint64_t x = s.got[i];
             if (x <= bar) continue;
             const uint32_t at = atomicAdd(&s.left, 1u);
-            if (at < GPUOS_TOPB_FEW) s.few[at] = x;
+            if (at < GPUOS_TOPB_SOME) s.few[at] = x;
         }
         __syncthreads();
-        if (s.left <= GPUOS_TOPB_FEW) n = s.left, from = s.few;
+        if (s.left <= GPUOS_TOPB_SOME) n = s.left, from = s.few;
     }
     if (t < K) s.sorted[t] = 0;
     const uint32_t n8 = top_fill(from, n);
@@ -1568,7 +1590,7 @@ DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K)
     for (uint32_t i = t; i < n; i += GPUOS_TOPB_THREADS) {
         const uint64_t x = from[i];
         const uint32_t r = top_rank(from, n8, x);
-        if (r < K) s.sorted[r] = x;
+        if (r < K && x) s.sorted[r] = x;
     }
     __syncthreads();
 }
@@ -1597,9 +1619,9 @@ DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s
     if (d.aux1 && t == 0) reinterpret_cast<float *>(d.aux1)[row] = m + ls;
 }
 /* A unit's elements in this thread, -infinity outside [lo, hi): those at places
- * [b0, b1) (whole vectors) out of `stage`, which begins at u0; the others, of
- * which a row's ends have a few, from the row. */
-template <bool F32>
+ * [b0, b1) (whole vectors) out of `stage`, which begins at u0 (or, not STAGED,
+ * from the row); the others, of which a row's ends have a few, from the row. */
+template <bool F32, bool STAGED>
 DEV void top_load(const ChooseRow<F32> &r, const unsigned char *stage, uint32_t u0, uint32_t b0, uint32_t b1, uint32_t lo, uint32_t hi,
                   float (&x)[TopUnit<F32>::G][8])
 {
@@ -1610,7 +1632,7 @@ DEV void top_load(const ChooseRow<F32> &r, const unsigned char *stage, uint32_t 
         for (uint32_t j = 0; j < 8; j += U::PER) {
             const uint32_t p = u0 + U::at(u, j);
             if (p >= b0 && p < b1) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(stage + U::at(u, j) * (F32 ? 4u : 2u));
+                const uint4 v = STAGED ? *reinterpret_cast<const uint4 *>(stage + U::at(u, j) * (F32 ? 4u : 2u)) : __ldcg(r.vec(p));
                 if (F32) {
                     x[u][j & 4u] = __uint_as_float(v.x), x[u][(j & 4u) + 1] = __uint_as_float(v.y), x[u][(j & 4u) + 2] = __uint_as_float(v.z),
                     x[u][(j & 4u) + 3] = __uint_as_float(v.w);
@@ -1664,6 +1686,7 @@ DEV void top_push(TopBlock &s, uint64_t bar, float x, uint32_t p, uint32_t lo, u
 template <bool F32>
 __device__ __noinline__ uint32_t top_gather_slow(TopBlock &s, const ChooseRow<F32> r, uint32_t from, uint32_t lo, uint32_t hi, uint32_t K)
 {
+    using U = TopUnit<F32>;
     const uint32_t t = threadIdx.x;
     uint64_t bar = 0;
     __syncthreads();
@@ -1671,7 +1694,7 @@ __device__ __noinline__ uint32_t top_gather_slow(TopBlock &s, const ChooseRow<F3
 #pragma unroll 1
     for (uint32_t u0 = from; u0 < hi; u0 += TopUnit<F32>::N) {
         float x[TopUnit<F32>::G][8];
-        top_load(r, nullptr, u0, 0u, 0u, lo, hi, x); /* (element by element: nothing here is often) */
+        top_load<F32, false>(r, nullptr, u0, (lo + U::PER - 1u) & ~(U::PER - 1u), hi & ~(U::PER - 1u), lo, hi, x);
         const uint64_t mine = top_mine<F32>(x, u0, lo, hi, r.lo);
         const uint32_t above = (uint32_t)__syncthreads_count(mine > bar);
         if (above == 0) continue;
@@ -1825,7 +1848,7 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
             const uint2 b = whole(r, u0, lo, hi);
             float x[U::G][8], most[U::G], unit = -INFINITY;
             if (!mbar_wait(&full[at], turn)) lost = true;
-            top_load(r, top_ring + at * U::BYTES, u0, b.x, b.y, lo, hi, x);
+            top_load<F32, true>(r, top_ring + at * U::BYTES, u0, b.x, b.y, lo, hi, x);
 #pragma unroll
             for (uint32_t u = 0; u < U::G; u++) {
                 most[u] = -INFINITY; /* (a maximum passes a NaN over) */
@@ -1868,10 +1891,15 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
                 bar = top_bar(s, top_mine<F32>(x, u0, lo, hi, r.lo), K);
                 barf = bar ? choose_unkey((uint32_t)(bar >> 32)) : -INFINITY; /* (that bar's value itself may pass) */
             }
-            if (u0 == from ? unit >= barf : unit > barf || bar == 0) { /* (an equal one in a later unit comes after) */
+            const bool strict = u0 != from && bar != 0; /* (an equal one in a later unit comes after) */
+            if (strict ? unit > barf : unit >= barf) {
                 uint32_t reach = 0;
 #pragma unroll
-                for (uint32_t i = 0; i < 8u * U::G; i++) reach |= !(x[i >> 3][i & 7u] < barf) ? 1u << i : 0u;
+                for (uint32_t i = 0; i < 8u * U::G; i++) reach |= x[i >> 3][i & 7u] > barf ? 1u << i : 0u;
+                if (!strict) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 8u * U::G; i++) reach |= !(x[i >> 3][i & 7u] < barf) ? 1u << i : 0u;
+                }
 #pragma unroll 1
                 for (; reach; reach &= reach - 1u) { /* (few: read again, so that no array needs an index) */
                     const uint32_t k = (uint32_t)__ffs((int)reach) - 1u, o = U::at(k >> 3, k & 7u), p = u0 + o;
@@ -1956,7 +1984,7 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
                 for (uint32_t i = t; i < F * K; i += GPUOS_TOPB_THREADS) /* (entries that are not there are 0, and below all others) */
                     s.got[i] = __ldcg(reinterpret_cast<const unsigned long long *>(part(i / K) + 16) + i % K);
                 __syncthreads();
-                top_sort(s, F * K, K);
+                top_sort(s, F * K, K, F);
                 top_block_softmax(s, m, l);
                 top_block_write(d, row, s, m, l);
             }
