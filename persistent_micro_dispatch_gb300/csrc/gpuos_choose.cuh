@@ -1518,10 +1518,14 @@ DEV uint32_t top_fill(uint64_t *e, uint32_t n) /* (before a barrier) */
     if (threadIdx.x < 8u) e[n + threadIdx.x] = 0;
     return (n + 7u) & ~7u;
 }
-/* A bar that at least K of the threads' entries are above (0: there are not
+/* (The bars and the sort are functions of their own: inlined at each of their
+ * places, 509 x 128,000 took 57.8 us, so 56.6. A launch runs them from a cold
+ * instruction cache.)
+ *
+ * A bar that at least K of the threads' entries are above (0: there are not
  * K): the K-th of them less one; or, for few, the K-th of the warps' best few
  * less one, which takes a third of the time. Every thread. */
-DEV uint64_t top_bar_exact(TopBlock &s, uint64_t mine, uint32_t K)
+__device__ __noinline__ uint64_t top_bar_exact(TopBlock &s, uint64_t mine, uint32_t K)
 {
     const uint32_t t = threadIdx.x;
     __syncthreads(); /* (the last use of best and bar is over) */
@@ -1532,7 +1536,7 @@ DEV uint64_t top_bar_exact(TopBlock &s, uint64_t mine, uint32_t K)
     __syncthreads();
     return s.bar;
 }
-DEV uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
+__device__ __noinline__ uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
 {
     if (K > 32u) return top_bar_exact(s, mine, K); /* (the warps' eight best are 64: their K-th lets far too many pass) */
     const uint32_t t = threadIdx.x, lane = lane_id();
@@ -1559,7 +1563,7 @@ DEV uint64_t top_bar(TopBlock &s, uint64_t mine, uint32_t K)
 /* The K best of the n gathered ones, in order, into `sorted` (0 where there
  * are none); every thread, after a barrier. `lists`: they are so many lists of K
  * in order (0: they are in none). */
-DEV void top_sort(TopBlock &s, uint32_t n, uint32_t K, uint32_t lists = 0)
+__device__ __noinline__ void top_sort(TopBlock &s, uint32_t n, uint32_t K, uint32_t lists = 0)
 {
     const uint32_t t = threadIdx.x;
     uint64_t *from = s.got;
