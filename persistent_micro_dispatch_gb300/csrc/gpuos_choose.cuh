@@ -865,8 +865,9 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
         if (lane == k && k < a.K) id = e;
     }
     const float x = lane < a.K ? route_logit(d, a, n, id) : -INFINITY;
-    /* (a chosen logit below -80: its weight may be all that is seen) */
-    if (sigmoid && __any_sync(GPUOS_FULL, x < -80.0f && x != -INFINITY)) sure = false;
+    /* (a chosen score below e^-80, that floats do not hold: its share may be all
+     * that is seen. Without a bias a softmax's largest is among the chosen.) */
+    if ((sigmoid || a.bias) && __any_sync(GPUOS_FULL, x - (sigmoid ? 0.0f : most) < -80.0f && x != -INFINITY)) sure = false;
     if (!sure) return false;
     route_write(a, n, id, route_score(sigmoid, x, most, inv));
     return true;
@@ -1329,7 +1330,8 @@ __global__ void __launch_bounds__(GPUOS_ADJUSTB_THREADS, (VECS == 2 ? 1280 : 102
 #define GPUOS_ADJUSTL_THREADS 512u
 DEV void choose_cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    /* (not the aligned form: it follows loops whose lanes end apart) */
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 template <bool F32, bool SAME>
 __global__ void __launch_bounds__(GPUOS_ADJUSTL_THREADS) gpuos_adjust_long_kernel(const __grid_constant__ gpuos_devdesc d)
@@ -1460,9 +1462,9 @@ static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
  * blocks an SM, 7 TB/s); a piece's start and end take it about 5 us (first copy
  * 1, bar 1, ranks 0.5, sums 0.5, a part's way to the row's last block 1 to 2,
  * joining 2), which the SM's other two blocks cover only in part. 456 rows of
- * 128,000 in f32, K = 5: 43.5 us, 5.4 TB/s (K = 1: 41); 509 rows, whose runs
- * cross rows, 55.5, 4.7 TB/s (three equal runs for each row, 4 waves: 62); 64
- * rows in bf16, K = 20: 16; one row of 32,000, K = 1: 6.1. Loads to registers
+ * 128,000 in f32, K = 5: 44 us, 5.3 TB/s (K = 1: 42); 509 rows, whose runs
+ * cross rows, 56.5, 4.6 TB/s (three equal runs for each row, 4 waves: 62); 64
+ * rows in bf16, K = 20: 16.5; one row of 32,000, K = 1: 6.2. Loads to registers
  * instead of the ring took the same time while they were the only change.
  * ------------------------------------------------------------------------- */
 #define GPUOS_TOPB_THREADS 256
@@ -2414,7 +2416,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         }
         const uint32_t id = GPUOS_FULL - (uint32_t)s.best[mine];
         const float x = s.best_logit[mine];
-        if (sigmoid && chosen && x < -80.0f && x != -INFINITY) sure = false; /* (its weight may be all that is seen) */
+        if ((sigmoid || biased) && chosen && x - (sigmoid ? 0.0f : most) < -80.0f && x != -INFINITY) sure = false; /* (see route_token) */
         float w = chosen ? route_score(sigmoid, x, most, inv) : 0.0f;
         if (norm) {
             const float sum = lanes_sum<L>(w);

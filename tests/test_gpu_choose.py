@@ -363,6 +363,22 @@ def test_experts_ties_and_masked(sigmoid, groups, keep, biased, run):
 
 
 @pytest.mark.parametrize("run", ["eager", "executor"])
+@pytest.mark.parametrize("E,K", [(64, 6), (256, 8), (256, 20)])
+@pytest.mark.parametrize("f32", [True, False])
+def test_experts_whose_scores_no_float_holds(f32, E, K, run):
+    """A softmax whose bias chooses experts far below the largest: their weights are shares of one another."""
+    rng = np.random.default_rng(12)
+    x = (rng.standard_normal((9, E)) * 2 - np.array([60, 79, 81, 85, 90, 100, 150, 300, 600])[:, None]).astype(np.float32)
+    x[:, 3] = 0.0
+    x[4, 10:] = -np.inf
+    x = x if f32 else R.bf16(x)
+    bias = (8 + rng.random(E)).astype(np.float32)
+    bias[3] = -4.0
+    _check_experts(run, x, f32, 0, K, bias, sigmoid=False, groups=1, keep=1, top2=False)
+    _check_experts(run, x, f32, 0, K, bias, sigmoid=False, groups=4, keep=2, top2=True)
+
+
+@pytest.mark.parametrize("run", ["eager", "executor"])
 def test_experts_of_a_padded_batch(run):
     rng = np.random.default_rng(1)
     x = rng.standard_normal((50, 32)).astype(np.float32)
