@@ -177,8 +177,9 @@ enum {
                                best member or the sum of their two best. Ties go to the lower expert (or
                                group); the choice is that of 64-bit arithmetic. Weights are divided by
                                their sum if asked, then multiplied by fparam[0]. A NaN logit counts as
-                               -infinity (score 0); weights of sum 0 stay 0. aux1 = i32[1] on the device
-                               (0: none): tokens from there on are padding, with ids -1 and weights 0.
+                               -infinity (score 0); weights of sum 0 stay 0, and one below 2^-126 may
+                               be 0. aux1 = i32[1] on the device (0: none): tokens from there on are
+                               padding, with ids -1 and weights 0.
                                dims = {N < 2^31, E <= 1024, ld, K <= 32, G | keep << 16, GPUOS_ROUTE_* flags},
                                G <= 32, E % G == 0, K <= keep * (E / G) */
     GPUOS_OP_EXPERT_COUNT = 22, /* the pairs of each expert in runs of a = ids i32[P], into aux2 = workspace

@@ -2031,9 +2031,10 @@ static int top_launch(const gpuos_devdesc &d, void *stream)
  * all with all. Values are floats to the end; NaN is what may not be chosen.
  *
  * 32,768 tokens of 256 experts (f32, sigmoid, bias, four of eight groups by their
- * two best, K = 8): 32 us against 5.3 of memory: 1,100 warp instructions for two
- * tokens, issue slots 65 % used, the half-rate pipe of minima, maxima and
- * comparisons 53 %. Without bias and groups 18 us. 65,536 of 64 experts 16.1 us.
+ * two best, K = 8): 31 us against 5.3 of memory: 1,060 warp instructions for two
+ * tokens, issue slots 63 % used, the half-rate pipe of minima, maxima and
+ * comparisons 50 %. Without bias and groups 18 us. 65,536 of 64 experts 16.1 us.
+ * (A warp's next rows asked for ahead: 30.7; 1,024 to 4,096 blocks: 32 to 35.)
  * Where values are near, 1 token in 1,000 here, sums of two floats tell them
  * apart (with 64-bit arithmetic instead the launch took 45 us, its last tokens
  * 15 of them). A kernel for each kind of score and bias would save 6 % of it.
@@ -2064,18 +2065,19 @@ DEV float lanes_sum(float v)
     for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(GPUOS_FULL, v, o);
     return v;
 }
-/* The lanes' values from the largest down. */
+/* The lanes' values from the largest down: runs of a size are merged by a
+ * comparison of each lane with its mirror image, then with lanes ever nearer;
+ * the larger always goes to the lower lane. */
 template <int L>
 DEV float lanes_sort(float v)
 {
-    const uint32_t lane = lane_id() & (L - 1);
+    const uint32_t lane = lane_id();
 #pragma unroll
     for (uint32_t size = 2; size <= L; size <<= 1)
 #pragma unroll
         for (uint32_t o = size >> 1; o; o >>= 1) {
-            const float other = __shfl_xor_sync(GPUOS_FULL, v, (int)o);
-            const bool down = (lane & size) == 0 || size == L, first = (lane & o) == 0;
-            v = down == first ? fmaxf(v, other) : fminf(v, other);
+            const float other = __shfl_xor_sync(GPUOS_FULL, v, (int)(o == size >> 1 ? size - 1u : o));
+            v = lane & o ? fminf(v, other) : fmaxf(v, other);
         }
     return v;
 }
@@ -2084,7 +2086,7 @@ DEV float lanes_sort(float v)
 DEV float route_sigmoid_fast(float x)
 {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(x * -1.44269504f, 126.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f)); /* (infinite below -88: 0) */
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
@@ -2242,7 +2244,12 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         }
         float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) c[i] = fmaxf(c[i], -INFINITY), most = fmaxf(most, c[i]); /* (a NaN counts as -infinity) */
+        for (int i = 0; i < VPL; i++) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(c[i]));
+        if (__any_sync(GPUOS_FULL, most != most)) { /* a NaN counts as -infinity */
+            most = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) c[i] = fmaxf(c[i], -INFINITY), most = fmaxf(most, c[i]);
+        }
         most = fminf(lanes_max<L>(most), FLT_MAX);
         float inv = 1.0f; /* (a softmax whose scores are only divided by one another does without its sum) */
         if (!sigmoid && (biased || summed || !norm)) {
@@ -2261,7 +2268,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
          * and a sum) and, where x < 0, 1.5 |x| 2^-24 of itself (its argument's
          * rounding); |x| s(x) is at most (1 + |most|) s(most) there. A softmax's
          * 2^-19 (its sum's errors too). A sum with the bias: 2^-24 more of itself. */
-        const float low = fminf(most, 0.0f);
+        const float low = fmaxf(fminf(most, 0.0f), -256.0f); /* (s(most) is 0 before that) */
         const float unsure = (sigmoid ? route_sigmoid_fast(most) * (0x1.8p-20f - low * 0x1p-21f) : inv * 0x1p-18f) + wide * 0x1p-22f;
         bool sure = !sigmoid || most >= -60.0f || most == -INFINITY;
         if (!VEC) {
@@ -2273,11 +2280,16 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         float one, two, three;
         {
             float p1 = -INFINITY, p2 = -INFINITY, q1 = -INFINITY, q2 = -INFINITY;
+            auto v = [&](int k) { return VEC || c[k] == c[k] ? c[k] : -INFINITY; };
+            auto two_more = [](float &best, float &second, float x, float y) {
+                const float more = fmaxf(x, y);
+                second = fmaxf(fmaxf(second, fminf(x, y)), fminf(best, more));
+                best = fmaxf(best, more);
+            };
 #pragma unroll
-            for (int i = 0; i < VPL; i += 2) {
-                const float p = VEC || c[i] == c[i] ? c[i] : -INFINITY, q = VEC || c[i + 1] == c[i + 1] ? c[i + 1] : -INFINITY;
-                p2 = fmaxf(p2, fminf(p1, p)), p1 = fmaxf(p1, p);
-                q2 = fmaxf(q2, fminf(q1, q)), q1 = fmaxf(q1, q);
+            for (int i = 0; i < VPL; i += 4) {
+                two_more(p1, p2, v(i), v(i + 2));
+                two_more(q1, q2, v(i + 1), v(i + 3));
             }
             one = fmaxf(p1, q1);
             const float r = fminf(p1, q1), t = fmaxf(p2, q2);
