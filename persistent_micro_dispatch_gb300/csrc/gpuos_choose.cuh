@@ -70,6 +70,13 @@ DEV uint32_t choose_key(float x)
 }
 /* e^x for x <= 80 (-infinity included; exp_ex2 takes no larger arguments either way). */
 DEV float choose_exp(float x) { return exp_ex2(fmaxf(x, -200.0f)); }
+/* The largest of three in one instruction; a NaN is passed over. */
+DEV float choose_max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 DEV float choose_unkey(uint32_t k) { return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u)); }
 
 /* ---------------------------------------------------------------------------
@@ -1624,6 +1631,17 @@ DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s
     }
     if (d.aux1 && t == 0) reinterpret_cast<float *>(d.aux1)[row] = m + ls;
 }
+/* A vector as a thread's elements from i on. */
+template <bool F32>
+DEV void top_vector(const uint4 &v, float (&x)[TopUnit<F32>::G][8], uint32_t i)
+{
+    if (F32) {
+        const uint32_t u = i >> 3, j = i & 4u;
+        x[u][j] = __uint_as_float(v.x), x[u][j + 1] = __uint_as_float(v.y), x[u][j + 2] = __uint_as_float(v.z), x[u][j + 3] = __uint_as_float(v.w);
+    } else {
+        unpack8(v, x[i >> 3]);
+    }
+}
 /* A unit's elements in this thread, -infinity outside [lo, hi): those at places
  * [b0, b1) (whole vectors) out of `stage`, which begins at u0 (or, not STAGED,
  * from the row); the others, of which a row's ends have a few, from the row. */
@@ -1638,13 +1656,7 @@ DEV void top_load(const ChooseRow<F32> &r, const unsigned char *stage, uint32_t 
         for (uint32_t j = 0; j < 8; j += U::PER) {
             const uint32_t p = u0 + U::at(u, j);
             if (p >= b0 && p < b1) {
-                const uint4 v = STAGED ? *reinterpret_cast<const uint4 *>(stage + U::at(u, j) * (F32 ? 4u : 2u)) : __ldcg(r.vec(p));
-                if (F32) {
-                    x[u][j & 4u] = __uint_as_float(v.x), x[u][(j & 4u) + 1] = __uint_as_float(v.y), x[u][(j & 4u) + 2] = __uint_as_float(v.z),
-                    x[u][(j & 4u) + 3] = __uint_as_float(v.w);
-                } else {
-                    unpack8(v, x[u]);
-                }
+                top_vector<F32>(STAGED ? *reinterpret_cast<const uint4 *>(stage + U::at(u, j) * (F32 ? 4u : 2u)) : __ldcg(r.vec(p)), x, 8u * u + j);
             } else {
 #pragma unroll
                 for (uint32_t k = 0; k < U::PER; k++) x[u][(j + k) & 7u] = p + k >= lo && p + k < hi ? r.one(p + k) : -INFINITY;
@@ -1852,16 +1864,17 @@ __global__ void __launch_bounds__(GPUOS_TOPB_THREADS, 3) gpuos_top_kernel(const 
         do {
             const uint32_t u0 = c.u0;
             const uint2 b = whole(r, u0, lo, hi);
-            float x[U::G][8], most[U::G], unit = -INFINITY;
+            float x[U::G][8], unit = -INFINITY;
             if (!mbar_wait(&full[at], turn)) lost = true;
-            top_load<F32, true>(r, top_ring + at * U::BYTES, u0, b.x, b.y, lo, hi, x);
+            if (b.x == u0 && b.y == u0 + U::N) {
 #pragma unroll
-            for (uint32_t u = 0; u < U::G; u++) {
-                most[u] = -INFINITY; /* (a maximum passes a NaN over) */
-#pragma unroll
-                for (uint32_t j = 0; j < 8; j++) most[u] = fmaxf(most[u], x[u][j]);
-                unit = fmaxf(unit, most[u]);
+                for (uint32_t i = 0; i < 8u * U::G; i += U::PER)
+                    top_vector<F32>(*reinterpret_cast<const uint4 *>(top_ring + at * U::BYTES + U::at(i >> 3, i & 7u) * SIZE), x, i);
+            } else { /* a row's first or last */
+                top_load<F32, true>(r, top_ring + at * U::BYTES, u0, b.x, b.y, lo, hi, x);
             }
+#pragma unroll
+            for (uint32_t i = 0; i < 8u * U::G; i += 2) unit = choose_max3(unit, x[i >> 3][i & 7u], x[i >> 3][(i & 7u) + 1]);
             if (fabsf(unit) <= 1e6f) {
                 if (unit > m) {
                     const float to = unit * L2E;
@@ -2244,7 +2257,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         }
         float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(c[i]));
+        for (int i = 0; i < VPL; i += 2) asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(most) : "f"(c[i]), "f"(c[i + 1]));
         if (__any_sync(GPUOS_FULL, most != most)) { /* a NaN counts as -infinity */
             most = -INFINITY;
 #pragma unroll
@@ -2283,7 +2296,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
             auto v = [&](int k) { return VEC || c[k] == c[k] ? c[k] : -INFINITY; };
             auto two_more = [](float &best, float &second, float x, float y) {
                 const float more = fmaxf(x, y);
-                second = fmaxf(fmaxf(second, fminf(x, y)), fminf(best, more));
+                second = choose_max3(second, fminf(x, y), fminf(best, more));
                 best = fmaxf(best, more);
             };
 #pragma unroll
