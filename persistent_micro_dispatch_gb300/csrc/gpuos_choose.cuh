@@ -1469,9 +1469,10 @@ static int adjust_launch_of(const gpuos_devdesc &d, void *stream)
  * blocks an SM, 7 TB/s); a piece's start and end take it about 5 us (first copy
  * 1, bar 1, ranks 0.5, sums 0.5, a part's way to the row's last block 1 to 2,
  * joining 2), which the SM's other two blocks cover only in part. 456 rows of
- * 128,000 in f32, K = 5: 44 us, 5.3 TB/s (K = 1: 42); 509 rows, whose runs
- * cross rows, 56.5, 4.6 TB/s (three equal runs for each row, 4 waves: 62); 64
- * rows in bf16, K = 20: 16.5; one row of 32,000, K = 1: 6.2. Loads to registers
+ * 128,000 in f32, K = 5: 42.3 us, 5.5 TB/s (K = 1: 40.5); 509 rows, whose runs
+ * cross rows, 53, 4.9 TB/s (three equal runs for each row, 4 waves: 62 where this
+ * took 56); 64 rows in bf16, K = 20: 16; one row of 32,000, K = 1: 6.2. Units
+ * that are whole are read without a look at each place (56.8 us without that). Loads to registers
  * instead of the ring took the same time while they were the only change.
  * ------------------------------------------------------------------------- */
 #define GPUOS_TOPB_THREADS 256
@@ -1528,7 +1529,7 @@ DEV uint32_t top_fill(uint64_t *e, uint32_t n) /* (before a barrier) */
     return (n + 7u) & ~7u;
 }
 /* (The bars and the sort are functions of their own: inlined at each of their
- * places, 509 x 128,000 took 57.8 us, so 56.6. A launch runs them from a cold
+ * places, 509 x 128,000 took 57.8 us where they take 56.6. A launch runs them from a cold
  * instruction cache.)
  *
  * A bar that at least K of the threads' entries are above (0: there are not
