@@ -139,11 +139,11 @@ TRAFFIC_SOURCES = ("persistent_micro_dispatch_gb300/csrc/gpuos_device.cu",
 TRAFFIC_INCLUDES = ("persistent_micro_dispatch_gb300/csrc/gpuos_kv4.cuh",  # by gpuos_device.cu
                     "persistent_micro_dispatch_gb300/csrc/gpuos_choose.cuh")
 TRAFFIC = {
-    "c2": dict(bytes=252_671_744, descs=4096, sources="2a920200555672ad"),
-    "c2l": dict(bytes=1_088_947_456, descs=400, sources="2a920200555672ad"),
-    "c3": dict(bytes=415_183_360, descs=2048, sources="2a920200555672ad"),
-    "c4": dict(bytes=31_080_491_264, descs=600, sources="2a920200555672ad"),
-    "c5": dict(bytes=494_220_544, descs=224, sources="2a920200555672ad"),
+    "c2": dict(bytes=252_751_872, descs=4096, sources="c271e8602efa53c9"),
+    "c2l": dict(bytes=1_087_886_592, descs=400, sources="c271e8602efa53c9"),
+    "c3": dict(bytes=414_561_536, descs=2048, sources="c271e8602efa53c9"),
+    "c4": dict(bytes=31_089_103_872, descs=600, sources="c271e8602efa53c9"),
+    "c5": dict(bytes=494_423_040, descs=224, sources="c271e8602efa53c9"),
 }
 
 
