@@ -187,7 +187,7 @@ def eager_run(descs: np.ndarray, stream_ptr: int = 0, stage_bytes: int = 16384) 
         descs = np.ascontiguousarray(descs, dtype=DESC_DTYPE).reshape(-1)
     n = descs.size
     # (a few descriptors are copied: cheaper than numpy's way to their address)
-    rc = (_lib or lib()).gpuos_eager_run(descs.tobytes() if n <= 16 else descs.ctypes.data, n, stage_bytes, stream_ptr)
+    rc = lib().gpuos_eager_run(descs.tobytes() if n <= 16 else descs.ctypes.data, n, stage_bytes, stream_ptr)
     if rc != OK:
         check(rc, "gpuos_eager_run")
 
