@@ -29,6 +29,8 @@ PRODUCERS = os.path.join(HERE, "gpuos_producers")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc")
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-I" + INCLUDE, "-I" + CSRC]
+# the image that each hand-off links: line tables would be three fifths of it, and a fifth of the link's time
+LINKED = [f for f in COMMON if f != "-lineinfo"]
 
 SOURCES = ["gpuos_device.cu", "gpuos_host.cpp", "gpuos_nvrtc.cpp"]
 
@@ -83,7 +85,7 @@ def build(force: bool = False) -> str:
     if force or _stale(EXEC_RDC, [dev_src] + headers):
         # every function of the relocatable build must fit the executor's
         # per-thread register budget (launch bounds: 384 threads, 1 block/SM)
-        jobs.append(([NVCC] + ARCH + COMMON + ["-cubin", "-rdc=true", "-maxrregcount", "168", "-Xptxas", "-v",
+        jobs.append(([NVCC] + ARCH + LINKED + ["-cubin", "-rdc=true", "-maxrregcount", "168", "-Xptxas", "-v",
                                                "-DGPUOS_EXECUTOR_ONLY", dev_src, "-o", EXEC_RDC + ".tmp"],
                      os.path.join(BUILD, "gpuos_exec_rdc.ptxas.txt")))
     with cf.ThreadPoolExecutor(max_workers=4) as ex:

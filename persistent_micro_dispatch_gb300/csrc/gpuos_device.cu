@@ -2683,6 +2683,8 @@ extern "C" __global__ void __launch_bounds__(GPUOS_MAX_WPB * 32, 1) gpuos_execut
     }
 }
 
+#ifndef GPUOS_EXECUTOR_ONLY /* (the relocatable build, linked anew for each op module that arrives, holds no
+                             * other kernel: they were a fifth of its code) */
 /* ===========================================================================
  * Eager baseline: the same op bodies, one launch per descriptor, one warp
  * per tile, one warp per block (spreads a descriptor over many SMs).
@@ -2737,9 +2739,7 @@ extern "C" int gpuos_dev_preload(void)
     cudaFuncAttributes a;
     if (cudaFuncGetAttributes(&a, gpuos_executor_kernel) != cudaSuccess) return -1;
     if (cudaFuncGetAttributes(&a, gpuos_eager_kernel) != cudaSuccess) return -1;
-#ifndef GPUOS_EXECUTOR_ONLY
     if (kv4_preload() != 0 || choose_preload() != 0) return -1;
-#endif
     return 0;
 }
 
@@ -2749,10 +2749,8 @@ extern "C" int gpuos_dev_eager_launch(const gpuos_desc *d, uint32_t ntiles, uint
     static_assert(sizeof(dd) == sizeof(*d), "layout");
     memcpy(&dd, d, sizeof(dd));
     dd.ntiles = ntiles;
-#ifndef GPUOS_EXECUTOR_ONLY
     if (d->op_id >= GPUOS_OP_KV4_WRITE && d->op_id <= GPUOS_OP_PAGE_COPY) return kv4_eager_launch(dd, stream);
     if (d->op_id >= GPUOS_OP_LOGITS_ADJUST && d->op_id <= GPUOS_OP_EXPERT_PLACE) return choose_eager_launch(dd, stream);
-#endif
     const uint32_t grid = (ntiles + EAGER_WPB - 1) / EAGER_WPB;
     const uint32_t dyn = gpuos_dev_dyn_smem(EAGER_WPB, stage_bytes);
     static uint32_t attr_set = 0;
@@ -2840,3 +2838,4 @@ extern "C" GPUOS_API int gpuos_sdpa_noalloc(const void *q, const void *Kc, const
     gpuos_sdpa_noalloc_kernel<<<d.ntiles, 32, gpuos_dev_dyn_smem(1, 0), (cudaStream_t)stream>>>(d);
     return cudaGetLastError() == cudaSuccess ? GPUOS_OK : GPUOS_ECUDA;
 }
+#endif /* GPUOS_EXECUTOR_ONLY */
