@@ -1622,9 +1622,7 @@ DEV void top_block_softmax(TopBlock &s, float &m, float &l)
 DEV void top_block_write(const gpuos_devdesc &d, uint32_t row, const TopBlock &s, float m, float l)
 {
     const uint32_t K = d.dims[3], t = threadIdx.x;
-    float ls; /* (-infinity if nothing but -infinity was there) */
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(ls) : "f"(l));
-    ls *= 0.693147181f;
+    const float ls = logf(l); /* (-infinity if nothing but -infinity was there; next to 1 the hardware's is off by 2^-22) */
     if (t < K) {
         const float x = choose_unkey((uint32_t)(s.sorted[t] >> 32));
         reinterpret_cast<uint32_t *>(d.out)[(uint64_t)row * K + t] = GPUOS_FULL - (uint32_t)s.sorted[t];
