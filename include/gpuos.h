@@ -171,11 +171,15 @@ enum {
     GPUOS_OP_RESERVED = 20, /* no op: refused wherever an id is given */
     GPUOS_OP_EXPERT_ROUTE = 21, /* a = router logits [N][E], f32|bf16 -> out = ids i32[N][K], the K best
                                experts of each token, and aux0 = their weights f32[N][K]. A score is
-                               softmax or sigmoid of the logit; the choice goes by score + b[e] (b =
-                               f32[E] or 0), the weight by the score alone. With G > 1 groups of E / G
-                               neighbouring experts, only the `keep` best groups are chosen from, by their
-                               best member or the sum of their two best. Ties go to the lower expert (or
-                               group); the choice is that of 64-bit arithmetic. Weights are divided by
+                               softmax or sigmoid of the logit. With b (f32[E]) the choice goes by
+                               score + b[e], as in 64-bit arithmetic. Without (b = 0) it goes by the
+                               logits themselves, whose order is the scores' own, also where 64-bit
+                               scores are equal and logits are not (sigmoids of 40 and 41, of 0 and
+                               1e-20; biases of zero choose the lower expert there). The weight goes by
+                               the score alone. With G > 1 groups of E / G neighbouring experts, only the
+                               `keep` best groups are chosen from: by their best member, compared as the
+                               experts are, or by the sum of their two best, which is of 64-bit scores (and
+                               biases) either way. Ties go to the lower expert (or group). Weights are divided by
                                their sum if asked, then multiplied by fparam[0]. A NaN logit counts as
                                -infinity (score 0); weights of sum 0 stay 0, and one below 2^-126 may
                                be 0. aux1 = i32[1] on the device (0: none): tokens from there on are

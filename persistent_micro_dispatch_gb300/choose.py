@@ -205,9 +205,11 @@ def experts(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, *, s
     """The K experts of each token of the router's logits [N, E] into ids int32
     [N, K], best first, and their weights into weights float32 [N, K]. Scores
     are the row's softmax, or sigmoids; the choice goes by score + bias
-    (float32 [E]), among the ``keep`` best of ``groups`` groups of neighbouring
-    experts (by their best, or with top2 by the sum of their two best), ties to
-    the lower number, as in 64-bit arithmetic. Weights are the scores, divided by their sum
+    (float32 [E]) as in 64-bit arithmetic, or without a bias by the logits, whose
+    order is the scores' (also where 64-bit scores run out of digits: a bias of
+    zeros may choose otherwise there), among the ``keep`` best of ``groups`` groups of neighbouring
+    experts (by their best, or with top2 by the sum of their two best scores plus biases), ties to
+    the lower number. Weights are the scores, divided by their sum
     with normalise, times scale. rows (int32 [1]): the tokens from there on are
     padding, with ids -1 and weights 0."""
     dt, N, E, ld, a = _rows("logits", logits)
