@@ -637,6 +637,9 @@ DEV float route_logit(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n, ui
 /* Scores from a logit, the row's largest and 1 / the row's sum. The upper
  * limits keep an infinite logit's share, and sums of 1024, finite. */
 DEV float route_exp(float x) { return choose_exp(fminf(x, 80.0f)); }
+/* Two groups' values that fp32 holds as one infinity, where sums of two finite
+ * values (none larger than `wide`) may be what is infinite: 64 bits tell them apart. */
+DEV bool route_beyond(float edge, float next, float wide) { return wide > 0x1p126f && edge == next && fabsf(edge) > FLT_MAX; }
 DEV float route_score(bool sigmoid, float x, float most, float inv)
 {
     if (x == -INFINITY) return 0.0f;
@@ -799,11 +802,12 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
             if (fabsf(c) <= FLT_MAX) wide = fmaxf(wide, fabsf(c));
         }
     }
+    wide = warp_max(wide);
     /* A sigmoid is off by less than 2^-21 of itself (ex2 2^-22, three roundings),
      * a softmax by less than 2^-19 (its sum's errors too), the sum with the bias
      * by 2^-24 more; two values may swap within twice that. Scores of logits
      * below -80 are cut off (route_exp), which is nothing beside a larger one. */
-    const float unsure = route_score(sigmoid, most, most, inv) * (sigmoid ? 0x1p-20f : 0x1p-18f) + warp_max(wide) * 0x1p-22f;
+    const float unsure = route_score(sigmoid, most, most, inv) * (sigmoid ? 0x1p-20f : 0x1p-18f) + wide * 0x1p-22f;
     bool sure = !sigmoid || most >= -60.0f || most == -INFINITY;
     if (a.G > 1) {
         uint32_t mine = 0, edge; /* lane g: group g's value */
@@ -841,7 +845,10 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
             }
         }
         const uint32_t kept = route_groups(a, mine, edge);
-        if (a.keep < a.G && (a.bias || top2) && choose_unkey(edge) - choose_unkey(route_max(mine)) <= 2.0f * unsure) sure = false;
+        if (a.keep < a.G && (a.bias || top2)) {
+            const float last = choose_unkey(edge), next = choose_unkey(route_max(mine));
+            if (last - next <= 2.0f * unsure || route_beyond(last, next, wide)) sure = false;
+        }
 #pragma unroll
         for (int i = 0; i < VPL; i++)
             if (lane + 32u * i < a.E && !(kept >> ((lane + 32u * i) / a.size) & 1u)) key[i] = 0u;
@@ -2327,7 +2334,8 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
                 rank += ahead;
                 if (!ahead && k != group) next = fmaxf(next, v);
             }
-            const bool near = (biased || summed) && rank == a.keep - 1u && a.keep < a.G && mine - next <= 2.0f * unsure;
+            const bool edge = (biased || summed) && rank == a.keep - 1u && a.keep < a.G, near = edge && mine - next <= 2.0f * unsure;
+            if (edge && route_beyond(mine, next, wide)) sure = false;
             if (__any_sync(GPUOS_FULL, near)) {
                 if (sigmoid && biased) {
                     /* the groups' values again, finer: of what may be their best, which are few */
