@@ -23,6 +23,18 @@ beside.
     gpuos.eager_run(choose.experts(router_logits, ids, weights, sigmoid=True, bias=bias, groups=8, keep=4, top2=True), stream)
     gpuos.eager_run(choose.plan(ids, order, place, offsets, ws), stream)
 
+In the executor a descriptor starts when a worker is free, whatever came before
+it in the batch: each must depend on those whose results it reads, and on the
+last one that used its workspace. ``plan``'s second record depends on its first;
+nothing else is set here. A step as a chain, each record after the one before:
+
+    d = numpy.concatenate([choose.adjust(...), choose.top(...), choose.experts(...), choose.plan(...)])
+    d["flags"], d["dep"][1:, 0] = gpuos.FLAG_DEP_REL, 1
+    ex.submit_batch(d)
+
+(Two chains side by side, tokens and experts, take a workspace each. Launches on
+one stream run in order by themselves.)
+
 Logits are [rows, columns], float32 or bfloat16, with neighbouring columns next
 to each other and rows any distance apart; everything else is contiguous.
 Nothing here reads device memory or computes gradients. Launch with the
