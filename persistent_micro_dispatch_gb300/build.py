@@ -77,7 +77,8 @@ def build(force: bool = False) -> str:
             cmd = [NVCC] + ARCH + COMMON + ["-Xcompiler", "-fPIC,-fvisibility=hidden", "-c", sp, "-o", obj]
             log = None
             if src.endswith(".cu"):
-                cmd += ["-Xptxas", "-v"]
+                # (device code of this size is compressed otherwise, and a process's first call unpacks it)
+                cmd += ["-Xptxas", "-v", "--no-compress"]
                 log = os.path.join(BUILD, src.replace(".cu", ".ptxas.txt"))
             jobs.append((cmd, log))
     ext_src = os.path.join(CSRC, "gpuos_ext_ops.cu")
