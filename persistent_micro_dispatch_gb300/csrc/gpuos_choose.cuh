@@ -886,13 +886,15 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
     route_write(a, n, id, route_score(sigmoid, x, most, inv));
     return true;
 }
+/* A tile's tokens (at most 32); bit k of the result: token first + k is not sure. */
 template <int VPL>
-DEV void route_tile(const gpuos_devdesc *d, uint32_t first, uint32_t count)
+DEV uint32_t route_tile(const gpuos_devdesc *d, uint32_t first, uint32_t count)
 {
     RouteArgs a;
     route_args(d, a);
     const uint32_t lane = lane_id(), end = min(first + count, a.N);
     const uint32_t rows = a.rows ? (uint32_t)max(__ldcg(a.rows), 0) : a.N;
+    uint32_t again = 0;
 #pragma unroll 1
     for (uint32_t n = first; n < end; n++) {
         if (n >= rows) { /* padding */
@@ -901,9 +903,25 @@ DEV void route_tile(const gpuos_devdesc *d, uint32_t first, uint32_t count)
                 __stcg(a.weights + (uint64_t)n * a.K + lane, 0.0f);
             }
         } else if (!route_token<VPL>(d, a, n)) {
-            op_y_sure<VPL>(d, n);
+            again |= 1u << (n - first);
         }
     }
+    return again;
+}
+template <int VPL>
+DEV void route_again(const gpuos_devdesc *d, uint32_t first, uint32_t again)
+{
+#pragma unroll 1
+    for (; again; again &= again - 1u) op_y_sure<VPL>(d, first + (uint32_t)__ffs((int)again) - 1u);
+}
+/* Out of line, and done before its tokens go the sure way, so that no frame lies
+ * on another: the executor's stack is 952 bytes a thread so. With all in line it
+ * was 1,280, beyond the 1,024 that a context keeps for each thread, and its
+ * launch had the device's local memory made larger (86 MB, once it is idle). */
+template <int VPL>
+__device__ __noinline__ uint32_t op_y_tile(const gpuos_devdesc *d, uint32_t first, uint32_t count)
+{
+    return route_tile<VPL>(d, first, count);
 }
 DEV int route_op(const gpuos_devdesc *d, uint32_t tile)
 {
@@ -913,9 +931,9 @@ DEV int route_op(const gpuos_devdesc *d, uint32_t tile)
         (m[0] - 1u) / gpuos_route_rows(m[0]) + 1u != d->ntiles)
         return GPUOS_ST_BAD_ARGS;
     if (tile >= d->ntiles) return GPUOS_ST_OK;
-    const uint32_t rows = gpuos_route_rows(m[0]);
-    if (m[1] <= 256) route_tile<8>(d, tile * rows, rows);
-    else route_tile<32>(d, tile * rows, rows);
+    const uint32_t rows = gpuos_route_rows(m[0]), first = tile * rows;
+    if (m[1] <= 256) route_again<8>(d, first, op_y_tile<8>(d, first, rows));
+    else route_again<32>(d, first, op_y_tile<32>(d, first, rows));
     return GPUOS_ST_OK;
 }
 
@@ -2471,7 +2489,8 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS) gpuos_route_any_kernel(c
 {
     kv4_after_previous();
     const uint32_t step = gridDim.x * (GPUOS_ROUTEB_THREADS / 32u);
-    for (uint32_t n = blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + (threadIdx.x >> 5); n < d.dims[0]; n += step) route_tile<VPL>(&d, n, 1u);
+    for (uint32_t n = blockIdx.x * (GPUOS_ROUTEB_THREADS / 32u) + (threadIdx.x >> 5); n < d.dims[0]; n += step)
+        route_again<VPL>(&d, n, route_tile<VPL>(&d, n, 1u));
 }
 
 template <bool F32, int L, int VPL>
