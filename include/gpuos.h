@@ -156,10 +156,13 @@ enum {
                                is no entry); the sum is divided by the temperature (if above 0); and
                                tokens whose bit in row `mask` of aux1 = u32[M][ceil(V / 32)] is 0 get
                                -infinity, whatever they held. Arithmetic in fp32 (factors are divided by
-                               the temperature first), one rounding to the type. Tokens outside the vocabulary are passed over. A request whose
-                               record does not fit (length outside 0 .. Lcap, prompt outside 0 ..
-                               length, mask >= M, biases outside 0 .. Nb) keeps its output row and gives
-                               status GPUOS_ST_BAD_ARGS. b, aux1, aux2 may be 0 with Lcap, M, Nb 0;
+                               the temperature first, by reciprocals: a temperature above 0 and a
+                               repetition penalty lie within 2^-126 to 2^126), one rounding to the type.
+                               Tokens outside the vocabulary are passed over. A request whose record does
+                               not fit (length outside 0 .. Lcap, prompt outside 0 .. length, mask >= M,
+                               biases outside 0 .. Nb) keeps its output row and gives status
+                               GPUOS_ST_BAD_ARGS. Launches go by Lcap, not by the lengths: a few long
+                               histories are shared by clusters for 12,289 to 229,376 tokens. b, aux1, aux2 may be 0 with Lcap, M, Nb 0;
                                dims = {B, V, ld of a, ld of out, Lcap <= 2^28, M | Nb << 16}, Nb <= 1024 */
     GPUOS_OP_LOGITS_TOP = 19, /* the K best of each row of a[B][V], f32|bf16: out = ids i32[B][K], by
                                value, then by id; aux0 = f32[B][K] their log-probabilities x - lse;

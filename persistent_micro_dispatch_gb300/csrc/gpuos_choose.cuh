@@ -1096,7 +1096,10 @@ DEV int plan_place_op(const gpuos_devdesc *d, uint32_t tile)
  *   1 x 128,000  5.0   6.3    6.4   6.4    7.7   6.4    10.4   6.4    18.3   6.7
  *   8 x 128,000  6.2  12.0    7.6  12.1    9.0  12.1    11.9  12.3    20.0  12.6
  * (64, 32 and 256 blocks that share; 2,048 of them, 64 x 128,000 with 16,000
- * tokens, take 69 us against 18). */
+ * tokens, take 69 us against 18). A row with room for more than 229,376 tokens
+ * is not shared, as its 16-bit counters could overflow: 8 x 32,000 with 20,000
+ * to 131,071 tokens in it 47 us against 8. With at most 100 tokens in a row of
+ * 12,289 or more the shared way takes 5.9 us where the direct one took 2.5. */
 #define GPUOS_ADJUSTL_LONG 12288u   /* as long as each block has an SM ... */
 #define GPUOS_ADJUSTL_LONGER 24576u /* ... or half of one */
 #define GPUOS_ADJUSTL_FEW 152u
@@ -2470,7 +2473,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         float w = chosen ? route_score(sigmoid, x, most, inv) : 0.0f;
         if (norm) {
             const float sum = lanes_sum<L>(w);
-            if (sum != 0.0f) w = __fdividef(w, sum);
+            if (sum != 0.0f) w = __fdividef(w, sum); /* (two units in the last place, as a score's own error; sums lie within 2^-116 to 32) */
         }
         uint32_t again = __ballot_sync(GPUOS_FULL, !sure && !pad);
         if (chosen && !(again & lanes)) {

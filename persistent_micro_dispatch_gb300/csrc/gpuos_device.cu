@@ -2620,7 +2620,8 @@ DEV void worker(const gpuos_exec_params &p, gpuos_devdesc *sd, uint32_t gw, uint
             const uint64_t t_fin = globaltimer();
             const uint64_t add[GPUOS_PROF_FIELDS] = {count, t_body - t_deps, t_fin - t_body, t_deps - t_found};
             /* (the 4-bit cache's read back, attention and page copy, whose
-             * tiles are long, go to the row itself) */
+             * tiles are long, go to the row itself; so do the choosing ops,
+             * some of whose tiles are not: shared memory holds no more buckets) */
             const uint32_t sk = bk == GPUOS_OP_BUILTIN_COUNT ? GPUOS_PROF_SMEM_BUCKETS - 1 : bk;
             if (bk < GPUOS_PROF_SMEM_BUCKETS - 1 || bk == GPUOS_OP_BUILTIN_COUNT) {
 #pragma unroll
