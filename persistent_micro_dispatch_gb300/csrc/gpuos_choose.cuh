@@ -872,7 +872,17 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
         if (a.bias) {
             /* values that may have swapped, unless they are of equal logits and biases */
             if (k && choose_unkey(before) - choose_unkey(win) <= unsure) {
-                if (!(route_logit(d, a, n, e) == route_logit(d, a, n, e_before) && __ldcg(a.bias + e) == __ldcg(a.bias + e_before))) sure = false;
+                const float x = route_logit(d, a, n, e_before), b = __ldcg(a.bias + e_before);
+                if (!(route_logit(d, a, n, e) == x && __ldcg(a.bias + e) == b)) {
+                    sure = false;
+                } else if (k == a.K) { /* the last one's like is not chosen: what else is near comes behind it */
+                    bool other = false;
+#pragma unroll
+                    for (int i = 0; i < VPL; i++)
+                        if (key[i] && choose_unkey(before) - choose_unkey(key[i]) <= unsure)
+                            other |= !(route_logit(d, a, n, lane + 32u * i) == x && __ldcg(a.bias + lane + 32u * i) == b);
+                    if (__any_sync(GPUOS_FULL, other)) sure = false;
+                }
             }
             before = win, e_before = e;
         }
@@ -2453,8 +2463,19 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
             if (chosen && sub + 1u < have) {
                 /* values that may have swapped, unless they are of equal logits and biases */
                 const uint64_t e = s.best[sub], o = s.best[sub + 1u];
-                near = choose_unkey((uint32_t)(e >> 32)) - choose_unkey((uint32_t)(o >> 32)) <= unsure &&
-                       !(s.best_logit[sub] == s.best_logit[sub + 1u] && flat[GPUOS_FULL - (uint32_t)e] == flat[GPUOS_FULL - (uint32_t)o]);
+                const float v = choose_unkey((uint32_t)(e >> 32));
+                near = v - choose_unkey((uint32_t)(o >> 32)) <= unsure;
+                if (near && s.best_logit[sub] == s.best_logit[sub + 1u] && flat[GPUOS_FULL - (uint32_t)e] == flat[GPUOS_FULL - (uint32_t)o]) {
+                    near = false;
+                    if (sub + 1u == a.K) { /* the last one's like is not chosen: what else is near comes behind it */
+#pragma unroll 1
+                        for (uint32_t k = 0; k < have; k++) {
+                            const uint64_t g = s.got[k];
+                            if (g < o && v - choose_unkey((uint32_t)(g >> 32)) <= unsure)
+                                near |= !(s.logit[k] == s.best_logit[sub] && flat[s.id[k]] == flat[GPUOS_FULL - (uint32_t)e]);
+                        }
+                    }
+                }
             }
             const uint32_t who = __ballot_sync(GPUOS_FULL, near);
             if (who & lanes) {
