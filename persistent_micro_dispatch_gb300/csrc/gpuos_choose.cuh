@@ -2201,7 +2201,7 @@ struct RouteGathered {
 /* A token whose groups are sure, but not its experts: all that may be among
  * them are gathered, and are ranked again by finer values (sigmoid scores and
  * biases). Every lane of the token; false if that does not tell either. Only
- * values of equal logits and biases may be equal. */
+ * values of equal logits and biases may be equal, and infinite ones. */
 __device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, const RouteGathered q)
 {
 #pragma unroll 1
@@ -2222,8 +2222,9 @@ __device__ __noinline__ bool op_y_fine(RouteToken *s, uint32_t sub, uint32_t L, 
             if (k == i) continue;
             const float2 o = s->fine[k];
             const float more = pair_less(o, v);
-            const bool alike = s->logit[k] == x && q.bias[s->id[k]] == b;
-            if (alike ? s->id[k] < id : more > 0.0f || o.x > v.x) rank++; /* (an infinite one's difference is NaN) */
+            /* (infinite values are equal whatever their logits; their difference is NaN) */
+            const bool alike = (s->logit[k] == x && q.bias[s->id[k]] == b) || (o.x == v.x && fabsf(v.x) > FLT_MAX);
+            if (alike ? s->id[k] < id : more > 0.0f || o.x > v.x) rank++;
             if (!alike && fabsf(more) <= pair_unsure(q.wide)) told = false;
         }
         if (rank < 16u) s->best[rank] = s->got[i], s->best_logit[rank] = x;
