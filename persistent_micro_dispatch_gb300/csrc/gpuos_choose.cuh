@@ -650,6 +650,14 @@ DEV double route_score(bool sigmoid, double x, double most, double inv)
     if (x == -INFINITY) return 0.0;
     return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(fmin(x - most, 700.0)) * inv;
 }
+/* A chosen expert's score: as above, but for the difference's own rounding,
+ * which is up to 2^-18 of the score of a logit 64 to 80 below the largest. */
+DEV float route_weight(bool sigmoid, float x, float most, float inv)
+{
+    if (sigmoid) return route_score(true, x, most, inv);
+    const float w = route_score(false, x, most, inv), h = x - most, z = h - x, l = (x - (h - z)) + (-most - z); /* h + l = x - most (Knuth) */
+    return fabsf(h) <= 80.0f ? fmaf(w, l, w) : w;
+}
 /* Lane k's chosen expert and score -> the token's answer. */
 template <typename T>
 DEV void route_write(const RouteArgs &a, uint32_t n, uint32_t id, T got)
@@ -804,7 +812,8 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
     }
     wide = warp_max(wide);
     /* A sigmoid is off by less than 2^-21 of itself (ex2 2^-22, three roundings),
-     * a softmax by less than 2^-19 (its sum's errors too), the sum with the bias
+     * a softmax by less than 2^-19 (its sum's errors too; farther than 32 below the
+     * largest by 2^-18, of next to nothing), the sum with the bias
      * by 2^-24 more; two values may swap within twice that. Scores of logits
      * below -80 are cut off (route_exp), which is nothing beside a larger one. */
     const float unsure = route_score(sigmoid, most, most, inv) * (sigmoid ? 0x1p-20f : 0x1p-18f) + wide * 0x1p-22f;
@@ -893,7 +902,7 @@ DEV bool route_token(const gpuos_devdesc *d, const RouteArgs &a, uint32_t n)
      * that is seen. Without a bias a softmax's largest is among the chosen.) */
     if ((sigmoid || a.bias) && __any_sync(GPUOS_FULL, x - (sigmoid ? 0.0f : most) < -80.0f && x != -INFINITY)) sure = false;
     if (!sure) return false;
-    route_write(a, n, id, route_score(sigmoid, x, most, inv));
+    route_write(a, n, id, route_weight(sigmoid, x, most, inv));
     return true;
 }
 /* A tile's tokens (at most 32); bit k of the result: token first + k is not sure. */
@@ -2492,7 +2501,7 @@ __global__ void __launch_bounds__(GPUOS_ROUTEB_THREADS, VPL <= 16 ? 8 : 7) gpuos
         const uint32_t id = GPUOS_FULL - (uint32_t)s.best[mine];
         const float x = s.best_logit[mine];
         if ((sigmoid || biased) && chosen && x - (sigmoid ? 0.0f : most) < -80.0f && x != -INFINITY) sure = false; /* (see route_token) */
-        float w = chosen ? route_score(sigmoid, x, most, inv) : 0.0f;
+        float w = chosen ? route_weight(sigmoid, x, most, inv) : 0.0f;
         if (norm) {
             const float sum = lanes_sum<L>(w);
             if (sum != 0.0f) w = __fdividef(w, sum); /* (two units in the last place, as a score's own error; sums lie within 2^-116 to 32) */
