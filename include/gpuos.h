@@ -182,10 +182,10 @@ enum {
                                the score alone. With G > 1 groups of E / G neighbouring experts, only the
                                `keep` best groups are chosen from: by their best member, compared as the
                                experts are, or by the sum of their two best, which is of 64-bit scores (and
-                               biases) either way. Ties go to the lower expert (or group). Weights are divided by
-                               their sum if asked, then multiplied by fparam[0]. A NaN logit counts as
-                               -infinity (score 0); weights of sum 0 stay 0, and one below 2^-126 may
-                               be 0. aux1 = i32[1] on the device (0: none): tokens from there on are
+                               biases) either way. Ties go to the lower expert (or group). Weights are
+                               divided by their sum if asked, then multiplied by fparam[0]. A NaN logit
+                               counts as -infinity (score 0); logits of +infinity share a softmax's whole
+                               weight; weights of sum 0 stay 0, and one below 2^-126 may be 0. aux1 = i32[1] on the device (0: none): tokens from there on are
                                padding, with ids -1 and weights 0.
                                dims = {N < 2^31, E <= 1024, ld, K <= 32, G | keep << 16, GPUOS_ROUTE_* flags},
                                G <= 32, E % G == 0, K <= keep * (E / G) */
