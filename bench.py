@@ -139,11 +139,11 @@ TRAFFIC_SOURCES = ("persistent_micro_dispatch_gb300/csrc/gpuos_device.cu",
 TRAFFIC_INCLUDES = ("persistent_micro_dispatch_gb300/csrc/gpuos_kv4.cuh",  # by gpuos_device.cu
                     "persistent_micro_dispatch_gb300/csrc/gpuos_choose.cuh")
 TRAFFIC = {
-    "c2": dict(bytes=252_751_872, descs=4096, sources="c271e8602efa53c9"),
-    "c2l": dict(bytes=1_087_886_592, descs=400, sources="c271e8602efa53c9"),
-    "c3": dict(bytes=414_561_536, descs=2048, sources="c271e8602efa53c9"),
-    "c4": dict(bytes=31_089_103_872, descs=600, sources="c271e8602efa53c9"),
-    "c5": dict(bytes=494_423_040, descs=224, sources="c271e8602efa53c9"),
+    "c2": dict(bytes=252_364_288, descs=4096, sources="c4a2590984155aa9"),
+    "c2l": dict(bytes=1_088_726_784, descs=400, sources="c4a2590984155aa9"),
+    "c3": dict(bytes=413_984_000, descs=2048, sources="c4a2590984155aa9"),
+    "c4": dict(bytes=31_075_835_136, descs=600, sources="c4a2590984155aa9"),
+    "c5": dict(bytes=493_719_296, descs=224, sources="c4a2590984155aa9"),
 }
 
 
