@@ -162,7 +162,8 @@ enum {
                                not fit (length outside 0 .. Lcap, prompt outside 0 .. length, mask >= M,
                                biases outside 0 .. Nb) keeps its output row and gives status
                                GPUOS_ST_BAD_ARGS. Launches go by Lcap, not by the lengths: a few long
-                               histories are shared by clusters for 12,289 to 229,376 tokens. b, aux1, aux2 may be 0 with Lcap, M, Nb 0;
+                               histories are shared by clusters for 12,289 to 229,376 tokens. b, aux1,
+                               aux2 may be 0 with Lcap, M, Nb 0;
                                dims = {B, V, ld of a, ld of out, Lcap <= 2^28, M | Nb << 16}, Nb <= 1024 */
     GPUOS_OP_LOGITS_TOP = 19, /* the K best of each row of a[B][V], f32|bf16: out = ids i32[B][K], by
                                value, then by id; aux0 = f32[B][K] their log-probabilities x - lse;
@@ -185,8 +186,9 @@ enum {
                                biases) either way. Ties go to the lower expert (or group). Weights are
                                divided by their sum if asked, then multiplied by fparam[0]. A NaN logit
                                counts as -infinity (score 0); logits of +infinity share a softmax's whole
-                               weight; weights of sum 0 stay 0, and one below 2^-126 may be 0. aux1 = i32[1] on the device (0: none): tokens from there on are
-                               padding, with ids -1 and weights 0.
+                               weight; weights of sum 0 stay 0, and one below 2^-126 may be 0. aux1 =
+                               i32[1] on the device (0: none): tokens from there on are padding, with ids
+                               -1 and weights 0.
                                dims = {N < 2^31, E <= 1024, ld, K <= 32, G | keep << 16, GPUOS_ROUTE_* flags},
                                G <= 32, E % G == 0, K <= keep * (E / G) */
     GPUOS_OP_EXPERT_COUNT = 22, /* the pairs of each expert in runs of a = ids i32[P], into aux2 = workspace
