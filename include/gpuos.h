@@ -185,8 +185,9 @@ enum {
                                experts are, or by the sum of their two best, which is of 64-bit scores (and
                                biases) either way. Ties go to the lower expert (or group). Weights are
                                divided by their sum if asked, then multiplied by fparam[0]. A NaN logit
-                               counts as -infinity (score 0); logits of +infinity share a softmax's whole
-                               weight; weights of sum 0 stay 0, and one below 2^-126 may be 0. aux1 =
+                               counts as -infinity (score 0), a NaN bias too (where a group's two best are
+                               +infinity and -infinity, it may be kept or not); logits of +infinity share
+                               a softmax's whole weight; weights of sum 0 stay 0, and one below 2^-126 may be 0. aux1 =
                                i32[1] on the device (0: none): tokens from there on are padding, with ids
                                -1 and weights 0.
                                dims = {N < 2^31, E <= 1024, ld, K <= 32, G | keep << 16, GPUOS_ROUTE_* flags},
